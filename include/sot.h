@@ -300,6 +300,120 @@ int sot_grad_x_coo(const float* X, const float* Y, int B, int n, int m, int d,
                    const int* rows, const int* cols, const float* vals,
                    const long long* batch_offsets, float* grad, void* stream);
 
+/* ---- language-model training losses -------------------------------------- */
+/*
+ * Losses over rows of logits, with their gradients.  They stand beside the
+ * transport losses above in a model's training step and follow the same
+ * conventions, except for types and strides:
+ *   - logits [T][V] are SOT_F32, SOT_F16 or SOT_BF16; row t starts at element
+ *     t * ld (ld >= V) and its V elements are contiguous.  A gradient has the
+ *     logits' type and a row stride of its own (ld_grad).  It may be the logits'
+ *     own array with the same stride (the gradient then replaces them).
+ *   - Pointers are aligned to their type, no further.  The 16-byte granules
+ *     that a row's first and last element lie in are read whole.
+ *   - Everything else is float32; indices are SOT_I32 or SOT_I64.
+ *   - Sums, maxima and probabilities are held in 32 bits or more; a gradient is
+ *     rounded once, to the logits' type.  Results do not depend on the order in
+ *     which blocks run.
+ * With y = x / temperature: lse = log sum_v exp(y_v), p_v = exp(y_v - lse).
+ * A logit of -inf is a masked column (p = 0).  A row in use whose logits are all
+ * -inf, or hold NaN or +inf, gives NaN.  All calls are asynchronous.
+ */
+enum sot_dtype { SOT_F32 = 0, SOT_F16 = 1, SOT_BF16 = 2, SOT_I32 = 3, SOT_I64 = 4 };
+
+/*
+ * Log-probability of one token per row (scoring drafted tokens, or rollouts
+ * under an old or a reference model):
+ *   logp[t] = y[t][target[t]] - lse[t]      (either output may be NULL)
+ * A target outside [0, V) leaves its row out: it is not read, logp = lse = 0.
+ * SOT_ERR_UNSUPPORTED when a row does not fit the shared memory of a cluster of
+ * eight (above 800000 16-bit or 400000 32-bit logits).
+ */
+int sot_token_logprob(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                      const void* target, int target_type, float* logp, float* lse, void* stream);
+
+/*
+ * Its gradient, from the lse that sot_token_logprob wrote:
+ *   grad[t][v] = grad_logp[t] / temperature * ([v = target[t]] - p_v)
+ * Rows left out, and rows with grad_logp = 0, are written as zeros without
+ * being read.
+ */
+int sot_token_logprob_grad(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                           const void* target, int target_type, const float* lse, const float* grad_logp, void* grad,
+                           long long ld_grad, void* stream);
+
+/*
+ * Distillation from a teacher's top entries, loss and gradient in one pass.
+ * Row t has K entries: columns ids[t][k] and teacher values teacher[t][k]
+ * (contiguous [T][K]; 1 <= K <= 1024).  An entry whose column lies outside [0, V)
+ * is unused; the used columns of a row are distinct (a row that repeats one has
+ * an unspecified result).
+ *   tail = 0: teacher values are logits; q = softmax over the used entries at the
+ *     same temperature, loss[t] = weight[t] temperature^2 sum_k q_k (log q_k - log p_k).
+ *   tail = 1 (temperature 1): teacher values are log-probabilities of the whole
+ *     distribution, q_k = exp(value); the rest q_r = max(0, 1 - sum_k q_k) is one more
+ *     outcome, matched with the student's mass outside the entries, p_r:
+ *     loss[t] = weight[t] (sum_k q_k (log q_k - log p_k) + q_r (log q_r - log p_r)).
+ *     Where every column outside the entries is masked, or there is none, the
+ *     rest takes no part.
+ *   grad = d(sum_t loss) / d logits (NULL: losses only; loss may be NULL instead).
+ * weight NULL = 1/T.  A row of weight 0 is left out: not read, loss and gradient 0.
+ * A row without used entries has loss 0 and, without tail, gradient 0.
+ */
+int sot_distill_topk(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                     const void* ids, int ids_type, const void* teacher, int teacher_type, int K, int tail,
+                     const float* weight, float* loss, void* grad, long long ld_grad, void* stream);
+
+/*
+ * Clipped policy loss with a KL term, loss and gradient in one pass.  With
+ * logp as in sot_token_logprob, r = exp(logp - old_logp), d = ref_logp - logp and
+ * A = advantage:
+ *   kl[t]   = exp(d) - d - 1                                  (0 when ref_logp is NULL)
+ *   loss[t] = weight[t] (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef kl)
+ *   grad    = d(sum_t loss) / d logits                        (NULL: losses only)
+ * old_logp, ref_logp and advantage are [T] and constants of the gradient.
+ * weight NULL = 1/T.  A row of weight 0, or whose target lies outside [0, V), is
+ * left out: not read, all its outputs 0.  loss, logp, kl and grad may be NULL, not
+ * all of them.
+ */
+int sot_policy_loss(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                    const void* target, int target_type, const float* old_logp, const float* ref_logp,
+                    const float* advantage, const float* weight, float clip_low, float clip_high, float kl_coef,
+                    float* loss, float* logp, float* kl, void* grad, long long ld_grad, void* stream);
+
+/*
+ * Paired preference loss on token log-probabilities.  2 P packed sequences of T
+ * tokens in all; pair p's chosen sequence is tokens offsets[2p] .. offsets[2p+1] - 1
+ * and its rejected one offsets[2p+1] .. offsets[2p+2] - 1 (device array [2P+1],
+ * non-decreasing, within [0, T]; they are clamped to it).
+ *   margin[p] = sum_chosen (logp - ref_logp) - sum_rejected (logp - ref_logp)
+ *               (means instead of sums when average != 0; ref_logp NULL = 0)
+ *   loss[p]   = -(1 - s) log sigma(beta margin) - s log sigma(-beta margin),  s = label_smoothing
+ *   grad_logp[t] = scale d(sum_p loss) / d logp[t]
+ * With target given, a token whose target is negative takes no part (and is not
+ * counted by the means).  Tokens of no sequence get gradient 0.  Sums are formed
+ * in 64 bits.  Outputs may be NULL, not all of them.  The gradient goes on to the
+ * logits through sot_token_logprob_grad.
+ */
+int sot_preference_loss(const float* logp, const float* ref_logp, const void* target, int target_type,
+                        const long long* offsets, int P, long long T, float beta, float label_smoothing, int average,
+                        float scale, float* loss, float* margin, float* grad_logp, void* stream);
+
+/*
+ * A router's balance loss, z loss and per-expert counts, with the gradient.
+ * logits [T][E] (E <= 1024, temperature 1), ids [T][K] the experts each token
+ * chose (outside [0, E): a dropped choice, not counted), mask [T] bytes (0: the
+ * token takes no part; NULL: all do).  With N tokens that take part,
+ * f_e = E counts[e] / (K N):
+ *   counts[e] = number of choices of expert e
+ *   loss[0] = balance_coef / N sum_t sum_e f_e p_te,   loss[1] = z_coef / N sum_t lse_t^2
+ *   grad = d(loss[0] + loss[1]) / d logits with the counts held fixed (NULL: losses only)
+ * N = 0 gives zeros.  T K < 2^31.
+ */
+int sot_balance_loss(const void* logits, long long T, int E, long long ld, int dtype, const void* ids, int ids_type,
+                     int K, const unsigned char* mask, float balance_coef, float z_coef, int* counts, float* loss,
+                     void* grad, long long ld_grad, void* stream);
+
 /*
  * Synchronous input validation: every coordinate finite, every weight finite
  * and > 0.  Returns SOT_OK, SOT_ERR_NONFINITE or SOT_ERR_INVALID_ARG.

@@ -2,7 +2,8 @@
 
 Only argument marshalling lives here: every step of the computation runs in
 the CUDA kernels of libsot.  Tensors must be float32, contiguous and on the
-current CUDA device; the calls are stream-ordered on
+current CUDA device (the language-model losses take logits in three types and
+with a row stride); the calls are stream-ordered on
 ``torch.cuda.current_stream()`` unless a stream is given.  Outputs are
 allocated with torch when not supplied (plain device memory, no compute).
 A missing or unloadable libsot raises at once: there is no CPU fallback.
@@ -34,6 +35,10 @@ SOT_STAGE_EARLY_EXIT = 1 << 5
 SOT_TC_NO_SCREEN = 1 << 6
 SOT_NO_CLUSTER = 1 << 7
 SOT_COST_COSINE = 1 << 8
+
+SOT_F32, SOT_F16, SOT_BF16, SOT_I32, SOT_I64 = range(5)  # sot_dtype
+_FLOATS = {torch.float32: SOT_F32, torch.float16: SOT_F16, torch.bfloat16: SOT_BF16}
+_INDICES = {torch.int32: SOT_I32, torch.int64: SOT_I64}
 
 HEADER = os.path.join(_build.ROOT, "include", "sot.h")
 
@@ -104,6 +109,12 @@ def load(path: str | None = None):
         "sot_test_hold_tile": [i, i, ll],
         "sot_plan_coo_operands": [P, P, P, P, i, i, i, i, P, P, f, f, P, P, P, P, P, P, P, P,
                                   C.POINTER(C.c_float), P],
+        "sot_token_logprob": [P, ll, i, ll, i, f, P, i, P, P, P],
+        "sot_token_logprob_grad": [P, ll, i, ll, i, f, P, i, P, P, P, ll, P],
+        "sot_distill_topk": [P, ll, i, ll, i, f, P, i, P, i, i, i, P, P, P, ll, P],
+        "sot_policy_loss": [P, ll, i, ll, i, f, P, i, P, P, P, P, f, f, f, P, P, P, P, ll, P],
+        "sot_preference_loss": [P, P, P, i, P, i, ll, f, f, i, f, P, P, P, P],
+        "sot_balance_loss": [P, ll, i, ll, i, P, i, i, P, f, f, P, P, P, ll, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -420,6 +431,203 @@ def sot_grad_x_coo(X, Y, rows, cols, vals, batch_offsets, grad=None, stream=None
                                _ptr(batch_offsets), _ptr(grad), _stream(stream))
     _check(rc, "sot_grad_x_coo")
     return grad
+
+
+# ---- language-model training losses ---------------------------------------------------------------------------------
+def _rows(x, name="logits"):
+    """(tensor, T, V, row stride, sot_dtype) of logits [T, V] whose rows are contiguous."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dt = _FLOATS.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [rows, columns], got shape {tuple(x.shape)}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    T, V = x.shape
+    ld, inner = x.stride()
+    if inner != 1 and V > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if T <= 1:
+        ld = V
+    elif ld < V:
+        raise ValueError(f"{name}: rows must not overlap (row stride {ld}, {V} columns)")
+    return T, V, ld, dt
+
+
+def _index(t, name, shape, dev):
+    """sot_dtype of an index tensor of this shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    ty = _INDICES.get(t.dtype)
+    if ty is None:
+        raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return ty
+
+
+def _stream_of(stream, make):
+    """(stream handle, outputs): the outputs are made on the stream that will write
+    them, so that their memory is not still in use by another one's work."""
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream, make()
+    with torch.cuda.stream(stream):
+        return stream.cuda_stream, make()
+
+
+def _grad_rows(grad, logits, T, V, dt):
+    """(grad tensor or None, row stride) of an output asked for as True, False, None or a tensor."""
+    if grad is None or grad is False:
+        return None, 0
+    if grad is True:
+        return torch.empty((T, V), dtype=logits.dtype, device=logits.device), V
+    gT, gV, ld, gdt = _rows(grad, "grad")
+    if (gT, gV, gdt) != (T, V, dt) or grad.device != logits.device:
+        raise ValueError(f"grad must be {logits.dtype} of shape {(T, V)} on {logits.device}")
+    return grad, ld
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def sot_token_logprob(logits, target, temperature=1.0, logp=None, lse=None, stream=None):
+    """Log-probability of one token per row: (logp [T], lse [T]) float32 of logits
+    [T, V] (float32, float16 or bfloat16, any row stride) and target [T].  A
+    target outside [0, V) leaves its row out (both values 0)."""
+    T, V, ld, dt = _rows(logits)
+    dev = logits.device
+    ty = _index(target, "target", (T,), dev)
+    _want(logp, "logp", T, dev)
+    _want(lse, "lse", T, dev)
+    s, (logp, lse) = _stream_of(stream, lambda: (torch.empty(T, device=dev) if logp is None else logp,
+                                                 torch.empty(T, device=dev) if lse is None else lse))
+    rc = load().sot_token_logprob(logits.data_ptr(), T, V, ld, dt, temperature, target.data_ptr(), ty, logp.data_ptr(),
+                                  lse.data_ptr(), s)
+    _check(rc, "sot_token_logprob")
+    return logp, lse
+
+
+def sot_token_logprob_grad(logits, target, lse, grad_logp, temperature=1.0, grad=True, stream=None):
+    """Gradient [T, V] (the logits' type) of sum_t grad_logp[t] logp[t], from the lse of
+    sot_token_logprob.  ``grad`` may be a tensor to write, the logits included."""
+    T, V, ld, dt = _rows(logits)
+    dev = logits.device
+    ty = _index(target, "target", (T,), dev)
+    for t, name in ((lse, "lse"), (grad_logp, "grad_logp")):
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+        _want(t, name, T, dev)
+    s, (grad, ldg) = _stream_of(stream, lambda: _grad_rows(grad, logits, T, V, dt))
+    rc = load().sot_token_logprob_grad(logits.data_ptr(), T, V, ld, dt, temperature, target.data_ptr(), ty,
+                                       lse.data_ptr(), grad_logp.data_ptr(), _at(grad), ldg, s)
+    _check(rc, "sot_token_logprob_grad")
+    return grad
+
+
+def sot_distill_topk(logits, ids, teacher, weight=None, temperature=1.0, tail=False, grad=True, loss=None, stream=None):
+    """Distillation from a teacher's top entries: (loss [T], grad [T, V] or None).
+    ids and teacher are [T, K]; an id outside [0, V) is an unused entry.  Without
+    ``tail`` the teacher values are logits; with it they are log-probabilities and
+    the mass outside the entries is one more outcome.  weight [T] (None = 1/T), 0
+    leaves a row out.  ``grad``: True, False or a tensor (the logits included)."""
+    T, V, ld, dt = _rows(logits)
+    dev = logits.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [rows, entries]")
+    K = ids.shape[1]
+    ty = _index(ids, "ids", (T, K), dev)
+    if not isinstance(teacher, torch.Tensor) or teacher.dtype not in _FLOATS:
+        raise TypeError("teacher must be a float32, float16 or bfloat16 torch.Tensor")
+    _want(teacher, "teacher", T * K, dev, teacher.dtype)
+    _want(weight, "weight", T, dev)
+    _want(loss, "loss", T, dev)
+    s, (loss, (g, ldg)) = _stream_of(stream, lambda: (torch.empty(T, device=dev) if loss is None else loss,
+                                                      _grad_rows(grad, logits, T, V, dt)))
+    rc = load().sot_distill_topk(logits.data_ptr(), T, V, ld, dt, temperature, ids.data_ptr(), ty, teacher.data_ptr(),
+                                 _FLOATS[teacher.dtype], K, 1 if tail else 0, _at(weight), loss.data_ptr(), _at(g), ldg,
+                                 s)
+    _check(rc, "sot_distill_topk")
+    return loss, g
+
+
+def sot_policy_loss(logits, target, old_logp, advantage, ref_logp=None, weight=None, temperature=1.0, clip_low=0.2,
+                    clip_high=0.2, kl_coef=0.0, grad=True, stream=None):
+    """Clipped policy loss with a KL term: (loss [T], logp [T], kl [T], grad [T, V] or
+    None).  old_logp, advantage, ref_logp and weight are [T]; weight None = 1/T, 0
+    leaves a row out, as does a target outside [0, V).  Without ref_logp, kl_coef
+    takes no part.  ``grad``: True, False or a tensor (the logits included)."""
+    T, V, ld, dt = _rows(logits)
+    dev = logits.device
+    ty = _index(target, "target", (T,), dev)
+    for t, name in ((old_logp, "old_logp"), (advantage, "advantage")):
+        if t is None:
+            raise TypeError(f"{name} must be a torch.Tensor")
+        _want(t, name, T, dev)
+    _want(ref_logp, "ref_logp", T, dev)
+    _want(weight, "weight", T, dev)
+    s, (out, (g, ldg)) = _stream_of(stream, lambda: (torch.empty((3, T), device=dev),
+                                                     _grad_rows(grad, logits, T, V, dt)))
+    at = out.data_ptr()
+    rc = load().sot_policy_loss(logits.data_ptr(), T, V, ld, dt, temperature, target.data_ptr(), ty, old_logp.data_ptr(),
+                                _at(ref_logp), advantage.data_ptr(), _at(weight), clip_low, clip_high,
+                                kl_coef if ref_logp is not None else 0.0, at, at + 4 * T, at + 8 * T, _at(g), ldg, s)
+    _check(rc, "sot_policy_loss")
+    loss, logp, kl = out
+    return loss, logp, kl, g
+
+
+def sot_preference_loss(logp, offsets, ref_logp=None, target=None, beta=0.1, label_smoothing=0.0, average=False,
+                        scale=None, stream=None):
+    """Paired preference loss on token log-probabilities [T]: (loss [P], margin [P],
+    grad_logp [T]).  offsets [2P+1] int64 packs chosen, rejected, chosen, ...; a
+    token whose target is negative takes no part.  scale None = 1/P."""
+    if not isinstance(logp, torch.Tensor) or not isinstance(offsets, torch.Tensor):
+        raise TypeError("logp and offsets must be torch.Tensors")
+    dev, T = logp.device, logp.numel()
+    _want(logp, "logp", T, dev)
+    if not logp.is_cuda:
+        raise ValueError("logp must be on a CUDA device")
+    if offsets.numel() % 2 == 0:
+        raise ValueError("offsets must hold 2 P + 1 elements")
+    _want(offsets, "offsets", None, dev, torch.int64)
+    P = offsets.numel() // 2
+    _want(ref_logp, "ref_logp", T, dev)
+    ty = _index(target, "target", (T,), dev) if target is not None else SOT_I32
+    if scale is None:
+        scale = 1.0 / max(P, 1)
+    s, (out, g) = _stream_of(stream, lambda: (torch.empty((2, P), device=dev), torch.empty(T, device=dev)))
+    at = out.data_ptr()
+    rc = load().sot_preference_loss(logp.data_ptr(), _at(ref_logp), _at(target), ty, offsets.data_ptr(), P, T, beta,
+                                    label_smoothing, 1 if average else 0, scale, at, at + 4 * P, g.data_ptr(), s)
+    _check(rc, "sot_preference_loss")
+    loss, margin = out
+    return loss, margin, g
+
+
+def sot_balance_loss(logits, ids, mask=None, balance_coef=1.0, z_coef=0.0, grad=True, stream=None):
+    """A router's balance and z losses with per-expert counts: (counts [E] int32,
+    loss [2], grad [T, E] or None) of router logits [T, E] and the experts chosen,
+    ids [T, K] (outside [0, E): dropped).  mask [T] bool: False leaves a token out."""
+    T, E, ld, dt = _rows(logits)
+    dev = logits.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [rows, choices]")
+    K = ids.shape[1]
+    ty = _index(ids, "ids", (T, K), dev)
+    _want(mask, "mask", T, dev, torch.bool)
+    s, (counts, loss, (g, ldg)) = _stream_of(stream, lambda: (
+        torch.empty(E, dtype=torch.int32, device=dev), torch.empty(2, device=dev), _grad_rows(grad, logits, T, E, dt)))
+    rc = load().sot_balance_loss(logits.data_ptr(), T, E, ld, dt, ids.data_ptr(), ty, K, _at(mask), balance_coef, z_coef,
+                                 counts.data_ptr(), loss.data_ptr(), _at(g), ldg, s)
+    _check(rc, "sot_balance_loss")
+    return counts, loss, g
 
 
 def sot_async_status(stream=None):

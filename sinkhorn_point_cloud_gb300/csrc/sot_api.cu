@@ -20,6 +20,7 @@
 #include "sot.h"
 #include "apml.h"
 #include "hvp.h"
+#include "lm.h"
 #include "tc.h"
 #include "transport.h"
 
@@ -1551,3 +1552,267 @@ extern "C" int sot_potentials_noalloc(const float* X, const float* Y, const floa
     if (e != cudaSuccess) return fail(SOT_ERR_CUDA, "%s", cudaGetErrorString(e));
     return SOT_OK;
 }
+
+// ===========================================================================
+// Language-model training losses (k_lm.cu, k_lm_balance.cu).
+
+namespace {
+
+size_t type_bytes(int type) { return type == SOT_F32 || type == SOT_I32 ? 4 : type == SOT_I64 ? 8 : 2; }
+
+int check_float_type(const char* name, int type) {
+    if (type != SOT_F32 && type != SOT_F16 && type != SOT_BF16)
+        return fail(SOT_ERR_INVALID_ARG, "%s must be SOT_F32, SOT_F16 or SOT_BF16 (got %d)", name, type);
+    return SOT_OK;
+}
+int check_index_type(const char* name, int type) {
+    if (type != SOT_I32 && type != SOT_I64)
+        return fail(SOT_ERR_INVALID_ARG, "%s must be SOT_I32 or SOT_I64 (got %d)", name, type);
+    return SOT_OK;
+}
+int check_pointer(const char* name, const void* p, int type) {
+    if (!p) return fail(SOT_ERR_INVALID_ARG, "%s must not be NULL", name);
+    if ((unsigned long long)p % type_bytes(type))
+        return fail(SOT_ERR_INVALID_ARG, "%s is not aligned to its type", name);
+    return SOT_OK;
+}
+#define SOT_TRY(call)               \
+    do {                            \
+        const int _rc = (call);     \
+        if (_rc != SOT_OK) return _rc; \
+    } while (0)
+
+// Rows of logits and, where it is wanted, of their gradient.
+int check_rows(const void* x, long long T, int V, long long ld, int dtype, const void* grad, long long ldg) {
+    SOT_TRY(check_float_type("dtype", dtype));
+    if (T < 0 || V < 1) return fail(SOT_ERR_INVALID_ARG, "sizes must satisfy T >= 0 and V >= 1 (got T=%lld V=%d)", T, V);
+    if (T >= (1LL << 31)) return fail(SOT_ERR_INVALID_ARG, "T must be < 2^31 (got %lld)", T);
+    if (T == 0) return SOT_OK;
+    if (ld < V || (grad && ldg < V))
+        return fail(SOT_ERR_INVALID_ARG, "a row stride is below the row's length %d", V);
+    if (ld >= (1LL << 30) || (grad && ldg >= (1LL << 30)))
+        return fail(SOT_ERR_INVALID_ARG, "a row stride must be < 2^30 elements");
+    SOT_TRY(check_pointer("logits", x, dtype));
+    if (grad) SOT_TRY(check_pointer("grad", grad, dtype));
+    return SOT_OK;
+}
+int check_temperature(float tau) {
+    if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(1.4426951f / tau))
+        return fail(SOT_ERR_INVALID_ARG, "temperature must be finite and > 0");
+    return SOT_OK;
+}
+int check_row_fits(int dtype, int V, int K) {
+    if (!lm_row_fits(dtype, V, K))
+        return fail(SOT_ERR_UNSUPPORTED, "a row of %d logits does not fit a cluster's shared memory", V);
+    return SOT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sot_token_logprob(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                      const void* target, int target_type, float* logp, float* lse, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_rows(logits, T, V, ld, dtype, nullptr, 0));
+    SOT_TRY(check_temperature(temperature));
+    SOT_TRY(check_index_type("target_type", target_type));
+    SOT_TRY(check_row_fits(dtype, V, 0));
+    if (T == 0) return SOT_OK;
+    SOT_TRY(check_pointer("target", target, target_type));
+    if (!logp && !lse) return fail(SOT_ERR_INVALID_ARG, "logp and lse must not both be NULL");
+    LmRowArgs a = {};
+    a.x = logits;
+    a.T = T;
+    a.V = V;
+    a.ld = ld;
+    a.dtype = dtype;
+    a.tau = temperature;
+    a.target = target;
+    a.target_type = target_type;
+    a.logp = logp;
+    a.lse = lse;
+    SOT_CUDA(launch_lm_row(LM_LOGPROB, a, device_sms(), (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_token_logprob_grad(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                           const void* target, int target_type, const float* lse, const float* grad_logp, void* grad,
+                           long long ld_grad, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_rows(logits, T, V, ld, dtype, grad, ld_grad));
+    SOT_TRY(check_temperature(temperature));
+    SOT_TRY(check_index_type("target_type", target_type));
+    if (T == 0) return SOT_OK;
+    SOT_TRY(check_pointer("target", target, target_type));
+    SOT_TRY(check_pointer("grad", grad, dtype));
+    if (!lse || !grad_logp) return fail(SOT_ERR_INVALID_ARG, "lse and grad_logp must not be NULL");
+    LmGradArgs a = {};
+    a.x = logits;
+    a.T = T;
+    a.V = V;
+    a.ld = ld;
+    a.ldg = ld_grad;
+    a.dtype = dtype;
+    a.tau = temperature;
+    a.target = target;
+    a.target_type = target_type;
+    a.lse = lse;
+    a.g = grad_logp;
+    a.grad = grad;
+    SOT_CUDA(launch_lm_grad(a, (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_distill_topk(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                     const void* ids, int ids_type, const void* teacher, int teacher_type, int K, int tail,
+                     const float* weight, float* loss, void* grad, long long ld_grad, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_rows(logits, T, V, ld, dtype, grad, ld_grad));
+    SOT_TRY(check_temperature(temperature));
+    SOT_TRY(check_index_type("ids_type", ids_type));
+    SOT_TRY(check_float_type("teacher_type", teacher_type));
+    if (K < 1 || K > LM_MAX_K) return fail(SOT_ERR_INVALID_ARG, "K must satisfy 1 <= K <= %d (got %d)", LM_MAX_K, K);
+    if (tail && temperature != 1.f)
+        return fail(SOT_ERR_INVALID_ARG, "the tail outcome needs temperature 1 (the teacher's rest cannot be re-scaled)");
+    SOT_TRY(check_row_fits(dtype, V, K));
+    if (T == 0) return SOT_OK;
+    SOT_TRY(check_pointer("ids", ids, ids_type));
+    SOT_TRY(check_pointer("teacher", teacher, teacher_type));
+    if (!loss && !grad) return fail(SOT_ERR_INVALID_ARG, "loss and grad must not both be NULL");
+    LmRowArgs a = {};
+    a.x = logits;
+    a.T = T;
+    a.V = V;
+    a.ld = ld;
+    a.ldg = ld_grad;
+    a.dtype = dtype;
+    a.grad = grad;
+    a.tau = temperature;
+    a.weight = weight;
+    a.ids = ids;
+    a.ids_type = ids_type;
+    a.K = K;
+    a.teacher = teacher;
+    a.teacher_type = teacher_type;
+    a.tail = tail != 0;
+    a.loss = loss;
+    SOT_CUDA(launch_lm_row(LM_DISTILL, a, device_sms(), (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_policy_loss(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                    const void* target, int target_type, const float* old_logp, const float* ref_logp,
+                    const float* advantage, const float* weight, float clip_low, float clip_high, float kl_coef,
+                    float* loss, float* logp, float* kl, void* grad, long long ld_grad, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_rows(logits, T, V, ld, dtype, grad, ld_grad));
+    SOT_TRY(check_temperature(temperature));
+    SOT_TRY(check_index_type("target_type", target_type));
+    if (!(clip_low >= 0.f) || !(clip_low <= 1.f) || !(clip_high >= 0.f) || !std::isfinite(clip_high))
+        return fail(SOT_ERR_INVALID_ARG, "clip_low must be in [0, 1] and clip_high finite and >= 0");
+    if (!std::isfinite(kl_coef)) return fail(SOT_ERR_INVALID_ARG, "kl_coef must be finite");
+    if (kl_coef != 0.f && !ref_logp && T > 0) return fail(SOT_ERR_INVALID_ARG, "kl_coef needs ref_logp");
+    SOT_TRY(check_row_fits(dtype, V, 0));
+    if (T == 0) return SOT_OK;
+    SOT_TRY(check_pointer("target", target, target_type));
+    if (!old_logp || !advantage) return fail(SOT_ERR_INVALID_ARG, "old_logp and advantage must not be NULL");
+    if (!loss && !logp && !kl && !grad) return fail(SOT_ERR_INVALID_ARG, "no output is wanted");
+    LmRowArgs a = {};
+    a.x = logits;
+    a.T = T;
+    a.V = V;
+    a.ld = ld;
+    a.ldg = ld_grad;
+    a.dtype = dtype;
+    a.grad = grad;
+    a.tau = temperature;
+    a.weight = weight;
+    a.target = target;
+    a.target_type = target_type;
+    a.old_logp = old_logp;
+    a.ref_logp = ref_logp;
+    a.adv = advantage;
+    a.clip_lo = 1.f - clip_low;
+    a.clip_hi = 1.f + clip_high;
+    a.kl_coef = kl_coef;
+    a.loss = loss;
+    a.logp = logp;
+    a.kl = kl;
+    SOT_CUDA(launch_lm_row(LM_POLICY, a, device_sms(), (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_preference_loss(const float* logp, const float* ref_logp, const void* target, int target_type,
+                        const long long* offsets, int P, long long T, float beta, float label_smoothing, int average,
+                        float scale, float* loss, float* margin, float* grad_logp, void* stream) {
+    g_err[0] = 0;
+    if (P < 0 || T < 0 || T >= (1LL << 31))
+        return fail(SOT_ERR_INVALID_ARG, "sizes must satisfy P >= 0 and 0 <= T < 2^31 (got P=%d T=%lld)", P, T);
+    if (!std::isfinite(beta) || !std::isfinite(scale)) return fail(SOT_ERR_INVALID_ARG, "beta and scale must be finite");
+    if (!(label_smoothing >= 0.f) || !(label_smoothing <= 0.5f))
+        return fail(SOT_ERR_INVALID_ARG, "label_smoothing must be in [0, 0.5]");
+    if (target) {
+        SOT_TRY(check_index_type("target_type", target_type));
+        SOT_TRY(check_pointer("target", target, target_type));
+    }
+    if (P > 0 && T > 0 && !logp) return fail(SOT_ERR_INVALID_ARG, "logp must not be NULL");
+    if (P > 0) SOT_TRY(check_pointer("offsets", offsets, SOT_I64));
+    if (P > 0 && !loss && !margin && !grad_logp) return fail(SOT_ERR_INVALID_ARG, "no output is wanted");
+    LmPrefArgs a = {};
+    a.logp = logp;
+    a.ref_logp = ref_logp;
+    a.target = target;
+    a.target_type = target_type;
+    a.offsets = offsets;
+    a.P = P;
+    a.T = T;
+    a.beta = beta;
+    a.smoothing = label_smoothing;
+    a.scale = scale;
+    a.average = average != 0;
+    a.loss = loss;
+    a.margin = margin;
+    a.grad = grad_logp;
+    SOT_CUDA(launch_lm_preference(a, (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_balance_loss(const void* logits, long long T, int E, long long ld, int dtype, const void* ids, int ids_type,
+                     int K, const unsigned char* mask, float balance_coef, float z_coef, int* counts, float* loss,
+                     void* grad, long long ld_grad, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_rows(logits, T, E, ld, dtype, grad, ld_grad));
+    SOT_TRY(check_index_type("ids_type", ids_type));
+    if (E > LM_MAX_E) return fail(SOT_ERR_UNSUPPORTED, "at most %d experts (got %d)", LM_MAX_E, E);
+    if (K < 1 || (long long)K * T >= (1LL << 31))
+        return fail(SOT_ERR_INVALID_ARG, "K must be >= 1 and T K < 2^31 (got T=%lld K=%d)", T, K);
+    if (!std::isfinite(balance_coef) || !std::isfinite(z_coef))
+        return fail(SOT_ERR_INVALID_ARG, "the coefficients must be finite");
+    if (!counts || !loss) return fail(SOT_ERR_INVALID_ARG, "counts and loss must not be NULL");
+    if (T > 0) SOT_TRY(check_pointer("ids", ids, ids_type));
+    Scratch S((cudaStream_t)stream);
+    LmBalanceArgs a = {};
+    a.x = logits;
+    a.T = T;
+    a.E = E;
+    a.ld = ld;
+    a.ldg = ld_grad;
+    a.dtype = dtype;
+    a.ids = ids;
+    a.ids_type = ids_type;
+    a.K = K;
+    a.mask = mask;
+    a.coef = balance_coef;
+    a.z_coef = z_coef;
+    a.counts = counts;
+    a.loss = loss;
+    a.grad = grad;
+    a.kept = S.alloc<int>(1);
+    a.part = S.alloc<float>(2 * (size_t)lm_balance_parts());
+    if (!a.kept || !a.part) return fail(SOT_ERR_NOMEM, "scratch allocation failed");
+    SOT_CUDA(launch_lm_balance(a, (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+}  // extern "C"
