@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(BAL_NT) lm_balance_kernel(LmBalanceArgs a) {
             m = fmaxf(m, v[i]);
         }
         m = warp_max(m);
-        const float u = stab(m);
+        const float u = m == -INFINITY ? 0.f : m;
         float s = 0.f, d = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "sot.h"
+#include "tc_ptx.cuh"
 
 namespace sot {
 
@@ -23,6 +24,7 @@ struct Elem<SOT_F32> {
 template <>
 struct Elem<SOT_F16> {
     using T = __half;
+    using T2 = __half2;
     static constexpr int N = 8;
     __device__ static float get(T v) { return __half2float(v); }
     __device__ static T put(float v) { return __float2half_rn(v); }
@@ -30,10 +32,22 @@ struct Elem<SOT_F16> {
 template <>
 struct Elem<SOT_BF16> {
     using T = __nv_bfloat16;
+    using T2 = __nv_bfloat162;
     static constexpr int N = 8;
     __device__ static float get(T v) { return __bfloat162float(v); }
     __device__ static T put(float v) { return __float2bfloat16_rn(v); }
 };
+
+// Packed product of two floats by two (one instruction, each lane rounded as the scalar product).
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2,%3};\n\tmov.b64 rb, {%4,%5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0,%1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
 // 16 bytes <-> N floats, in pairs.
 template <int DT>
@@ -54,6 +68,46 @@ __device__ __forceinline__ void unpack(const uint4& v, float2 (&f)[Elem<DT>::N /
             }
         }
     }
+}
+// Largest of the N elements (packed maxima for the 16-bit types; NaN is passed over).
+template <int DT>
+__device__ __forceinline__ float max_of(const uint4& v) {
+    if constexpr (DT == SOT_F32) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else if constexpr (DT == SOT_BF16) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return __bfloat162float(__hmax(m.x, m.y));
+    } else {
+        const __half2* h = reinterpret_cast<const __half2*>(&v);
+        const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return __half2float(__hmax(__low2half(m), __high2half(m)));
+    }
+}
+// Largest elements of two vectors, element by element.
+template <int DT>
+__device__ __forceinline__ uint4 max2(const uint4& a, const uint4& b) {
+    uint4 r;
+    if constexpr (DT == SOT_F32) {
+        r.x = __float_as_uint(fmaxf(__uint_as_float(a.x), __uint_as_float(b.x)));
+        r.y = __float_as_uint(fmaxf(__uint_as_float(a.y), __uint_as_float(b.y)));
+        r.z = __float_as_uint(fmaxf(__uint_as_float(a.z), __uint_as_float(b.z)));
+        r.w = __float_as_uint(fmaxf(__uint_as_float(a.w), __uint_as_float(b.w)));
+    } else {
+        using H = typename Elem<DT>::T2;
+        const H *p = reinterpret_cast<const H*>(&a), *q = reinterpret_cast<const H*>(&b);
+        H* o = reinterpret_cast<H*>(&r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = __hmax2(p[i], q[i]);
+    }
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ float max_of(const float2 (&f)[Elem<DT>::N / 2]) {
+    float mx = fmaxf(f[0].x, f[0].y);
+#pragma unroll
+    for (int i = 1; i < Elem<DT>::N / 2; ++i) mx = fmaxf(mx, fmaxf(f[i].x, f[i].y));
+    return mx;
 }
 template <int DT>
 __device__ __forceinline__ uint4 pack(const float2 (&f)[Elem<DT>::N / 2]) {
@@ -89,60 +143,99 @@ __device__ __forceinline__ int load_index(const void* p, int type, long long i, 
     return v >= 0 && v < n ? (int)v : -1;
 }
 
-// Softmax statistics of a set of logits: m = max x, s = sum exp2((x - m) sc)
-// with sc = log2(e) / temperature.  The difference is taken before the
-// scaling, so logits near the type's largest and lowest values neither
-// overflow nor lose a row of equal lowest values.  A set whose largest value
-// is -inf has s = 0: its stabiliser is taken as 0.
+// Softmax statistics of a set of logits with sc = log2(e) / temperature: its
+// largest value m and s = sum exp2(x sc - m2), m2 = m sc rounded to 32 bits.
+// Taking the rounded m2 everywhere (sums, joins, probabilities) makes its
+// rounding cancel; only the fused x sc - m2 is rounded, at the size of the
+// result.  Where m2 overflows (m near the type's lowest or largest value) the
+// neighbouring numbers are so far apart that only logits equal to m have any
+// weight: s counts those.  A set of nothing but -inf has s = 0.
 struct MS {
     float m, s;
 };
-__device__ __forceinline__ float stab(float m) { return m == -INFINITY ? 0.f : m; }
+// Weight of a logit x <= m against stabiliser m.
+__device__ __forceinline__ float weight_of(float x, float m, float sc) {
+    const float m2 = __fmul_rn(m, sc);
+    if (fabsf(m2) < INFINITY) return ex2f(fmaf(x, sc, -m2));
+    return x - m == 0.f ? 1.f : 0.f;
+}
+// Factor that takes sums against stabiliser m to stabiliser M >= m.
+__device__ __forceinline__ float rescale(float m, float M, float sc) {
+    const float M2 = __fmul_rn(M, sc);
+    if (fabsf(M2) < INFINITY) return ex2f(__fsub_rn(__fmul_rn(m, sc), M2));  // not fused: the rounded products
+    return m - M == 0.f ? 1.f : 0.f;
+}
 __device__ __forceinline__ MS ms_combine(MS a, MS b, float sc) {
-    const float M = fmaxf(a.m, b.m), u = stab(M);
-    return MS{M, a.s * ex2f((a.m - u) * sc) + b.s * ex2f((b.m - u) * sc)};
+    const float M = fmaxf(a.m, b.m);
+    return MS{M, a.s * rescale(a.m, M, sc) + b.s * rescale(b.m, M, sc)};
+}
+// Largest value of a warp, in every lane: one reduction instruction.
+__device__ __forceinline__ float warp_max1(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 __device__ __forceinline__ MS ms_warp(MS v, float sc) {
+    const float M = warp_max1(v.m);
+    return MS{M, warp_sum(v.s * rescale(v.m, M, sc))};
+}
+
+// exp2(x sc - u) of a pair.
+__device__ __forceinline__ float2 ex2_pair(float2 x, float u, float sc) {
+    const float2 t = ffma2(x, make_float2(sc, sc), make_float2(-u, -u));
+    return make_float2(ex2f(t.x), ex2f(t.y));
+}
+
+// A thread's running statistics: s in two halves, u = m sc where that is
+// finite; `far` where it is not (s then counts the logits equal to m).
+struct Running {
+    float m, u;
+    float2 s;
+    bool far;
+    __device__ __forceinline__ Running() : m(-INFINITY), u(0.f), s(make_float2(0.f, 0.f)), far(false) {}
+    // mx: the largest of the logits that come next
+    __device__ __forceinline__ void raise(float mx, float sc) {
+        if (mx > m) {
+            const float k = rescale(m, mx, sc);
+            s = fmul2(s, make_float2(k, k));
+            m = mx;
+            const float v = __fmul_rn(mx, sc);
+            far = !(fabsf(v) < INFINITY);
+            u = far ? 0.f : v;
+        }
+    }
+    template <int P>
+    __device__ __forceinline__ void add(const float2 (&f)[P], float sc) {
+        if (!far) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) s = fadd2(s, ex2_pair(f[i], u, sc));
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                s = fadd2(s, make_float2(f[i].x - m == 0.f ? 1.f : 0.f, f[i].y - m == 0.f ? 1.f : 0.f));
+        }
+    }
+};
+
+// log s for s > 0 as an unevaluated sum, absolute error near 2^-25: s = 2^e f with
+// f in [0.75, 1.5), e times a 12-bit head of ln 2 is exact, the rest is rounded
+// at the size of log f.  +-0, infinities and NaN go to logf.
+__device__ __forceinline__ float2 log_ff(float s) {
+    if (!(s >= 1.17549435e-38f && s < INFINITY)) return make_float2(logf(s), 0.f);
+    constexpr float head = 2839.f / 4096.f, rest = (float)(0.69314718055994530942 - 2839.0 / 4096.0);
+    const int e = (int)(__float_as_uint(s) - 0x3f400000u) >> 23;
+    const float f = __uint_as_float(__float_as_uint(s) - ((uint32_t)e << 23));
+    const float2 r = two_sum(__fmul_rn((float)e, head), fmaf((float)e, rest, logf(f)));
+    return r;
+}
+__device__ __forceinline__ double to_double(float2 v) { return (double)v.x + (double)v.y; }
+__device__ __forceinline__ float2 ff_warp_sum(float2 v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        MS w;
-        w.m = __shfl_xor_sync(0xffffffffu, v.m, o);
-        w.s = __shfl_xor_sync(0xffffffffu, v.s, o);
-        v = ms_combine(v, w, sc);
+        const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
+        v = ff_add(v, w);
     }
     return v;
-}
-
-// Adds N logits to a thread's running statistics.
-template <int DT>
-__device__ __forceinline__ void ms_add(MS& r, const float2 (&f)[Elem<DT>::N / 2], float sc) {
-    constexpr int P = Elem<DT>::N / 2;
-    float mx = fmaxf(f[0].x, f[0].y);
-#pragma unroll
-    for (int i = 1; i < P; ++i) mx = fmaxf(mx, fmaxf(f[i].x, f[i].y));
-    if (mx > r.m) {
-        r.s *= ex2f((r.m - mx) * sc);
-        r.m = mx;
-    }
-    const float u = stab(r.m);
-    float2 t = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const float2 d = fadd2(f[i], make_float2(-u, -u));
-        t = fadd2(t, make_float2(ex2f(d.x * sc), ex2f(d.y * sc)));
-    }
-    r.s += t.x + t.y;
-}
-
-// log s for s > 0 with an absolute error near 2^-25: the exponent's part is
-// exact in 64 bits, the rest is the logarithm of a number in [0.75, 1.5).
-// +-0, infinities and NaN go to logf.
-__device__ __forceinline__ double log_wide(float s) {
-    if (!(s >= 1.17549435e-38f && s < INFINITY)) return (double)logf(s);
-    const uint32_t b = __float_as_uint(s) - 0x3f400000u;
-    const int e = (int)b >> 23;
-    const float f = __uint_as_float(__float_as_uint(s) - ((uint32_t)e << 23));
-    return (double)e * 0.69314718055994530942 + (double)logf(f);
 }
 
 // exp(u) - u - 1 without the cancellation of small u (Taylor series to u^9).
@@ -176,12 +269,38 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Store to the same shared-memory location in CTA `rank` of the cluster.
-__device__ __forceinline__ void cluster_store(const float* local_ptr, uint32_t rank, float v) {
-    const uint32_t la = (uint32_t)__cvta_generic_to_shared(local_ptr);
+// The address in CTA `rank` of the cluster of a shared-memory address of this one.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     uint32_t ra;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(la), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(rank));
+    return ra;
+}
+__device__ __forceinline__ void cluster_store(uint32_t ra, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ra), "f"(v) : "memory");
+}
+// Arrives on a barrier of another CTA, after this thread's stores to it.
+__device__ __forceinline__ void cluster_arrive(uint32_t ra) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
+}
+// mbar_wait_bounded for a barrier that other CTAs of the cluster arrive on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                  uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > limit_ns) {
+            *abort = 1;
+            return false;
+        }
+    }
 }
 
 }  // namespace sot

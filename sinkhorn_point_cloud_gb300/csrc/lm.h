@@ -20,6 +20,7 @@ struct LmRowArgs {
     int V, dtype;
     void* grad;  // NULL: losses only
     float tau;
+    double inv_tau;
     const float* weight;  // NULL: every row weighs 1/T
     // token log-probability and policy loss
     const void* target;

@@ -1622,6 +1622,7 @@ int sot_token_logprob(const void* logits, long long T, int V, long long ld, int 
     SOT_TRY(check_pointer("target", target, target_type));
     if (!logp && !lse) return fail(SOT_ERR_INVALID_ARG, "logp and lse must not both be NULL");
     LmRowArgs a = {};
+    a.inv_tau = 1.0 / (double)temperature;
     a.x = logits;
     a.T = T;
     a.V = V;
@@ -1681,6 +1682,7 @@ int sot_distill_topk(const void* logits, long long T, int V, long long ld, int d
     SOT_TRY(check_pointer("teacher", teacher, teacher_type));
     if (!loss && !grad) return fail(SOT_ERR_INVALID_ARG, "loss and grad must not both be NULL");
     LmRowArgs a = {};
+    a.inv_tau = 1.0 / (double)temperature;
     a.x = logits;
     a.T = T;
     a.V = V;
@@ -1719,6 +1721,7 @@ int sot_policy_loss(const void* logits, long long T, int V, long long ld, int dt
     if (!old_logp || !advantage) return fail(SOT_ERR_INVALID_ARG, "old_logp and advantage must not be NULL");
     if (!loss && !logp && !kl && !grad) return fail(SOT_ERR_INVALID_ARG, "no output is wanted");
     LmRowArgs a = {};
+    a.inv_tau = 1.0 / (double)temperature;
     a.x = logits;
     a.T = T;
     a.V = V;
