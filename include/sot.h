@@ -326,8 +326,6 @@ enum sot_dtype { SOT_F32 = 0, SOT_F16 = 1, SOT_BF16 = 2, SOT_I32 = 3, SOT_I64 = 
  * under an old or a reference model):
  *   logp[t] = y[t][target[t]] - lse[t]      (either output may be NULL)
  * A target outside [0, V) leaves its row out: it is not read, logp = lse = 0.
- * SOT_ERR_UNSUPPORTED when a row does not fit the shared memory of a cluster of
- * eight (above 800000 16-bit or 400000 32-bit logits).
  */
 int sot_token_logprob(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
                       const void* target, int target_type, float* logp, float* lse, void* stream);
@@ -359,6 +357,8 @@ int sot_token_logprob_grad(const void* logits, long long T, int V, long long ld,
  *   grad = d(sum_t loss) / d logits (NULL: losses only; loss may be NULL instead).
  * weight NULL = 1/T.  A row of weight 0 is left out: not read, loss and gradient 0.
  * A row without used entries has loss 0 and, without tail, gradient 0.
+ * SOT_ERR_UNSUPPORTED with tail = 1 above 12 million 16-bit or 6 million 32-bit
+ * columns (a mark for each 16 bytes of a row is kept in shared memory).
  */
 int sot_distill_topk(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
                      const void* ids, int ids_type, const void* teacher, int teacher_type, int K, int tail,

@@ -2,6 +2,8 @@
 // log-probabilities from a known log-sum-exp, and the paired preference loss.
 #include <cuda_runtime.h>
 
+#include <cstdlib>
+#include <cstdio>
 #include "kernels.h"
 #include "lm_row.cuh"
 #include "tc.h"
@@ -110,39 +112,59 @@ __global__ void __launch_bounds__(PREF_NT) lm_preference_kernel(LmPrefArgs a) {
 
 int row_granule(int dtype) { return dtype == SOT_F32 ? 4 : 8; }
 
-// Shared memory of a CTA's ring, and how a row is cut.
-bool row_plan(int dtype, int V, int K, int sms, LmRowPlan* p) {
+// How a row is cut and who works on it.
+void row_plan(bool grads, long long T, int dtype, int V, int K, bool tail, int sms, LmRowPlan* p) {
     const int N = row_granule(dtype);
     const long long total = ((long long)V + 2 * N - 2) / N;  // granules, whatever the row's alignment
-    const long long row = total * 16;
-    const size_t most = 220u * 1024;
-    auto fill = [&](int NW, int CL, int ST, int lag) {
+    const auto plan = [&](int NW, int CL) {
         const long long G = (total + CL - 1) / CL;
-        const size_t smem = NW == 1 ? ((size_t)G * 32 + (size_t)K * 12) * WARP_ROWS : ((size_t)G * 16 + (size_t)K * 12) * ST;
-        if (smem > most) return false;
-        *p = LmRowPlan{NW, CL, (int)G, ST, lag, smem, sms};
-        return true;
+        const size_t smem = NW == 1 ? ((size_t)G * 32 + (size_t)K * 12) * WARP_ROWS
+                                    : (size_t)K * 12 + (tail ? ((size_t)G + 3) / 4 * 4 : 0);
+        *p = LmRowPlan{NW, CL, (int)G, smem, sms};
     };
-    if (row <= 8 * 1024 && fill(1, 1, 2, 0)) return true;
-    if (row <= 24 * 1024 && fill(4, 1, 3, 1)) return true;
-    for (int CL = 1; CL <= ROW_MAX_CL; CL *= 2)
-        if (row <= (long long)CL * 72 * 1024 && fill(16, CL, 3, 1)) return true;
-    for (int ST = 3; ST >= 1; --ST)
-        if (fill(16, ROW_MAX_CL, ST, ST > 1)) return true;
-    return false;
+    const auto warps = [](long long G, int per) { return G <= per * 128ll ? 4 : G <= per * 256ll ? 8 : 16; };
+    if (const char* e = getenv("LM_TUNE")) {
+        int nw, cl;
+        if (sscanf(e, "%d,%d", &nw, &cl) == 2) { plan(nw, cl); return; }
+    }
+    // Up to 8 KB a warp takes the row alone: 16384 rows of 4096 bf16 with gradient take
+    // 57 us, with a CTA each 81 us; at 6144 a CTA is as fast (95 us both).
+    if (total <= 528) {
+        plan(1, 1);
+    } else if (T < sms) {
+        // Few rows: cut a row further, down to 512 granules a CTA, while the SMs have
+        // room, and give it enough warps for eight granules a thread.
+        int CL = 1;
+        while (CL < ROW_MAX_CL && T * CL * 2 <= sms && total / (2 * CL) >= 512) CL *= 2;
+        plan(warps((total + CL - 1) / CL, 8), CL);
+    } else if (!grads) {
+        // Read once: small CTAs, many on an SM (2048 rows of 131072 bf16: 80 us, with
+        // 16 warps 86 us).
+        plan(4, 1);
+    } else {
+        // Read twice: a thread takes up to 26 granules.  Smaller CTAs spend more on
+        // starting (16384 rows of 16384 bf16: 4 warps 175 us, 8 warps 189 us); larger
+        // shares keep more rows under way than L2 holds until their second pass (8192
+        // rows of 65536, a third left out: 16 warps 284 us, 8 warps 320 us).
+        int CL = 1;
+        while (CL < ROW_MAX_CL && total > CL * 26ll * 512) CL *= 2;
+        plan(warps((total + CL - 1) / CL, 26), CL);
+    }
 }
 
 }  // namespace
 
-bool lm_row_fits(int dtype, int V, int K) {
+bool lm_tail_fits(int dtype, int V, int K) {
     LmRowPlan p;
-    return row_plan(dtype, V, K, 0, &p);
+    row_plan(true, 1ll << 31, dtype, V, K, true, 1, &p);
+    return p.smem <= 200 * 1024;
 }
 
 cudaError_t launch_lm_row(LmOp op, const LmRowArgs& a, int sms, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     LmRowPlan p;
-    if (!row_plan(a.dtype, a.V, a.K, sms, &p)) return cudaErrorInvalidValue;
+    row_plan(op != LM_LOGPROB, a.T, a.dtype, a.V, a.K, a.tail != 0, sms, &p);
+    if (a.T * p.CL > 0x7fffffffll) return cudaErrorInvalidValue;
     LmRowLaunch L = {};
     tc_test_hold(&L.hold, &L.wait_ns);
     cudaError_t e = async_status_address(&L.status);

@@ -84,6 +84,31 @@ __device__ __forceinline__ float max_of(const uint4& v) {
         return __half2float(__hmax(__low2half(m), __high2half(m)));
     }
 }
+// L2 eviction policies of 16-byte accesses: what is read again soon stays longest,
+// what is read for the last time or written goes first.
+__device__ __forceinline__ uint64_t policy_keep() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t policy_drop() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint4 load16(const uint4* p, uint64_t policy) {
+    uint4 v;
+    asm("ld.global.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p), "l"(policy));
+    return v;
+}
+__device__ __forceinline__ void store16(uint4* p, const uint4& v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1,%2,%3,%4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w), "l"(policy)
+                 : "memory");
+}
+
 // Largest elements of two vectors, element by element.
 template <int DT>
 __device__ __forceinline__ uint4 max2(const uint4& a, const uint4& b) {
@@ -101,13 +126,6 @@ __device__ __forceinline__ uint4 max2(const uint4& a, const uint4& b) {
         for (int i = 0; i < 4; ++i) o[i] = __hmax2(p[i], q[i]);
     }
     return r;
-}
-template <int DT>
-__device__ __forceinline__ float max_of(const float2 (&f)[Elem<DT>::N / 2]) {
-    float mx = fmaxf(f[0].x, f[0].y);
-#pragma unroll
-    for (int i = 1; i < Elem<DT>::N / 2; ++i) mx = fmaxf(mx, fmaxf(f[i].x, f[i].y));
-    return mx;
 }
 template <int DT>
 __device__ __forceinline__ uint4 pack(const float2 (&f)[Elem<DT>::N / 2]) {
@@ -144,7 +162,8 @@ __device__ __forceinline__ int load_index(const void* p, int type, long long i, 
 }
 
 // Softmax statistics of a set of logits with sc = log2(e) / temperature: its
-// largest value m and s = sum exp2(x sc - m2), m2 = m sc rounded to 32 bits.
+// stabiliser m (its largest value, or one near enough for the sums' range) and
+// s = sum exp2(x sc - m2), m2 = m sc rounded to 32 bits.
 // Taking the rounded m2 everywhere (sums, joins, probabilities) makes its
 // rounding cancel; only the fused x sc - m2 is rounded, at the size of the
 // result.  Where m2 overflows (m near the type's lowest or largest value) the
@@ -153,7 +172,7 @@ __device__ __forceinline__ int load_index(const void* p, int type, long long i, 
 struct MS {
     float m, s;
 };
-// Weight of a logit x <= m against stabiliser m.
+// Weight of a logit x against stabiliser m.
 __device__ __forceinline__ float weight_of(float x, float m, float sc) {
     const float m2 = __fmul_rn(m, sc);
     if (fabsf(m2) < INFINITY) return ex2f(fmaf(x, sc, -m2));
@@ -186,34 +205,74 @@ __device__ __forceinline__ float2 ex2_pair(float2 x, float u, float sc) {
     return make_float2(ex2f(t.x), ex2f(t.y));
 }
 
-// A thread's running statistics: s in two halves, u = m sc where that is
-// finite; `far` where it is not (s then counts the logits equal to m).
+// A thread's running statistics: s (in two halves) against stabiliser m, u = m sc
+// where that is finite; `far` where it is not (s then counts the logits equal to
+// m).  Nothing needs m to be the largest value, only the sums to stay clear of
+// overflow and underflow, and logits seldom leave the range where the first
+// guess, 0, does that.  So a batch is summed against the m at hand, with no
+// maximum to wait for, and only a batch whose sum comes out beyond 2^60 or
+// below 2^-40 is looked at again.
 struct Running {
     float m, u;
     float2 s;
     bool far;
-    __device__ __forceinline__ Running() : m(-INFINITY), u(0.f), s(make_float2(0.f, 0.f)), far(false) {}
-    // mx: the largest of the logits that come next
-    __device__ __forceinline__ void raise(float mx, float sc) {
-        if (mx > m) {
-            const float k = rescale(m, mx, sc);
+    __device__ __forceinline__ Running() : m(0.f), u(0.f), s(make_float2(0.f, 0.f)), far(false) {}
+
+    template <int DT>
+    __device__ __forceinline__ float2 sum(const uint4& v, float sc) const {
+        float2 f[Elem<DT>::N / 2], t = make_float2(0.f, 0.f);
+        unpack<DT>(v, f);
+        if (!far) {
+#pragma unroll
+            for (int i = 0; i < Elem<DT>::N / 2; ++i) t = fadd2(t, ex2_pair(f[i], u, sc));
+        } else {
+#pragma unroll
+            for (int i = 0; i < Elem<DT>::N / 2; ++i)
+                t = fadd2(t, make_float2(f[i].x - m == 0.f ? 1.f : 0.f, f[i].y - m == 0.f ? 1.f : 0.f));
+        }
+        return t;
+    }
+    // A batch with largest value mx whose sum is out of range: m moves to mx if
+    // that is larger, or if nothing has been summed yet.
+    __device__ __forceinline__ void move(float mx, float sc) {
+        const bool none = s.x == 0.f && s.y == 0.f;
+        if ((none && mx > -INFINITY) || mx > m) {
+            const float k = none ? 0.f : rescale(m, mx, sc), v = __fmul_rn(mx, sc);
             s = fmul2(s, make_float2(k, k));
             m = mx;
-            const float v = __fmul_rn(mx, sc);
             far = !(fabsf(v) < INFINITY);
             u = far ? 0.f : v;
         }
     }
-    template <int P>
-    __device__ __forceinline__ void add(const float2 (&f)[P], float sc) {
+    template <int DT, int P>
+    __device__ __forceinline__ void add(const uint4 (&v)[P], float sc) {
+        float2 t = make_float2(0.f, 0.f);
         if (!far) {
+            float2 f[Elem<DT>::N / 2];
 #pragma unroll
-            for (int i = 0; i < P; ++i) s = fadd2(s, ex2_pair(f[i], u, sc));
-        } else {
+            for (int j = 0; j < P; ++j) {
+                unpack<DT>(v[j], f);
+                float2 w = ex2_pair(f[0], u, sc);
 #pragma unroll
-            for (int i = 0; i < P; ++i)
-                s = fadd2(s, make_float2(f[i].x - m == 0.f ? 1.f : 0.f, f[i].y - m == 0.f ? 1.f : 0.f));
+                for (int i = 1; i < Elem<DT>::N / 2; ++i) w = fadd2(w, ex2_pair(f[i], u, sc));
+                t = fadd2(t, w);
+            }
         }
+        const float both = t.x + t.y;
+        if (!(both > 9.094947e-13f && both < 1.1529215e18f)) {
+            uint4 top = v[0];
+#pragma unroll
+            for (int j = 1; j < P; ++j) top = max2<DT>(top, v[j]);
+            move(max_of<DT>(top), sc);
+            t = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < P; ++j) t = fadd2(t, sum<DT>(v[j], sc));
+        }
+        s = fadd2(s, t);
+    }
+    __device__ __forceinline__ MS result() const {
+        const float both = s.x + s.y;
+        return MS{both == 0.f ? -INFINITY : m, both};
     }
 };
 
@@ -269,6 +328,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Its two halves, without ordering memory: this CTA has started; all have.
+__device__ __forceinline__ void cluster_arrive_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // The address in CTA `rank` of the cluster of a shared-memory address of this one.
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     uint32_t ra;
@@ -282,25 +348,31 @@ __device__ __forceinline__ void cluster_store(uint32_t ra, float v) {
 __device__ __forceinline__ void cluster_arrive(uint32_t ra) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
 }
-// mbar_wait_bounded for a barrier that other CTAs of the cluster arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort,
-                                                  uint64_t limit_ns) {
+// Waits for a phase of a barrier, other CTAs' arrivals included; the thread sleeps
+// in the hardware for up to 2 us at a time.  Gives up like mbar_wait_bounded.
+__device__ __forceinline__ bool row_try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+static __device__ __noinline__ bool row_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok) return true;
+        if (row_try_wait(bar, parity)) return true;
         if (*abort) return false;
         if (globaltimer_ns() - t0 > limit_ns) {
             *abort = 1;
             return false;
         }
     }
+}
+__device__ __forceinline__ bool row_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
+    return row_try_wait(bar, parity) || row_wait_slow(bar, parity, abort, limit_ns);
 }
 
 }  // namespace sot

@@ -3,21 +3,20 @@
 // A row x of V logits at temperature tau has p = softmax(x / tau).  Every loss
 // here depends on the row through log p at a few columns, so its gradient is
 //   dx_v = c p_v   at every column, corrected at those few columns,
-// with c known once the row's log-sum-exp is.  The row stays in shared memory
-// between the two, so it is read from memory once and its gradient written
-// once, the least any form can do; memory traffic is what bounds the kernel.
+// with c known once the row's log-sum-exp is.  Memory traffic bounds all of it:
+// the least is one read of the row and one write of the gradient.
 //
-// One thread-block cluster takes a row, each CTA a slice of it, and the grid
-// stays resident and walks the rows through a ring of stages.  A stage has a
-// warp of its own for everything about its row but the row itself: it starts
-// the row's bulk copy, prepares the teacher's side while the copy is under way,
-// joins the slice's statistics, exchanges them with the other CTAs through
-// distributed shared memory, forms the loss and the gradient's coefficients,
-// corrects the few columns at the end and starts the next copy.  The consumer
-// warps only stream: statistics of row i, then the gradient of row i - lag, so
-// the stage warps' latencies pass while the consumers have other rows to work on.
-// Every wait is bounded; one that runs out ends the CTA's loops, leaves NaN
-// losses and reports through sot_async_status.
+// lm_row_kernel: a CTA takes a row, or a cluster of CTAs a slice of it each, in
+// two passes: statistics, then the gradient.  The second pass reads the row
+// again, from L2 or L1, where it still is: the rows under way at one time take
+// less than half of L2.  Several CTAs share an SM and are in different phases, so
+// loads, reductions and stores of different rows overlap without any hand-over
+// inside a CTA.  A warp of its own prepares the teacher's side during the first
+// pass, joins the statistics (with the cluster's other CTAs through distributed
+// shared memory) and forms the loss and the gradient's coefficients.
+//
+// lm_warp_kernel: short rows, a warp each, kept in shared memory between the
+// passes.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -27,12 +26,12 @@
 namespace sot {
 
 constexpr int ROW_MAX_CL = 8;
-constexpr int ROW_MAX_ST = 4;
-constexpr int NREC = 6;  // a CTA's record: (m, s), the entries' (m, s), a 64-bit sum
+constexpr int ROW_MAX_NW = 16;  // streaming warps of a CTA
+constexpr int NREC = 6;         // a CTA's record: (m, s), the entries' (m, s), the entries' sum q x in two parts
 
 struct LmRowLaunch {
-    int CL, G, ST, lag;          // CTAs a row, granules a slice, stages, rows between statistics and gradient
-    int hold;                    // testing hook: no copy from this row of a cluster on (-1: off)
+    int CL, G;                   // CTAs a row, granules a slice
+    int hold;                    // testing hook: no copy from this row of a warp on (-1: off)
     unsigned long long wait_ns;  // limit of every wait
     unsigned* status;            // the device's status word of asynchronous calls
 };
@@ -106,21 +105,6 @@ __device__ __forceinline__ void mask_cols(float2 (&f)[Elem<DT>::N / 2], int e, i
     }
 }
 
-// Barriers of a stage: its copy has landed; (tail) the entries are taken out of
-// the slice; the slice's statistics, the coefficients, the gradient are done;
-// the other CTAs' records have arrived (two, used in turn).
-enum { RB_FULL = 0, RB_CUT, RB_REC, RB_COEF, RB_GRAD, RB_MAIL, RB_COUNT = RB_MAIL + 2 };
-
-template <int NW>
-struct RowShared {
-    uint64_t bar[ROW_MAX_ST][RB_COUNT];
-    MS rec[ROW_MAX_ST][NW];
-    RowCoef coef[ROW_MAX_ST];
-    float mail[ROW_MAX_ST][2][ROW_MAX_CL][NREC];
-    int keep[ROW_MAX_ST];
-    int abort;
-};
-
 // The teacher's entries of a row (one warp): weights q in eq, columns in eid
 // (-1: unused), and the sums Q = sum q and B = sum q log q.
 __device__ __forceinline__ void teacher_side(const LmRowArgs& a, long long row, float* eq, int* eid, float2& Q, float2& B) {
@@ -175,56 +159,84 @@ __device__ __forceinline__ float2 ff_sum_or_far(float2 v) {
     return fabsf(f) < INFINITY ? s : make_float2(f, 0.f);
 }
 
-// The entries' logits in this slice: ex, D = sum q x, and for the tail their
-// statistics, with the entries themselves taken out of the slice.
+// The entries' logits in columns [c0, c1) of a row at x: ex, D = sum q x; eid
+// becomes -1 for the others.  For the tail also the entries' statistics.
 template <int DT>
-__device__ __forceinline__ void student_side(const LmRowArgs& a, const Slice& s, typename Elem<DT>::T* se, float* ex,
+__device__ __forceinline__ void student_side(const LmRowArgs& a, int c0, int c1, const typename Elem<DT>::T* x, float* ex,
                                              const float* eq, int* eid, float sc, float2& D, MS& top) {
     const int lane = threadIdx.x & 31;
-    const int e_end = s.e0 + s.ng * Elem<DT>::N;
     D = make_float2(0.f, 0.f);
     top = MS{-INFINITY, 0.f};
-    for (int k = lane; k < a.K; k += 32) {
-        const int id = eid[k];
-        float v = -INFINITY;
-        if (id >= 0 && id >= s.e0 && id < e_end) {
-            v = Elem<DT>::get(se[id - s.e0]);
-            if (eq[k] != 0.f) D = fabsf(v) < INFINITY ? ff_add(D, two_prod(eq[k], v)) : make_float2(D.x + v, 0.f);
-            if (a.tail) {
-                se[id - s.e0] = Elem<DT>::put(-INFINITY);
-                top.m = fmaxf(top.m, v);
+    for (int k0 = 0; k0 < a.K; k0 += 128) {  // four loads in flight a lane
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = k0 + 32 * j + lane, id = k < a.K ? eid[k] : -1;
+            v[j] = id >= 0 && id >= c0 && id < c1 ? Elem<DT>::get(x[id]) : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = k0 + 32 * j + lane;
+            if (k >= a.K) continue;
+            ex[k] = v[j];
+            const int id = eid[k];
+            if (!(id >= 0 && id >= c0 && id < c1)) {
+                eid[k] = -1;
+                continue;
             }
-        } else
-            eid[k] = -1;  // not this CTA's
-        ex[k] = v;
+            if (eq[k] != 0.f) D = fabsf(v[j]) < INFINITY ? ff_add(D, two_prod(eq[k], v[j])) : make_float2(D.x + v[j], 0.f);
+            top.m = fmaxf(top.m, v[j]);
+        }
     }
     D = ff_sum_or_far(D);
     if (a.tail) {
         top.m = warp_max1(top.m);
-        for (int k = lane; k < a.K; k += 32) top.s += weight_of(ex[k], top.m, sc);
+        for (int k = lane; k < a.K; k += 32)
+            if (eid[k] >= 0) top.s += weight_of(ex[k], top.m, sc);
         top.s = top.m == -INFINITY ? 0.f : warp_sum(top.s);
-        fence_proxy_async_smem();  // the removals come before the stage's next copy
-        __syncwarp();
     }
 }
 
-// What a row's stage warp knows of the row before its copy starts.
+// What is known of a row before its copy starts.  RowLoad holds it as it was
+// loaded: nothing is computed from it, so a load for a later row is waited for
+// only when that row's turn comes.
 struct RowMeta {
     int tgt;
     float w, old, ref, adv;
     bool keep;
 };
+struct RowLoad {
+    int t32;
+    long long t64;
+    float w, old, ref, adv;
+};
 template <int OP>
-__device__ __forceinline__ RowMeta row_meta(const LmRowArgs& a, long long row) {
-    RowMeta m;
-    m.tgt = OP == LM_DISTILL ? 0 : load_index(a.target, a.target_type, row, a.V);
-    m.w = OP == LM_LOGPROB ? 1.f : a.weight ? a.weight[row] : 1.f / (float)a.T;
-    m.old = m.ref = m.adv = 0.f;
-    if (OP == LM_POLICY) {
+__device__ __forceinline__ RowLoad row_load(const LmRowArgs& a, long long row, bool all) {
+    RowLoad m;
+    m.t32 = 0;
+    m.t64 = 0;
+    m.w = m.old = m.ref = m.adv = 0.f;
+    if (OP != LM_DISTILL) {
+        if (a.target_type == SOT_I64) m.t64 = static_cast<const long long*>(a.target)[row];
+        else m.t32 = static_cast<const int*>(a.target)[row];
+    }
+    if (OP != LM_LOGPROB && a.weight) m.w = a.weight[row];
+    if (OP == LM_POLICY && all) {
         m.old = a.old_logp[row];
         m.adv = a.adv[row];
         if (a.ref_logp) m.ref = a.ref_logp[row];
     }
+    return m;
+}
+template <int OP>
+__device__ __forceinline__ RowMeta row_meta(const LmRowArgs& a, const RowLoad& l) {
+    RowMeta m;
+    const long long t = a.target_type == SOT_I64 ? l.t64 : l.t32;
+    m.tgt = OP == LM_DISTILL ? 0 : t >= 0 && t < a.V ? (int)t : -1;
+    m.w = OP == LM_LOGPROB ? 1.f : a.weight ? l.w : 1.f / (float)a.T;
+    m.old = l.old;
+    m.ref = l.ref;
+    m.adv = l.adv;
     m.keep = m.tgt >= 0 && m.w != 0.f;
     return m;
 }
@@ -319,48 +331,80 @@ __device__ __forceinline__ void row_outputs(const LmRowArgs& a, long long row, f
     if (a.kl) a.kl[row] = v;
 }
 
-// ---- what the consumers do with a slice (threads tid = 0 .. NT - 1).  Granules inside
-// the row go in batches of four a thread, so that their loads are under way
-// together and one comparison serves 4 N logits; the granule the row starts in
-// and the one it ends in belong to two lanes of the first warp.
+// ---- what NT threads (tid = 0 .. NT - 1) do with a slice.  Granules inside the
+// row, [lo, hi), go in batches, so that their loads are under way together; the
+// granule the row starts in and the one it ends in belong to two threads.  With
+// CUT, byte g of `cut` names the elements of granule g that are left out.
 __device__ __forceinline__ int edge_granule(const Slice& s, int tid) {
     if (tid == 0 && s.ng > 0 && s.lo > 0) return 0;
     if (tid == 1 && s.ng > 0 && s.hi < s.ng && (s.ng > 1 || s.lo == 0)) return s.ng - 1;
     return -1;
 }
-template <int DT, int NT>
-__device__ __forceinline__ MS slice_stats(const Slice& s, const uint4* src, int V, float sc, int tid) {
-    constexpr int N = Elem<DT>::N;
-    Running r;
-    int g = s.lo + tid;
-    for (; g + 3 * NT < s.hi; g += 4 * NT) {
-        uint4 v[4];
+template <int DT>
+__device__ __forceinline__ uint4 nothing() {  // N times -inf
+    constexpr unsigned w = DT == SOT_F32 ? 0xff800000u : DT == SOT_F16 ? 0xfc00fc00u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
+template <int DT>
+__device__ __forceinline__ uint4 without(const uint4& v, unsigned out) {
+    float2 f[Elem<DT>::N / 2];
+    unpack<DT>(v, f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = src[g + j * NT];
-        r.raise(max_of<DT>(max2<DT>(max2<DT>(v[0], v[1]), max2<DT>(v[2], v[3]))), sc);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float2 f[N / 2];
-            unpack<DT>(v[j], f);
-            r.add(f, sc);
-        }
+    for (int i = 0; i < Elem<DT>::N / 2; ++i) {
+        if (out >> (2 * i) & 1u) f[i].x = -INFINITY;
+        if (out >> (2 * i + 1) & 1u) f[i].y = -INFINITY;
     }
-    for (; g < s.hi; g += NT) {
-        const uint4 v = src[g];
-        float2 f[N / 2];
-        unpack<DT>(v, f);
-        r.raise(max_of<DT>(v), sc);
-        r.add(f, sc);
+    return pack<DT>(f);
+}
+
+// Where a slice's granules come from and the gradient's go to: device memory, with
+// L2 policies, or (short rows) shared memory.
+struct FromGlobal {
+    const uint4* p;
+    uint64_t policy;
+    __device__ __forceinline__ uint4 operator()(int g) const { return load16(p + g, policy); }
+};
+struct FromShared {
+    const uint4* p;
+    __device__ __forceinline__ uint4 operator()(int g) const { return p[g]; }
+};
+
+template <int DT, bool CUT, class Src>
+__device__ __forceinline__ void slice_stats(Running& r, const Slice& s, const Src& src, const unsigned char* cut, int V,
+                                            float sc, int tid, int NT) {
+    constexpr int N = Elem<DT>::N, U = 4;
+    for (int g = s.lo + tid; g < s.hi; g += 2 * U * NT) {
+        uint4 v[U], w[U];
+        if (g + (2 * U - 1) * NT < s.hi) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) v[j] = src(g + j * NT);
+#pragma unroll
+            for (int j = 0; j < U; ++j) w[j] = src(g + (U + j) * NT);
+        } else {  // the last batch: -inf for what is not there
+#pragma unroll
+            for (int j = 0; j < U; ++j) v[j] = g + j * NT < s.hi ? src(g + j * NT) : nothing<DT>();
+#pragma unroll
+            for (int j = 0; j < U; ++j) w[j] = g + (U + j) * NT < s.hi ? src(g + (U + j) * NT) : nothing<DT>();
+        }
+        if (CUT) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (g + j * NT < s.hi && cut[g + j * NT]) v[j] = without<DT>(v[j], cut[g + j * NT]);
+                if (g + (U + j) * NT < s.hi && cut[g + (U + j) * NT]) w[j] = without<DT>(w[j], cut[g + (U + j) * NT]);
+            }
+        }
+        r.template add<DT>(v, sc);
+        if (g + U * NT < s.hi) r.template add<DT>(w, sc);
     }
     const int e = edge_granule(s, tid);
     if (e >= 0) {
         float2 f[N / 2];
-        unpack<DT>(src[e], f);
+        unpack<DT>(src(e), f);
         mask_cols<DT>(f, s.e0 + e * N, V, -INFINITY);
-        r.raise(max_of<DT>(f), sc);
-        r.add(f, sc);
+        uint4 v[1] = {pack<DT>(f)};
+        if (CUT && cut[e]) v[0] = without<DT>(v[0], cut[e]);
+        r.template add<DT>(v, sc);
     }
-    return MS{r.m, r.s.x + r.s.y};
 }
 
 template <int DT>
@@ -377,260 +421,179 @@ __device__ __forceinline__ void grad_of(float2 (&f)[Elem<DT>::N / 2], const RowC
     }
 }
 
-template <int DT, int NT>
-__device__ __forceinline__ void slice_grad(const Slice& s, const uint4* src, const RowCoef& coef,
-                                           typename Elem<DT>::T* grow, int V, float sc, bool aligned, int tid) {
-    constexpr int N = Elem<DT>::N;
-    const RowCoef c = coef;
+// grow: the gradient's row; aligned: its granules are the logits' granules.
+template <int DT, class Src>
+__device__ __forceinline__ void slice_grad(const Slice& s, const Src& src, const RowCoef& c, typename Elem<DT>::T* grow,
+                                           int V, float sc, bool aligned, uint64_t policy, int tid, int NT) {
+    constexpr int N = Elem<DT>::N, U = 4;
     if (aligned) {
         uint4* const dst = reinterpret_cast<uint4*>(grow + s.e0);
-        int g = s.lo + tid;
-        for (; g + 3 * NT < s.hi; g += 4 * NT) {
-            uint4 v[4];
+        for (int g = s.lo + tid; g < s.hi; g += U * NT) {
+            uint4 v[U];
+            if (g + (U - 1) * NT < s.hi) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = src[g + j * NT];
+                for (int j = 0; j < U; ++j) v[j] = src(g + j * NT);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float2 f[N / 2];
-                unpack<DT>(v[j], f);
-                grad_of<DT>(f, c, sc);
-                dst[g + j * NT] = pack<DT>(f);
+                for (int j = 0; j < U; ++j) {
+                    float2 f[N / 2];
+                    unpack<DT>(v[j], f);
+                    grad_of<DT>(f, c, sc);
+                    store16(dst + g + j * NT, pack<DT>(f), policy);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < U - 1; ++j)
+                    if (g + j * NT < s.hi) v[j] = src(g + j * NT);
+#pragma unroll
+                for (int j = 0; j < U - 1; ++j)
+                    if (g + j * NT < s.hi) {
+                        float2 f[N / 2];
+                        unpack<DT>(v[j], f);
+                        grad_of<DT>(f, c, sc);
+                        store16(dst + g + j * NT, pack<DT>(f), policy);
+                    }
             }
-        }
-        for (; g < s.hi; g += NT) {
-            float2 f[N / 2];
-            unpack<DT>(src[g], f);
-            grad_of<DT>(f, c, sc);
-            dst[g] = pack<DT>(f);
         }
         const int e = edge_granule(s, tid);
         if (e >= 0) {
             float2 f[N / 2];
-            unpack<DT>(src[e], f);
+            unpack<DT>(src(e), f);
             grad_of<DT>(f, c, sc);
             store_cols<DT>(grow, s.e0 + e * N, V, f, false);
         }
     } else {
         for (int g = tid; g < s.ng; g += NT) {
             float2 f[N / 2];
-            unpack<DT>(src[g], f);
+            unpack<DT>(src(g), f);
             grad_of<DT>(f, c, sc);
             store_cols<DT>(grow, s.e0 + g * N, V, f, false);
         }
     }
 }
 
-template <int DT, int NT>
-__device__ __forceinline__ void slice_zero(const Slice& s, typename Elem<DT>::T* grow, int V, bool aligned, int tid) {
+template <int DT>
+__device__ __forceinline__ void slice_zero(const Slice& s, typename Elem<DT>::T* grow, int V, bool aligned, int tid, int NT) {
     constexpr int N = Elem<DT>::N;
     float2 z[N / 2];
 #pragma unroll
     for (int k = 0; k < N / 2; ++k) z[k] = make_float2(0.f, 0.f);
     for (int g = tid; g < s.ng; g += NT) store_cols<DT>(grow, s.e0 + g * N, V, z, aligned);
 }
+template <class T>
+__device__ __forceinline__ bool same_granules(const T* x, const T* g) {
+    return ((uint32_t)((unsigned long long)x ^ (unsigned long long)g) & 15u) == 0;
+}
 
-template <int DT, int OP, int NW>
-__global__ void __launch_bounds__((NW + ROW_MAX_ST) * 32, NW == 4 ? 5 : NW == 8 ? 3 : 2)
+// NW streaming warps and the row's own warp.
+template <int DT, int OP, int NW, bool TAIL>
+__global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? 7 : NW == 8 ? 4 : 2)
     lm_row_kernel(const LmRowArgs a, const LmRowLaunch L) {
     using T = typename Elem<DT>::T;
     constexpr int N = Elem<DT>::N, NT = NW * 32;
-    extern __shared__ __align__(128) uint4 sm[];
-    __shared__ RowShared<NW> S;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ MS rec[NW];
+    __shared__ float mail[ROW_MAX_CL][NREC];
+    __shared__ RowCoef coef;
+    float* const ex = reinterpret_cast<float*>(dyn);  // entries: logit, weight, column; then (tail) the slice's cut bytes
+    float* const eq = ex + a.K;
+    int* const eid = reinterpret_cast<int*>(eq + a.K);
+    unsigned* const cut = reinterpret_cast<unsigned*>(eid + a.K);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const float sc = SOT_LOG2E / a.tau;
-    const int ST = L.ST, lag = L.lag;
-    const long long first = blockIdx.x / L.CL, step = gridDim.x / L.CL;
-    const long long n = (a.T - first + step - 1) / step;  // rows of this cluster
-    volatile int* const abort = &S.abort;
-    auto bar = [&](int st, int k) { return smem_u32(&S.bar[st][k]); };
-
-    if (tid == 0) {
-        for (int st = 0; st < ST; ++st) {
-            mbar_init(bar(st, RB_FULL), 1);
-            mbar_init(bar(st, RB_CUT), 1);
-            mbar_init(bar(st, RB_REC), NW);
-            mbar_init(bar(st, RB_COEF), 1);
-            mbar_init(bar(st, RB_GRAD), NW);
-            mbar_init(bar(st, RB_MAIL), L.CL);
-            mbar_init(bar(st, RB_MAIL + 1), L.CL);
-        }
-        S.abort = 0;
-        fence_mbar_init();
+    const long long row = blockIdx.x / L.CL;
+    const RowMeta m = row_meta<OP>(a, row_load<OP>(a, row, warp == NW));
+    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
+    T* const grow = a.grad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
+    const bool aligned = same_granules<T>(x, grow);
+    const Slice s = slice_at<DT>(x, a.V, L.G, rank);
+    const int c0 = s.e0, c1 = s.e0 + s.ng * N;  // the slice's columns
+    const uint64_t last = policy_drop(), first = grow ? policy_keep() : last;
+    if (!m.keep) {  // the same for the whole cluster
+        if (grow && warp < NW) slice_zero<DT>(s, grow, a.V, aligned, tid, NT);
+        if (rank == 0 && tid == 0) row_outputs(a, row, 0.f);
+        return;
     }
-    if (L.CL > 1) cluster_sync();  // the barriers exist before a peer arrives on them
-    else __syncthreads();
-
-    if (warp < NW) {
-        // ---- consumers: statistics of row i, gradient of row i - lag
-        const uint32_t ready = OP == LM_DISTILL && a.tail ? RB_CUT : RB_FULL;
-        const long long end = n + (a.grad ? lag : 0);
-        const T *x = static_cast<const T*>(a.x) + first * a.ld, *gx = x;  // rows i and i - lag
-        T* grow = static_cast<T*>(a.grad) + (a.grad ? first * a.ldg : 0);
-        const long long x_step = step * a.ld, g_step = step * a.ldg;
-        int st = 0, gst = 0;         // their stages
-        uint32_t ph = 0u, gph = 0u;  // and these stages' phases
-        for (long long i = 0; i < end; ++i) {
-            if (i < n) {
-                if (!mbar_wait_bounded(bar(st, ready), ph, abort, L.wait_ns)) break;
-                if (S.keep[st]) {
-                    const MS r = ms_warp(slice_stats<DT, NT>(slice_at<DT>(x, a.V, L.G, rank), sm + (size_t)st * L.G, a.V, sc, tid), sc);
-                    if (lane == 0) S.rec[st][warp] = r;
+    if (L.CL > 1) cluster_arrive_started();
+    if (TAIL) {
+        for (int g = tid; g < (L.G + 3) / 4; g += NT + 32) cut[g] = 0u;
+        __syncthreads();
+    }
+    float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
+    MS top{-INFINITY, 0.f};
+    if (warp == NW) {
+        if (OP == LM_DISTILL) {
+            teacher_side(a, row, eq, eid, Q, B);
+            if (TAIL) {
+                for (int k = lane; k < a.K; k += 32) {
+                    const int at = eid[k] - c0;
+                    if (eid[k] >= 0 && at >= 0 && eid[k] < c1) atomicOr(cut + at / N / 4, 1u << (at / N % 4 * 8 + at % N));
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(st, RB_REC));
-                x += x_step;
-                if (++st == ST) {
-                    st = 0;
-                    ph ^= 1u;
-                }
+                __syncthreads();
             }
-            if (a.grad && i >= lag) {
-                const Slice s = slice_at<DT>(gx, a.V, L.G, rank);
-                const bool aligned = ((uint32_t)((unsigned long long)grow ^ (unsigned long long)gx) & 15u) == 0;
-                if (!mbar_wait_bounded(bar(gst, RB_COEF), gph, abort, L.wait_ns)) break;
-                if (S.keep[gst])
-                    slice_grad<DT, NT>(s, sm + (size_t)gst * L.G, S.coef[gst], grow, a.V, sc, aligned, tid);
-                else
-                    slice_zero<DT, NT>(s, grow, a.V, aligned, tid);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(gst, RB_GRAD));
-                gx += x_step;
-                grow += g_step;
-                if (++gst == ST) {
-                    gst = 0;
-                    gph ^= 1u;
-                }
-            }
-        }
+            student_side<DT>(a, c0, c1, x, ex, eq, eid, sc, D, top);
+        } else if (m.tgt >= c0 && m.tgt < c1)
+            D.x = Elem<DT>::get(x[m.tgt]);
     } else {
-        // ---- stage warps: stage st has rows st, st + ST, ...
-        const int st = warp - NW;
-        T* const se = reinterpret_cast<T*>(sm + (size_t)st * L.G);
-        float* const ex = reinterpret_cast<float*>(sm + (size_t)ST * L.G) + (size_t)st * 3 * a.K;
-        float* const eq = ex + a.K;
-        int* const eid = reinterpret_cast<int*>(eq + a.K);
-        uint32_t ph = 0u, kept = 0u;  // phase of the stage's barriers; kept rows (phase of the mail)
-        bool fine = true, copying = false;
-        uint32_t cph = 1u;  // phase of the copy under way
-        auto start = [&](long long i, const RowMeta& m) {  // row i's copy
-            const Slice s = slice_of<DT>(a.x, first + i * step, a.ld, a.V, L.G, rank);
-            copying = false;
-            if (i == L.hold) return;
-            copying = true;
-            cph ^= 1u;
-            if (lane == 0) {
-                S.keep[st] = m.keep;
-                if (m.keep && s.ng > 0) {
-                    mbar_arrive_expect_tx(bar(st, RB_FULL), (uint32_t)s.ng * 16);
-                    bulk_g2s(smem_u32(se), s.src, (uint32_t)s.ng * 16, bar(st, RB_FULL));
-                } else
-                    mbar_arrive(bar(st, RB_FULL));
-            }
-        };
-        long long i = st;
-        RowMeta next;
-        if (i < n) {
-            next = row_meta<OP>(a, first + i * step);
-            start(i, next);
-        }
-        for (; i < n; i += ST) {
-            const long long row = first + i * step;
-            const RowMeta m = next;
-            if (i + ST < n) next = row_meta<OP>(a, first + (i + ST) * step);  // used when this row is done
-            const Slice s = slice_of<DT>(a.x, row, a.ld, a.V, L.G, rank);
-            MS r{-INFINITY, 0.f}, top{-INFINITY, 0.f};
-            float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
-            if (OP == LM_DISTILL && m.keep) teacher_side(a, row, eq, eid, Q, B);
-            if (!(fine = mbar_wait_bounded(bar(st, RB_FULL), ph, abort, L.wait_ns))) break;
-            copying = false;
-            if (m.keep) {
-                if (OP == LM_DISTILL)
-                    student_side<DT>(a, s, se, ex, eq, eid, sc, D, top);
-                else if (m.tgt >= s.e0 && m.tgt < s.e0 + s.ng * N)
-                    D.x = Elem<DT>::get(se[m.tgt - s.e0]);
-            }
-            const float xt = D.x;  // the target's logit, where this slice has it
-            if (OP == LM_DISTILL && a.tail && lane == 0) mbar_arrive(bar(st, RB_CUT));
-            if (!(fine = mbar_wait_bounded(bar(st, RB_REC), ph, abort, L.wait_ns))) break;
-            if (m.keep) {
-                if (lane < NW) r = S.rec[st][lane];
-                r = ms_warp(r, sc);
-            }
-            if (!a.grad && i + ST < n) {  // the slice is done with
-                __syncwarp();
-                start(i + ST, next);
-            }
-            if (m.keep && L.CL > 1) {
-                const uint32_t par = kept & 1u;
-                if (lane < L.CL) {
-                    const uint32_t to = cluster_addr(smem_u32(S.mail[st][par][rank]), lane);
-                    cluster_store(to, r.m);
-                    cluster_store(to + 4, r.s);
-                    cluster_store(to + 8, top.m);
-                    cluster_store(to + 12, top.s);
-                    cluster_store(to + 16, D.x);
-                    cluster_store(to + 20, D.y);
-                    cluster_arrive(cluster_addr(bar(st, RB_MAIL + par), lane));
-                }
-                if (!(fine = mbar_wait_cluster(bar(st, RB_MAIL + par), (kept >> 1) & 1u, abort, L.wait_ns))) break;
-                r = top = MS{-INFINITY, 0.f};
-                D = make_float2(0.f, 0.f);
-                if (lane < L.CL) {
-                    const float* p = S.mail[st][par][lane];
-                    r = MS{p[0], p[1]};
-                    top = MS{p[2], p[3]};
-                    D = make_float2(p[4], p[5]);
-                }
-                r = ms_warp(r, sc);
-                if (OP == LM_DISTILL) {
-                    if (a.tail) top = ms_warp(top, sc);
-                    D = ff_sum_or_far(D);
-                } else
-                    D.x = warp_sum(D.x);  // the one slice that has the target gave its logit
-                ++kept;
-            }
-            RowCoef c;
-            if (m.keep) {
-                c = row_finish<OP>(a, row, m, r, top, Q, B, D, sc, rank == 0 && lane == 0, [&](const RowCoef& k) {
-                    if (a.grad && lane == 0) {
-                        S.coef[st] = k;
-                        mbar_arrive(bar(st, RB_COEF));
-                    }
-                });
-            } else if (lane == 0) {
-                if (a.grad) mbar_arrive(bar(st, RB_COEF));
-                if (rank == 0) row_outputs(a, row, 0.f);
-            }
-            if (a.grad) {
-                // the corrections come after the columns they replace
-                if (!(fine = mbar_wait_bounded(bar(st, RB_GRAD), ph, abort, L.wait_ns))) break;
-                T* const grow = static_cast<T*>(a.grad) + row * a.ldg;
-                if (m.keep) {
-                    if (OP == LM_DISTILL) {
-                        for (int k = lane; k < a.K; k += 32)
-                            if (eid[k] >= 0)
-                                grow[eid[k]] = Elem<DT>::put(c.fa * (weight_of(ex[k], c.M, sc) * c.inv_S) - c.fb * eq[k]);
-                    } else if (lane == 0 && m.tgt >= s.e0 && m.tgt < s.e0 + s.ng * N)
-                        grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(xt, c.M, sc) * c.inv_S) - c.fb);
-                }
-                __syncwarp();
-                if (i + ST < n) start(i + ST, next);
-            }
-            ph ^= 1u;
-        }
-        if (!fine) {
-            if (copying) {  // no copy may be in flight when the CTA ends
-                int dummy = 0;
-                mbar_wait_bounded(bar(st, RB_FULL), cph, &dummy, L.wait_ns);
-            }
-            if (lane == 0) atomicOr(L.status, SOT_DEV_TIMEOUT);
-            if (rank == 0 && lane == 0)
-                for (; i < n; i += ST) row_outputs(a, first + i * step, NAN);
-        }
+        if (TAIL) __syncthreads();
+        Running r;
+        slice_stats<DT, TAIL>(r, s, FromGlobal{s.src, first}, reinterpret_cast<const unsigned char*>(cut), a.V, sc, tid, NT);
+        const MS w = ms_warp(r.result(), sc);
+        if (lane == 0) rec[warp] = w;
     }
-    __syncwarp();
-    if (L.CL > 1) cluster_sync();  // no CTA leaves while a peer may still store to it
+    const float xt = D.x;  // the target's logit, where this slice has it
+    if (L.CL > 1) cluster_wait_started();  // every CTA of the cluster is there to be stored to
+    __syncthreads();
+    MS r{-INFINITY, 0.f};
+    if (warp == NW) {
+        if (lane < NW) r = rec[lane];
+        r = ms_warp(r, sc);
+        if (L.CL > 1 && lane < L.CL) {
+            const uint32_t to = cluster_addr(smem_u32(mail[rank]), lane);
+            cluster_store(to, r.m);
+            cluster_store(to + 4, r.s);
+            cluster_store(to + 8, top.m);
+            cluster_store(to + 12, top.s);
+            cluster_store(to + 16, D.x);
+            cluster_store(to + 20, D.y);
+        }
+        __syncwarp();
+    }
+    if (L.CL > 1) cluster_sync();
+    if (warp == NW) {
+        if (L.CL > 1) {
+            r = top = MS{-INFINITY, 0.f};
+            D = make_float2(0.f, 0.f);
+            if (lane < L.CL) {
+                const float* p = mail[lane];
+                r = MS{p[0], p[1]};
+                top = MS{p[2], p[3]};
+                D = make_float2(p[4], p[5]);
+            }
+            r = ms_warp(r, sc);
+            if (OP == LM_DISTILL) {
+                if (TAIL) top = ms_warp(top, sc);
+                D = ff_sum_or_far(D);
+            } else
+                D.x = warp_sum(D.x);  // the one slice that has the target gave its logit
+        }
+        row_finish<OP>(a, row, m, r, top, Q, B, D, sc, rank == 0 && lane == 0, [&](const RowCoef& k) {
+            if (lane == 0) coef = k;
+            if (grow) __syncthreads();  // the streaming warps go on while the losses are finished
+        });
+        if (!grow) return;
+    } else {
+        if (!grow) return;
+        __syncthreads();
+        slice_grad<DT>(s, FromGlobal{s.src, last}, coef, grow, a.V, sc, aligned, last, tid, NT);
+    }
+    __syncthreads();  // the corrections come after the columns they replace
+    const RowCoef c = coef;
+    if (OP == LM_DISTILL) {
+        for (int k = tid; k < a.K; k += NT + 32)
+            if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * (weight_of(ex[k], c.M, sc) * c.inv_S) - c.fb * eq[k]);
+    } else if (tid == NT && m.tgt >= c0 && m.tgt < c1)
+        grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(xt, c.M, sc) * c.inv_S) - c.fb);
 }
 
 // Short rows: one warp takes a row from its copy to its corrections, so nothing is
@@ -639,13 +602,15 @@ __global__ void __launch_bounds__((NW + ROW_MAX_ST) * 32, NW == 4 ? 5 : NW == 8 
 constexpr int WARP_ROWS = 4;  // warps of a CTA
 
 template <int DT, int OP>
-__global__ void __launch_bounds__(WARP_ROWS * 32, 6) lm_warp_kernel(const LmRowArgs a, const LmRowLaunch L) {
+__global__ void __launch_bounds__(WARP_ROWS * 32, 5) lm_warp_kernel(const LmRowArgs a, const LmRowLaunch L) {
     using T = typename Elem<DT>::T;
+    constexpr int N = Elem<DT>::N;
     extern __shared__ __align__(128) uint4 sm[];
     __shared__ uint64_t full[WARP_ROWS][2];
     __shared__ int timed_out[WARP_ROWS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float sc = SOT_LOG2E / a.tau;
+    const uint64_t drop_policy = policy_drop();
     uint4* const buf = sm + (size_t)warp * 2 * L.G;
     float* const ex = reinterpret_cast<float*>(sm + (size_t)WARP_ROWS * 2 * L.G) + (size_t)warp * 3 * a.K;
     float* const eq = ex + a.K;
@@ -673,38 +638,50 @@ __global__ void __launch_bounds__(WARP_ROWS * 32, 6) lm_warp_kernel(const LmRowA
         }
     };
     long long row = first;
-    RowMeta m, next;
+    RowMeta m = {}, next = {};
+    RowLoad ahead = {};
     if (row < a.T) {
-        m = row_meta<OP>(a, row);
+        m = row_meta<OP>(a, row_load<OP>(a, row, true));
         start(row, m, 0);
-        if (row + step < a.T) next = row_meta<OP>(a, row + step);
+        if (row + step < a.T) ahead = row_load<OP>(a, row + step, true);
     }
     uint32_t ph = 0u;
     int b = 0;
     for (; row < a.T; row += step) {
-        RowMeta after;
         if (row + step < a.T) {
+            next = row_meta<OP>(a, ahead);
             start(row + step, next, b ^ 1);  // that buffer's row is done
-            if (row + 2 * step < a.T) after = row_meta<OP>(a, row + 2 * step);
+            if (row + 2 * step < a.T) ahead = row_load<OP>(a, row + 2 * step, true);
         }
         float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
         if (OP == LM_DISTILL && m.keep) teacher_side(a, row, eq, eid, Q, B);
-        if (!mbar_wait_bounded(bar0 + 8 * b, ph, abort, L.wait_ns)) break;
+        __syncwarp();
+        if (!row_wait(bar0 + 8 * b, ph, abort, L.wait_ns)) break;
         copying[b] = false;
         const Slice s = slice_of<DT>(a.x, row, a.ld, a.V, L.G, 0);
         uint4* const src = buf + (size_t)b * L.G;
         T* const se = reinterpret_cast<T*>(src);
+        const T* const xrow = static_cast<const T*>(a.x) + row * a.ld;
         T* const grow = a.grad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
-        const bool aligned =
-            ((uint32_t)((unsigned long long)grow ^ (unsigned long long)(static_cast<const T*>(a.x) + row * a.ld)) & 15u) == 0;
+        const bool aligned = same_granules<T>(xrow, grow);
         if (m.keep) {
             MS top{-INFINITY, 0.f};
-            if (OP == LM_DISTILL) student_side<DT>(a, s, se, ex, eq, eid, sc, D, top);
-            else D.x = Elem<DT>::get(se[m.tgt - s.e0]);
-            const MS r = ms_warp(slice_stats<DT, 32>(s, src, a.V, sc, lane), sc);
+            if (OP == LM_DISTILL) {
+                student_side<DT>(a, s.e0, s.e0 + s.ng * N, se - s.e0, ex, eq, eid, sc, D, top);
+                if (a.tail) {  // the entries leave the row; its copy comes later than the removals
+                    for (int k = lane; k < a.K; k += 32)
+                        if (eid[k] >= 0) se[eid[k] - s.e0] = Elem<DT>::put(-INFINITY);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            } else
+                D.x = Elem<DT>::get(se[m.tgt - s.e0]);
+            Running run;
+            slice_stats<DT, false>(run, s, FromShared{src}, nullptr, a.V, sc, lane, 32);
+            const MS r = ms_warp(run.result(), sc);
             const RowCoef c = row_finish<OP>(a, row, m, r, top, Q, B, D, sc, lane == 0, [](const RowCoef&) {});
             if (grow) {
-                slice_grad<DT, 32>(s, src, c, grow, a.V, sc, aligned, lane);
+                slice_grad<DT>(s, FromShared{src}, c, grow, a.V, sc, aligned, drop_policy, lane, 32);
                 __syncwarp();  // the corrections come after the columns they replace
                 if (OP == LM_DISTILL) {
                     for (int k = lane; k < a.K; k += 32)
@@ -714,19 +691,18 @@ __global__ void __launch_bounds__(WARP_ROWS * 32, 6) lm_warp_kernel(const LmRowA
                     grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(D.x, c.M, sc) * c.inv_S) - c.fb);
             }
         } else {
-            if (grow) slice_zero<DT, 32>(s, grow, a.V, aligned, lane);
+            if (grow) slice_zero<DT>(s, grow, a.V, aligned, lane, 32);
             if (lane == 0) row_outputs(a, row, 0.f);
         }
         __syncwarp();
         m = next;
-        next = after;
         b ^= 1;
         if (b == 0) ph ^= 1u;
     }
     if (row < a.T) {  // a wait ran out: no copy may be in flight when the CTA ends
         int dummy = 0;
-        if (copying[b]) mbar_wait_bounded(bar0 + 8 * b, ph, &dummy, L.wait_ns);
-        if (copying[b ^ 1]) mbar_wait_bounded(bar0 + 8 * (b ^ 1), b ? ph ^ 1u : ph, &dummy, L.wait_ns);
+        if (copying[b]) row_wait(bar0 + 8 * b, ph, &dummy, L.wait_ns);
+        if (copying[b ^ 1]) row_wait(bar0 + 8 * (b ^ 1), b ? ph ^ 1u : ph, &dummy, L.wait_ns);
         if (lane == 0) {
             atomicOr(L.status, SOT_DEV_TIMEOUT);
             for (; row < a.T; row += step) row_outputs(a, row, NAN);
@@ -735,19 +711,24 @@ __global__ void __launch_bounds__(WARP_ROWS * 32, 6) lm_warp_kernel(const LmRowA
 }
 
 struct LmRowPlan {
-    int NW, CL, G, ST, lag;  // NW = 1: the short-row kernel
+    int NW;     // streaming warps of a CTA (1: the short-row kernel)
+    int CL, G;  // CTAs a row, granules a slice
     size_t smem;
     int sms;
 };
 
-template <int DT, int OP, int NW>
+template <int DT, int OP, int NW, bool TAIL>
 cudaError_t launch_row_n(const LmRowArgs& a, const LmRowPlan& p, LmRowLaunch L, cudaStream_t st) {
-    auto kern = lm_row_kernel<DT, OP, NW>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
-    if (e != cudaSuccess) return e;
+    auto kern = lm_row_kernel<DT, OP, NW, TAIL>;
+    if (p.smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+        if (e != cudaSuccess) return e;
+    }
+    L.CL = p.CL;
+    L.G = p.G;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.CL, 1, 1);
-    cfg.blockDim = dim3((NW + p.ST) * 32, 1, 1);
+    cfg.gridDim = dim3((unsigned)p.CL, 1, 1);
+    cfg.blockDim = dim3((NW + 1) * 32, 1, 1);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -757,18 +738,15 @@ cudaError_t launch_row_n(const LmRowArgs& a, const LmRowPlan& p, LmRowLaunch L, 
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int clusters = 0;
-    e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-    if (e != cudaSuccess) return e;
-    if (clusters < 1) return cudaErrorInvalidConfiguration;
-    const long long n = a.T < clusters ? a.T : clusters;
-    cfg.gridDim = dim3((unsigned)(n * p.CL), 1, 1);
-    L.CL = p.CL;
-    L.G = p.G;
-    L.ST = p.ST;
-    L.lag = p.lag;
-    e = cudaLaunchKernelEx(&cfg, kern, a, L);
+    cfg.gridDim.x = (unsigned)(a.T * p.CL);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, L);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <int DT, int OP, int NW>
+cudaError_t launch_row_k(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaunch& L, cudaStream_t st) {
+    if constexpr (OP == LM_DISTILL)
+        if (a.tail) return launch_row_n<DT, OP, NW, true>(a, p, L, st);
+    return launch_row_n<DT, OP, NW, false>(a, p, L, st);
 }
 
 template <int DT, int OP>
@@ -791,9 +769,9 @@ template <int DT, int OP>
 cudaError_t launch_row_o(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaunch& L, cudaStream_t st) {
     switch (p.NW) {
         case 1: return launch_row_w<DT, OP>(a, p, L, st);
-        case 4: return launch_row_n<DT, OP, 4>(a, p, L, st);
-        case 8: return launch_row_n<DT, OP, 8>(a, p, L, st);
-        default: return launch_row_n<DT, OP, 16>(a, p, L, st);
+        case 4: return launch_row_k<DT, OP, 4>(a, p, L, st);
+        case 8: return launch_row_k<DT, OP, 8>(a, p, L, st);
+        default: return launch_row_k<DT, OP, 16>(a, p, L, st);
     }
 }
 

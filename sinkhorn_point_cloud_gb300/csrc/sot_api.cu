@@ -1601,12 +1601,6 @@ int check_temperature(float tau) {
         return fail(SOT_ERR_INVALID_ARG, "temperature must be finite and > 0");
     return SOT_OK;
 }
-int check_row_fits(int dtype, int V, int K) {
-    if (!lm_row_fits(dtype, V, K))
-        return fail(SOT_ERR_UNSUPPORTED, "a row of %d logits does not fit a cluster's shared memory", V);
-    return SOT_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -1617,7 +1611,6 @@ int sot_token_logprob(const void* logits, long long T, int V, long long ld, int 
     SOT_TRY(check_rows(logits, T, V, ld, dtype, nullptr, 0));
     SOT_TRY(check_temperature(temperature));
     SOT_TRY(check_index_type("target_type", target_type));
-    SOT_TRY(check_row_fits(dtype, V, 0));
     if (T == 0) return SOT_OK;
     SOT_TRY(check_pointer("target", target, target_type));
     if (!logp && !lse) return fail(SOT_ERR_INVALID_ARG, "logp and lse must not both be NULL");
@@ -1676,7 +1669,8 @@ int sot_distill_topk(const void* logits, long long T, int V, long long ld, int d
     if (K < 1 || K > LM_MAX_K) return fail(SOT_ERR_INVALID_ARG, "K must satisfy 1 <= K <= %d (got %d)", LM_MAX_K, K);
     if (tail && temperature != 1.f)
         return fail(SOT_ERR_INVALID_ARG, "the tail outcome needs temperature 1 (the teacher's rest cannot be re-scaled)");
-    SOT_TRY(check_row_fits(dtype, V, K));
+    if (tail && !lm_tail_fits(dtype, V, K))
+        return fail(SOT_ERR_UNSUPPORTED, "the tail outcome's marks for %d columns do not fit shared memory", V);
     if (T == 0) return SOT_OK;
     SOT_TRY(check_pointer("ids", ids, ids_type));
     SOT_TRY(check_pointer("teacher", teacher, teacher_type));
@@ -1715,7 +1709,6 @@ int sot_policy_loss(const void* logits, long long T, int V, long long ld, int dt
         return fail(SOT_ERR_INVALID_ARG, "clip_low must be in [0, 1] and clip_high finite and >= 0");
     if (!std::isfinite(kl_coef)) return fail(SOT_ERR_INVALID_ARG, "kl_coef must be finite");
     if (kl_coef != 0.f && !ref_logp && T > 0) return fail(SOT_ERR_INVALID_ARG, "kl_coef needs ref_logp");
-    SOT_TRY(check_row_fits(dtype, V, 0));
     if (T == 0) return SOT_OK;
     SOT_TRY(check_pointer("target", target, target_type));
     if (!old_logp || !advantage) return fail(SOT_ERR_INVALID_ARG, "old_logp and advantage must not be NULL");
