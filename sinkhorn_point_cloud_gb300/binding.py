@@ -434,101 +434,136 @@ def sot_grad_x_coo(X, Y, rows, cols, vals, batch_offsets, grad=None, stream=None
 
 
 # ---- language-model training losses ---------------------------------------------------------------------------------
-def _rows(x, name="logits"):
-    """(tensor, T, V, row stride, sot_dtype) of logits [T, V] whose rows are contiguous."""
+# A call on a handful of tokens takes the GPU 4 to 6 us, so these marshal with
+# as few interpreter steps as the checks allow: each helper answers with the
+# tensor's address once everything about it is right, and only what is wrong is
+# looked at again to say what.
+_F32 = torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _logits(x, name="logits"):
+    """(address, rows, columns, row stride, sot_dtype, device index) of [rows, columns] whose rows are contiguous."""
+    try:
+        dt = _FLOATS[x.dtype]
+        T, V = x.shape
+        ld, inner = x.stride()
+        dev = x.get_device()
+        if dev >= 0 and (inner == 1 or V == 1) and (ld >= V or T <= 1):
+            return x.data_ptr(), T, V, ld if T > 1 else V, dt, dev
+    except (AttributeError, KeyError, ValueError):
+        pass
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    dt = _FLOATS.get(x.dtype)
-    if dt is None:
+    if x.dtype not in _FLOATS:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
     if x.dim() != 2:
         raise ValueError(f"{name} must be [rows, columns], got shape {tuple(x.shape)}")
     if not x.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    T, V = x.shape
-    ld, inner = x.stride()
-    if inner != 1 and V > 1:
+    if x.shape[1] > 1 and x.stride(1) != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if T <= 1:
-        ld = V
-    elif ld < V:
-        raise ValueError(f"{name}: rows must not overlap (row stride {ld}, {V} columns)")
-    return T, V, ld, dt
+    raise ValueError(f"{name}: rows must not overlap (row stride {x.stride(0)}, {x.shape[1]} columns)")
 
 
-def _index(t, name, shape, dev):
-    """sot_dtype of an index tensor of this shape."""
+def _floats(t, name, n, dev, dtype=_F32):
+    """Address of a contiguous tensor of n elements of this type on this device; None for None."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _want(t, name, n, torch.device("cuda", dev), dtype)
+
+
+def _needed(t, name, n, dev):
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return _floats(t, name, n, dev)
+
+
+def _indices(t, name, shape, dev):
+    """(address, sot_dtype) of a contiguous int32 or int64 tensor of this shape on this device."""
+    try:
+        ty = _INDICES[t.dtype]
+        if t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr(), ty
+    except (AttributeError, KeyError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    ty = _INDICES.get(t.dtype)
-    if ty is None:
+    if t.dtype not in _INDICES:
         raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return ty
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _stream_of(stream, make):
-    """(stream handle, outputs): the outputs are made on the stream that will write
-    them, so that their memory is not still in use by another one's work."""
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream, make()
-    with torch.cuda.stream(stream):
-        return stream.cuda_stream, make()
+def _pairs(t, name, T, dev):
+    """(address, sot_dtype, columns) of an index tensor [T, columns]."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, entries]")
+    K = t.shape[1]
+    return *_indices(t, name, (T, K), dev), K
 
 
-def _grad_rows(grad, logits, T, V, dt):
-    """(grad tensor or None, row stride) of an output asked for as True, False, None or a tensor."""
-    if grad is None or grad is False:
-        return None, 0
+def _grad_of(grad, logits, T, V, ld, dt, dev):
+    """(tensor or None, address, row stride) of a gradient asked for as True, False, None or a tensor."""
     if grad is True:
-        return torch.empty((T, V), dtype=logits.dtype, device=logits.device), V
-    gT, gV, ld, gdt = _rows(grad, "grad")
-    if (gT, gV, gdt) != (T, V, dt) or grad.device != logits.device:
+        g = torch.empty_like(logits) if ld == V else torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        return g, g.data_ptr(), V
+    if grad is None or grad is False:
+        return None, None, 0
+    at, gT, gV, gld, gdt, gdev = _logits(grad, "grad")
+    if (gT, gV, gdt, gdev) != (T, V, dt, dev):
         raise ValueError(f"grad must be {logits.dtype} of shape {(T, V)} on {logits.device}")
-    return grad, ld
+    return grad, at, gld
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+def _on(stream, call):
+    """call(handle) on the given stream: what it allocates is then the stream's own,
+    not memory that another stream's work may still be using."""
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def sot_token_logprob(logits, target, temperature=1.0, logp=None, lse=None, stream=None):
     """Log-probability of one token per row: (logp [T], lse [T]) float32 of logits
     [T, V] (float32, float16 or bfloat16, any row stride) and target [T].  A
     target outside [0, V) leaves its row out (both values 0)."""
-    T, V, ld, dt = _rows(logits)
-    dev = logits.device
-    ty = _index(target, "target", (T,), dev)
-    _want(logp, "logp", T, dev)
-    _want(lse, "lse", T, dev)
-    s, (logp, lse) = _stream_of(stream, lambda: (torch.empty(T, device=dev) if logp is None else logp,
-                                                 torch.empty(T, device=dev) if lse is None else lse))
-    rc = load().sot_token_logprob(logits.data_ptr(), T, V, ld, dt, temperature, target.data_ptr(), ty, logp.data_ptr(),
-                                  lse.data_ptr(), s)
-    _check(rc, "sot_token_logprob")
-    return logp, lse
+    x, T, V, ld, dt, dev = _logits(logits)
+    tg, ty = _indices(target, "target", (T,), dev)
+    _floats(logp, "logp", T, dev)
+    _floats(lse, "lse", T, dev)
+
+    def call(s):
+        p = torch.empty(T, device=logits.device) if logp is None else logp
+        q = torch.empty_like(p) if lse is None else lse
+        rc = load().sot_token_logprob(x, T, V, ld, dt, temperature, tg, ty, p.data_ptr(), q.data_ptr(), s)
+        if rc:
+            _check(rc, "sot_token_logprob")
+        return p, q
+    return call(_raw_stream(dev)) if stream is None else _on(stream, call)
 
 
 def sot_token_logprob_grad(logits, target, lse, grad_logp, temperature=1.0, grad=True, stream=None):
     """Gradient [T, V] (the logits' type) of sum_t grad_logp[t] logp[t], from the lse of
     sot_token_logprob.  ``grad`` may be a tensor to write, the logits included."""
-    T, V, ld, dt = _rows(logits)
-    dev = logits.device
-    ty = _index(target, "target", (T,), dev)
-    for t, name in ((lse, "lse"), (grad_logp, "grad_logp")):
-        if t is None:
-            raise TypeError(f"{name} must be a torch.Tensor")
-        _want(t, name, T, dev)
-    s, (grad, ldg) = _stream_of(stream, lambda: _grad_rows(grad, logits, T, V, dt))
-    rc = load().sot_token_logprob_grad(logits.data_ptr(), T, V, ld, dt, temperature, target.data_ptr(), ty,
-                                       lse.data_ptr(), grad_logp.data_ptr(), _at(grad), ldg, s)
-    _check(rc, "sot_token_logprob_grad")
-    return grad
+    x, T, V, ld, dt, dev = _logits(logits)
+    tg, ty = _indices(target, "target", (T,), dev)
+    l, g = _needed(lse, "lse", T, dev), _needed(grad_logp, "grad_logp", T, dev)
+
+    def call(s):
+        out, at, ldg = _grad_of(grad, logits, T, V, ld, dt, dev)
+        rc = load().sot_token_logprob_grad(x, T, V, ld, dt, temperature, tg, ty, l, g, at, ldg, s)
+        if rc:
+            _check(rc, "sot_token_logprob_grad")
+        return out
+    return call(_raw_stream(dev)) if stream is None else _on(stream, call)
 
 
 def sot_distill_topk(logits, ids, teacher, weight=None, temperature=1.0, tail=False, grad=True, loss=None, stream=None):
@@ -537,24 +572,24 @@ def sot_distill_topk(logits, ids, teacher, weight=None, temperature=1.0, tail=Fa
     ``tail`` the teacher values are logits; with it they are log-probabilities and
     the mass outside the entries is one more outcome.  weight [T] (None = 1/T), 0
     leaves a row out.  ``grad``: True, False or a tensor (the logits included)."""
-    T, V, ld, dt = _rows(logits)
-    dev = logits.device
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
-        raise ValueError("ids must be [rows, entries]")
-    K = ids.shape[1]
-    ty = _index(ids, "ids", (T, K), dev)
-    if not isinstance(teacher, torch.Tensor) or teacher.dtype not in _FLOATS:
+    x, T, V, ld, dt, dev = _logits(logits)
+    i, ty, K = _pairs(ids, "ids", T, dev)
+    tt = _FLOATS.get(teacher.dtype) if isinstance(teacher, torch.Tensor) else None
+    if tt is None:
         raise TypeError("teacher must be a float32, float16 or bfloat16 torch.Tensor")
-    _want(teacher, "teacher", T * K, dev, teacher.dtype)
-    _want(weight, "weight", T, dev)
-    _want(loss, "loss", T, dev)
-    s, (loss, (g, ldg)) = _stream_of(stream, lambda: (torch.empty(T, device=dev) if loss is None else loss,
-                                                      _grad_rows(grad, logits, T, V, dt)))
-    rc = load().sot_distill_topk(logits.data_ptr(), T, V, ld, dt, temperature, ids.data_ptr(), ty, teacher.data_ptr(),
-                                 _FLOATS[teacher.dtype], K, 1 if tail else 0, _at(weight), loss.data_ptr(), _at(g), ldg,
-                                 s)
-    _check(rc, "sot_distill_topk")
-    return loss, g
+    z = _floats(teacher, "teacher", T * K, dev, teacher.dtype)
+    w = _floats(weight, "weight", T, dev)
+    _floats(loss, "loss", T, dev)
+
+    def call(s):
+        lo = torch.empty(T, device=logits.device) if loss is None else loss
+        g, at, ldg = _grad_of(grad, logits, T, V, ld, dt, dev)
+        rc = load().sot_distill_topk(x, T, V, ld, dt, temperature, i, ty, z, tt, K, 1 if tail else 0, w, lo.data_ptr(), at,
+                                     ldg, s)
+        if rc:
+            _check(rc, "sot_distill_topk")
+        return lo, g
+    return call(_raw_stream(dev)) if stream is None else _on(stream, call)
 
 
 def sot_policy_loss(logits, target, old_logp, advantage, ref_logp=None, weight=None, temperature=1.0, clip_low=0.2,
@@ -563,24 +598,21 @@ def sot_policy_loss(logits, target, old_logp, advantage, ref_logp=None, weight=N
     None).  old_logp, advantage, ref_logp and weight are [T]; weight None = 1/T, 0
     leaves a row out, as does a target outside [0, V).  Without ref_logp, kl_coef
     takes no part.  ``grad``: True, False or a tensor (the logits included)."""
-    T, V, ld, dt = _rows(logits)
-    dev = logits.device
-    ty = _index(target, "target", (T,), dev)
-    for t, name in ((old_logp, "old_logp"), (advantage, "advantage")):
-        if t is None:
-            raise TypeError(f"{name} must be a torch.Tensor")
-        _want(t, name, T, dev)
-    _want(ref_logp, "ref_logp", T, dev)
-    _want(weight, "weight", T, dev)
-    s, (out, (g, ldg)) = _stream_of(stream, lambda: (torch.empty((3, T), device=dev),
-                                                     _grad_rows(grad, logits, T, V, dt)))
-    at = out.data_ptr()
-    rc = load().sot_policy_loss(logits.data_ptr(), T, V, ld, dt, temperature, target.data_ptr(), ty, old_logp.data_ptr(),
-                                _at(ref_logp), advantage.data_ptr(), _at(weight), clip_low, clip_high,
-                                kl_coef if ref_logp is not None else 0.0, at, at + 4 * T, at + 8 * T, _at(g), ldg, s)
-    _check(rc, "sot_policy_loss")
-    loss, logp, kl = out
-    return loss, logp, kl, g
+    x, T, V, ld, dt, dev = _logits(logits)
+    tg, ty = _indices(target, "target", (T,), dev)
+    old, adv = _needed(old_logp, "old_logp", T, dev), _needed(advantage, "advantage", T, dev)
+    ref, w = _floats(ref_logp, "ref_logp", T, dev), _floats(weight, "weight", T, dev)
+
+    def call(s):
+        out = torch.empty((3, T), device=logits.device)
+        p = out.data_ptr()
+        g, at, ldg = _grad_of(grad, logits, T, V, ld, dt, dev)
+        rc = load().sot_policy_loss(x, T, V, ld, dt, temperature, tg, ty, old, ref, adv, w, clip_low, clip_high,
+                                    0.0 if ref is None else kl_coef, p, p + 4 * T, p + 8 * T, at, ldg, s)
+        if rc:
+            _check(rc, "sot_policy_loss")
+        return *out.unbind(), g
+    return call(_raw_stream(dev)) if stream is None else _on(stream, call)
 
 
 def sot_preference_loss(logp, offsets, ref_logp=None, target=None, beta=0.1, label_smoothing=0.0, average=False,
@@ -590,44 +622,49 @@ def sot_preference_loss(logp, offsets, ref_logp=None, target=None, beta=0.1, lab
     token whose target is negative takes no part.  scale None = 1/P."""
     if not isinstance(logp, torch.Tensor) or not isinstance(offsets, torch.Tensor):
         raise TypeError("logp and offsets must be torch.Tensors")
-    dev, T = logp.device, logp.numel()
-    _want(logp, "logp", T, dev)
     if not logp.is_cuda:
         raise ValueError("logp must be on a CUDA device")
-    if offsets.numel() % 2 == 0:
+    dev, T, n = logp.get_device(), logp.numel(), offsets.numel()
+    lp = _floats(logp, "logp", T, dev)
+    if n % 2 == 0:
         raise ValueError("offsets must hold 2 P + 1 elements")
-    _want(offsets, "offsets", None, dev, torch.int64)
-    P = offsets.numel() // 2
-    _want(ref_logp, "ref_logp", T, dev)
-    ty = _index(target, "target", (T,), dev) if target is not None else SOT_I32
+    off = _floats(offsets, "offsets", n, dev, torch.int64)
+    P = n // 2
+    ref = _floats(ref_logp, "ref_logp", T, dev)
+    tg, ty = (None, SOT_I32) if target is None else _indices(target, "target", (T,), dev)
     if scale is None:
         scale = 1.0 / max(P, 1)
-    s, (out, g) = _stream_of(stream, lambda: (torch.empty((2, P), device=dev), torch.empty(T, device=dev)))
-    at = out.data_ptr()
-    rc = load().sot_preference_loss(logp.data_ptr(), _at(ref_logp), _at(target), ty, offsets.data_ptr(), P, T, beta,
-                                    label_smoothing, 1 if average else 0, scale, at, at + 4 * P, g.data_ptr(), s)
-    _check(rc, "sot_preference_loss")
-    loss, margin = out
-    return loss, margin, g
+
+    def call(s):
+        out = torch.empty((2, P), device=logp.device)
+        g = torch.empty(T, device=logp.device)
+        p = out.data_ptr()
+        rc = load().sot_preference_loss(lp, ref, tg, ty, off, P, T, beta, label_smoothing, 1 if average else 0, scale, p,
+                                        p + 4 * P, g.data_ptr(), s)
+        if rc:
+            _check(rc, "sot_preference_loss")
+        return *out.unbind(), g
+    return call(_raw_stream(dev)) if stream is None else _on(stream, call)
 
 
 def sot_balance_loss(logits, ids, mask=None, balance_coef=1.0, z_coef=0.0, grad=True, stream=None):
     """A router's balance and z losses with per-expert counts: (counts [E] int32,
     loss [2], grad [T, E] or None) of router logits [T, E] and the experts chosen,
     ids [T, K] (outside [0, E): dropped).  mask [T] bool: False leaves a token out."""
-    T, E, ld, dt = _rows(logits)
-    dev = logits.device
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
-        raise ValueError("ids must be [rows, choices]")
-    K = ids.shape[1]
-    ty = _index(ids, "ids", (T, K), dev)
-    _want(mask, "mask", T, dev, torch.bool)
-    s, (counts, loss, (g, ldg)) = _stream_of(stream, lambda: (
-        torch.empty(E, dtype=torch.int32, device=dev), torch.empty(2, device=dev), _grad_rows(grad, logits, T, E, dt)))
-    rc = load().sot_balance_loss(logits.data_ptr(), T, E, ld, dt, ids.data_ptr(), ty, K, _at(mask), balance_coef, z_coef,
-                                 counts.data_ptr(), loss.data_ptr(), _at(g), ldg, s)
-    _check(rc, "sot_balance_loss")
-    return counts, loss, g
+    x, T, E, ld, dt, dev = _logits(logits)
+    i, ty, K = _pairs(ids, "ids", T, dev)
+    m = _floats(mask, "mask", T, dev, torch.bool)
+
+    def call(s):
+        counts = torch.empty(E, dtype=torch.int32, device=logits.device)
+        loss = torch.empty(2, device=logits.device)
+        g, at, ldg = _grad_of(grad, logits, T, E, ld, dt, dev)
+        rc = load().sot_balance_loss(x, T, E, ld, dt, i, ty, K, m, balance_coef, z_coef, counts.data_ptr(),
+                                     loss.data_ptr(), at, ldg, s)
+        if rc:
+            _check(rc, "sot_balance_loss")
+        return counts, loss, g
+    return call(_raw_stream(dev)) if stream is None else _on(stream, call)
 
 
 def sot_async_status(stream=None):

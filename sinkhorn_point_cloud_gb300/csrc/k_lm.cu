@@ -2,8 +2,6 @@
 // log-probabilities from a known log-sum-exp, and the paired preference loss.
 #include <cuda_runtime.h>
 
-#include <cstdlib>
-#include <cstdio>
 #include "kernels.h"
 #include "lm_row.cuh"
 #include "tc.h"
@@ -123,10 +121,6 @@ void row_plan(bool grads, long long T, int dtype, int V, int K, bool tail, int s
         *p = LmRowPlan{NW, CL, (int)G, smem, sms};
     };
     const auto warps = [](long long G, int per) { return G <= per * 128ll ? 4 : G <= per * 256ll ? 8 : 16; };
-    if (const char* e = getenv("LM_TUNE")) {
-        int nw, cl;
-        if (sscanf(e, "%d,%d", &nw, &cl) == 2) { plan(nw, cl); return; }
-    }
     // Up to 8 KB a warp takes the row alone: 16384 rows of 4096 bf16 with gradient take
     // 57 us, with a CTA each 81 us; at 6144 a CTA is as fast (95 us both).
     if (total <= 528) {

@@ -5,9 +5,18 @@
 // f_e = E c_e / (K N):
 //   loss[0] = coef / N sum_t sum_e f_e p_te,   loss[1] = z_coef / N sum_t lse_t^2,
 //   dx_te = 1/N ( coef p_te (f_e - sum_j f_j p_tj) + 2 z_coef lse_t p_te ).
-// The counts come first (a small pass over the choices); then one warp takes a
-// token, holds its E logits in registers and writes the gradient from them, so
-// each logit is read once and each gradient written once.
+// The counts come first, then every token's row is read once, its softmax and its
+// two sums formed in registers, and its gradient written from them; the sums over
+// the tokens are joined in a fixed order.
+//   Small batches: one cluster of CTAs does all of it in one launch, counting and
+// joining through distributed shared memory.
+//   Large ones: a counting kernel leaves each cluster's counts in scratch; the main
+// kernel is launched along with it (programmatic dependent launch), reads its
+// first rows meanwhile, adds the counts up and goes on; its last CTA to finish joins
+// the sums.
+// A power of two of lanes takes a row, two granules of 16 bytes a lane (four
+// elements a lane where the rows are not aligned to granules; more of both for
+// many experts), as many rows at a time as fit a warp.
 #include <cuda_runtime.h>
 
 #include "kernels.h"
@@ -19,136 +28,421 @@ namespace sot {
 namespace {
 
 constexpr int BAL_NT = 256;
-constexpr int BAL_PARTS = 304;
+constexpr int CNT_NT = 512;
+constexpr int CNT_CL = 8;      // CTAs of a counting cluster
+constexpr int CNT_PARTS = 16;  // counting clusters at most
+constexpr int SMALL_CL = 8;    // CTAs of the small-batch kernel at most
 
-__global__ void __launch_bounds__(BAL_NT) lm_count_kernel(LmBalanceArgs a) {
-    __shared__ int hist[LM_MAX_E];
-    __shared__ int kept;
-    for (int e = threadIdx.x; e < a.E; e += BAL_NT) hist[e] = 0;
-    if (threadIdx.x == 0) kept = 0;
-    __syncthreads();
-    int n = 0;
-    for (long long t = (long long)blockIdx.x * BAL_NT + threadIdx.x; t < a.T; t += (long long)gridDim.x * BAL_NT) {
-        if (a.mask && !a.mask[t]) continue;
-        ++n;
-        for (int k = 0; k < a.K; ++k) {
-            const int id = load_index(a.ids, a.ids_type, t * a.K + k, a.E);
-            if (id >= 0) atomicAdd(&hist[id], 1);
+// Adds the choices of tokens first, first + step, ... to hist; returns how many of
+// these tokens are kept.
+__device__ __forceinline__ int count_tokens(const LmBalanceArgs& a, long long first, long long step, int* hist) {
+    int kept = 0;
+    for (long long t = first; t < a.T; t += step) {
+        const bool keep = !a.mask || a.mask[t];
+        kept += keep;
+        for (int k0 = 0; k0 < a.K; k0 += 4) {  // four loads under way
+            int id[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) id[j] = k0 + j < a.K ? load_index(a.ids, a.ids_type, t * a.K + k0 + j, a.E) : -1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (keep && id[j] >= 0) atomicAdd(&hist[id[j]], 1);
         }
     }
-    if (n) atomicAdd(&kept, n);
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += BAL_NT)
-        if (hist[e]) atomicAdd(&a.counts[e], hist[e]);
-    if (threadIdx.x == 0 && kept) atomicAdd(a.kept, kept);
+    return kept;
 }
 
-// One warp per token; lane l holds experts l, l + 32, ...
-template <int DT, int R>
-__global__ void __launch_bounds__(BAL_NT) lm_balance_kernel(LmBalanceArgs a) {
+// A thread's sums over its tokens (compensated): the balance terms, the squares of lse.
+struct Sums {
+    float2 dot, z;
+    __device__ __forceinline__ static void add(float2& s, float v) {
+        const float2 t = two_sum(s.x, v);
+        s = make_float2(t.x, s.y + t.y);
+    }
+};
+
+__device__ __forceinline__ float group_max(float v, int lanes) {
+    if (lanes == 32) return warp_max1(v);
+    for (int o = lanes >> 1; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// The rows of one warp of `warps`: `lanes` lanes a row, 32 / lanes rows at a time,
+// the next rows' loads under way while these are worked on.  VEC: R granules a
+// lane.  Otherwise 2 R elements a lane, `lanes` apart.  f holds coef f_e, then
+// zeros; `counted` is called once the first loads are under way, and gives 1/N.
+template <int DT, int R, bool VEC, class Counted>
+__device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long warp, long long warps, const float* f,
+                                             Sums& out, Counted counted) {
     using T = typename Elem<DT>::T;
-    __shared__ float f[LM_MAX_E];
-    __shared__ double red[2][BAL_NT / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kept = *a.kept;
-    const float inv_n = kept > 0 ? 1.f / (float)kept : 0.f;
-    for (int e = threadIdx.x; e < a.E; e += BAL_NT)
-        f[e] = (float)a.counts[e] * (float)((double)a.E / ((double)a.K * (double)(kept > 0 ? kept : 1)));
-    __syncthreads();
-    double sum_dot = 0.0, sum_z = 0.0;
-    for (long long t = (long long)blockIdx.x * (BAL_NT / 32) + warp; t < a.T; t += (long long)gridDim.x * (BAL_NT / 32)) {
-        T* const g = a.grad ? static_cast<T*>(a.grad) + t * a.ldg : nullptr;
-        if (a.mask && !a.mask[t]) {
-            if (g)
-                for (int e = lane; e < a.E; e += 32) g[e] = Elem<DT>::put(0.f);
-            continue;
-        }
-        const T* const x = static_cast<const T*>(a.x) + t * a.ld;
-        float v[R], m = -INFINITY;
+    constexpr int N = VEC ? Elem<DT>::N : 2, H = R * N / 2;  // H pairs a lane
+    const int lane = threadIdx.x & 31;
+    const int units = VEC ? a.E / N : (a.E + 1) / 2;
+    int lanes = 32;
+    while (lanes > 1 && lanes / 2 * R >= units) lanes >>= 1;
+    const int per = 32 / lanes, sub = lane & (lanes - 1);
+    const long long step = warps * per;
+    out = Sums{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    long long t = warp * per + lane / lanes;
+    const auto kept = [&](long long r) { return r < a.T && (!a.mask || a.mask[r]); };
+    uint4 v[VEC ? R : 1];
+    float2 w[VEC ? 1 : R];
+    const auto load = [&](long long r, bool keep) {
+        const T* const row = static_cast<const T*>(a.x) + r * a.ld;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = e < a.E ? Elem<DT>::get(x[e]) : -INFINITY;
-            m = fmaxf(m, v[i]);
+            if constexpr (VEC) {
+                const int g = sub + i * lanes;
+                v[i] = keep && g < units ? reinterpret_cast<const uint4*>(row)[g] : nothing<DT>();
+            } else {
+                const int e = sub + 2 * i * lanes;
+                w[i].x = keep && e < a.E ? Elem<DT>::get(row[e]) : -INFINITY;
+                w[i].y = keep && e + lanes < a.E ? Elem<DT>::get(row[e + lanes]) : -INFINITY;
+            }
         }
-        m = warp_max(m);
-        const float u = m == -INFINITY ? 0.f : m;
-        float s = 0.f, d = 0.f;
+    };
+    bool keep = kept(t), next = kept(t + step);
+    load(t, keep);
+    const float inv_n = counted();
+    for (long long base = warp * per; base < a.T; base += step, t += step) {
+        float2 x[H];
+        float m;
+        if constexpr (VEC) {
+            uint4 top = v[0];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = ex2f((v[i] - u) * SOT_LOG2E);
-            s += v[i];
-            d = fmaf(v[i], e < a.E ? f[e] : 0.f, d);
-        }
-        s = warp_sum(s);
-        d = warp_sum(d) / s;
-        const float lse = m + logf(s);
-        sum_dot += d;
-        sum_z += (double)lse * lse;
-        if (g) {
-            const float base = 2.f * a.z_coef * lse - a.coef * d, k = inv_n / s;
+            for (int i = 1; i < R; ++i) top = max2<DT>(top, v[i]);
+            m = max_of<DT>(top);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const int e = lane + 32 * i;
-                if (e < a.E) g[e] = Elem<DT>::put(v[i] * k * fmaf(a.coef, f[e], base));
+                float2 p[N / 2];
+                unpack<DT>(v[i], p);
+#pragma unroll
+                for (int k = 0; k < N / 2; ++k) x[i * (N / 2) + k] = p[k];
+            }
+        } else {
+            m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                x[i] = w[i];
+                m = fmaxf(m, fmaxf(x[i].x, x[i].y));
+            }
+        }
+        const bool now = keep;
+        keep = next;
+        if (base + step < a.T) {
+            load(t + step, keep);
+            next = kept(t + 2 * step);
+        }
+        m = group_max(m, lanes);
+        const float u = __fmul_rn(m, SOT_LOG2E);
+        const bool far = !(fabsf(u) < INFINITY);
+        if (!far) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) x[i] = ex2_pair(x[i], u, SOT_LOG2E);
+        } else {
+#pragma unroll
+            for (int i = 0; i < H; ++i) x[i] = make_float2(weight_of(x[i].x, m, SOT_LOG2E), weight_of(x[i].y, m, SOT_LOG2E));
+        }
+        // coef f of the lane's experts, in the order of x
+        const auto shares = [&](int i, float2 (&c)[VEC ? N / 2 : 1]) {
+            if constexpr (VEC) {
+                const float4* const q = reinterpret_cast<const float4*>(f + (sub + i * lanes) * N);
+#pragma unroll
+                for (int k = 0; k < N / 4; ++k) {
+                    const float4 r = q[k];
+                    c[2 * k] = make_float2(r.x, r.y);
+                    c[2 * k + 1] = make_float2(r.z, r.w);
+                }
+            } else
+                c[0] = make_float2(f[sub + 2 * i * lanes], f[sub + (2 * i + 1) * lanes]);
+        };
+        constexpr int C = VEC ? N / 2 : 1;
+        float2 sum = make_float2(0.f, 0.f), dots = sum;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float2 c[C];
+            shares(i, c);
+#pragma unroll
+            for (int k = 0; k < C; ++k) {
+                sum = fadd2(sum, x[i * C + k]);
+                dots = ffma2(x[i * C + k], c[k], dots);
+            }
+        }
+        float s = sum.x + sum.y, d = dots.x + dots.y;
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            d += __shfl_xor_sync(0xffffffffu, d, o);
+        }
+        const float inv_s = __fdividef(1.f, s), dot = d * inv_s;  // coef sum f p
+        const float lse = far ? m + __logf(s) : (u + __log2f(s)) * SOT_LN2;
+        if (now && sub == 0) {
+            Sums::add(out.dot, dot);
+            Sums::add(out.z, lse * lse);
+        }
+        if (!a.grad || t >= a.T) continue;
+        T* const g = static_cast<T*>(a.grad) + t * a.ldg;
+        // (the weights of a token that is left out are 0)
+        const float bias = now ? 2.f * a.z_coef * lse - dot : 0.f, k = now ? inv_n * inv_s : 0.f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float2 c[C];
+            shares(i, c);
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                x[i * C + j] = fmul2(x[i * C + j], fmul2(fadd2(c[j], make_float2(bias, bias)), make_float2(k, k)));
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            if constexpr (VEC) {
+                float2 p[N / 2];
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) p[j] = x[i * (N / 2) + j];
+                if (sub + i * lanes < units) reinterpret_cast<uint4*>(g)[sub + i * lanes] = pack<DT>(p);
+            } else {
+                const int e = sub + 2 * i * lanes;
+                if (e < a.E) g[e] = Elem<DT>::put(x[i].x);
+                if (e + lanes < a.E) g[e + lanes] = Elem<DT>::put(x[i].y);
             }
         }
     }
+}
+
+// The two sums of a CTA, in every lane of warp 0 (fixed order).
+template <int NT>
+__device__ __forceinline__ float2 block_sums(const Sums& s, float (&red)[2][NT / 32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float d = warp_sum(s.dot.x + s.dot.y), z = warp_sum(s.z.x + s.z.y);
     if (lane == 0) {
-        red[0][warp] = sum_dot;
-        red[1][warp] = sum_z;
+        red[0][warp] = d;
+        red[1][warp] = z;
     }
     __syncthreads();
-    if (threadIdx.x < 2) {
-        double v = 0.0;
-        for (int w = 0; w < BAL_NT / 32; ++w) v += red[threadIdx.x][w];
-        a.part[2 * blockIdx.x + threadIdx.x] = (float)v;
+    if (warp != 0) return make_float2(0.f, 0.f);
+    return make_float2(warp_sum(lane < NT / 32 ? red[0][lane] : 0.f), warp_sum(lane < NT / 32 ? red[1][lane] : 0.f));
+}
+// f_e = E c_e / (K N): the factor of c_e.
+__device__ __forceinline__ float share_of(const LmBalanceArgs& a, int kept) {
+    return (float)a.E / ((float)a.K * (float)max(kept, 1));
+}
+// coef is already in the dot sums
+__device__ __forceinline__ void write_loss(const LmBalanceArgs& a, float dot, float z, int kept) {
+    a.loss[0] = kept > 0 ? dot / (float)kept : 0.f;
+    a.loss[1] = kept > 0 ? a.z_coef * (z / (float)kept) : 0.f;
+}
+// A 32-bit value of another CTA's shared memory.
+__device__ __forceinline__ int cluster_load(const int* local_ptr, uint32_t rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(smem_u32(local_ptr), rank)) : "memory");
+    return v;
+}
+
+// ---- large batches ------------------------------------------------------------
+// Each cluster leaves its counts and its number of kept tokens in scratch.
+__global__ void __launch_bounds__(CNT_NT) lm_count_kernel(LmBalanceArgs a) {
+    __shared__ int hist[LM_MAX_E + 1];  // the last: kept tokens
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t rank = cluster_rank();
+    const int part = blockIdx.x / CNT_CL;
+    for (int e = threadIdx.x; e <= a.E; e += CNT_NT) hist[e] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
+    __syncthreads();
+    const int n = count_tokens(a, (long long)blockIdx.x * CNT_NT + threadIdx.x, (long long)gridDim.x * CNT_NT, hist);
+    if (n) atomicAdd(&hist[a.E], n);
+    cluster_sync();
+    for (int e = rank * CNT_NT + threadIdx.x; e <= a.E; e += CNT_CL * CNT_NT) {
+        int c = 0;
+#pragma unroll
+        for (int p = 0; p < CNT_CL; ++p) c += cluster_load(&hist[e], p);
+        a.part_counts[part * (a.E + 1) + e] = c;
+    }
+    cluster_sync();  // no CTA leaves while a peer may still read it
+}
+
+template <int DT, int R, bool VEC>
+__global__ void __launch_bounds__(BAL_NT, R <= 2 ? 4 : 2) lm_balance_kernel(LmBalanceArgs a) {
+    __shared__ __align__(16) float f[LM_MAX_E];
+    __shared__ float red[2][BAL_NT / 32];
+    __shared__ bool last;
+    int kept = 0;
+    Sums s;
+    balance_rows<DT, R, VEC>(a, (long long)blockIdx.x * (BAL_NT / 32) + (threadIdx.x >> 5),
+                             (long long)gridDim.x * (BAL_NT / 32), f, s, [&]() {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        const auto total = [&](int e) {  // all loads under way at once
+            int c[CNT_PARTS], sum = 0;
+#pragma unroll
+            for (int p = 0; p < CNT_PARTS; ++p) c[p] = p < a.parts ? a.part_counts[p * (a.E + 1) + e] : 0;
+#pragma unroll
+            for (int p = 0; p < CNT_PARTS; ++p) sum += c[p];
+            return sum;
+        };
+        kept = total(a.E);
+        const float k = a.coef * share_of(a, kept);
+        for (int e = threadIdx.x; e < LM_MAX_E; e += BAL_NT) {
+            const int c = e < a.E ? total(e) : 0;
+            if (e < a.E && blockIdx.x == 0) a.counts[e] = c;
+            f[e] = (float)c * k;
+        }
+        __syncthreads();
+        return kept > 0 ? 1.f / (float)kept : 0.f;
+    });
+    const float2 v = block_sums<BAL_NT>(s, red);
+    if (threadIdx.x == 0) {
+        a.part_sums[blockIdx.x] = v;
+        __threadfence();
+        last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (last) {
+        __threadfence();
+        Sums all{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int b = threadIdx.x; b < (int)gridDim.x; b += BAL_NT) {
+            const float2 w = __ldcg(&a.part_sums[b]);
+            Sums::add(all.dot, w.x);
+            Sums::add(all.z, w.y);
+        }
+        const float2 w = block_sums<BAL_NT>(all, red);
+        if (threadIdx.x == 0) write_loss(a, w.x, w.y, kept);
     }
 }
 
-__global__ void lm_balance_sum_kernel(LmBalanceArgs a, int parts) {
-    const int i = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    double v = 0.0;
-    for (int p = lane; p < parts; p += 32) v += (double)a.part[2 * p + i];
-    v = warp_sum_d(v);
-    const int kept = *a.kept;
-    if (lane == 0) a.loss[i] = kept > 0 ? (float)(v * (double)(i ? a.z_coef : a.coef) / (double)kept) : 0.f;
+// ---- small batches --------------------------------------------------------------
+template <int DT, int R, bool VEC>
+__global__ void __launch_bounds__(CNT_NT) lm_balance_small_kernel(LmBalanceArgs a) {
+    __shared__ int hist[LM_MAX_E + 1];  // the last: kept tokens
+    __shared__ __align__(16) float f[LM_MAX_E];
+    __shared__ float red[2][CNT_NT / 32];
+    __shared__ float sums[SMALL_CL][2];
+    const uint32_t rank = cluster_rank();
+    const int CL = gridDim.x;
+    for (int e = threadIdx.x; e <= a.E; e += CNT_NT) hist[e] = 0;
+    __syncthreads();
+    const int n = count_tokens(a, (long long)rank * CNT_NT + threadIdx.x, (long long)CL * CNT_NT, hist);
+    if (n) atomicAdd(&hist[a.E], n);
+    int kept = 0;
+    Sums s;
+    balance_rows<DT, R, VEC>(a, (long long)rank * (CNT_NT / 32) + (threadIdx.x >> 5), (long long)CL * (CNT_NT / 32), f, s, [&]() {
+        if (CL > 1) cluster_sync();
+        else __syncthreads();
+        for (int p = 0; p < CL; ++p) kept += cluster_load(&hist[a.E], p);
+        const float k = a.coef * share_of(a, kept);
+        for (int e = threadIdx.x; e < LM_MAX_E; e += CNT_NT) {
+            int c = 0;
+            if (e < a.E) {
+                for (int p = 0; p < CL; ++p) c += cluster_load(&hist[e], p);
+                if (rank == 0) a.counts[e] = c;
+            }
+            f[e] = (float)c * k;
+        }
+        __syncthreads();
+        return kept > 0 ? 1.f / (float)kept : 0.f;
+    });
+    const float2 v = block_sums<CNT_NT>(s, red);
+    if (threadIdx.x == 0) {
+        const uint32_t to = cluster_addr(smem_u32(sums[rank]), 0);
+        cluster_store(to, v.x);
+        cluster_store(to + 4, v.y);
+    }
+    if (CL > 1) cluster_sync();  // the sums are there, and nobody reads a CTA's counts any more
+    else __syncthreads();
+    if (rank == 0 && threadIdx.x == 0) {
+        Sums t{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        for (int p = 0; p < CL; ++p) {
+            Sums::add(t.dot, sums[p][0]);
+            Sums::add(t.z, sums[p][1]);
+        }
+        write_loss(a, t.dot.x + t.dot.y, t.z.x + t.z.y, kept);
+    }
+}
+
+template <int DT, int R, bool VEC>
+cudaError_t launch_r(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(blocks, 1, 1);
+    if (a.parts == 0) {
+        cfg.blockDim = dim3(CNT_NT, 1, 1);
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = blocks;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        count_launches(1);
+        return cudaLaunchKernelEx(&cfg, lm_balance_small_kernel<DT, R, VEC>, a);
+    }
+    count_launches(2);
+    cfg.gridDim = dim3(a.parts * CNT_CL, 1, 1);
+    cfg.blockDim = dim3(CNT_NT, 1, 1);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CNT_CL;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, lm_count_kernel, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(blocks, 1, 1);
+    cfg.blockDim = dim3(BAL_NT, 1, 1);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelEx(&cfg, lm_balance_kernel<DT, R, VEC>, a);
 }
 
 template <int DT>
-void launch_main(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
-    const int r = (a.E + 31) / 32;
-    if (r <= 1) lm_balance_kernel<DT, 1><<<blocks, BAL_NT, 0, st>>>(a);
-    else if (r <= 2) lm_balance_kernel<DT, 2><<<blocks, BAL_NT, 0, st>>>(a);
-    else if (r <= 4) lm_balance_kernel<DT, 4><<<blocks, BAL_NT, 0, st>>>(a);
-    else if (r <= 8) lm_balance_kernel<DT, 8><<<blocks, BAL_NT, 0, st>>>(a);
-    else if (r <= 16) lm_balance_kernel<DT, 16><<<blocks, BAL_NT, 0, st>>>(a);
-    else lm_balance_kernel<DT, 32><<<blocks, BAL_NT, 0, st>>>(a);
+cudaError_t launch_d(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
+    using T = typename Elem<DT>::T;
+    constexpr int N = Elem<DT>::N;
+    const auto whole = [](const void* p, long long ld) {
+        return (unsigned long long)p % 16 == 0 && ld * (long long)sizeof(T) % 16 == 0;
+    };
+    if (a.E % N == 0 && whole(a.x, a.ld) && (!a.grad || whole(a.grad, a.ldg))) {
+        const int g = a.E / N;
+        if (g <= 4) return launch_r<DT, 1, true>(a, blocks, st);
+        if (g <= 8) return launch_r<DT, 2, true>(a, blocks, st);
+        if (g <= 128) return launch_r<DT, 4, true>(a, blocks, st);
+        if constexpr (N == 4) return launch_r<DT, 8, true>(a, blocks, st);
+    }
+    if (a.E <= 128) return launch_r<DT, 2, false>(a, blocks, st);
+    if (a.E <= 256) return launch_r<DT, 4, false>(a, blocks, st);
+    return launch_r<DT, 16, false>(a, blocks, st);
 }
 
 }  // namespace
 
-int lm_balance_parts() { return BAL_PARTS; }
-
-cudaError_t launch_lm_balance(const LmBalanceArgs& a, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(a.counts, 0, sizeof(int) * a.E, st);
-    if (e != cudaSuccess) return e;
-    e = cudaMemsetAsync(a.kept, 0, sizeof(int), st);
-    if (e != cudaSuccess) return e;
-    const long long want = (a.T + BAL_NT / 32 - 1) / (BAL_NT / 32);
-    const int blocks = (int)(want < 1 ? 1 : want < BAL_PARTS ? want : BAL_PARTS);
-    const long long cw = (a.T + BAL_NT - 1) / BAL_NT;
-    const int cblocks = (int)(cw < 1 ? 1 : cw < BAL_PARTS ? cw : BAL_PARTS);
-    count_launches(3);
-    lm_count_kernel<<<cblocks, BAL_NT, 0, st>>>(a);
-    switch (a.dtype) {
-        case SOT_F32: launch_main<SOT_F32>(a, blocks, st); break;
-        case SOT_F16: launch_main<SOT_F16>(a, blocks, st); break;
-        default: launch_main<SOT_BF16>(a, blocks, st); break;
+// Scratch of a call: none for a small batch.
+LmBalancePlan lm_balance_plan(long long T, int E, int K, int dtype, int sms) {
+    LmBalancePlan p = {};
+    const long long bytes = T * ((long long)E * (dtype == SOT_F32 ? 4 : 2) + 4ll * K);
+    // One cluster up to 256 KB of logits and choices: one launch instead of two and a
+    // scratch allocation outweigh the SMs that stay idle.
+    if (bytes <= 256 * 1024) {
+        const long long want = (T + CNT_NT / 32 - 1) / (CNT_NT / 32);
+        p.blocks = 1;
+        while (p.blocks < SMALL_CL && p.blocks < want) p.blocks *= 2;
+        return p;
     }
-    lm_balance_sum_kernel<<<1, 64, 0, st>>>(a, blocks);
-    return cudaGetLastError();
+    const long long cw = (T + CNT_CL * CNT_NT - 1) / (CNT_CL * CNT_NT), w = (T + BAL_NT / 32 - 1) / (BAL_NT / 32);
+    p.parts = (int)(cw < CNT_PARTS ? cw : CNT_PARTS);
+    p.blocks = (int)(w < 2ll * sms ? w : 2ll * sms);
+    p.sums_at = 0;
+    p.counts_at = sizeof(float2) * p.blocks;
+    p.ticket_at = p.counts_at + sizeof(int) * (size_t)p.parts * (E + 1);
+    p.scratch = p.ticket_at + sizeof(unsigned);
+    return p;
+}
+
+cudaError_t launch_lm_balance(LmBalanceArgs a, const LmBalancePlan& p, unsigned char* scratch, cudaStream_t st) {
+    a.parts = p.parts;
+    if (p.parts) {
+        a.part_sums = reinterpret_cast<float2*>(scratch + p.sums_at);
+        a.part_counts = reinterpret_cast<int*>(scratch + p.counts_at);
+        a.ticket = reinterpret_cast<unsigned*>(scratch + p.ticket_at);
+    }
+    switch (a.dtype) {
+        case SOT_F32: return launch_d<SOT_F32>(a, p.blocks, st);
+        case SOT_F16: return launch_d<SOT_F16>(a, p.blocks, st);
+        default: return launch_d<SOT_BF16>(a, p.blocks, st);
+    }
 }
 
 }  // namespace sot

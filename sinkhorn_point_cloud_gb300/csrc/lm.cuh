@@ -109,6 +109,11 @@ __device__ __forceinline__ void store16(uint4* p, const uint4& v, uint64_t polic
                  : "memory");
 }
 
+template <int DT>
+__device__ __forceinline__ uint4 nothing() {  // N times -inf
+    constexpr unsigned w = DT == SOT_F32 ? 0xff800000u : DT == SOT_F16 ? 0xfc00fc00u : 0xff80ff80u;
+    return make_uint4(w, w, w, w);
+}
 // Largest elements of two vectors, element by element.
 template <int DT>
 __device__ __forceinline__ uint4 max2(const uint4& a, const uint4& b) {

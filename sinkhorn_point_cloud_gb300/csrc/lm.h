@@ -70,8 +70,11 @@ struct LmBalanceArgs {
     int* counts;
     float* loss;  // [2]
     void* grad;   // NULL: losses only
-    int* kept;    // scratch: number of kept tokens
-    float* part;  // scratch: [2 * lm_balance_parts()]
+    // scratch of a large batch (parts = 0: a small one)
+    int parts;
+    float2* part_sums;
+    int* part_counts;
+    unsigned* ticket;
 };
 
 // Whether the tail's marks of a row of V logits fit a CTA's shared memory.
@@ -79,7 +82,11 @@ bool lm_tail_fits(int dtype, int V, int K);
 cudaError_t launch_lm_row(LmOp op, const LmRowArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_lm_grad(const LmGradArgs& a, cudaStream_t st);
 cudaError_t launch_lm_preference(const LmPrefArgs& a, cudaStream_t st);
-int lm_balance_parts();
-cudaError_t launch_lm_balance(const LmBalanceArgs& a, cudaStream_t st);
+struct LmBalancePlan {
+    int blocks, parts;
+    size_t sums_at, counts_at, ticket_at, scratch;
+};
+LmBalancePlan lm_balance_plan(long long T, int E, int K, int dtype, int sms);
+cudaError_t launch_lm_balance(LmBalanceArgs a, const LmBalancePlan& p, unsigned char* scratch, cudaStream_t st);
 
 }  // namespace sot

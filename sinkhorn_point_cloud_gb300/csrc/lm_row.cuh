@@ -341,11 +341,6 @@ __device__ __forceinline__ int edge_granule(const Slice& s, int tid) {
     return -1;
 }
 template <int DT>
-__device__ __forceinline__ uint4 nothing() {  // N times -inf
-    constexpr unsigned w = DT == SOT_F32 ? 0xff800000u : DT == SOT_F16 ? 0xfc00fc00u : 0xff80ff80u;
-    return make_uint4(w, w, w, w);
-}
-template <int DT>
 __device__ __forceinline__ uint4 without(const uint4& v, unsigned out) {
     float2 f[Elem<DT>::N / 2];
     unpack<DT>(v, f);

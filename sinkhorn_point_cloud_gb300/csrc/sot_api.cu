@@ -1804,10 +1804,11 @@ int sot_balance_loss(const void* logits, long long T, int E, long long ld, int d
     a.counts = counts;
     a.loss = loss;
     a.grad = grad;
-    a.kept = S.alloc<int>(1);
-    a.part = S.alloc<float>(2 * (size_t)lm_balance_parts());
-    if (!a.kept || !a.part) return fail(SOT_ERR_NOMEM, "scratch allocation failed");
-    SOT_CUDA(launch_lm_balance(a, (cudaStream_t)stream));
+    const LmBalancePlan p = lm_balance_plan(T, E, K, dtype, device_sms());
+    unsigned char* scratch = nullptr;
+    if (p.scratch && !(scratch = S.alloc<unsigned char>(p.scratch)))
+        return fail(SOT_ERR_NOMEM, "scratch allocation failed");
+    SOT_CUDA(launch_lm_balance(a, p, scratch, (cudaStream_t)stream));
     return SOT_OK;
 }
 
