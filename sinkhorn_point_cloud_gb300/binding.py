@@ -604,14 +604,15 @@ def sot_policy_loss(logits, target, old_logp, advantage, ref_logp=None, weight=N
     ref, w = _floats(ref_logp, "ref_logp", T, dev), _floats(weight, "weight", T, dev)
 
     def call(s):
-        out = torch.empty((3, T), device=logits.device)
-        p = out.data_ptr()
+        loss = torch.empty_like(old_logp)
+        logp, kl = torch.empty_like(loss), torch.empty_like(loss)
         g, at, ldg = _grad_of(grad, logits, T, V, ld, dt, dev)
         rc = load().sot_policy_loss(x, T, V, ld, dt, temperature, tg, ty, old, ref, adv, w, clip_low, clip_high,
-                                    0.0 if ref is None else kl_coef, p, p + 4 * T, p + 8 * T, at, ldg, s)
+                                    0.0 if ref is None else kl_coef, loss.data_ptr(), logp.data_ptr(), kl.data_ptr(), at,
+                                    ldg, s)
         if rc:
             _check(rc, "sot_policy_loss")
-        return *out.unbind(), g
+        return loss, logp, kl, g
     return call(_raw_stream(dev)) if stream is None else _on(stream, call)
 
 
@@ -636,14 +637,13 @@ def sot_preference_loss(logp, offsets, ref_logp=None, target=None, beta=0.1, lab
         scale = 1.0 / max(P, 1)
 
     def call(s):
-        out = torch.empty((2, P), device=logp.device)
-        g = torch.empty(T, device=logp.device)
-        p = out.data_ptr()
-        rc = load().sot_preference_loss(lp, ref, tg, ty, off, P, T, beta, label_smoothing, 1 if average else 0, scale, p,
-                                        p + 4 * P, g.data_ptr(), s)
+        loss = torch.empty(P, device=logp.device)
+        margin, g = torch.empty_like(loss), torch.empty_like(logp)
+        rc = load().sot_preference_loss(lp, ref, tg, ty, off, P, T, beta, label_smoothing, 1 if average else 0, scale,
+                                        loss.data_ptr(), margin.data_ptr(), g.data_ptr(), s)
         if rc:
             _check(rc, "sot_preference_loss")
-        return *out.unbind(), g
+        return loss, margin, g
     return call(_raw_stream(dev)) if stream is None else _on(stream, call)
 
 

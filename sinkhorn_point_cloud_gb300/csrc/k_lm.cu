@@ -4,7 +4,6 @@
 
 #include "kernels.h"
 #include "lm_row.cuh"
-#include "tc.h"
 
 namespace sot {
 
@@ -12,77 +11,122 @@ namespace {
 
 // Gradient of the token log-probabilities from a known log-sum-exp:
 // dx_v = (g / tau) (1[v = target] - p_v).  No statistic is missing, so every
-// granule stands alone: one read and one write per logit.
+// granule stands alone: one read and one write per logit, memory-bound.  A
+// thread's loads go in batches of four.
 constexpr int GRAD_NT = 256;
 
 template <int DT>
-__global__ void __launch_bounds__(GRAD_NT) lm_grad_kernel(LmGradArgs a, int G, int chunks) {
+__global__ void __launch_bounds__(GRAD_NT) lm_grad_kernel(const LmGradArgs a, int G, int chunks) {
     using T = typename Elem<DT>::T;
-    constexpr int N = Elem<DT>::N;
+    constexpr int N = Elem<DT>::N, U = 4;
     const long long row = blockIdx.x / chunks;
-    const int part = (int)(blockIdx.x % chunks);
-    const Slice s = slice_of<DT>(a.x, row, a.ld, a.V, G, part);
+    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
     T* const grow = static_cast<T*>(a.grad) + row * a.ldg;
-    const bool aligned = (((unsigned long long)grow ^ (unsigned long long)(static_cast<const T*>(a.x) + row * a.ld)) & 15) == 0;
+    const Slice s = slice_at<DT>(x, a.V, G, blockIdx.x % chunks);
+    const bool aligned = same_granules<T>(x, grow);
     const int tgt = load_index(a.target, a.target_type, row, a.V);
     const float g = tgt >= 0 ? a.g[row] / a.tau : 0.f;
     const float sc = SOT_LOG2E / a.tau;
-    const float lse = a.lse[row];
-    const float u = lse * a.tau;  // (x - u) / tau = log p
-    for (int i = threadIdx.x; i < s.ng; i += GRAD_NT) {
-        const int e = s.e0 + i * N;
-        float2 f[N / 2];
-        if (g != 0.f) {
-            unpack<DT>(s.src[i], f);
+    const float u = a.lse[row] * SOT_LOG2E;  // log2 p = x sc - u
+    const bool far = !(fabsf(u) < INFINITY);
+    const uint64_t policy = policy_drop();
+    const auto finish = [&](float2 (&f)[N / 2], int c) {  // columns c ..
 #pragma unroll
-            for (int j = 0; j < N / 2; ++j) {
-                const int c = e + 2 * j;
-                f[j].x = g * ((c == tgt ? 1.f : 0.f) - ex2f((f[j].x - u) * sc));
-                f[j].y = g * ((c + 1 == tgt ? 1.f : 0.f) - ex2f((f[j].y - u) * sc));
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < N / 2; ++j) f[j] = make_float2(0.f, 0.f);
+        for (int j = 0; j < N / 2; ++j) {
+            float2 p;
+            if (!far) p = ex2_pair(f[j], u, sc);
+            else p = make_float2(expf((f[j].x - a.lse[row] * a.tau) / a.tau), expf((f[j].y - a.lse[row] * a.tau) / a.tau));
+            f[j].x = g * ((c + 2 * j == tgt ? 1.f : 0.f) - p.x);
+            f[j].y = g * ((c + 2 * j + 1 == tgt ? 1.f : 0.f) - p.y);
         }
-        store_cols<DT>(grow, e, a.V, f, aligned);
+    };
+    if (g == 0.f) {  // not read
+        slice_zero<DT>(s, grow, a.V, aligned, threadIdx.x, GRAD_NT);
+        return;
+    }
+    if (!aligned) {
+        for (int i = threadIdx.x; i < s.ng; i += GRAD_NT) {
+            float2 f[N / 2];
+            unpack<DT>(s.src[i], f);
+            finish(f, s.e0 + i * N);
+            store_cols<DT>(grow, s.e0 + i * N, a.V, f, false);
+        }
+        return;
+    }
+    uint4* const dst = reinterpret_cast<uint4*>(grow + s.e0);
+    for (int i = s.lo + threadIdx.x; i < s.hi; i += U * GRAD_NT) {
+        uint4 v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (i + j * GRAD_NT < s.hi) v[j] = load16(s.src + i + j * GRAD_NT, policy);
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (i + j * GRAD_NT < s.hi) {
+                float2 f[N / 2];
+                unpack<DT>(v[j], f);
+                finish(f, s.e0 + (i + j * GRAD_NT) * N);
+                store16(dst + i + j * GRAD_NT, pack<DT>(f), policy);
+            }
+    }
+    const int e = edge_granule(s, threadIdx.x);
+    if (e >= 0) {
+        float2 f[N / 2];
+        unpack<DT>(s.src[e], f);
+        finish(f, s.e0 + e * N);
+        store_cols<DT>(grow, s.e0 + e * N, a.V, f, false);
     }
 }
 
 // Paired preference loss.  One CTA per pair: the two sequences' sums of
-// (logp - ref) in 64 bits (they cancel in the margin), then the token
+// (logp - ref) to about 48 bits (they cancel in the margin), then the token
 // gradients.  Offsets are clamped to [0, T], so wrong ones touch nothing else.
+// A few KB a pair: the chain of loads, reductions and stores is all it costs.
 constexpr int PREF_NT = 256;
 
-__global__ void __launch_bounds__(PREF_NT) lm_preference_kernel(LmPrefArgs a) {
-    __shared__ double red[4][PREF_NT / 32];
+__global__ void __launch_bounds__(PREF_NT) lm_preference_kernel(const LmPrefArgs a) {
+    constexpr int NW = PREF_NT / 32;
+    __shared__ float2 red[2][NW];
+    __shared__ int count[2][NW];
     const int p = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long off[3];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const long long o = a.offsets[2 * (long long)p + i];
-        off[i] = o < 0 ? 0 : (o > a.T ? a.T : o);
-    }
-    double v[4] = {0.0, 0.0, 0.0, 0.0};  // sums and counts of the chosen and the rejected
+    for (int i = 0; i < 3; ++i) off[i] = min(max(a.offsets[2 * (long long)p + i], 0ll), a.T);
+    float2 v[2];
+    int n[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2; ++h) {
+        v[h] = make_float2(0.f, 0.f);
+        n[h] = 0;
         for (long long t = off[h] + tid; t < off[h + 1]; t += PREF_NT) {
             if (a.target && load_index(a.target, a.target_type, t, 0x7fffffff) < 0) continue;
-            v[2 * h] += (double)a.logp[t] - (a.ref_logp ? (double)a.ref_logp[t] : 0.0);
-            v[2 * h + 1] += 1.0;
+            v[h] = ff_add(v[h], two_sum(a.logp[t], a.ref_logp ? -a.ref_logp[t] : 0.f));
+            ++n[h];
         }
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = warp_sum_d(v[i]);
-        if (lane == 0) red[i][warp] = v[i];
+    for (int h = 0; h < 2; ++h) {
+        v[h] = ff_sum_or_far(v[h]);
+        n[h] = __reduce_add_sync(0xffffffffu, n[h]);
+        if (lane == 0) {
+            red[h][warp] = v[h];
+            count[h][warp] = n[h];
+        }
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = 0.0;
-        for (int k = 0; k < PREF_NT / 32; ++k) v[i] += red[i][k];
+    for (int h = 0; h < 2; ++h) {
+        v[h] = ff_sum_or_far(lane < NW ? red[h][lane] : make_float2(0.f, 0.f));
+        n[h] = __reduce_add_sync(0xffffffffu, lane < NW ? count[h][lane] : 0);
     }
-    const double nc = a.average ? fmax(v[1], 1.0) : 1.0, nr = a.average ? fmax(v[3], 1.0) : 1.0;
-    const float margin = (float)(v[0] / nc - v[2] / nr);
+    const float nc = a.average ? (float)max(n[0], 1) : 1.f, nr = a.average ? (float)max(n[1], 1) : 1.f;
+    float margin;
+    if (a.average) {
+        margin = (float)(to_double(v[0]) / nc - to_double(v[1]) / nr);
+    } else {
+        const float2 d = ff_add(v[0], make_float2(-v[1].x, -v[1].y));
+        const float f = v[0].x - v[1].x;
+        margin = fabsf(f) < INFINITY ? d.x + d.y : f;
+    }
     const float z = a.beta * margin;
     const float e = expf(-fabsf(z)), l = log1pf(e);
     const float sp = (z >= 0.f ? 1.f : e) / (1.f + e), sn = (z >= 0.f ? e : 1.f) / (1.f + e);  // sigma(z), sigma(-z)
@@ -94,7 +138,7 @@ __global__ void __launch_bounds__(PREF_NT) lm_preference_kernel(LmPrefArgs a) {
     }
     if (!a.grad) return;
     const float d = a.scale * a.beta * (a.smoothing * sp - (1.f - a.smoothing) * sn);
-    const float gc = (float)(d / nc), gr = (float)(-d / nr);
+    const float gc = d / nc, gr = -d / nr;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         for (long long t = off[h] + tid; t < off[h + 1]; t += PREF_NT) {
@@ -111,20 +155,19 @@ __global__ void __launch_bounds__(PREF_NT) lm_preference_kernel(LmPrefArgs a) {
 int row_granule(int dtype) { return dtype == SOT_F32 ? 4 : 8; }
 
 // How a row is cut and who works on it.
-void row_plan(bool grads, long long T, int dtype, int V, int K, bool tail, int sms, LmRowPlan* p) {
+void row_plan(bool grads, bool whole, long long T, int dtype, int V, int K, bool tail, int sms, LmRowPlan* p) {
     const int N = row_granule(dtype);
-    const long long total = ((long long)V + 2 * N - 2) / N;  // granules, whatever the row's alignment
+    // granules of a row: `whole` where every row starts with one, otherwise whatever its alignment
+    const long long total = ((long long)V + (whole ? N - 1 : 2 * N - 2)) / N;
     const auto plan = [&](int NW, int CL) {
         const long long G = (total + CL - 1) / CL;
-        const size_t smem = NW == 1 ? ((size_t)G * 32 + (size_t)K * 12) * WARP_ROWS
-                                    : (size_t)K * 12 + (tail ? ((size_t)G + 3) / 4 * 4 : 0);
-        *p = LmRowPlan{NW, CL, (int)G, smem, sms};
+        const size_t smem = NW == 0 ? (size_t)K * 12 * SHORT_NW : (size_t)K * 12 + (tail ? ((size_t)G + 3) / 4 * 4 : 0);
+        *p = LmRowPlan{NW, CL, (int)G, smem};
     };
     const auto warps = [](long long G, int per) { return G <= per * 128ll ? 4 : G <= per * 256ll ? 8 : 16; };
-    // Up to 8 KB a warp takes the row alone: 16384 rows of 4096 bf16 with gradient take
-    // 57 us, with a CTA each 81 us; at 6144 a CTA is as fast (95 us both).
-    if (total <= 528) {
-        plan(1, 1);
+    // Up to 8 KB a warp takes the row alone.
+    if (total <= 512 && K <= SHORT_MAX_K) {
+        plan(0, 1);
     } else if (T < sms) {
         // Few rows: cut a row further, down to 512 granules a CTA, while the SMs have
         // room, and give it enough warps for eight granules a thread.
@@ -150,19 +193,17 @@ void row_plan(bool grads, long long T, int dtype, int V, int K, bool tail, int s
 
 bool lm_tail_fits(int dtype, int V, int K) {
     LmRowPlan p;
-    row_plan(true, 1ll << 31, dtype, V, K, true, 1, &p);
+    row_plan(true, false, 1ll << 31, dtype, V, K, true, 1, &p);
     return p.smem <= 200 * 1024;
 }
 
 cudaError_t launch_lm_row(LmOp op, const LmRowArgs& a, int sms, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     LmRowPlan p;
-    row_plan(op != LM_LOGPROB, a.T, a.dtype, a.V, a.K, a.tail != 0, sms, &p);
+    const bool whole = (unsigned long long)a.x % 16 == 0 && a.ld % row_granule(a.dtype) == 0;
+    row_plan(op != LM_LOGPROB, whole, a.T, a.dtype, a.V, a.K, a.tail != 0, sms, &p);
     if (a.T * p.CL > 0x7fffffffll) return cudaErrorInvalidValue;
-    LmRowLaunch L = {};
-    tc_test_hold(&L.hold, &L.wait_ns);
-    cudaError_t e = async_status_address(&L.status);
-    if (e != cudaSuccess) return e;
+    const LmRowLaunch L = {p.CL, p.G};
     count_launches(1);
     switch (a.dtype) {
         case SOT_F32: return launch_row_f32(op, a, p, L, st);
@@ -171,12 +212,13 @@ cudaError_t launch_lm_row(LmOp op, const LmRowArgs& a, int sms, cudaStream_t st)
     }
 }
 
-cudaError_t launch_lm_grad(const LmGradArgs& a, cudaStream_t st) {
+cudaError_t launch_lm_grad(const LmGradArgs& a, int sms, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     const int N = row_granule(a.dtype);
     const long long total = ((long long)a.V + 2 * N - 2) / N;
-    // blocks of at least 2048 granules (32 KB), fewer blocks where the grid's limit asks for it
-    long long G = 2048;
+    // Eight granules a thread, or four where that leaves SMs without work; more where
+    // the grid's limit asks for it.
+    long long G = (total + 2047) / 2048 * a.T < 2ll * sms ? 1024 : 2048;
     while ((total + G - 1) / G * a.T > 0x7fffffffll) G *= 2;
     const int chunks = (int)((total + G - 1) / G);
     const dim3 grid((unsigned)(chunks * a.T));

@@ -2,8 +2,6 @@
 // half-steps: centring, packing, state <-> potential conversion, the stop
 // decision, deterministic partial reductions, the COO scan and the gradient
 // on a stored COO support.
-#include <atomic>
-
 #include "common.cuh"
 #include "kernels.h"
 
@@ -268,21 +266,6 @@ __global__ void status_merge_kernel(const int* status) { atomicOr(&g_async_statu
 cudaError_t launch_status_merge(const int* status, cudaStream_t st) {
     count_launches(1); status_merge_kernel<<<1, 1, 0, st>>>(status);
     return cudaGetLastError();
-}
-// Its address on the current device, for kernels that report by themselves.
-cudaError_t async_status_address(unsigned** out) {
-    static std::atomic<unsigned*> cached[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const bool keep = dev >= 0 && dev < 64;
-    if (keep && (*out = cached[dev].load(std::memory_order_relaxed))) return cudaSuccess;
-    void* p = nullptr;
-    e = cudaGetSymbolAddress(&p, g_async_status);
-    if (e != cudaSuccess) return e;
-    *out = static_cast<unsigned*>(p);
-    if (keep) cached[dev].store(*out, std::memory_order_relaxed);
-    return cudaSuccess;
 }
 cudaError_t read_clear_async_status(cudaStream_t st, unsigned* out) {
     unsigned v = 0;

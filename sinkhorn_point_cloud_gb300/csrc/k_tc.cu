@@ -252,12 +252,11 @@ void tc_set_test_hold(int tile, int after, unsigned long long wait_ns) {
     g_wait_ns.store(wait_ns > 0 ? wait_ns : TC_WAIT_NS);
 }
 
-void tc_test_hold(int* tile, unsigned long long* wait_ns) {
-    *tile = g_hold_tile.load();
-    *wait_ns = g_wait_ns.load();
-    if (*tile >= 0 && g_hold_after.load() > 0 && g_hold_after.fetch_sub(1) > 0) *tile = -1;
+static void tc_fill_waits(TcOps& ops) {
+    ops.hold_tile = g_hold_tile.load();
+    ops.wait_ns = g_wait_ns.load();
+    if (ops.hold_tile >= 0 && g_hold_after.load() > 0 && g_hold_after.fetch_sub(1) > 0) ops.hold_tile = -1;
 }
-static void tc_fill_waits(TcOps& ops) { tc_test_hold(&ops.hold_tile, &ops.wait_ns); }
 
 // Column biases of one half-step, c_j = log2 w_j - state_j, padded with -inf
 // to whole tiles: the producer moves a tile's biases with one bulk copy.

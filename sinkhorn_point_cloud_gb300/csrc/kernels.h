@@ -153,7 +153,6 @@ cudaError_t launch_count_iter(const int* stop_flag, int* counter, cudaStream_t s
 // OR a call's status word into the device's word for asynchronous calls.
 cudaError_t launch_status_merge(const int* status, cudaStream_t st);
 // Read and clear that word (synchronises `st`).
-cudaError_t async_status_address(unsigned** out);
 cudaError_t read_clear_async_status(cudaStream_t st, unsigned* out);
 cudaError_t launch_check_inputs(const float* X, const float* w, long long count_pts, int d,
                                 long long count_w, int* bad, cudaStream_t st);

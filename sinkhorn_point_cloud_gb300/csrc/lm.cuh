@@ -349,35 +349,4 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_store(uint32_t ra, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ra), "f"(v) : "memory");
 }
-// Arrives on a barrier of another CTA, after this thread's stores to it.
-__device__ __forceinline__ void cluster_arrive(uint32_t ra) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
-}
-// Waits for a phase of a barrier, other CTAs' arrivals included; the thread sleeps
-// in the hardware for up to 2 us at a time.  Gives up like mbar_wait_bounded.
-__device__ __forceinline__ bool row_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 2000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-static __device__ __noinline__ bool row_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (row_try_wait(bar, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer_ns() - t0 > limit_ns) {
-            *abort = 1;
-            return false;
-        }
-    }
-}
-__device__ __forceinline__ bool row_wait(uint32_t bar, uint32_t parity, volatile int* abort, unsigned long long limit_ns) {
-    return row_try_wait(bar, parity) || row_wait_slow(bar, parity, abort, limit_ns);
-}
-
 }  // namespace sot

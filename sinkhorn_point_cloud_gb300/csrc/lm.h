@@ -80,7 +80,7 @@ struct LmBalanceArgs {
 // Whether the tail's marks of a row of V logits fit a CTA's shared memory.
 bool lm_tail_fits(int dtype, int V, int K);
 cudaError_t launch_lm_row(LmOp op, const LmRowArgs& a, int sms, cudaStream_t st);
-cudaError_t launch_lm_grad(const LmGradArgs& a, cudaStream_t st);
+cudaError_t launch_lm_grad(const LmGradArgs& a, int sms, cudaStream_t st);
 cudaError_t launch_lm_preference(const LmPrefArgs& a, cudaStream_t st);
 struct LmBalancePlan {
     int blocks, parts;

@@ -15,8 +15,7 @@
 // pass, joins the statistics (with the cluster's other CTAs through distributed
 // shared memory) and forms the loss and the gradient's coefficients.
 //
-// lm_warp_kernel: short rows, a warp each, kept in shared memory between the
-// passes.
+// lm_short_kernel: short rows, a warp each, kept in registers between the passes.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -30,10 +29,7 @@ constexpr int ROW_MAX_NW = 16;  // streaming warps of a CTA
 constexpr int NREC = 6;         // a CTA's record: (m, s), the entries' (m, s), the entries' sum q x in two parts
 
 struct LmRowLaunch {
-    int CL, G;                   // CTAs a row, granules a slice
-    int hold;                    // testing hook: no copy from this row of a warp on (-1: off)
-    unsigned long long wait_ns;  // limit of every wait
-    unsigned* status;            // the device's status word of asynchronous calls
+    int CL, G;  // CTAs a row, granules a slice
 };
 
 // What the row's threads need once its statistics are known.
@@ -352,21 +348,10 @@ __device__ __forceinline__ uint4 without(const uint4& v, unsigned out) {
     return pack<DT>(f);
 }
 
-// Where a slice's granules come from and the gradient's go to: device memory, with
-// L2 policies, or (short rows) shared memory.
-struct FromGlobal {
-    const uint4* p;
-    uint64_t policy;
-    __device__ __forceinline__ uint4 operator()(int g) const { return load16(p + g, policy); }
-};
-struct FromShared {
-    const uint4* p;
-    __device__ __forceinline__ uint4 operator()(int g) const { return p[g]; }
-};
-
-template <int DT, bool CUT, class Src>
-__device__ __forceinline__ void slice_stats(Running& r, const Slice& s, const Src& src, const unsigned char* cut, int V,
+template <int DT, bool CUT>
+__device__ __forceinline__ void slice_stats(Running& r, const Slice& s, uint64_t policy, const unsigned char* cut, int V,
                                             float sc, int tid, int NT) {
+    const auto src = [&](int g) { return load16(s.src + g, policy); };
     constexpr int N = Elem<DT>::N, U = 4;
     for (int g = s.lo + tid; g < s.hi; g += 2 * U * NT) {
         uint4 v[U], w[U];
@@ -417,9 +402,10 @@ __device__ __forceinline__ void grad_of(float2 (&f)[Elem<DT>::N / 2], const RowC
 }
 
 // grow: the gradient's row; aligned: its granules are the logits' granules.
-template <int DT, class Src>
-__device__ __forceinline__ void slice_grad(const Slice& s, const Src& src, const RowCoef& c, typename Elem<DT>::T* grow,
-                                           int V, float sc, bool aligned, uint64_t policy, int tid, int NT) {
+template <int DT>
+__device__ __forceinline__ void slice_grad(const Slice& s, const RowCoef& c, typename Elem<DT>::T* grow, int V, float sc,
+                                           bool aligned, uint64_t policy, int tid, int NT) {
+    const auto src = [&](int g) { return load16(s.src + g, policy); };
     constexpr int N = Elem<DT>::N, U = 4;
     if (aligned) {
         uint4* const dst = reinterpret_cast<uint4*>(grow + s.e0);
@@ -481,7 +467,7 @@ __device__ __forceinline__ bool same_granules(const T* x, const T* g) {
 
 // NW streaming warps and the row's own warp.
 template <int DT, int OP, int NW, bool TAIL>
-__global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? 7 : NW == 8 ? 4 : 2)
+__global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8 : 7) : NW == 8 ? 4 : 2)
     lm_row_kernel(const LmRowArgs a, const LmRowLaunch L) {
     using T = typename Elem<DT>::T;
     constexpr int N = Elem<DT>::N, NT = NW * 32;
@@ -499,7 +485,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? 7 : NW == 8 ? 4 : 2)
     const long long row = blockIdx.x / L.CL;
     const RowMeta m = row_meta<OP>(a, row_load<OP>(a, row, warp == NW));
     const T* const x = static_cast<const T*>(a.x) + row * a.ld;
-    T* const grow = a.grad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
+    T* const grow = OP != LM_LOGPROB && a.grad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
     const bool aligned = same_granules<T>(x, grow);
     const Slice s = slice_at<DT>(x, a.V, L.G, rank);
     const int c0 = s.e0, c1 = s.e0 + s.ng * N;  // the slice's columns
@@ -532,7 +518,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? 7 : NW == 8 ? 4 : 2)
     } else {
         if (TAIL) __syncthreads();
         Running r;
-        slice_stats<DT, TAIL>(r, s, FromGlobal{s.src, first}, reinterpret_cast<const unsigned char*>(cut), a.V, sc, tid, NT);
+        slice_stats<DT, TAIL>(r, s, first, reinterpret_cast<const unsigned char*>(cut), a.V, sc, tid, NT);
         const MS w = ms_warp(r.result(), sc);
         if (lane == 0) rec[warp] = w;
     }
@@ -580,7 +566,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? 7 : NW == 8 ? 4 : 2)
     } else {
         if (!grow) return;
         __syncthreads();
-        slice_grad<DT>(s, FromGlobal{s.src, last}, coef, grow, a.V, sc, aligned, last, tid, NT);
+        slice_grad<DT>(s, coef, grow, a.V, sc, aligned, last, tid, NT);
     }
     __syncthreads();  // the corrections come after the columns they replace
     const RowCoef c = coef;
@@ -591,136 +577,115 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? 7 : NW == 8 ? 4 : 2)
         grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(xt, c.M, sc) * c.inv_S) - c.fb);
 }
 
-// Short rows: one warp takes a row from its copy to its corrections, so nothing is
-// handed from warp to warp and a row costs one warp's instructions.  Two buffers
-// a warp: the next row's copy is under way while this one is worked on.
-constexpr int WARP_ROWS = 4;  // warps of a CTA
+// Short rows: one warp takes a row, R granules a lane, and keeps them in registers,
+// so a row costs one warp's instructions and is read once.
+constexpr int SHORT_NW = 8;  // rows of a CTA
+constexpr int SHORT_MAX_K = 256;
 
-template <int DT, int OP>
-__global__ void __launch_bounds__(WARP_ROWS * 32, 5) lm_warp_kernel(const LmRowArgs a, const LmRowLaunch L) {
+template <int DT, int OP, int R, bool TAIL>
+__global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm_short_kernel(const LmRowArgs a) {
     using T = typename Elem<DT>::T;
-    constexpr int N = Elem<DT>::N;
-    extern __shared__ __align__(128) uint4 sm[];
-    __shared__ uint64_t full[WARP_ROWS][2];
-    __shared__ int timed_out[WARP_ROWS];
+    constexpr int N = Elem<DT>::N, U = 4;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ unsigned marks[TAIL ? SHORT_NW : 1][TAIL ? R * 8 : 1];  // a byte a granule
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const float sc = SOT_LOG2E / a.tau;
-    const uint64_t drop_policy = policy_drop();
-    uint4* const buf = sm + (size_t)warp * 2 * L.G;
-    float* const ex = reinterpret_cast<float*>(sm + (size_t)WARP_ROWS * 2 * L.G) + (size_t)warp * 3 * a.K;
+    const long long row = (long long)blockIdx.x * SHORT_NW + warp;
+    if (row >= a.T) return;
+    float* const ex = reinterpret_cast<float*>(dyn) + (size_t)warp * 3 * a.K;
     float* const eq = ex + a.K;
     int* const eid = reinterpret_cast<int*>(eq + a.K);
-    const uint32_t bar0 = smem_u32(&full[warp][0]);
-    volatile int* const abort = &timed_out[warp];
-    if (lane == 0) {
-        mbar_init(bar0, 1);
-        mbar_init(bar0 + 8, 1);
-        *abort = 0;
-        fence_mbar_init();
+    unsigned* const cut = marks[TAIL ? warp : 0];
+    const RowMeta m = row_meta<OP>(a, row_load<OP>(a, row, true));
+    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
+    T* const grow = OP != LM_LOGPROB && a.grad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
+    const bool aligned = same_granules<T>(x, grow);
+    const Slice s = slice_at<DT>(x, a.V, 32 * R, 0);
+    if (!m.keep) {
+        if (grow) slice_zero<DT>(s, grow, a.V, aligned, lane, 32);
+        if (lane == 0) row_outputs(a, row, 0.f);
+        return;
     }
-    __syncwarp();
-    const long long first = (long long)blockIdx.x * WARP_ROWS + warp, step = (long long)gridDim.x * WARP_ROWS;
-    bool copying[2] = {false, false};
-    auto start = [&](long long row, const RowMeta& m, int b) {
-        copying[b] = row / step != L.hold;
-        if (lane == 0 && copying[b]) {
-            const Slice s = slice_of<DT>(a.x, row, a.ld, a.V, L.G, 0);
-            if (m.keep) {
-                mbar_arrive_expect_tx(bar0 + 8 * b, (uint32_t)s.ng * 16);
-                bulk_g2s(smem_u32(buf + (size_t)b * L.G), s.src, (uint32_t)s.ng * 16, bar0 + 8 * b);
-            } else
-                mbar_arrive(bar0 + 8 * b);
-        }
-    };
-    long long row = first;
-    RowMeta m = {}, next = {};
-    RowLoad ahead = {};
-    if (row < a.T) {
-        m = row_meta<OP>(a, row_load<OP>(a, row, true));
-        start(row, m, 0);
-        if (row + step < a.T) ahead = row_load<OP>(a, row + step, true);
+    const uint64_t policy = policy_drop();
+    uint4 v[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int g = lane + 32 * i;
+        v[i] = g < s.ng ? load16(s.src + g, policy) : nothing<DT>();
     }
-    uint32_t ph = 0u;
-    int b = 0;
-    for (; row < a.T; row += step) {
-        if (row + step < a.T) {
-            next = row_meta<OP>(a, ahead);
-            start(row + step, next, b ^ 1);  // that buffer's row is done
-            if (row + 2 * step < a.T) ahead = row_load<OP>(a, row + 2 * step, true);
-        }
-        float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
-        if (OP == LM_DISTILL && m.keep) teacher_side(a, row, eq, eid, Q, B);
-        __syncwarp();
-        if (!row_wait(bar0 + 8 * b, ph, abort, L.wait_ns)) break;
-        copying[b] = false;
-        const Slice s = slice_of<DT>(a.x, row, a.ld, a.V, L.G, 0);
-        uint4* const src = buf + (size_t)b * L.G;
-        T* const se = reinterpret_cast<T*>(src);
-        const T* const xrow = static_cast<const T*>(a.x) + row * a.ld;
-        T* const grow = a.grad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
-        const bool aligned = same_granules<T>(xrow, grow);
-        if (m.keep) {
-            MS top{-INFINITY, 0.f};
-            if (OP == LM_DISTILL) {
-                student_side<DT>(a, s.e0, s.e0 + s.ng * N, se - s.e0, ex, eq, eid, sc, D, top);
-                if (a.tail) {  // the entries leave the row; its copy comes later than the removals
-                    for (int k = lane; k < a.K; k += 32)
-                        if (eid[k] >= 0) se[eid[k] - s.e0] = Elem<DT>::put(-INFINITY);
-                    fence_proxy_async_smem();
-                    __syncwarp();
+    float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
+    MS top{-INFINITY, 0.f};
+    if (OP == LM_DISTILL) {
+        teacher_side(a, row, eq, eid, Q, B);
+        if constexpr (TAIL) {
+            for (int i = lane; i < R * 8; i += 32) cut[i] = 0u;
+            __syncwarp();
+            for (int k = lane; k < a.K; k += 32)
+                if (eid[k] >= 0) {
+                    const int at = eid[k] - s.e0;
+                    atomicOr(cut + at / N / 4, 1u << (at / N % 4 * 8 + at % N));
                 }
-            } else
-                D.x = Elem<DT>::get(se[m.tgt - s.e0]);
-            Running run;
-            slice_stats<DT, false>(run, s, FromShared{src}, nullptr, a.V, sc, lane, 32);
-            const MS r = ms_warp(run.result(), sc);
-            const RowCoef c = row_finish<OP>(a, row, m, r, top, Q, B, D, sc, lane == 0, [](const RowCoef&) {});
-            if (grow) {
-                slice_grad<DT>(s, FromShared{src}, c, grow, a.V, sc, aligned, drop_policy, lane, 32);
-                __syncwarp();  // the corrections come after the columns they replace
-                if (OP == LM_DISTILL) {
-                    for (int k = lane; k < a.K; k += 32)
-                        if (eid[k] >= 0)
-                            grow[eid[k]] = Elem<DT>::put(c.fa * (weight_of(ex[k], c.M, sc) * c.inv_S) - c.fb * eq[k]);
-                } else if (lane == 0)
-                    grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(D.x, c.M, sc) * c.inv_S) - c.fb);
-            }
-        } else {
-            if (grow) slice_zero<DT>(s, grow, a.V, aligned, lane, 32);
-            if (lane == 0) row_outputs(a, row, 0.f);
         }
         __syncwarp();
-        m = next;
-        b ^= 1;
-        if (b == 0) ph ^= 1u;
-    }
-    if (row < a.T) {  // a wait ran out: no copy may be in flight when the CTA ends
-        int dummy = 0;
-        if (copying[b]) row_wait(bar0 + 8 * b, ph, &dummy, L.wait_ns);
-        if (copying[b ^ 1]) row_wait(bar0 + 8 * (b ^ 1), b ? ph ^ 1u : ph, &dummy, L.wait_ns);
-        if (lane == 0) {
-            atomicOr(L.status, SOT_DEV_TIMEOUT);
-            for (; row < a.T; row += step) row_outputs(a, row, NAN);
+        student_side<DT>(a, s.e0, s.e0 + s.ng * N, x, ex, eq, eid, sc, D, top);
+    } else
+        D.x = Elem<DT>::get(x[m.tgt]);
+    Running run;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int g = lane + 32 * i;
+        if (g < s.ng && (g < s.lo || g >= s.hi)) {
+            float2 f[N / 2];
+            unpack<DT>(v[i], f);
+            mask_cols<DT>(f, s.e0 + g * N, a.V, -INFINITY);
+            v[i] = pack<DT>(f);
+        }
+        if (TAIL && g < s.ng) {
+            const unsigned out = reinterpret_cast<const unsigned char*>(cut)[g];
+            if (out) v[i] = without<DT>(v[i], out);
         }
     }
+#pragma unroll
+    for (int i = 0; i < R; i += U)
+        if (32 * i < s.ng) {
+            const uint4 w[U] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+            run.template add<DT>(w, sc);
+        }
+    const MS r = ms_warp(run.result(), sc);
+    const RowCoef c = row_finish<OP>(a, row, m, r, top, Q, B, D, sc, lane == 0, [](const RowCoef&) {});
+    if (!grow) return;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int g = lane + 32 * i;
+        if (g < s.ng) {
+            float2 f[N / 2];
+            unpack<DT>(v[i], f);
+            grad_of<DT>(f, c, sc);
+            if (aligned && g >= s.lo && g < s.hi) store16(reinterpret_cast<uint4*>(grow + s.e0) + g, pack<DT>(f), policy);
+            else store_cols<DT>(grow, s.e0 + g * N, a.V, f, false);
+        }
+    }
+    __syncwarp();  // the corrections come after the columns they replace
+    if (OP == LM_DISTILL) {
+        for (int k = lane; k < a.K; k += 32)
+            if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * (weight_of(ex[k], c.M, sc) * c.inv_S) - c.fb * eq[k]);
+    } else if (lane == 0)
+        grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(D.x, c.M, sc) * c.inv_S) - c.fb);
 }
 
 struct LmRowPlan {
-    int NW;     // streaming warps of a CTA (1: the short-row kernel)
+    int NW;     // streaming warps of a CTA (0: the short-row kernel)
     int CL, G;  // CTAs a row, granules a slice
     size_t smem;
-    int sms;
 };
 
 template <int DT, int OP, int NW, bool TAIL>
-cudaError_t launch_row_n(const LmRowArgs& a, const LmRowPlan& p, LmRowLaunch L, cudaStream_t st) {
+cudaError_t launch_row_n(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaunch& L, cudaStream_t st) {
     auto kern = lm_row_kernel<DT, OP, NW, TAIL>;
     if (p.smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
         if (e != cudaSuccess) return e;
     }
-    L.CL = p.CL;
-    L.G = p.G;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.CL, 1, 1);
     cfg.blockDim = dim3((NW + 1) * 32, 1, 1);
@@ -744,26 +709,20 @@ cudaError_t launch_row_k(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaun
     return launch_row_n<DT, OP, NW, false>(a, p, L, st);
 }
 
-template <int DT, int OP>
-cudaError_t launch_row_w(const LmRowArgs& a, const LmRowPlan& p, LmRowLaunch L, cudaStream_t st) {
-    auto kern = lm_warp_kernel<DT, OP>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
-    if (e != cudaSuccess) return e;
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, WARP_ROWS * 32, p.smem);
-    if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
-    const long long want = (a.T + WARP_ROWS - 1) / WARP_ROWS, most = (long long)per_sm * p.sms;
-    L.CL = 1;
-    L.G = p.G;
-    kern<<<(unsigned)(want < most ? want : most), WARP_ROWS * 32, p.smem, st>>>(a, L);
+template <int DT, int OP, int R>
+cudaError_t launch_row_r(const LmRowArgs& a, const LmRowPlan& p, cudaStream_t st) {
+    const unsigned blocks = (unsigned)((a.T + SHORT_NW - 1) / SHORT_NW);
+    if (OP == LM_DISTILL && a.tail) lm_short_kernel<DT, OP, R, OP == LM_DISTILL><<<blocks, SHORT_NW * 32, p.smem, st>>>(a);
+    else lm_short_kernel<DT, OP, R, false><<<blocks, SHORT_NW * 32, p.smem, st>>>(a);
     return cudaGetLastError();
 }
 
 template <int DT, int OP>
 cudaError_t launch_row_o(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaunch& L, cudaStream_t st) {
     switch (p.NW) {
-        case 1: return launch_row_w<DT, OP>(a, p, L, st);
+        case 0: return p.G <= 128 ? launch_row_r<DT, OP, 4>(a, p, st)
+                       : p.G <= 256 ? launch_row_r<DT, OP, 8>(a, p, st)
+                                    : launch_row_r<DT, OP, 16>(a, p, st);
         case 4: return launch_row_k<DT, OP, 4>(a, p, L, st);
         case 8: return launch_row_k<DT, OP, 8>(a, p, L, st);
         default: return launch_row_k<DT, OP, 16>(a, p, L, st);

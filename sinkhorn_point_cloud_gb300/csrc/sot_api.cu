@@ -1654,7 +1654,7 @@ int sot_token_logprob_grad(const void* logits, long long T, int V, long long ld,
     a.lse = lse;
     a.g = grad_logp;
     a.grad = grad;
-    SOT_CUDA(launch_lm_grad(a, (cudaStream_t)stream));
+    SOT_CUDA(launch_lm_grad(a, device_sms(), (cudaStream_t)stream));
     return SOT_OK;
 }
 

@@ -39,8 +39,6 @@ struct TcScreen {
 // chunk on (tile < 0: off), and every bounded wait gives up after wait_ns
 // (0: 2 s).
 void tc_set_test_hold(int tile, int after, unsigned long long wait_ns);
-// The hook's tile (-1: off) and the limit of waits for one launch of a kernel.
-void tc_test_hold(int* tile, unsigned long long* wait_ns);
 // The screened half-step takes d = 64, 128, 192, 256; the full half-step and
 // the plan application d = 64 only.
 bool tc_supported(int d);
