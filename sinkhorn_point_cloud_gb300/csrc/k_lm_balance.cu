@@ -14,9 +14,8 @@
 // kernel is launched along with it (programmatic dependent launch), reads its
 // first rows meanwhile, adds the counts up and goes on; its last CTA to finish joins
 // the sums.
-// A power of two of lanes takes a row, two granules of 16 bytes a lane (four
-// elements a lane where the rows are not aligned to granules; more of both for
-// many experts), as many rows at a time as fit a warp.
+// A power of two of lanes takes a row, four granules of 16 bytes a lane (fewer
+// for few experts, more for many), as many rows at a time as fit a warp.
 #include <cuda_runtime.h>
 
 #include "kernels.h"
@@ -67,17 +66,29 @@ __device__ __forceinline__ float group_max(float v, int lanes) {
     return v;
 }
 
-// The rows of one warp of `warps`: `lanes` lanes a row, 32 / lanes rows at a time,
-// the next rows' loads under way while these are worked on.  VEC: R granules a
-// lane.  Otherwise 2 R elements a lane, `lanes` apart.  f holds coef f_e, then
-// zeros; `counted` is called once the first loads are under way, and gives 1/N.
-template <int DT, int R, bool VEC, class Counted>
+// f in shared memory: coef f_e, zeros around it; where rows may start inside a
+// granule, a copy for each number of elements before them, so that a granule's
+// experts are always whole aligned float4s.
+constexpr int F_LEN = LM_MAX_E + 16;
+template <int DT, bool SHIFT>
+constexpr int f_copies = SHIFT ? Elem<DT>::N : 1;
+template <int DT, bool SHIFT>
+__device__ __forceinline__ void put_share(float* f, int e, float v) {
+#pragma unroll
+    for (int h = 0; h < f_copies<DT, SHIFT>; ++h) f[h * F_LEN + e + h] = v;
+}
+
+// The rows of one warp of `warps`: `lanes` lanes a row, R granules a lane, 32 / lanes
+// rows at a time, the next rows' loads under way while these are worked on.
+// SHIFT: rows may start and end inside a granule.  `counted` is called once the
+// first loads are under way, and gives 1/N.
+template <int DT, int R, bool SHIFT, class Counted>
 __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long warp, long long warps, const float* f,
                                              Sums& out, Counted counted) {
     using T = typename Elem<DT>::T;
-    constexpr int N = VEC ? Elem<DT>::N : 2, H = R * N / 2;  // H pairs a lane
+    constexpr int N = Elem<DT>::N, H = R * N / 2;  // H pairs a lane
     const int lane = threadIdx.x & 31;
-    const int units = VEC ? a.E / N : (a.E + 1) / 2;
+    const int units = (a.E + (SHIFT ? 2 * N - 2 : 0)) / N;
     int lanes = 32;
     while (lanes > 1 && lanes / 2 * R >= units) lanes >>= 1;
     const int per = 32 / lanes, sub = lane & (lanes - 1);
@@ -85,47 +96,46 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
     out = Sums{make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     long long t = warp * per + lane / lanes;
     const auto kept = [&](long long r) { return r < a.T && (!a.mask || a.mask[r]); };
-    uint4 v[VEC ? R : 1];
-    float2 w[VEC ? 1 : R];
+    const auto head_of = [&](const T* row) { return SHIFT ? (int)((uint32_t)(unsigned long long)row & 15u) / (int)sizeof(T) : 0; };
+    const auto granules = [&](int head) { return SHIFT ? (head + a.E + N - 1) / N : units; };
+    uint4 v[R];
     const auto load = [&](long long r, bool keep) {
         const T* const row = static_cast<const T*>(a.x) + r * a.ld;
+        const int head = head_of(row), ng = granules(head);
+        const uint4* const src = reinterpret_cast<const uint4*>(row - head);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            if constexpr (VEC) {
-                const int g = sub + i * lanes;
-                v[i] = keep && g < units ? reinterpret_cast<const uint4*>(row)[g] : nothing<DT>();
-            } else {
-                const int e = sub + 2 * i * lanes;
-                w[i].x = keep && e < a.E ? Elem<DT>::get(row[e]) : -INFINITY;
-                w[i].y = keep && e + lanes < a.E ? Elem<DT>::get(row[e + lanes]) : -INFINITY;
-            }
+            const int g = sub + i * lanes;
+            v[i] = keep && g < ng ? src[g] : nothing<DT>();
         }
     };
     bool keep = kept(t), next = kept(t + step);
     load(t, keep);
     const float inv_n = counted();
     for (long long base = warp * per; base < a.T; base += step, t += step) {
+        const T* const row = static_cast<const T*>(a.x) + t * a.ld;
+        const int head = head_of(row), ng = granules(head);
         float2 x[H];
         float m;
-        if constexpr (VEC) {
+        if constexpr (!SHIFT) {
             uint4 top = v[0];
 #pragma unroll
             for (int i = 1; i < R; ++i) top = max2<DT>(top, v[i]);
             m = max_of<DT>(top);
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                float2 p[N / 2];
-                unpack<DT>(v[i], p);
-#pragma unroll
-                for (int k = 0; k < N / 2; ++k) x[i * (N / 2) + k] = p[k];
-            }
-        } else {
+        } else
             m = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                x[i] = w[i];
-                m = fmaxf(m, fmaxf(x[i].x, x[i].y));
+        for (int i = 0; i < R; ++i) {
+            float2 p[N / 2];
+            unpack<DT>(v[i], p);
+            if (SHIFT) {
+                const int g = sub + i * lanes;
+                if (g == 0 || g == ng - 1) mask_cols<DT>(p, g * N - head, a.E, -INFINITY);
+#pragma unroll
+                for (int k = 0; k < N / 2; ++k) m = fmaxf(m, fmaxf(p[k].x, p[k].y));
             }
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) x[i * (N / 2) + k] = p[k];
         }
         const bool now = keep;
         keep = next;
@@ -143,29 +153,26 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
 #pragma unroll
             for (int i = 0; i < H; ++i) x[i] = make_float2(weight_of(x[i].x, m, SOT_LOG2E), weight_of(x[i].y, m, SOT_LOG2E));
         }
-        // coef f of the lane's experts, in the order of x
-        const auto shares = [&](int i, float2 (&c)[VEC ? N / 2 : 1]) {
-            if constexpr (VEC) {
-                const float4* const q = reinterpret_cast<const float4*>(f + (sub + i * lanes) * N);
+        // coef f of the experts of granule i, in the order of x
+        const auto shares = [&](int i, float2 (&c)[N / 2]) {
+            const int g = sub + i * lanes;
+            const float4* const q = reinterpret_cast<const float4*>(f + head * F_LEN + g * N);
 #pragma unroll
-                for (int k = 0; k < N / 4; ++k) {
-                    const float4 r = q[k];
-                    c[2 * k] = make_float2(r.x, r.y);
-                    c[2 * k + 1] = make_float2(r.z, r.w);
-                }
-            } else
-                c[0] = make_float2(f[sub + 2 * i * lanes], f[sub + (2 * i + 1) * lanes]);
+            for (int k = 0; k < N / 4; ++k) {
+                const float4 r = g < ng ? q[k] : make_float4(0.f, 0.f, 0.f, 0.f);
+                c[2 * k] = make_float2(r.x, r.y);
+                c[2 * k + 1] = make_float2(r.z, r.w);
+            }
         };
-        constexpr int C = VEC ? N / 2 : 1;
         float2 sum = make_float2(0.f, 0.f), dots = sum;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            float2 c[C];
+            float2 c[N / 2];
             shares(i, c);
 #pragma unroll
-            for (int k = 0; k < C; ++k) {
-                sum = fadd2(sum, x[i * C + k]);
-                dots = ffma2(x[i * C + k], c[k], dots);
+            for (int k = 0; k < N / 2; ++k) {
+                sum = fadd2(sum, x[i * (N / 2) + k]);
+                dots = ffma2(x[i * (N / 2) + k], c[k], dots);
             }
         }
         float s = sum.x + sum.y, d = dots.x + dots.y;
@@ -180,28 +187,21 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
             Sums::add(out.z, lse * lse);
         }
         if (!a.grad || t >= a.T) continue;
-        T* const g = static_cast<T*>(a.grad) + t * a.ldg;
+        T* const grow = static_cast<T*>(a.grad) + t * a.ldg;
+        const bool aligned = !SHIFT || same_granules<T>(row, grow);
         // (the weights of a token that is left out are 0)
         const float bias = now ? 2.f * a.z_coef * lse - dot : 0.f, k = now ? inv_n * inv_s : 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            float2 c[C];
+            const int g = sub + i * lanes;
+            float2 c[N / 2], p[N / 2];
             shares(i, c);
 #pragma unroll
-            for (int j = 0; j < C; ++j)
-                x[i * C + j] = fmul2(x[i * C + j], fmul2(fadd2(c[j], make_float2(bias, bias)), make_float2(k, k)));
-        }
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            if constexpr (VEC) {
-                float2 p[N / 2];
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j) p[j] = x[i * (N / 2) + j];
-                if (sub + i * lanes < units) reinterpret_cast<uint4*>(g)[sub + i * lanes] = pack<DT>(p);
-            } else {
-                const int e = sub + 2 * i * lanes;
-                if (e < a.E) g[e] = Elem<DT>::put(x[i].x);
-                if (e + lanes < a.E) g[e + lanes] = Elem<DT>::put(x[i].y);
+            for (int j = 0; j < N / 2; ++j)
+                p[j] = fmul2(x[i * (N / 2) + j], fmul2(fadd2(c[j], make_float2(bias, bias)), make_float2(k, k)));
+            if (g < ng) {
+                if (SHIFT) store_cols<DT>(grow, g * N - head, a.E, p, aligned);
+                else reinterpret_cast<uint4*>(grow)[g] = pack<DT>(p);
             }
         }
     }
@@ -258,14 +258,16 @@ __global__ void __launch_bounds__(CNT_NT) lm_count_kernel(LmBalanceArgs a) {
     cluster_sync();  // no CTA leaves while a peer may still read it
 }
 
-template <int DT, int R, bool VEC>
-__global__ void __launch_bounds__(BAL_NT, R <= 2 ? 4 : 2) lm_balance_kernel(LmBalanceArgs a) {
-    __shared__ __align__(16) float f[LM_MAX_E];
+template <int DT, int R, bool SHIFT>
+__global__ void __launch_bounds__(BAL_NT, R <= 2 ? 4 : R <= 4 ? 2 : 1) lm_balance_kernel(LmBalanceArgs a) {
+    __shared__ __align__(16) float f[f_copies<DT, SHIFT> * F_LEN];
     __shared__ float red[2][BAL_NT / 32];
     __shared__ bool last;
     int kept = 0;
     Sums s;
-    balance_rows<DT, R, VEC>(a, (long long)blockIdx.x * (BAL_NT / 32) + (threadIdx.x >> 5),
+    for (int i = threadIdx.x; i < f_copies<DT, SHIFT> * F_LEN; i += BAL_NT) f[i] = 0.f;
+    __syncthreads();
+    balance_rows<DT, R, SHIFT>(a, (long long)blockIdx.x * (BAL_NT / 32) + (threadIdx.x >> 5),
                              (long long)gridDim.x * (BAL_NT / 32), f, s, [&]() {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         const auto total = [&](int e) {  // all loads under way at once
@@ -278,10 +280,10 @@ __global__ void __launch_bounds__(BAL_NT, R <= 2 ? 4 : 2) lm_balance_kernel(LmBa
         };
         kept = total(a.E);
         const float k = a.coef * share_of(a, kept);
-        for (int e = threadIdx.x; e < LM_MAX_E; e += BAL_NT) {
-            const int c = e < a.E ? total(e) : 0;
-            if (e < a.E && blockIdx.x == 0) a.counts[e] = c;
-            f[e] = (float)c * k;
+        for (int e = threadIdx.x; e < a.E; e += BAL_NT) {
+            const int c = total(e);
+            if (blockIdx.x == 0) a.counts[e] = c;
+            put_share<DT, SHIFT>(f, e, (float)c * k);
         }
         __syncthreads();
         return kept > 0 ? 1.f / (float)kept : 0.f;
@@ -307,32 +309,31 @@ __global__ void __launch_bounds__(BAL_NT, R <= 2 ? 4 : 2) lm_balance_kernel(LmBa
 }
 
 // ---- small batches --------------------------------------------------------------
-template <int DT, int R, bool VEC>
+template <int DT, int R, bool SHIFT>
 __global__ void __launch_bounds__(CNT_NT) lm_balance_small_kernel(LmBalanceArgs a) {
     __shared__ int hist[LM_MAX_E + 1];  // the last: kept tokens
-    __shared__ __align__(16) float f[LM_MAX_E];
+    __shared__ __align__(16) float f[f_copies<DT, SHIFT> * F_LEN];
     __shared__ float red[2][CNT_NT / 32];
     __shared__ float sums[SMALL_CL][2];
     const uint32_t rank = cluster_rank();
     const int CL = gridDim.x;
     for (int e = threadIdx.x; e <= a.E; e += CNT_NT) hist[e] = 0;
+    for (int i = threadIdx.x; i < f_copies<DT, SHIFT> * F_LEN; i += CNT_NT) f[i] = 0.f;
     __syncthreads();
     const int n = count_tokens(a, (long long)rank * CNT_NT + threadIdx.x, (long long)CL * CNT_NT, hist);
     if (n) atomicAdd(&hist[a.E], n);
     int kept = 0;
     Sums s;
-    balance_rows<DT, R, VEC>(a, (long long)rank * (CNT_NT / 32) + (threadIdx.x >> 5), (long long)CL * (CNT_NT / 32), f, s, [&]() {
+    balance_rows<DT, R, SHIFT>(a, (long long)rank * (CNT_NT / 32) + (threadIdx.x >> 5), (long long)CL * (CNT_NT / 32), f, s, [&]() {
         if (CL > 1) cluster_sync();
         else __syncthreads();
         for (int p = 0; p < CL; ++p) kept += cluster_load(&hist[a.E], p);
         const float k = a.coef * share_of(a, kept);
-        for (int e = threadIdx.x; e < LM_MAX_E; e += CNT_NT) {
+        for (int e = threadIdx.x; e < a.E; e += CNT_NT) {
             int c = 0;
-            if (e < a.E) {
-                for (int p = 0; p < CL; ++p) c += cluster_load(&hist[e], p);
-                if (rank == 0) a.counts[e] = c;
-            }
-            f[e] = (float)c * k;
+            for (int p = 0; p < CL; ++p) c += cluster_load(&hist[e], p);
+            if (rank == 0) a.counts[e] = c;
+            put_share<DT, SHIFT>(f, e, (float)c * k);
         }
         __syncthreads();
         return kept > 0 ? 1.f / (float)kept : 0.f;
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(CNT_NT) lm_balance_small_kernel(LmBalanceArgs 
     }
 }
 
-template <int DT, int R, bool VEC>
+template <int DT, int R, bool SHIFT>
 cudaError_t launch_r(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -370,7 +371,7 @@ cudaError_t launch_r(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         count_launches(1);
-        return cudaLaunchKernelEx(&cfg, lm_balance_small_kernel<DT, R, VEC>, a);
+        return cudaLaunchKernelEx(&cfg, lm_balance_small_kernel<DT, R, SHIFT>, a);
     }
     count_launches(2);
     cfg.gridDim = dim3(a.parts * CNT_CL, 1, 1);
@@ -385,7 +386,17 @@ cudaError_t launch_r(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
     cfg.blockDim = dim3(BAL_NT, 1, 1);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    return cudaLaunchKernelEx(&cfg, lm_balance_kernel<DT, R, VEC>, a);
+    return cudaLaunchKernelEx(&cfg, lm_balance_kernel<DT, R, SHIFT>, a);
+}
+
+template <int DT, bool SHIFT>
+cudaError_t launch_s(const LmBalanceArgs& a, int granules, int blocks, cudaStream_t st) {
+    if (granules <= 4) return launch_r<DT, 1, SHIFT>(a, blocks, st);
+    if (granules <= 8) return launch_r<DT, 2, SHIFT>(a, blocks, st);
+    if (granules <= 128) return launch_r<DT, 4, SHIFT>(a, blocks, st);
+    if constexpr (DT == SOT_F32 && SHIFT)
+        if (granules > 256) return launch_r<DT, 16, SHIFT>(a, blocks, st);
+    return launch_r<DT, 8, SHIFT>(a, blocks, st);
 }
 
 template <int DT>
@@ -395,16 +406,8 @@ cudaError_t launch_d(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
     const auto whole = [](const void* p, long long ld) {
         return (unsigned long long)p % 16 == 0 && ld * (long long)sizeof(T) % 16 == 0;
     };
-    if (a.E % N == 0 && whole(a.x, a.ld) && (!a.grad || whole(a.grad, a.ldg))) {
-        const int g = a.E / N;
-        if (g <= 4) return launch_r<DT, 1, true>(a, blocks, st);
-        if (g <= 8) return launch_r<DT, 2, true>(a, blocks, st);
-        if (g <= 128) return launch_r<DT, 4, true>(a, blocks, st);
-        if constexpr (N == 4) return launch_r<DT, 8, true>(a, blocks, st);
-    }
-    if (a.E <= 128) return launch_r<DT, 2, false>(a, blocks, st);
-    if (a.E <= 256) return launch_r<DT, 4, false>(a, blocks, st);
-    return launch_r<DT, 16, false>(a, blocks, st);
+    if (a.E % N == 0 && whole(a.x, a.ld) && (!a.grad || whole(a.grad, a.ldg))) return launch_s<DT, false>(a, a.E / N, blocks, st);
+    return launch_s<DT, true>(a, (a.E + 2 * N - 2) / N, blocks, st);
 }
 
 }  // namespace
@@ -413,9 +416,9 @@ cudaError_t launch_d(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
 LmBalancePlan lm_balance_plan(long long T, int E, int K, int dtype, int sms) {
     LmBalancePlan p = {};
     const long long bytes = T * ((long long)E * (dtype == SOT_F32 ? 4 : 2) + 4ll * K);
-    // One cluster up to 256 KB of logits and choices: one launch instead of two and a
+    // One cluster up to 512 KB of logits and choices: one launch instead of two and a
     // scratch allocation outweigh the SMs that stay idle.
-    if (bytes <= 256 * 1024) {
+    if (bytes <= 512 * 1024) {
         const long long want = (T + CNT_NT / 32 - 1) / (CNT_NT / 32);
         p.blocks = 1;
         while (p.blocks < SMALL_CL && p.blocks < want) p.blocks *= 2;

@@ -166,6 +166,37 @@ __device__ __forceinline__ int load_index(const void* p, int type, long long i, 
     return v >= 0 && v < n ? (int)v : -1;
 }
 
+// Writes N elements at columns e .. e + N - 1 of a row.
+template <int DT>
+__device__ __forceinline__ void store_cols(typename Elem<DT>::T* row, int e, int V,
+                                           const float2 (&f)[Elem<DT>::N / 2], bool aligned) {
+    constexpr int N = Elem<DT>::N;
+    if (aligned && e >= 0 && e + N <= V) {
+        *reinterpret_cast<uint4*>(row + e) = pack<DT>(f);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        if (e + 2 * i >= 0 && e + 2 * i < V) row[e + 2 * i] = Elem<DT>::put(f[i].x);
+        if (e + 2 * i + 1 >= 0 && e + 2 * i + 1 < V) row[e + 2 * i + 1] = Elem<DT>::put(f[i].y);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void mask_cols(float2 (&f)[Elem<DT>::N / 2], int e, int V, float fill) {
+#pragma unroll
+    for (int i = 0; i < Elem<DT>::N / 2; ++i) {
+        if (e + 2 * i < 0 || e + 2 * i >= V) f[i].x = fill;
+        if (e + 2 * i + 1 < 0 || e + 2 * i + 1 >= V) f[i].y = fill;
+    }
+}
+
+// Whether two rows start at the same place of a granule.
+template <class T>
+__device__ __forceinline__ bool same_granules(const T* x, const T* g) {
+    return ((uint32_t)((unsigned long long)x ^ (unsigned long long)g) & 15u) == 0;
+}
+
 // Softmax statistics of a set of logits with sc = log2(e) / temperature: its
 // stabiliser m (its largest value, or one near enough for the sums' range) and
 // s = sum exp2(x sc - m2), m2 = m sc rounded to 32 bits.

@@ -76,34 +76,10 @@ __device__ __forceinline__ Slice slice_of(const void* x, long long row, long lon
     return slice_at<DT>(static_cast<const typename Elem<DT>::T*>(x) + row * ld, V, G, rank);
 }
 
-// Writes N elements at columns e .. e + N - 1 of a row.
-template <int DT>
-__device__ __forceinline__ void store_cols(typename Elem<DT>::T* row, int e, int V,
-                                           const float2 (&f)[Elem<DT>::N / 2], bool aligned) {
-    constexpr int N = Elem<DT>::N;
-    if (aligned && e >= 0 && e + N <= V) {
-        *reinterpret_cast<uint4*>(row + e) = pack<DT>(f);
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        if (e + 2 * i >= 0 && e + 2 * i < V) row[e + 2 * i] = Elem<DT>::put(f[i].x);
-        if (e + 2 * i + 1 >= 0 && e + 2 * i + 1 < V) row[e + 2 * i + 1] = Elem<DT>::put(f[i].y);
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ void mask_cols(float2 (&f)[Elem<DT>::N / 2], int e, int V, float fill) {
-#pragma unroll
-    for (int i = 0; i < Elem<DT>::N / 2; ++i) {
-        if (e + 2 * i < 0 || e + 2 * i >= V) f[i].x = fill;
-        if (e + 2 * i + 1 < 0 || e + 2 * i + 1 >= V) f[i].y = fill;
-    }
-}
-
-// The teacher's entries of a row (one warp): weights q in eq, columns in eid
-// (-1: unused), and the sums Q = sum q and B = sum q log q.
-__device__ __forceinline__ void teacher_side(const LmRowArgs& a, long long row, float* eq, int* eid, float2& Q, float2& B) {
+// The teacher's entries of a row (one warp), in two steps.  First the entries as
+// they are: values in eq (-inf: unused), columns in eid (-1: unused); returns the
+// largest value.
+__device__ __forceinline__ float teacher_entries(const LmRowArgs& a, long long row, float* eq, int* eid) {
     const int lane = threadIdx.x & 31;
     float zmax = -INFINITY;
     for (int k0 = 0; k0 < a.K; k0 += 128) {  // four loads in flight a lane
@@ -126,7 +102,11 @@ __device__ __forceinline__ void teacher_side(const LmRowArgs& a, long long row, 
             }
         }
     }
-    zmax = warp_max1(zmax);
+    return warp_max1(zmax);
+}
+// Then the weights q in eq, and the sums Q = sum q and B = sum q log q.
+__device__ __forceinline__ void teacher_weights(const LmRowArgs& a, float zmax, float* eq, float2& Q, float2& B) {
+    const int lane = threadIdx.x & 31;
     const float z0 = a.tail || zmax == -INFINITY ? 0.f : zmax, inv_tau = (float)a.inv_tau;
     Q = B = make_float2(0.f, 0.f);
     for (int k = lane; k < a.K; k += 32) {
@@ -460,11 +440,6 @@ __device__ __forceinline__ void slice_zero(const Slice& s, typename Elem<DT>::T*
     for (int k = 0; k < N / 2; ++k) z[k] = make_float2(0.f, 0.f);
     for (int g = tid; g < s.ng; g += NT) store_cols<DT>(grow, s.e0 + g * N, V, z, aligned);
 }
-template <class T>
-__device__ __forceinline__ bool same_granules(const T* x, const T* g) {
-    return ((uint32_t)((unsigned long long)x ^ (unsigned long long)g) & 15u) == 0;
-}
-
 // NW streaming warps and the row's own warp.
 template <int DT, int OP, int NW, bool TAIL>
 __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8 : 7) : NW == 8 ? 4 : 2)
@@ -504,14 +479,15 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
     MS top{-INFINITY, 0.f};
     if (warp == NW) {
         if (OP == LM_DISTILL) {
-            teacher_side(a, row, eq, eid, Q, B);
+            const float zmax = teacher_entries(a, row, eq, eid);
             if (TAIL) {
                 for (int k = lane; k < a.K; k += 32) {
                     const int at = eid[k] - c0;
                     if (eid[k] >= 0 && at >= 0 && eid[k] < c1) atomicOr(cut + at / N / 4, 1u << (at / N % 4 * 8 + at % N));
                 }
-                __syncthreads();
+                __syncthreads();  // the others can start
             }
+            teacher_weights(a, zmax, eq, Q, B);
             student_side<DT>(a, c0, c1, x, ex, eq, eid, sc, D, top);
         } else if (m.tgt >= c0 && m.tgt < c1)
             D.x = Elem<DT>::get(x[m.tgt]);
@@ -616,7 +592,7 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
     float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
     MS top{-INFINITY, 0.f};
     if (OP == LM_DISTILL) {
-        teacher_side(a, row, eq, eid, Q, B);
+        teacher_weights(a, teacher_entries(a, row, eq, eid), eq, Q, B);
         if constexpr (TAIL) {
             for (int i = lane; i < R * 8; i += 32) cut[i] = 0u;
             __syncwarp();
