@@ -169,10 +169,11 @@ void row_plan(bool grads, bool whole, long long T, int dtype, int V, int K, bool
     if (total <= 512 && K <= SHORT_MAX_K) {
         plan(0, 1);
     } else if (T < sms) {
-        // Few rows: cut a row further, down to 512 granules a CTA, while the SMs have
-        // room, and give it enough warps for eight granules a thread.
+        // Few rows: cut a row further, down to 512 granules a CTA, up to two CTAs an SM,
+        // and give it enough warps for eight granules a thread.
         int CL = 1;
-        while (CL < ROW_MAX_CL && T * CL * 2 <= sms && total / (2 * CL) >= 512) CL *= 2;
+        while (CL < ROW_MAX_CL && T * CL <= sms && total / (2 * CL) >= 512) CL *= 2;
+        while (CL < ROW_MAX_CL && tail && total > CL * 65536ll) CL *= 2;  // the tail's marks, a byte a granule
         plan(warps((total + CL - 1) / CL, 8), CL);
     } else if (!grads) {
         // Read once: small CTAs, many on an SM (2048 rows of 131072 bf16: 80 us, with

@@ -246,7 +246,7 @@ __device__ __forceinline__ float2 ex2_pair(float2 x, float u, float sc) {
 // m).  Nothing needs m to be the largest value, only the sums to stay clear of
 // overflow and underflow, and logits seldom leave the range where the first
 // guess, 0, does that.  So a batch is summed against the m at hand, with no
-// maximum to wait for, and only a batch whose sum comes out beyond 2^60 or
+// maximum to wait for, and only a batch whose sum comes out beyond 2^24 or
 // below 2^-40 is looked at again.
 struct Running {
     float m, u;
@@ -295,7 +295,7 @@ struct Running {
             }
         }
         const float both = t.x + t.y;
-        if (!(both > 9.094947e-13f && both < 1.1529215e18f)) {
+        if (!(both > 0x1p-40f && both < 0x1p24f)) {
             uint4 top = v[0];
 #pragma unroll
             for (int j = 1; j < P; ++j) top = max2<DT>(top, v[j]);

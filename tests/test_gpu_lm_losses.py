@@ -352,6 +352,71 @@ def test_row_offsets_beyond_32_bits(sot):
     close_grad(x, *R.token_grad(host(y), tg.cpu().numpy(), 1.0, np.ones(T)), "bf16")
 
 
+def wide_reference(x, tg, tau, d):
+    """Log-probabilities and their gradient in 64 bits for whole batches, on the GPU."""
+    y = x.double() / tau
+    lse = torch.logsumexp(y, 1)
+    p = torch.exp(y - lse[:, None])
+    logp = y.gather(1, tg[:, None])[:, 0] - lse
+    grad, size = -p, p.clone()
+    one = torch.ones_like(lse)[:, None]
+    grad.scatter_add_(1, tg[:, None], one)
+    size.scatter_add_(1, tg[:, None], one)
+    return host(logp), host(lse), host(grad * (d / tau)[:, None]), host(size * (d.abs() / tau)[:, None])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(400, 1003), (400, 2040), (300, 4096), (200, 6001), (160, 17000), (170, 50021), (160, 107003),
+                                 (100, 140001), (30, 300001), (60, 9000), (153, 30000)])
+def test_every_way_of_cutting_rows(sot, T, V, dtype):
+    """Batches on both sides of each choice: a warp, a CTA or a cluster a row, few rows and many."""
+    x, tg = rows(T, V, dtype, 0, seed=V), targets(T, V)
+    d = torch.randn(T, generator=torch.Generator().manual_seed(5)).double().cuda()
+    rp, rl, rg, size = wide_reference(x, tg, 0.9, d)
+    logp, lse = sot.sot_token_logprob(x, tg, temperature=0.9)
+    close(logp, rp, size=np.abs(host(x)).max() / 0.9)
+    close(lse, rl, size=np.abs(host(x)).max() / 0.9)
+    # at old = logp the policy's gradient is -A w times the log-probability's
+    loss, lp, _, grad = sot.sot_policy_loss(x, tg, logp, -torch.ones(T).cuda(), weight=d.float(), temperature=0.9)
+    close(lp, rp, size=np.abs(host(x)).max() / 0.9)
+    close_grad(grad, rg, size, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,V", [(3, 5003), (200, 5003), (200, 1500), (4, 40000)])
+def test_sharp_and_offset_logits(sot, T, V, dtype):
+    """Rows far from zero and rows whose logits span hundreds: the sums' first stabiliser does
+    not serve them."""
+    x, tg = rows(T, V, dtype, 0, seed=3, spread=1.0), targets(T, V)
+    scale = torch.tensor([1.0, 60.0, 10.0, 1.0])[torch.arange(T) % 4].cuda()[:, None]
+    shift = torch.tensor([300.0, 0.0, -200.0, -900.0])[torch.arange(T) % 4].cuda()[:, None]
+    x.copy_((x.float() * scale + shift).to(x.dtype))
+    d = torch.ones(T).double().cuda()
+    rp, rl, rg, size = wide_reference(x, tg, 1.0, d)
+    logp, lse = sot.sot_token_logprob(x, tg)
+    close(lse, rl, size=np.abs(rl) + np.abs(rp))
+    close(logp, rp, size=np.abs(rl) + np.abs(rp))
+    grad = sot.sot_policy_loss(x, tg, logp, -torch.ones(T).cuda(), weight=torch.ones(T).cuda())[3]
+    # a log-probability of size |rl| + |rp| moves by its rounding
+    wide = 1.0 + 2.0 ** -8 * (np.abs(rl) + np.abs(rp))[:, None]
+    close_grad(grad, rg, size * wide, dtype)
+
+
+@pytest.mark.parametrize("T,V,K", [(5, 2000, 300), (200, 2000, 300), (200, 3000, 40), (160, 120001, 64), (2, 200000, 8)])
+def test_tail_of_many_shapes(sot, T, V, K):
+    x = rows(T, V, "f32", 0, 6)
+    rng = np.random.default_rng(K)
+    ids = np.stack([np.sort(rng.permutation(V)[:K]) for _ in range(T)])
+    ids[:, 0] = 0
+    ids[:, -1] = V - 1
+    z = torch.log_softmax(torch.randn(T, K, generator=torch.Generator().manual_seed(1)), 1) - 0.2
+    zt, w = z.cuda(), torch.ones(T).cuda()
+    loss, grad = sot.sot_distill_topk(x, torch.from_numpy(ids).cuda(), zt, weight=w, tail=True)
+    rl, rg, size = R.distill(host(x), ids, host(zt), host(w), 1.0, True)
+    close(loss, rl, scale=4.0, size=64.0)
+    close_grad(grad, rg, size, "f32")
+
+
 def test_empty_batches(sot):
     x = torch.zeros(0, 10, device="cuda")
     tg = torch.zeros(0, dtype=torch.int64, device="cuda")
