@@ -14,6 +14,9 @@
 // kernel is launched along with it (programmatic dependent launch), reads its
 // first rows meanwhile, adds the counts up and goes on; its last CTA to finish joins
 // the sums.
+//   Measured: 65536 x 256 bf16, 8 choices, a tenth left out: 22.8 us, of which the
+// counting 7 us (0.42 of the copy bandwidth for 66 MB: each warp walks four to
+// seven dependent steps of load, maximum, sums and store); 256 x 64 fp32: 6 us.
 // A power of two of lanes takes a row, four granules of 16 bytes a lane (fewer
 // for few experts, more for many), as many rows at a time as fit a warp.
 #include <cuda_runtime.h>
@@ -416,8 +419,9 @@ cudaError_t launch_d(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
 LmBalancePlan lm_balance_plan(long long T, int E, int K, int dtype, int sms) {
     LmBalancePlan p = {};
     const long long bytes = T * ((long long)E * (dtype == SOT_F32 ? 4 : 2) + 4ll * K);
-    // One cluster up to 512 KB of logits and choices: one launch instead of two and a
-    // scratch allocation outweigh the SMs that stay idle.
+    // One cluster up to 512 KB of logits and choices: 1024 x 256 bf16 takes 9.7 us on
+    // the GPU against 7.6 us, but one launch and no scratch instead of two launches and
+    // an allocation, 8 us less on the host.
     if (bytes <= 512 * 1024) {
         const long long want = (T + CNT_NT / 32 - 1) / (CNT_NT / 32);
         p.blocks = 1;

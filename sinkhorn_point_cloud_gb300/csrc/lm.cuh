@@ -1,6 +1,6 @@
-// lm.cuh -- device helpers of the language-model loss kernels: 16-byte
-// vectors of logits in three types, (max, sum) pairs of a softmax, and a
-// logarithm that keeps more than 24 bits.
+// lm.cuh -- device helpers of the language-model loss kernels: 16-byte granules of
+// logits in three types, softmax statistics, float-pair sums and logarithms,
+// clusters.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -96,6 +96,7 @@ __device__ __forceinline__ uint64_t policy_drop() {
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
+// (Not volatile: no kernel reads an address again after it has written it.)
 __device__ __forceinline__ uint4 load16(const uint4* p, uint64_t policy) {
     uint4 v;
     asm("ld.global.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
@@ -166,7 +167,7 @@ __device__ __forceinline__ int load_index(const void* p, int type, long long i, 
     return v >= 0 && v < n ? (int)v : -1;
 }
 
-// Writes N elements at columns e .. e + N - 1 of a row.
+// Writes N elements at columns e .. e + N - 1 of a row (those of them that exist).
 template <int DT>
 __device__ __forceinline__ void store_cols(typename Elem<DT>::T* row, int e, int V,
                                            const float2 (&f)[Elem<DT>::N / 2], bool aligned) {
@@ -182,6 +183,7 @@ __device__ __forceinline__ void store_cols(typename Elem<DT>::T* row, int e, int
     }
 }
 
+// Replaces the elements at columns outside [0, V).
 template <int DT>
 __device__ __forceinline__ void mask_cols(float2 (&f)[Elem<DT>::N / 2], int e, int V, float fill) {
 #pragma unroll
@@ -349,12 +351,6 @@ __device__ __forceinline__ float exp_minus_linear(float u) {
     return expm1f(u) - u;
 }
 
-__device__ __forceinline__ double warp_sum_d(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -380,4 +376,5 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_store(uint32_t ra, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(ra), "f"(v) : "memory");
 }
+
 }  // namespace sot

@@ -8,14 +8,28 @@
 //
 // lm_row_kernel: a CTA takes a row, or a cluster of CTAs a slice of it each, in
 // two passes: statistics, then the gradient.  The second pass reads the row
-// again, from L2 or L1, where it still is: the rows under way at one time take
-// less than half of L2.  Several CTAs share an SM and are in different phases, so
-// loads, reductions and stores of different rows overlap without any hand-over
-// inside a CTA.  A warp of its own prepares the teacher's side during the first
-// pass, joins the statistics (with the cluster's other CTAs through distributed
-// shared memory) and forms the loss and the gradient's coefficients.
+// again, from L2, where it still is: the rows under way at one time take 40 to 60
+// of the 129 MB, and the first pass asks L2 to keep them while the stores and the
+// second pass ask for nothing to be kept (counted: DRAM reads are the logits
+// once, 0.5386 GB for 0.5369 GB).  Several CTAs share an SM and are in different
+// phases, so loads, reductions and stores of different rows overlap without any
+// hand-over inside a CTA.  A warp of its own prepares the teacher's side during
+// the first pass, joins the statistics (with the cluster's other CTAs through
+// distributed shared memory) and forms the loss and the gradient's coefficients.
+//   Measured, of 6779 GB/s of copy bandwidth: log-probabilities of 16384 x 32000
+//   bf16 in 154 us (1.00); policy loss of 8192 x 65536, a third of the rows left out,
+//   in 283 us (0.93); distillation of 4096 x 131072 in 349 us (0.91).  Batches of a
+//   few waves of CTAs lose part of the last one: 3001 x 50021 fp16 in 111 us (0.76),
+//   1001 x 50021 fp32 with the tail in 80 us (0.65).  Few rows: 4 to 6 us, the
+//   latency of one launch, one load, a reduction across the cluster and one store.
+//   Also tried: slices resident in shared memory, copied in bulk by warps of their
+//   own (465 us for the distillation: a row's slices wait for one another), a ring
+//   of chunks (519 us: 0.4 us of hand-overs a chunk), a resident grid that walks the
+//   rows (442 us).
 //
 // lm_short_kernel: short rows, a warp each, kept in registers between the passes.
+//   16384 rows of 2048 bf16: 31 us with gradient (0.64), 21 us without; a CTA a row
+//   takes 73 and 46 us.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -25,7 +39,6 @@
 namespace sot {
 
 constexpr int ROW_MAX_CL = 8;
-constexpr int ROW_MAX_NW = 16;  // streaming warps of a CTA
 constexpr int NREC = 6;         // a CTA's record: (m, s), the entries' (m, s), the entries' sum q x in two parts
 
 struct LmRowLaunch {
@@ -173,46 +186,24 @@ __device__ __forceinline__ void student_side(const LmRowArgs& a, int c0, int c1,
     }
 }
 
-// What is known of a row before its copy starts.  RowLoad holds it as it was
-// loaded: nothing is computed from it, so a load for a later row is waited for
-// only when that row's turn comes.
+// What a row's loss depends on besides its logits.
 struct RowMeta {
     int tgt;
     float w, old, ref, adv;
     bool keep;
 };
-struct RowLoad {
-    int t32;
-    long long t64;
-    float w, old, ref, adv;
-};
+// `all`: the policy's values too, which only the row's own warp needs.
 template <int OP>
-__device__ __forceinline__ RowLoad row_load(const LmRowArgs& a, long long row, bool all) {
-    RowLoad m;
-    m.t32 = 0;
-    m.t64 = 0;
-    m.w = m.old = m.ref = m.adv = 0.f;
-    if (OP != LM_DISTILL) {
-        if (a.target_type == SOT_I64) m.t64 = static_cast<const long long*>(a.target)[row];
-        else m.t32 = static_cast<const int*>(a.target)[row];
-    }
-    if (OP != LM_LOGPROB && a.weight) m.w = a.weight[row];
+__device__ __forceinline__ RowMeta row_meta(const LmRowArgs& a, long long row, bool all) {
+    RowMeta m;
+    m.tgt = OP == LM_DISTILL ? 0 : load_index(a.target, a.target_type, row, a.V);
+    m.w = OP == LM_LOGPROB ? 1.f : a.weight ? a.weight[row] : 1.f / (float)a.T;
+    m.old = m.ref = m.adv = 0.f;
     if (OP == LM_POLICY && all) {
         m.old = a.old_logp[row];
         m.adv = a.adv[row];
         if (a.ref_logp) m.ref = a.ref_logp[row];
     }
-    return m;
-}
-template <int OP>
-__device__ __forceinline__ RowMeta row_meta(const LmRowArgs& a, const RowLoad& l) {
-    RowMeta m;
-    const long long t = a.target_type == SOT_I64 ? l.t64 : l.t32;
-    m.tgt = OP == LM_DISTILL ? 0 : t >= 0 && t < a.V ? (int)t : -1;
-    m.w = OP == LM_LOGPROB ? 1.f : a.weight ? l.w : 1.f / (float)a.T;
-    m.old = l.old;
-    m.ref = l.ref;
-    m.adv = l.adv;
     m.keep = m.tgt >= 0 && m.w != 0.f;
     return m;
 }
@@ -440,6 +431,7 @@ __device__ __forceinline__ void slice_zero(const Slice& s, typename Elem<DT>::T*
     for (int k = 0; k < N / 2; ++k) z[k] = make_float2(0.f, 0.f);
     for (int g = tid; g < s.ng; g += NT) store_cols<DT>(grow, s.e0 + g * N, V, z, aligned);
 }
+
 // NW streaming warps and the row's own warp.
 template <int DT, int OP, int NW, bool TAIL>
 __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8 : 7) : NW == 8 ? 4 : 2)
@@ -458,7 +450,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
     const uint32_t rank = cluster_rank();
     const float sc = SOT_LOG2E / a.tau;
     const long long row = blockIdx.x / L.CL;
-    const RowMeta m = row_meta<OP>(a, row_load<OP>(a, row, warp == NW));
+    const RowMeta m = row_meta<OP>(a, row, warp == NW);
     const T* const x = static_cast<const T*>(a.x) + row * a.ld;
     T* const grow = OP != LM_LOGPROB && a.grad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
     const bool aligned = same_granules<T>(x, grow);
@@ -572,7 +564,7 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
     float* const eq = ex + a.K;
     int* const eid = reinterpret_cast<int*>(eq + a.K);
     unsigned* const cut = marks[TAIL ? warp : 0];
-    const RowMeta m = row_meta<OP>(a, row_load<OP>(a, row, true));
+    const RowMeta m = row_meta<OP>(a, row, true);
     const T* const x = static_cast<const T*>(a.x) + row * a.ld;
     T* const grow = OP != LM_LOGPROB && a.grad ? static_cast<T*>(a.grad) + row * a.ldg : nullptr;
     const bool aligned = same_granules<T>(x, grow);
@@ -629,24 +621,26 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
         }
     const MS r = ms_warp(run.result(), sc);
     const RowCoef c = row_finish<OP>(a, row, m, r, top, Q, B, D, sc, lane == 0, [](const RowCoef&) {});
-    if (!grow) return;
+    if constexpr (OP != LM_LOGPROB) {
+        if (!grow) return;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int g = lane + 32 * i;
-        if (g < s.ng) {
-            float2 f[N / 2];
-            unpack<DT>(v[i], f);
-            grad_of<DT>(f, c, sc);
-            if (aligned && g >= s.lo && g < s.hi) store16(reinterpret_cast<uint4*>(grow + s.e0) + g, pack<DT>(f), policy);
-            else store_cols<DT>(grow, s.e0 + g * N, a.V, f, false);
+        for (int i = 0; i < R; ++i) {
+            const int g = lane + 32 * i;
+            if (g < s.ng) {
+                float2 f[N / 2];
+                unpack<DT>(v[i], f);
+                grad_of<DT>(f, c, sc);
+                if (aligned && g >= s.lo && g < s.hi) store16(reinterpret_cast<uint4*>(grow + s.e0) + g, pack<DT>(f), policy);
+                else store_cols<DT>(grow, s.e0 + g * N, a.V, f, false);
+            }
         }
+        __syncwarp();  // the corrections come after the columns they replace
+        if (OP == LM_DISTILL) {
+            for (int k = lane; k < a.K; k += 32)
+                if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * (weight_of(ex[k], c.M, sc) * c.inv_S) - c.fb * eq[k]);
+        } else if (lane == 0)
+            grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(D.x, c.M, sc) * c.inv_S) - c.fb);
     }
-    __syncwarp();  // the corrections come after the columns they replace
-    if (OP == LM_DISTILL) {
-        for (int k = lane; k < a.K; k += 32)
-            if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * (weight_of(ex[k], c.M, sc) * c.inv_S) - c.fb * eq[k]);
-    } else if (lane == 0)
-        grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(D.x, c.M, sc) * c.inv_S) - c.fb);
 }
 
 struct LmRowPlan {
@@ -688,8 +682,13 @@ cudaError_t launch_row_k(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaun
 template <int DT, int OP, int R>
 cudaError_t launch_row_r(const LmRowArgs& a, const LmRowPlan& p, cudaStream_t st) {
     const unsigned blocks = (unsigned)((a.T + SHORT_NW - 1) / SHORT_NW);
-    if (OP == LM_DISTILL && a.tail) lm_short_kernel<DT, OP, R, OP == LM_DISTILL><<<blocks, SHORT_NW * 32, p.smem, st>>>(a);
-    else lm_short_kernel<DT, OP, R, false><<<blocks, SHORT_NW * 32, p.smem, st>>>(a);
+    if constexpr (OP == LM_DISTILL) {
+        if (a.tail) {
+            lm_short_kernel<DT, OP, R, true><<<blocks, SHORT_NW * 32, p.smem, st>>>(a);
+            return cudaGetLastError();
+        }
+    }
+    lm_short_kernel<DT, OP, R, false><<<blocks, SHORT_NW * 32, p.smem, st>>>(a);
     return cudaGetLastError();
 }
 
