@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(GRAD_NT) lm_grad_kernel(const LmGradArgs a, in
                 store16(dst + i + j * GRAD_NT, pack<DT>(f), policy);
             }
     }
-    const int e = edge_granule(s, threadIdx.x);
+    const int e = edge_granule(s, threadIdx.x, GRAD_NT);
     if (e >= 0) {
         float2 f[N / 2];
         unpack<DT>(s.src[e], f);

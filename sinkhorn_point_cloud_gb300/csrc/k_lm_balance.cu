@@ -14,9 +14,11 @@
 // kernel is launched along with it (programmatic dependent launch), reads its
 // first rows meanwhile, adds the counts up and goes on; its last CTA to finish joins
 // the sums.
-//   Measured: 65536 x 256 bf16, 8 choices, a tenth left out: 22.8 us, of which the
-// counting 7 us (0.42 of the copy bandwidth for 66 MB: each warp walks four to
-// seven dependent steps of load, maximum, sums and store); 256 x 64 fp32: 6 us.
+//   Measured: 65536 x 256 bf16, 8 choices, a tenth left out: 19.8 us, 0.49 of the copy
+// bandwidth for 66 MB; the counting and the waits around it take 5 us of it, the
+// rest is each warp's seven dependent steps of load, maximum, sums and store.  65536 x
+// 256 fp32: 30 us (0.67); 256 x 64 fp32: 6 us.  Loads into shared memory several steps
+// ahead and more, lighter CTAs were no faster (22 to 24 us).
 // A power of two of lanes takes a row, four granules of 16 bytes a lane (fewer
 // for few experts, more for many), as many rows at a time as fit a warp.
 #include <cuda_runtime.h>
@@ -75,10 +77,17 @@ __device__ __forceinline__ float group_max(float v, int lanes) {
 constexpr int F_LEN = LM_MAX_E + 16;
 template <int DT, bool SHIFT>
 constexpr int f_copies = SHIFT ? Elem<DT>::N : 1;
+// The float4s of a granule's experts lie F_HALF apart, so that neighbouring lanes'
+// float4s are neighbours.
+constexpr int F_HALF = F_LEN / 2;
+template <int DT>
+__device__ __forceinline__ int f_at(int e) {
+    return Elem<DT>::N == 4 ? e : e / 8 * 4 + (e & 3) + (e & 4 ? F_HALF : 0);
+}
 template <int DT, bool SHIFT>
 __device__ __forceinline__ void put_share(float* f, int e, float v) {
 #pragma unroll
-    for (int h = 0; h < f_copies<DT, SHIFT>; ++h) f[h * F_LEN + e + h] = v;
+    for (int h = 0; h < f_copies<DT, SHIFT>; ++h) f[h * F_LEN + f_at<DT>(e + h)] = v;
 }
 
 // The rows of one warp of `warps`: `lanes` lanes a row, R granules a lane, 32 / lanes
@@ -115,6 +124,31 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
     bool keep = kept(t), next = kept(t + step);
     load(t, keep);
     const float inv_n = counted();
+    // coef f of the experts of granule i, in the order of x
+    const auto shares_at = [&](int i, int head, int ng, float2 (&c)[N / 2]) {
+        const int g = sub + i * lanes;
+        const float4* const q = reinterpret_cast<const float4*>(f + head * F_LEN + g * 4);
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            const float4 r = g < ng ? q[k * (F_HALF / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+            c[2 * k] = make_float2(r.x, r.y);
+            c[2 * k + 1] = make_float2(r.z, r.w);
+        }
+    };
+    // With whole granules a lane's experts are the same in every row: from 32 of them a
+    // lane their shares stay in registers (65536 x 256 bf16 20.0 us, read again for every
+    // row 21.1); with fewer the registers pay for more warps (65536 x 64: 12.3 and 13.0).
+    constexpr bool OWN = !SHIFT && H >= 16;
+    float2 own[OWN ? H : 1];
+    if constexpr (OWN) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float2 c[N / 2];
+            shares_at(i, 0, units, c);
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) own[i * (N / 2) + k] = c[k];
+        }
+    }
     for (long long base = warp * per; base < a.T; base += step, t += step) {
         const T* const row = static_cast<const T*>(a.x) + t * a.ld;
         const int head = head_of(row), ng = granules(head);
@@ -156,15 +190,11 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
 #pragma unroll
             for (int i = 0; i < H; ++i) x[i] = make_float2(weight_of(x[i].x, m, SOT_LOG2E), weight_of(x[i].y, m, SOT_LOG2E));
         }
-        // coef f of the experts of granule i, in the order of x
         const auto shares = [&](int i, float2 (&c)[N / 2]) {
-            const int g = sub + i * lanes;
-            const float4* const q = reinterpret_cast<const float4*>(f + head * F_LEN + g * N);
+            if constexpr (!OWN) shares_at(i, head, ng, c);
+            else {
 #pragma unroll
-            for (int k = 0; k < N / 4; ++k) {
-                const float4 r = g < ng ? q[k] : make_float4(0.f, 0.f, 0.f, 0.f);
-                c[2 * k] = make_float2(r.x, r.y);
-                c[2 * k + 1] = make_float2(r.z, r.w);
+                for (int k = 0; k < N / 2; ++k) c[k] = own[i * (N / 2) + k];
             }
         };
         float2 sum = make_float2(0.f, 0.f), dots = sum;
@@ -396,10 +426,14 @@ template <int DT, bool SHIFT>
 cudaError_t launch_s(const LmBalanceArgs& a, int granules, int blocks, cudaStream_t st) {
     if (granules <= 4) return launch_r<DT, 1, SHIFT>(a, blocks, st);
     if (granules <= 8) return launch_r<DT, 2, SHIFT>(a, blocks, st);
-    if (granules <= 128) return launch_r<DT, 4, SHIFT>(a, blocks, st);
-    if constexpr (DT == SOT_F32 && SHIFT)
-        if (granules > 256) return launch_r<DT, 16, SHIFT>(a, blocks, st);
-    return launch_r<DT, 8, SHIFT>(a, blocks, st);
+    if constexpr (DT == SOT_F32 || SHIFT) {
+        if (granules > 128) {
+            if constexpr (DT == SOT_F32 && SHIFT)
+                if (granules > 256) return launch_r<DT, 16, SHIFT>(a, blocks, st);
+            return launch_r<DT, 8, SHIFT>(a, blocks, st);
+        }
+    }
+    return launch_r<DT, 4, SHIFT>(a, blocks, st);
 }
 
 template <int DT>

@@ -19,7 +19,7 @@
 //   Measured, of 6779 GB/s of copy bandwidth: log-probabilities of 16384 x 32000
 //   bf16 in 154 us (1.00); policy loss of 8192 x 65536, a third of the rows left out,
 //   in 283 us (0.93); distillation of 4096 x 131072 in 349 us (0.91).  Batches of a
-//   few waves of CTAs lose part of the last one: 3001 x 50021 fp16 in 111 us (0.76),
+//   few waves of CTAs lose part of the last one: 3001 x 50021 fp16 in 110 us (0.77),
 //   1001 x 50021 fp32 with the tail in 80 us (0.65).  Few rows: 4 to 6 us, the
 //   latency of one launch, one load, a reduction across the cluster and one store.
 //   Also tried: slices resident in shared memory, copied in bulk by warps of their
@@ -300,11 +300,13 @@ __device__ __forceinline__ void row_outputs(const LmRowArgs& a, long long row, f
 
 // ---- what NT threads (tid = 0 .. NT - 1) do with a slice.  Granules inside the
 // row, [lo, hi), go in batches, so that their loads are under way together; the
-// granule the row starts in and the one it ends in belong to two threads.  With
+// granule the row starts in and the one it ends in belong to two threads of the last
+// warp, whose share is the shortest (with the first warp 6080 x 50021 fp16 take 222 us,
+// so 219).  With
 // CUT, byte g of `cut` names the elements of granule g that are left out.
-__device__ __forceinline__ int edge_granule(const Slice& s, int tid) {
-    if (tid == 0 && s.ng > 0 && s.lo > 0) return 0;
-    if (tid == 1 && s.ng > 0 && s.hi < s.ng && (s.ng > 1 || s.lo == 0)) return s.ng - 1;
+__device__ __forceinline__ int edge_granule(const Slice& s, int tid, int NT) {
+    if (tid == NT - 1 && s.ng > 0 && s.lo > 0) return 0;
+    if (tid == NT - 2 && s.ng > 0 && s.hi < s.ng && (s.ng > 1 || s.lo == 0)) return s.ng - 1;
     return -1;
 }
 template <int DT>
@@ -347,7 +349,7 @@ __device__ __forceinline__ void slice_stats(Running& r, const Slice& s, uint64_t
         r.template add<DT>(v, sc);
         if (g + U * NT < s.hi) r.template add<DT>(w, sc);
     }
-    const int e = edge_granule(s, tid);
+    const int e = edge_granule(s, tid, NT);
     if (e >= 0) {
         float2 f[N / 2];
         unpack<DT>(src(e), f);
@@ -406,7 +408,7 @@ __device__ __forceinline__ void slice_grad(const Slice& s, const RowCoef& c, typ
                     }
             }
         }
-        const int e = edge_granule(s, tid);
+        const int e = edge_granule(s, tid, NT);
         if (e >= 0) {
             float2 f[N / 2];
             unpack<DT>(src(e), f);
