@@ -14,11 +14,14 @@
 // kernel is launched along with it (programmatic dependent launch), reads its
 // first rows meanwhile, adds the counts up and goes on; its last CTA to finish joins
 // the sums.
-//   Measured: 65536 x 256 bf16, 8 choices, a tenth left out: 19.8 us, 0.49 of the copy
-// bandwidth for 66 MB; the counting and the waits around it take 5 us of it, the
-// rest is each warp's seven dependent steps of load, maximum, sums and store.  65536 x
-// 256 fp32: 30 us (0.67); 256 x 64 fp32: 6 us.  Loads into shared memory several steps
-// ahead and more, lighter CTAs were no faster (22 to 24 us).
+//   Weights are formed against 0, which needs no maximum first, and against the
+// row's maximum only where their sum leaves the middle of the range.
+//   Measured: 65536 x 256 bf16, 8 choices, a tenth left out: 17.9 us, 0.54 of the copy
+// bandwidth for 66 MB (with the maximum first 19.8 us); the counting and the waits
+// around it take 5 us of it, the rest is each warp's seven dependent steps of load,
+// sums and store.  65536 x 256 fp32: 29.6 us (0.68); 65536 x 500 fp16: 37 us (0.53);
+// 256 x 64 fp32: 6 us.  Loads into shared memory several steps ahead and more, lighter
+// CTAs were no faster.
 // A power of two of lanes takes a row, four granules of 16 bytes a lane (fewer
 // for few experts, more for many), as many rows at a time as fit a warp.
 #include <cuda_runtime.h>
@@ -136,8 +139,8 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
         }
     };
     // With whole granules a lane's experts are the same in every row: from 32 of them a
-    // lane their shares stay in registers (65536 x 256 bf16 20.0 us, read again for every
-    // row 21.1); with fewer the registers pay for more warps (65536 x 64: 12.3 and 13.0).
+    // lane their shares stay in registers (65536 x 256 bf16 17.9 us, read again for every
+    // row 19.0); with fewer the registers pay for more warps (65536 x 64: 12.3 and 13.0).
     constexpr bool OWN = !SHIFT && H >= 16;
     float2 own[OWN ? H : 1];
     if constexpr (OWN) {
@@ -153,42 +156,25 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
         const T* const row = static_cast<const T*>(a.x) + t * a.ld;
         const int head = head_of(row), ng = granules(head);
         float2 x[H];
-        float m;
-        if constexpr (!SHIFT) {
-            uint4 top = v[0];
+        const auto open = [&](const uint4 (&v)[R]) {
 #pragma unroll
-            for (int i = 1; i < R; ++i) top = max2<DT>(top, v[i]);
-            m = max_of<DT>(top);
-        } else
-            m = -INFINITY;
+            for (int i = 0; i < R; ++i) {
+                float2 p[N / 2];
+                unpack<DT>(v[i], p);
+                if (SHIFT) {
+                    const int g = sub + i * lanes;
+                    if (g == 0 || g == ng - 1) mask_cols<DT>(p, g * N - head, a.E, -INFINITY);
+                }
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float2 p[N / 2];
-            unpack<DT>(v[i], p);
-            if (SHIFT) {
-                const int g = sub + i * lanes;
-                if (g == 0 || g == ng - 1) mask_cols<DT>(p, g * N - head, a.E, -INFINITY);
-#pragma unroll
-                for (int k = 0; k < N / 2; ++k) m = fmaxf(m, fmaxf(p[k].x, p[k].y));
+                for (int k = 0; k < N / 2; ++k) x[i * (N / 2) + k] = p[k];
             }
-#pragma unroll
-            for (int k = 0; k < N / 2; ++k) x[i * (N / 2) + k] = p[k];
-        }
+        };
+        open(v);
         const bool now = keep;
         keep = next;
         if (base + step < a.T) {
             load(t + step, keep);
             next = kept(t + 2 * step);
-        }
-        m = group_max(m, lanes);
-        const float u = __fmul_rn(m, SOT_LOG2E);
-        const bool far = !(fabsf(u) < INFINITY);
-        if (!far) {
-#pragma unroll
-            for (int i = 0; i < H; ++i) x[i] = ex2_pair(x[i], u, SOT_LOG2E);
-        } else {
-#pragma unroll
-            for (int i = 0; i < H; ++i) x[i] = make_float2(weight_of(x[i].x, m, SOT_LOG2E), weight_of(x[i].y, m, SOT_LOG2E));
         }
         const auto shares = [&](int i, float2 (&c)[N / 2]) {
             if constexpr (!OWN) shares_at(i, head, ng, c);
@@ -197,21 +183,61 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
                 for (int k = 0; k < N / 2; ++k) c[k] = own[i * (N / 2) + k];
             }
         };
-        float2 sum = make_float2(0.f, 0.f), dots = sum;
+        // The row's sums: of its weights, and of them times the shares.
+        const auto add_up = [&](float& s, float& d) {
+            float2 sum = make_float2(0.f, 0.f), dots = sum;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            float2 c[N / 2];
-            shares(i, c);
+            for (int i = 0; i < R; ++i) {
+                float2 c[N / 2];
+                shares(i, c);
 #pragma unroll
-            for (int k = 0; k < N / 2; ++k) {
-                sum = fadd2(sum, x[i * (N / 2) + k]);
-                dots = ffma2(x[i * (N / 2) + k], c[k], dots);
+                for (int k = 0; k < N / 2; ++k) {
+                    sum = fadd2(sum, x[i * (N / 2) + k]);
+                    dots = ffma2(x[i * (N / 2) + k], c[k], dots);
+                }
             }
-        }
-        float s = sum.x + sum.y, d = dots.x + dots.y;
-        for (int o = lanes >> 1; o > 0; o >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-            d += __shfl_xor_sync(0xffffffffu, d, o);
+            s = sum.x + sum.y;
+            d = dots.x + dots.y;
+            for (int o = lanes >> 1; o > 0; o >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+                d += __shfl_xor_sync(0xffffffffu, d, o);
+            }
+        };
+        // Weights against 0; where their sum leaves the middle of the range, the row is
+        // read again and its weights are formed against its maximum.
+        float m = 0.f, u = 0.f, s, d;
+        bool far = false;
+#pragma unroll
+        for (int i = 0; i < H; ++i) x[i] = ex2_pair(x[i], 0.f, SOT_LOG2E);
+        add_up(s, d);
+        const bool again = now && !(s > 0x1p-40f && s < 0x1p24f);
+        if (__any_sync(0xffffffffu, again)) {
+            const float s0 = s, d0 = d;
+            if (again) {
+                const uint4* const src = reinterpret_cast<const uint4*>(row - head);
+                uint4 w[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) w[i] = sub + i * lanes < ng ? src[sub + i * lanes] : nothing<DT>();
+                open(w);
+                m = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < H; ++i) m = fmaxf(m, fmaxf(x[i].x, x[i].y));
+            }
+            m = group_max(m, lanes);
+            if (again) {
+                u = __fmul_rn(m, SOT_LOG2E);
+                far = !(fabsf(u) < INFINITY);
+                if (far) u = 0.f;
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    x[i] = far ? make_float2(weight_of(x[i].x, m, SOT_LOG2E), weight_of(x[i].y, m, SOT_LOG2E))
+                               : ex2_pair(x[i], u, SOT_LOG2E);
+            }
+            add_up(s, d);
+            if (!again) {
+                s = s0;
+                d = d0;
+            }
         }
         const float inv_s = __fdividef(1.f, s), dot = d * inv_s;  // coef sum f p
         const float lse = far ? m + __logf(s) : (u + __log2f(s)) * SOT_LN2;
@@ -223,7 +249,7 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
         T* const grow = static_cast<T*>(a.grad) + t * a.ldg;
         const bool aligned = !SHIFT || same_granules<T>(row, grow);
         // (the weights of a token that is left out are 0)
-        const float bias = now ? 2.f * a.z_coef * lse - dot : 0.f, k = now ? inv_n * inv_s : 0.f;
+        const float k = now ? inv_n * inv_s : 0.f, bias = now ? (2.f * a.z_coef * lse - dot) * k : 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int g = sub + i * lanes;
@@ -231,7 +257,7 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
             shares(i, c);
 #pragma unroll
             for (int j = 0; j < N / 2; ++j)
-                p[j] = fmul2(x[i * (N / 2) + j], fmul2(fadd2(c[j], make_float2(bias, bias)), make_float2(k, k)));
+                p[j] = fmul2(x[i * (N / 2) + j], ffma2(c[j], make_float2(k, k), make_float2(bias, bias)));
             if (g < ng) {
                 if (SHIFT) store_cols<DT>(grow, g * N - head, a.E, p, aligned);
                 else reinterpret_cast<uint4*>(grow)[g] = pack<DT>(p);

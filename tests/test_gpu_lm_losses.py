@@ -574,3 +574,33 @@ def test_preference_from_logits_to_gradient(sot):
     close(loss, rl, scale=10.0)
     rg, size = R.token_grad(host(x), tg.cpu().numpy(), 1.0, rd)
     close_grad(grad, rg, size + 0.1, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,E", [(40, 60), (40, 64), (3000, 60), (3000, 256), (1500, 520), (700, 1024)])
+@pytest.mark.parametrize("empty", [True, False])
+def test_balance_loss_of_offset_logits(sot, T, E, dtype, empty):
+    """Neighbouring rows far from zero in different directions, so that their sums of
+    exponentials leave the range of a float, and rows with few experts left.  Some rows have none
+    left: they make the losses NaN and touch no other row's gradient, or (empty = False) are masked."""
+    x = rows(T, E, dtype, 0, seed=E + T, spread=2.0)
+    off = torch.tensor([0, 30, -30, 17, -45, 200, -200, 3000, -26, 16, -3000], dtype=x.dtype).cuda()
+    x += off[torch.arange(T).cuda() % 11, None]
+    x[3::7, 1:] = float("-inf")
+    x[4::9, : E // 2] = float("-inf")
+    ids = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(t))[:2] for t in range(T)]).int()
+    mask = torch.arange(T) % 13 != 5
+    some = torch.isfinite(x).any(1).cpu()
+    if not empty:
+        mask &= some
+    scale = 256.0 * T
+    counts, loss, grad = sot.sot_balance_loss(x, ids.cuda(), mask=mask.cuda(), balance_coef=scale, z_coef=1e-5 * scale)
+    with np.errstate(invalid="ignore"):
+        rc, rl, rg, size = R.balance(host(x), ids.numpy(), mask.numpy(), scale, 1e-5 * scale)
+    assert np.array_equal(counts.cpu().numpy(), rc)
+    assert np.array_equal(np.isnan(host(loss)), np.isnan(rl))
+    assert np.isnan(rl).any() == bool((mask & ~some).any())
+    if not np.isnan(rl).any():
+        assert np.all(np.abs(host(loss) - rl) <= ATOL * np.abs(rl))
+    fine = (some | ~mask).numpy()
+    close_grad(grad[torch.from_numpy(fine).cuda()], rg[fine], size[fine], dtype)
