@@ -174,7 +174,8 @@ void row_plan(bool grads, bool whole, long long T, int dtype, int V, int K, bool
     const long long total = ((long long)V + (whole ? N - 1 : 2 * N - 2)) / N;
     const auto plan = [&](int NW, int CL) {
         const long long G = (total + CL - 1) / CL;
-        const size_t smem = NW == 0 ? (size_t)K * 12 * SHORT_NW : (size_t)K * 12 + (tail ? ((size_t)G + 3) / 4 * 4 : 0);
+        const size_t smem = NW == 0 ? (size_t)K * 12 * SHORT_NW
+                                    : (size_t)K * 12 + (tail ? cut_bytes((int)G) + cut_batches((int)G, NW * 32) : 0);
         *p = LmRowPlan{NW, CL, (int)G, smem};
     };
     const auto warps = [](long long G, int per) { return G <= per * 128ll ? 4 : G <= per * 256ll ? 8 : 16; };
@@ -209,7 +210,7 @@ void row_plan(bool grads, bool whole, long long T, int dtype, int V, int K, bool
 bool lm_tail_fits(int dtype, int V, int K) {
     LmRowPlan p;
     row_plan(true, false, 1ll << 31, dtype, V, K, true, 1, &p);
-    return p.smem <= 200 * 1024;
+    return p.smem <= 220 * 1024;
 }
 
 cudaError_t launch_lm_row(LmOp op, const LmRowArgs& a, int sms, cudaStream_t st) {

@@ -110,6 +110,25 @@ __device__ __forceinline__ void store16(uint4* p, const uint4& v, uint64_t polic
                  : "memory");
 }
 
+// One element at p, copied to shared memory behind the thread's back as the 32-bit word
+// around it; element_of gives it after async_wait.
+template <class T>
+__device__ __forceinline__ void fetch_element(float* to, const T* p) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"((unsigned long long)p & ~3ull) : "memory");
+}
+__device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+template <int DT>
+__device__ __forceinline__ float element_of(float word, const typename Elem<DT>::T* p) {
+    if constexpr (sizeof(*p) == 4) return word;
+    else {
+        const uint32_t b = __float_as_uint(word);
+        const unsigned short h = (unsigned short)((unsigned long long)p & 2ull ? b >> 16 : b);
+        typename Elem<DT>::T e;
+        memcpy(&e, &h, sizeof(e));
+        return Elem<DT>::get(e);
+    }
+}
+
 template <int DT>
 __device__ __forceinline__ uint4 nothing() {  // N times -inf
     constexpr unsigned w = DT == SOT_F32 ? 0xff800000u : DT == SOT_F16 ? 0xfc00fc00u : 0xff80ff80u;

@@ -18,9 +18,9 @@
 // distributed shared memory) and forms the loss and the gradient's coefficients.
 //   Measured, of 6779 GB/s of copy bandwidth: log-probabilities of 16384 x 32000
 //   bf16 in 154 us (1.00); policy loss of 8192 x 65536, a third of the rows left out,
-//   in 283 us (0.93); distillation of 4096 x 131072 in 349 us (0.91).  Batches of a
+//   in 283 us (0.93); distillation of 4096 x 131072 in 347 us (0.91).  Batches of a
 //   few waves of CTAs lose part of the last one: 3001 x 50021 fp16 in 110 us (0.77),
-//   1001 x 50021 fp32 with the tail in 80 us (0.65).  Few rows: 4 to 6 us, the
+//   1001 x 50021 fp32 with the tail in 78 us (0.66).  Few rows: 4 to 6 us, the
 //   latency of one launch, one load, a reduction across the cluster and one store.
 //   Also tried: slices resident in shared memory, copied in bulk by warps of their
 //   own (465 us for the distillation: a row's slices wait for one another), a ring
@@ -29,7 +29,8 @@
 //
 // lm_short_kernel: short rows, a warp each, kept in registers between the passes.
 //   16384 rows of 2048 bf16: 31 us with gradient (0.64), 21 us without; a CTA a row
-//   takes 73 and 46 us.
+//   takes 73 and 46 us.  Distillation with 8 entries 45 us, with the tail 54 us: the
+//   chain of the entries' loads and sums is what a row waits for.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -91,24 +92,30 @@ __device__ __forceinline__ Slice slice_of(const void* x, long long row, long lon
 
 // The teacher's entries of a row (one warp), in two steps.  First the entries as
 // they are: values in eq (-inf: unused), columns in eid (-1: unused); returns the
-// largest value.
-__device__ __forceinline__ float teacher_entries(const LmRowArgs& a, long long row, float* eq, int* eid) {
+// largest value.  The student's logits in columns [c0, c1) of the row at x are on
+// their way to ex meanwhile.  U loads in flight: 4096 x 32000 with 256 entries take
+// 121 us with four and the logits fetched after the weights, 115 with the logits
+// fetched here, 106 with eight; short rows have no registers for eight (57 and 65 us).
+template <int DT, int U>
+__device__ __forceinline__ float teacher_entries(const LmRowArgs& a, long long row, int c0, int c1,
+                                                 const typename Elem<DT>::T* x, float* ex, float* eq, int* eid) {
     const int lane = threadIdx.x & 31;
     float zmax = -INFINITY;
-    for (int k0 = 0; k0 < a.K; k0 += 128) {  // four loads in flight a lane
-        int id[4];
-        float z[4];
+    for (int k0 = 0; k0 < a.K; k0 += 32 * U) {  // U loads in flight a lane
+        int id[U];
+        float z[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < U; ++j) {
             const int k = k0 + 32 * j + lane;
             id[j] = k < a.K ? load_index(a.ids, a.ids_type, row * a.K + k, a.V) : -1;
             z[j] = k < a.K ? load_float(a.teacher, a.teacher_type, row * a.K + k) : 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < U; ++j) {
             const int k = k0 + 32 * j + lane;
             if (id[j] < 0) z[j] = -INFINITY;
             zmax = fmaxf(zmax, z[j]);
+            if (id[j] >= 0 && id[j] >= c0 && id[j] < c1) fetch_element(ex + k, x + id[j]);
             if (k < a.K) {
                 eid[k] = id[j];
                 eq[k] = z[j];
@@ -148,34 +155,26 @@ __device__ __forceinline__ float2 ff_sum_or_far(float2 v) {
     return fabsf(f) < INFINITY ? s : make_float2(f, 0.f);
 }
 
-// The entries' logits in columns [c0, c1) of a row at x: ex, D = sum q x; eid
-// becomes -1 for the others.  For the tail also the entries' statistics.
+// The entries' logits in columns [c0, c1) of a row at x, from what teacher_entries
+// fetched: ex, D = sum q x; eid becomes -1 for the others.  For the tail also the entries' statistics.
 template <int DT>
 __device__ __forceinline__ void student_side(const LmRowArgs& a, int c0, int c1, const typename Elem<DT>::T* x, float* ex,
                                              const float* eq, int* eid, float sc, float2& D, MS& top) {
     const int lane = threadIdx.x & 31;
     D = make_float2(0.f, 0.f);
     top = MS{-INFINITY, 0.f};
-    for (int k0 = 0; k0 < a.K; k0 += 128) {  // four loads in flight a lane
-        float v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = k0 + 32 * j + lane, id = k < a.K ? eid[k] : -1;
-            v[j] = id >= 0 && id >= c0 && id < c1 ? Elem<DT>::get(x[id]) : -INFINITY;
+    async_wait();
+    for (int k = lane; k < a.K; k += 32) {
+        const int id = eid[k];
+        if (!(id >= 0 && id >= c0 && id < c1)) {
+            ex[k] = -INFINITY;
+            eid[k] = -1;
+            continue;
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = k0 + 32 * j + lane;
-            if (k >= a.K) continue;
-            ex[k] = v[j];
-            const int id = eid[k];
-            if (!(id >= 0 && id >= c0 && id < c1)) {
-                eid[k] = -1;
-                continue;
-            }
-            if (eq[k] != 0.f) D = fabsf(v[j]) < INFINITY ? ff_add(D, two_prod(eq[k], v[j])) : make_float2(D.x + v[j], 0.f);
-            top.m = fmaxf(top.m, v[j]);
-        }
+        const float v = element_of<DT>(ex[k], x + id);
+        ex[k] = v;
+        if (eq[k] != 0.f) D = fabsf(v) < INFINITY ? ff_add(D, two_prod(eq[k], v)) : make_float2(D.x + v, 0.f);
+        top.m = fmaxf(top.m, v);
     }
     D = ff_sum_or_far(D);
     if (a.tail) {
@@ -240,17 +239,34 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
         }
         publish(c);
         if (write && a.loss) {
-            const double logS = to_double(log_ff(all.s)), q = to_double(Q), k = 0.69314718055994530942;
-            double loss = 0.0;
-            if (q > 0.0)
-                loss = to_double(B) + q * logS -
-                       (far ? (to_double(D) - q * (double)all.m) * a.inv_tau : (to_double(D) * (double)sc - q * (double)m2) * k);
-            if (a.tail && !(qr <= 0.f)) {
-                const double apart = far ? ((double)r.m - (double)all.m) * a.inv_tau
-                                         : ((double)__fmul_rn(r.m, sc) - (double)m2) * k;
-                loss += (double)qr * (to_double(log_ff(qr)) - (apart + to_double(log_ff(r.s)) - logS));
+            // In pairs of floats: with doubles throughout, 16384 rows of 2048 take 57 us, so 45.
+            const bool tail = a.tail && !(qr <= 0.f);
+            const float2 logS = log_ff(all.s), logR = tail ? log_ff(r.s) : logS, logq = tail ? log_ff(qr) : logS;
+            float2 sum = make_float2(0.f, 0.f);
+            if (Q.x > 0.f) {  // B + Q log s - (D sc - Q m2) ln 2
+                const float2 d = ff_add(ff_mul(D, make_float2(sc, 0.f)), ff_mul(Q, make_float2(-m2, 0.f)));
+                sum = ff_add(ff_add(B, ff_mul(Q, logS)), ff_mul(d, make_float2(-ln2.x, -ln2.y)));
             }
-            a.loss[row] = (float)(loss * (double)m.w * (double)a.tau * (double)a.tau);
+            if (tail) {  // + q_r (log q_r - log p_r)
+                const float2 apart = ff_mul(two_sum(__fmul_rn(r.m, sc), -m2), ln2);
+                const float2 logp = ff_add(ff_add(apart, logR), make_float2(-logS.x, -logS.y));
+                sum = ff_add(sum, ff_mul(ff_add(logq, make_float2(-logp.x, -logp.y)), make_float2(qr, 0.f)));
+            }
+            float loss = (sum.x + sum.y) * m.w * a.tau * a.tau;
+            if (far || !(fabsf(loss) < INFINITY)) {  // with the range of a double
+                const double q = to_double(Q), k = 0.69314718055994530942;
+                double l = 0.0;
+                if (q > 0.0)
+                    l = to_double(B) + q * to_double(logS) -
+                        (far ? (to_double(D) - q * (double)all.m) * a.inv_tau : (to_double(D) * (double)sc - q * (double)m2) * k);
+                if (tail) {
+                    const double apart = far ? ((double)r.m - (double)all.m) * a.inv_tau
+                                             : ((double)__fmul_rn(r.m, sc) - (double)m2) * k;
+                    l += (double)qr * (to_double(logq) - (apart + to_double(logR) - to_double(logS)));
+                }
+                loss = (float)(l * (double)m.w * (double)a.tau * (double)a.tau);
+            }
+            a.loss[row] = loss;
         }
         return c;
     }
@@ -321,11 +337,19 @@ __device__ __forceinline__ uint4 without(const uint4& v, unsigned out) {
     return pack<DT>(f);
 }
 
+// Behind the bytes, one for each batch of a thread names the granules of it that
+// have any: one load tells a batch that it is whole (a load for each granule takes
+// 318 us instead of 305 for 4096 x 50021 fp32 with 100 entries).
+constexpr int BATCH = 8;  // granules of a thread
+__host__ __device__ inline int cut_bytes(int G) { return (G + 3) / 4 * 4; }
+__host__ __device__ inline int cut_batches(int G, int NT) { return (G + BATCH * NT - 1) / (BATCH * NT) * NT; }
+
 template <int DT, bool CUT>
-__device__ __forceinline__ void slice_stats(Running& r, const Slice& s, uint64_t policy, const unsigned char* cut, int V,
-                                            float sc, int tid, int NT) {
+__device__ __forceinline__ void slice_stats(Running& r, const Slice& s, uint64_t policy, const unsigned char* cut, int G,
+                                            int V, float sc, int tid, int NT) {
     const auto src = [&](int g) { return load16(s.src + g, policy); };
-    constexpr int N = Elem<DT>::N, U = 4;
+    constexpr int N = Elem<DT>::N, U = BATCH / 2;
+    const unsigned char* mine = cut + cut_bytes(G) + tid;
     for (int g = s.lo + tid; g < s.hi; g += 2 * U * NT) {
         uint4 v[U], w[U];
         if (g + (2 * U - 1) * NT < s.hi) {
@@ -340,10 +364,14 @@ __device__ __forceinline__ void slice_stats(Running& r, const Slice& s, uint64_t
             for (int j = 0; j < U; ++j) w[j] = g + (U + j) * NT < s.hi ? src(g + (U + j) * NT) : nothing<DT>();
         }
         if (CUT) {
+            const unsigned marked = *mine;
+            mine += NT;
+            if (marked) {
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                if (g + j * NT < s.hi && cut[g + j * NT]) v[j] = without<DT>(v[j], cut[g + j * NT]);
-                if (g + (U + j) * NT < s.hi && cut[g + (U + j) * NT]) w[j] = without<DT>(w[j], cut[g + (U + j) * NT]);
+                for (int j = 0; j < U; ++j) {
+                    if (marked >> j & 1u) v[j] = without<DT>(v[j], cut[g + j * NT]);
+                    if (marked >> (U + j) & 1u) w[j] = without<DT>(w[j], cut[g + (U + j) * NT]);
+                }
             }
         }
         r.template add<DT>(v, sc);
@@ -466,18 +494,21 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
     }
     if (L.CL > 1) cluster_arrive_started();
     if (TAIL) {
-        for (int g = tid; g < (L.G + 3) / 4; g += NT + 32) cut[g] = 0u;
+        for (int g = tid; g < (cut_bytes(L.G) + cut_batches(L.G, NT)) / 4; g += NT + 32) cut[g] = 0u;
         __syncthreads();
     }
     float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
     MS top{-INFINITY, 0.f};
     if (warp == NW) {
         if (OP == LM_DISTILL) {
-            const float zmax = teacher_entries(a, row, eq, eid);
+            const float zmax = teacher_entries<DT, 8>(a, row, c0, c1, x, ex, eq, eid);
             if (TAIL) {
                 for (int k = lane; k < a.K; k += 32) {
                     const int at = eid[k] - c0;
-                    if (eid[k] >= 0 && at >= 0 && eid[k] < c1) atomicOr(cut + at / N / 4, 1u << (at / N % 4 * 8 + at % N));
+                    if (eid[k] < 0 || at < 0 || eid[k] >= c1) continue;
+                    const int g = at / N, q = g - s.lo, f = q / (BATCH * NT) * NT + q % NT;
+                    atomicOr(cut + g / 4, 1u << (g % 4 * 8 + at % N));
+                    if (q >= 0 && g < s.hi) atomicOr(cut + cut_bytes(L.G) / 4 + f / 4, 1u << (f % 4 * 8 + q / NT % BATCH));
                 }
                 __syncthreads();  // the others can start
             }
@@ -488,7 +519,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
     } else {
         if (TAIL) __syncthreads();
         Running r;
-        slice_stats<DT, TAIL>(r, s, first, reinterpret_cast<const unsigned char*>(cut), a.V, sc, tid, NT);
+        slice_stats<DT, TAIL>(r, s, first, reinterpret_cast<const unsigned char*>(cut), L.G, a.V, sc, tid, NT);
         const MS w = ms_warp(r.result(), sc);
         if (lane == 0) rec[warp] = w;
     }
@@ -586,7 +617,7 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
     float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
     MS top{-INFINITY, 0.f};
     if (OP == LM_DISTILL) {
-        teacher_weights(a, teacher_entries(a, row, eq, eid), eq, Q, B);
+        teacher_weights(a, teacher_entries<DT, 4>(a, row, s.e0, s.e0 + s.ng * N, x, ex, eq, eid), eq, Q, B);
         if constexpr (TAIL) {
             for (int i = lane; i < R * 8; i += 32) cut[i] = 0u;
             __syncwarp();
@@ -654,7 +685,7 @@ struct LmRowPlan {
 template <int DT, int OP, int NW, bool TAIL>
 cudaError_t launch_row_n(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaunch& L, cudaStream_t st) {
     auto kern = lm_row_kernel<DT, OP, NW, TAIL>;
-    if (p.smem > 48 * 1024) {
+    if (p.smem > 40 * 1024) {  // 48 KB with the static part need no leave
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
         if (e != cudaSuccess) return e;
     }

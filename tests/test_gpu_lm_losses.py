@@ -604,3 +604,18 @@ def test_balance_loss_of_offset_logits(sot, T, E, dtype, empty):
         assert np.all(np.abs(host(loss) - rl) <= ATOL * np.abs(rl))
     fine = (some | ~mask).numpy()
     close_grad(grad[torch.from_numpy(fine).cuda()], rg[fine], size[fine], dtype)
+
+
+@pytest.mark.parametrize("V", [1384698, 1566394])
+def test_tail_marks_near_the_default_shared_memory(sot, V):
+    """Rows whose marks fill a CTA's shared memory to just below what needs no special leave."""
+    T, K = 2, 8
+    x = rows(T, V, "f32", 0, 3)
+    rng = np.random.default_rng(V)
+    ids = np.stack([np.sort(rng.permutation(V)[:K]) for _ in range(T)])
+    z = torch.log_softmax(torch.randn(T, K, generator=torch.Generator().manual_seed(1)), 1) - 0.2
+    zt, w = z.cuda(), torch.ones(T).cuda()
+    loss, grad = sot.sot_distill_topk(x, torch.from_numpy(ids).cuda(), zt, weight=w, tail=True)
+    rl, rg, size = R.distill(host(x), ids, host(zt), host(w), 1.0, True)
+    close(loss, rl, scale=4.0, size=64.0)
+    close_grad(grad, rg, size, "f32")
