@@ -204,13 +204,14 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
             }
         };
         // Weights against 0; where their sum leaves the middle of the range, the row is
-        // read again and its weights are formed against its maximum.
+        // read again and its weights are formed against its maximum.  (A sum of 2^-10 loses
+        // probabilities below 2^-116.)
         float m = 0.f, u = 0.f, s, d;
         bool far = false;
 #pragma unroll
         for (int i = 0; i < H; ++i) x[i] = ex2_pair(x[i], 0.f, SOT_LOG2E);
         add_up(s, d);
-        const bool again = now && !(s > 0x1p-40f && s < 0x1p24f);
+        const bool again = now && !(s > 0x1p-10f && s < 0x1p24f);
         if (__any_sync(0xffffffffu, again)) {
             const float s0 = s, d0 = d;
             if (again) {

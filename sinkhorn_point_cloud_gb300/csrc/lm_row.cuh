@@ -46,18 +46,32 @@ struct LmRowLaunch {
     int CL, G;  // CTAs a row, granules a slice
 };
 
+// Sums against the guessed stabiliser 0 may be as small as 2^-40, and weights that are
+// formed against it again would vanish where probabilities are still 2^-86.  For such a sum,
+// k = floor(log2 s) is the better stabiliser, and an exact one; returns 2^k.
+__device__ __forceinline__ float small_sum(float m, float s, float& k) {
+    const bool small = m == 0.f && s > 0.f && s < 1.f;
+    const uint32_t e = __float_as_uint(s) & 0x7f800000u;
+    k = small ? (float)((int)(e >> 23) - 127) : 0.f;
+    return small ? __uint_as_float(e) : 1.f;
+}
+
 // What the row's threads need once its statistics are known.
 struct RowCoef {
     float u, c;      // dx_v = c exp2(x_v sc - u)
     float far;       // not 0: u overflows, and dx_v = c where x_v = m, 0 elsewhere
     float m;
-    float M, inv_S;  // p_v = weight of x_v against M times inv_S
+    float M, inv_S;  // p_v = weight of x_v against M times inv_S;
+    float k;         // k < 0: weight of x_v is exp2(x_v sc - k) instead
     float fa, fb;    // a corrected column: fa p_v - fb q_v
     __device__ __forceinline__ void set(float v, float sc) {
         const float v2 = __fmul_rn(v, sc);
         m = v;
         far = fabsf(v2) < INFINITY ? 0.f : 1.f;
         u = far != 0.f ? 0.f : v2;
+    }
+    __device__ __forceinline__ float prob(float x, float sc) const {
+        return (k < 0.f ? ex2f(fmaf(x, sc, -k)) : weight_of(x, M, sc)) * inv_S;
     }
 };
 
@@ -222,8 +236,10 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
     const float2 ln2 = make_float2(0.693147182f, -1.904654212e-9f);
     RowCoef c;
     c.M = all.m;
-    c.inv_S = __frcp_rn(all.s);
+    const float inv = __frcp_rn(all.s);
+    c.inv_S = inv * small_sum(all.m, all.s, c.k);
     c.set(all.m, sc);
+    if (c.k < 0.f) c.u = c.k;
     if (OP == LM_DISTILL) {
         const float wt = m.w * a.tau;
         float qr = 0.f;
@@ -234,8 +250,11 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
             // no column outside the entries: no tail outcome
             qr = r.s == 0.f ? 0.f : r.s > 0.f ? fmaxf(0.f, (1.f - Q.x) - Q.y) : r.s;
             c.fa = wt * (Q.x + qr);
+            float k;
+            const float two_k = small_sum(r.m, r.s, k);
             c.set(r.m, sc);
-            c.c = r.s == 0.f ? 0.f : wt * ((Q.x + qr) * rescale(r.m, c.M, sc) * c.inv_S - qr / r.s);
+            if (k < 0.f) c.u = k;
+            c.c = r.s == 0.f ? 0.f * inv : wt * ((Q.x + qr) * rescale(r.m, c.M, sc) * inv - qr / r.s) * two_k;
         }
         publish(c);
         if (write && a.loss) {
@@ -573,9 +592,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
     const RowCoef c = coef;
     if (OP == LM_DISTILL) {
         for (int k = tid; k < a.K; k += NT + 32)
-            if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * (weight_of(ex[k], c.M, sc) * c.inv_S) - c.fb * eq[k]);
+            if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * c.prob(ex[k], sc) - c.fb * eq[k]);
     } else if (tid == NT && m.tgt >= c0 && m.tgt < c1)
-        grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(xt, c.M, sc) * c.inv_S) - c.fb);
+        grow[m.tgt] = Elem<DT>::put(c.fa * c.prob(xt, sc) - c.fb);
 }
 
 // Short rows: one warp takes a row, R granules a lane, and keeps them in registers,
@@ -670,9 +689,9 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
         __syncwarp();  // the corrections come after the columns they replace
         if (OP == LM_DISTILL) {
             for (int k = lane; k < a.K; k += 32)
-                if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * (weight_of(ex[k], c.M, sc) * c.inv_S) - c.fb * eq[k]);
+                if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * c.prob(ex[k], sc) - c.fb * eq[k]);
         } else if (lane == 0)
-            grow[m.tgt] = Elem<DT>::put(c.fa * (weight_of(D.x, c.M, sc) * c.inv_S) - c.fb);
+            grow[m.tgt] = Elem<DT>::put(c.fa * c.prob(D.x, sc) - c.fb);
     }
 }
 

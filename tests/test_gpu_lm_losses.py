@@ -619,3 +619,41 @@ def test_tail_marks_near_the_default_shared_memory(sot, V):
     rl, rg, size = R.distill(host(x), ids, host(zt), host(w), 1.0, True)
     close(loss, rl, scale=4.0, size=64.0)
     close_grad(grad, rg, size, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(3, 100), (200, 1000), (3, 5003), (200, 5003), (2, 60000)])
+@pytest.mark.parametrize("level", [-10.0, -19.0, -26.0])
+def test_small_probabilities_of_low_logits(sot, T, V, dtype, level):
+    """Rows whose exponentials sum to as little as 2^-40: probabilities down to 2^-115 are still there."""
+    g = torch.Generator().manual_seed(V)
+    x = (level - 80.0 * torch.rand(T, V, generator=g)).to(TYPES[dtype]).cuda()
+    x[:, 0] = level
+    tg = torch.ones(T, dtype=torch.int64).cuda()
+    ones, zero = torch.ones(T).cuda(), torch.zeros(T).cuda()
+    lp, _ = R.token_logprob(host(x), tg.cpu().numpy(), 1.0)
+    old = torch.from_numpy(lp.astype(np.float32)).cuda()
+    _, _, _, grad = sot.sot_policy_loss(x, tg, old, ones, weight=ones)
+    rg, size = R.token_grad(host(x), tg.cpu().numpy(), 1.0, -np.exp(lp - host(old)))
+    close_grad(grad, rg, size, dtype)
+    ids = torch.tensor([[5, 2, 70]] * T).cuda()
+    z = torch.tensor([[-1.0, -2.0, -80.0]] * T).cuda()
+    for tail in (False, True):
+        _, grad = sot.sot_distill_topk(x, ids, z, weight=ones, tail=tail)
+        _, rg, size = R.distill(host(x), ids.cpu().numpy(), host(z), host(ones), 1.0, tail)
+        close_grad(grad, rg, size, dtype)
+    if V <= 1000:
+        ids = torch.zeros(T, 1, dtype=torch.int32)
+        _, _, grad = sot.sot_balance_loss(x, ids.cuda(), balance_coef=1.0, z_coef=1.0)
+        _, _, rg, size = R.balance(host(x), ids.numpy(), None, 1.0, 1.0)
+        # (a balance row of sum 2^-10 loses what lies below 2^-116)
+        close_grad(grad, rg, size + 2.0 ** -102, dtype)
+
+
+def test_tail_of_masked_rows_is_nan(sot):
+    """A row in use whose logits are all -inf gives NaN, with and without used entries."""
+    for V in (1, 7, 700, 40000):
+        x = torch.full((3, V), float("-inf")).cuda()
+        ids = torch.tensor([[0], [-1], [V - 1]]).cuda()
+        _, grad = sot.sot_distill_topk(x, ids, torch.full((3, 1), -0.5).cuda(), weight=torch.ones(3).cuda(), tail=True)
+        assert torch.isnan(grad).all()
