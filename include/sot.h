@@ -334,7 +334,7 @@ int sot_token_logprob(const void* logits, long long T, int V, long long ld, int 
  * Its gradient, from the lse that sot_token_logprob wrote:
  *   grad[t][v] = grad_logp[t] / temperature * ([v = target[t]] - p_v)
  * Rows left out, and rows with grad_logp = 0, are written as zeros without
- * being read.
+ * being read.  The probabilities are as good as the lse: 2^-24 of its size.
  */
 int sot_token_logprob_grad(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
                            const void* target, int target_type, const float* lse, const float* grad_logp, void* grad,

@@ -31,8 +31,14 @@ __global__ void __launch_bounds__(GRAD_NT) lm_grad_kernel(const LmGradArgs a, in
     const int tgt = load_index(a.target, a.target_type, row, a.V);
     const float g = tgt >= 0 ? a.g[row] / a.tau : 0.f;
     const float sc = SOT_LOG2E / a.tau;
-    const float u = a.lse[row] * SOT_LOG2E;  // log2 p = x sc - u
-    const bool far = !(fabsf(u) < INFINITY);
+    const float lse = a.lse[row], u = lse * SOT_LOG2E;  // log2 p = x sc - u
+    // Far from 0 the rounding of u would show: the difference comes first there.  What
+    // lse itself has lost (2^-24 of it) can leave p too large, but not above 1.
+    const bool far = !(fabsf(u) < 0x1p10f);
+    const auto prob = [&](float x) {
+        const float d = (x - lse * a.tau) / a.tau;
+        return expf(d > 0.f ? 0.f : d);
+    };
     const uint64_t policy = policy_drop();
     const auto finish = [&](float2 (&f)[N / 2], int c) {  // columns c ..
         const bool here = (unsigned)(tgt - c) < (unsigned)N;
@@ -40,7 +46,7 @@ __global__ void __launch_bounds__(GRAD_NT) lm_grad_kernel(const LmGradArgs a, in
         for (int j = 0; j < N / 2; ++j) {
             float2 p;
             if (!far) p = ex2_pair(f[j], u, sc);
-            else p = make_float2(expf((f[j].x - a.lse[row] * a.tau) / a.tau), expf((f[j].y - a.lse[row] * a.tau) / a.tau));
+            else p = make_float2(prob(f[j].x), prob(f[j].y));
             f[j] = p;
         }
         if (here) {

@@ -227,7 +227,7 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
             m = group_max(m, lanes);
             if (again) {
                 u = __fmul_rn(m, SOT_LOG2E);
-                far = !(fabsf(u) < INFINITY);
+                far = is_far(u);
                 if (far) u = 0.f;
 #pragma unroll
                 for (int i = 0; i < H; ++i)

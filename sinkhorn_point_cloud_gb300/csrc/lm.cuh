@@ -229,16 +229,22 @@ __device__ __forceinline__ bool same_granules(const T* x, const T* g) {
 struct MS {
     float m, s;
 };
+// Whether a stabiliser is so far from 0 (m2 its rounded product with sc) that floats next to
+// it lie 2^6 or more apart in the exponent: then only the logits equal to it count.
+// Below that, m2 is off by 2^5 at most, which all weights share.
+__device__ __forceinline__ bool is_far(float m2) { return !(fabsf(m2) < 0x1p30f); }
+// (infinite x and m are not equal here: such a row has no sum)
+__device__ __forceinline__ float equal_weight(float x, float m) { return x - m == 0.f ? 1.f : x != x ? x : 0.f; }
 // Weight of a logit x against stabiliser m.
 __device__ __forceinline__ float weight_of(float x, float m, float sc) {
     const float m2 = __fmul_rn(m, sc);
-    if (fabsf(m2) < INFINITY) return ex2f(fmaf(x, sc, -m2));
-    return x - m == 0.f ? 1.f : 0.f;
+    if (!is_far(m2)) return ex2f(fmaf(x, sc, -m2));
+    return equal_weight(x, m);
 }
 // Factor that takes sums against stabiliser m to stabiliser M >= m.
 __device__ __forceinline__ float rescale(float m, float M, float sc) {
     const float M2 = __fmul_rn(M, sc);
-    if (fabsf(M2) < INFINITY) return ex2f(__fsub_rn(__fmul_rn(m, sc), M2));  // not fused: the rounded products
+    if (!is_far(M2)) return ex2f(__fsub_rn(__fmul_rn(m, sc), M2));  // not fused: the rounded products
     return m - M == 0.f ? 1.f : 0.f;
 }
 __device__ __forceinline__ MS ms_combine(MS a, MS b, float sc) {
@@ -263,8 +269,7 @@ __device__ __forceinline__ float2 ex2_pair(float2 x, float u, float sc) {
 }
 
 // A thread's running statistics: s (in two halves) against stabiliser m, u = m sc
-// where that is finite; `far` where it is not (s then counts the logits equal to
-// m).  Nothing needs m to be the largest value, only the sums to stay clear of
+// rounded; where that is far from 0, s counts the logits equal to m.  Nothing needs m to be the largest value, only the sums to stay clear of
 // overflow and underflow, and logits seldom leave the range where the first
 // guess, 0, does that.  So a batch is summed against the m at hand, with no
 // maximum to wait for, and only a batch whose sum comes out beyond 2^24 or
@@ -285,7 +290,7 @@ struct Running {
         } else {
 #pragma unroll
             for (int i = 0; i < Elem<DT>::N / 2; ++i)
-                t = fadd2(t, make_float2(f[i].x - m == 0.f ? 1.f : 0.f, f[i].y - m == 0.f ? 1.f : 0.f));
+                t = fadd2(t, make_float2(equal_weight(f[i].x, m), equal_weight(f[i].y, m)));
         }
         return t;
     }
@@ -297,8 +302,9 @@ struct Running {
             const float k = none ? 0.f : rescale(m, mx, sc), v = __fmul_rn(mx, sc);
             s = fmul2(s, make_float2(k, k));
             m = mx;
-            far = !(fabsf(v) < INFINITY);
+            far = is_far(v);
             u = far ? 0.f : v;
+            if (mx == INFINITY) s = make_float2(NAN, 0.f);  // and stays
         }
     }
     template <int DT, int P>

@@ -59,7 +59,7 @@ __device__ __forceinline__ float small_sum(float m, float s, float& k) {
 // What the row's threads need once its statistics are known.
 struct RowCoef {
     float u, c;      // dx_v = c exp2(x_v sc - u)
-    float far;       // not 0: u overflows, and dx_v = c where x_v = m, 0 elsewhere
+    float far;       // not 0: dx_v = c where x_v = m, 0 elsewhere
     float m;
     float M, inv_S;  // p_v = weight of x_v against M times inv_S;
     float k;         // k < 0: weight of x_v is exp2(x_v sc - k) instead
@@ -67,7 +67,7 @@ struct RowCoef {
     __device__ __forceinline__ void set(float v, float sc) {
         const float v2 = __fmul_rn(v, sc);
         m = v;
-        far = fabsf(v2) < INFINITY ? 0.f : 1.f;
+        far = is_far(v2) ? 1.f : 0.f;
         u = far != 0.f ? 0.f : v2;
     }
     __device__ __forceinline__ float prob(float x, float sc) const {
@@ -232,7 +232,7 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
     // log(sum exp(x / tau)) = m2 ln 2 + log s with the rounded m2 that the sums
     // were formed with; where m2 overflows, m / tau + log s
     const float m2 = __fmul_rn(all.m, sc);
-    const bool far = !(fabsf(m2) < INFINITY);
+    const bool far = is_far(m2);
     const float2 ln2 = make_float2(0.693147182f, -1.904654212e-9f);
     RowCoef c;
     c.M = all.m;
@@ -293,7 +293,7 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
     const float2 logS = log_ff(all.s), minus = make_float2(-logS.x, -logS.y);
     const float2 t = two_prod(D.x, sc), ts = two_sum(t.x, -m2);
     float2 logp = ff_add(ff_mul(ff_renorm(ts.x, ts.y + t.y), ln2), minus);
-    if (!(fabsf(logp.x) < INFINITY)) logp = make_float2((float)(((double)D.x - (double)all.m) * a.inv_tau) - logS.x, 0.f);
+    if (far || !(fabsf(logp.x) < INFINITY)) logp = make_float2((float)(((double)D.x - (double)all.m) * a.inv_tau) - logS.x, 0.f);
     float g = 0.f, loss = 0.f, kl = 0.f;
     if (OP == LM_POLICY) {
         const float2 d0 = two_sum(logp.x, -m.old);

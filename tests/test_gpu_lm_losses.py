@@ -657,3 +657,88 @@ def test_tail_of_masked_rows_is_nan(sot):
         ids = torch.tensor([[0], [-1], [V - 1]]).cuda()
         _, grad = sot.sot_distill_topk(x, ids, torch.full((3, 1), -0.5).cuda(), weight=torch.ones(3).cuda(), tail=True)
         assert torch.isnan(grad).all()
+
+
+LEVELS = {"f32": [-1e4, -1e9, 3e9, -1e10, -1e20, 1e30, -1.7e38, -3.4028234663852886e38], "f16": [-65504.0, 3e4],
+          "bf16": [-1e4, -1e9, -1e10, -1.7e38, -3.3895313892515355e38]}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("V", [6, 100, 1000, 5003, 60000])
+@pytest.mark.parametrize("tau", [1.0, 2.0, 0.7])
+def test_rows_at_one_level(sot, V, dtype, tau):
+    """Rows whose columns all hold one value however large, and rows where half of them are far below it."""
+    levels = LEVELS[dtype]
+    T = 2 * len(levels)
+    x = torch.empty(T, V, dtype=TYPES[dtype])
+    for i, c in enumerate(levels):
+        x[2 * i:2 * i + 2] = c
+        if c > -3e38 and dtype != "f16":
+            x[2 * i + 1, V // 2:] = c * 1.5 if c < 0 else c / 1.5
+    x = x.cuda()
+    n = (x == x[:, :1]).sum(1).double().cpu().numpy()
+    tg, ones = torch.ones(T, dtype=torch.int64).cuda(), torch.ones(T).cuda()
+    p = np.where(host(x) == host(x)[:, :1], 1.0 / n[:, None], 0.0)
+    lp = torch.from_numpy(-np.log(n).astype(np.float32)).cuda()
+
+    logp, lse = sot.sot_token_logprob(x, tg, temperature=tau)
+    close(logp, -np.log(n), scale=4.0)
+    with np.errstate(over="ignore"):
+        want = (host(x)[:, 0] / tau + np.log(n)).astype(np.float32).astype(np.float64)
+    close(lse, want, size=2.0 * np.where(np.isfinite(want), np.abs(want), 0.0))
+    # the gradient from the stored lse knows p to 2^-24 |lse| only, and stays below 1
+    grad = host(sot.sot_token_logprob_grad(x, tg, lse, ones, temperature=tau))
+    assert (np.abs(grad) * tau <= 1.0 + 2.0 ** -7).all()
+
+    _, _, _, grad = sot.sot_policy_loss(x, tg, lp, ones, weight=ones, temperature=tau)
+    ref = p.copy()
+    ref[:, 1] -= 1.0
+    close_grad(grad, ref / tau, (p + 1.0) / tau, dtype)
+    ids, z = torch.tensor([[1, 4]] * T).cuda(), torch.tensor([[-1.0, -2.0]] * T).cuda()
+    q = np.exp([-1.0, -2.0])
+    loss, grad = sot.sot_distill_topk(x, ids, z, weight=ones, temperature=tau)
+    qn = np.exp(np.array([-1.0, -2.0]) / tau) / np.exp(np.array([-1.0, -2.0]) / tau).sum()
+    ref = tau * p
+    ref[:, [1, 4]] -= tau * qn
+    close_grad(grad, ref, tau * (p + 1.0), dtype)
+    if tau == 1.0:
+        loss, grad = sot.sot_distill_topk(x, ids, z, weight=ones, tail=True)
+        rest = p.copy()
+        rest[:, [1, 4]] = 0.0
+        pr = rest.sum(1, keepdims=True)
+        used = pr[:, 0] > 0  # the others' rest is one that does not show in 64 bits either
+        ref = p - (1.0 - q.sum()) * rest / np.where(pr > 0, pr, 1.0)
+        ref[:, [1, 4]] -= q
+        close_grad(grad[torch.from_numpy(used).cuda()], ref[used], p[used] + 2.0, dtype)
+        if V <= 1000 and dtype != "f16":
+            cid = torch.zeros(T, 1, dtype=torch.int32)
+            counts, _, grad = sot.sot_balance_loss(x, cid.cuda(), balance_coef=1.0)
+            f = np.zeros(V)
+            f[0] = V
+            dot = p @ f
+            close_grad(grad, p * (f - dot[:, None]) / T, p * (f + dot[:, None]) / T, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("V", [6, 100, 1000, 5003, 60000])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("masked", [False, True])
+def test_one_bad_logit_spoils_its_row(sot, V, dtype, bad, masked):
+    T = 200
+    x = rows(T, V, dtype, 3, seed=V)
+    if masked:
+        x[::2] = torch.finfo(x.dtype).min
+    x[::2, V // 3] = bad
+    tg, ones = torch.zeros(T, dtype=torch.int64).cuda(), torch.ones(T).cuda()
+    spoilt = torch.arange(T).cuda() % 2 == 0
+    logp, lse = sot.sot_token_logprob(x, tg)
+    assert torch.equal(torch.isnan(logp), spoilt) and torch.equal(torch.isnan(lse), spoilt)
+    loss, _, _, grad = sot.sot_policy_loss(x, tg, torch.nan_to_num(logp), ones, weight=ones)
+    assert torch.equal(torch.isnan(loss), spoilt) and torch.equal(torch.isnan(grad).any(1), spoilt)
+    ids, z = torch.tensor([[1, 4]] * T).cuda(), torch.tensor([[-1.0, -2.0]] * T).cuda()
+    for tail in (False, True):
+        loss, grad = sot.sot_distill_topk(x, ids, z, weight=ones, tail=tail)
+        assert torch.equal(torch.isnan(loss), spoilt) and torch.equal(torch.isnan(grad).any(1), spoilt)
+    if V <= 1000:
+        _, _, grad = sot.sot_balance_loss(x, ids.int(), z_coef=1.0)
+        assert torch.equal(torch.isnan(grad).any(1), spoilt)
