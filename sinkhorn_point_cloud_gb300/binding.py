@@ -404,10 +404,9 @@ def sot_plan_coo_operands(X, Y, a, b, f, g, eps, threshold=1e-8, stream=None):
     dev = X.device
     _potentials_args(f, g, B, n, m, dev)
     L = load()
-    out = dict(xc=torch.empty(B, n, d, device=dev), lwx=torch.empty(B, n, device=dev),
-               Lx=torch.empty(B, n, device=dev), yc=torch.empty(B, m, d, device=dev),
-               lwy=torch.empty(B, m, device=dev), Ly=torch.empty(B, m, device=dev),
-               Mr=torch.empty(B, n, device=dev), Mc=torch.empty(B, m, device=dev))
+    new = lambda *shape: torch.empty(*shape, device=dev, dtype=torch.float32)  # noqa: E731
+    out = dict(xc=new(B, n, d), lwx=new(B, n), Lx=new(B, n), yc=new(B, m, d), lwy=new(B, m), Ly=new(B, m), Mr=new(B, n),
+               Mc=new(B, m))
     sc = (C.c_float * 2)()
     rc = L.sot_plan_coo_operands(_ptr(X), _ptr(Y), _ptr(a), _ptr(b), B, n, m, d, _ptr(f), _ptr(g), float(eps),
                                  float(threshold), *(_ptr(out[k]) for k in ("xc", "lwx", "Lx", "yc", "lwy", "Ly",
@@ -541,7 +540,7 @@ def sot_token_logprob(logits, target, temperature=1.0, logp=None, lse=None, stre
     _floats(lse, "lse", T, dev)
 
     def call(s):
-        p = torch.empty(T, device=logits.device) if logp is None else logp
+        p = torch.empty(T, dtype=_F32, device=logits.device) if logp is None else logp
         q = torch.empty_like(p) if lse is None else lse
         rc = load().sot_token_logprob(x, T, V, ld, dt, temperature, tg, ty, p.data_ptr(), q.data_ptr(), s)
         if rc:
@@ -582,7 +581,7 @@ def sot_distill_topk(logits, ids, teacher, weight=None, temperature=1.0, tail=Fa
     _floats(loss, "loss", T, dev)
 
     def call(s):
-        lo = torch.empty(T, device=logits.device) if loss is None else loss
+        lo = torch.empty(T, dtype=_F32, device=logits.device) if loss is None else loss
         g, at, ldg = _grad_of(grad, logits, T, V, ld, dt, dev)
         rc = load().sot_distill_topk(x, T, V, ld, dt, temperature, i, ty, z, tt, K, 1 if tail else 0, w, lo.data_ptr(), at,
                                      ldg, s)
@@ -637,7 +636,7 @@ def sot_preference_loss(logp, offsets, ref_logp=None, target=None, beta=0.1, lab
         scale = 1.0 / max(P, 1)
 
     def call(s):
-        loss = torch.empty(P, device=logp.device)
+        loss = torch.empty(P, dtype=_F32, device=logp.device)
         margin, g = torch.empty_like(loss), torch.empty_like(logp)
         rc = load().sot_preference_loss(lp, ref, tg, ty, off, P, T, beta, label_smoothing, 1 if average else 0, scale,
                                         loss.data_ptr(), margin.data_ptr(), g.data_ptr(), s)
@@ -657,7 +656,7 @@ def sot_balance_loss(logits, ids, mask=None, balance_coef=1.0, z_coef=0.0, grad=
 
     def call(s):
         counts = torch.empty(E, dtype=torch.int32, device=logits.device)
-        loss = torch.empty(2, device=logits.device)
+        loss = torch.empty(2, dtype=_F32, device=logits.device)
         g, at, ldg = _grad_of(grad, logits, T, E, ld, dt, dev)
         rc = load().sot_balance_loss(x, T, E, ld, dt, i, ty, K, m, balance_coef, z_coef, counts.data_ptr(),
                                      loss.data_ptr(), at, ldg, s)
