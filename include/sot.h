@@ -357,6 +357,7 @@ int sot_token_logprob_grad(const void* logits, long long T, int V, long long ld,
  *   grad = d(sum_t loss) / d logits (NULL: losses only; loss may be NULL instead).
  * weight NULL = 1/T.  A row of weight 0 is left out: not read, loss and gradient 0.
  * A row without used entries has loss 0 and, without tail, gradient 0.
+ * A used entry whose teacher value is NaN or +inf makes its row's loss and gradient NaN.
  * SOT_ERR_UNSUPPORTED with tail = 1 above 12 million 16-bit or 6 million 32-bit
  * columns (a mark for each 16 bytes of a row is kept in shared memory).
  */

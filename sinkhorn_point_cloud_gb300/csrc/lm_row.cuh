@@ -247,14 +247,15 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
         c.fb = wt;
         c.c = c.fa * c.inv_S;
         if (a.tail) {
-            // no column outside the entries: no tail outcome
-            qr = r.s == 0.f ? 0.f : r.s > 0.f ? fmaxf(0.f, (1.f - Q.x) - Q.y) : r.s;
+            // no column outside the entries: no tail outcome (a NaN of the entries stays one)
+            const float rest = (1.f - Q.x) - Q.y;
+            qr = r.s == 0.f ? 0.f : r.s > 0.f ? (rest <= 0.f ? 0.f : rest) : r.s;
             c.fa = wt * (Q.x + qr);
             float k;
             const float two_k = small_sum(r.m, r.s, k);
             c.set(r.m, sc);
             if (k < 0.f) c.u = k;
-            c.c = r.s == 0.f ? 0.f * inv : wt * ((Q.x + qr) * rescale(r.m, c.M, sc) * inv - qr / r.s) * two_k;
+            c.c = r.s == 0.f ? 0.f * inv * c.fa : wt * ((Q.x + qr) * rescale(r.m, c.M, sc) * inv - qr / r.s) * two_k;
         }
         publish(c);
         if (write && a.loss) {
@@ -262,7 +263,7 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
             const bool tail = a.tail && !(qr <= 0.f);
             const float2 logS = log_ff(all.s), logR = tail ? log_ff(r.s) : logS, logq = tail ? log_ff(qr) : logS;
             float2 sum = make_float2(0.f, 0.f);
-            if (Q.x > 0.f) {  // B + Q log s - (D sc - Q m2) ln 2
+            if (!(Q.x <= 0.f)) {  // B + Q log s - (D sc - Q m2) ln 2; NaN where a used entry is NaN or +inf
                 const float2 d = ff_add(ff_mul(D, make_float2(sc, 0.f)), ff_mul(Q, make_float2(-m2, 0.f)));
                 sum = ff_add(ff_add(B, ff_mul(Q, logS)), ff_mul(d, make_float2(-ln2.x, -ln2.y)));
             }
@@ -275,7 +276,7 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
             if (far || !(fabsf(loss) < INFINITY)) {  // with the range of a double
                 const double q = to_double(Q), k = 0.69314718055994530942;
                 double l = 0.0;
-                if (q > 0.0)
+                if (!(q <= 0.0))
                     l = to_double(B) + q * to_double(logS) -
                         (far ? (to_double(D) - q * (double)all.m) * a.inv_tau : (to_double(D) * (double)sc - q * (double)m2) * k);
                 if (tail) {

@@ -61,3 +61,39 @@ def test_outputs_are_float32_under_any_default_type(sot, default):
         torch.set_default_dtype(before)
     for a, b in zip(got, want):
         assert a.dtype == b.dtype and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("bad,tt", [(NAN, "f32"), (INF, "f32"), (NAN, "bf16"), (INF, "f16")])
+@pytest.mark.parametrize("T,V,K", [(6, 50, 4), (200, 3000, 70), (6, 50021, 40), (200, 5003, 8)])
+def test_a_bad_teacher_value_spoils_its_row(sot, T, V, K, bad, tt, tail):
+    x = rows(T, V, "bf16", 0, V)
+    rng = np.random.default_rng(V)
+    ids = torch.from_numpy(np.stack([rng.permutation(V)[:K] for _ in range(T)])).cuda()
+    z = torch.log_softmax(torch.randn(T, K, generator=torch.Generator().manual_seed(1)), 1).sub(0.3).to(TYPES[tt]).cuda()
+    w = torch.ones(T).cuda()
+    ids[1, 0] = -1  # unused: what it holds does not count
+    w[2] = 0.0      # left out
+    want = sot.sot_distill_topk(x, ids, z, weight=w, tail=tail)
+    z[1, 0] = bad
+    z[2, 1] = bad
+    spoilt = torch.arange(T).cuda() % 3 == 0
+    z[spoilt, torch.arange(T).cuda()[spoilt] % K] = bad
+    loss, grad = sot.sot_distill_topk(x, ids, z, weight=w, tail=tail)
+    only, _ = sot.sot_distill_topk(x, ids, z, weight=w, tail=tail, grad=False)
+    for got in (loss, only):
+        assert torch.isnan(got[spoilt]).all() and torch.equal(got[~spoilt], want[0][~spoilt])
+    assert torch.isnan(grad[spoilt]).all() and torch.equal(grad[~spoilt], want[1][~spoilt])
+
+
+@pytest.mark.parametrize("V", [60, 40000])
+def test_a_bad_teacher_value_where_nothing_else_is_left(sot, V):
+    """Every column outside the entries masked: the rest takes no part, the row's loss and gradient are NaN all the same."""
+    x = torch.full((3, V), -INF).cuda()
+    ids = torch.tensor([[3, 20, 41]] * 3).cuda()
+    x[:, ids[0]] = 0.5
+    z = torch.tensor([[-1.0, -2.0, -3.0], [-1.0, NAN, -3.0], [-1.0, -2.0, INF]]).cuda()
+    for tail in (False, True):
+        loss, grad = sot.sot_distill_topk(x, ids, z, weight=torch.ones(3).cuda(), tail=tail)
+        assert torch.isfinite(loss[0]) and torch.isfinite(grad[0]).all()
+        assert torch.isnan(loss[1:]).all() and torch.isnan(grad[1:]).all()
