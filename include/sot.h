@@ -393,8 +393,9 @@ int sot_policy_loss(const void* logits, long long T, int V, long long ld, int dt
  *   grad_logp[t] = scale d(sum_p loss) / d logp[t]
  * With target given, a token whose target is negative takes no part (and is not
  * counted by the means).  Tokens of no sequence get gradient 0.  Sums are formed
- * in pairs of floats, to about 48 bits.  Outputs may be NULL, not all of them.  The gradient goes on to the
- * logits through sot_token_logprob_grad.
+ * in pairs of floats, to about 48 bits.  A log-probability of -inf makes its sum -inf and the margin infinite
+ * (NaN where both sums are); losses and gradients follow from that.  Outputs may be NULL, not all of them.  The
+ * gradient goes on to the logits through sot_token_logprob_grad.
  */
 int sot_preference_loss(const float* logp, const float* ref_logp, const void* target, int target_type,
                         const long long* offsets, int P, long long T, float beta, float label_smoothing, int average,

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(PREF_NT) lm_preference_kernel(const LmPrefArgs
         n[h] = 0;
         for (long long t = off[h] + tid; t < off[h + 1]; t += PREF_NT) {
             if (a.target && load_index(a.target, a.target_type, t, 0x7fffffff) < 0) continue;
-            v[h] = ff_add(v[h], two_sum(a.logp[t], a.ref_logp ? -a.ref_logp[t] : 0.f));
+            v[h] = ff_add_or_far(v[h], two_sum(a.logp[t], a.ref_logp ? -a.ref_logp[t] : 0.f));
             ++n[h];
         }
     }

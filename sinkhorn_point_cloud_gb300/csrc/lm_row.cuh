@@ -162,7 +162,13 @@ __device__ __forceinline__ void teacher_weights(const LmRowArgs& a, float zmax, 
     }
 }
 
-// Sum over a warp; a sum that is not finite goes without its low parts.
+// s + v; a sum that is not finite goes without its low part (which would be NaN), so that an
+// infinity stays one whatever is added after it.
+__device__ __forceinline__ float2 ff_add_or_far(float2 s, float2 v) {
+    const float f = s.x + v.x;
+    return fabsf(f) < INFINITY ? ff_add(s, v) : make_float2(f, 0.f);
+}
+// Sum over a warp, with the same exception.
 __device__ __forceinline__ float2 ff_sum_or_far(float2 v) {
     const float2 s = ff_warp_sum(v);
     const float f = warp_sum(v.x);

@@ -97,3 +97,43 @@ def test_a_bad_teacher_value_where_nothing_else_is_left(sot, V):
         loss, grad = sot.sot_distill_topk(x, ids, z, weight=torch.ones(3).cuda(), tail=tail)
         assert torch.isfinite(loss[0]) and torch.isfinite(grad[0]).all()
         assert torch.isnan(loss[1:]).all() and torch.isnan(grad[1:]).all()
+
+
+@pytest.mark.parametrize("average", [False, True])
+@pytest.mark.parametrize("smoothing", [0.0, 0.1])
+@pytest.mark.parametrize("at", [0, 31, 300, -1])
+def test_preference_with_a_token_of_no_probability(sot, average, smoothing, at):
+    """A log-probability of -inf leaves the losses and gradients that the definition gives."""
+    rng = np.random.default_rng(5)
+    lens = rng.integers(301, 700, 12)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    T, P, beta, scale = off[-1], 6, 0.3, 0.5
+    logp, ref = (-3 * rng.random(T)).astype(np.float32), (-3 * rng.random(T)).astype(np.float32)
+    tg = rng.integers(0, 100, T)
+
+    def put(a, seq, value):
+        a[off[seq + 1] - 1 if at < 0 else off[seq] + at] = value
+    put(logp, 3, -INF)   # pair 1: in the rejected answer
+    put(logp, 4, -INF)   # pair 2: in the chosen one
+    put(logp, 6, -INF)   # pair 3: in both
+    put(logp, 7, -INF)
+    put(logp, 8, -INF)   # pair 4: at a token that takes no part
+    put(tg, 8, -100)
+    put(ref, 10, -INF)   # pair 5: the reference model rules a chosen token out
+    loss, margin, grad = sot.sot_preference_loss(f32(logp), torch.from_numpy(off).cuda(), ref_logp=f32(ref),
+                                                 target=torch.from_numpy(tg).cuda(), beta=beta, label_smoothing=smoothing,
+                                                 average=average, scale=scale)
+    with np.errstate(all="ignore"):
+        rl, rm, rd = R.preference(np.where(np.isinf(logp), 0.0, logp), np.where(np.isinf(ref), 0.0, ref), tg, off, beta,
+                                  smoothing, average, scale)
+    far = INF if smoothing else 0.0
+    for p, m, l, sn in ((1, INF, far, 0.0), (2, -INF, INF, 1.0), (3, NAN, NAN, NAN), (5, INF, far, 0.0)):
+        rm[p], rl[p] = m, l
+        d = scale * beta * (smoothing * (1 - sn) - (1 - smoothing) * sn)
+        for h, s in ((0, d), (1, -d)):
+            i = np.arange(off[2 * p + h], off[2 * p + h + 1])
+            i = i[tg[i] >= 0]
+            rd[i] = s / (len(i) if average else 1)
+    # sums in 64 bits: a few roundings of 32 bits at the end
+    for got, want in ((loss, rl), (margin, rm), (grad, rd)):
+        alike(got, want, 2.0 ** -20 * np.abs(want) + 2.0 ** -22)
