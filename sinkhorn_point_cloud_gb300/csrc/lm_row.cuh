@@ -193,7 +193,7 @@ __device__ __forceinline__ void student_side(const LmRowArgs& a, int c0, int c1,
         }
         const float v = element_of<DT>(ex[k], x + id);
         ex[k] = v;
-        if (eq[k] != 0.f) D = fabsf(v) < INFINITY ? ff_add(D, two_prod(eq[k], v)) : make_float2(D.x + v, 0.f);
+        if (eq[k] != 0.f) D = ff_add_or_far(D, two_prod(eq[k], v));
         top.m = fmaxf(top.m, v);
     }
     D = ff_sum_or_far(D);

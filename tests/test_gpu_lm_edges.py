@@ -137,3 +137,26 @@ def test_preference_with_a_token_of_no_probability(sot, average, smoothing, at):
     # sums in 64 bits: a few roundings of 32 bits at the end
     for got, want in ((loss, rl), (margin, rm), (grad, rd)):
         alike(got, want, 2.0 ** -20 * np.abs(want) + 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,K", [(5, 3000, 33), (5, 3000, 64), (5, 3000, 256), (5, 50021, 33), (5, 50021, 256),
+                                   (200, 5003, 64), (5, 9000, 1024)])
+def test_an_entry_on_a_masked_column_in_any_place(sot, T, V, K, dtype):
+    """A used entry whose column is masked makes the row's loss +inf wherever it stands, and the gradient
+    stays what the definition gives."""
+    x = rows(T, V, dtype, 0, V)
+    rng = np.random.default_rng(K)
+    ids = np.stack([rng.permutation(V)[:K] for _ in range(T)])
+    place = [0, K // 2, K - 33, K - 1]  # row 4, 9, ... is whole
+    for t in range(T):
+        if t % 5 < 4:
+            x[t, ids[t, place[t % 5]]] = -INF
+    z = torch.log_softmax(torch.randn(T, K, generator=torch.Generator().manual_seed(1)), 1).sub(0.3).cuda()
+    w = torch.ones(T).cuda()
+    for tail in (False, True):
+        loss, grad = sot.sot_distill_topk(x, torch.from_numpy(ids).cuda(), z, weight=w, tail=tail)
+        rl, rg, size = R.distill(host(x), ids, host(z), host(w), 1.0, tail)
+        assert np.array_equal(np.isinf(rl), np.arange(T) % 5 < 4)
+        alike(loss, rl, 4.0 * ATOL + RTOL * 64.0)
+        close_grad(grad, rg, size, dtype)
