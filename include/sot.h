@@ -373,6 +373,7 @@ int sot_distill_topk(const void* logits, long long T, int V, long long ld, int d
  *   loss[t] = weight[t] (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef kl)
  *   grad    = d(sum_t loss) / d logits                        (NULL: losses only)
  * old_logp, ref_logp and advantage are [T] and constants of the gradient.
+ * With kl_coef = 0 the KL term takes no part in loss and grad, whatever kl is.
  * weight NULL = 1/T.  A row of weight 0, or whose target lies outside [0, V), is
  * left out: not read, all its outputs 0.  loss, logp, kl and grad may be NULL, not
  * all of them.

@@ -360,7 +360,7 @@ __device__ __forceinline__ float2 ff_warp_sum(float2 v) {
     return v;
 }
 
-// exp(u) - u - 1 without the cancellation of small u (Taylor series to u^9).
+// exp(u) - u - 1 without the cancellation of small u (Taylor series to u^9); +inf at both ends.
 __device__ __forceinline__ float exp_minus_linear(float u) {
     if (fabsf(u) < 0.5f) {
         float p = 1.f / 362880.f;
@@ -373,7 +373,7 @@ __device__ __forceinline__ float exp_minus_linear(float u) {
         p = fmaf(p, u, 0.5f);
         return u * u * p;
     }
-    return expm1f(u) - u;
+    return u == INFINITY ? u : expm1f(u) - u;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

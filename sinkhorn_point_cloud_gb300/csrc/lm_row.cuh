@@ -313,8 +313,10 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
             const float2 d1 = two_sum(m.ref, -logp.x);
             const float d = fabsf(d1.x) < INFINITY ? d1.x + (d1.y - logp.y) : d1.x;
             kl = exp_minus_linear(d);
-            loss += a.kl_coef * kl;
-            g -= a.kl_coef * (kl + d);
+            if (a.kl_coef != 0.f) {
+                loss += a.kl_coef * kl;
+                g -= a.kl_coef * expm1f(d);  // (kl + d would have lost it in the rounding of a large -d)
+            }
         }
         g *= m.w;
     }

@@ -160,3 +160,40 @@ def test_an_entry_on_a_masked_column_in_any_place(sot, T, V, K, dtype):
         assert np.array_equal(np.isinf(rl), np.arange(T) % 5 < 4)
         alike(loss, rl, 4.0 * ATOL + RTOL * 64.0)
         close_grad(grad, rg, size, dtype)
+
+
+@pytest.mark.parametrize("T,V", [(4, 1000), (200, 5003), (4, 50021)])
+def test_kl_term_far_from_the_reference(sot, T, V):
+    """The KL term's gradient is kl_coef (1 - exp d) however negative d is, its value +inf where exp d leaves the
+    range, and with kl_coef = 0 it takes no part."""
+    x, tg = rows(T, V, "f32", 0, V), targets(T, V)
+    lp, _ = R.token_logprob(host(x), tg.cpu().numpy(), 1.0)
+    far = np.array([-1e4, -1e8, -INF, -60.0])[np.arange(T) % 4]
+    ref = np.where(far > -100, lp + far, far).astype(np.float32)
+    old, adv, w = f32(lp), f32(np.full(T, 0.5)), torch.ones(T).cuda()
+    loss, logp, kl, grad = sot.sot_policy_loss(x, tg, old, adv, f32(ref), w, kl_coef=0.05)
+    with np.errstate(all="ignore"):
+        rl, _, rk, d = R.policy(host(x), tg.cpu().numpy(), host(old), host(adv), ref, np.ones(T), 1.0, 0.2, 0.2, 0.05)
+    alike(kl, rk, 4.0 * ATOL + 2.0 * RTOL * np.abs(rk))
+    alike(loss, rl, 8.0 * ATOL + 4.0 * RTOL * np.abs(rl))
+    rg, size = R.token_grad(host(x), tg.cpu().numpy(), 1.0, d)
+    # d = -A r + 0.05: both are as large as 10 times their sum at most, and r moves by the error of logp
+    close_grad(grad, rg, 2.0 * size, "f32")
+    above = f32(lp + 200.0)  # exp 200 is out of range
+    assert torch.equal(sot.sot_policy_loss(x, tg, old, adv, above, w, kl_coef=0.05)[2], torch.full((T,), INF).cuda())
+    want = sot.sot_policy_loss(x, tg, old, adv, None, w)
+    for r in (f32(ref), above):
+        got = sot.sot_policy_loss(x, tg, old, adv, r, w, kl_coef=0.0)
+        for i in (0, 1, 3):
+            assert torch.equal(got[i], want[i])
+
+
+@pytest.mark.parametrize("V", [1000, 50021])
+def test_kl_of_a_masked_token(sot, V):
+    """The token's own probability is 0, the reference's is not: the estimate of the KL term is +inf."""
+    x, tg = rows(2, V, "f32", 0, V), targets(2, V)
+    x[0, tg[0]] = -INF
+    lp = f32([-3.0, -4.0])
+    loss, logp, kl, _ = sot.sot_policy_loss(x, tg, lp, torch.ones(2).cuda(), lp, torch.ones(2).cuda(), kl_coef=0.1, grad=False)
+    assert logp[0].item() == -INF and kl[0].item() == INF and loss[0].item() == INF
+    assert bool(torch.isfinite(torch.stack([loss, logp, kl])[:, 1]).all())
