@@ -305,7 +305,9 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
     if (OP == LM_POLICY) {
         const float2 d0 = two_sum(logp.x, -m.old);
         const float ratio = expf(fabsf(d0.x) < INFINITY ? d0.x + (d0.y + logp.y) : d0.x);
-        const float free = ratio * m.adv, held = fminf(fmaxf(ratio, a.clip_lo), a.clip_hi) * m.adv;
+        // (a ratio beyond the range of a float times no advantage is 0)
+        const float free = m.adv == 0.f && ratio == INFINITY ? 0.f : ratio * m.adv;
+        const float held = fminf(fmaxf(ratio, a.clip_lo), a.clip_hi) * m.adv;
         loss = -fminf(free, held);
         g = free <= held ? -free : 0.f;
         if (free != free) loss = g = free;

@@ -197,3 +197,24 @@ def test_kl_of_a_masked_token(sot, V):
     loss, logp, kl, _ = sot.sot_policy_loss(x, tg, lp, torch.ones(2).cuda(), lp, torch.ones(2).cuda(), kl_coef=0.1, grad=False)
     assert logp[0].item() == -INF and kl[0].item() == INF and loss[0].item() == INF
     assert bool(torch.isfinite(torch.stack([loss, logp, kl])[:, 1]).all())
+
+
+@pytest.mark.parametrize("T,V", [(4, 1000), (200, 5003), (4, 50021)])
+def test_no_advantage_gives_no_policy_term(sot, T, V):
+    """Advantage 0: the ratio does not count, also where it leaves the range of a float."""
+    x, tg = rows(T, V, "f32", 0, V), targets(T, V)
+    lp, _ = R.token_logprob(host(x), tg.cpu().numpy(), 1.0)
+    old = f32(lp - np.array([0.1, 90.0, 200.0, -200.0])[np.arange(T) % 4])
+    zero, w = torch.zeros(T).cuda(), torch.ones(T).cuda()
+    loss, logp, _, grad = sot.sot_policy_loss(x, tg, old, zero, weight=w)
+    assert bool((loss == 0).all()) and bool((grad == 0).all())
+    ref = f32(lp + 0.2)
+    loss, _, kl, grad = sot.sot_policy_loss(x, tg, old, zero, ref, w, kl_coef=0.5)
+    rl, _, rk, d = R.policy(host(x), tg.cpu().numpy(), host(old), np.zeros(T), host(ref), np.ones(T), 1.0, 0.2, 0.2, 0.5)
+    alike(loss, rl, 8.0 * ATOL)
+    rg, size = R.token_grad(host(x), tg.cpu().numpy(), 1.0, d)
+    # exp d - 1 with d near 0.2 moves by the error of logp, ATOL, times exp d: 2^-13.5 of its value
+    close_grad(grad, rg, 4.0 * size, "f32")
+    x[0, 0] = NAN
+    loss, _, _, grad = sot.sot_policy_loss(x, tg, old, zero, weight=w)
+    assert np.isnan(loss[0].item()) and torch.isnan(grad[0]).all() and bool((grad[1:] == 0).all())
