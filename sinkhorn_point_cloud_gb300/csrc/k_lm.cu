@@ -216,7 +216,7 @@ void row_plan(bool grads, bool whole, long long T, int dtype, int V, int K, bool
 bool lm_tail_fits(int dtype, int V, int K) {
     LmRowPlan p;
     row_plan(true, false, 1ll << 31, dtype, V, K, true, 1, &p);
-    return p.smem <= 220 * 1024;
+    return p.smem <= MAX_SMEM;
 }
 
 cudaError_t launch_lm_row(LmOp op, const LmRowArgs& a, int sms, cudaStream_t st) {

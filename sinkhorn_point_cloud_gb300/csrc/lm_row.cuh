@@ -706,6 +706,7 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
     }
 }
 
+constexpr int MAX_SMEM = 220 * 1024;  // dynamic shared memory of a CTA
 struct LmRowPlan {
     int NW;     // streaming warps of a CTA (0: the short-row kernel)
     int CL, G;  // CTAs a row, granules a slice
@@ -716,7 +717,9 @@ template <int DT, int OP, int NW, bool TAIL>
 cudaError_t launch_row_n(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaunch& L, cudaStream_t st) {
     auto kern = lm_row_kernel<DT, OP, NW, TAIL>;
     if (p.smem > 40 * 1024) {  // 48 KB with the static part need no leave
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+        // The leave belongs to the kernel, not to the call: always the same one, so that a call on
+        // another host thread cannot lower it between here and the launch.
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

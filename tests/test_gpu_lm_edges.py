@@ -218,3 +218,30 @@ def test_no_advantage_gives_no_policy_term(sot, T, V):
     x[0, 0] = NAN
     loss, _, _, grad = sot.sot_policy_loss(x, tg, old, zero, weight=w)
     assert np.isnan(loss[0].item()) and torch.isnan(grad[0]).all() and bool((grad[1:] == 0).all())
+
+
+def test_wide_tails_from_two_host_threads(sot):
+    """Two threads whose rows need different amounts of the same kernel's shared memory.  (Straight through the C
+    interface, so that the calls overlap; rows of weight 0, so that the GPU keeps up.)"""
+    from sinkhorn_point_cloud_gb300 import binding
+    lib, runs = binding.load(), 20000
+    ids, z, w = torch.tensor([[1, 70, 500, 9000]]).cuda(), torch.full((1, 4), -2.0).cuda(), torch.zeros(1).cuda()
+    refused = []
+
+    def work(x, loss, st):
+        V = x.shape[1]
+        args = (x.data_ptr(), 1, V, V, binding.SOT_F32, 1.0, ids.data_ptr(), binding.SOT_I64, z.data_ptr(), binding.SOT_F32, 4,
+                1, w.data_ptr(), loss.data_ptr(), None, 0, st.cuda_stream)
+        for _ in range(runs):
+            if lib.sot_distill_topk(*args):
+                refused.append(lib.sot_last_error())
+    arrays = [(torch.zeros(1, V).cuda(), torch.ones(1).cuda(), torch.cuda.Stream()) for V in (1500000, 3000000)]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=a) for a in arrays]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, (len(refused), refused[0])
+    assert all(loss.item() == 0.0 for _, loss, _ in arrays)
