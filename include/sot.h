@@ -411,7 +411,7 @@ int sot_preference_loss(const float* logp, const float* ref_logp, const void* ta
  *   counts[e] = number of choices of expert e
  *   loss[0] = balance_coef / N sum_t sum_e f_e p_te,   loss[1] = z_coef / N sum_t lse_t^2
  *   grad = d(loss[0] + loss[1]) / d logits with the counts held fixed (NULL: losses only)
- * N = 0 gives zeros.  T K < 2^31.
+ * N = 0 gives zeros.  A z loss beyond the range of a float is +inf, and 0 where z_coef is 0.  T K < 2^31.
  */
 int sot_balance_loss(const void* logits, long long T, int E, long long ld, int dtype, const void* ids, int ids_type,
                      int K, const unsigned char* mask, float balance_coef, float z_coef, int* counts, float* loss,

@@ -66,6 +66,8 @@ struct Sums {
         const float2 t = two_sum(s.x, v);
         s = make_float2(t.x, s.y + t.y);
     }
+    // (the compensation of an infinite sum is NaN)
+    __device__ __forceinline__ static float value(float2 s) { return fabsf(s.x) < INFINITY ? s.x + s.y : s.x; }
 };
 
 __device__ __forceinline__ float group_max(float v, int lanes) {
@@ -241,7 +243,8 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
             }
         }
         const float inv_s = __fdividef(1.f, s), dot = d * inv_s;  // coef sum f p
-        const float lse = far ? m + __logf(s) : (u + __log2f(s)) * SOT_LN2;
+        // (a row of nothing but -inf is far, and has no sum)
+        const float lse = !far ? (u + __log2f(s)) * SOT_LN2 : s > 0.f ? m + __logf(s) : NAN;
         if (now && sub == 0) {
             Sums::add(out.dot, dot);
             Sums::add(out.z, lse * lse);
@@ -271,7 +274,7 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
 template <int NT>
 __device__ __forceinline__ float2 block_sums(const Sums& s, float (&red)[2][NT / 32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float d = warp_sum(s.dot.x + s.dot.y), z = warp_sum(s.z.x + s.z.y);
+    const float d = warp_sum(Sums::value(s.dot)), z = warp_sum(Sums::value(s.z));
     if (lane == 0) {
         red[0][warp] = d;
         red[1][warp] = z;
@@ -284,10 +287,10 @@ __device__ __forceinline__ float2 block_sums(const Sums& s, float (&red)[2][NT /
 __device__ __forceinline__ float share_of(const LmBalanceArgs& a, int kept) {
     return (float)a.E / ((float)a.K * (float)max(kept, 1));
 }
-// coef is already in the dot sums
+// coef is already in the dot sums.  A z loss that is not wanted is 0 also where the squares leave the range.
 __device__ __forceinline__ void write_loss(const LmBalanceArgs& a, float dot, float z, int kept) {
     a.loss[0] = kept > 0 ? dot / (float)kept : 0.f;
-    a.loss[1] = kept > 0 ? a.z_coef * (z / (float)kept) : 0.f;
+    a.loss[1] = kept > 0 && !(a.z_coef == 0.f && z == INFINITY) ? a.z_coef * (z / (float)kept) : 0.f;
 }
 // A 32-bit value of another CTA's shared memory.
 __device__ __forceinline__ int cluster_load(const int* local_ptr, uint32_t rank) {
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(CNT_NT) lm_balance_small_kernel(LmBalanceArgs 
             Sums::add(t.dot, sums[p][0]);
             Sums::add(t.z, sums[p][1]);
         }
-        write_loss(a, t.dot.x + t.dot.y, t.z.x + t.z.y, kept);
+        write_loss(a, Sums::value(t.dot), Sums::value(t.z), kept);
     }
 }
 

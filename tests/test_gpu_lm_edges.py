@@ -245,3 +245,36 @@ def test_wide_tails_from_two_host_threads(sot):
     torch.cuda.synchronize()
     assert not refused, (len(refused), refused[0])
     assert all(loss.item() == 0.0 for _, loss, _ in arrays)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E", [(40, 60), (40, 64), (3000, 60), (3000, 256)])
+def test_z_loss_out_of_range(sot, T, E, dtype):
+    """A row whose squared log-sum-exp leaves the range of a float makes the z loss +inf, and no loss at all where
+    its coefficient is 0."""
+    x = rows(T, E, dtype, 0, seed=E + T)
+    x[T // 2] = 1e25
+    x[T // 3] = -1e30
+    ids = x.float().topk(2, 1).indices.int().contiguous()
+    counts, loss, grad = sot.sot_balance_loss(x, ids, balance_coef=float(T), z_coef=0.0)
+    rc, rl, rg, size = R.balance(host(x), ids.cpu().numpy(), None, float(T), 0.0)
+    alike(loss, rl, ATOL * np.abs(rl))
+    close_grad(grad, rg, size, dtype)
+    loss = sot.sot_balance_loss(x, ids, balance_coef=float(T), z_coef=0.01)[1]
+    alike(loss, [rl[0], INF], ATOL * np.abs(rl))
+    x[1, 0] = NAN
+    for cz in (0.0, 0.01):
+        assert torch.isnan(sot.sot_balance_loss(x, ids, balance_coef=float(T), z_coef=cz)[1]).all()
+
+
+@pytest.mark.parametrize("T,E", [(40, 60), (3000, 256)])
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_balance_losses_of_a_row_without_a_sum(sot, T, E, bad):
+    x = rows(T, E, "f32", 0, seed=E)
+    ids = x.topk(2, 1).indices.int().contiguous()
+    if bad == -INF:
+        x[1] = bad
+    else:
+        x[1, 5] = bad
+    for cz in (0.0, 0.01):
+        assert torch.isnan(sot.sot_balance_loss(x, ids, z_coef=cz)[1]).all()
