@@ -438,7 +438,8 @@ def sot_grad_x_coo(X, Y, rows, cols, vals, batch_offsets, grad=None, stream=None
 # tensor's address once everything about it is right, and only what is wrong is
 # looked at again to say what.
 _F32 = torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (the handle without a stream object around it; a torch without CUDA has neither)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _logits(x, name="logits"):
