@@ -577,6 +577,8 @@ def sot_distill_topk(logits, ids, teacher, weight=None, temperature=1.0, tail=Fa
     tt = _FLOATS.get(teacher.dtype) if isinstance(teacher, torch.Tensor) else None
     if tt is None:
         raise TypeError("teacher must be a float32, float16 or bfloat16 torch.Tensor")
+    if teacher.dim() > 1 and teacher.shape != ids.shape:
+        raise ValueError(f"teacher must have the shape of ids, {(T, K)}, got {tuple(teacher.shape)}")
     z = _floats(teacher, "teacher", T * K, dev, teacher.dtype)
     w = _floats(weight, "weight", T, dev)
     _floats(loss, "loss", T, dev)

@@ -278,3 +278,10 @@ def test_balance_losses_of_a_row_without_a_sum(sot, T, E, bad):
         x[1, 5] = bad
     for cz in (0.0, 0.01):
         assert torch.isnan(sot.sot_balance_loss(x, ids, z_coef=cz)[1]).all()
+
+
+def test_a_transposed_teacher_is_refused(sot):
+    x, ids = rows(3, 50, "f32"), torch.arange(5).expand(3, 5).contiguous().cuda()
+    with pytest.raises(ValueError, match="teacher"):
+        sot.sot_distill_topk(x, ids, torch.zeros(5, 3).cuda())
+    assert sot.sot_distill_topk(x, ids, torch.zeros(3, 5).cuda())[0].shape == (3,)
