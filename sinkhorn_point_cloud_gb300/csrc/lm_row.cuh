@@ -75,7 +75,7 @@ struct RowCoef {
     }
 };
 
-// The slice of row `row` that CTA `rank` of its cluster takes, in 16-byte
+// The slice of a row that CTA `rank` of its cluster takes, in 16-byte
 // granules of memory.  A row that starts or ends inside a granule is read with
 // the whole granule: memory is allocated in larger aligned pieces, so the
 // other bytes are readable; they are masked.
@@ -98,10 +98,6 @@ __device__ __forceinline__ Slice slice_at(const typename Elem<DT>::T* row, int V
     s.lo = s.e0 < 0 ? 1 : 0;
     s.hi = s.ng - (s.e0 + s.ng * N > V ? 1 : 0);
     return s;
-}
-template <int DT>
-__device__ __forceinline__ Slice slice_of(const void* x, long long row, long long ld, int V, int G, uint32_t rank) {
-    return slice_at<DT>(static_cast<const typename Elem<DT>::T*>(x) + row * ld, V, G, rank);
 }
 
 // The teacher's entries of a row (one warp), in two steps.  First the entries as
@@ -723,7 +719,7 @@ cudaError_t launch_row_n(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaun
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.CL, 1, 1);
+    cfg.gridDim = dim3((unsigned)(a.T * p.CL), 1, 1);
     cfg.blockDim = dim3((NW + 1) * 32, 1, 1);
     cfg.dynamicSmemBytes = p.smem;
     cfg.stream = st;
@@ -734,7 +730,6 @@ cudaError_t launch_row_n(const LmRowArgs& a, const LmRowPlan& p, const LmRowLaun
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cfg.gridDim.x = (unsigned)(a.T * p.CL);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, L);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
