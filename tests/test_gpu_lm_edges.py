@@ -285,3 +285,148 @@ def test_a_transposed_teacher_is_refused(sot):
     with pytest.raises(ValueError, match="teacher"):
         sot.sot_distill_topk(x, ids, torch.zeros(5, 3).cuda())
     assert sot.sot_distill_topk(x, ids, torch.zeros(3, 5).cuda())[0].shape == (3,)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,V", SIZES)
+def test_policy_gradient_of_every_column(sot, T, V, dtype):
+    """Clipped, weighted and with a KL term.  The coefficient d of a row moves by w (|A| r + kc e^u) times the error of
+    logp (ATOL and the logits' rounding) and the rounding of the exponentials (under 2^-20 of their value); at a column
+    this counts with p_v + [v = target]."""
+    for pad, tau, kc in ((0, 1.0, 0.05), (5, 0.8, 0.3)):
+        x, tg, old, adv, ref, w = policy_inputs(T, V, dtype, pad, tau, seed=V + T)
+        grad = sot.sot_policy_loss(x, tg, old, adv, ref_logp=ref, weight=w, temperature=tau, kl_coef=kc)[3]
+        _, lp, _, d = R.policy(host(x), tg.cpu().numpy(), host(old), host(adv), host(ref), host(w), tau, 0.2, 0.2, kc)
+        rg, size = R.token_grad(host(x), tg.cpu().numpy(), tau, d)
+        terms = host(w) * (np.abs(host(adv)) * np.exp(lp - host(old)) + kc * np.exp(host(ref) - lp))
+        _, unit = R.token_grad(host(x), tg.cpu().numpy(), tau, np.ones(T))
+        moved = terms * (ATOL + RTOL * np.abs(host(x)).max() / tau + 2.0 ** -20)
+        close_grad(grad, rg, size + unit * moved[:, None] / GTOL, dtype)
+
+
+@pytest.mark.parametrize("off", [[-5, 3, 40], [18, 5, 2], [30, 40, 50], [0, 1 << 40, 1 << 41], [4, 4, 9, 90, -3]])
+@pytest.mark.parametrize("average", [False, True])
+def test_clamped_offsets_give_the_losses_of_what_is_left(sot, off, average):
+    T = 20
+    lp = -torch.rand(T, generator=torch.Generator().manual_seed(4)).cuda()
+    loss, margin, grad = sot.sot_preference_loss(lp, torch.tensor(off).cuda(), beta=0.3, average=average)
+    held = np.clip(np.array(off, np.float64), 0, T).astype(int)
+    rl, rm, rd = R.preference(host(lp), None, None, held, 0.3, 0.0, average, 1.0 / (len(off) // 2))
+    alike(loss, rl, 2.0 ** -20 * np.abs(rl) + 2.0 ** -22)
+    alike(margin, rm, 2.0 ** -20 * np.abs(rm) + 2.0 ** -22)
+    if np.all(np.diff(held) >= 0):
+        alike(grad, rd, 2.0 ** -20 * np.abs(rd) + 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,E,pad", [(40, 64, 0), (40, 60, 1), (300, 33, 0), (6000, 64, 0), (6000, 61, 3), (2000, 500, 0)])
+def test_balance_gradient_in_place(sot, T, E, pad, dtype):
+    x = rows(T, E + pad, dtype, 0, seed=E)
+    x[T // 2] -= 300.0  # a row that is read twice
+    v = x[:, :E]
+    ids = v.float().topk(3, 1).indices.int().contiguous()
+    mask = torch.rand(T, generator=torch.Generator().manual_seed(1)).cuda() > 0.2
+    args = dict(mask=mask, balance_coef=float(T), z_coef=0.1)
+    counts, loss, _ = sot.sot_balance_loss(v, ids, grad=False, **args)
+    out = x.clone()[:, :E]  # the same strides and alignment
+    sot.sot_balance_loss(v, ids, grad=out, **args)
+    beside = x[:, E:].clone()
+    c2, l2, g2 = sot.sot_balance_loss(v, ids, grad=v, **args)
+    assert g2 is v and torch.equal(c2, counts) and torch.equal(l2, loss)
+    assert torch.equal(v, out) and torch.equal(x[:, E:], beside)
+
+
+def everything(sot, s):
+    """One of each call on the tensors of `s`."""
+    out = list(sot.sot_token_logprob(s["x"], s["tg"]))
+    pref = sot.sot_preference_loss(out[0], s["off"], beta=0.3)
+    out += [*pref, sot.sot_token_logprob_grad(s["x"], s["tg"], out[1], pref[2])]
+    out += sot.sot_policy_loss(s["x"], s["tg"], s["old"], s["adv"], s["ref"], s["w"], kl_coef=0.1)
+    for tail in (False, True):
+        out += sot.sot_distill_topk(s["x"], s["ids"], s["z"], weight=s["w"], tail=tail)
+    for r, c in ((s["r"], s["c"]), (s["r"][:50], s["c"][:50])):  # with scratch and without
+        out += sot.sot_balance_loss(r, c, z_coef=0.1)
+    return out
+
+
+def some_inputs(seed, T=40, V=9001):
+    x, tg, old, adv, ref, w = policy_inputs(T, V, "bf16", 0, 1.0, seed)
+    g = torch.Generator().manual_seed(seed)
+    r = rows(4000, 128, "bf16", 0, seed)
+    return dict(x=x, tg=tg, old=old, adv=adv, ref=ref, w=w, off=torch.tensor([0, 9, 17, 30, 40]).cuda(),
+                ids=torch.stack([torch.randperm(V, generator=g)[:20] for _ in range(T)]).cuda(),
+                z=torch.log_softmax(torch.randn(T, 20, generator=g), 1).sub(0.2).cuda(), r=r,
+                c=r.float().topk(4, 1).indices.int().contiguous())
+
+
+def test_in_a_captured_graph(sot):
+    s, t = some_inputs(1), some_inputs(2)
+    want = [[o.clone() for o in everything(sot, v)] for v in (s, t)]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        everything(sot, s)
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = everything(sot, s)
+    for v, w in ((s, want[0]), (t, want[1]), (t, want[1])):
+        for k in s:
+            s[k].copy_(v[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, w):
+            assert torch.equal(a, b)
+
+
+def test_from_two_host_threads(sot):
+    inputs = [some_inputs(3), some_inputs(4)]
+    want = [everything(sot, s) for s in inputs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(s, w):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(30):
+                    got = everything(sot, s)
+                st.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, w)):
+                wrong.append("results differ")
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in zip(inputs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong[0]
+
+
+@pytest.mark.parametrize("T,V", [(400, 2040), (300, 4096), (200, 6001), (160, 107003), (160, 140001), (30, 300001), (60, 9000),
+                                 (153, 30000)])
+def test_losses_alone_are_the_same_bits(sot, T, V):
+    """A loss does not depend on whether its gradient is asked for, whichever way the rows are cut."""
+    x, tg, old, adv, ref, w = policy_inputs(T, V, "bf16", 0, 1.0, V)
+    a = sot.sot_policy_loss(x, tg, old, adv, ref, w, kl_coef=0.1)
+    b = sot.sot_policy_loss(x, tg, old, adv, ref, w, kl_coef=0.1, grad=False)
+    for i in range(3):
+        assert torch.equal(a[i], b[i])
+    ids = (torch.arange(20) * (V // 20)).expand(T, 20).contiguous().cuda()
+    z = torch.log_softmax(torch.randn(T, 20, generator=torch.Generator().manual_seed(1)), 1).sub(0.2).cuda()
+    for tail in (False, True):
+        loss = sot.sot_distill_topk(x, ids, z, weight=w, tail=tail)[0]
+        assert torch.equal(loss, sot.sot_distill_topk(x, ids, z, weight=w, tail=tail, grad=False)[0])
+
+
+def test_the_widest_tail(sot):
+    """Marks that fill nearly all of the shared memory that a tail row may take."""
+    V, K = 6300000, 4
+    x = rows(1, V, "f32", 0, 3)
+    ids = torch.tensor([[0, 70, 3000001, V - 1]])
+    z, w = torch.log(torch.tensor([[0.3, 0.2, 0.1, 0.1]])).cuda(), torch.ones(1).cuda()
+    loss, grad = sot.sot_distill_topk(x, ids.cuda(), z, weight=w, tail=True)
+    rl, rg, size = R.distill(host(x), ids.numpy(), host(z), host(w), 1.0, True)
+    alike(loss, rl, 4.0 * ATOL + RTOL * 64.0)
+    close_grad(grad, rg, size, "f32")
