@@ -21,6 +21,7 @@ struct LmRowArgs {
     void* grad;  // NULL: losses only
     float tau;
     double inv_tau;
+    float inv_hi, inv_lo;  // the same in two floats
     const float* weight;  // NULL: every row weighs 1/T
     // token log-probability and policy loss
     const void* target;

@@ -201,6 +201,13 @@ __device__ __forceinline__ void student_side(const LmRowArgs& a, int c0, int c1,
     }
 }
 
+// log sum exp((x - m) / tau) from sums against the rounded m2, which hold exp2(m sc - m2) as a factor.
+__device__ __forceinline__ float2 log_sum(MS v, float sc) {
+    const float m2 = __fmul_rn(v.m, sc);
+    const float2 l = log_ff(v.s);
+    return is_far(m2) ? l : ff_add(l, make_float2(-fmaf(v.m, sc, -m2) * SOT_LN2, 0.f));
+}
+
 // What a row's loss depends on besides its logits.
 struct RowMeta {
     int tgt;
@@ -231,8 +238,6 @@ template <int OP, class Publish>
 __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row, const RowMeta& m, MS r, MS top, float2 Q,
                                               float2 B, float2 D, float sc, bool write, Publish publish) {
     const MS all = OP == LM_DISTILL && a.tail ? ms_combine(r, top, sc) : r;
-    // log(sum exp(x / tau)) = m2 ln 2 + log s with the rounded m2 that the sums
-    // were formed with; where m2 overflows, m / tau + log s
     const float m2 = __fmul_rn(all.m, sc);
     const bool far = is_far(m2);
     const float2 ln2 = make_float2(0.693147182f, -1.904654212e-9f);
@@ -292,11 +297,13 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
         }
         return c;
     }
-    // logp = (x sc - m2) ln 2 - log s, kept to more than 24 bits until it is compared
-    const float2 logS = log_ff(all.s), minus = make_float2(-logS.x, -logS.y);
-    const float2 t = two_prod(D.x, sc), ts = two_sum(t.x, -m2);
-    float2 logp = ff_add(ff_mul(ff_renorm(ts.x, ts.y + t.y), ln2), minus);
-    if (far || !(fabsf(logp.x) < INFINITY)) logp = make_float2((float)(((double)D.x - (double)all.m) * a.inv_tau) - logS.x, 0.f);
+    // logp = (x - m) / tau - log S, kept to more than 24 bits until it is compared.  The difference
+    // is exact; through the rounded sc and m2 a logit at -65504 would be off by 1e-3.  Beyond
+    // 2^24 a log-probability that was stored in 32 bits says nothing of the low part.
+    const float2 logS = log_sum(all, sc), d = two_sum(D.x, -all.m);
+    float2 logp = ff_add(ff_mul(d, make_float2(a.inv_hi, a.inv_lo)), make_float2(-logS.x, -logS.y));
+    if (!(fabsf(logp.x) < INFINITY)) logp = make_float2((float)(((double)D.x - (double)all.m) * a.inv_tau) - logS.x, 0.f);
+    if (fabsf(logp.x) >= 0x1p24f) logp.y = 0.f;
     float g = 0.f, loss = 0.f, kl = 0.f;
     if (OP == LM_POLICY) {
         const float2 d0 = two_sum(logp.x, -m.old);
@@ -326,7 +333,8 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
         if (a.kl) a.kl[row] = kl;
         if (a.logp) a.logp[row] = logp.x + logp.y;
         if (a.lse) {
-            const float2 l = ff_add(ff_mul(make_float2(m2, 0.f), ln2), logS);
+            // (with m2 and s as they are: what the gradient from it forms again)
+            const float2 l = ff_add(ff_mul(make_float2(m2, 0.f), ln2), log_ff(all.s));
             a.lse[row] = far ? (float)((double)all.m * a.inv_tau) + logS.x : l.x + l.y;
         }
     }

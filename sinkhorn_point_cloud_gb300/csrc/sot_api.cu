@@ -1596,6 +1596,12 @@ int check_rows(const void* x, long long T, int V, long long ld, int dtype, const
     if (grad) SOT_TRY(check_pointer("grad", grad, dtype));
     return SOT_OK;
 }
+void set_temperature(LmRowArgs& a, float tau) {
+    a.tau = tau;
+    a.inv_tau = 1.0 / (double)tau;
+    a.inv_hi = (float)a.inv_tau;
+    a.inv_lo = (float)(a.inv_tau - (double)a.inv_hi);
+}
 int check_temperature(float tau) {
     if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(1.4426951f / tau))
         return fail(SOT_ERR_INVALID_ARG, "temperature must be finite and > 0");
@@ -1615,13 +1621,12 @@ int sot_token_logprob(const void* logits, long long T, int V, long long ld, int 
     SOT_TRY(check_pointer("target", target, target_type));
     if (!logp && !lse) return fail(SOT_ERR_INVALID_ARG, "logp and lse must not both be NULL");
     LmRowArgs a = {};
-    a.inv_tau = 1.0 / (double)temperature;
     a.x = logits;
     a.T = T;
     a.V = V;
     a.ld = ld;
     a.dtype = dtype;
-    a.tau = temperature;
+    set_temperature(a, temperature);
     a.target = target;
     a.target_type = target_type;
     a.logp = logp;
@@ -1676,7 +1681,6 @@ int sot_distill_topk(const void* logits, long long T, int V, long long ld, int d
     SOT_TRY(check_pointer("teacher", teacher, teacher_type));
     if (!loss && !grad) return fail(SOT_ERR_INVALID_ARG, "loss and grad must not both be NULL");
     LmRowArgs a = {};
-    a.inv_tau = 1.0 / (double)temperature;
     a.x = logits;
     a.T = T;
     a.V = V;
@@ -1684,7 +1688,7 @@ int sot_distill_topk(const void* logits, long long T, int V, long long ld, int d
     a.ldg = ld_grad;
     a.dtype = dtype;
     a.grad = grad;
-    a.tau = temperature;
+    set_temperature(a, temperature);
     a.weight = weight;
     a.ids = ids;
     a.ids_type = ids_type;
@@ -1714,7 +1718,6 @@ int sot_policy_loss(const void* logits, long long T, int V, long long ld, int dt
     if (!old_logp || !advantage) return fail(SOT_ERR_INVALID_ARG, "old_logp and advantage must not be NULL");
     if (!loss && !logp && !kl && !grad) return fail(SOT_ERR_INVALID_ARG, "no output is wanted");
     LmRowArgs a = {};
-    a.inv_tau = 1.0 / (double)temperature;
     a.x = logits;
     a.T = T;
     a.V = V;
@@ -1722,7 +1725,7 @@ int sot_policy_loss(const void* logits, long long T, int V, long long ld, int dt
     a.ldg = ld_grad;
     a.dtype = dtype;
     a.grad = grad;
-    a.tau = temperature;
+    set_temperature(a, temperature);
     a.weight = weight;
     a.target = target;
     a.target_type = target_type;

@@ -430,3 +430,28 @@ def test_the_widest_tail(sot):
     rl, rg, size = R.distill(host(x), ids.numpy(), host(z), host(w), 1.0, True)
     alike(loss, rl, 4.0 * ATOL + RTOL * 64.0)
     close_grad(grad, rg, size, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,V", [(12, 900), (12, 50021), (200, 5003)])
+@pytest.mark.parametrize("tau", [1.0, 2.0, 0.75])
+def test_policy_of_a_token_on_a_masked_column(sot, T, V, dtype, tau):
+    """Tokens whose logit is a mask's finite value, with old and reference log-probabilities from sot_token_logprob: the
+    ratio is exp of what their rounding left, and 1 beyond 2^24, where neighbouring floats lie 2 and more apart."""
+    levels = {"f32": [-300.0, -1e4, -1e9, -1.7e38], "f16": [-300.0, -1e4, -65504.0, -32752.0],
+              "bf16": [-300.0, -1e4, -1e9, -1.7e38]}[dtype]
+    x, tg = rows(T, V, dtype, 0, V), targets(T, V)
+    at = torch.arange(T).cuda()
+    x[at, tg] = torch.tensor(levels, dtype=x.dtype).cuda()[at % 4]
+    lp, _ = R.token_logprob(host(x), tg.cpu().numpy(), tau)
+    logp, _ = sot.sot_token_logprob(x, tg, temperature=tau)
+    alike(logp, lp, ATOL + RTOL * np.abs(lp))
+    adv, w = f32(np.where(np.arange(T) % 3 == 0, -1.0, 0.5)), torch.ones(T).cuda()
+    loss, again, kl, grad = sot.sot_policy_loss(x, tg, logp, adv, logp, w, temperature=tau, kl_coef=0.1)
+    assert torch.equal(again, logp)
+    u = np.where(np.abs(lp) < 2.0 ** 24, lp - host(logp), 0.0)
+    alike(loss, -host(adv) * np.exp(u), 8.0 * ATOL)
+    alike(kl, np.expm1(-u) + u, 4.0 * ATOL)
+    rg, size = R.token_grad(host(x), tg.cpu().numpy(), tau, -host(adv) * np.exp(u) - 0.1 * np.expm1(-u))
+    # the coefficient moves by (|A| + 0.1) times the error of u, ATOL: 0.3 GTOL of it
+    close_grad(grad, rg, 2.0 * size, dtype)
