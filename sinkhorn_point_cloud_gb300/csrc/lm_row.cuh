@@ -40,7 +40,7 @@
 namespace sot {
 
 constexpr int ROW_MAX_CL = 8;
-constexpr int NREC = 6;         // a CTA's record: (m, s), the entries' (m, s), the entries' sum q x in two parts
+constexpr int NREC = 8;  // a CTA's record: (m, s), the entries' (m, s), its part of their distance or the target's logit
 
 struct LmRowLaunch {
     int CL, G;  // CTAs a row, granules a slice
@@ -171,28 +171,74 @@ __device__ __forceinline__ float2 ff_sum_or_far(float2 v) {
     return fabsf(f) < INFINITY ? s : make_float2(f, 0.f);
 }
 
+// A sum whose low parts are summed apart (y), so that the chain from term to term is one addition.
+__device__ __forceinline__ void sum_apart(float2& s, float2 v) {
+    const float2 t = two_sum(s.x, v.x);
+    s = make_float2(t.x, s.y + (t.y + v.y));
+}
+__device__ __forceinline__ float2 warp_sum_apart(float2 s) {
+    return ff_sum_or_far(fabsf(s.x) < INFINITY ? ff_renorm(s.x, s.y) : make_float2(s.x, 0.f));
+}
+// sum q (x - m) over the entries (one warp): what a row's loss needs of the student's logits.
+// Against m the terms have one sign, or are small, so nothing is lost where the logits lie far from 0.
+// (Seldom needed, so kept out of line: inside, 4096 x 32000 bf16 with 64 entries take 88.1 us, so 86.3.)
+static __device__ __noinline__ float2 entries_distance(int K, const float* ex, const float* eq, float m) {
+    float2 D = make_float2(0.f, 0.f);
+    for (int k = threadIdx.x & 31; k < K; k += 32)
+        if (eq[k] != 0.f) sum_apart(D, two_prod(eq[k], ex[k] - m));  // (0: unused ones too)
+    return warp_sum_apart(D);
+}
+// The same before m is known: D against X.  X is 0, or in a slice with a logit beyond 64 the largest; Q =
+// sum q of a slice takes D from there to m.
+struct Part {
+    float X, Q;
+    float2 D;
+    __device__ __forceinline__ float2 distance(float m) const {
+        const float up = X - m;
+        return ff_add_or_far(D, fabsf(up) < INFINITY ? two_prod(Q, up) : make_float2(Q * up, 0.f));
+    }
+};
+// And once it is, for entries in one piece: from 0 if that is near, otherwise all over again.
+__device__ __forceinline__ float2 row_distance(const LmRowArgs& a, const float* ex, const float* eq, const Part& part,
+                                               float2 Q, float m) {
+    if (m == 0.f) return part.D;
+    if (fabsf(m) <= 64.f) return ff_add_or_far(part.D, ff_mul(Q, make_float2(-m, 0.f)));
+    return entries_distance(a.K, ex, eq, m);
+}
+
 // The entries' logits in columns [c0, c1) of a row at x, from what teacher_entries
-// fetched: ex, D = sum q x; eid becomes -1 for the others.  For the tail also the entries' statistics.
+// fetched: ex and their part; eid becomes -1 (and q 0) for the others.  For the tail also the
+// entries' statistics.
 template <int DT>
 __device__ __forceinline__ void student_side(const LmRowArgs& a, int c0, int c1, const typename Elem<DT>::T* x, float* ex,
-                                             const float* eq, int* eid, float sc, float2& D, MS& top) {
+                                             float* eq, int* eid, float sc, bool slice, Part& part, MS& top) {
     const int lane = threadIdx.x & 31;
-    D = make_float2(0.f, 0.f);
+    part = Part{0.f, 0.f, make_float2(0.f, 0.f)};
     top = MS{-INFINITY, 0.f};
     async_wait();
     for (int k = lane; k < a.K; k += 32) {
         const int id = eid[k];
         if (!(id >= 0 && id >= c0 && id < c1)) {
             ex[k] = -INFINITY;
+            eq[k] = 0.f;
             eid[k] = -1;
             continue;
         }
-        const float v = element_of<DT>(ex[k], x + id);
+        const float v = element_of<DT>(ex[k], x + id), q = eq[k];
         ex[k] = v;
-        if (eq[k] != 0.f) D = ff_add_or_far(D, two_prod(eq[k], v));
         top.m = fmaxf(top.m, v);
+        if (q != 0.f) sum_apart(part.D, two_prod(q, v));
+        part.Q += q;
     }
-    D = ff_sum_or_far(D);
+    const bool far = fabsf(top.m) < INFINITY && fabsf(top.m) > 64.f;
+    part.D = warp_sum_apart(part.D);
+    if (slice) {
+        part.Q = warp_sum(part.Q);
+        if (__any_sync(0xffffffffu, far)) {
+            part.X = warp_max1(fabsf(top.m) < INFINITY ? top.m : -INFINITY);
+            part.D = entries_distance(a.K, ex, eq, part.X);
+        }
+    }
     if (a.tail) {
         top.m = warp_max1(top.m);
         for (int k = lane; k < a.K; k += 32)
@@ -205,7 +251,7 @@ __device__ __forceinline__ void student_side(const LmRowArgs& a, int c0, int c1,
 __device__ __forceinline__ float2 log_sum(MS v, float sc) {
     const float m2 = __fmul_rn(v.m, sc);
     const float2 l = log_ff(v.s);
-    return is_far(m2) ? l : ff_add(l, make_float2(-fmaf(v.m, sc, -m2) * SOT_LN2, 0.f));
+    return v.m == 0.f || is_far(m2) ? l : ff_add(l, make_float2(-fmaf(v.m, sc, -m2) * SOT_LN2, 0.f));
 }
 
 // What a row's loss depends on besides its logits.
@@ -231,12 +277,14 @@ __device__ __forceinline__ RowMeta row_meta(const LmRowArgs& a, long long row, b
 }
 
 // The row's loss and the gradient's coefficients from its joined statistics
-// (one lane): r without and top with the entries of a tail, D = sum q x or the
-// target's logit.  `publish` hands the coefficients on before the losses, which
-// nothing waits for, are finished.
-template <int OP, class Publish>
+// (one warp): r without and top with the entries of a tail, xt the target's logit.  `publish` hands
+// the coefficients on before the losses, which nothing waits for, are finished; `distance` gives the
+// entries' sum q (x - m) to every lane, `lead` is whether this CTA writes the row's losses.
+template <int OP, class Publish, class Distance>
 __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row, const RowMeta& m, MS r, MS top, float2 Q,
-                                              float2 B, float2 D, float sc, bool write, Publish publish) {
+                                              float2 B, float xt, float sc, bool lead, Publish publish,
+                                              Distance distance) {
+    const bool write = lead && (threadIdx.x & 31) == 0;
     const MS all = OP == LM_DISTILL && a.tail ? ms_combine(r, top, sc) : r;
     const float m2 = __fmul_rn(all.m, sc);
     const bool far = is_far(m2);
@@ -265,32 +313,33 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
             c.c = r.s == 0.f ? 0.f * inv * c.fa : wt * ((Q.x + qr) * rescale(r.m, c.M, sc) * inv - qr / r.s) * two_k;
         }
         publish(c);
-        if (write && a.loss) {
+        if (!a.loss || !lead) return c;
+        const float2 E = distance(all.m);
+        if (write) {
+            // With y = (x - m) / tau and S = sum exp y over the row, R over what is not an entry:
+            //   log p = y - log S,  log p_r = (m_r - m) / tau + log R - log S.
             // In pairs of floats: with doubles throughout, 16384 rows of 2048 take 57 us, so 45.
             const bool tail = a.tail && !(qr <= 0.f);
-            const float2 logS = log_ff(all.s), logR = tail ? log_ff(r.s) : logS, logq = tail ? log_ff(qr) : logS;
+            const float2 inv_tau = make_float2(a.inv_hi, a.inv_lo), logS = log_sum(all, sc);
+            const float2 logR = tail ? log_sum(r, sc) : logS, logq = tail ? log_ff(qr) : logS;
             float2 sum = make_float2(0.f, 0.f);
-            if (!(Q.x <= 0.f)) {  // B + Q log s - (D sc - Q m2) ln 2; NaN where a used entry is NaN or +inf
-                const float2 d = ff_add(ff_mul(D, make_float2(sc, 0.f)), ff_mul(Q, make_float2(-m2, 0.f)));
-                sum = ff_add(ff_add(B, ff_mul(Q, logS)), ff_mul(d, make_float2(-ln2.x, -ln2.y)));
+            if (!(Q.x <= 0.f)) {  // B + Q log S - E / tau; NaN where a used entry is NaN or +inf
+                const float2 d = ff_mul(E, inv_tau);
+                sum = ff_add(ff_add(B, ff_mul(Q, logS)), make_float2(-d.x, -d.y));
             }
             if (tail) {  // + q_r (log q_r - log p_r)
-                const float2 apart = ff_mul(two_sum(__fmul_rn(r.m, sc), -m2), ln2);
+                const float2 apart = ff_mul(two_sum(r.m, -all.m), inv_tau);
                 const float2 logp = ff_add(ff_add(apart, logR), make_float2(-logS.x, -logS.y));
                 sum = ff_add(sum, ff_mul(ff_add(logq, make_float2(-logp.x, -logp.y)), make_float2(qr, 0.f)));
             }
             float loss = (sum.x + sum.y) * m.w * a.tau * a.tau;
-            if (far || !(fabsf(loss) < INFINITY)) {  // with the range of a double
-                const double q = to_double(Q), k = 0.69314718055994530942;
+            if (!(fabsf(loss) < INFINITY)) {  // with the range of a double
+                const double q = to_double(Q);
                 double l = 0.0;
-                if (!(q <= 0.0))
-                    l = to_double(B) + q * to_double(logS) -
-                        (far ? (to_double(D) - q * (double)all.m) * a.inv_tau : (to_double(D) * (double)sc - q * (double)m2) * k);
-                if (tail) {
-                    const double apart = far ? ((double)r.m - (double)all.m) * a.inv_tau
-                                             : ((double)__fmul_rn(r.m, sc) - (double)m2) * k;
-                    l += (double)qr * (to_double(logq) - (apart + to_double(logR) - to_double(logS)));
-                }
+                if (!(q <= 0.0)) l = to_double(B) + q * to_double(logS) - to_double(E) * a.inv_tau;
+                if (tail)
+                    l += (double)qr * (to_double(logq) -
+                                       (((double)r.m - (double)all.m) * a.inv_tau + to_double(logR) - to_double(logS)));
                 loss = (float)(l * (double)m.w * (double)a.tau * (double)a.tau);
             }
             a.loss[row] = loss;
@@ -300,9 +349,9 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
     // logp = (x - m) / tau - log S, kept to more than 24 bits until it is compared.  The difference
     // is exact; through the rounded sc and m2 a logit at -65504 would be off by 1e-3.  Beyond
     // 2^24 a log-probability that was stored in 32 bits says nothing of the low part.
-    const float2 logS = log_sum(all, sc), d = two_sum(D.x, -all.m);
+    const float2 logS = log_sum(all, sc), d = two_sum(xt, -all.m);
     float2 logp = ff_add(ff_mul(d, make_float2(a.inv_hi, a.inv_lo)), make_float2(-logS.x, -logS.y));
-    if (!(fabsf(logp.x) < INFINITY)) logp = make_float2((float)(((double)D.x - (double)all.m) * a.inv_tau) - logS.x, 0.f);
+    if (!(fabsf(logp.x) < INFINITY)) logp = make_float2((float)(((double)xt - (double)all.m) * a.inv_tau) - logS.x, 0.f);
     if (fabsf(logp.x) >= 0x1p24f) logp.y = 0.f;
     float g = 0.f, loss = 0.f, kl = 0.f;
     if (OP == LM_POLICY) {
@@ -531,7 +580,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
         for (int g = tid; g < (cut_bytes(L.G) + cut_batches(L.G, NT)) / 4; g += NT + 32) cut[g] = 0u;
         __syncthreads();
     }
-    float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
+    float2 Q = make_float2(0.f, 0.f), B = Q;
+    Part part{0.f, 0.f, Q};
+    float xt = 0.f;  // the target's logit, where this slice has it
     MS top{-INFINITY, 0.f};
     if (warp == NW) {
         if (OP == LM_DISTILL) {
@@ -547,9 +598,9 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
                 __syncthreads();  // the others can start
             }
             teacher_weights(a, zmax, eq, Q, B);
-            student_side<DT>(a, c0, c1, x, ex, eq, eid, sc, D, top);
+            student_side<DT>(a, c0, c1, x, ex, eq, eid, sc, L.CL > 1, part, top);
         } else if (m.tgt >= c0 && m.tgt < c1)
-            D.x = Elem<DT>::get(x[m.tgt]);
+            xt = Elem<DT>::get(x[m.tgt]);
     } else {
         if (TAIL) __syncthreads();
         Running r;
@@ -557,7 +608,6 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
         const MS w = ms_warp(r.result(), sc);
         if (lane == 0) rec[warp] = w;
     }
-    const float xt = D.x;  // the target's logit, where this slice has it
     if (L.CL > 1) cluster_wait_started();  // every CTA of the cluster is there to be stored to
     __syncthreads();
     MS r{-INFINITY, 0.f};
@@ -570,8 +620,13 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
             cluster_store(to + 4, r.s);
             cluster_store(to + 8, top.m);
             cluster_store(to + 12, top.s);
-            cluster_store(to + 16, D.x);
-            cluster_store(to + 20, D.y);
+            if (OP == LM_DISTILL) {
+                cluster_store(to + 16, part.X);
+                cluster_store(to + 20, part.Q);
+                cluster_store(to + 24, part.D.x);
+                cluster_store(to + 28, part.D.y);
+            } else
+                cluster_store(to + 16, xt);
         }
         __syncwarp();
     }
@@ -579,24 +634,26 @@ __global__ void __launch_bounds__((NW + 1) * 32, NW == 4 ? (OP == LM_LOGPROB ? 8
     if (warp == NW) {
         if (L.CL > 1) {
             r = top = MS{-INFINITY, 0.f};
-            D = make_float2(0.f, 0.f);
+            part = Part{0.f, 0.f, make_float2(0.f, 0.f)};
             if (lane < L.CL) {
                 const float* p = mail[lane];
                 r = MS{p[0], p[1]};
                 top = MS{p[2], p[3]};
-                D = make_float2(p[4], p[5]);
+                if (OP == LM_DISTILL) part = Part{p[4], p[5], make_float2(p[6], p[7])};
+                else xt = p[4];
             }
             r = ms_warp(r, sc);
-            if (OP == LM_DISTILL) {
-                if (TAIL) top = ms_warp(top, sc);
-                D = ff_sum_or_far(D);
-            } else
-                D.x = warp_sum(D.x);  // the one slice that has the target gave its logit
+            if (TAIL) top = ms_warp(top, sc);
+            if (OP != LM_DISTILL) xt = warp_sum(lane < L.CL ? xt : 0.f);  // the one slice that has the target gave its logit
         }
-        row_finish<OP>(a, row, m, r, top, Q, B, D, sc, rank == 0 && lane == 0, [&](const RowCoef& k) {
+        const auto distance = [&](float M) {
+            return L.CL > 1 ? ff_sum_or_far(part.distance(M)) : row_distance(a, ex, eq, part, Q, M);
+        };
+        const auto publish = [&](const RowCoef& k) {
             if (lane == 0) coef = k;
             if (grow) __syncthreads();  // the streaming warps go on while the losses are finished
-        });
+        };
+        row_finish<OP>(a, row, m, r, top, Q, B, xt, sc, rank == 0, publish, distance);
         if (!grow) return;
     } else {
         if (!grow) return;
@@ -648,7 +705,9 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
         const int g = lane + 32 * i;
         v[i] = g < s.ng ? load16(s.src + g, policy) : nothing<DT>();
     }
-    float2 Q = make_float2(0.f, 0.f), B = Q, D = Q;
+    float2 Q = make_float2(0.f, 0.f), B = Q;
+    Part part;
+    float xt = 0.f;
     MS top{-INFINITY, 0.f};
     if (OP == LM_DISTILL) {
         teacher_weights(a, teacher_entries<DT, 4>(a, row, s.e0, s.e0 + s.ng * N, x, ex, eq, eid), eq, Q, B);
@@ -662,9 +721,9 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
                 }
         }
         __syncwarp();
-        student_side<DT>(a, s.e0, s.e0 + s.ng * N, x, ex, eq, eid, sc, D, top);
+        student_side<DT>(a, s.e0, s.e0 + s.ng * N, x, ex, eq, eid, sc, false, part, top);
     } else
-        D.x = Elem<DT>::get(x[m.tgt]);
+        xt = Elem<DT>::get(x[m.tgt]);
     Running run;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -687,7 +746,8 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
             run.template add<DT>(w, sc);
         }
     const MS r = ms_warp(run.result(), sc);
-    const RowCoef c = row_finish<OP>(a, row, m, r, top, Q, B, D, sc, lane == 0, [](const RowCoef&) {});
+    const RowCoef c = row_finish<OP>(a, row, m, r, top, Q, B, xt, sc, true, [](const RowCoef&) {},
+                                      [&](float M) { return row_distance(a, ex, eq, part, Q, M); });
     if constexpr (OP != LM_LOGPROB) {
         if (!grow) return;
 #pragma unroll
@@ -706,7 +766,7 @@ __global__ void __launch_bounds__(SHORT_NW * 32, R <= 4 ? 4 : R <= 8 ? 3 : 2) lm
             for (int k = lane; k < a.K; k += 32)
                 if (eid[k] >= 0) grow[eid[k]] = Elem<DT>::put(c.fa * c.prob(ex[k], sc) - c.fb * eq[k]);
         } else if (lane == 0)
-            grow[m.tgt] = Elem<DT>::put(c.fa * c.prob(D.x, sc) - c.fb);
+            grow[m.tgt] = Elem<DT>::put(c.fa * c.prob(xt, sc) - c.fb);
     }
 }
 

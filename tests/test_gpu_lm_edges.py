@@ -455,3 +455,58 @@ def test_policy_of_a_token_on_a_masked_column(sot, T, V, dtype, tau):
     rg, size = R.token_grad(host(x), tg.cpu().numpy(), tau, -host(adv) * np.exp(u) - 0.1 * np.expm1(-u))
     # the coefficient moves by (|A| + 0.1) times the error of u, ATOL: 0.3 GTOL of it
     close_grad(grad, rg, 2.0 * size, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,V", [(16, 100), (16, 60000), (200, 5003)])
+@pytest.mark.parametrize("tau", [1.0, 2.0, 0.75])
+def test_distillation_of_rows_far_from_zero(sot, T, V, dtype, tau):
+    """A row's loss does not change with the level of its logits: all columns at one masked value, half of them far
+    below it, or usual logits moved far away."""
+    levels = {"f32": [-1e4, -1e9, -1.7e38, -3.4028234663852886e38], "f16": [-1e4, -32752.0, -65504.0, 3e4],
+              "bf16": [-1e4, -1e9, -1.7e38, -3.3895313892515355e38]}[dtype]
+    x = rows(T, V, dtype, 0, V)
+    for t in range(T):
+        c, kind = levels[t % 4], t // 4 % 4
+        if kind == 0:
+            x[t] = c
+        elif kind == 1 and abs(c) < 3e4:
+            x[t] = x[t] + c
+        elif kind == 2:
+            x[t] = c
+            x[t, V // 2:] = -INF
+        elif kind == 3 and abs(c) < 3e38 and dtype != "f16":
+            x[t] = c
+            x[t, V // 2:] = 1.25 * c
+    g = torch.Generator().manual_seed(5)
+    for K in (1, 8, 40):
+        ids = torch.stack([torch.randperm(V // 2 - 1, generator=g)[:K] for _ in range(T)])
+        z = torch.log_softmax(torch.randn(T, K, generator=g), 1).sub(0.3).cuda()
+        w = torch.ones(T).cuda()
+        for tail in ((False, True) if tau == 1.0 else (False,)):
+            loss, _ = sot.sot_distill_topk(x, ids.cuda(), z, weight=w, temperature=tau, tail=tail)
+            rl, _, _ = R.distill(host(x), ids.numpy(), host(z), host(w), tau, tail)
+            # the terms of a KL divergence are as large as the log-probabilities, at most 64 here
+            alike(loss, rl, 4.0 * tau * tau * (ATOL + RTOL * 64.0))
+    # entries on the lower half: as large a loss as their distance, to the rounding of its terms
+    ids = torch.full((T, 2), V - 1)
+    ids[:, 0] = 3
+    z = torch.log(torch.tensor([[0.4, 0.3]] * T)).cuda()
+    for tail in ((False, True) if tau == 1.0 else (False,)):
+        loss, _ = sot.sot_distill_topk(x, ids.cuda(), z, weight=torch.ones(T).cuda(), temperature=tau, tail=tail)
+        rl, _, _ = R.distill(host(x), ids.numpy(), host(z), np.ones(T), tau, tail)
+        far = np.abs(np.where(np.isfinite(rl), rl, 0.0))
+        alike(loss, np.where(far < 3e37, rl, np.nan_to_num(host(loss))) if (far >= 3e37).any() else rl,
+              4.0 * tau * tau * (ATOL + RTOL * 64.0) + 8.0 * RTOL * far)
+
+
+def test_distillation_with_the_rest_at_the_lowest_value(sot):
+    """The rest of the vocabulary masked with the type's lowest value: its log-probability is that value."""
+    low = torch.finfo(torch.float32).min
+    for V in (60, 40000):
+        x = torch.full((1, V), low).cuda()
+        x[0, :2] = 1.0
+        z = torch.log(torch.tensor([[0.5, 0.375]])).cuda()
+        loss, _ = sot.sot_distill_topk(x, torch.tensor([[0, 1]]).cuda(), z, weight=torch.ones(1).cuda(), tail=True)
+        want = 0.125 * -float(low)  # everything else is far below its rounding
+        assert abs(loss.item() - want) <= 2.0 ** -20 * want
