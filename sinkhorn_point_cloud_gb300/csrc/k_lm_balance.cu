@@ -253,7 +253,8 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
         T* const grow = static_cast<T*>(a.grad) + t * a.ldg;
         const bool aligned = !SHIFT || same_granules<T>(row, grow);
         // (the weights of a token that is left out are 0)
-        const float k = now ? inv_n * inv_s : 0.f, bias = now ? (2.f * a.z_coef * lse - dot) * k : 0.f;
+        // (k first: the coefficient times lse may be out of range where their share of N tokens is not)
+        const float k = now ? inv_n * inv_s : 0.f, bias = now ? fmaf(2.f * k * a.z_coef, lse, -dot * k) : 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int g = sub + i * lanes;

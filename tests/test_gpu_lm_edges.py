@@ -510,3 +510,17 @@ def test_distillation_with_the_rest_at_the_lowest_value(sot):
         loss, _ = sot.sot_distill_topk(x, torch.tensor([[0, 1]]).cuda(), z, weight=torch.ones(1).cuda(), tail=True)
         want = 0.125 * -float(low)  # everything else is far below its rounding
         assert abs(loss.item() - want) <= 2.0 ** -20 * want
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E", [(600, 64), (600, 61), (6000, 64)])
+def test_z_gradient_of_rows_at_the_lowest_value(sot, T, E, dtype):
+    """The coefficient times the log-sum-exp is out of range, the gradient 1 / (N E) of it is not."""
+    x = rows(T, E, dtype, 0, seed=E)
+    x[::2] = torch.finfo(x.dtype).min
+    ids = x.float().topk(2, 1).indices.int().contiguous()
+    counts, loss, grad = sot.sot_balance_loss(x, ids, balance_coef=1.0, z_coef=300.0)
+    rc, rl, rg, size = R.balance(host(x), ids.cpu().numpy(), None, 1.0, 300.0)
+    assert np.abs(rg).max() < 3e38
+    alike(loss, [rl[0], INF], ATOL * np.abs(rl))
+    close_grad(grad, rg, size, dtype)
