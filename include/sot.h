@@ -317,7 +317,9 @@ int sot_grad_x_coo(const float* X, const float* Y, int B, int n, int m, int d,
  *     which blocks run.
  * With y = x / temperature: lse = log sum_v exp(y_v), p_v = exp(y_v - lse).
  * A logit of -inf is a masked column (p = 0).  A row in use whose logits are all
- * -inf, or hold NaN or +inf, gives NaN.  All calls are asynchronous.
+ * -inf, or hold NaN or +inf, gives NaN (its lse is -inf where all are -inf).  Masks
+ * by a finite value, down to the type's lowest, are logits like any other.  All
+ * calls are asynchronous.
  */
 enum sot_dtype { SOT_F32 = 0, SOT_F16 = 1, SOT_BF16 = 2, SOT_I32 = 3, SOT_I64 = 4 };
 

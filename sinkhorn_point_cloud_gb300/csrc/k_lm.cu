@@ -13,10 +13,10 @@ namespace {
 // dx_v = (g / tau) (1[v = target] - p_v).  No statistic is missing, so every
 // granule stands alone: one read and one write per logit, memory-bound.  A
 // thread's loads go in batches of four, eight granules a thread; only the granule
-// that holds the target looks at its columns (one at a time in all of them: 327 us).  With the
-// log-probabilities' pass before it and the paired loss between (a pair's sums are
-// needed before any of its gradients, so the logits are read twice), 10388 x 32768
-// bf16 take 321 us, 0.94 of the copy bandwidth for the 2.04 GB this moves.
+// that holds the target looks at its columns (one at a time in all of them takes 6 us more).
+// 10388 x 32768 bf16: 198 us, the copy bandwidth (1.02).  With the log-probabilities' pass before
+// it and the paired loss between, three launches that each run over the whole batch and so
+// read the logits twice, 308 us, 0.98 of the copy bandwidth for the 2.04 GB this moves.
 constexpr int GRAD_NT = 256;
 
 template <int DT>
@@ -223,6 +223,7 @@ cudaError_t launch_lm_row(LmOp op, const LmRowArgs& a, int sms, cudaStream_t st)
     if (a.T == 0) return cudaSuccess;
     LmRowPlan p;
     const bool whole = (unsigned long long)a.x % 16 == 0 && a.ld % row_granule(a.dtype) == 0;
+    // (Losses alone are cut as they are with their gradient: the same sums, so the same bits.)
     row_plan(op != LM_LOGPROB, whole, a.T, a.dtype, a.V, a.K, a.tail != 0, sms, &p);
     if (a.T * p.CL > 0x7fffffffll) return cudaErrorInvalidValue;
     const LmRowLaunch L = {p.CL, p.G};

@@ -16,11 +16,11 @@
 // the sums.
 //   Weights are formed against 0, which needs no maximum first, and against the
 // row's maximum only where their sum leaves the middle of the range.
-//   Measured: 65536 x 256 bf16, 8 choices, a tenth left out: 17.9 us, 0.54 of the copy
-// bandwidth for 66 MB (with the maximum first 19.8 us); the counting and the waits
-// around it take 5 us of it, the rest is each warp's seven dependent steps of load,
-// sums and store.  65536 x 256 fp32: 29.6 us (0.68); 65536 x 500 fp16: 37 us (0.53);
-// 256 x 64 fp32: 6 us.  Loads into shared memory several steps ahead and more, lighter
+//   Measured on the GPU: 65536 x 256 bf16, 8 choices, a tenth left out: 19.6 us, 0.50 of
+// the copy bandwidth for 66 MB, and 17.2 us where L2 holds them (with the maximum first
+// 2 us more); the counting and the waits around it take 5 us of it, the rest is each
+// warp's seven dependent steps of load, sums and store.  65536 x 256 fp32: 29.4 us (0.65);
+// 65536 x 500 fp16: 36.7 us (0.51); 256 x 64 fp32: 5.7 us.  Loads into shared memory several steps ahead and more, lighter
 // CTAs were no faster.
 // A power of two of lanes takes a row, four granules of 16 bytes a lane (fewer
 // for few experts, more for many), as many rows at a time as fit a warp.
@@ -141,8 +141,8 @@ __device__ __forceinline__ void balance_rows(const LmBalanceArgs& a, long long w
         }
     };
     // With whole granules a lane's experts are the same in every row: from 32 of them a
-    // lane their shares stay in registers (65536 x 256 bf16 17.9 us, read again for every
-    // row 19.0); with fewer the registers pay for more warps (65536 x 64: 12.3 and 13.0).
+    // lane their shares stay in registers (65536 x 256 bf16 in L2 17.2 us, read again for every
+    // row 1.1 us more); with fewer the registers pay for more warps (65536 x 64: 12.3 and 13.0).
     constexpr bool OWN = !SHIFT && H >= 16;
     float2 own[OWN ? H : 1];
     if constexpr (OWN) {
@@ -484,9 +484,9 @@ cudaError_t launch_d(const LmBalanceArgs& a, int blocks, cudaStream_t st) {
 LmBalancePlan lm_balance_plan(long long T, int E, int K, int dtype, int sms) {
     LmBalancePlan p = {};
     const long long bytes = T * ((long long)E * (dtype == SOT_F32 ? 4 : 2) + 4ll * K);
-    // One cluster up to 512 KB of logits and choices: 1024 x 256 bf16 takes 9.7 us on
-    // the GPU against 7.6 us, but one launch and no scratch instead of two launches and
-    // an allocation, 8 us less on the host.
+    // One cluster up to 512 KB of logits and choices: 900 x 256 bf16 with 8 choices takes 7.8 us
+    // on the GPU against 8.1 us, and one launch without scratch instead of two launches
+    // and an allocation is 5 us less on the host.
     if (bytes <= 512 * 1024) {
         const long long want = (T + CNT_NT / 32 - 1) / (CNT_NT / 32);
         p.blocks = 1;

@@ -11,26 +11,26 @@
 // again, from L2, where it still is: the rows under way at one time take 40 to 60
 // of the 129 MB, and the first pass asks L2 to keep them while the stores and the
 // second pass ask for nothing to be kept (counted: DRAM reads are the logits
-// once, 0.5386 GB for 0.5369 GB).  Several CTAs share an SM and are in different
+// once, 0.2697 GB for 0.2684 GB).  Several CTAs share an SM and are in different
 // phases, so loads, reductions and stores of different rows overlap without any
 // hand-over inside a CTA.  A warp of its own prepares the teacher's side during
 // the first pass, joins the statistics (with the cluster's other CTAs through
 // distributed shared memory) and forms the loss and the gradient's coefficients.
-//   Measured, of 6779 GB/s of copy bandwidth: log-probabilities of 16384 x 32000
-//   bf16 in 154 us (1.00); policy loss of 8192 x 65536, a third of the rows left out,
-//   in 283 us (0.93); distillation of 4096 x 131072 in 347 us (0.91).  Batches of a
-//   few waves of CTAs lose part of the last one: 3001 x 50021 fp16 in 110 us (0.77),
-//   1001 x 50021 fp32 with the tail in 78 us (0.66).  Few rows: 4 to 6 us, the
+//   Measured on the GPU, of 6779 GB/s of copy bandwidth: log-probabilities of 16384 x
+//   32000 bf16 in 155 us (1.00); policy loss of 8192 x 65536, a third of the rows left
+//   out, in 276 us (0.95); distillation of 4096 x 131072 in 340 us (0.93).  Batches of a
+//   few waves of CTAs lose part of the last one: 3001 x 50021 fp16 in 103 us (0.82),
+//   1001 x 50021 fp32 with the tail in 72 us (0.72).  Few rows: 4 to 6 us, the
 //   latency of one launch, one load, a reduction across the cluster and one store.
-//   Also tried: slices resident in shared memory, copied in bulk by warps of their
+//   Also tried (347 us for the distillation then): slices resident in shared memory, copied in bulk by warps of their
 //   own (465 us for the distillation: a row's slices wait for one another), a ring
 //   of chunks (519 us: 0.4 us of hand-overs a chunk), a resident grid that walks the
 //   rows (442 us).
 //
 // lm_short_kernel: short rows, a warp each, kept in registers between the passes.
-//   16384 rows of 2048 bf16: 31 us with gradient (0.64), 21 us without; a CTA a row
-//   takes 73 and 46 us.  Distillation with 8 entries 45 us, with the tail 54 us: the
-//   chain of the entries' loads and sums is what a row waits for.
+//   16384 rows of 2048 bf16: policy loss 28 us with gradient (0.71), 18 us without; with a
+//   CTA a row it was 73 and 46 us.  Distillation with 8 entries 44 us, with the tail 50
+//   us: the chain of the entries' loads and sums is what a row waits for.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -318,7 +318,7 @@ __device__ __forceinline__ RowCoef row_finish(const LmRowArgs& a, long long row,
         if (write) {
             // With y = (x - m) / tau and S = sum exp y over the row, R over what is not an entry:
             //   log p = y - log S,  log p_r = (m_r - m) / tau + log R - log S.
-            // In pairs of floats: with doubles throughout, 16384 rows of 2048 take 57 us, so 45.
+            // In pairs of floats: with doubles throughout, 16384 rows of 2048 take 12 us more.
             const bool tail = a.tail && !(qr <= 0.f);
             const float2 inv_tau = make_float2(a.inv_hi, a.inv_lo), logS = log_sum(all, sc);
             const float2 logR = tail ? log_sum(r, sc) : logS, logq = tail ? log_ff(qr) : logS;
