@@ -419,6 +419,77 @@ int sot_balance_loss(const void* logits, long long T, int E, long long ld, int d
                      int K, const unsigned char* mask, float balance_coef, float z_coef, int* counts, float* loss,
                      void* grad, long long ld_grad, void* stream);
 
+/* ---- language-model operators around the losses --------------------------- */
+/*
+ * Scores of given tokens with entropies and the best alternatives, in one pass
+ * over the logits (conventions as above):
+ *   logp[t] = y[t][target[t]] - lse[t],   entropy[t] = -sum_v p_v log p_v,
+ *   ids[t][0 .. K-1]: the columns of the K largest logits, largest first and the
+ *     lower column first among equal ones;  top_logp[t][k] their log-probabilities.
+ * 0 <= K <= 1024.  Masked columns (-inf) are no alternatives: where a row has fewer than K others, the rest of
+ * its entries are -1 with log-probability -inf.  ids and top_logp are what sot_distill_topk takes as its teacher.
+ * target NULL: every row takes part (logp must be NULL then).  A target outside
+ * [0, V) leaves its row out: not read, logp = lse = entropy = top_logp = 0, ids -1.
+ * A row in use without a log-sum-exp (all -inf, NaN or +inf) has NaN for entropy, logp and top_logp, and ids -1.
+ * Any output may be NULL, not all of them.  SOT_ERR_UNSUPPORTED with K > 0 above 16 million 16-bit or 8
+ * million 32-bit columns (the largest logits of a row's parts are kept in shared memory).
+ */
+int sot_token_topk(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                   const void* target, int target_type, int K, float* logp, float* lse, float* entropy, int* ids,
+                   float* top_logp, void* stream);
+
+/*
+ * Its gradient, from the lse and entropy it wrote and the gradients with respect to its outputs
+ * (grad_logp [T], grad_entropy [T], grad_top [T][K]; NULL: 0):
+ *   grad[t][v] = 1 / temperature (g_v - p_v sum g - grad_entropy[t] p_v (log p_v + entropy[t])),
+ *   g_v = grad_logp[t] [v = target[t]] + sum_k grad_top[t][k] [v = ids[t][k]].
+ * ids[t][k] outside [0, V) is an unused entry; the used ones of a row are distinct (a row that repeats one has an
+ * unspecified result).  Rows left out, and rows whose incoming gradients are all 0, are written as zeros without being
+ * read.  entropy may be NULL where grad_entropy is.  Probabilities are as good as the lse: 2^-24 of its size.
+ * grad may be the logits' own array with the same stride.
+ */
+int sot_token_topk_grad(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                        const void* target, int target_type, const float* lse, const float* entropy,
+                        const float* grad_logp, const float* grad_entropy, const int* ids, int K, const float* grad_top,
+                        void* grad, long long ld_grad, void* stream);
+
+/*
+ * Embedding lookup with scaling: out[t] = scale table[ids[t]], rounded once to out_type.  table [V][D] has row
+ * stride ld, out [T][D] row stride ld_out (in elements; both >= D), each a float type of its own.  An id outside
+ * [0, V) gives a row of zeros.  out must not overlap table.
+ */
+int sot_embed(const void* table, int V, int D, long long ld, int type, const void* ids, int ids_type, long long T,
+              float scale, void* out, long long ld_out, int out_type, void* stream);
+
+/*
+ * Its gradient with respect to the table, tokens sorted by row:
+ *   grad[v] = scale sum of grad_out[t] over the tokens t with ids[t] = v
+ * summed in 32 bits in the order of the tokens (in fixed pieces where a row has many) and rounded once to grad_type;
+ * the same bits on every call.  accumulate = 0 writes all V rows (zeros where no token names one);
+ * accumulate != 0 adds to grad the rows that tokens name and leaves the others untouched.  Tokens whose
+ * id lies outside [0, V) take no part.  grad must not overlap grad_out.  T < 2^31.
+ */
+int sot_embed_grad(const void* grad_out, long long T, int D, long long ld, int type, const void* ids, int ids_type,
+                   int V, float scale, int accumulate, void* grad, long long ld_grad, int grad_type, void* stream);
+
+/*
+ * A routed layer for a few tokens (T <= 128), from the router to the joined output.  x [T][H] (row stride ld), router
+ * [E][H], gate_up [E][2 F][H] (an expert's gate rows, then its up rows) and down [E][H][F] have one float type; bias [E]
+ * float or NULL.
+ *   logits[t][e] = x_t . router_e + bias_e         (to 32 bits, whatever the order of the sum)
+ *   ids[t]       = the K experts with the largest logits, largest first, the lower one first among equal ones
+ *   weights[t]   = scale softmax(logits[t]) at these, divided by their sum where renorm != 0
+ *   out[t]       = sum_k weights[t][k] down_e (silu(gate_e x_t) * up_e x_t),  e = ids[t][k]
+ * 1 <= K <= min(E, 32), E <= 1024.  A logit of -inf (a bias of -inf) removes an expert; where a token has fewer than K
+ * left, the rest of its ids are -1 with weight 0.  A token with a logit of NaN or +inf has ids -1, weights NaN and an
+ * output of NaN.  Sums are held in 32 bits.
+ * logits, ids and weights are what sot_balance_loss takes and what a backward pass needs; out [T][H] has
+ * row stride ld_out and must not overlap the inputs.
+ */
+int sot_routed_layer(const void* x, int T, int H, long long ld, int dtype, const void* router, const float* bias, int E,
+                     const void* gate_up, const void* down, int F, int K, int renorm, float scale, void* out,
+                     long long ld_out, float* logits, int* ids, float* weights, void* stream);
+
 /*
  * Synchronous input validation: every coordinate finite, every weight finite
  * and > 0.  Returns SOT_OK, SOT_ERR_NONFINITE or SOT_ERR_INVALID_ARG.

@@ -115,6 +115,11 @@ def load(path: str | None = None):
         "sot_policy_loss": [P, ll, i, ll, i, f, P, i, P, P, P, P, f, f, f, P, P, P, P, ll, P],
         "sot_preference_loss": [P, P, P, i, P, i, ll, f, f, i, f, P, P, P, P],
         "sot_balance_loss": [P, ll, i, ll, i, P, i, i, P, f, f, P, P, P, ll, P],
+        "sot_token_topk": [P, ll, i, ll, i, f, P, i, i, P, P, P, P, P, P],
+        "sot_token_topk_grad": [P, ll, i, ll, i, f, P, i, P, P, P, P, P, i, P, P, ll, P],
+        "sot_embed": [P, i, i, ll, i, P, i, ll, f, P, ll, i, P],
+        "sot_embed_grad": [P, ll, i, ll, i, P, i, i, f, i, P, ll, i, P],
+        "sot_routed_layer": [P, i, i, ll, i, P, P, i, P, P, i, i, i, f, P, ll, P, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -667,6 +672,178 @@ def sot_balance_loss(logits, ids, mask=None, balance_coef=1.0, z_coef=0.0, grad=
             _check(rc, "sot_balance_loss")
         return counts, loss, g
     return call(_raw_stream(dev)) if stream is None else _on(stream, call)
+
+
+# ---- language-model operators around the losses ---------------------------------------------------------------------
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _run(dev, stream, call):
+    """call(handle) on the given stream, or on the current stream of the tensors' device, with that device current."""
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+        return _on(stream, call)
+    if _current_device() == dev:
+        return call(_raw_stream(dev))
+    with torch.cuda.device(dev):
+        return call(_raw_stream(dev))
+
+
+def sot_token_topk(logits, K, target=None, temperature=1.0, stream=None):
+    """Scores of given tokens with entropies and the best alternatives: (logp [T] or None, lse [T], entropy [T],
+    ids [T, K] int32, top_logp [T, K]) of logits [T, V].  ids are the columns of the K largest logits, largest first,
+    lower columns first among equal ones; entries that do not exist (masked by -inf, beyond V) are -1 with -inf.
+    They are what sot_distill_topk takes as its teacher.  A target outside [0, V) leaves its row out (0, ids -1);
+    without target every row takes part and logp is None."""
+    x, T, V, ld, dt, dev = _logits(logits)
+    tg, ty = (None, SOT_I32) if target is None else _indices(target, "target", (T,), dev)
+    K = int(K)
+    if K < 0:
+        raise ValueError("K must be >= 0")
+
+    def call(s):
+        lse = torch.empty(T, dtype=_F32, device=logits.device)
+        entropy = torch.empty_like(lse)
+        logp = None if target is None else torch.empty_like(lse)
+        top = torch.empty((T, K), dtype=_F32, device=logits.device)
+        ids = torch.empty((T, K), dtype=torch.int32, device=logits.device)
+        rc = load().sot_token_topk(x, T, V, ld, dt, temperature, tg, ty, K, None if logp is None else logp.data_ptr(),
+                                   lse.data_ptr(), entropy.data_ptr(), ids.data_ptr(), top.data_ptr(), s)
+        if rc:
+            _check(rc, "sot_token_topk")
+        return logp, lse, entropy, ids, top
+    return _run(dev, stream, call)
+
+
+def sot_token_topk_grad(logits, lse, entropy=None, target=None, grad_logp=None, grad_entropy=None, ids=None, grad_top=None,
+                        temperature=1.0, grad=True, stream=None):
+    """Gradient [T, V] (the logits' type) of sot_token_topk's outputs, from the lse and entropy it gave and the gradients
+    with respect to logp [T], entropy [T] and top_logp [T, K] (None: 0; grad_top needs the ids, int32).  ``grad`` may be a
+    tensor to write, the logits included."""
+    x, T, V, ld, dt, dev = _logits(logits)
+    tg, ty = (None, SOT_I32) if target is None else _indices(target, "target", (T,), dev)
+    l, h = _needed(lse, "lse", T, dev), _floats(entropy, "entropy", T, dev)
+    gl, gh = _floats(grad_logp, "grad_logp", T, dev), _floats(grad_entropy, "grad_entropy", T, dev)
+    i, K, gt = None, 0, None
+    if grad_top is not None:
+        if ids is None:
+            raise TypeError("grad_top needs ids")
+        i, ity, K = _pairs(ids, "ids", T, dev)
+        if ity != SOT_I32:
+            raise TypeError("ids must be int32")
+        gt = _indices_like(grad_top, "grad_top", ids)
+    if grad is None or grad is False:
+        raise TypeError("grad must be True or a tensor")
+
+    def call(s):
+        out, at, ldg = _grad_of(grad, logits, T, V, ld, dt, dev)
+        rc = load().sot_token_topk_grad(x, T, V, ld, dt, temperature, tg, ty, l, h, gl, gh, i, K, gt, at, ldg, s)
+        if rc:
+            _check(rc, "sot_token_topk_grad")
+        return out
+    return _run(dev, stream, call)
+
+
+def _indices_like(t, name, ids):
+    """Address of a float32 tensor of the shape of ids."""
+    if isinstance(t, torch.Tensor) and t.shape != ids.shape:
+        raise ValueError(f"{name} must have the shape of ids, {tuple(ids.shape)}, got {tuple(t.shape)}")
+    return _floats(t, name, ids.numel(), ids.get_device())
+
+
+def _matrix(t, name, rows, D, dev):
+    """(address, row stride, sot_dtype) of a tensor [rows, D] whose rows are contiguous, on this device."""
+    at, n, d, ld, dt, on = _logits(t, name)
+    if (n, d) != (rows, D):
+        raise ValueError(f"{name} must have shape {(rows, D)}, got {(n, d)}")
+    if on != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    return at, ld, dt
+
+
+def sot_embed(table, ids, scale=1.0, dtype=None, out=None, stream=None):
+    """Embedding lookup with scaling: out [T, D] = scale table[ids], rounded once; rows of zeros for ids outside
+    [0, V).  table [V, D] may have a row stride, ids is [T]; ``dtype`` (default the table's) is the type of a new out."""
+    x, V, D, ld, dt, dev = _logits(table, "table")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
+        raise ValueError("ids must be a torch.Tensor of shape [T]")
+    T = ids.shape[0]
+    i, ty = _indices(ids, "ids", (T,), dev)
+    if out is None and dtype is not None and dtype not in _FLOATS:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+
+    def call(s):
+        o = torch.empty((T, D), dtype=dtype or table.dtype, device=table.device) if out is None else out
+        at, ldo, ot = _matrix(o, "out", T, D, dev)
+        rc = load().sot_embed(x, V, D, ld, dt, i, ty, T, scale, at, ldo, ot, s)
+        if rc:
+            _check(rc, "sot_embed")
+        return o
+    return _run(dev, stream, call)
+
+
+def sot_embed_grad(grad_out, ids, V, scale=1.0, dtype=None, grad=None, accumulate=False, stream=None):
+    """Gradient [V, D] of sot_embed with respect to the table: scale times the sums of grad_out [T, D] over the tokens
+    of each row, tokens sorted by row, the same bits on every call.  ``grad`` may be a tensor to write; with ``accumulate``
+    the sums are added to it and rows that no token names stay untouched (with weights tied to the output head, its
+    gradient).  ``dtype`` (default grad_out's) is the type of a new gradient."""
+    x, T, D, ld, dt, dev = _logits(grad_out, "grad_out")
+    i, ty = _indices(ids, "ids", (T,), dev)
+    V = int(V)
+    if V < 1:
+        raise ValueError("V must be >= 1")
+    if accumulate and grad is None:
+        raise TypeError("accumulate needs a gradient to add to")
+    if grad is None and dtype is not None and dtype not in _FLOATS:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+
+    def call(s):
+        g = torch.empty((V, D), dtype=dtype or grad_out.dtype, device=grad_out.device) if grad is None else grad
+        at, ldg, gt = _matrix(g, "grad", V, D, dev)
+        rc = load().sot_embed_grad(x, T, D, ld, dt, i, ty, V, scale, 1 if accumulate else 0, at, ldg, gt, s)
+        if rc:
+            _check(rc, "sot_embed_grad")
+        return g
+    return _run(dev, stream, call)
+
+
+def sot_routed_layer(x, router, gate_up, down, K, bias=None, renorm=True, scale=1.0, out=None, stream=None):
+    """A routed layer for a few tokens (at most 128): (out [T, H], logits [T, E] float32, ids [T, K] int32, weights [T, K]
+    float32) of x [T, H], router [E, H], gate_up [E, 2 F, H], down [E, H, F] (one type) and bias [E] float32.
+    out = sum over a token's K best experts of weight * down (silu(gate x) * up x).  logits and ids go on to
+    sot_balance_loss."""
+    at, T, H, ld, dt, dev = _logits(x, "x")
+    if not isinstance(router, torch.Tensor) or router.dim() != 2:
+        raise ValueError("router must be a torch.Tensor of shape [E, H]")
+    E = router.shape[0]
+    if not isinstance(down, torch.Tensor) or down.dim() != 3:
+        raise ValueError("down must be a torch.Tensor of shape [E, H, F]")
+    F, K = down.shape[2], int(K)
+    if not isinstance(gate_up, torch.Tensor) or tuple(gate_up.shape) != (E, 2 * F, H) or tuple(down.shape) != (E, H, F) or \
+            router.shape[1] != H:
+        raise ValueError(f"x [T, H], router [E, H], gate_up [E, 2 F, H] and down [E, H, F] disagree: {tuple(x.shape)}, "
+                         f"{tuple(router.shape)}, {tuple(getattr(gate_up, 'shape', ()))}, {tuple(down.shape)}")
+    r = _floats(router, "router", E * H, dev, x.dtype)
+    gu, dn = _floats(gate_up, "gate_up", E * 2 * F * H, dev, x.dtype), _floats(down, "down", E * H * F, dev, x.dtype)
+    b = _floats(bias, "bias", E, dev)
+    if K < 1 or K > E:
+        raise ValueError(f"K must satisfy 1 <= K <= {E}")
+
+    def call(s):
+        o = torch.empty((T, H), dtype=x.dtype, device=x.device) if out is None else out
+        oat, ldo, ot = _matrix(o, "out", T, H, dev)
+        if ot != dt:
+            raise TypeError(f"out must be {x.dtype}, got {o.dtype}")
+        logits = torch.empty((T, E), dtype=_F32, device=x.device)
+        ids = torch.empty((T, K), dtype=torch.int32, device=x.device)
+        weights = torch.empty((T, K), dtype=_F32, device=x.device)
+        rc = load().sot_routed_layer(at, T, H, ld, dt, r, b, E, gu, dn, F, K, 1 if renorm else 0, scale, oat, ldo,
+                                     logits.data_ptr(), ids.data_ptr(), weights.data_ptr(), s)
+        if rc:
+            _check(rc, "sot_routed_layer")
+        return o, logits, ids, weights
+    return _run(dev, stream, call)
 
 
 def sot_async_status(stream=None):

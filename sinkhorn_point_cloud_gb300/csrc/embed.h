@@ -1,0 +1,40 @@
+// embed.h -- launch interface of the embedding lookup and of its gradient.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace sot {
+
+struct EmbedArgs {
+    const void* table;  // [V, D], row v at element v * ld
+    long long T, ld, ldo;
+    int V, D, type, out_type;
+    const void* ids;
+    int ids_type;
+    float scale;
+    void* out;  // [T, D]
+};
+
+struct EmbedGradArgs {
+    const void* g;  // [T, D], row t at element t * ld
+    long long T, ld, ldg;
+    int V, D, type, grad_type;
+    const void* ids;
+    int ids_type;
+    float scale;
+    int accumulate;
+    void* grad;  // [V, D]
+    // scratch: tokens sorted by row (two buffers), partial sums of rows that span chunks
+    unsigned *key[2], *pos[2];
+    float* part;
+};
+
+struct EmbedGradPlan {
+    int passes, bits;  // of the sort
+    long long chunks;
+    size_t key_at[2], pos_at[2], part_at, scratch;
+};
+EmbedGradPlan embed_grad_plan(long long T, int V, int D);
+cudaError_t launch_embed(const EmbedArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_embed_grad(EmbedGradArgs a, const EmbedGradPlan& p, unsigned char* scratch, int sms, cudaStream_t st);
+
+}  // namespace sot

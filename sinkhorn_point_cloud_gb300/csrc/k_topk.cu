@@ -1,0 +1,83 @@
+// k_topk.cu -- how the rows of the scores kernel (topk.cuh) and of its gradient are cut.
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "topk.cuh"
+
+namespace sot {
+
+namespace {
+
+int pow2_from(int n) {
+    int p = 2;
+    while (p < n) p *= 2;
+    return p;
+}
+
+void topk_plan(bool whole, const TopkArgs& a, int sms, TopkPlan* p) {
+    const int N = a.dtype == SOT_F32 ? 4 : 8;
+    const long long total = ((long long)a.V + (whole ? N - 1 : 2 * N - 2)) / N;  // granules of a row
+    int CL = 1;
+    p->NT = total <= 512 ? 32 : 256;
+    // Few rows: cut a row further, up to eight granules a thread and a CTA for each SM, as far as the
+    // slices' alternatives can be joined in one place.
+    if (p->NT > 32 && a.T < sms)
+        while (CL < ROW_MAX_CL && a.T * CL <= sms && total > CL * 2048ll && CL * a.K <= 1024) CL *= 2;
+    // (a slice's chunk maxima have to fit shared memory)
+    while (CL < ROW_MAX_CL && total > CL * 262144ll) CL *= 2;
+    const long long G = (total + CL - 1) / CL;
+    // Chunks of eight granules where that leaves twice as many chunks as alternatives, otherwise single ones.
+    p->U = G >= 16ll * a.K || G > 16384 ? 8 : 1;
+    p->L.CL = CL;
+    p->L.G = (int)G;
+    p->L.chunks = a.K ? (int)((G + p->U * p->NT - 1) / (p->U * p->NT)) * p->NT : 0;
+    const int most = (CL > 2 ? CL : 2) * a.K;  // candidates to sort, or slices' alternatives to join
+    p->L.cap = a.K ? pow2_from(most > 256 ? most : 256) : 0;
+    p->smem = sizeof(unsigned long long) * p->L.cap + sizeof(unsigned) * p->L.chunks;
+}
+
+}  // namespace
+
+bool topk_fits(int dtype, int V, int K) {
+    TopkArgs a = {};
+    a.T = 1ll << 31;
+    a.dtype = dtype;
+    a.V = V;
+    a.K = K;
+    TopkPlan p;
+    topk_plan(false, a, 1, &p);
+    return p.smem <= TOPK_MAX_SMEM;
+}
+
+cudaError_t launch_topk(const TopkArgs& a, int sms, cudaStream_t st) {
+    if (a.T == 0) return cudaSuccess;
+    TopkPlan p;
+    const bool whole = (unsigned long long)a.x % 16 == 0 && a.ld % (a.dtype == SOT_F32 ? 4 : 8) == 0;
+    topk_plan(whole, a, sms, &p);
+    if (a.T * p.L.CL > 0x7fffffffll || p.smem > TOPK_MAX_SMEM) return cudaErrorInvalidValue;
+    count_launches(1);
+    switch (a.dtype) {
+        case SOT_F32: return launch_topk_f32(a, p, st);
+        case SOT_F16: return launch_topk_f16(a, p, st);
+        default: return launch_topk_bf16(a, p, st);
+    }
+}
+
+cudaError_t launch_topk_grad(const TopkGradArgs& a, int sms, cudaStream_t st) {
+    if (a.T == 0) return cudaSuccess;
+    const int N = a.dtype == SOT_F32 ? 4 : 8;
+    const long long total = ((long long)a.V + 2 * N - 2) / N;
+    // Eight granules a thread, or four where that leaves SMs without work; more where
+    // the grid's limit asks for it.
+    long long G = (total + 2047) / 2048 * a.T < 2ll * sms ? 1024 : 2048;
+    while ((total + G - 1) / G * a.T > 0x7fffffffll) G *= 2;
+    const int chunks = (int)((total + G - 1) / G);
+    count_launches(1);
+    switch (a.dtype) {
+        case SOT_F32: return launch_topk_grad_f32(a, (int)G, chunks, st);
+        case SOT_F16: return launch_topk_grad_f16(a, (int)G, chunks, st);
+        default: return launch_topk_grad_bf16(a, (int)G, chunks, st);
+    }
+}
+
+}  // namespace sot

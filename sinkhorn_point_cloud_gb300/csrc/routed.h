@@ -1,0 +1,35 @@
+// routed.h -- launch interface of the routed layer for a few tokens.
+#pragma once
+#include <cuda_runtime.h>
+
+namespace sot {
+
+constexpr int ROUTED_MAX_T = 128;  // tokens of a call
+constexpr int ROUTED_MAX_E = 1024;
+constexpr int ROUTED_MAX_K = 32;   // experts of a token
+
+struct RoutedArgs {
+    const void* x;  // [T, H], row t at element t * ldx
+    long long ldx, ldo;
+    int T, H, E, F, K, dtype;
+    const void* router;   // [E, H]
+    const float* bias;    // [E] or NULL
+    const void* gate_up;  // [E, 2 F, H]
+    const void* down;     // [E, H, F]
+    int renorm;
+    float scale;
+    void* out;       // [T, H]
+    float* logits;   // [T, E]
+    int* ids;        // [T, K]
+    float* weights;  // [T, K]
+    // scratch
+    float *h, *y;    // [T K, F], [T K, H]
+};
+
+struct RoutedPlan {
+    size_t h_at, y_at, scratch;
+};
+RoutedPlan routed_plan(const RoutedArgs& a, int sms);
+cudaError_t launch_routed(RoutedArgs a, const RoutedPlan& p, unsigned char* scratch, int sms, cudaStream_t st);
+
+}  // namespace sot

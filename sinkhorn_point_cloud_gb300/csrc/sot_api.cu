@@ -20,7 +20,10 @@
 #include "sot.h"
 #include "apml.h"
 #include "hvp.h"
+#include "embed.h"
 #include "lm.h"
+#include "routed.h"
+#include "topk.h"
 #include "tc.h"
 #include "transport.h"
 
@@ -1602,6 +1605,15 @@ void set_temperature(LmRowArgs& a, float tau) {
     a.inv_hi = (float)a.inv_tau;
     a.inv_lo = (float)(a.inv_tau - (double)a.inv_hi);
 }
+// Rows of D elements with a row stride.
+int check_matrix(const char* name, const void* p, long long rows, int D, long long ld, int type, bool needed) {
+    SOT_TRY(check_float_type(name, type));
+    if (rows < 0 || D < 1) return fail(SOT_ERR_INVALID_ARG, "%s: sizes must satisfy rows >= 0 and columns >= 1 (got %lld, %d)", name, rows, D);
+    if (rows >= (1LL << 31)) return fail(SOT_ERR_INVALID_ARG, "%s: rows must be < 2^31 (got %lld)", name, rows);
+    if (rows > 0 && (ld < D || ld >= (1LL << 30)))
+        return fail(SOT_ERR_INVALID_ARG, "%s: the row stride must be at least %d and below 2^30 (got %lld)", name, D, ld);
+    return needed ? check_pointer(name, p, type) : SOT_OK;
+}
 int check_temperature(float tau) {
     if (!(tau > 0.f) || !std::isfinite(tau) || !std::isfinite(1.4426951f / tau))
         return fail(SOT_ERR_INVALID_ARG, "temperature must be finite and > 0");
@@ -1812,6 +1824,190 @@ int sot_balance_loss(const void* logits, long long T, int E, long long ld, int d
     if (p.scratch && !(scratch = S.alloc<unsigned char>(p.scratch)))
         return fail(SOT_ERR_NOMEM, "scratch allocation failed");
     SOT_CUDA(launch_lm_balance(a, p, scratch, (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+// ---- operators around the losses (k_topk.cu, k_embed.cu, k_routed.cu) ----
+
+int sot_token_topk(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                   const void* target, int target_type, int K, float* logp, float* lse, float* entropy, int* ids,
+                   float* top_logp, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_rows(logits, T, V, ld, dtype, nullptr, 0));
+    SOT_TRY(check_temperature(temperature));
+    if (target) SOT_TRY(check_index_type("target_type", target_type));
+    if (K < 0 || K > TOPK_MAX_K) return fail(SOT_ERR_INVALID_ARG, "K must satisfy 0 <= K <= %d (got %d)", TOPK_MAX_K, K);
+    if (K && !topk_fits(dtype, V, K))
+        return fail(SOT_ERR_UNSUPPORTED, "the alternatives of rows of %d columns do not fit shared memory", V);
+    if (T == 0) return SOT_OK;
+    if (target) SOT_TRY(check_pointer("target", target, target_type));
+    if (logp && !target) return fail(SOT_ERR_INVALID_ARG, "logp needs target");
+    if (!logp && !lse && !entropy && !(K && (ids || top_logp))) return fail(SOT_ERR_INVALID_ARG, "no output is wanted");
+    if (K && T * K >= (1LL << 40)) return fail(SOT_ERR_INVALID_ARG, "T K must be < 2^40");
+    TopkArgs a = {};
+    a.x = logits;
+    a.T = T;
+    a.ld = ld;
+    a.V = V;
+    a.dtype = dtype;
+    a.tau = temperature;
+    a.inv_tau = 1.0 / (double)temperature;
+    a.inv_hi = (float)a.inv_tau;
+    a.inv_lo = (float)(a.inv_tau - (double)a.inv_hi);
+    a.target = target;
+    a.target_type = target_type;
+    a.K = ids || top_logp ? K : 0;
+    a.logp = logp;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.ids = ids;
+    a.top = top_logp;
+    SOT_CUDA(launch_topk(a, device_sms(), (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_token_topk_grad(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
+                        const void* target, int target_type, const float* lse, const float* entropy,
+                        const float* grad_logp, const float* grad_entropy, const int* ids, int K, const float* grad_top,
+                        void* grad, long long ld_grad, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_rows(logits, T, V, ld, dtype, grad, ld_grad));
+    SOT_TRY(check_temperature(temperature));
+    if (target) SOT_TRY(check_index_type("target_type", target_type));
+    if (K < 0 || K > TOPK_MAX_K) return fail(SOT_ERR_INVALID_ARG, "K must satisfy 0 <= K <= %d (got %d)", TOPK_MAX_K, K);
+    if (T == 0) return SOT_OK;
+    if (target) SOT_TRY(check_pointer("target", target, target_type));
+    SOT_TRY(check_pointer("grad", grad, dtype));
+    if (!lse) return fail(SOT_ERR_INVALID_ARG, "lse must not be NULL");
+    if (grad_logp && !target) return fail(SOT_ERR_INVALID_ARG, "grad_logp needs target");
+    if (grad_entropy && !entropy) return fail(SOT_ERR_INVALID_ARG, "grad_entropy needs entropy");
+    if (grad_top && K && !ids) return fail(SOT_ERR_INVALID_ARG, "grad_top needs ids");
+    TopkGradArgs a = {};
+    a.x = logits;
+    a.T = T;
+    a.ld = ld;
+    a.ldg = ld_grad;
+    a.V = V;
+    a.dtype = dtype;
+    a.tau = temperature;
+    a.target = target;
+    a.target_type = target_type;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.g_logp = grad_logp;
+    a.g_entropy = grad_entropy;
+    a.ids = ids;
+    a.g_top = K ? grad_top : nullptr;
+    a.K = K;
+    a.grad = grad;
+    SOT_CUDA(launch_topk_grad(a, device_sms(), (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_embed(const void* table, int V, int D, long long ld, int type, const void* ids, int ids_type, long long T,
+              float scale, void* out, long long ld_out, int out_type, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_matrix("table", table, V, D, ld, type, T > 0));
+    SOT_TRY(check_matrix("out", out, T, D, ld_out, out_type, T > 0));
+    SOT_TRY(check_index_type("ids_type", ids_type));
+    if (!std::isfinite(scale)) return fail(SOT_ERR_INVALID_ARG, "scale must be finite");
+    if (V < 1) return fail(SOT_ERR_INVALID_ARG, "V must be >= 1 (got %d)", V);
+    if (T == 0) return SOT_OK;
+    SOT_TRY(check_pointer("ids", ids, ids_type));
+    EmbedArgs a = {};
+    a.table = table;
+    a.T = T;
+    a.ld = ld;
+    a.ldo = ld_out;
+    a.V = V;
+    a.D = D;
+    a.type = type;
+    a.out_type = out_type;
+    a.ids = ids;
+    a.ids_type = ids_type;
+    a.scale = scale;
+    a.out = out;
+    SOT_CUDA(launch_embed(a, device_sms(), (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_embed_grad(const void* grad_out, long long T, int D, long long ld, int type, const void* ids, int ids_type,
+                   int V, float scale, int accumulate, void* grad, long long ld_grad, int grad_type, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_matrix("grad_out", grad_out, T, D, ld, type, T > 0));
+    SOT_TRY(check_matrix("grad", grad, V, D, ld_grad, grad_type, T > 0 || !accumulate));
+    SOT_TRY(check_index_type("ids_type", ids_type));
+    if (!std::isfinite(scale)) return fail(SOT_ERR_INVALID_ARG, "scale must be finite");
+    if (V < 1 || V == 0x7fffffff) return fail(SOT_ERR_INVALID_ARG, "V must satisfy 1 <= V < 2^31 - 1 (got %d)", V);
+    if (T > 0) SOT_TRY(check_pointer("ids", ids, ids_type));
+    if (T == 0 && accumulate) return SOT_OK;
+    EmbedGradArgs a = {};
+    a.g = grad_out;
+    a.T = T;
+    a.ld = ld;
+    a.ldg = ld_grad;
+    a.V = V;
+    a.D = D;
+    a.type = type;
+    a.grad_type = grad_type;
+    a.ids = ids;
+    a.ids_type = ids_type;
+    a.scale = scale;
+    a.accumulate = accumulate != 0;
+    a.grad = grad;
+    Scratch S((cudaStream_t)stream);
+    const EmbedGradPlan p = embed_grad_plan(T, V, D);
+    unsigned char* scratch = S.alloc<unsigned char>(p.scratch);
+    if (!scratch) return fail(SOT_ERR_NOMEM, "scratch allocation failed");
+    SOT_CUDA(launch_embed_grad(a, p, scratch, device_sms(), (cudaStream_t)stream));
+    return SOT_OK;
+}
+
+int sot_routed_layer(const void* x, int T, int H, long long ld, int dtype, const void* router, const float* bias, int E,
+                     const void* gate_up, const void* down, int F, int K, int renorm, float scale, void* out,
+                     long long ld_out, float* logits, int* ids, float* weights, void* stream) {
+    g_err[0] = 0;
+    SOT_TRY(check_matrix("x", x, T, H, ld, dtype, T > 0));
+    SOT_TRY(check_matrix("out", out, T, H, ld_out, dtype, T > 0));
+    if (T > ROUTED_MAX_T)
+        return fail(SOT_ERR_UNSUPPORTED, "the routed layer takes at most %d tokens a call (got %d)", ROUTED_MAX_T, T);
+    if (E < 1 || F < 1 || K < 1 || K > E)
+        return fail(SOT_ERR_INVALID_ARG, "sizes must satisfy E, F >= 1 and 1 <= K <= E (got E=%d F=%d K=%d)", E, F, K);
+    if (E > ROUTED_MAX_E || K > ROUTED_MAX_K)
+        return fail(SOT_ERR_UNSUPPORTED, "at most %d experts and %d of them a token (got E=%d K=%d)", ROUTED_MAX_E,
+                    ROUTED_MAX_K, E, K);
+    if (H > 1 << 20 || F > 1 << 20) return fail(SOT_ERR_UNSUPPORTED, "H and F must be <= 2^20 (got H=%d F=%d)", H, F);
+    if (!std::isfinite(scale)) return fail(SOT_ERR_INVALID_ARG, "scale must be finite");
+    if (T == 0) return SOT_OK;
+    SOT_TRY(check_pointer("router", router, dtype));
+    SOT_TRY(check_pointer("gate_up", gate_up, dtype));
+    SOT_TRY(check_pointer("down", down, dtype));
+    if (!logits || !ids || !weights) return fail(SOT_ERR_INVALID_ARG, "logits, ids and weights must not be NULL");
+    RoutedArgs a = {};
+    a.x = x;
+    a.ldx = ld;
+    a.ldo = ld_out;
+    a.T = T;
+    a.H = H;
+    a.E = E;
+    a.F = F;
+    a.K = K;
+    a.dtype = dtype;
+    a.router = router;
+    a.bias = bias;
+    a.gate_up = gate_up;
+    a.down = down;
+    a.renorm = renorm != 0;
+    a.scale = scale;
+    a.out = out;
+    a.logits = logits;
+    a.ids = ids;
+    a.weights = weights;
+    Scratch S((cudaStream_t)stream);
+    const RoutedPlan p = routed_plan(a, device_sms());
+    unsigned char* scratch = S.alloc<unsigned char>(p.scratch);
+    if (!scratch) return fail(SOT_ERR_NOMEM, "scratch allocation failed");
+    SOT_CUDA(launch_routed(a, p, scratch, device_sms(), (cudaStream_t)stream));
     return SOT_OK;
 }
 

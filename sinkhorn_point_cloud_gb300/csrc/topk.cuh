@@ -1,0 +1,636 @@
+// topk.cuh -- scores of given tokens with entropies and the best alternatives, over rows of logits.
+//
+// With y = x / tau and t_v = log2(e) / tau (x_v - m) against the row's largest logit m:
+//   S = sum 2^t,  A = sum 2^t t,   lse = m / tau + log S,   entropy = log S - ln 2 A / S,
+// both sums of one sign, so neither loses digits to cancellation.  One pass gives them, and
+// with them the largest value of every chunk (a thread's batch of granules).  At least K
+// chunks have a maximum that is not below the K-th largest chunk maximum, so neither is the row's
+// K-th largest logit: only chunks that reach this threshold, about K of them, are read again (from L2) for the
+// K best.  Memory bounds it: the logits are read once.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "lm.cuh"
+#include "lm_row.cuh"
+#include "topk.h"
+
+namespace sot {
+
+struct TopkLaunch {
+    int CL, G;     // CTAs a row, granules a slice
+    int chunks;    // places for chunk maxima in shared memory
+    int cap;       // places for candidates: a power of two, at least 2 K
+};
+
+// Running sums of a thread against the largest logit so far, m: s = sum 2^t and a = sum 2^t t with t = (x - m) sc. The
+// difference comes first, so t is good to 2^-23 of itself however far from 0 the logits lie, and the largest
+// logit's weight is 1 exactly.
+struct Scores {
+    float m;
+    float2 s, a;
+    __device__ __forceinline__ Scores() : m(-INFINITY), s(make_float2(0.f, 0.f)), a(s) {}
+
+    __device__ __forceinline__ void move(float mx, float sc) {  // mx > m
+        const float d = (m - mx) * sc, k = ex2f(d);
+        if (s.x + s.y == s.x + s.y) {
+            // (k = 0: what was summed so far is out of range, and d may be infinite)
+            a = k == 0.f ? make_float2(0.f, 0.f) : fmul2(ffma2(s, make_float2(d, d), a), make_float2(k, k));
+            s = fmul2(s, make_float2(k, k));
+        }
+        m = mx;
+        if (mx == INFINITY) s = make_float2(NAN, 0.f);  // and stays
+    }
+    // Sums of a granule.  Elements of -inf make a NaN (0 times infinity) of a, which add() looks at.
+    template <int DT>
+    __device__ __forceinline__ void granule(const uint4& v, float sc) {
+        float2 f[Elem<DT>::N / 2];
+        unpack<DT>(v, f);
+#pragma unroll
+        for (int i = 0; i < Elem<DT>::N / 2; ++i) {
+            const float2 t = fmul2(fadd2(f[i], make_float2(-m, -m)), make_float2(sc, sc));
+            const float2 w = make_float2(ex2f(t.x), ex2f(t.y));
+            s = fadd2(s, w);
+            a = ffma2(w, t, a);
+        }
+    }
+    __device__ __forceinline__ void one(float x, float sc) {
+        if (m == -INFINITY) {  // nothing but -inf so far, and NaN
+            s.x += x != x ? x : 0.f;
+            return;
+        }
+        const float t = (x - m) * sc, w = ex2f(t);
+        s.x += w;
+        if (w > 0.f) a.x = fmaf(w, t, a.x);
+    }
+    // n granules (of at most P) whose largest element is mx.
+    template <int DT, int P>
+    __device__ __forceinline__ void add(const uint4 (&v)[P], int n, float mx, float sc) {
+        if (mx > m) move(mx, sc);
+        const float2 s0 = s, a0 = a;
+        if (m > -INFINITY) {
+            if (n == P) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) granule<DT>(v[j], sc);
+            } else {
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    if (j < n) granule<DT>(v[j], sc);
+            }
+            if (fabsf(a.x + a.y) < INFINITY) return;
+            s = s0;
+            a = a0;
+        }
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+            if (j < n) {
+                float2 f[Elem<DT>::N / 2];
+                unpack<DT>(v[j], f);
+#pragma unroll
+                for (int i = 0; i < Elem<DT>::N / 2; ++i) {
+                    one(f[i].x, sc);
+                    one(f[i].y, sc);
+                }
+            }
+    }
+};
+
+struct MSA {
+    float m, s, a;
+};
+// Sums against stabiliser v.m taken to M >= v.m.
+__device__ __forceinline__ MSA msa_to(MSA v, float M, float sc) {
+    if (v.s != v.s) return MSA{M, v.s, 0.f};
+    const float d = (v.m - M) * sc, k = ex2f(d);
+    if (v.s == 0.f || !(k > 0.f)) return MSA{M, 0.f, 0.f};
+    return MSA{M, v.s * k, fmaf(d, v.s, v.a) * k};
+}
+__device__ __forceinline__ MSA msa_warp(MSA v, float sc) {
+    const float M = warp_max1(v.m);
+    v = msa_to(v, M, sc);
+    return MSA{M, warp_sum(v.s), warp_sum(v.a)};
+}
+
+// Order of the logits as whole numbers (0 and -0 alike), with the bits that a type does not have cut off.
+template <int DT>
+struct Key {
+    static constexpr int SHIFT = DT == SOT_F32 ? 0 : DT == SOT_BF16 ? 16 : 13;
+    __device__ static __forceinline__ unsigned of(float x) { return ord_encode(x + 0.f) >> SHIFT; }
+    __device__ static __forceinline__ float value(unsigned k) {
+        // (the bits cut off are 0 in a positive number's key, 1 in a negative one's)
+        const unsigned low = k << SHIFT & 0x80000000u ? 0u : (1u << SHIFT) - 1u;
+        return ord_decode(k << SHIFT | low);
+    }
+    static constexpr unsigned NOTHING = 0x007fffffu >> SHIFT;  // key of -inf
+};
+// One number for a logit and its column: larger values first, lower columns first among equal ones.
+__device__ __forceinline__ unsigned long long pair_of(unsigned key, int col) {
+    return (unsigned long long)key << 32 | (unsigned)~col;
+}
+
+// What the threads of a CTA share while they select.
+struct SelectSmem {
+    unsigned bound[2];   // smallest and largest chunk maximum
+    unsigned count[3];   // counters in turn
+    unsigned found;      // candidates
+    int got[33];         // ties of each warp
+};
+
+template <int NT>
+__device__ __forceinline__ void cta_sync() {
+    if (NT == 32) __syncwarp();
+    else __syncthreads();
+}
+
+// How many of the CTA's threads' counts there are in all; step: a running number of such sums.
+template <int NT>
+__device__ __forceinline__ unsigned cta_count(SelectSmem& sh, unsigned mine, int& step) {
+    const unsigned w = __reduce_add_sync(0xffffffffu, mine);
+    if (NT == 32) return w;
+    const int now = step % 3, next = (step + 1) % 3;
+    ++step;
+    if ((threadIdx.x & 31) == 0 && w) atomicAdd(&sh.count[now], w);
+    __syncthreads();
+    const unsigned r = sh.count[now];
+    if (threadIdx.x == 0) sh.count[next] = 0;  // (its last readers passed the barrier above)
+    return r;
+}
+
+// Sorts n2 (a power of two) numbers, largest first.
+template <int NT>
+__device__ __forceinline__ void sort_pairs(unsigned long long* v, int n2) {
+    for (int k = 2; k <= n2; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+            for (int i = threadIdx.x; i < n2 / 2; i += NT) {
+                const int p = 2 * i - (i & (j - 1)), q = p + j;
+                const unsigned long long x = v[p], y = v[q];
+                if ((x < y) == ((p & k) == 0)) {
+                    v[p] = y;
+                    v[q] = x;
+                }
+            }
+            cta_sync<NT>();
+        }
+}
+__device__ __forceinline__ unsigned long long cluster_load64(uint32_t ra) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(ra) : "memory");
+    return v;
+}
+// A granule with -inf at the columns outside [0, V).
+template <int DT>
+__device__ __forceinline__ uint4 inside(const uint4& v, int e, int V) {
+    float2 f[Elem<DT>::N / 2];
+    unpack<DT>(v, f);
+    mask_cols<DT>(f, e, V, -INFINITY);
+    return pack<DT>(f);
+}
+
+// Calls use(key, column) for the elements of a granule that lie in the row.
+template <int DT, class Use>
+__device__ __forceinline__ void each_key(const uint4& v, int e, int V, Use use) {
+    float2 f[Elem<DT>::N / 2];
+    unpack<DT>(v, f);
+#pragma unroll
+    for (int i = 0; i < Elem<DT>::N; ++i) {
+        const float x = i & 1 ? f[i / 2].y : f[i / 2].x;
+        if (e + i >= 0 && e + i < V) use(Key<DT>::of(x), e + i);
+    }
+}
+
+// The slice's K best (fewer where it has fewer that are not -inf), sorted, in cand; the rest of cand's first
+// K places 0.  ckey: the chunks' maxima, chunk c = granules (c / NT * U + j) * NT + c % NT.
+template <int DT, int NT, int U>
+__device__ __forceinline__ void select_best(SelectSmem& sh, const unsigned* ckey, int C, const Slice& s, int V, int K, int cap,
+                                            unsigned long long* cand) {
+    constexpr int N = Elem<DT>::N;
+    const int tid = threadIdx.x;
+    int step = 0;
+    unsigned lo = 0xffffffffu, hi = 0;
+    for (int c = tid; c < C; c += NT) {
+        lo = min(lo, ckey[c]);
+        hi = max(hi, ckey[c]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (NT > 32) {
+        if ((tid & 31) == 0) {
+            atomicMin(&sh.bound[0], lo);
+            atomicMax(&sh.bound[1], hi);
+        }
+        __syncthreads();
+        lo = sh.bound[0];
+        hi = sh.bound[1];
+    }
+    const unsigned floor = Key<DT>::NOTHING + 1;
+    lo = C < K ? floor : max(lo, floor);
+    hi = max(hi, lo);
+    // The largest threshold that K chunks reach lies in [lo, hi]; any that not many more reach will do.
+    const auto reach = [&](unsigned at) {
+        unsigned n = 0;
+        for (int c = tid; c < C; c += NT) n += ckey[c] >= at;
+        return cta_count<NT>(sh, n, step);
+    };
+    const unsigned enough = K + K / 2 + 16;
+    bool narrow = C < K;  // whether [lo, hi] may still shrink
+    unsigned top = hi;
+    if (!narrow)
+        while (lo < hi) {
+            const unsigned mid = lo + (hi - lo + 1) / 2, n = reach(mid);
+            if (n >= (unsigned)K) lo = mid;
+            else hi = mid - 1;
+            if (n >= (unsigned)K && n <= enough) break;
+        }
+    // The elements that reach `at` (more than cap of them: only counted).
+    const auto gather = [&](unsigned at) {
+        cta_sync<NT>();
+        if (tid == 0) sh.found = 0;
+        cta_sync<NT>();
+        for (int c = tid; c < C; c += NT)
+            if (ckey[c] >= at) {
+                uint4 v[U];
+                const int g0 = c / NT * U * NT + c % NT;
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (g0 + j * NT < s.ng) v[j] = s.src[g0 + j * NT];
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (g0 + j * NT < s.ng)
+                        each_key<DT>(v[j], s.e0 + (g0 + j * NT) * N, V, [&](unsigned key, int col) {
+                            if (key >= at) {
+                                const unsigned i = atomicAdd(&sh.found, 1u);
+                                if (i < (unsigned)cap) cand[i] = pair_of(key, col);
+                            }
+                        });
+            }
+        cta_sync<NT>();
+        return sh.found;
+    };
+    unsigned n = gather(lo);
+    if (n > (unsigned)cap) {
+        // Many equal logits, or many large ones in few chunks: the K-th largest logit itself by counting over the
+        // whole slice, those above it, and as many of those equal to it as are missing, lowest columns first.
+        unsigned a = lo, b = top;
+        const auto above = [&](unsigned at) {
+            unsigned n = 0;
+            for (int g = tid; g < s.ng; g += NT)
+                each_key<DT>(s.src[g], s.e0 + g * N, V, [&](unsigned key, int) { n += key >= at; });
+            return cta_count<NT>(sh, n, step);
+        };
+        while (a < b) {
+            const unsigned mid = a + (b - a + 1) / 2;
+            if (above(mid) >= (unsigned)K) a = mid;
+            else b = mid - 1;
+        }
+        n = a == 0xffffffffu ? 0 : gather(a + 1);  // fewer than K
+        for (int g0 = 0; g0 < s.ng && n < (unsigned)K; g0 += NT) {
+            const int g = g0 + tid;
+            uint4 v = nothing<DT>();
+            unsigned mine = 0;
+            if (g < s.ng) {
+                v = s.src[g];
+                each_key<DT>(v, s.e0 + g * N, V, [&](unsigned key, int) { mine += key == a; });
+            }
+            unsigned before = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned w = __shfl_up_sync(0xffffffffu, before, o);
+                if ((tid & 31) >= o) before += w;
+            }
+            unsigned all = __shfl_sync(0xffffffffu, before, 31), at = n + before - mine;
+            if (NT > 32) {
+                __syncthreads();
+                if ((tid & 31) == 31) sh.got[tid >> 5] = (int)before;
+                __syncthreads();
+                all = 0;
+                for (int w = 0; w < NT / 32; ++w) {
+                    if (w < tid >> 5) at += sh.got[w];
+                    all += sh.got[w];
+                }
+            }
+            if (mine)
+                each_key<DT>(v, s.e0 + g * N, V, [&](unsigned key, int col) {
+                    if (key == a && at++ < (unsigned)K) cand[at - 1] = pair_of(key, col);
+                });
+            n = min(n + all, (unsigned)K);
+        }
+        cta_sync<NT>();
+    }
+    int n2 = 2;
+    while (n2 < (int)n || n2 < K) n2 *= 2;
+    for (int i = n + tid; i < n2; i += NT) cand[i] = 0ull;
+    cta_sync<NT>();
+    sort_pairs<NT>(cand, n2);
+}
+
+// One row a CTA, or a cluster's CTAs a slice of it each.
+template <int DT, int NT, int U>
+__global__ void __launch_bounds__(NT, NT == 32 ? 20 : 1024 / NT) topk_kernel(const TopkArgs a, const TopkLaunch L) {
+    using T = typename Elem<DT>::T;
+    constexpr int N = Elem<DT>::N, P = 8, NW = NT / 32;
+    extern __shared__ __align__(16) unsigned char dyn[];
+    __shared__ SelectSmem sh;
+    __shared__ MSA rec[NW];
+    __shared__ MSA mail[ROW_MAX_CL];
+    unsigned long long* const cand = reinterpret_cast<unsigned long long*>(dyn);
+    unsigned* const ckey = reinterpret_cast<unsigned*>(cand + L.cap);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    const float sc = SOT_LOG2E / a.tau;
+    const long long row = blockIdx.x / L.CL;
+    const int tgt = a.target ? load_index(a.target, a.target_type, row, a.V) : -1;
+    if (a.target && tgt < 0) {  // left out: the same for the whole cluster
+        if (rank) return;
+        for (int k = tid; k < a.K; k += NT) {
+            if (a.ids) a.ids[row * a.K + k] = -1;
+            if (a.top) a.top[row * a.K + k] = 0.f;
+        }
+        if (tid == 0) {
+            if (a.logp) a.logp[row] = 0.f;
+            if (a.lse) a.lse[row] = 0.f;
+            if (a.entropy) a.entropy[row] = 0.f;
+        }
+        return;
+    }
+    if (L.CL > 1) cluster_arrive_started();
+    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
+    const Slice s = slice_at<DT>(x, a.V, L.G, rank);
+    const float xt = tgt >= 0 && rank == 0 && tid == 0 ? Elem<DT>::get(x[tgt]) : 0.f;
+    const uint64_t policy = a.K ? policy_keep() : policy_drop();
+    if (NT > 32 && tid == 0) {
+        sh.bound[0] = 0xffffffffu;
+        sh.bound[1] = 0;
+        sh.count[0] = sh.count[1] = sh.count[2] = 0;
+    }
+    Scores run;
+    int c = tid;  // the next chunk
+    for (int g = tid; g < s.ng; g += P * NT) {
+        uint4 v[P];
+        const int n = min(P, (s.ng - g + NT - 1) / NT);
+        if (n == P) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] = load16(s.src + g + j * NT, policy);
+        } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] = j < n ? load16(s.src + g + j * NT, policy) : nothing<DT>();
+        }
+        if (s.lo > 0 && g == 0) v[0] = inside<DT>(v[0], s.e0, a.V);
+        if (s.hi < s.ng) {
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                if (g + j * NT == s.ng - 1) v[j] = inside<DT>(v[j], s.e0 + (s.ng - 1) * N, a.V);
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < P; j += U) {
+            uint4 top = v[j];
+#pragma unroll
+            for (int i = 1; i < U; ++i) top = max2<DT>(top, v[j + i]);
+            const float w = max_of<DT>(top);
+            mx = fmaxf(mx, w);
+            if (a.K) {
+                if (j < n) ckey[c] = Key<DT>::of(w);
+                c += NT;
+            }
+        }
+        run.template add<DT>(v, n, mx, sc);
+    }
+    MSA w = msa_warp(MSA{run.m, run.s.x + run.s.y, run.a.x + run.a.y}, sc);
+    if (lane == 0) rec[warp] = w;
+    const int chunks = min((s.ng + U * NT - 1) / (U * NT) * NT, L.chunks);
+    if (a.K)  // places that no chunk has taken
+        for (int i = tid; i < chunks; i += NT)
+            if (i / NT * U * NT + tid >= s.ng) ckey[i] = 0;
+    cta_sync<NT>();
+    w = rec[lane < NW ? lane : 0];
+    if (lane >= NW) w = MSA{-INFINITY, 0.f, 0.f};
+    w = msa_warp(w, sc);
+    // A row without a sum has no alternatives; a slice without one may still stand beside others.
+    if (a.K) {
+        if (w.s > 0.f) select_best<DT, NT, U>(sh, ckey, chunks, s, a.V, a.K, L.cap, cand);
+        else
+            for (int i = tid; i < a.K; i += NT) cand[i] = 0ull;
+        cta_sync<NT>();
+    }
+    if (L.CL > 1) {
+        cluster_wait_started();
+        if (tid == 0) {
+            const uint32_t to = cluster_addr(smem_u32(&mail[rank]), 0);
+            cluster_store(to, w.m);
+            cluster_store(to + 4, w.s);
+            cluster_store(to + 8, w.a);
+        }
+        cluster_sync();
+        if (rank == 0) {
+            w = lane < L.CL ? mail[lane] : MSA{-INFINITY, 0.f, 0.f};
+            w = msa_warp(w, sc);
+            if (a.K) {
+                int n2 = 2;
+                while (n2 < L.CL * a.K) n2 *= 2;
+                for (int i = a.K + tid; i < n2; i += NT) {
+                    const uint32_t r = i / a.K;
+                    cand[i] = r < (uint32_t)L.CL ? cluster_load64(cluster_addr(smem_u32(cand + (i - r * a.K)), r)) : 0ull;
+                }
+                __syncthreads();
+                sort_pairs<NT>(cand, n2);
+            }
+        }
+        cluster_sync();  // nobody leaves while rank 0 reads
+        if (rank) return;
+    }
+    const float2 logS = log_ff(w.s);
+    // log p of a logit: the difference to the stabiliser is exact, only what comes after it is rounded.
+    const auto logp_of = [&](float v) {
+        const float2 d = two_sum(v, -w.m);
+        const float2 r = ff_add(ff_mul(d, make_float2(a.inv_hi, a.inv_lo)), make_float2(-logS.x, -logS.y));
+        return fabsf(r.x) < INFINITY ? r.x + r.y : (float)(((double)v - (double)w.m) * a.inv_tau) - logS.x;
+    };
+    if (tid == 0) {
+        if (a.logp) a.logp[row] = logp_of(xt);
+        if (a.lse) {
+            const float2 l = ff_add(ff_mul(make_float2(w.m, 0.f), make_float2(a.inv_hi, a.inv_lo)), logS);
+            a.lse[row] = fabsf(l.x) < INFINITY ? l.x + l.y : (float)((double)w.m * a.inv_tau) + logS.x;
+        }
+        if (a.entropy) {
+            const float h = logS.x + fmaf(-SOT_LN2, __fdiv_rn(w.a, w.s), logS.y);
+            a.entropy[row] = w.s > 0.f ? (h < 0.f ? 0.f : h) : NAN;
+        }
+    }
+    for (int k = tid; k < a.K; k += NT) {
+        const unsigned long long p = w.s > 0.f ? cand[k] : 0ull;
+        if (a.ids) a.ids[row * a.K + k] = p ? (int)~(unsigned)p : -1;
+        if (a.top) a.top[row * a.K + k] = p ? logp_of(Key<DT>::value((unsigned)(p >> 32))) : w.s > 0.f ? -INFINITY : NAN;
+    }
+}
+
+// Gradient from the stored lse and entropy: with G = sum of the gradients with respect to
+// log-probabilities, those of the entries and of the target, and t = log2 p,
+//   tau dx_v = G_v - p_v (G + gH (ln 2 t_v + H)) = G_v + p_v (c0 + c1 t_v).
+// One read and one write per logit, each granule on its own.  The entries' columns are
+// formed again after the rest, from logits read before anything is written.
+constexpr int TOPK_GRAD_NT = 256;
+
+template <int DT>
+__global__ void __launch_bounds__(TOPK_GRAD_NT) topk_grad_kernel(const TopkGradArgs a, int G, int chunks) {
+    using T = typename Elem<DT>::T;
+    constexpr int N = Elem<DT>::N, U = 4, NT = TOPK_GRAD_NT;
+    extern __shared__ __align__(16) float ent[];  // entries of the slice: logit
+    __shared__ float red[NT / 32];
+    const int tid = threadIdx.x;
+    const long long row = blockIdx.x / chunks;
+    const T* const x = static_cast<const T*>(a.x) + row * a.ld;
+    T* const grow = static_cast<T*>(a.grad) + row * a.ldg;
+    const Slice s = slice_at<DT>(x, a.V, G, blockIdx.x % chunks);
+    const bool aligned = same_granules<T>(x, grow);
+    const int tgt = a.target ? load_index(a.target, a.target_type, row, a.V) : -1;
+    const bool keep = !a.target || tgt >= 0;
+    const float inv_tau = 1.f / a.tau;
+    const float gl = keep && tgt >= 0 && a.g_logp ? a.g_logp[row] : 0.f;
+    const float gh = keep && a.g_entropy ? a.g_entropy[row] : 0.f;
+    float gt = 0.f;
+    bool any = gl != 0.f || gh != 0.f;
+    const int e0 = s.e0, e1 = s.e0 + s.ng * N;  // the slice's columns
+    if (keep && a.g_top) {
+        float mine = 0.f;
+        bool some = false;
+        for (int k = tid; k < a.K; k += NT) {
+            const int id = a.ids[row * a.K + k];
+            const float g = id >= 0 && id < a.V ? a.g_top[row * a.K + k] : 0.f;
+            mine += g;
+            some = some || g != 0.f;
+            if (id >= e0 && id < e1 && id >= 0 && id < a.V) ent[k] = Elem<DT>::get(x[id]);
+        }
+        gt = block_sum<NT>(mine, red);
+        any = __syncthreads_or(some) || any;
+    }
+    if (!any) {  // not read
+        slice_zero<DT>(s, grow, a.V, aligned, tid, NT);
+        return;
+    }
+    const float lse = a.lse[row], u = lse * SOT_LOG2E, sc = SOT_LOG2E / a.tau;
+    const float H = gh != 0.f ? a.entropy[row] : 0.f;
+    // (a row without a lse has no gradient: NaN)
+    const float c0 = -(gl + gt + gh * H) * inv_tau + (lse - lse), c1 = -gh * SOT_LN2 * inv_tau;
+    const bool far = !(fabsf(u) < 0x1p10f);
+    // p (c0 + c1 t).  Below 2^-160 p is 0, whatever t is.
+    const auto near2 = [&](float2 f) {
+        const float2 t = ffma2(f, make_float2(sc, sc), make_float2(-u, -u));
+        const float2 b = make_float2(fmaxf(t.x, -160.f), fmaxf(t.y, -160.f));
+        const float2 p = make_float2(ex2f(t.x), ex2f(t.y));
+        return fmul2(p, ffma2(b, make_float2(c1, c1), make_float2(c0, c0)));
+    };
+    // Far from 0 the rounding of u would show: the difference comes first there.
+    const auto far1 = [&](float v) {
+        float d = (v - lse * a.tau) / a.tau;
+        d = d > 0.f ? 0.f : d;
+        const float p = expf(d);
+        return p * fmaf(c1, fmaxf(d * SOT_LOG2E, -160.f), c0);
+    };
+    const auto value = [&](float2 f) { return far ? make_float2(far1(f.x), far1(f.y)) : near2(f); };
+    const float hot = gl * inv_tau;
+    const auto finish = [&](float2 (&f)[N / 2], int c) {  // columns c ..
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) f[j] = value(f[j]);
+        if ((unsigned)(tgt - c) < (unsigned)N && tgt >= 0) {
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                f[j].x += c + 2 * j == tgt ? hot : 0.f;
+                f[j].y += c + 2 * j + 1 == tgt ? hot : 0.f;
+            }
+        }
+    };
+    const uint64_t policy = policy_drop();
+    if (!aligned) {
+        for (int i = tid; i < s.ng; i += NT) {
+            float2 f[N / 2];
+            unpack<DT>(s.src[i], f);
+            finish(f, s.e0 + i * N);
+            store_cols<DT>(grow, s.e0 + i * N, a.V, f, false);
+        }
+    } else {
+        uint4* const dst = reinterpret_cast<uint4*>(grow + s.e0);
+        for (int i = s.lo + tid; i < s.hi; i += U * NT) {
+            uint4 v[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (i + j * NT < s.hi) v[j] = load16(s.src + i + j * NT, policy);
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (i + j * NT < s.hi) {
+                    float2 f[N / 2];
+                    unpack<DT>(v[j], f);
+                    finish(f, s.e0 + (i + j * NT) * N);
+                    store16(dst + i + j * NT, pack<DT>(f), policy);
+                }
+        }
+        const int e = edge_granule(s, tid, NT);
+        if (e >= 0) {
+            float2 f[N / 2];
+            unpack<DT>(s.src[e], f);
+            finish(f, s.e0 + e * N);
+            store_cols<DT>(grow, s.e0 + e * N, a.V, f, false);
+        }
+    }
+    if (!a.g_top) return;
+    __syncthreads();  // the entries come after the columns they replace
+    for (int k = tid; k < a.K; k += NT) {
+        const int id = a.ids[row * a.K + k];
+        if (id >= e0 && id < e1 && id >= 0 && id < a.V) {
+            const float g = a.g_top[row * a.K + k] + (id == tgt ? gl : 0.f);
+            grow[id] = Elem<DT>::put(fmaf(g, inv_tau, value(make_float2(ent[k], ent[k])).x));
+        }
+    }
+}
+
+constexpr int TOPK_MAX_SMEM = 200 * 1024;
+
+template <int DT, int NT, int U>
+cudaError_t launch_topk_n(const TopkArgs& a, const TopkLaunch& L, size_t smem, cudaStream_t st) {
+    auto kern = topk_kernel<DT, NT, U>;
+    if (smem > 40 * 1024) {
+        // (the kernel's leave, not the call's: another host thread's call cannot lower it before the launch)
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TOPK_MAX_SMEM);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.T * L.CL), 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = L.CL;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, L);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+struct TopkPlan {
+    int NT, U;
+    TopkLaunch L;
+    size_t smem;
+};
+
+template <int DT>
+cudaError_t launch_topk_t(const TopkArgs& a, const TopkPlan& p, cudaStream_t st) {
+    if (p.NT == 32) return p.U == 1 ? launch_topk_n<DT, 32, 1>(a, p.L, p.smem, st) : launch_topk_n<DT, 32, 8>(a, p.L, p.smem, st);
+    return p.U == 1 ? launch_topk_n<DT, 256, 1>(a, p.L, p.smem, st) : launch_topk_n<DT, 256, 8>(a, p.L, p.smem, st);
+}
+
+template <int DT>
+cudaError_t launch_topk_grad_t(const TopkGradArgs& a, int G, int chunks, cudaStream_t st) {
+    topk_grad_kernel<DT><<<(unsigned)(a.T * chunks), TOPK_GRAD_NT, a.g_top ? a.K * sizeof(float) : 0, st>>>(a, G, chunks);
+    return cudaGetLastError();
+}
+
+// One translation unit per type (k_topk_f32.cu, k_topk_f16.cu, k_topk_bf16.cu).
+cudaError_t launch_topk_f32(const TopkArgs& a, const TopkPlan& p, cudaStream_t st);
+cudaError_t launch_topk_f16(const TopkArgs& a, const TopkPlan& p, cudaStream_t st);
+cudaError_t launch_topk_bf16(const TopkArgs& a, const TopkPlan& p, cudaStream_t st);
+cudaError_t launch_topk_grad_f32(const TopkGradArgs& a, int G, int chunks, cudaStream_t st);
+cudaError_t launch_topk_grad_f16(const TopkGradArgs& a, int G, int chunks, cudaStream_t st);
+cudaError_t launch_topk_grad_bf16(const TopkGradArgs& a, int G, int chunks, cudaStream_t st);
+
+}  // namespace sot
