@@ -267,6 +267,12 @@ cudaError_t launch_status_merge(const int* status, cudaStream_t st) {
     count_launches(1); status_merge_kernel<<<1, 1, 0, st>>>(status);
     return cudaGetLastError();
 }
+cudaError_t async_status_address(unsigned** out) {
+    void* at = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&at, g_async_status);
+    *out = static_cast<unsigned*>(at);
+    return e;
+}
 cudaError_t read_clear_async_status(cudaStream_t st, unsigned* out) {
     unsigned v = 0;
     const unsigned zero = 0;

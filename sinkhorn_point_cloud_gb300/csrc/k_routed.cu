@@ -7,8 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
-#include "lm.cuh"
-#include "routed.h"
+#include "routed.cuh"
 
 namespace sot {
 
@@ -18,76 +17,81 @@ constexpr int NT = 256, NW = NT / 32;
 
 // Scores.  Two experts' scores may lie closer than a 32-bit sum tells them apart, and which is chosen must not
 // depend on the order of a sum: products of 16-bit types are exact in 32 bits, and sums go in pairs of floats.
+// A CTA takes an expert and up to eight tokens; with fewer, each token's sum is split over several warps.
 template <int DT>
-__global__ void __launch_bounds__(NT) routed_scores_kernel(const RoutedArgs a) {
+__device__ __forceinline__ void add_product(float2& s, float2& low, float2 x, float2 r) {
+    const float2 minus = make_float2(-1.f, -1.f), p = fmul2(x, r), t = fadd2(s, p), z = ffma2(s, minus, t);
+    // what t has lost of s + p, lane by lane
+    const float2 e = fadd2(ffma2(ffma2(z, minus, t), minus, s), ffma2(z, minus, p));
+    if constexpr (DT == SOT_F32) low = fadd2(low, ffma2(x, r, make_float2(-p.x, -p.y)));
+    low = fadd2(low, e);
+    s = t;
+}
+template <int DT>
+__global__ void __launch_bounds__(NT) routed_scores_kernel(const RoutedArgs a, int tokens, bool whole, unsigned* barrier) {
     using T = typename Elem<DT>::T;
-    const int lane = threadIdx.x & 31, w = blockIdx.x * NW + (threadIdx.x >> 5);
-    if (w >= a.T * a.E) return;
-    const int t = w / a.E, e = w % a.E;
-    const T* const x = static_cast<const T*>(a.x) + t * a.ldx;
-    const T* const r = static_cast<const T*>(a.router) + (long long)e * a.H;
-    float2 s = make_float2(0.f, 0.f);
-    for (int i = lane; i < a.H; i += 32) {
-        const float2 p = two_prod(Elem<DT>::get(x[i]), Elem<DT>::get(r[i])), q = two_sum(s.x, p.x);
-        s = make_float2(q.x, s.y + (q.y + p.y));
+    constexpr int N = Elem<DT>::N;
+    __shared__ float2 part[NW];
+    __shared__ float plain[NW];
+    if (barrier && blockIdx.x == 0 && threadIdx.x < 4) barrier[threadIdx.x] = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, splits = NW / tokens;
+    const int e = blockIdx.x % a.E, t = blockIdx.x / a.E * tokens + warp / splits, split = warp % splits;
+    float2 s = make_float2(0.f, 0.f), low = s;
+    if (t < a.T) {
+        const T* const x = static_cast<const T*>(a.x) + t * a.ldx;
+        const T* const r = static_cast<const T*>(a.router) + (long long)e * a.H;
+        if (whole) {
+#pragma unroll 4
+            for (int i = (split * 32 + lane) * N; i < a.H; i += splits * 32 * N) {
+                float2 f[N / 2], g[N / 2];
+                unpack<DT>(*reinterpret_cast<const uint4*>(x + i), f);
+                unpack<DT>(*reinterpret_cast<const uint4*>(r + i), g);
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) add_product<DT>(s, low, f[j], g[j]);
+            }
+        } else
+            for (int i = split * 32 + lane; i < a.H; i += splits * 32)
+                add_product<DT>(s, low, make_float2(Elem<DT>::get(x[i]), 0.f), make_float2(Elem<DT>::get(r[i]), 0.f));
     }
-    const float far = warp_sum(s.x);
-    s = ff_warp_sum(ff_renorm(s.x, s.y));
-    if (a.bias) s = ff_add(s, make_float2(a.bias[e], 0.f));
+    const float far = warp_sum(s.x + s.y);
+    const float2 both = ff_warp_sum(ff_add(ff_renorm(s.x, low.x), ff_renorm(s.y, low.y)));
+    if (lane == 0) {
+        part[warp] = both;
+        plain[warp] = far;
+    }
+    __syncthreads();
+    if (split || lane || t >= a.T) return;
+    const float bias = a.bias ? a.bias[e] : 0.f;
+    float2 sum = make_float2(bias, 0.f);
+    float all = bias;
+    for (int w = warp; w < warp + splits; ++w) {
+        sum = ff_add(sum, part[w]);
+        all += plain[w];
+    }
     // (an infinity or NaN goes without the low parts, which would make a NaN of either)
-    if (lane == 0) a.logits[w] = fabsf(far) < INFINITY && !(a.bias && !(fabsf(a.bias[e]) < INFINITY)) ? s.x + s.y
-                                                                        : far + (a.bias ? a.bias[e] : 0.f);
+    a.logits[(long long)t * a.E + e] = fabsf(all) < INFINITY ? sum.x + sum.y : all;
+}
+template <int DT>
+cudaError_t launch_scores(const RoutedArgs& a, unsigned* barrier, cudaStream_t st) {
+    int tokens = 1;
+    while (tokens < NW && tokens < a.T) tokens *= 2;
+    const bool whole = a.H % Elem<DT>::N == 0 && a.ldx % Elem<DT>::N == 0 && (unsigned long long)a.x % 16 == 0 &&
+                       (unsigned long long)a.router % 16 == 0;
+    count_launches(1);
+    routed_scores_kernel<DT><<<a.E * ((a.T + tokens - 1) / tokens), NT, 0, st>>>(a, tokens, whole, barrier);
+    return cudaGetLastError();
 }
 
 // Choice: a warp a token.
 __global__ void __launch_bounds__(NT) routed_choose_kernel(const RoutedArgs a) {
     const int lane = threadIdx.x & 31, t = blockIdx.x * NW + (threadIdx.x >> 5);
     if (t >= a.T) return;
-    const float* const r = a.logits + (long long)t * a.E;
-    constexpr int R = ROUTED_MAX_E / 32;
-    unsigned key[R];  // 0: -inf, or no expert
-    float m = -INFINITY, bad = 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int e = i * 32 + lane;
-        const float v = e < a.E ? r[e] : -INFINITY;
-        if (!(v < INFINITY)) bad = 1.f;
-        m = fmaxf(m, v);
-        key[i] = v > -INFINITY ? ord_encode(v + 0.f) : 0u;
-    }
-    m = warp_max(m);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (key[i]) sum += expf(ord_decode(key[i]) - m);
-    sum = warp_sum(sum);
-    bad = warp_max(bad);
-    float chosen = 0.f, mine = 0.f;
-    int id = -1;  // lane k: the k-th choice
-    for (int k = 0; k < a.K; ++k) {
-        unsigned best = 0;
-#pragma unroll
-        for (int i = 0; i < R; ++i) best = max(best, key[i]);
-        best = __reduce_max_sync(0xffffffffu, best);
-        if (best == 0 || bad != 0.f) break;
-        int at = 0x7fffffff;
-#pragma unroll
-        for (int i = R - 1; i >= 0; --i)
-            if (key[i] == best) at = i * 32 + lane;
-        at = __reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (i * 32 + lane == at) key[i] = 0;
-        const float v = expf(ord_decode(best) - m);
-        chosen += v;
-        if (lane == k) {
-            id = at;
-            mine = v;
-        }
-    }
+    int id;
+    float w;
+    routed_choose(a.logits + (long long)t * a.E, a.E, a.K, a.renorm, a.scale, id, w);
     if (lane < a.K) {
         a.ids[t * a.K + lane] = id;
-        a.weights[t * a.K + lane] = bad != 0.f ? NAN : id < 0 ? 0.f : mine / (a.renorm ? chosen : sum) * a.scale;
+        a.weights[t * a.K + lane] = w;
     }
 }
 
@@ -153,8 +157,9 @@ __global__ void __launch_bounds__(NT) routed_join_kernel(const RoutedArgs a) {
 template <int DT>
 cudaError_t launch_plain(const RoutedArgs& a, cudaStream_t st) {
     const int up = (a.F + NW - 1) / NW, down = (a.H + NW - 1) / NW;
-    count_launches(5);
-    routed_scores_kernel<DT><<<(a.T * a.E + NW - 1) / NW, NT, 0, st>>>(a);
+    const cudaError_t e = launch_scores<DT>(a, nullptr, st);
+    if (e != cudaSuccess) return e;
+    count_launches(4);
     routed_choose_kernel<<<(a.T + NW - 1) / NW, NT, 0, st>>>(a);
     routed_up_kernel<DT><<<a.E * up, NT, 0, st>>>(a, up);
     routed_down_kernel<DT><<<a.E * down, NT, 0, st>>>(a, down);
@@ -164,15 +169,27 @@ cudaError_t launch_plain(const RoutedArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-RoutedPlan routed_plan(const RoutedArgs& a, int) {
+// The tensor cores need whole granules; the other form takes any size, stride and type, with a warp an output.
+RoutedPlan routed_plan(const RoutedArgs& a, int sms) {
     RoutedPlan p = {};
+    p.tc = routed_tc_fits(a);
+    if (p.tc) {
+        p.on_tc = routed_tc_plan(a, sms);
+        p.scratch = p.on_tc.scratch;
+        return p;
+    }
     p.y_at = (sizeof(float) * (size_t)a.T * a.K * a.F + 255) & ~(size_t)255;
     p.scratch = p.y_at + sizeof(float) * (size_t)a.T * a.K * a.H;
     return p;
 }
 
-cudaError_t launch_routed(RoutedArgs a, const RoutedPlan& p, unsigned char* scratch, int, cudaStream_t st) {
+cudaError_t launch_routed(RoutedArgs a, const RoutedPlan& p, unsigned char* scratch, int sms, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
+    if (p.tc) {
+        unsigned* const barrier = reinterpret_cast<unsigned*>(scratch + p.on_tc.barrier_at);
+        const cudaError_t e = a.dtype == SOT_BF16 ? launch_scores<SOT_BF16>(a, barrier, st) : launch_scores<SOT_F16>(a, barrier, st);
+        return e != cudaSuccess ? e : launch_routed_tc(a, p.on_tc, scratch, sms, st);
+    }
     a.h = reinterpret_cast<float*>(scratch + p.h_at);
     a.y = reinterpret_cast<float*>(scratch + p.y_at);
     switch (a.dtype) {

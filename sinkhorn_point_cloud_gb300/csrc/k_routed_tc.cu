@@ -1,0 +1,596 @@
+// k_routed_tc.cu -- the routed layer for a few tokens on the tensor cores, 16-bit types.
+//
+// After the scores (k_routed.cu) one cooperative kernel, a CTA an SM, does the rest:
+//   choose  every CTA forms the choice of all tokens and each expert's list of tokens for itself;
+//   up      products gate_up x^T: an expert's rows are the M of a tcgen05.mma (64 gate rows and the 64 up rows that
+//           belong to them), its tokens the N.  The units of all experts (16 KB of weights, K = 64) are dealt out evenly, so a
+//           CTA starts and ends inside a tile; it leaves a partial sum for each piece;
+//   act     h = silu(gate) up of the joined pieces, rounded to the type;
+//   down    products down h^T, the same way;
+//   join    the weighted sum over a token's experts.
+// The weights are read once and bound it.  They come by TMA through a ring of stages, 16 KB each, from a warp that waits
+// for nothing but free stages: across the phases' grid barriers the next phase's weights are already on their way.
+// Every wait is bounded; one that runs out ends the call with NaN outputs and the timeout status.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "routed.cuh"
+#include "tc_ptx.cuh"
+
+namespace sot {
+
+namespace {
+
+constexpr int NWARP = 10, NT = NWARP * 32;
+constexpr int W_PRODUCER = 0, W_MMA = 1, W_EPI = 2, W_LOAD = 6;  // first warps of each role (4 epilogue, 4 loading)
+constexpr int WORKERS = 256;                                     // threads of the last two
+constexpr int KSTEP = 64, A_BYTES = 128 * KSTEP * 2;
+constexpr int MAX_STAGES = 12, LAG = 3;
+constexpr unsigned long long WAIT_NS = 2000000000ull;
+constexpr int PHASES = 2;  // 0: up, 1: down
+
+struct Layout {  // byte offsets in dynamic shared memory (from a 1024-byte boundary)
+    int stage, stages, npad;
+    int bars, weight, list, act, id, info, mask, total;
+};
+
+struct TcArgs {
+    RoutedArgs r;
+    Layout L;
+    unsigned* barrier;   // [4] grid barriers, zeroed by the scores' kernel
+    unsigned* status;    // the device's status word
+    float* part[PHASES];  // [pieces][T K][2 F or H]
+    void* h;              // [T K][F]
+    int pieces[PHASES];   // of a tile, at most
+};
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int k, int row, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], "
+        "%5;" ::"r"(dst),
+        "l"(map), "r"(k), "r"(row), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {  // bytes 0: zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void worker_sync() { asm volatile("bar.sync 1, %0;" ::"n"(WORKERS) : "memory"); }
+
+struct Info {  // an expert that some token chose
+    int expert, start, n;
+};
+
+// What the roles share: where things lie, and how the units of a phase are dealt out.
+struct Ctx {
+    unsigned char* sm;
+    uint32_t base, bars;
+    volatile int* abort;
+    float* weight;
+    unsigned short *list, *act;
+    short* id;
+    Info* info;
+    int P, active;
+    int KS[PHASES], tiles[PHASES];
+    int chunk[PHASES];  // units of a CTA
+    int first[PHASES], end[PHASES];
+    int S;
+    __device__ __forceinline__ uint32_t full(int s) const { return bars + 8 * s; }
+    __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8 * (MAX_STAGES + s); }
+    __device__ __forceinline__ uint32_t accfull(int b) const { return bars + 8 * (2 * MAX_STAGES + b); }
+    __device__ __forceinline__ uint32_t accempty(int b) const { return bars + 8 * (2 * MAX_STAGES + 2 + b); }
+    __device__ __forceinline__ uint32_t drain() const { return bars + 8 * (2 * MAX_STAGES + 4); }
+};
+constexpr int BAR_BYTES = 8 * (2 * MAX_STAGES + 5) + 8;  // and the TMEM address, and the abort flag
+
+// A piece: units [u, u + n) of one tile.
+struct Piece {
+    int job, ks, n;
+};
+__device__ __forceinline__ Piece piece_at(const Ctx& c, int ph, int u) {
+    const int job = u / c.KS[ph], ks = u - job * c.KS[ph];
+    return Piece{job, ks, min(c.KS[ph] - ks, c.end[ph] - u)};
+}
+__device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
+
+__device__ void produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, const CUtensorMap* down) {
+    const uint64_t policy = policy_drop();
+    int it = 0;
+    for (int ph = 0; ph < PHASES; ++ph) {
+        const CUtensorMap* const map = ph ? down : up;
+        for (int u = c.first[ph]; u < c.end[ph];) {
+            const Piece p = piece_at(c, ph, u);
+            const int a = p.job / c.tiles[ph], tile = p.job - a * c.tiles[ph], e = c.info[a].expert;
+            const int r0 = ph ? e * t.r.H + tile * 128 : e * 2 * t.r.F + tile * 64, r1 = ph ? r0 + 64 : r0 + t.r.F;
+            for (int i = 0; i < p.n; ++i, ++it) {
+                const int s = it % c.S;
+                if (!mbar_wait_bounded(c.empty(s), ((it / c.S) & 1) ^ 1, c.abort, WAIT_NS)) goto out;
+                mbar_arrive_expect_tx(c.full(s), A_BYTES);
+                const uint32_t dst = c.base + s * t.L.stage;
+                tma_rows(dst, map, (p.ks + i) * KSTEP, r0, c.full(s), policy);
+                tma_rows(dst + A_BYTES / 2, map, (p.ks + i) * KSTEP, r1, c.full(s), policy);
+            }
+            u += p.n;
+        }
+    }
+out:
+    if (*c.abort) {
+        // Copies in flight land before the CTA goes: the loading warps may have given up, so their arrivals are made here.
+        int dummy = 0;
+        for (int i = max(0, it - c.S); i < it; ++i) {
+            const int s = i % c.S;
+            for (int k = 0; k < 4; ++k)
+                if (!mbar_try_wait(c.full(s), (i / c.S) & 1)) mbar_arrive(c.full(s));
+            mbar_wait_bounded(c.full(s), (i / c.S) & 1, &dummy, WAIT_NS);
+        }
+    }
+}
+
+template <int DT>
+__device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
+    constexpr uint32_t format = DT == SOT_BF16 ? (1u << 7) | (1u << 10) : 0u;
+    int it = 0, seg = 0;
+    bool ok = true, issued = false;
+    for (int ph = 0; ok && ph < PHASES; ++ph)
+        for (int u = c.first[ph]; ok && u < c.end[ph]; ++seg) {
+            const Piece p = piece_at(c, ph, u);
+            const uint32_t idesc = f16_idesc(128, pad16(c.info[p.job / c.tiles[ph]].n)) | format;
+            const uint32_t d = tmem + (seg & 1) * t.L.npad;
+            ok = mbar_wait_bounded(c.accempty(seg & 1), ((seg >> 1) & 1) ^ 1, c.abort, WAIT_NS);
+            for (int i = 0; ok && i < p.n; ++i, ++it) {
+                const int s = it % c.S;
+                if (!mbar_wait_bounded(c.full(s), (it / c.S) & 1, c.abort, WAIT_NS)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a = c.base + s * t.L.stage, b = a + A_BYTES;
+#pragma unroll
+                for (int k = 0; k < KSTEP / 16; ++k)
+                    tc_mma_f16(d, sw128_desc(a + 32 * k), sw128_desc(b + 32 * k), idesc, i > 0 || k > 0 ? 1u : 0u);
+                issued = true;
+                tc_commit(c.empty(s));
+            }
+            if (ok) tc_commit(c.accfull(seg & 1));
+            u += p.n;
+        }
+    if (issued) {  // nothing is under way when the CTA frees its TMEM
+        int dummy = 0;
+        tc_commit(c.drain());
+        mbar_wait_bounded(c.drain(), 0, &dummy, WAIT_NS);
+    }
+}
+
+// The tokens' side of a phase: rows of x or h, swizzled as the tensor cores read them.  A row past the expert's
+// last token is not written: what it holds only reaches columns that nobody reads.
+__device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, int& it) {
+    const int tid = threadIdx.x - W_LOAD * 32, lane = tid & 31;
+    const int K = ph ? t.r.F : t.r.H;
+    const int from = it;
+    bool ok = true;
+    const auto arrive = [&](int i) {  // this thread's copies for unit i have landed
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.full(i % c.S));
+    };
+    for (int u = c.first[ph]; ok && u < c.end[ph];) {
+        const Piece p = piece_at(c, ph, u);
+        const Info e = c.info[p.job / c.tiles[ph]];
+        for (int i = 0; i < p.n; ++i, ++it) {
+            const int s = it % c.S, k0 = (p.ks + i) * KSTEP;
+            ok = mbar_wait_bounded(c.empty(s), ((it / c.S) & 1) ^ 1, c.abort, WAIT_NS);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t dst = c.base + s * t.L.stage + A_BYTES;
+            for (int q = tid; q < e.n * 8; q += 128) {
+                const int row = q >> 3, ch = q & 7, k = k0 + ch * 8, pair = c.list[e.start + row];
+                const unsigned short* const src = ph ? static_cast<const unsigned short*>(t.h) + (long long)pair * K
+                                                     : static_cast<const unsigned short*>(t.r.x) + pair / t.r.K * t.r.ldx;
+                copy16(dst + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4), k < K ? src + k : src, k < K ? 16 : 0);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (it - from >= LAG) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
+                arrive(it - LAG);
+            }
+        }
+        u += p.n;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (ok)
+        for (int i = max(from, it - LAG); i < it; ++i) arrive(i);
+    return ok;
+}
+
+// The accumulators of a phase's pieces, as partial sums [piece of the tile][pair][row].
+__device__ bool store_pieces(const Ctx& c, const TcArgs& t, int ph, int& seg, uint32_t tmem) {
+    const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, m = q * 32 + lane;
+    const int ld = ph ? t.r.H : 2 * t.r.F;
+    for (int u = c.first[ph]; u < c.end[ph]; ++seg) {
+        const Piece p = piece_at(c, ph, u);
+        const int a = p.job / c.tiles[ph], tile = p.job - a * c.tiles[ph];
+        const Info e = c.info[a];
+        const int col = ph ? tile * 128 + m : tile * 64 + (m & 63) + (m < 64 ? 0 : t.r.F);
+        const bool real = ph ? col < t.r.H : tile * 64 + (m & 63) < t.r.F;
+        const int ord = blockIdx.x - p.job * c.KS[ph] / c.chunk[ph];
+        float* const to = t.part[ph] + (long long)ord * c.P * ld + col;
+        bool ok = mbar_wait_bounded(c.accfull(seg & 1), (seg >> 1) & 1, c.abort, WAIT_NS);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        tc_fence_after();
+        const uint32_t from = tmem + (seg & 1) * t.L.npad + ((uint32_t)(q * 32) << 16);
+        for (int n0 = 0; n0 < e.n; n0 += 16) {
+            float v[16];
+            tmem_ld16(from + n0, v);
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+                if (n0 + n < e.n && real) __stcg(to + (long long)c.list[e.start + n0 + n] * ld, v[n]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.accempty(seg & 1));
+        u += p.n;
+    }
+    return true;
+}
+
+// All CTAs' workers have come this far, and what they wrote is seen.
+__device__ bool grid_barrier(const Ctx& c, const TcArgs& t, int which) {
+    worker_sync();
+    if (threadIdx.x == W_EPI * 32) {
+        unsigned* const at = t.barrier + which;
+        __threadfence();
+        if (!*c.abort) atomicAdd(at, 1u);  // (a CTA that gave up holds the others, whose waits then run out too)
+        const uint64_t t0 = globaltimer_ns();
+        for (;;) {
+            unsigned v;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+            if (v >= gridDim.x || *c.abort) break;
+            if (globaltimer_ns() - t0 > WAIT_NS) *c.abort = 1;
+        }
+        __threadfence();
+    }
+    worker_sync();
+    return !*c.abort;
+}
+
+// Pieces of a tile: the CTAs that have units of it.
+__device__ __forceinline__ int pieces_of(const Ctx& c, int ph, int job) {
+    const int u = job * c.KS[ph];
+    return (u + c.KS[ph] - 1) / c.chunk[ph] - u / c.chunk[ph] + 1;
+}
+
+template <int DT>
+__device__ void activate(const Ctx& c, const TcArgs& t) {
+    using T = typename Elem<DT>::T;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - W_EPI, tiles = c.tiles[0], F = t.r.F;
+    for (int i = blockIdx.x + w * gridDim.x; i < c.P * tiles; i += gridDim.x * (WORKERS / 32)) {
+        const int p = i / tiles, tile = i - p * tiles, f = tile * 64 + lane * 2;
+        if (c.id[p] < 0 || f >= F) continue;
+        const int n = pieces_of(c, 0, c.act[p] * tiles + tile);
+        float2 g = make_float2(0.f, 0.f), u = g;
+        const float* from = t.part[0] + (long long)p * 2 * F + f;
+        for (int k = 0; k < n; ++k, from += (long long)c.P * 2 * F) {
+            g = fadd2(g, __ldcg(reinterpret_cast<const float2*>(from)));
+            u = fadd2(u, __ldcg(reinterpret_cast<const float2*>(from + F)));
+        }
+        T* const to = static_cast<T*>(t.h) + (long long)p * F + f;
+        to[0] = Elem<DT>::put(g.x / (1.f + expf(-g.x)) * u.x);
+        to[1] = Elem<DT>::put(g.y / (1.f + expf(-g.y)) * u.y);
+    }
+}
+
+template <int DT>
+__device__ void join(const Ctx& c, const TcArgs& t) {
+    using T = typename Elem<DT>::T;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - W_EPI, tiles = c.tiles[1], H = t.r.H;
+    for (int i = blockIdx.x + w * gridDim.x; i < t.r.T * tiles; i += gridDim.x * (WORKERS / 32)) {
+        const int tok = i / tiles, tile = i - tok * tiles, col = tile * 128 + lane * 4;
+        if (col >= H) continue;
+        float s[4] = {};
+        for (int k = 0; k < t.r.K; ++k) {
+            const int p = tok * t.r.K + k;
+            const float wt = c.weight[p];
+            if (c.id[p] < 0) {  // 0, or NaN
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j] += wt;
+                continue;
+            }
+            const int n = pieces_of(c, 1, c.act[p] * tiles + tile);
+            const float* from = t.part[1] + (long long)p * H + col;
+            float4 y = __ldcg(reinterpret_cast<const float4*>(from));
+            for (int j = 1; j < n; ++j) {
+                from += (long long)c.P * H;
+                const float4 z = __ldcg(reinterpret_cast<const float4*>(from));
+                y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
+            }
+            s[0] = fmaf(wt, y.x, s[0]);
+            s[1] = fmaf(wt, y.y, s[1]);
+            s[2] = fmaf(wt, y.z, s[2]);
+            s[3] = fmaf(wt, y.w, s[3]);
+        }
+        T* const to = static_cast<T*>(t.r.out) + tok * t.r.ldo + col;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = Elem<DT>::put(s[j]);
+    }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const __grid_constant__ CUtensorMap up,
+                                                          const __grid_constant__ CUtensorMap down) {
+    extern __shared__ unsigned char raw[];
+    __shared__ int counts[2][NWARP];
+    const uint32_t lead = smem_u32(raw);
+    const uint32_t skip = (1024 - (lead & 1023)) & 1023;
+    Ctx c;
+    c.sm = raw + skip;
+    c.base = lead + skip;
+    c.bars = c.base + t.L.bars;
+    uint32_t* const slot = reinterpret_cast<uint32_t*>(c.sm + t.L.bars + BAR_BYTES - 8);
+    c.abort = reinterpret_cast<volatile int*>(slot + 1);
+    c.weight = reinterpret_cast<float*>(c.sm + t.L.weight);
+    c.list = reinterpret_cast<unsigned short*>(c.sm + t.L.list);
+    c.act = reinterpret_cast<unsigned short*>(c.sm + t.L.act);
+    c.id = reinterpret_cast<short*>(c.sm + t.L.id);
+    c.info = reinterpret_cast<Info*>(c.sm + t.L.info);
+    unsigned(*const mask)[4] = reinterpret_cast<unsigned(*)[4]>(c.sm + t.L.mask);  // the tokens of each expert
+    c.S = t.L.stages;
+    c.P = t.r.T * t.r.K;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = t.r.E, K = t.r.K;
+    if (tid == 0) {
+        for (int s = 0; s < c.S; ++s) {
+            mbar_init(c.full(s), 5);  // the producer's, and one of each loading warp
+            mbar_init(c.empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(c.accfull(b), 1);
+            mbar_init(c.accempty(b), 4);
+        }
+        mbar_init(c.drain(), 1);
+        fence_mbar_init();
+        *c.abort = 0;
+    }
+    int cols = 32;
+    while (cols < 2 * t.L.npad) cols *= 2;
+    if (warp == W_MMA) {
+        tmem_alloc(smem_u32(slot), cols);
+        tmem_relinquish();
+    }
+    // choose
+    for (int i = tid; i < E * 4; i += NT) mask[i / 4][i % 4] = 0u;
+    __syncthreads();
+    for (int tok = warp; tok < t.r.T; tok += NWARP) {
+        int id;
+        float w;
+        routed_choose(t.r.logits + (long long)tok * E, E, K, t.r.renorm, t.r.scale, id, w);
+        if (lane < K) {
+            const int p = tok * K + lane;
+            c.id[p] = (short)id;
+            c.weight[p] = w;
+            if (id >= 0) atomicOr(&mask[id][tok >> 5], 1u << (tok & 31));
+            if (tok % gridDim.x == blockIdx.x) {
+                t.r.ids[p] = id;
+                t.r.weights[p] = w;
+            }
+        }
+    }
+    __syncthreads();
+    // The experts in use, in order, and where their lists start: a thread four experts.
+    constexpr int PER = (ROUTED_MAX_E + NT - 1) / NT;
+    int used = 0, tokens = 0, n[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = tid * PER + j;
+        n[j] = e < E ? __popc(mask[e][0]) + __popc(mask[e][1]) + __popc(mask[e][2]) + __popc(mask[e][3]) : 0;
+        used += n[j] > 0;
+        tokens += n[j];
+    }
+    int before = used | tokens << 16;  // (at most 1024 and 4096)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+    }
+    if (lane == 31) counts[0][warp] = before;
+    __syncthreads();
+    int at = before - (used | tokens << 16), all = 0;
+    for (int w = 0; w < NWARP; ++w) {
+        if (w < warp) at += counts[0][w];
+        all += counts[0][w];
+    }
+    c.active = all & 0xffff;
+    int a = at & 0xffff, start = at >> 16;
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        if (n[j] > 0) {
+            c.info[a] = Info{tid * PER + j, start, n[j]};
+            for (int q = 0, k = start; q < 4; ++q)
+                for (unsigned m = mask[tid * PER + j][q]; m; m &= m - 1) c.list[k++] = (unsigned short)(q * 32 + __ffs(m) - 1);
+            ++a;
+            start += n[j];
+        }
+    __syncthreads();
+    // From tokens to pairs: which of the token's choices it is, and the pair's expert.
+    for (int i = warp; i < c.active; i += NWARP) {
+        const Info e = c.info[i];
+        for (int j = lane; j < e.n; j += 32) {
+            const int tok = c.list[e.start + j];
+            int k = 0;
+            while (c.id[tok * K + k] != e.expert) ++k;
+            c.list[e.start + j] = (unsigned short)(tok * K + k);
+            c.act[tok * K + k] = (unsigned short)i;
+        }
+    }
+    const int dims[PHASES] = {t.r.H, t.r.F};
+    c.tiles[0] = (t.r.F + 63) / 64;
+    c.tiles[1] = (t.r.H + 127) / 128;
+    for (int ph = 0; ph < PHASES; ++ph) {
+        c.KS[ph] = (dims[ph] + KSTEP - 1) / KSTEP;
+        const int U = c.active * c.tiles[ph] * c.KS[ph];
+        // An even share each, but not so small that a tile has more pieces than there is room for.
+        c.chunk[ph] = max(1, max((U + (int)gridDim.x - 1) / (int)gridDim.x,
+                                 t.pieces[ph] > 1 ? (c.KS[ph] + t.pieces[ph] - 2) / (t.pieces[ph] - 1) : c.KS[ph]));
+        c.first[ph] = (int)min((long long)U, (long long)blockIdx.x * c.chunk[ph]);
+        c.end[ph] = min(U, c.first[ph] + c.chunk[ph]);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+
+    if (warp == W_PRODUCER) {
+        if (lane == 0) produce(c, t, &up, &down);
+    } else if (warp == W_MMA) {
+        if (lane == 0) multiply<DT>(c, t, tmem);
+    } else {
+        int seg = 0, it = 0;
+        bool ok = warp < W_LOAD ? store_pieces(c, t, 0, seg, tmem) : load_tokens(c, t, 0, it);
+        ok = grid_barrier(c, t, 0);
+        if (ok) activate<DT>(c, t);
+        if (ok) ok = grid_barrier(c, t, 1);
+        if (ok) {
+            if (warp < W_LOAD) store_pieces(c, t, 1, seg, tmem);
+            else load_tokens(c, t, 1, it);
+            ok = grid_barrier(c, t, 2);
+        }
+        if (ok) join<DT>(c, t);
+        else {
+            using T = typename Elem<DT>::T;
+            for (long long i = (long long)blockIdx.x * WORKERS + tid - W_EPI * 32; i < (long long)t.r.T * t.r.H;
+                 i += (long long)gridDim.x * WORKERS)
+                static_cast<T*>(t.r.out)[i / t.r.H * t.r.ldo + i % t.r.H] = Elem<DT>::put(NAN);
+            if (tid == W_EPI * 32) atomicOr(t.status, SOT_DEV_TIMEOUT);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) tmem_dealloc(tmem, cols);
+}
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// rows x cols of 16-bit elements in boxes of 64 x 64, 128-byte swizzle.
+bool weight_map(CUtensorMap* map, const void* p, int dtype, long long rows, int cols) {
+    const EncodeTiled encode = encoder();
+    if (!encode) return false;
+    const cuuint64_t dim[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)cols * 2};
+    const cuuint32_t box[2] = {KSTEP, 64}, step[2] = {1, 1};
+    return encode(map, dtype == SOT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void*>(p), dim, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int MAX_SMEM = 227 * 1024 - 1024;  // the kernel's static part is below 1 KB
+
+Layout layout(const RoutedArgs& a) {
+    Layout L = {};
+    const int P = a.T * a.K;
+    int at = 0;
+    const auto place = [&](int bytes) {
+        const int here = at;
+        at = (at + bytes + 15) / 16 * 16;
+        return here;
+    };
+    L.npad = (a.T + 15) / 16 * 16;
+    L.stage = A_BYTES + (L.npad * KSTEP * 2 + 1023) / 1024 * 1024;
+    const int other = (BAR_BYTES + 15) / 16 * 16 + (4 * P + 15) / 16 * 16 + 3 * ((2 * P + 15) / 16 * 16) +
+                      ((int)sizeof(Info) * a.E + 15) / 16 * 16 + 16 * a.E;
+    L.stages = (MAX_SMEM - 1024 - other) / L.stage;
+    if (L.stages > MAX_STAGES) L.stages = MAX_STAGES;
+    place(L.stages * L.stage);
+    L.bars = place(BAR_BYTES);
+    L.weight = place(4 * P);
+    L.list = place(2 * P);
+    L.act = place(2 * P);
+    L.id = place(2 * P);
+    L.info = place((int)sizeof(Info) * a.E);
+    L.mask = place(16 * a.E);
+    L.total = at + 1024;
+    return L;
+}
+
+// Pieces of a tile that there is room for: those an even share leaves where the tokens choose no more than K experts.
+int pieces(const RoutedArgs& a, int ph, int sms) {
+    const int KS = ((ph ? a.F : a.H) + KSTEP - 1) / KSTEP, tiles = ph ? (a.H + 127) / 128 : (a.F + 63) / 64;
+    const int p = (sms + tiles * a.K - 1) / (tiles * a.K) + 1;
+    return p < KS ? p : KS;
+}
+
+}  // namespace
+
+bool routed_tc_fits(const RoutedArgs& a) {
+    return a.dtype != SOT_F32 && a.H % 8 == 0 && a.F % 8 == 0 && a.ldx % 8 == 0 && (unsigned long long)a.x % 16 == 0 &&
+           (unsigned long long)a.gate_up % 16 == 0 && (unsigned long long)a.down % 16 == 0 &&
+           (long long)a.E * 2 * a.F < 1ll << 31 && (long long)a.E * a.H < 1ll << 31 &&
+           // (units are counted in 32 bits)
+           (long long)a.E * ((a.F + 63) / 64) * ((a.H + 63) / 64) < 1ll << 30 &&
+           (long long)a.E * ((a.H + 127) / 128) * ((a.F + 63) / 64) < 1ll << 30 && layout(a).stages > LAG;
+}
+
+RoutedTcPlan routed_tc_plan(const RoutedArgs& a, int sms) {
+    RoutedTcPlan p = {};
+    const auto place = [&](size_t bytes) {
+        const size_t at = p.scratch;
+        p.scratch = (at + bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    const size_t P = (size_t)a.T * a.K;
+    p.barrier_at = place(4 * sizeof(unsigned));
+    p.up_at = place(sizeof(float) * pieces(a, 0, sms) * P * 2 * a.F);
+    p.down_at = place(sizeof(float) * pieces(a, 1, sms) * P * a.H);
+    p.h_at = place(2 * P * a.F);
+    return p;
+}
+
+cudaError_t launch_routed_tc(const RoutedArgs& a, const RoutedTcPlan& p, unsigned char* scratch, int sms, cudaStream_t st) {
+    TcArgs t = {};
+    t.r = a;
+    t.L = layout(a);
+    t.barrier = reinterpret_cast<unsigned*>(scratch + p.barrier_at);
+    t.part[0] = reinterpret_cast<float*>(scratch + p.up_at);
+    t.part[1] = reinterpret_cast<float*>(scratch + p.down_at);
+    t.h = scratch + p.h_at;
+    for (int ph = 0; ph < PHASES; ++ph) t.pieces[ph] = pieces(a, ph, sms);
+    cudaError_t e = async_status_address(&t.status);
+    if (e != cudaSuccess) return e;
+    CUtensorMap up, down;
+    if (!weight_map(&up, a.gate_up, a.dtype, (long long)a.E * 2 * a.F, a.H) ||
+        !weight_map(&down, a.down, a.dtype, (long long)a.E * a.H, a.F))
+        return cudaErrorInvalidValue;
+    const void* const kern = a.dtype == SOT_BF16 ? (const void*)routed_tc_kernel<SOT_BF16> : (const void*)routed_tc_kernel<SOT_F16>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_SMEM);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&t, &up, &down};
+    count_launches(1);
+    return cudaLaunchCooperativeKernel(kern, dim3(sms), dim3(NT), args, t.L.total, st);
+}
+
+}  // namespace sot

@@ -26,10 +26,20 @@ struct RoutedArgs {
     float *h, *y;    // [T K, F], [T K, H]
 };
 
+struct RoutedTcPlan {
+    size_t barrier_at, up_at, down_at, h_at, scratch;
+};
 struct RoutedPlan {
+    bool tc;  // the experts' products on the tensor cores
     size_t h_at, y_at, scratch;
+    RoutedTcPlan on_tc;
 };
 RoutedPlan routed_plan(const RoutedArgs& a, int sms);
 cudaError_t launch_routed(RoutedArgs a, const RoutedPlan& p, unsigned char* scratch, int sms, cudaStream_t st);
+
+// The tensor cores' part (k_routed_tc.cu): everything after the scores.
+bool routed_tc_fits(const RoutedArgs& a);
+RoutedTcPlan routed_tc_plan(const RoutedArgs& a, int sms);
+cudaError_t launch_routed_tc(const RoutedArgs& a, const RoutedTcPlan& p, unsigned char* scratch, int sms, cudaStream_t st);
 
 }  // namespace sot
