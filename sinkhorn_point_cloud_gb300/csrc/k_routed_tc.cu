@@ -22,17 +22,18 @@ namespace sot {
 
 namespace {
 
-constexpr int NWARP = 10, NT = NWARP * 32;
-constexpr int W_PRODUCER = 0, W_MMA = 1, W_EPI = 2, W_LOAD = 6;  // first warps of each role (4 epilogue, 4 loading)
-constexpr int WORKERS = 256;                                     // threads of the last two
+constexpr int LOADERS = 8;  // warps that fetch the tokens' side, a unit each in turn
+constexpr int NWARP = 6 + LOADERS, NT = NWARP * 32;
+constexpr int W_PRODUCER = 0, W_MMA = 1, W_EPI = 2, W_LOAD = 6;  // first warps of each role (4 in the epilogue)
+constexpr int WORKERS = (4 + LOADERS) * 32;                      // threads of the last two
 constexpr int KSTEP = 64, A_BYTES = 128 * KSTEP * 2;
-constexpr int MAX_STAGES = 12, LAG = 3;
+constexpr int MIN_STAGES = 3, MAX_STAGES = 12;
 constexpr unsigned long long WAIT_NS = 2000000000ull;
 constexpr int PHASES = 2;  // 0: up, 1: down
 
 struct Layout {  // byte offsets in dynamic shared memory (from a 1024-byte boundary)
     int stage, stages, npad;
-    int bars, weight, list, act, id, info, mask, total;
+    int bars, weight, toks, list, act, id, info, mask, total;
 };
 
 struct TcArgs {
@@ -80,7 +81,7 @@ struct Ctx {
     uint32_t base, bars;
     volatile int* abort;
     float* weight;
-    unsigned short *list, *act;
+    unsigned short *toks, *list, *act;  // by expert: tokens, pairs (token, choice); by pair: its expert's place in info
     short* id;
     Info* info;
     int P, active;
@@ -104,37 +105,60 @@ __device__ __forceinline__ Piece piece_at(const Ctx& c, int ph, int u) {
     const int job = u / c.KS[ph], ks = u - job * c.KS[ph];
     return Piece{job, ks, min(c.KS[ph] - ks, c.end[ph] - u)};
 }
+// A role's place in the ring, counted without divisions: these would be most of what a unit costs the
+// producing and the multiplying thread (400 ns a unit with them).
+struct Turn {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ void skip(int n, int stages) {
+        s += n;
+        while (s >= stages) {
+            s -= stages;
+            phase ^= 1;
+        }
+    }
+};
 __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
 
 __device__ void produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, const CUtensorMap* down) {
     const uint64_t policy = policy_drop();
-    int it = 0;
-    for (int ph = 0; ph < PHASES; ++ph) {
+    const int stages = c.S, stage = t.L.stage;
+    Turn at;
+    int issued = 0;
+    bool ok = true;
+    for (int ph = 0; ok && ph < PHASES; ++ph) {
         const CUtensorMap* const map = ph ? down : up;
-        for (int u = c.first[ph]; u < c.end[ph];) {
+        for (int u = c.first[ph]; ok && u < c.end[ph];) {
             const Piece p = piece_at(c, ph, u);
             const int a = p.job / c.tiles[ph], tile = p.job - a * c.tiles[ph], e = c.info[a].expert;
             const int r0 = ph ? e * t.r.H + tile * 128 : e * 2 * t.r.F + tile * 64, r1 = ph ? r0 + 64 : r0 + t.r.F;
-            for (int i = 0; i < p.n; ++i, ++it) {
-                const int s = it % c.S;
-                if (!mbar_wait_bounded(c.empty(s), ((it / c.S) & 1) ^ 1, c.abort, WAIT_NS)) goto out;
-                mbar_arrive_expect_tx(c.full(s), A_BYTES);
-                const uint32_t dst = c.base + s * t.L.stage;
-                tma_rows(dst, map, (p.ks + i) * KSTEP, r0, c.full(s), policy);
-                tma_rows(dst + A_BYTES / 2, map, (p.ks + i) * KSTEP, r1, c.full(s), policy);
+            for (int k = p.ks * KSTEP, end = k + p.n * KSTEP; k < end; k += KSTEP) {
+                ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
+                if (!ok) break;
+                const uint32_t full = c.full(at.s), dst = c.base + at.s * stage;
+                mbar_arrive_expect_tx(full, A_BYTES);
+                tma_rows(dst, map, k, r0, full, policy);
+                tma_rows(dst + A_BYTES / 2, map, k, r1, full, policy);
+                at.next(stages);
+                ++issued;
             }
             u += p.n;
         }
     }
-out:
     if (*c.abort) {
-        // Copies in flight land before the CTA goes: the loading warps may have given up, so their arrivals are made here.
+        // Copies in flight land before the CTA goes: the loading warps may have given up, so their arrivals are made
+        // here (one too many does no harm any more).
         int dummy = 0;
-        for (int i = max(0, it - c.S); i < it; ++i) {
-            const int s = i % c.S;
-            for (int k = 0; k < 4; ++k)
-                if (!mbar_try_wait(c.full(s), (i / c.S) & 1)) mbar_arrive(c.full(s));
-            mbar_wait_bounded(c.full(s), (i / c.S) & 1, &dummy, WAIT_NS);
+        for (int i = max(0, issued - stages); i < issued; ++i) {
+            const int s = i % stages;
+            if (!mbar_try_wait(c.full(s), (i / stages) & 1)) mbar_arrive(c.full(s));
+            mbar_wait_bounded(c.full(s), (i / stages) & 1, &dummy, WAIT_NS);
         }
     }
 }
@@ -142,7 +166,10 @@ out:
 template <int DT>
 __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
     constexpr uint32_t format = DT == SOT_BF16 ? (1u << 7) | (1u << 10) : 0u;
-    int it = 0, seg = 0;
+    const int stages = c.S;
+    const uint64_t a0 = sw128_desc(c.base), step = t.L.stage >> 4;
+    Turn at;
+    int seg = 0;
     bool ok = true, issued = false;
     for (int ph = 0; ok && ph < PHASES; ++ph)
         for (int u = c.first[ph]; ok && u < c.end[ph]; ++seg) {
@@ -150,19 +177,17 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
             const uint32_t idesc = f16_idesc(128, pad16(c.info[p.job / c.tiles[ph]].n)) | format;
             const uint32_t d = tmem + (seg & 1) * t.L.npad;
             ok = mbar_wait_bounded(c.accempty(seg & 1), ((seg >> 1) & 1) ^ 1, c.abort, WAIT_NS);
-            for (int i = 0; ok && i < p.n; ++i, ++it) {
-                const int s = it % c.S;
-                if (!mbar_wait_bounded(c.full(s), (it / c.S) & 1, c.abort, WAIT_NS)) {
-                    ok = false;
-                    break;
-                }
+            for (int i = 0; ok && i < p.n; ++i) {
+                ok = mbar_wait_bounded(c.full(at.s), at.phase, c.abort, WAIT_NS);
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t a = c.base + s * t.L.stage, b = a + A_BYTES;
+                const uint64_t a = a0 + at.s * step, b = a + (A_BYTES >> 4);
+                tc_mma_f16(d, a, b, idesc, i > 0);
 #pragma unroll
-                for (int k = 0; k < KSTEP / 16; ++k)
-                    tc_mma_f16(d, sw128_desc(a + 32 * k), sw128_desc(b + 32 * k), idesc, i > 0 || k > 0 ? 1u : 0u);
+                for (int k = 1; k < KSTEP / 16; ++k) tc_mma_f16(d, a + 2 * k, b + 2 * k, idesc, 1u);
                 issued = true;
-                tc_commit(c.empty(s));
+                tc_commit(c.empty(at.s));
+                at.next(stages);
             }
             if (ok) tc_commit(c.accfull(seg & 1));
             u += p.n;
@@ -176,43 +201,36 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
 
 // The tokens' side of a phase: rows of x or h, swizzled as the tensor cores read them.  A row past the expert's
 // last token is not written: what it holds only reaches columns that nobody reads.
-__device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, int& it) {
-    const int tid = threadIdx.x - W_LOAD * 32, lane = tid & 31;
+__device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int& turn) {
+    const int lane = threadIdx.x & 31, ch = lane & 7, stages = c.S, stage = t.L.stage;
     const int K = ph ? t.r.F : t.r.H;
-    const int from = it;
-    bool ok = true;
-    const auto arrive = [&](int i) {  // this thread's copies for unit i have landed
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(c.full(i % c.S));
-    };
-    for (int u = c.first[ph]; ok && u < c.end[ph];) {
+    const long long ld = ph ? t.r.F : t.r.ldx;
+    const unsigned short* const from = static_cast<const unsigned short*>(ph ? t.h : t.r.x) + ch * 8;
+    const unsigned short* const rows = ph ? c.list : c.toks;
+    for (int u = c.first[ph]; u < c.end[ph];) {
         const Piece p = piece_at(c, ph, u);
         const Info e = c.info[p.job / c.tiles[ph]];
-        for (int i = 0; i < p.n; ++i, ++it) {
-            const int s = it % c.S, k0 = (p.ks + i) * KSTEP;
-            ok = mbar_wait_bounded(c.empty(s), ((it / c.S) & 1) ^ 1, c.abort, WAIT_NS);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t dst = c.base + s * t.L.stage + A_BYTES;
-            for (int q = tid; q < e.n * 8; q += 128) {
-                const int row = q >> 3, ch = q & 7, k = k0 + ch * 8, pair = c.list[e.start + row];
-                const unsigned short* const src = ph ? static_cast<const unsigned short*>(t.h) + (long long)pair * K
-                                                     : static_cast<const unsigned short*>(t.r.x) + pair / t.r.K * t.r.ldx;
-                copy16(dst + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4), k < K ? src + k : src, k < K ? 16 : 0);
+        // turn: units until this warp's next one, whose place in the ring is `at`
+        for (; turn < p.n; turn += LOADERS) {
+            const int k0 = (p.ks + turn) * KSTEP;
+            const bool ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            const uint32_t dst = c.base + at.s * stage + A_BYTES;
+            const bool real = k0 + ch * 8 < K;
+            for (int row = lane >> 3; row < e.n; row += 4) {
+                const unsigned short* const src = from + rows[e.start + row] * ld;
+                copy16(dst + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4), real ? src + k0 : src, real ? 16 : 0);
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            if (it - from >= LAG) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(LAG) : "memory");
-                arrive(it - LAG);
-            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.full(at.s));
+            at.skip(LOADERS, stages);
         }
+        turn -= p.n;
         u += p.n;
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok)
-        for (int i = max(from, it - LAG); i < it; ++i) arrive(i);
-    return ok;
+    return true;
 }
 
 // The accumulators of a phase's pieces, as partial sums [piece of the tile][pair][row].
@@ -292,25 +310,27 @@ __device__ void activate(const Ctx& c, const TcArgs& t) {
     }
 }
 
+// A warp takes 32 columns of a token: four lanes share four columns and take a quarter of the experts each.
 template <int DT>
 __device__ void join(const Ctx& c, const TcArgs& t) {
     using T = typename Elem<DT>::T;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - W_EPI, tiles = c.tiles[1], H = t.r.H;
-    for (int i = blockIdx.x + w * gridDim.x; i < t.r.T * tiles; i += gridDim.x * (WORKERS / 32)) {
-        const int tok = i / tiles, tile = i - tok * tiles, col = tile * 128 + lane * 4;
-        if (col >= H) continue;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - W_EPI, H = t.r.H, per = (H + 31) / 32;
+    for (int i = blockIdx.x + w * gridDim.x; i < t.r.T * per; i += gridDim.x * (WORKERS / 32)) {
+        const int tok = i / per, col = (i - tok * per) * 32 + (lane & 7) * 4;
+        const bool real = col < H;
         float s[4] = {};
-        for (int k = 0; k < t.r.K; ++k) {
+        for (int k = lane >> 3; k < t.r.K; k += 4) {
             const int p = tok * t.r.K + k;
             const float wt = c.weight[p];
-            if (c.id[p] < 0) {  // 0, or NaN
+            if (c.id[p] < 0 || !real) {  // 0, or NaN
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[j] += wt;
                 continue;
             }
-            const int n = pieces_of(c, 1, c.act[p] * tiles + tile);
+            const int n = pieces_of(c, 1, c.act[p] * c.tiles[1] + (col >> 7));
             const float* from = t.part[1] + (long long)p * H + col;
             float4 y = __ldcg(reinterpret_cast<const float4*>(from));
+#pragma unroll 2
             for (int j = 1; j < n; ++j) {
                 from += (long long)c.P * H;
                 const float4 z = __ldcg(reinterpret_cast<const float4*>(from));
@@ -321,9 +341,16 @@ __device__ void join(const Ctx& c, const TcArgs& t) {
             s[2] = fmaf(wt, y.z, s[2]);
             s[3] = fmaf(wt, y.w, s[3]);
         }
-        T* const to = static_cast<T*>(t.r.out) + tok * t.r.ldo + col;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) to[j] = Elem<DT>::put(s[j]);
+        for (int j = 0; j < 4; ++j) {
+            s[j] += __shfl_xor_sync(0xffffffffu, s[j], 8);
+            s[j] += __shfl_xor_sync(0xffffffffu, s[j], 16);
+        }
+        if (lane < 8 && real) {
+            T* const to = static_cast<T*>(t.r.out) + tok * t.r.ldo + col;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[j] = Elem<DT>::put(s[j]);
+        }
     }
 }
 
@@ -341,6 +368,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     uint32_t* const slot = reinterpret_cast<uint32_t*>(c.sm + t.L.bars + BAR_BYTES - 8);
     c.abort = reinterpret_cast<volatile int*>(slot + 1);
     c.weight = reinterpret_cast<float*>(c.sm + t.L.weight);
+    c.toks = reinterpret_cast<unsigned short*>(c.sm + t.L.toks);
     c.list = reinterpret_cast<unsigned short*>(c.sm + t.L.list);
     c.act = reinterpret_cast<unsigned short*>(c.sm + t.L.act);
     c.id = reinterpret_cast<short*>(c.sm + t.L.id);
@@ -351,7 +379,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = t.r.E, K = t.r.K;
     if (tid == 0) {
         for (int s = 0; s < c.S; ++s) {
-            mbar_init(c.full(s), 5);  // the producer's, and one of each loading warp
+            mbar_init(c.full(s), 2);  // the producer's arrival and a loading warp's
             mbar_init(c.empty(s), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -417,7 +445,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         if (n[j] > 0) {
             c.info[a] = Info{tid * PER + j, start, n[j]};
             for (int q = 0, k = start; q < 4; ++q)
-                for (unsigned m = mask[tid * PER + j][q]; m; m &= m - 1) c.list[k++] = (unsigned short)(q * 32 + __ffs(m) - 1);
+                for (unsigned m = mask[tid * PER + j][q]; m; m &= m - 1) c.toks[k++] = (unsigned short)(q * 32 + __ffs(m) - 1);
             ++a;
             start += n[j];
         }
@@ -426,7 +454,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     for (int i = warp; i < c.active; i += NWARP) {
         const Info e = c.info[i];
         for (int j = lane; j < e.n; j += 32) {
-            const int tok = c.list[e.start + j];
+            const int tok = c.toks[e.start + j];
             int k = 0;
             while (c.id[tok * K + k] != e.expert) ++k;
             c.list[e.start + j] = (unsigned short)(tok * K + k);
@@ -455,14 +483,19 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     } else if (warp == W_MMA) {
         if (lane == 0) multiply<DT>(c, t, tmem);
     } else {
-        int seg = 0, it = 0;
-        bool ok = warp < W_LOAD ? store_pieces(c, t, 0, seg, tmem) : load_tokens(c, t, 0, it);
-        ok = grid_barrier(c, t, 0);
+        int seg = 0, turn = warp - W_LOAD;
+        Turn at;
+        if (warp < W_LOAD) store_pieces(c, t, 0, seg, tmem);
+        else {
+            at.skip(turn, c.S);
+            load_tokens(c, t, 0, at, turn);
+        }
+        bool ok = grid_barrier(c, t, 0);
         if (ok) activate<DT>(c, t);
         if (ok) ok = grid_barrier(c, t, 1);
         if (ok) {
             if (warp < W_LOAD) store_pieces(c, t, 1, seg, tmem);
-            else load_tokens(c, t, 1, it);
+            else load_tokens(c, t, 1, at, turn);
             ok = grid_barrier(c, t, 2);
         }
         if (ok) join<DT>(c, t);
@@ -521,13 +554,14 @@ Layout layout(const RoutedArgs& a) {
     };
     L.npad = (a.T + 15) / 16 * 16;
     L.stage = A_BYTES + (L.npad * KSTEP * 2 + 1023) / 1024 * 1024;
-    const int other = (BAR_BYTES + 15) / 16 * 16 + (4 * P + 15) / 16 * 16 + 3 * ((2 * P + 15) / 16 * 16) +
+    const int other = (BAR_BYTES + 15) / 16 * 16 + (4 * P + 15) / 16 * 16 + 4 * ((2 * P + 15) / 16 * 16) +
                       ((int)sizeof(Info) * a.E + 15) / 16 * 16 + 16 * a.E;
     L.stages = (MAX_SMEM - 1024 - other) / L.stage;
     if (L.stages > MAX_STAGES) L.stages = MAX_STAGES;
     place(L.stages * L.stage);
     L.bars = place(BAR_BYTES);
     L.weight = place(4 * P);
+    L.toks = place(2 * P);
     L.list = place(2 * P);
     L.act = place(2 * P);
     L.id = place(2 * P);
@@ -552,7 +586,7 @@ bool routed_tc_fits(const RoutedArgs& a) {
            (long long)a.E * 2 * a.F < 1ll << 31 && (long long)a.E * a.H < 1ll << 31 &&
            // (units are counted in 32 bits)
            (long long)a.E * ((a.F + 63) / 64) * ((a.H + 63) / 64) < 1ll << 30 &&
-           (long long)a.E * ((a.H + 127) / 128) * ((a.F + 63) / 64) < 1ll << 30 && layout(a).stages > LAG;
+           (long long)a.E * ((a.H + 127) / 128) * ((a.F + 63) / 64) < 1ll << 30 && layout(a).stages >= MIN_STAGES;
 }
 
 RoutedTcPlan routed_tc_plan(const RoutedArgs& a, int sms) {
