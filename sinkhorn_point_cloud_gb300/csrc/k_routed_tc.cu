@@ -69,6 +69,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+// One lane of a warp that has come here as a whole.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
 __device__ __forceinline__ void worker_sync() { asm volatile("bar.sync 1, %0;" ::"n"(WORKERS) : "memory"); }
 
 struct Info {  // an expert that some token chose
@@ -94,8 +100,9 @@ struct Ctx {
     __device__ __forceinline__ uint32_t accfull(int b) const { return bars + 8 * (2 * MAX_STAGES + b); }
     __device__ __forceinline__ uint32_t accempty(int b) const { return bars + 8 * (2 * MAX_STAGES + 2 + b); }
     __device__ __forceinline__ uint32_t drain() const { return bars + 8 * (2 * MAX_STAGES + 4); }
+    __device__ __forceinline__ uint32_t go() const { return bars + 8 * (2 * MAX_STAGES + 5); }
 };
-constexpr int BAR_BYTES = 8 * (2 * MAX_STAGES + 5) + 8;  // and the TMEM address, and the abort flag
+constexpr int BAR_BYTES = 8 * (2 * MAX_STAGES + 6) + 8;  // and the TMEM address, and the abort flag
 
 // A piece: units [u, u + n) of one tile.
 struct Piece {
@@ -131,7 +138,8 @@ __device__ void produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, co
     const int stages = c.S, stage = t.L.stage;
     Turn at;
     int issued = 0;
-    bool ok = true;
+    // The loading warps' first requests go out first: behind a ring of weights they take 5 us instead of 1.
+    bool ok = mbar_wait_bounded(c.go(), 0, c.abort, WAIT_NS);
     for (int ph = 0; ok && ph < PHASES; ++ph) {
         const CUtensorMap* const map = ph ? down : up;
         for (int u = c.first[ph]; ok && u < c.end[ph];) {
@@ -177,22 +185,27 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
             const uint32_t idesc = f16_idesc(128, pad16(c.info[p.job / c.tiles[ph]].n)) | format;
             const uint32_t d = tmem + (seg & 1) * t.L.npad;
             ok = mbar_wait_bounded(c.accempty(seg & 1), ((seg >> 1) & 1) ^ 1, c.abort, WAIT_NS);
+            ok = __all_sync(0xffffffffu, ok);
             for (int i = 0; ok && i < p.n; ++i) {
                 ok = mbar_wait_bounded(c.full(at.s), at.phase, c.abort, WAIT_NS);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t a = a0 + at.s * step, b = a + (A_BYTES >> 4);
-                tc_mma_f16(d, a, b, idesc, i > 0);
+                if (elect_one()) {
+                    tc_mma_f16(d, a, b, idesc, i > 0);
 #pragma unroll
-                for (int k = 1; k < KSTEP / 16; ++k) tc_mma_f16(d, a + 2 * k, b + 2 * k, idesc, 1u);
+                    for (int k = 1; k < KSTEP / 16; ++k) tc_mma_f16(d, a + 2 * k, b + 2 * k, idesc, 1u);
+                    tc_commit(c.empty(at.s));
+                    if (i == p.n - 1) tc_commit(c.accfull(seg & 1));
+                }
+                __syncwarp();
                 issued = true;
-                tc_commit(c.empty(at.s));
                 at.next(stages);
             }
-            if (ok) tc_commit(c.accfull(seg & 1));
             u += p.n;
         }
-    if (issued) {  // nothing is under way when the CTA frees its TMEM
+    if (issued && elect_one()) {  // nothing is under way when the CTA frees its TMEM
         int dummy = 0;
         tc_commit(c.drain());
         mbar_wait_bounded(c.drain(), 0, &dummy, WAIT_NS);
@@ -207,6 +220,7 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
     const long long ld = ph ? t.r.F : t.r.ldx;
     const unsigned short* const from = static_cast<const unsigned short*>(ph ? t.h : t.r.x) + ch * 8;
     const unsigned short* const rows = ph ? c.list : c.toks;
+    bool first = ph == 0;
     for (int u = c.first[ph]; u < c.end[ph];) {
         const Piece p = piece_at(c, ph, u);
         const Info e = c.info[p.job / c.tiles[ph]];
@@ -221,6 +235,8 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
                 const unsigned short* const src = from + rows[e.start + row] * ld;
                 copy16(dst + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4), real ? src + k0 : src, real ? 16 : 0);
             }
+            if (first && lane == 0) mbar_arrive(c.go());
+            first = false;
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
@@ -230,6 +246,7 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
         turn -= p.n;
         u += p.n;
     }
+    if (first && lane == 0) mbar_arrive(c.go());  // (a warp without a unit)
     return true;
 }
 
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     c.act = reinterpret_cast<unsigned short*>(c.sm + t.L.act);
     c.id = reinterpret_cast<short*>(c.sm + t.L.id);
     c.info = reinterpret_cast<Info*>(c.sm + t.L.info);
-    unsigned(*const mask)[4] = reinterpret_cast<unsigned(*)[4]>(c.sm + t.L.mask);  // the tokens of each expert
+    uint4* const mask = reinterpret_cast<uint4*>(c.sm + t.L.mask);  // the tokens of each expert
     c.S = t.L.stages;
     c.P = t.r.T * t.r.K;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = t.r.E, K = t.r.K;
@@ -387,6 +404,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
             mbar_init(c.accempty(b), 4);
         }
         mbar_init(c.drain(), 1);
+        mbar_init(c.go(), LOADERS);
         fence_mbar_init();
         *c.abort = 0;
     }
@@ -397,7 +415,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         tmem_relinquish();
     }
     // choose
-    for (int i = tid; i < E * 4; i += NT) mask[i / 4][i % 4] = 0u;
+    for (int i = tid; i < E; i += NT) mask[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     for (int tok = warp; tok < t.r.T; tok += NWARP) {
         int id;
@@ -407,7 +425,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
             const int p = tok * K + lane;
             c.id[p] = (short)id;
             c.weight[p] = w;
-            if (id >= 0) atomicOr(&mask[id][tok >> 5], 1u << (tok & 31));
+            if (id >= 0) atomicOr(reinterpret_cast<unsigned*>(mask + id) + (tok >> 5), 1u << (tok & 31));
             if (tok % gridDim.x == blockIdx.x) {
                 t.r.ids[p] = id;
                 t.r.weights[p] = w;
@@ -418,10 +436,11 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     // The experts in use, in order, and where their lists start: a thread four experts.
     constexpr int PER = (ROUTED_MAX_E + NT - 1) / NT;
     int used = 0, tokens = 0, n[PER];
+    uint4 m[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int e = tid * PER + j;
-        n[j] = e < E ? __popc(mask[e][0]) + __popc(mask[e][1]) + __popc(mask[e][2]) + __popc(mask[e][3]) : 0;
+        m[j] = tid * PER + j < E ? mask[tid * PER + j] : make_uint4(0u, 0u, 0u, 0u);
+        n[j] = __popc(m[j].x) + __popc(m[j].y) + __popc(m[j].z) + __popc(m[j].w);
         used += n[j] > 0;
         tokens += n[j];
     }
@@ -434,6 +453,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     if (lane == 31) counts[0][warp] = before;
     __syncthreads();
     int at = before - (used | tokens << 16), all = 0;
+#pragma unroll
     for (int w = 0; w < NWARP; ++w) {
         if (w < warp) at += counts[0][w];
         all += counts[0][w];
@@ -444,8 +464,11 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     for (int j = 0; j < PER; ++j)
         if (n[j] > 0) {
             c.info[a] = Info{tid * PER + j, start, n[j]};
-            for (int q = 0, k = start; q < 4; ++q)
-                for (unsigned m = mask[tid * PER + j][q]; m; m &= m - 1) c.toks[k++] = (unsigned short)(q * 32 + __ffs(m) - 1);
+            const unsigned word[4] = {m[j].x, m[j].y, m[j].z, m[j].w};
+            int k = start;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                for (unsigned left = word[q]; left; left &= left - 1) c.toks[k++] = (unsigned short)(q * 32 + __ffs(left) - 1);
             ++a;
             start += n[j];
         }
@@ -481,7 +504,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     if (warp == W_PRODUCER) {
         if (lane == 0) produce(c, t, &up, &down);
     } else if (warp == W_MMA) {
-        if (lane == 0) multiply<DT>(c, t, tmem);
+        multiply<DT>(c, t, tmem);
     } else {
         int seg = 0, turn = warp - W_LOAD;
         Turn at;
