@@ -33,7 +33,7 @@ void topk_plan(bool whole, const TopkArgs& a, int sms, TopkPlan* p) {
     p->L.chunks = a.K ? (int)((G + p->U * p->NT - 1) / (p->U * p->NT)) * p->NT : 0;
     const int most = (CL > 2 ? CL : 2) * a.K;  // candidates to sort, or slices' alternatives to join
     p->L.cap = a.K ? pow2_from(most > 256 ? most : 256) : 0;
-    p->smem = sizeof(unsigned long long) * p->L.cap + sizeof(unsigned) * p->L.chunks;
+    p->smem = (sizeof(unsigned long long) + sizeof(int)) * p->L.cap + sizeof(unsigned) * p->L.chunks;
 }
 
 }  // namespace

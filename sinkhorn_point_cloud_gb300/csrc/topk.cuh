@@ -82,15 +82,20 @@ struct Scores {
         }
 #pragma unroll
         for (int j = 0; j < P; ++j)
-            if (j < n) {
-                float2 f[Elem<DT>::N / 2];
-                unpack<DT>(v[j], f);
+            if (j < n) *this = with_masked<DT>(*this, v[j], sc);
+    }
+    // A granule that may hold -inf (out of line: eight copies of it in the loop cost more in fetched instructions than
+    // the calls do).
+    template <int DT>
+    static __device__ __noinline__ Scores with_masked(Scores r, uint4 v, float sc) {
+        float2 f[Elem<DT>::N / 2];
+        unpack<DT>(v, f);
 #pragma unroll
-                for (int i = 0; i < Elem<DT>::N / 2; ++i) {
-                    one(f[i].x, sc);
-                    one(f[i].y, sc);
-                }
-            }
+        for (int i = 0; i < Elem<DT>::N / 2; ++i) {
+            r.one(f[i].x, sc);
+            r.one(f[i].y, sc);
+        }
+        return r;
     }
 };
 
@@ -128,11 +133,13 @@ __device__ __forceinline__ unsigned long long pair_of(unsigned key, int col) {
 }
 
 // What the threads of a CTA share while they select.
+template <int NT>
 struct SelectSmem {
-    unsigned bound[2];   // smallest and largest chunk maximum
-    unsigned count[3];   // counters in turn
-    unsigned found;      // candidates
-    int got[33];         // ties of each warp
+    unsigned bound[2];  // the range of a threshold
+    unsigned count[3];  // counters in turn
+    unsigned found;     // candidates
+    unsigned hits;      // chunks to look at again
+    unsigned best[NT > 32 ? NT : 1];  // the threads' maxima
 };
 
 template <int NT>
@@ -143,7 +150,7 @@ __device__ __forceinline__ void cta_sync() {
 
 // How many of the CTA's threads' counts there are in all; step: a running number of such sums.
 template <int NT>
-__device__ __forceinline__ unsigned cta_count(SelectSmem& sh, unsigned mine, int& step) {
+__device__ __forceinline__ unsigned cta_count(SelectSmem<NT>& sh, unsigned mine, int& step) {
     const unsigned w = __reduce_add_sync(0xffffffffu, mine);
     if (NT == 32) return w;
     const int now = step % 3, next = (step + 1) % 3;
@@ -185,141 +192,234 @@ __device__ __forceinline__ uint4 inside(const uint4& v, int e, int V) {
     return pack<DT>(f);
 }
 
-// Calls use(key, column) for the elements of a granule that lie in the row.
+// Calls use(logit, column) for the elements of granule g of a slice (-inf outside the row).
 template <int DT, class Use>
-__device__ __forceinline__ void each_key(const uint4& v, int e, int V, Use use) {
-    float2 f[Elem<DT>::N / 2];
+__device__ __forceinline__ void each_logit(const Slice& s, int g, int V, Use use) {
+    constexpr int N = Elem<DT>::N;
+    uint4 v = s.src[g];
+    const int e = s.e0 + g * N;
+    if (g < s.lo || g >= s.hi) v = inside<DT>(v, e, V);
+    float2 f[N / 2];
     unpack<DT>(v, f);
 #pragma unroll
-    for (int i = 0; i < Elem<DT>::N; ++i) {
-        const float x = i & 1 ? f[i / 2].y : f[i / 2].x;
-        if (e + i >= 0 && e + i < V) use(Key<DT>::of(x), e + i);
+    for (int i = 0; i < N; ++i) use(i & 1 ? f[i / 2].y : f[i / 2].x, e + i);
+}
+
+// The K largest of the n numbers of v in order, zeros behind them where there are fewer.  Few of them are placed by counting
+// the larger ones, which needs no step to wait for another; many go through a sorting network.
+template <int NT>
+__device__ __forceinline__ void order(unsigned long long* v, int n, int K) {
+    constexpr int FEW = 256, PER = FEW / NT;
+    const int tid = threadIdx.x;
+    if (n <= FEW) {
+        unsigned long long mine[PER];
+        int rank[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            mine[j] = j * NT + tid < n ? v[j * NT + tid] : 0ull;
+            rank[j] = 0;
+        }
+        if (PER == 1 ? (tid & ~31) < n : true) {
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const unsigned long long x = v[i];
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (j * NT < n) rank[j] += x > mine[j];
+            }
+        }
+        cta_sync<NT>();
+        for (int i = tid; i < K; i += NT) v[i] = 0ull;
+        cta_sync<NT>();
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (mine[j] && rank[j] < K) v[rank[j]] = mine[j];  // (a 0 is a place that a slice could not fill)
+        cta_sync<NT>();
+        return;
     }
+    int n2 = 2;
+    while (n2 < n || n2 < K) n2 *= 2;
+    for (int i = n + tid; i < n2; i += NT) v[i] = 0ull;
+    cta_sync<NT>();
+    sort_pairs<NT>(v, n2);
+}
+
+// The largest threshold in [lo, hi] that K of the numbers of a warp reach (lo does), R of them a lane; one that not
+// more than `enough` reach will do.
+template <int R>
+__device__ __forceinline__ unsigned warp_threshold(const unsigned (&key)[R], unsigned lo, unsigned hi, unsigned K, unsigned enough) {
+    while (lo < hi) {
+        const unsigned mid = lo + (hi - lo + 1) / 2;
+        unsigned n = 0;
+#pragma unroll
+        for (int j = 0; j < R; ++j) n += key[j] >= mid;
+        n = R == 1 ? __popc(__ballot_sync(0xffffffffu, n)) : __reduce_add_sync(0xffffffffu, n);
+        if (n >= K) lo = mid;
+        else hi = mid - 1;
+        if (n >= K && n <= enough) break;
+    }
+    return lo;
 }
 
 // The slice's K best (fewer where it has fewer that are not -inf), sorted, in cand; the rest of cand's first
-// K places 0.  ckey: the chunks' maxima, chunk c = granules (c / NT * U + j) * NT + c % NT.
+// K places 0.  ckey: the chunks' maxima, chunk c = granules (c / NT * U + j) * NT + c % NT; best: the largest of this thread's.
 template <int DT, int NT, int U>
-__device__ __forceinline__ void select_best(SelectSmem& sh, const unsigned* ckey, int C, const Slice& s, int V, int K, int cap,
-                                            unsigned long long* cand) {
-    constexpr int N = Elem<DT>::N;
-    const int tid = threadIdx.x;
-    int step = 0;
-    unsigned lo = 0xffffffffu, hi = 0;
-    for (int c = tid; c < C; c += NT) {
-        lo = min(lo, ckey[c]);
-        hi = max(hi, ckey[c]);
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (NT > 32) {
-        if ((tid & 31) == 0) {
-            atomicMin(&sh.bound[0], lo);
-            atomicMax(&sh.bound[1], hi);
-        }
-        __syncthreads();
-        lo = sh.bound[0];
-        hi = sh.bound[1];
-    }
+__device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* ckey, unsigned best, int C, const Slice& s, int V, int K,
+                                            int cap, unsigned long long* cand, int* hit) {
+    const int tid = threadIdx.x, lane = tid & 31;
     const unsigned floor = Key<DT>::NOTHING + 1;
-    lo = C < K ? floor : max(lo, floor);
-    hi = max(hi, lo);
-    // The largest threshold that K chunks reach lies in [lo, hi]; any that not many more reach will do.
-    const auto reach = [&](unsigned at) {
-        unsigned n = 0;
-        for (int c = tid; c < C; c += NT) n += ckey[c] >= at;
-        return cta_count<NT>(sh, n, step);
-    };
-    const unsigned enough = K + K / 2 + 16;
-    bool narrow = C < K;  // whether [lo, hi] may still shrink
-    unsigned top = hi;
-    if (!narrow)
+    unsigned at, top;  // a threshold that K logits reach (or all there are); the largest key
+    int step = 0;
+    if (K <= NT / 2) {
+        // K threads have a logit that reaches the K-th largest of the threads' maxima.
+        constexpr int R = NT / 32;
+        unsigned key[R] = {best};
+        if (NT > 32) {
+            sh.best[tid] = best;
+            __syncthreads();
+            if (tid < 32) {
+#pragma unroll
+                for (int j = 0; j < R; ++j) key[j] = sh.best[j * 32 + lane];
+            }
+        }
+        if (tid < 32) {
+            unsigned lo = 0xffffffffu, hi = 0, n = 0;
+#pragma unroll
+            for (int j = 0; j < R; ++j) {
+                hi = max(hi, key[j]);
+                if (key[j] >= floor) {
+                    lo = min(lo, key[j]);
+                    ++n;
+                }
+            }
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            n = __reduce_add_sync(0xffffffffu, n);
+            at = n < (unsigned)K ? floor : warp_threshold<R>(key, lo, hi, K, K + K / 4 + 4);
+            top = max(hi, floor);
+            if (lane == 0) {
+                sh.bound[0] = at;
+                sh.bound[1] = top;
+                sh.found = sh.hits = 0;
+            }
+        }
+        cta_sync<NT>();
+        at = sh.bound[0];
+        top = sh.bound[1];
+    } else {
+        // The same with the chunks' maxima, which are more.
+        unsigned lo = 0xffffffffu, hi = 0;
+        for (int c = tid; c < C; c += NT) {
+            lo = min(lo, ckey[c]);
+            hi = max(hi, ckey[c]);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (NT > 32) {
+            if (lane == 0) {
+                atomicMin(&sh.bound[0], lo);
+                atomicMax(&sh.bound[1], hi);
+            }
+            __syncthreads();
+            lo = sh.bound[0];
+            hi = sh.bound[1];
+        }
+        const auto reach = [&](unsigned at) {
+            unsigned n = 0;
+            for (int c = tid; c < C; c += NT) n += ckey[c] >= at;
+            return cta_count<NT>(sh, n, step);
+        };
+        lo = max(lo, floor);
+        hi = max(hi, lo);
+        top = hi;
+        if (C < K || reach(lo) < (unsigned)K) lo = hi = floor;
         while (lo < hi) {
             const unsigned mid = lo + (hi - lo + 1) / 2, n = reach(mid);
             if (n >= (unsigned)K) lo = mid;
             else hi = mid - 1;
-            if (n >= (unsigned)K && n <= enough) break;
+            if (n >= (unsigned)K && n <= (unsigned)(K + K / 4)) break;
         }
-    // The elements that reach `at` (more than cap of them: only counted).
+        at = lo;
+        if (tid == 0) sh.found = sh.hits = 0;
+        cta_sync<NT>();
+    }
+    // The elements that reach `at` (more than cap of them: only counted).  Their chunks go into a list first, so that the
+    // granules to read again are shared out evenly: looked at by the thread that found its chunk, with few
+    // lanes of a warp at a time, 4096 rows of 131072 bf16 and K = 64 take 566 us, so 278.
     const auto gather = [&](unsigned at) {
+        if (best >= at)
+            for (int c = tid; c < C; c += NT)
+                if (ckey[c] >= at) {
+                    const unsigned i = atomicAdd(&sh.hits, 1u);
+                    if (i < (unsigned)cap) hit[i] = c;
+                }
         cta_sync<NT>();
-        if (tid == 0) sh.found = 0;
-        cta_sync<NT>();
-        for (int c = tid; c < C; c += NT)
-            if (ckey[c] >= at) {
-                uint4 v[U];
-                const int g0 = c / NT * U * NT + c % NT;
-#pragma unroll
-                for (int j = 0; j < U; ++j)
-                    if (g0 + j * NT < s.ng) v[j] = s.src[g0 + j * NT];
-#pragma unroll
-                for (int j = 0; j < U; ++j)
-                    if (g0 + j * NT < s.ng)
-                        each_key<DT>(v[j], s.e0 + (g0 + j * NT) * N, V, [&](unsigned key, int col) {
-                            if (key >= at) {
-                                const unsigned i = atomicAdd(&sh.found, 1u);
-                                if (i < (unsigned)cap) cand[i] = pair_of(key, col);
-                            }
-                        });
-            }
+        const unsigned hits = sh.hits;
+        if (hits > (unsigned)cap) return hits;  // each has one at least
+        const float least = Key<DT>::value(at);
+        for (unsigned i = tid; i < hits * U; i += NT) {
+            const int c = hit[i / U], g = c / NT * U * NT + c % NT + (int)(i % U) * NT;
+            if (g < s.ng)
+                each_logit<DT>(s, g, V, [&](float x, int col) {
+                    if (x >= least) {
+                        const unsigned k = atomicAdd(&sh.found, 1u);
+                        if (k < (unsigned)cap) cand[k] = pair_of(Key<DT>::of(x), col);
+                    }
+                });
+        }
         cta_sync<NT>();
         return sh.found;
     };
-    unsigned n = gather(lo);
+    unsigned n = gather(at);
     if (n > (unsigned)cap) {
         // Many equal logits, or many large ones in few chunks: the K-th largest logit itself by counting over the
         // whole slice, those above it, and as many of those equal to it as are missing, lowest columns first.
-        unsigned a = lo, b = top;
         const auto above = [&](unsigned at) {
+            const float least = Key<DT>::value(at);
             unsigned n = 0;
-            for (int g = tid; g < s.ng; g += NT)
-                each_key<DT>(s.src[g], s.e0 + g * N, V, [&](unsigned key, int) { n += key >= at; });
+            for (int g = tid; g < s.ng; g += NT) each_logit<DT>(s, g, V, [&](float x, int) { n += x >= least; });
             return cta_count<NT>(sh, n, step);
         };
-        while (a < b) {
-            const unsigned mid = a + (b - a + 1) / 2;
-            if (above(mid) >= (unsigned)K) a = mid;
-            else b = mid - 1;
+        while (at < top) {
+            const unsigned mid = at + (top - at + 1) / 2;
+            if (above(mid) >= (unsigned)K) at = mid;
+            else top = mid - 1;
         }
-        n = a == 0xffffffffu ? 0 : gather(a + 1);  // fewer than K
+        cta_sync<NT>();
+        if (tid == 0) sh.found = sh.hits = 0;
+        cta_sync<NT>();
+        n = gather(at + 1);  // fewer than K
+        const float tie = Key<DT>::value(at);
         for (int g0 = 0; g0 < s.ng && n < (unsigned)K; g0 += NT) {
             const int g = g0 + tid;
-            uint4 v = nothing<DT>();
             unsigned mine = 0;
-            if (g < s.ng) {
-                v = s.src[g];
-                each_key<DT>(v, s.e0 + g * N, V, [&](unsigned key, int) { mine += key == a; });
-            }
+            if (g < s.ng) each_logit<DT>(s, g, V, [&](float x, int) { mine += x == tie; });
             unsigned before = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const unsigned w = __shfl_up_sync(0xffffffffu, before, o);
-                if ((tid & 31) >= o) before += w;
+                if (lane >= o) before += w;
             }
-            unsigned all = __shfl_sync(0xffffffffu, before, 31), at = n + before - mine;
+            unsigned all = __shfl_sync(0xffffffffu, before, 31), place = n + before - mine;
             if (NT > 32) {
                 __syncthreads();
-                if ((tid & 31) == 31) sh.got[tid >> 5] = (int)before;
+                if (lane == 31) sh.best[tid >> 5] = before;
                 __syncthreads();
                 all = 0;
                 for (int w = 0; w < NT / 32; ++w) {
-                    if (w < tid >> 5) at += sh.got[w];
-                    all += sh.got[w];
+                    if (w < tid >> 5) place += sh.best[w];
+                    all += sh.best[w];
                 }
             }
             if (mine)
-                each_key<DT>(v, s.e0 + g * N, V, [&](unsigned key, int col) {
-                    if (key == a && at++ < (unsigned)K) cand[at - 1] = pair_of(key, col);
+                each_logit<DT>(s, g, V, [&](float x, int col) {
+                    if (x == tie && place++ < (unsigned)K) cand[place - 1] = pair_of(at, col);
                 });
             n = min(n + all, (unsigned)K);
         }
         cta_sync<NT>();
     }
-    int n2 = 2;
-    while (n2 < (int)n || n2 < K) n2 *= 2;
-    for (int i = n + tid; i < n2; i += NT) cand[i] = 0ull;
-    cta_sync<NT>();
-    sort_pairs<NT>(cand, n2);
+    order<NT>(cand, n, K);
 }
 
 // One row a CTA, or a cluster's CTAs a slice of it each.
@@ -328,11 +428,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : 1024 / NT) topk_kernel(con
     using T = typename Elem<DT>::T;
     constexpr int N = Elem<DT>::N, P = 8, NW = NT / 32;
     extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ SelectSmem sh;
+    __shared__ SelectSmem<NT> sh;
     __shared__ MSA rec[NW];
     __shared__ MSA mail[ROW_MAX_CL];
     unsigned long long* const cand = reinterpret_cast<unsigned long long*>(dyn);
-    unsigned* const ckey = reinterpret_cast<unsigned*>(cand + L.cap);
+    int* const hit = reinterpret_cast<int*>(cand + L.cap);
+    unsigned* const ckey = reinterpret_cast<unsigned*>(hit + L.cap);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const float sc = SOT_LOG2E / a.tau;
@@ -388,7 +489,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : 1024 / NT) topk_kernel(con
             const float w = max_of<DT>(top);
             mx = fmaxf(mx, w);
             if (a.K) {
-                if (j < n) ckey[c] = Key<DT>::of(w);
+                if (j < n) ckey[c] = Key<DT>::of(w);  // (a key of -inf where all are)
                 c += NT;
             }
         }
@@ -406,7 +507,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : 1024 / NT) topk_kernel(con
     w = msa_warp(w, sc);
     // A row without a sum has no alternatives; a slice without one may still stand beside others.
     if (a.K) {
-        if (w.s > 0.f) select_best<DT, NT, U>(sh, ckey, chunks, s, a.V, a.K, L.cap, cand);
+        if (w.s > 0.f) select_best<DT, NT, U>(sh, ckey, Key<DT>::of(run.m), chunks, s, a.V, a.K, L.cap, cand, hit);
         else
             for (int i = tid; i < a.K; i += NT) cand[i] = 0ull;
         cta_sync<NT>();
@@ -424,14 +525,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : 1024 / NT) topk_kernel(con
             w = lane < L.CL ? mail[lane] : MSA{-INFINITY, 0.f, 0.f};
             w = msa_warp(w, sc);
             if (a.K) {
-                int n2 = 2;
-                while (n2 < L.CL * a.K) n2 *= 2;
-                for (int i = a.K + tid; i < n2; i += NT) {
+                for (int i = a.K + tid; i < L.CL * a.K; i += NT) {
                     const uint32_t r = i / a.K;
-                    cand[i] = r < (uint32_t)L.CL ? cluster_load64(cluster_addr(smem_u32(cand + (i - r * a.K)), r)) : 0ull;
+                    cand[i] = cluster_load64(cluster_addr(smem_u32(cand + (i - r * a.K)), r));
                 }
                 __syncthreads();
-                sort_pairs<NT>(cand, n2);
+                order<NT>(cand, L.CL * a.K, a.K);
             }
         }
         cluster_sync();  // nobody leaves while rank 0 reads
