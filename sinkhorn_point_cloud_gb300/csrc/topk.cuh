@@ -30,15 +30,17 @@ struct Scores {
     float2 s, a;
     __device__ __forceinline__ Scores() : m(-INFINITY), s(make_float2(0.f, 0.f)), a(s) {}
 
-    __device__ __forceinline__ void move(float mx, float sc) {  // mx > m
-        const float d = (m - mx) * sc, k = ex2f(d);
-        if (s.x + s.y == s.x + s.y) {
-            // (k = 0: what was summed so far is out of range, and d may be infinite)
-            a = k == 0.f ? make_float2(0.f, 0.f) : fmul2(ffma2(s, make_float2(d, d), a), make_float2(k, k));
-            s = fmul2(s, make_float2(k, k));
-        }
-        m = mx;
-        if (mx == INFINITY) s = make_float2(NAN, 0.f);  // and stays
+    // m becomes the larger of itself and mx.  (Without a branch: lanes that take one go through the sums behind it apart
+    // from the others, which doubles the instructions of a batch.)
+    __device__ __forceinline__ void move(float mx, float sc) {
+        const float M = fmaxf(m, mx), d = M == m ? 0.f : (m - M) * sc, k = ex2f(d);
+        // (k = 0: what was summed so far is out of range, and d may be infinite)
+        const float2 moved = fmul2(ffma2(s, make_float2(d, d), a), make_float2(k, k));
+        a.x = k == 0.f ? 0.f : moved.x;
+        a.y = k == 0.f ? 0.f : moved.y;
+        s = fmul2(s, make_float2(k, k));
+        s.x = M == INFINITY ? NAN : s.x;  // and stays
+        m = M;
     }
     // Sums of a granule.  Elements of -inf make a NaN (0 times infinity) of a, which add() looks at.
     template <int DT>
@@ -65,7 +67,7 @@ struct Scores {
     // n granules (of at most P) whose largest element is mx.
     template <int DT, int P>
     __device__ __forceinline__ void add(const uint4 (&v)[P], int n, float mx, float sc) {
-        if (mx > m) move(mx, sc);
+        move(mx, sc);
         const float2 s0 = s, a0 = a;
         if (m > -INFINITY) {
             if (n == P) {
