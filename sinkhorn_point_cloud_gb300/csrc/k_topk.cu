@@ -18,7 +18,9 @@ void topk_plan(bool whole, const TopkArgs& a, int sms, TopkPlan* p) {
     const int N = a.dtype == SOT_F32 ? 4 : 8;
     const long long total = ((long long)a.V + (whole ? N - 1 : 2 * N - 2)) / N;  // granules of a row
     int CL = 1;
-    p->NT = total <= 512 ? 32 : 256;
+    if (total <= 512 && a.K <= 256) p->NT = 32;
+    else if (a.T < sms || total > 8192) p->NT = 256;
+    else p->NT = 128;
     // Few rows: cut a row further, up to eight granules a thread and a CTA for each SM, as far as the
     // slices' alternatives can be joined in one place.
     if (p->NT > 32 && a.T < sms)
@@ -33,7 +35,8 @@ void topk_plan(bool whole, const TopkArgs& a, int sms, TopkPlan* p) {
     p->L.chunks = a.K ? (int)((G + p->U * p->NT - 1) / (p->U * p->NT)) * p->NT : 0;
     const int most = (CL > 2 ? CL : 2) * a.K;  // candidates to sort, or slices' alternatives to join
     p->L.cap = a.K ? pow2_from(most > 256 ? most : 256) : 0;
-    p->smem = (sizeof(unsigned long long) + sizeof(int)) * p->L.cap + sizeof(unsigned) * p->L.chunks;
+    const long long bytes = (long long)(sizeof(unsigned long long) + sizeof(int)) * p->L.cap + sizeof(unsigned) * p->L.chunks;
+    p->L.bytes = (int)(bytes < TOPK_MAX_SMEM + 1 ? bytes : TOPK_MAX_SMEM + 1);
 }
 
 }  // namespace
@@ -46,7 +49,7 @@ bool topk_fits(int dtype, int V, int K) {
     a.K = K;
     TopkPlan p;
     topk_plan(false, a, 1, &p);
-    return p.smem <= TOPK_MAX_SMEM;
+    return p.L.bytes * (p.NT == 32 ? TEAMS<32> : 1) <= TOPK_MAX_SMEM;
 }
 
 cudaError_t launch_topk(const TopkArgs& a, int sms, cudaStream_t st) {
@@ -54,7 +57,7 @@ cudaError_t launch_topk(const TopkArgs& a, int sms, cudaStream_t st) {
     TopkPlan p;
     const bool whole = (unsigned long long)a.x % 16 == 0 && a.ld % (a.dtype == SOT_F32 ? 4 : 8) == 0;
     topk_plan(whole, a, sms, &p);
-    if (a.T * p.L.CL > 0x7fffffffll || p.smem > TOPK_MAX_SMEM) return cudaErrorInvalidValue;
+    if (a.T * p.L.CL > 0x7fffffffll) return cudaErrorInvalidValue;
     count_launches(1);
     switch (a.dtype) {
         case SOT_F32: return launch_topk_f32(a, p, st);

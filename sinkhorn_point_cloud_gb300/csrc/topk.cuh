@@ -20,6 +20,7 @@ struct TopkLaunch {
     int CL, G;     // CTAs a row, granules a slice
     int chunks;    // places for chunk maxima in shared memory
     int cap;       // places for candidates: a power of two, at least 2 K
+    int bytes;     // of shared memory for a team
 };
 
 // Running sums of a thread against the largest logit so far, m: s = sum 2^t and a = sum 2^t t with t = (x - m) sc. The
@@ -144,15 +145,23 @@ struct SelectSmem {
     unsigned best[NT > 32 ? NT : 1];  // the threads' maxima
 };
 
+// A team of NT threads takes a row (or a cluster's slice of one): a CTA, or for short rows one of eight warps of a CTA
+// (a CTA for each warp would leave an SM with seven of them at a time).
 template <int NT>
-__device__ __forceinline__ void cta_sync() {
+constexpr int TEAMS = NT == 32 ? 8 : 1;
+template <int NT>
+__device__ __forceinline__ int team_tid() {
+    return NT == 32 ? threadIdx.x & 31 : threadIdx.x;
+}
+template <int NT>
+__device__ __forceinline__ void team_sync() {
     if (NT == 32) __syncwarp();
     else __syncthreads();
 }
 
-// How many of the CTA's threads' counts there are in all; step: a running number of such sums.
+// How many of the team's threads' counts there are in all; step: a running number of such sums.
 template <int NT>
-__device__ __forceinline__ unsigned cta_count(SelectSmem<NT>& sh, unsigned mine, int& step) {
+__device__ __forceinline__ unsigned team_count(SelectSmem<NT>& sh, unsigned mine, int& step) {
     const unsigned w = __reduce_add_sync(0xffffffffu, mine);
     if (NT == 32) return w;
     const int now = step % 3, next = (step + 1) % 3;
@@ -169,7 +178,7 @@ template <int NT>
 __device__ __forceinline__ void sort_pairs(unsigned long long* v, int n2) {
     for (int k = 2; k <= n2; k *= 2)
         for (int j = k / 2; j > 0; j /= 2) {
-            for (int i = threadIdx.x; i < n2 / 2; i += NT) {
+            for (int i = team_tid<NT>(); i < n2 / 2; i += NT) {
                 const int p = 2 * i - (i & (j - 1)), q = p + j;
                 const unsigned long long x = v[p], y = v[q];
                 if ((x < y) == ((p & k) == 0)) {
@@ -177,7 +186,7 @@ __device__ __forceinline__ void sort_pairs(unsigned long long* v, int n2) {
                     v[q] = x;
                 }
             }
-            cta_sync<NT>();
+            team_sync<NT>();
         }
 }
 __device__ __forceinline__ unsigned long long cluster_load64(uint32_t ra) {
@@ -211,8 +220,8 @@ __device__ __forceinline__ void each_logit(const Slice& s, int g, int V, Use use
 // the larger ones, which needs no step to wait for another; many go through a sorting network.
 template <int NT>
 __device__ __forceinline__ void order(unsigned long long* v, int n, int K) {
-    constexpr int FEW = 256, PER = FEW / NT;
-    const int tid = threadIdx.x;
+    constexpr int FEW = NT > 128 ? 256 : 128, PER = FEW > NT ? FEW / NT : 1;
+    const int tid = team_tid<NT>();
     if (n <= FEW) {
         unsigned long long mine[PER];
         int rank[PER];
@@ -221,7 +230,7 @@ __device__ __forceinline__ void order(unsigned long long* v, int n, int K) {
             mine[j] = j * NT + tid < n ? v[j * NT + tid] : 0ull;
             rank[j] = 0;
         }
-        if (PER == 1 ? (tid & ~31) < n : true) {
+        if (PER > 1 || (tid & ~31) < n) {
 #pragma unroll 4
             for (int i = 0; i < n; ++i) {
                 const unsigned long long x = v[i];
@@ -230,19 +239,19 @@ __device__ __forceinline__ void order(unsigned long long* v, int n, int K) {
                     if (j * NT < n) rank[j] += x > mine[j];
             }
         }
-        cta_sync<NT>();
+        team_sync<NT>();
         for (int i = tid; i < K; i += NT) v[i] = 0ull;
-        cta_sync<NT>();
+        team_sync<NT>();
 #pragma unroll
         for (int j = 0; j < PER; ++j)
             if (mine[j] && rank[j] < K) v[rank[j]] = mine[j];  // (a 0 is a place that a slice could not fill)
-        cta_sync<NT>();
+        team_sync<NT>();
         return;
     }
     int n2 = 2;
     while (n2 < n || n2 < K) n2 *= 2;
     for (int i = n + tid; i < n2; i += NT) v[i] = 0ull;
-    cta_sync<NT>();
+    team_sync<NT>();
     sort_pairs<NT>(v, n2);
 }
 
@@ -268,7 +277,7 @@ __device__ __forceinline__ unsigned warp_threshold(const unsigned (&key)[R], uns
 template <int DT, int NT, int U>
 __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* ckey, unsigned best, int C, const Slice& s, int V, int K,
                                             int cap, unsigned long long* cand, int* hit) {
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = team_tid<NT>(), lane = tid & 31;
     const unsigned floor = Key<DT>::NOTHING + 1;
     unsigned at, top;  // a threshold that K logits reach (or all there are); the largest key
     int step = 0;
@@ -305,7 +314,7 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
                 sh.found = sh.hits = 0;
             }
         }
-        cta_sync<NT>();
+        team_sync<NT>();
         at = sh.bound[0];
         top = sh.bound[1];
     } else {
@@ -329,7 +338,7 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
         const auto reach = [&](unsigned at) {
             unsigned n = 0;
             for (int c = tid; c < C; c += NT) n += ckey[c] >= at;
-            return cta_count<NT>(sh, n, step);
+            return team_count<NT>(sh, n, step);
         };
         lo = max(lo, floor);
         hi = max(hi, lo);
@@ -343,7 +352,7 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
         }
         at = lo;
         if (tid == 0) sh.found = sh.hits = 0;
-        cta_sync<NT>();
+        team_sync<NT>();
     }
     // The elements that reach `at` (more than cap of them: only counted).  Their chunks go into a list first, so that the
     // granules to read again are shared out evenly: looked at by the thread that found its chunk, with few
@@ -355,7 +364,7 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
                     const unsigned i = atomicAdd(&sh.hits, 1u);
                     if (i < (unsigned)cap) hit[i] = c;
                 }
-        cta_sync<NT>();
+        team_sync<NT>();
         const unsigned hits = sh.hits;
         if (hits > (unsigned)cap) return hits;  // each has one at least
         const float least = Key<DT>::value(at);
@@ -369,7 +378,7 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
                     }
                 });
         }
-        cta_sync<NT>();
+        team_sync<NT>();
         return sh.found;
     };
     unsigned n = gather(at);
@@ -380,16 +389,16 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
             const float least = Key<DT>::value(at);
             unsigned n = 0;
             for (int g = tid; g < s.ng; g += NT) each_logit<DT>(s, g, V, [&](float x, int) { n += x >= least; });
-            return cta_count<NT>(sh, n, step);
+            return team_count<NT>(sh, n, step);
         };
         while (at < top) {
             const unsigned mid = at + (top - at + 1) / 2;
             if (above(mid) >= (unsigned)K) at = mid;
             else top = mid - 1;
         }
-        cta_sync<NT>();
+        team_sync<NT>();
         if (tid == 0) sh.found = sh.hits = 0;
-        cta_sync<NT>();
+        team_sync<NT>();
         n = gather(at + 1);  // fewer than K
         const float tie = Key<DT>::value(at);
         for (int g0 = 0; g0 < s.ng && n < (unsigned)K; g0 += NT) {
@@ -419,27 +428,29 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
                 });
             n = min(n + all, (unsigned)K);
         }
-        cta_sync<NT>();
+        team_sync<NT>();
     }
     order<NT>(cand, n, K);
 }
 
-// One row a CTA, or a cluster's CTAs a slice of it each.
+// A row a team, or a cluster's CTAs a slice of it each.
 template <int DT, int NT, int U>
-__global__ void __launch_bounds__(NT, NT == 32 ? 20 : 1024 / NT) topk_kernel(const TopkArgs a, const TopkLaunch L) {
+__global__ void __launch_bounds__(NT * TEAMS<NT>, NT == 32 ? 3 : 1024 / NT) topk_kernel(const TopkArgs a, const TopkLaunch L) {
     using T = typename Elem<DT>::T;
     constexpr int N = Elem<DT>::N, P = 8, NW = NT / 32;
     extern __shared__ __align__(16) unsigned char dyn[];
-    __shared__ SelectSmem<NT> sh;
+    __shared__ SelectSmem<NT> select[TEAMS<NT>];
     __shared__ MSA rec[NW];
     __shared__ MSA mail[ROW_MAX_CL];
-    unsigned long long* const cand = reinterpret_cast<unsigned long long*>(dyn);
+    const int tid = team_tid<NT>(), lane = tid & 31, warp = tid >> 5, team = threadIdx.x / NT;
+    SelectSmem<NT>& sh = select[team];
+    unsigned long long* const cand = reinterpret_cast<unsigned long long*>(dyn + (NT == 32 ? team * L.bytes : 0));
     int* const hit = reinterpret_cast<int*>(cand + L.cap);
     unsigned* const ckey = reinterpret_cast<unsigned*>(hit + L.cap);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = NT == 32 ? 0 : cluster_rank();
     const float sc = SOT_LOG2E / a.tau;
-    const long long row = blockIdx.x / L.CL;
+    const long long row = NT == 32 ? (long long)blockIdx.x * TEAMS<NT> + team : blockIdx.x / L.CL;
+    if (NT == 32 && row >= a.T) return;
     const int tgt = a.target ? load_index(a.target, a.target_type, row, a.V) : -1;
     if (a.target && tgt < 0) {  // left out: the same for the whole cluster
         if (rank) return;
@@ -454,7 +465,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : 1024 / NT) topk_kernel(con
         }
         return;
     }
-    if (L.CL > 1) cluster_arrive_started();
+    if (NT > 32 && L.CL > 1) cluster_arrive_started();
     const T* const x = static_cast<const T*>(a.x) + row * a.ld;
     const Slice s = slice_at<DT>(x, a.V, L.G, rank);
     const float xt = tgt >= 0 && rank == 0 && tid == 0 ? Elem<DT>::get(x[tgt]) : 0.f;
@@ -498,23 +509,25 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 20 : 1024 / NT) topk_kernel(con
         run.template add<DT>(v, n, mx, sc);
     }
     MSA w = msa_warp(MSA{run.m, run.s.x + run.s.y, run.a.x + run.a.y}, sc);
-    if (lane == 0) rec[warp] = w;
+    if (NT > 32 && lane == 0) rec[warp] = w;
     const int chunks = min((s.ng + U * NT - 1) / (U * NT) * NT, L.chunks);
     if (a.K)  // places that no chunk has taken
         for (int i = tid; i < chunks; i += NT)
             if (i / NT * U * NT + tid >= s.ng) ckey[i] = 0;
-    cta_sync<NT>();
-    w = rec[lane < NW ? lane : 0];
-    if (lane >= NW) w = MSA{-INFINITY, 0.f, 0.f};
-    w = msa_warp(w, sc);
+    team_sync<NT>();
+    if (NT > 32) {
+        w = rec[lane < NW ? lane : 0];
+        if (lane >= NW) w = MSA{-INFINITY, 0.f, 0.f};
+        w = msa_warp(w, sc);
+    }
     // A row without a sum has no alternatives; a slice without one may still stand beside others.
     if (a.K) {
         if (w.s > 0.f) select_best<DT, NT, U>(sh, ckey, Key<DT>::of(run.m), chunks, s, a.V, a.K, L.cap, cand, hit);
         else
             for (int i = tid; i < a.K; i += NT) cand[i] = 0ull;
-        cta_sync<NT>();
+        team_sync<NT>();
     }
-    if (L.CL > 1) {
+    if (NT > 32 && L.CL > 1) {
         cluster_wait_started();
         if (tid == 0) {
             const uint32_t to = cluster_addr(smem_u32(&mail[rank]), 0);
@@ -685,16 +698,17 @@ __global__ void __launch_bounds__(TOPK_GRAD_NT) topk_grad_kernel(const TopkGradA
 constexpr int TOPK_MAX_SMEM = 200 * 1024;
 
 template <int DT, int NT, int U>
-cudaError_t launch_topk_n(const TopkArgs& a, const TopkLaunch& L, size_t smem, cudaStream_t st) {
+cudaError_t launch_topk_n(const TopkArgs& a, const TopkLaunch& L, cudaStream_t st) {
     auto kern = topk_kernel<DT, NT, U>;
+    const size_t smem = (size_t)L.bytes * TEAMS<NT>;
     if (smem > 40 * 1024) {
         // (the kernel's leave, not the call's: another host thread's call cannot lower it before the launch)
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TOPK_MAX_SMEM);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.T * L.CL), 1, 1);
-    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.gridDim = dim3((unsigned)((a.T + TEAMS<NT> - 1) / TEAMS<NT> * L.CL), 1, 1);
+    cfg.blockDim = dim3(NT * TEAMS<NT>, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -711,13 +725,15 @@ cudaError_t launch_topk_n(const TopkArgs& a, const TopkLaunch& L, size_t smem, c
 struct TopkPlan {
     int NT, U;
     TopkLaunch L;
-    size_t smem;
 };
 
+template <int DT, int NT>
+cudaError_t launch_topk_u(const TopkArgs& a, const TopkPlan& p, cudaStream_t st) {
+    return p.U == 1 ? launch_topk_n<DT, NT, 1>(a, p.L, st) : launch_topk_n<DT, NT, 8>(a, p.L, st);
+}
 template <int DT>
 cudaError_t launch_topk_t(const TopkArgs& a, const TopkPlan& p, cudaStream_t st) {
-    if (p.NT == 32) return p.U == 1 ? launch_topk_n<DT, 32, 1>(a, p.L, p.smem, st) : launch_topk_n<DT, 32, 8>(a, p.L, p.smem, st);
-    return p.U == 1 ? launch_topk_n<DT, 256, 1>(a, p.L, p.smem, st) : launch_topk_n<DT, 256, 8>(a, p.L, p.smem, st);
+    return p.NT == 32 ? launch_topk_u<DT, 32>(a, p, st) : p.NT == 128 ? launch_topk_u<DT, 128>(a, p, st) : launch_topk_u<DT, 256>(a, p, st);
 }
 
 template <int DT>
