@@ -20,34 +20,29 @@ namespace sot {
 
 namespace {
 
-// Eight elements as floats, from an address aligned to 16 bytes.
+// Eight elements, one or two granules, as floats.
 template <int DT>
-__device__ __forceinline__ void load8(const typename Elem<DT>::T* p, float (&f)[8]) {
-    float2 h[4];
+__device__ __forceinline__ void floats_of(const uint4 (&v)[DT == SOT_F32 ? 2 : 1], float2 (&f)[4]) {
     if constexpr (DT == SOT_F32) {
-        const uint4* q = reinterpret_cast<const uint4*>(p);
-        const uint4 a = __ldg(q), b = __ldg(q + 1);
-        h[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
-        h[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
-        h[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
-        h[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+        float2 h[2];
+        unpack<DT>(v[0], h);
+        f[0] = h[0];
+        f[1] = h[1];
+        unpack<DT>(v[1], h);
+        f[2] = h[0];
+        f[3] = h[1];
     } else
-        unpack<DT>(__ldg(reinterpret_cast<const uint4*>(p)), h);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = h[i].x;
-        f[2 * i + 1] = h[i].y;
-    }
+        unpack<DT>(v[0], f);
 }
 template <int DT>
-__device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float (&f)[8]) {
+__device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float2 (&f)[4], uint64_t policy) {
+    uint4* const q = reinterpret_cast<uint4*>(p);
     if constexpr (DT == SOT_F32) {
-        __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
-        __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
-    } else {
-        const float2 h[4] = {{f[0], f[1]}, {f[2], f[3]}, {f[4], f[5]}, {f[6], f[7]}};
-        __stcs(reinterpret_cast<uint4*>(p), pack<DT>(h));
-    }
+        const float2 h[2] = {f[0], f[1]}, g[2] = {f[2], f[3]};
+        store16(q, pack<DT>(h), policy);
+        store16(q + 1, pack<DT>(g), policy);
+    } else
+        store16(q, pack<DT>(f), policy);
 }
 
 // ---- lookup ----
@@ -60,41 +55,55 @@ __global__ void __launch_bounds__(EMB_NT) embed_kernel(const EmbedArgs a, unsign
     using O = typename Elem<DO>::T;
     constexpr int W = VEC ? 8 : 1;
     const long long total = a.T * per_row, tile = (long long)EMB_NT * EMB_U;
+    const uint64_t keep = policy_keep(), drop = policy_drop();
     for (long long base = blockIdx.x * tile; base < total; base += gridDim.x * tile) {
-        float f[EMB_U][W];
-        O* to[EMB_U];
+        // (one division in 64 bits for a tile, the others in 32)
+        const long long row0 = base / per_row;
+        const unsigned first = (unsigned)(base - row0 * per_row), left = (unsigned)min(tile, total - base);
+        uint4 raw[EMB_U][VEC && DT == SOT_F32 ? 2 : 1];
+        T one[EMB_U];
+        long long to[EMB_U];
+        bool named[EMB_U];
 #pragma unroll
         for (int j = 0; j < EMB_U; ++j) {
-            const long long i = base + j * EMB_NT + threadIdx.x;
-            to[j] = nullptr;
-            if (i < total) {
-                const long long t = i / per_row;
-                const int c = (int)(i - t * per_row) * W;
+            const unsigned i = j * EMB_NT + threadIdx.x, at = first + i, r = at / per_row;
+            const int c = (int)(at - r * per_row) * W;
+            named[j] = false;
+            to[j] = -1;
+            if (i < left) {
+                const long long t = row0 + r;
                 const int id = load_index(a.ids, a.ids_type, t, a.V);
-                to[j] = static_cast<O*>(a.out) + t * a.ldo + c;
+                to[j] = t * a.ldo + c;
                 if (id >= 0) {
                     const T* from = static_cast<const T*>(a.table) + id * a.ld + c;
-                    if constexpr (VEC) load8<DT>(from, f[j]);
-                    else f[j][0] = Elem<DT>::get(*from);
-#pragma unroll
-                    for (int w = 0; w < W; ++w) f[j][w] *= a.scale;
-                } else {
-#pragma unroll
-                    for (int w = 0; w < W; ++w) f[j][w] = 0.f;
+                    named[j] = true;
+                    if constexpr (VEC) {
+                        // (rows of frequent tokens stay in L2, what is written does not)
+                        raw[j][0] = load16(reinterpret_cast<const uint4*>(from), keep);
+                        if constexpr (DT == SOT_F32) raw[j][1] = load16(reinterpret_cast<const uint4*>(from) + 1, keep);
+                    } else
+                        one[j] = *from;
                 }
             }
         }
 #pragma unroll
         for (int j = 0; j < EMB_U; ++j)
-            if (to[j]) {
-                if constexpr (VEC) store8<DO>(to[j], f[j]);
-                else *to[j] = Elem<DO>::put(f[j][0]);
+            if (to[j] >= 0) {
+                O* const out = static_cast<O*>(a.out) + to[j];
+                if constexpr (VEC) {
+                    float2 f[4];
+                    floats_of<DT>(raw[j], f);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) f[w] = named[j] ? make_float2(f[w].x * a.scale, f[w].y * a.scale) : make_float2(0.f, 0.f);
+                    store8<DO>(out, f, drop);
+                } else
+                    *out = Elem<DO>::put(named[j] ? Elem<DT>::get(one[j]) * a.scale : 0.f);
             }
     }
 }
 
 // ---- gradient: sort ----
-constexpr int SORT_NT = 1024, SORT_NW = SORT_NT / 32, SORT_CL = 8, SORT_MAX_BITS = 9, SORT_MAX_BINS = 1 << SORT_MAX_BITS;
+constexpr int SORT_NT = 1024, SORT_NW = SORT_NT / 32, SORT_CL = 8, SORT_MAX_BITS = 9, SORT_MAX_BINS = 1 << SORT_MAX_BITS, SORT_U = 8;
 
 struct SortSmem {
     unsigned at[SORT_NW][SORT_MAX_BINS];  // per warp: counts, then places
@@ -122,14 +131,28 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
         const unsigned *key_in = odd ? a.key[0] : a.key[1], *pos_in = odd ? a.pos[0] : a.pos[1];
         unsigned *key_out = odd ? a.key[1] : a.key[0], *pos_out = odd ? a.pos[1] : a.pos[0];
         const int shift = p * bits;
-        const auto key_of = [&](long long t) { return p == 0 ? token_key(a, t) : __ldcg(key_in + t); };
+        // (keys come SORT_U steps at a time: a load a step would leave the warp waiting for each)
+        const auto load_keys = [&](long long t, unsigned (&key)[SORT_U]) {
+#pragma unroll
+            for (int u = 0; u < SORT_U; ++u) {
+                const long long i = t + u * 32;
+                key[u] = i < end ? (p == 0 ? token_key(a, i) : __ldcg(key_in + i)) : 0u;
+            }
+        };
         for (int b = lane; b < bins; b += 32) sm.at[warp][b] = 0;
         __syncwarp();
-        for (long long t = begin + lane; t < begin + per && t - lane < end; t += 32) {
-            const unsigned d = t < end ? key_of(t) >> shift & (bins - 1) : 0xffffffffu;
-            const unsigned peers = __match_any_sync(0xffffffffu, d);
-            if (t < end && lane == __ffs(peers) - 1) sm.at[warp][d] += __popc(peers);
-            __syncwarp();
+        for (long long t0 = begin; t0 < end; t0 += 32 * SORT_U) {
+            unsigned key[SORT_U];
+            load_keys(t0 + lane, key);
+#pragma unroll
+            for (int u = 0; u < SORT_U; ++u) {
+                if (t0 + u * 32 >= end) break;
+                const bool in = t0 + u * 32 + lane < end;
+                const unsigned d = in ? key[u] >> shift & (bins - 1) : 0xffffffffu;
+                const unsigned peers = __match_any_sync(0xffffffffu, d);
+                if (in && lane == __ffs(peers) - 1) sm.at[warp][d] += __popc(peers);
+                __syncwarp();
+            }
         }
         __syncthreads();
         unsigned mine = 0;  // this CTA's count of bin tid
@@ -166,17 +189,29 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
         if (tid < bins)
             for (int w = 0; w < SORT_NW; ++w) sm.at[w][tid] += base;
         __syncthreads();
-        for (long long t = begin + lane; t < begin + per && t - lane < end; t += 32) {
-            const unsigned key = t < end ? key_of(t) : 0u, d = t < end ? key >> shift & (bins - 1) : 0xffffffffu;
-            const unsigned peers = __match_any_sync(0xffffffffu, d);
-            if (t < end) {
-                const unsigned to = sm.at[warp][d] + __popc(peers & ((1u << lane) - 1u));
-                key_out[to] = key;
-                pos_out[to] = p == 0 ? (unsigned)t : __ldcg(pos_in + t);
+        for (long long t0 = begin; t0 < end; t0 += 32 * SORT_U) {
+            unsigned key[SORT_U], pos[SORT_U];
+            load_keys(t0 + lane, key);
+#pragma unroll
+            for (int u = 0; u < SORT_U; ++u) {
+                const long long i = t0 + u * 32 + lane;
+                pos[u] = p == 0 || i >= end ? (unsigned)i : __ldcg(pos_in + i);
             }
-            __syncwarp();
-            if (t < end && lane == __ffs(peers) - 1) sm.at[warp][d] += __popc(peers);
-            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < SORT_U; ++u) {
+                if (t0 + u * 32 >= end) break;
+                const bool in = t0 + u * 32 + lane < end;
+                const unsigned d = in ? key[u] >> shift & (bins - 1) : 0xffffffffu;
+                const unsigned peers = __match_any_sync(0xffffffffu, d);
+                if (in) {
+                    const unsigned to = sm.at[warp][d] + __popc(peers & ((1u << lane) - 1u));
+                    key_out[to] = key[u];
+                    pos_out[to] = pos[u];
+                }
+                __syncwarp();
+                if (in && lane == __ffs(peers) - 1) sm.at[warp][d] += __popc(peers);
+                __syncwarp();
+            }
         }
         cluster_sync();  // the other CTAs' part of the order is written, and nobody reads this CTA's totals any more
     }
@@ -184,171 +219,233 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
 
 // Zeros of the rows in [v0, v1) that no token names.
 template <int DG>
-__device__ void zero_rows(const EmbedGradArgs& a, int v0, int v1, unsigned* named, bool vec) {
+__device__ void zero_rows(const EmbedGradArgs& a, int v0, int v1, unsigned* named) {
     using G = typename Elem<DG>::T;
+    constexpr int N = Elem<DG>::N, U = 8;
     const int tid = threadIdx.x, n = v1 - v0;
+    const uint64_t policy = policy_drop();
     for (int i = tid; i < (n + 31) / 32; i += SORT_NT) named[i] = 0;
     __syncthreads();
-    for (long long t = tid; t < a.T; t += SORT_NT) {
-        const unsigned r = token_key(a, t) - (unsigned)v0;
-        if (r < (unsigned)n) atomicOr(&named[r / 32], 1u << (r % 32));
+    for (long long t0 = tid; t0 < a.T; t0 += U * SORT_NT) {
+        unsigned r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = t0 + u * SORT_NT < a.T ? token_key(a, t0 + u * SORT_NT) - (unsigned)v0 : (unsigned)n;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (r[u] < (unsigned)n) atomicOr(&named[r[u] / 32], 1u << (r[u] % 32));
     }
     __syncthreads();
-    const int per = vec ? (a.D * (int)sizeof(G)) / 16 : a.D;
-    const int width = min(SORT_NT, (per + 31) / 32 * 32), rows = SORT_NT / width;  // threads a row, rows at a time
-    const int r = tid / width;
+    // threads a row, rows at a time
+    const int granules = (a.D + N - 1) / N, width = min(SORT_NT, (granules + 31) / 32 * 32), rows = SORT_NT / width;
+    const int r = tid / width, c = tid % width;
     if (r >= rows) return;
     for (int v = r; v < n; v += rows) {
         if (named[v / 32] >> (v % 32) & 1u) continue;
         G* const to = static_cast<G*>(a.grad) + (long long)(v0 + v) * a.ldg;
-        if (vec)
-            for (int c = tid % width; c < per; c += width) __stcs(reinterpret_cast<uint4*>(to) + c, make_uint4(0, 0, 0, 0));
-        else
-            for (int c = tid % width; c < per; c += width) to[c] = Elem<DG>::put(0.f);
+        // whole granules, and the elements before and after them one by one
+        const int head = min(a.D, (int)((16 - ((unsigned long long)to & 15)) & 15) / (int)sizeof(G)), whole = (a.D - head) / N;
+        uint4* const mid = reinterpret_cast<uint4*>(to + head);
+        for (int i = c; i < whole; i += width) store16(mid + i, make_uint4(0, 0, 0, 0), policy);
+        const int tail = a.D - head - whole * N;
+        if (c < head) to[c] = Elem<DG>::put(0.f);
+        if (c < tail) to[head + whole * N + c] = Elem<DG>::put(0.f);
     }
 }
 
 constexpr int ZERO_ROWS = 8192;  // of a CTA at a time, at most (a bit each)
 
 template <int DG>
-__global__ void __launch_bounds__(SORT_NT) embed_sort_kernel(const EmbedGradArgs a, int passes, int bits, bool vec) {
+__global__ void __launch_bounds__(SORT_NT) embed_sort_kernel(const EmbedGradArgs a, int passes, int bits) {
     extern __shared__ __align__(16) unsigned char dyn[];
     if (blockIdx.x < SORT_CL) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.spans = 0;
         if (a.T > 0) sort_tokens(a, passes, bits, *reinterpret_cast<SortSmem*>(dyn));
         return;
     }
     const int parts = gridDim.x - SORT_CL, part = blockIdx.x - SORT_CL;
     const int share = (int)min((long long)ZERO_ROWS, ((long long)a.V + parts - 1) / parts);
     for (long long v0 = (long long)part * share; v0 < a.V; v0 += (long long)parts * share) {
-        zero_rows<DG>(a, (int)v0, (int)min((long long)a.V, v0 + share), reinterpret_cast<unsigned*>(dyn), vec);
+        zero_rows<DG>(a, (int)v0, (int)min((long long)a.V, v0 + share), reinterpret_cast<unsigned*>(dyn));
         __syncthreads();
     }
 }
 
 // ---- gradient: sums ----
-constexpr int SUM_NT = 128, SUM_R = 32, SUM_U = 8, SUM_COLS = SUM_NT * 8;
+constexpr int SUM_NT = 128, SUM_R = 32, SUM_COLS = SUM_NT * 8;
 
-// The columns of a thread: eight in a row where rows are whole granules (VEC), else SUM_NT apart.
-template <bool VEC>
-__device__ __forceinline__ int sum_col(int c0, int j) {
-    return VEC ? c0 + threadIdx.x * 8 + j : c0 + j * SUM_NT + threadIdx.x;
+// The columns of a thread, of NT that share a tile: eight in a row where rows are whole granules (VEC), else NT apart.
+template <bool VEC, int NT>
+__device__ __forceinline__ int sum_col(int c0, int i, int j) {
+    return VEC ? c0 + i * 8 + j : c0 + j * NT + i;
 }
-template <int DG, bool VEC>
-__device__ __forceinline__ void write_row(const EmbedGradArgs& a, unsigned v, int c0, const float (&acc)[8]) {
+template <int DG, bool VEC, int NT>
+__device__ __forceinline__ void write_row(const EmbedGradArgs& a, unsigned v, int c0, int i, const float (&acc)[8]) {
     using G = typename Elem<DG>::T;
     G* const to = static_cast<G*>(a.grad) + (long long)v * a.ldg;
-    float f[8];
     if constexpr (VEC) {
-        const int c = sum_col<VEC>(c0, 0);
+        const int c = sum_col<VEC, NT>(c0, i, 0);
         if (c >= a.D) return;
-        float old[8] = {};
-        if (a.accumulate) load8<DG>(to + c, old);
+        uint4 was[DG == SOT_F32 ? 2 : 1] = {};
+        float2 old[4] = {}, f[4];
+        if (a.accumulate) {
+            was[0] = *reinterpret_cast<const uint4*>(to + c);
+            if constexpr (DG == SOT_F32) was[1] = *(reinterpret_cast<const uint4*>(to + c) + 1);
+            floats_of<DG>(was, old);
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = a.accumulate ? fmaf(a.scale, acc[j], old[j]) : a.scale * acc[j];
-        store8<DG>(to + c, f);
+        for (int j = 0; j < 4; ++j)
+            f[j] = a.accumulate ? make_float2(fmaf(a.scale, acc[2 * j], old[j].x), fmaf(a.scale, acc[2 * j + 1], old[j].y))
+                                : make_float2(a.scale * acc[2 * j], a.scale * acc[2 * j + 1]);
+        store8<DG>(to + c, f, policy_drop());
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int c = sum_col<VEC>(c0, j);
+            const int c = sum_col<VEC, NT>(c0, i, j);
             if (c < a.D)
                 to[c] = Elem<DG>::put(a.accumulate ? fmaf(a.scale, acc[j], Elem<DG>::get(to[c])) : a.scale * acc[j]);
         }
     }
 }
 // Partial sums: slot 0 of a chunk is what it has of the row that began before it, slot 1 of the row that goes on after it.
-template <bool VEC>
 __device__ __forceinline__ float* part_row(const EmbedGradArgs& a, long long chunk, int slot) {
     return a.part + (chunk * 2 + slot) * a.D;
 }
 
 template <int DT, int DG, bool VEC>
-__global__ void __launch_bounds__(SUM_NT) embed_sum_kernel(const EmbedGradArgs a, int tiles) {
+__global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArgs a, int tiles) {
     using T = typename Elem<DT>::T;
+    constexpr int RAW = DT == SOT_F32 ? 2 : 1;
+    constexpr int SUM_U = VEC && RAW == 1 ? 8 : 4;  // rows whose loads are under way together: as many as registers hold
     __shared__ unsigned key[SUM_R + 2], pos[SUM_R];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long chunk = blockIdx.x / tiles;
     const int c0 = (int)(blockIdx.x % tiles) * SUM_COLS, tid = threadIdx.x;
     const long long at = chunk * SUM_R;
-    const int n = (int)min((long long)SUM_R, a.T - at);
+    unsigned mine = (unsigned)a.V;
     if (tid < SUM_R + 2) {  // with the token before and the one after; V: none
         const long long i = at + tid - 1;
-        key[tid] = i >= 0 && i < a.T ? a.key[0][i] : (unsigned)a.V;
-        if (tid < n) pos[tid] = a.pos[0][at + tid];
+        if (i >= 0 && i < a.T) mine = a.key[0][i];
+        key[tid] = mine;
+        if (tid < SUM_R) pos[tid] = at + tid < a.T ? a.pos[0][at + tid] : 0u;
     }
-    __syncthreads();
+    // tokens of the chunk that have a row: they come first
+    const int n = __syncthreads_count(tid >= 1 && tid <= SUM_R && mine < (unsigned)a.V);
     float acc[8] = {};
-    const auto flush = [&](int i, bool first, bool ends) {  // the row of token i
-        const unsigned v = key[i + 1];
-        const bool before = first && key[0] == v, after = ends && key[n + 1] == v;
-        if (before || after) {
-            float* const to = part_row<VEC>(a, chunk, before ? 0 : 1);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = sum_col<VEC>(c0, j);
-                if (c < a.D) to[c] = acc[j];
-            }
-        } else
-            write_row<DG, VEC>(a, v, c0, acc);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-    };
     bool first = true;
     for (int i0 = 0; i0 < n; i0 += SUM_U) {
-        float f[SUM_U][8];
+        uint4 raw[SUM_U][RAW];
+        T one[VEC ? 1 : SUM_U][8];
 #pragma unroll
-        for (int u = 0; u < SUM_U; ++u) {
-            const int i = i0 + u;
-            if (i >= n || key[i + 1] >= (unsigned)a.V) continue;
-            const T* const from = static_cast<const T*>(a.g) + (long long)pos[i] * a.ld;
-            if constexpr (VEC) {
-                const int c = sum_col<VEC>(c0, 0);
-                if (c < a.D) load8<DT>(from + c, f[u]);
-            } else {
+        for (int u = 0; u < SUM_U; ++u)
+            if (i0 + u < n) {
+                const T* const from = static_cast<const T*>(a.g) + (long long)pos[i0 + u] * a.ld;
+                if constexpr (VEC) {
+                    const int c = sum_col<VEC, SUM_NT>(c0, tid, 0);
+                    if (c < a.D) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = sum_col<VEC>(c0, j);
-                    f[u][j] = c < a.D ? Elem<DT>::get(from[c]) : 0.f;
+                        for (int w = 0; w < RAW; ++w) raw[u][w] = __ldcs(reinterpret_cast<const uint4*>(from + c) + w);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int c = sum_col<VEC, SUM_NT>(c0, tid, j);
+                        one[u][j] = c < a.D ? from[c] : Elem<DT>::put(0.f);
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int u = 0; u < SUM_U; ++u) {
-            const int i = i0 + u;
-            if (i >= n || key[i + 1] >= (unsigned)a.V) continue;
+        for (int u = 0; u < SUM_U; ++u)
+            if (i0 + u < n) {
+                const int i = i0 + u;
+                if constexpr (VEC) {
+                    float2 f[4];
+                    floats_of<DT>(raw[u], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += f[u][j];
-            if (i == n - 1 || key[i + 2] != key[i + 1]) {
-                flush(i, first, i == n - 1);
-                first = false;
+                    for (int j = 0; j < 4; ++j) {
+                        acc[2 * j] += f[j].x;
+                        acc[2 * j + 1] += f[j].y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[j] += Elem<DT>::get(one[u][j]);
+                }
+                const unsigned v = key[i + 1];
+                if (i == n - 1 || key[i + 2] != v) {  // the last token of the row in this chunk
+                    const bool before = first && key[0] == v, after = key[i + 2] == v;
+                    if (before || after) {
+                        float* const to = part_row(a, chunk, before ? 0 : 1);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int c = sum_col<VEC, SUM_NT>(c0, tid, j);
+                            if (c < a.D) __stcg(to + c, acc[j]);
+                        }
+                        if (!before && tid == 0 && c0 == 0) a.span[atomicAdd(a.spans, 1u)] = (unsigned)chunk;
+                    } else
+                        write_row<DG, VEC, SUM_NT>(a, v, c0, tid, acc);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+                    first = false;
+                }
             }
-        }
     }
 }
 
-// Rows that span chunks: the chunk where one begins adds up what the others have of it.
+// Rows that span chunks, from the list of the chunks where one begins (in no order: each is summed by itself).  A CTA takes
+// JOIN_COLS columns of a row; its warps add up a share of the chunks each, in order, and the shares are added in order.
+constexpr int JOIN_NT = 256, JOIN_NW = JOIN_NT / 32, JOIN_COLS = 256;
+
 template <int DG, bool VEC>
-__global__ void __launch_bounds__(SUM_NT) embed_join_kernel(const EmbedGradArgs a, int tiles) {
+__global__ void __launch_bounds__(JOIN_NT) embed_join_kernel(const EmbedGradArgs a, int tiles) {
+    __shared__ float sums[JOIN_NW][JOIN_COLS];
+    __shared__ int length;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long chunk = blockIdx.x / tiles;
-    const int c0 = (int)(blockIdx.x % tiles) * SUM_COLS;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned* const key = a.key[0];
-    const long long end = (chunk + 1) * SUM_R;
-    if (end >= a.T) return;
-    const unsigned v = key[end - 1];
-    if (v >= (unsigned)a.V || key[end] != v) return;                    // nothing goes on after the chunk
-    if (chunk > 0 && key[end - SUM_R] == v && key[end - SUM_R - 1] == v) return;  // it began before
-    float acc[8];
-    const auto add = [&](const float* from, bool set) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = sum_col<VEC>(c0, j);
-            const float x = c < a.D ? from[c] : 0.f;
-            acc[j] = set ? x : acc[j] + x;
+    const long long work = (long long)__ldcg(a.spans) * tiles, chunks = (a.T + SUM_R - 1) / SUM_R;
+    for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+        const long long chunk = __ldcg(a.span + w / tiles);
+        const int c0 = (int)(w % tiles) * JOIN_COLS;
+        const unsigned v = key[(chunk + 1) * SUM_R - 1];
+        // chunks after the first that start with the row
+        if (tid == 0) length = 0x7fffffff;
+        __syncthreads();
+        for (long long c = chunk + 1 + tid;; c += JOIN_NT) {
+            const bool off = c >= chunks || key[c * SUM_R] != v;
+            if (off) atomicMin(&length, (int)(c - chunk - 1));
+            if (__syncthreads_or(off)) break;
         }
-    };
-    add(part_row<VEC>(a, chunk, 1), true);
-    for (long long c = chunk + 1; c * SUM_R < a.T && key[c * SUM_R] == v; ++c) add(part_row<VEC>(a, c, 0), false);
-    write_row<DG, VEC>(a, v, c0, acc);
+        const int n = length, per = (n + JOIN_NW - 1) / JOIN_NW, from = warp * per, to = min(n, from + per);
+        float acc[8] = {};
+        const auto fetch = [&](long long c, int slot, float (&f)[8]) {
+            const float* const p = part_row(a, c, slot);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int col = sum_col<false, 32>(c0, lane, j);
+                f[j] = col < a.D ? __ldcg(p + col) : 0.f;
+            }
+        };
+        if (warp == 0) fetch(chunk, 1, acc);
+#pragma unroll 4
+        for (int i = from; i < to; ++i) {
+            float f[8];
+            fetch(chunk + 1 + i, 0, f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += f[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[warp][j * 32 + lane] = acc[j];
+        __syncthreads();
+        if (tid < JOIN_COLS / 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = sum_col<VEC, 32>(0, tid, j);
+                acc[j] = sums[0][at];
+                for (int k = 1; k < JOIN_NW; ++k) acc[j] += sums[k][at];
+            }
+            write_row<DG, VEC, 32>(a, v, c0, tid, acc);
+        }
+        __syncthreads();
+    }
 }
 
 bool whole_rows(const void* p, long long ld, int D, int type) {
@@ -381,7 +478,7 @@ cudaError_t launch_after(const void* kern, unsigned blocks, int threads, void** 
 }
 
 template <int DG>
-cudaError_t launch_sort(const EmbedGradArgs& a, const EmbedGradPlan& p, bool vec, int sms, cudaStream_t st) {
+cudaError_t launch_sort(const EmbedGradArgs& a, const EmbedGradPlan& p, int sms, cudaStream_t st) {
     auto kern = embed_sort_kernel<DG>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SortSmem));
     if (e != cudaSuccess) return e;
@@ -404,22 +501,26 @@ cudaError_t launch_sort(const EmbedGradArgs& a, const EmbedGradPlan& p, bool vec
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, kern, a, p.passes, p.bits, vec);
+    return cudaLaunchKernelEx(&cfg, kern, a, p.passes, p.bits);
 }
 
 template <int DT, int DG>
-cudaError_t launch_sum(const EmbedGradArgs& a, const EmbedGradPlan& p, bool vec, cudaStream_t st) {
+cudaError_t launch_sum(const EmbedGradArgs& a, const EmbedGradPlan& p, bool vec, int sms, cudaStream_t st) {
     int tiles = (a.D + SUM_COLS - 1) / SUM_COLS;
     if (p.chunks * tiles > 0x7fffffffll) return cudaErrorInvalidValue;
     const unsigned blocks = (unsigned)(p.chunks * tiles);
     EmbedGradArgs b = a;
     void* args[] = {&b, &tiles};
+    int join_tiles = (a.D + JOIN_COLS - 1) / JOIN_COLS;
+    void* join_args[] = {&b, &join_tiles};
+    const long long most = p.chunks * join_tiles;  // rows that span chunks are fewer than chunks
+    const unsigned join_blocks = (unsigned)(most < 4ll * sms ? most : 4ll * sms);
     count_launches(2);
     const cudaError_t e = launch_after(vec ? (const void*)embed_sum_kernel<DT, DG, true> : (const void*)embed_sum_kernel<DT, DG, false>,
                                        blocks, SUM_NT, args, st);
     if (e != cudaSuccess) return e;
-    return launch_after(vec ? (const void*)embed_join_kernel<DG, true> : (const void*)embed_join_kernel<DG, false>, blocks,
-                        SUM_NT, args, st);
+    return launch_after(vec ? (const void*)embed_join_kernel<DG, true> : (const void*)embed_join_kernel<DG, false>, join_blocks,
+                        JOIN_NT, join_args, st);
 }
 
 }  // namespace
@@ -457,6 +558,8 @@ EmbedGradPlan embed_grad_plan(long long T, int V, int D) {
         p.key_at[i] = place(sizeof(unsigned) * T);
         p.pos_at[i] = place(sizeof(unsigned) * T);
     }
+    p.spans_at = place(sizeof(unsigned));
+    p.span_at = place(sizeof(unsigned) * p.chunks);
     p.part_at = place(sizeof(float) * 2 * (size_t)p.chunks * D);
     return p;
 }
@@ -467,18 +570,20 @@ cudaError_t launch_embed_grad(EmbedGradArgs a, const EmbedGradPlan& p, unsigned 
         a.key[i] = reinterpret_cast<unsigned*>(scratch + p.key_at[i]);
         a.pos[i] = reinterpret_cast<unsigned*>(scratch + p.pos_at[i]);
     }
+    a.spans = reinterpret_cast<unsigned*>(scratch + p.spans_at);
+    a.span = reinterpret_cast<unsigned*>(scratch + p.span_at);
     a.part = reinterpret_cast<float*>(scratch + p.part_at);
     const bool vec_out = whole_rows(a.grad, a.ldg, a.D, a.grad_type);
-    const cudaError_t e = a.grad_type == SOT_F32   ? launch_sort<SOT_F32>(a, p, vec_out, sms, st)
-                          : a.grad_type == SOT_F16 ? launch_sort<SOT_F16>(a, p, vec_out, sms, st)
-                                                   : launch_sort<SOT_BF16>(a, p, vec_out, sms, st);
+    const cudaError_t e = a.grad_type == SOT_F32   ? launch_sort<SOT_F32>(a, p, sms, st)
+                          : a.grad_type == SOT_F16 ? launch_sort<SOT_F16>(a, p, sms, st)
+                                                   : launch_sort<SOT_BF16>(a, p, sms, st);
     if (e != cudaSuccess || a.T == 0) return e;
     const bool vec = vec_out && whole_rows(a.g, a.ld, a.D, a.type);
 #define SOT_OUT(DT)                                                            \
     switch (a.grad_type) {                                                     \
-        case SOT_F32: return launch_sum<DT, SOT_F32>(a, p, vec, st);           \
-        case SOT_F16: return launch_sum<DT, SOT_F16>(a, p, vec, st);           \
-        default: return launch_sum<DT, SOT_BF16>(a, p, vec, st);               \
+        case SOT_F32: return launch_sum<DT, SOT_F32>(a, p, vec, sms, st);      \
+        case SOT_F16: return launch_sum<DT, SOT_F16>(a, p, vec, sms, st);      \
+        default: return launch_sum<DT, SOT_BF16>(a, p, vec, sms, st);          \
     }
     switch (a.type) {
         case SOT_F32: SOT_OUT(SOT_F32)
