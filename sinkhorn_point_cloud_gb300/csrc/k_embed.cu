@@ -4,11 +4,13 @@
 //
 // Gradient: grad[v] = scale sum of g[t] over the tokens t with id[t] = v, in the order of t.
 //   sort     one cluster sorts the tokens by row, stably (radix passes over shared-memory
-//            counts, joined through distributed shared memory), while the other CTAs of the launch
-//            write the zeros of the rows that no token names;
+//            counts, joined through distributed shared memory), and marks the rows that tokens name; the other CTAs of
+//            the launch fill the time with zeros for the table's first rows;
 //   sum      a CTA takes a chunk of sorted tokens and a tile of columns, and writes
-//            the rows that lie inside its chunk.  A row that spans chunks leaves a partial sum in each;
-//   join     adds these up, in the order of the chunks.
+//            the rows that lie inside its chunk.  A row that spans chunks leaves a partial sum in each.  Other CTAs,
+//            in between, write the zeros of the remaining rows that no token names (reads and writes at the same
+//            time: writes alone reach 0.8 of the copy bandwidth);
+//   join     adds up the partial sums, in a fixed order.
 // No atomics on floats: repeated calls give the same bits.
 #include <cuda_runtime.h>
 
@@ -106,10 +108,23 @@ __global__ void __launch_bounds__(EMB_NT) embed_kernel(const EmbedArgs a, unsign
 constexpr int SORT_NT = 1024, SORT_NW = SORT_NT / 32, SORT_CL = 8, SORT_MAX_BITS = 9, SORT_MAX_BINS = 1 << SORT_MAX_BITS, SORT_U = 8;
 
 struct SortSmem {
-    unsigned at[SORT_NW][SORT_MAX_BINS];  // per warp: counts, then places
+    unsigned at[SORT_NW][SORT_MAX_BINS];  // per warp: counts, then places within the CTA's
     unsigned total[SORT_MAX_BINS];        // of this CTA
+    unsigned base[SORT_MAX_BINS];         // place of the first token of a bin in this CTA
     unsigned sums[SORT_NW];
 };
+
+// The lanes of a warp with the same digit, from a vote for each of its bits.  `in`: lanes that have one.
+__device__ __forceinline__ unsigned same_digit(unsigned digit, int bits, bool in) {
+    unsigned peers = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+    for (int b = 0; b < SORT_MAX_BITS; ++b)
+        if (b < bits) {
+            const unsigned set = __ballot_sync(0xffffffffu, digit >> b & 1u);
+            peers &= digit >> b & 1u ? set : ~set;
+        }
+    return peers;
+}
 
 // Row of token t; tokens without one come last.
 __device__ __forceinline__ unsigned token_key(const EmbedGradArgs& a, long long t) {
@@ -139,34 +154,52 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
                 key[u] = i < end ? (p == 0 ? token_key(a, i) : __ldcg(key_in + i)) : 0u;
             }
         };
+        if (p == 0 && a.named)
+            for (int i = (int)rank * SORT_NT + tid; i < (a.V + 31) / 32; i += SORT_CL * SORT_NT) a.named[i] = 0u;
         for (int b = lane; b < bins; b += 32) sm.at[warp][b] = 0;
         __syncwarp();
-        for (long long t0 = begin; t0 < end; t0 += 32 * SORT_U) {
-            unsigned key[SORT_U];
+        // Counts, and each token's rank among those of its digit in the warp.
+        unsigned key[SORT_U], pos[SORT_U], rank_of[SORT_U];
+        const auto count = [&](long long t0) {
             load_keys(t0 + lane, key);
 #pragma unroll
             for (int u = 0; u < SORT_U; ++u) {
-                if (t0 + u * 32 >= end) break;
-                const bool in = t0 + u * 32 + lane < end;
-                const unsigned d = in ? key[u] >> shift & (bins - 1) : 0xffffffffu;
-                const unsigned peers = __match_any_sync(0xffffffffu, d);
-                if (in && lane == __ffs(peers) - 1) sm.at[warp][d] += __popc(peers);
-                __syncwarp();
+                const long long i = t0 + u * 32 + lane;
+                pos[u] = p == 0 || i >= end ? (unsigned)i : __ldcg(pos_in + i);
             }
-        }
+#pragma unroll
+            for (int u = 0; u < SORT_U; ++u)
+                if (t0 + u * 32 < end) {
+                    const bool in = t0 + u * 32 + lane < end;
+                    const unsigned d = key[u] >> shift & (bins - 1), peers = same_digit(d, bits, in);
+                    const unsigned before = in ? sm.at[warp][d] : 0u;
+                    rank_of[u] = before + __popc(peers & ((1u << lane) - 1u));
+                    __syncwarp();
+                    if (in && lane == __ffs(peers) - 1) sm.at[warp][d] = before + __popc(peers);
+                    __syncwarp();
+                }
+        };
+        for (long long t0 = begin; t0 < end; t0 += 32 * SORT_U) count(t0);
         __syncthreads();
         unsigned mine = 0;  // this CTA's count of bin tid
         if (tid < bins) {
-            for (int w = 0; w < SORT_NW; ++w) {
-                const unsigned c = sm.at[w][tid];
-                sm.at[w][tid] = mine;
-                mine += c;
+#pragma unroll
+            for (int w0 = 0; w0 < SORT_NW; w0 += 8) {
+                unsigned c[8];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) c[w] = sm.at[w0 + w][tid];
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    sm.at[w0 + w][tid] = mine;
+                    mine += c[w];
+                }
             }
             sm.total[tid] = mine;
         }
         cluster_sync();
         unsigned all = 0, before = 0;
         if (tid < bins)
+#pragma unroll
             for (uint32_t r = 0; r < SORT_CL; ++r) {
                 unsigned c;
                 asm volatile("ld.shared::cluster.u32 %0, [%1];"
@@ -186,88 +219,60 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
         __syncthreads();
         unsigned base = scan - all + before;
         for (int w = 0; w < warp; ++w) base += sm.sums[w];
-        if (tid < bins)
-            for (int w = 0; w < SORT_NW; ++w) sm.at[w][tid] += base;
+        if (tid < bins) sm.base[tid] = base;
         __syncthreads();
+        // Places.  A share of one batch (65536 tokens in all) has its ranks still in registers; a longer one is counted
+        // again from the start, on top of the other warps' counts.
+        const bool once = end - begin <= 32 * SORT_U;
         for (long long t0 = begin; t0 < end; t0 += 32 * SORT_U) {
-            unsigned key[SORT_U], pos[SORT_U];
-            load_keys(t0 + lane, key);
+            if (!once) count(t0);
 #pragma unroll
-            for (int u = 0; u < SORT_U; ++u) {
-                const long long i = t0 + u * 32 + lane;
-                pos[u] = p == 0 || i >= end ? (unsigned)i : __ldcg(pos_in + i);
-            }
-#pragma unroll
-            for (int u = 0; u < SORT_U; ++u) {
-                if (t0 + u * 32 >= end) break;
-                const bool in = t0 + u * 32 + lane < end;
-                const unsigned d = in ? key[u] >> shift & (bins - 1) : 0xffffffffu;
-                const unsigned peers = __match_any_sync(0xffffffffu, d);
-                if (in) {
-                    const unsigned to = sm.at[warp][d] + __popc(peers & ((1u << lane) - 1u));
+            for (int u = 0; u < SORT_U; ++u)
+                if (t0 + u * 32 + lane < end) {
+                    const unsigned d = key[u] >> shift & (bins - 1);
+                    const unsigned to = sm.base[d] + rank_of[u] + (once ? sm.at[warp][d] : 0u);
                     key_out[to] = key[u];
                     pos_out[to] = pos[u];
+                    if (p == passes - 1 && a.named && key[u] < (unsigned)a.V) atomicOr(a.named + key[u] / 32, 1u << key[u] % 32);
                 }
-                __syncwarp();
-                if (in && lane == __ffs(peers) - 1) sm.at[warp][d] += __popc(peers);
-                __syncwarp();
-            }
         }
         cluster_sync();  // the other CTAs' part of the order is written, and nobody reads this CTA's totals any more
     }
 }
 
-// Zeros of the rows in [v0, v1) that no token names.
-template <int DG>
-__device__ void zero_rows(const EmbedGradArgs& a, int v0, int v1, unsigned* named) {
+// Zeros of the rows in [v0, v1), those in `named` (a bit each; NULL: none) excepted, by NT threads.
+template <int DG, int NT>
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, long long v0, long long v1, const unsigned* named) {
     using G = typename Elem<DG>::T;
-    constexpr int N = Elem<DG>::N, U = 8;
-    const int tid = threadIdx.x, n = v1 - v0;
+    constexpr int N = Elem<DG>::N;
     const uint64_t policy = policy_drop();
-    for (int i = tid; i < (n + 31) / 32; i += SORT_NT) named[i] = 0;
-    __syncthreads();
-    for (long long t0 = tid; t0 < a.T; t0 += U * SORT_NT) {
-        unsigned r[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = t0 + u * SORT_NT < a.T ? token_key(a, t0 + u * SORT_NT) - (unsigned)v0 : (unsigned)n;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (r[u] < (unsigned)n) atomicOr(&named[r[u] / 32], 1u << (r[u] % 32));
-    }
-    __syncthreads();
     // threads a row, rows at a time
-    const int granules = (a.D + N - 1) / N, width = min(SORT_NT, (granules + 31) / 32 * 32), rows = SORT_NT / width;
-    const int r = tid / width, c = tid % width;
-    if (r >= rows) return;
-    for (int v = r; v < n; v += rows) {
-        if (named[v / 32] >> (v % 32) & 1u) continue;
-        G* const to = static_cast<G*>(a.grad) + (long long)(v0 + v) * a.ldg;
+    int width = NT;
+    while (width > 1 && width / 2 * N >= a.D) width /= 2;
+    const int c = threadIdx.x % width;
+    for (long long v = v0 + threadIdx.x / width; v < v1; v += NT / width) {
+        if (named && named[v / 32] >> (v % 32) & 1u) continue;
+        G* const to = static_cast<G*>(a.grad) + v * a.ldg;
         // whole granules, and the elements before and after them one by one
         const int head = min(a.D, (int)((16 - ((unsigned long long)to & 15)) & 15) / (int)sizeof(G)), whole = (a.D - head) / N;
+        const int tail = a.D - head - whole * N;
         uint4* const mid = reinterpret_cast<uint4*>(to + head);
         for (int i = c; i < whole; i += width) store16(mid + i, make_uint4(0, 0, 0, 0), policy);
-        const int tail = a.D - head - whole * N;
-        if (c < head) to[c] = Elem<DG>::put(0.f);
-        if (c < tail) to[head + whole * N + c] = Elem<DG>::put(0.f);
+        for (int i = c; i < head; i += width) to[i] = Elem<DG>::put(0.f);
+        for (int i = c; i < tail; i += width) to[head + whole * N + i] = Elem<DG>::put(0.f);
     }
 }
 
-constexpr int ZERO_ROWS = 8192;  // of a CTA at a time, at most (a bit each)
-
 template <int DG>
-__global__ void __launch_bounds__(SORT_NT) embed_sort_kernel(const EmbedGradArgs a, int passes, int bits) {
+__global__ void __launch_bounds__(SORT_NT) embed_sort_kernel(const EmbedGradArgs a, int passes, int bits, long long rows) {
     extern __shared__ __align__(16) unsigned char dyn[];
     if (blockIdx.x < SORT_CL) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.spans = 0;
-        if (a.T > 0) sort_tokens(a, passes, bits, *reinterpret_cast<SortSmem*>(dyn));
+        sort_tokens(a, passes, bits, *reinterpret_cast<SortSmem*>(dyn));
         return;
     }
-    const int parts = gridDim.x - SORT_CL, part = blockIdx.x - SORT_CL;
-    const int share = (int)min((long long)ZERO_ROWS, ((long long)a.V + parts - 1) / parts);
-    for (long long v0 = (long long)part * share; v0 < a.V; v0 += (long long)parts * share) {
-        zero_rows<DG>(a, (int)v0, (int)min((long long)a.V, v0 + share), reinterpret_cast<unsigned*>(dyn));
-        __syncthreads();
-    }
+    const long long parts = gridDim.x - SORT_CL, part = blockIdx.x - SORT_CL;
+    zero_rows<DG, SORT_NT>(a, rows * part / parts, rows * (part + 1) / parts, nullptr);
 }
 
 // ---- gradient: sums ----
@@ -312,14 +317,22 @@ __device__ __forceinline__ float* part_row(const EmbedGradArgs& a, long long chu
 }
 
 template <int DT, int DG, bool VEC>
-__global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArgs a, int tiles) {
+__global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArgs a, int tiles, long long zeros, long long zero_from,
+                                                              int zero_share) {
     using T = typename Elem<DT>::T;
     constexpr int RAW = DT == SOT_F32 ? 2 : 1;
     constexpr int SUM_U = VEC && RAW == 1 ? 8 : 4;  // rows whose loads are under way together: as many as registers hold
     __shared__ unsigned key[SUM_R + 2], pos[SUM_R];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long chunk = blockIdx.x / tiles;
-    const int c0 = (int)(blockIdx.x % tiles) * SUM_COLS, tid = threadIdx.x;
+    // `zeros` CTAs, spread evenly over the grid, write zeros
+    const long long zero = blockIdx.x * zeros / gridDim.x, block = blockIdx.x - zero;
+    if ((blockIdx.x + 1) * zeros / gridDim.x > zero) {
+        const long long v = zero_from + zero * zero_share;
+        zero_rows<DG, SUM_NT>(a, v, min((long long)a.V, v + zero_share), a.named);
+        return;
+    }
+    const long long chunk = block / tiles;
+    const int c0 = (int)(block % tiles) * SUM_COLS, tid = threadIdx.x;
     const long long at = chunk * SUM_R;
     unsigned mine = (unsigned)a.V;
     if (tid < SUM_R + 2) {  // with the token before and the one after; V: none
@@ -379,7 +392,7 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
                             const int c = sum_col<VEC, SUM_NT>(c0, tid, j);
                             if (c < a.D) __stcg(to + c, acc[j]);
                         }
-                        if (!before && tid == 0 && c0 == 0) a.span[atomicAdd(a.spans, 1u)] = (unsigned)chunk;
+                        if (!before && tid == 0 && c0 == 0) a.span[atomicAdd(a.spans, 1u)] = make_uint2((unsigned)chunk, v);
                     } else
                         write_row<DG, VEC, SUM_NT>(a, v, c0, tid, acc);
 #pragma unroll
@@ -390,59 +403,94 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
     }
 }
 
-// Rows that span chunks, from the list of the chunks where one begins (in no order: each is summed by itself).  A CTA takes
-// JOIN_COLS columns of a row; its warps add up a share of the chunks each, in order, and the shares are added in order.
-constexpr int JOIN_NT = 256, JOIN_NW = JOIN_NT / 32, JOIN_COLS = 256;
+// Rows that span chunks, from the list of the chunks where one begins (in no order: each is summed by itself).  A warp takes
+// JOIN_COLS columns of a row and adds up what its first JOIN_OWN other chunks have; most rows span no more.  For those that
+// do, the CTA's warps take every eighth of the remaining chunks each, and their sums are added in order.  Eight chunks' sums are
+// fetched before it is known that they belong to the row, so that one wait finds both out.
+constexpr int JOIN_NT = 256, JOIN_NW = JOIN_NT / 32, JOIN_COLS = 128, JOIN_U = 8, JOIN_OWN = 8;
+
+// Adds what chunks c, c + step, ... (n of them at most) have of row v to acc; returns whether the row goes on.
+__device__ __forceinline__ bool add_chunks(const EmbedGradArgs& a, float (&acc)[4], long long c, int step, int n, long long chunks,
+                                           unsigned v, int c0, int lane) {
+    bool on = true;
+    for (int i = 0; on && i < n; i += JOIN_U, c += JOIN_U * step) {
+        float f[JOIN_U][4];
+        bool mine[JOIN_U];
+#pragma unroll
+        for (int u = 0; u < JOIN_U; ++u) {
+            const long long at = c + u * step;
+            mine[u] = at < chunks && __ldcg(a.key[0] + at * SUM_R) == v;
+            if (at < chunks) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int col = c0 + j * 32 + lane;
+                    f[u][j] = col < a.D ? __ldcg(part_row(a, at, 0) + col) : 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < JOIN_U; ++u) {
+            on = on && mine[u];
+            if (on) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] += f[u][j];
+            }
+        }
+    }
+    return on;
+}
 
 template <int DG, bool VEC>
 __global__ void __launch_bounds__(JOIN_NT) embed_join_kernel(const EmbedGradArgs a, int tiles) {
-    __shared__ float sums[JOIN_NW][JOIN_COLS];
-    __shared__ int length;
+    __shared__ float sums[JOIN_NW][JOIN_COLS], rest[JOIN_NW][JOIN_COLS];
+    __shared__ bool more[JOIN_NW];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned* const key = a.key[0];
-    const long long work = (long long)__ldcg(a.spans) * tiles, chunks = (a.T + SUM_R - 1) / SUM_R;
-    for (long long w = blockIdx.x; w < work; w += gridDim.x) {
-        const long long chunk = __ldcg(a.span + w / tiles);
-        const int c0 = (int)(w % tiles) * JOIN_COLS;
-        const unsigned v = key[(chunk + 1) * SUM_R - 1];
-        // chunks after the first that start with the row
-        if (tid == 0) length = 0x7fffffff;
-        __syncthreads();
-        for (long long c = chunk + 1 + tid;; c += JOIN_NT) {
-            const bool off = c >= chunks || key[c * SUM_R] != v;
-            if (off) atomicMin(&length, (int)(c - chunk - 1));
-            if (__syncthreads_or(off)) break;
-        }
-        const int n = length, per = (n + JOIN_NW - 1) / JOIN_NW, from = warp * per, to = min(n, from + per);
-        float acc[8] = {};
-        const auto fetch = [&](long long c, int slot, float (&f)[8]) {
-            const float* const p = part_row(a, c, slot);
+    const long long spans = __ldcg(a.spans), work = spans * tiles, chunks = (a.T + SUM_R - 1) / SUM_R;
+    // (columns go through shared memory from the order they are summed in to the order they are written in)
+    const auto write = [&](const float* from, unsigned v, int c0) {
+        float f[8];
+        if (lane >= 16) return;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int col = sum_col<false, 32>(c0, lane, j);
-                f[j] = col < a.D ? __ldcg(p + col) : 0.f;
+        for (int j = 0; j < 8; ++j) f[j] = from[sum_col<VEC, 16>(0, lane, j)];
+        write_row<DG, VEC, 16>(a, v, c0, lane, f);
+    };
+    for (long long w0 = (long long)blockIdx.x * JOIN_NW; w0 < work; w0 += (long long)gridDim.x * JOIN_NW) {
+        const long long w = w0 + warp;
+        if (lane == 0) more[warp] = false;
+        if (w < work) {
+            const uint2 span = __ldcg(a.span + w % spans);
+            const int c0 = (int)(w / spans) * JOIN_COLS;
+            float acc[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int col = c0 + j * 32 + lane;
+                acc[j] = col < a.D ? __ldcg(part_row(a, span.x, 1) + col) : 0.f;
             }
-        };
-        if (warp == 0) fetch(chunk, 1, acc);
-#pragma unroll 4
-        for (int i = from; i < to; ++i) {
-            float f[8];
-            fetch(chunk + 1 + i, 0, f);
+            const bool on = add_chunks(a, acc, span.x + 1, 1, JOIN_OWN, chunks, span.y, c0, lane);
+            if (lane == 0) more[warp] = on;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[j] += f[j];
+            for (int j = 0; j < 4; ++j) sums[warp][j * 32 + lane] = acc[j];
+            __syncwarp();
+            if (!on) write(sums[warp], span.y, c0);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sums[warp][j * 32 + lane] = acc[j];
         __syncthreads();
-        if (tid < JOIN_COLS / 8) {
+        for (int k = 0; k < JOIN_NW; ++k) {
+            if (!more[k]) continue;
+            const uint2 span = __ldcg(a.span + (w0 + k) % spans);
+            const int c0 = (int)((w0 + k) / spans) * JOIN_COLS;
+            float acc[4] = {}, own = tid < JOIN_COLS ? sums[k][tid] : 0.f;
+            add_chunks(a, acc, span.x + 1 + JOIN_OWN + warp, JOIN_NW, 0x7fffffff, chunks, span.y, c0, lane);
+            __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int at = sum_col<VEC, 32>(0, tid, j);
-                acc[j] = sums[0][at];
-                for (int k = 1; k < JOIN_NW; ++k) acc[j] += sums[k][at];
+            for (int j = 0; j < 4; ++j) rest[warp][j * 32 + lane] = acc[j];
+            __syncthreads();
+            if (tid < JOIN_COLS) {
+                for (int i = 0; i < JOIN_NW; ++i) own += rest[i][tid];
+                sums[k][tid] = own;
             }
-            write_row<DG, VEC, 32>(a, v, c0, tid, acc);
+            __syncthreads();
+            if (warp == 0) write(sums[k], span.y, c0);
         }
         __syncthreads();
     }
@@ -477,6 +525,14 @@ cudaError_t launch_after(const void* kern, unsigned blocks, int threads, void** 
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
+// Rows that get their zeros beside the sort: as many as that leaves time for.
+constexpr long long EARLY_BYTES = 40 << 20, EARLY_BYTES_A_TOKEN = 1200;
+long long early_rows(const EmbedGradArgs& a) {
+    if (a.accumulate) return 0;
+    const long long rows = (EARLY_BYTES + EARLY_BYTES_A_TOKEN * a.T) / ((long long)a.D * (a.grad_type == SOT_F32 ? 4 : 2));
+    return rows < a.V ? rows : a.V;
+}
+
 template <int DG>
 cudaError_t launch_sort(const EmbedGradArgs& a, const EmbedGradPlan& p, int sms, cudaStream_t st) {
     auto kern = embed_sort_kernel<DG>;
@@ -484,12 +540,10 @@ cudaError_t launch_sort(const EmbedGradArgs& a, const EmbedGradPlan& p, int sms,
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    long long zero = 0;
-    if (!a.accumulate) {
-        zero = ((long long)a.V * a.D + (1 << 16) - 1) >> 16;  // 64 Ki elements a CTA, up to two CTAs an SM
-        zero = zero < 2ll * sms ? zero : 2ll * sms;
-        zero = (zero + SORT_CL - 1) / SORT_CL * SORT_CL;
-    }
+    const long long rows = early_rows(a);
+    long long zero = (rows * a.D + (1 << 16) - 1) >> 16;  // 64 Ki elements a CTA
+    zero = zero < sms ? zero : sms;
+    zero = (zero + SORT_CL - 1) / SORT_CL * SORT_CL;
     cfg.gridDim = dim3((unsigned)(SORT_CL + zero), 1, 1);
     cfg.blockDim = dim3(SORT_NT, 1, 1);
     cfg.dynamicSmemBytes = sizeof(SortSmem);
@@ -501,26 +555,33 @@ cudaError_t launch_sort(const EmbedGradArgs& a, const EmbedGradPlan& p, int sms,
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, kern, a, p.passes, p.bits);
+    return cudaLaunchKernelEx(&cfg, kern, a, p.passes, p.bits, rows);
 }
 
 template <int DT, int DG>
 cudaError_t launch_sum(const EmbedGradArgs& a, const EmbedGradPlan& p, bool vec, int sms, cudaStream_t st) {
-    int tiles = (a.D + SUM_COLS - 1) / SUM_COLS;
-    if (p.chunks * tiles > 0x7fffffffll) return cudaErrorInvalidValue;
-    const unsigned blocks = (unsigned)(p.chunks * tiles);
     EmbedGradArgs b = a;
-    void* args[] = {&b, &tiles};
-    int join_tiles = (a.D + JOIN_COLS - 1) / JOIN_COLS;
-    void* join_args[] = {&b, &join_tiles};
-    const long long most = p.chunks * join_tiles;  // rows that span chunks are fewer than chunks
-    const unsigned join_blocks = (unsigned)(most < 4ll * sms ? most : 4ll * sms);
-    count_launches(2);
+    int tiles = (a.D + SUM_COLS - 1) / SUM_COLS, join_tiles = (a.D + JOIN_COLS - 1) / JOIN_COLS;
+    long long from = early_rows(a), zeros = 0;
+    int share = 1;
+    if (!a.accumulate) {  // 64 KB of zeros a CTA
+        const long long row = (long long)a.D * (a.grad_type == SOT_F32 ? 4 : 2), fit = (64 << 10) / row;
+        share = (int)(fit > 1 ? fit : 1);
+        zeros = (a.V - from + share - 1) / share;
+    }
+    const long long blocks = p.chunks * tiles + zeros;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    if (blocks == 0) return cudaSuccess;
+    void* args[] = {&b, &tiles, &zeros, &from, &share};
+    count_launches(1);
     const cudaError_t e = launch_after(vec ? (const void*)embed_sum_kernel<DT, DG, true> : (const void*)embed_sum_kernel<DT, DG, false>,
-                                       blocks, SUM_NT, args, st);
-    if (e != cudaSuccess) return e;
-    return launch_after(vec ? (const void*)embed_join_kernel<DG, true> : (const void*)embed_join_kernel<DG, false>, join_blocks,
-                        JOIN_NT, join_args, st);
+                                       (unsigned)blocks, SUM_NT, args, st);
+    if (e != cudaSuccess || p.chunks < 2) return e;
+    void* join_args[] = {&b, &join_tiles};
+    const long long most = (p.chunks * join_tiles + JOIN_NW - 1) / JOIN_NW;  // rows that span chunks are fewer than chunks
+    count_launches(1);
+    return launch_after(vec ? (const void*)embed_join_kernel<DG, true> : (const void*)embed_join_kernel<DG, false>,
+                        (unsigned)(most < 5ll * sms ? most : 5ll * sms), JOIN_NT, join_args, st);
 }
 
 }  // namespace
@@ -559,7 +620,8 @@ EmbedGradPlan embed_grad_plan(long long T, int V, int D) {
         p.pos_at[i] = place(sizeof(unsigned) * T);
     }
     p.spans_at = place(sizeof(unsigned));
-    p.span_at = place(sizeof(unsigned) * p.chunks);
+    p.span_at = place(sizeof(uint2) * p.chunks);
+    p.named_at = place(4 * (((size_t)V + 31) / 32));
     p.part_at = place(sizeof(float) * 2 * (size_t)p.chunks * D);
     return p;
 }
@@ -571,13 +633,14 @@ cudaError_t launch_embed_grad(EmbedGradArgs a, const EmbedGradPlan& p, unsigned 
         a.pos[i] = reinterpret_cast<unsigned*>(scratch + p.pos_at[i]);
     }
     a.spans = reinterpret_cast<unsigned*>(scratch + p.spans_at);
-    a.span = reinterpret_cast<unsigned*>(scratch + p.span_at);
+    a.span = reinterpret_cast<uint2*>(scratch + p.span_at);
+    a.named = a.accumulate ? nullptr : reinterpret_cast<unsigned*>(scratch + p.named_at);
     a.part = reinterpret_cast<float*>(scratch + p.part_at);
     const bool vec_out = whole_rows(a.grad, a.ldg, a.D, a.grad_type);
     const cudaError_t e = a.grad_type == SOT_F32   ? launch_sort<SOT_F32>(a, p, sms, st)
                           : a.grad_type == SOT_F16 ? launch_sort<SOT_F16>(a, p, sms, st)
                                                    : launch_sort<SOT_BF16>(a, p, sms, st);
-    if (e != cudaSuccess || a.T == 0) return e;
+    if (e != cudaSuccess) return e;
     const bool vec = vec_out && whole_rows(a.g, a.ld, a.D, a.type);
 #define SOT_OUT(DT)                                                            \
     switch (a.grad_type) {                                                     \
