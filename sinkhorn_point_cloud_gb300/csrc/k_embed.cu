@@ -7,8 +7,8 @@
 //            counts, joined through distributed shared memory), and marks the rows that tokens name; the other CTAs of
 //            the launch fill the time with zeros for the table's first rows;
 //   sum      a CTA takes a chunk of sorted tokens and a tile of columns, and writes
-//            the rows that lie inside its chunk.  A row that spans chunks leaves a partial sum in each.  Other CTAs,
-//            in between, write the zeros of the remaining rows that no token names (reads and writes at the same
+//            the rows that begin in its chunk and end there or in the next one.  A row that spans more leaves a partial sum in
+//            each chunk.  Other CTAs, in between, write the zeros of the remaining rows that no token names (reads and writes at the same
 //            time: writes alone reach 0.8 of the copy bandwidth);
 //   join     adds up the partial sums, in a fixed order.
 // No atomics on floats: repeated calls give the same bits.
@@ -47,6 +47,28 @@ __device__ __forceinline__ void store8(typename Elem<DT>::T* p, const float2 (&f
         store16(q, pack<DT>(f), policy);
 }
 
+// U indices, `step` apart from i on (the last one where i goes past n).  All loads go out before the first value is looked at: a
+// branch on one of them between two loads would wait for it.
+template <int U, class I>
+__device__ __forceinline__ void load_some(const I* p, long long i, int step, long long n, I (&v)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = __ldg(p + min(i + (long long)u * step, n - 1));
+}
+template <int U>
+__device__ __forceinline__ void load_indices(const void* ids, int type, long long i, int step, long long n, int V, int (&id)[U]) {
+    if (type == SOT_I64) {
+        long long v[U];
+        load_some<U>(static_cast<const long long*>(ids), i, step, n, v);
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = v[u] >= 0 && v[u] < V ? (int)v[u] : -1;
+    } else {
+        int v[U];
+        load_some<U>(static_cast<const int*>(ids), i, step, n, v);
+#pragma unroll
+        for (int u = 0; u < U; ++u) id[u] = v[u] >= 0 && v[u] < V ? v[u] : -1;
+    }
+}
+
 // ---- lookup ----
 constexpr int EMB_NT = 256, EMB_U = 4;
 
@@ -65,28 +87,39 @@ __global__ void __launch_bounds__(EMB_NT) embed_kernel(const EmbedArgs a, unsign
         uint4 raw[EMB_U][VEC && DT == SOT_F32 ? 2 : 1];
         T one[EMB_U];
         long long to[EMB_U];
-        bool named[EMB_U];
+        int id[EMB_U], col[EMB_U];
+        {
+            long long t[EMB_U];
+            long long wide[EMB_U];
+            int narrow[EMB_U];
 #pragma unroll
-        for (int j = 0; j < EMB_U; ++j) {
-            const unsigned i = j * EMB_NT + threadIdx.x, at = first + i, r = at / per_row;
-            const int c = (int)(at - r * per_row) * W;
-            named[j] = false;
-            to[j] = -1;
-            if (i < left) {
-                const long long t = row0 + r;
-                const int id = load_index(a.ids, a.ids_type, t, a.V);
-                to[j] = t * a.ldo + c;
-                if (id >= 0) {
-                    const T* from = static_cast<const T*>(a.table) + id * a.ld + c;
-                    named[j] = true;
-                    if constexpr (VEC) {
-                        // (rows of frequent tokens stay in L2, what is written does not)
-                        raw[j][0] = load16(reinterpret_cast<const uint4*>(from), keep);
-                        if constexpr (DT == SOT_F32) raw[j][1] = load16(reinterpret_cast<const uint4*>(from) + 1, keep);
-                    } else
-                        one[j] = *from;
-                }
+            for (int j = 0; j < EMB_U; ++j) {  // (a piece past the end is the tile's first one again, and is not written)
+                const unsigned i = j * EMB_NT + threadIdx.x, at = first + (i < left ? i : 0u), r = at / per_row;
+                col[j] = (int)(at - r * per_row) * W;
+                t[j] = row0 + r;
+                to[j] = i < left ? t[j] * a.ldo + col[j] : -1;
             }
+            if (a.ids_type == SOT_I64) {
+#pragma unroll
+                for (int j = 0; j < EMB_U; ++j) wide[j] = __ldg(static_cast<const long long*>(a.ids) + t[j]);
+#pragma unroll
+                for (int j = 0; j < EMB_U; ++j) id[j] = wide[j] >= 0 && wide[j] < a.V ? (int)wide[j] : -1;
+            } else {
+#pragma unroll
+                for (int j = 0; j < EMB_U; ++j) narrow[j] = __ldg(static_cast<const int*>(a.ids) + t[j]);
+#pragma unroll
+                for (int j = 0; j < EMB_U; ++j) id[j] = narrow[j] >= 0 && narrow[j] < a.V ? narrow[j] : -1;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < EMB_U; ++j) {  // (a row for a token without one too: a branch would wait)
+            const T* const src = static_cast<const T*>(a.table) + (long long)max(id[j], 0) * a.ld + col[j];
+            if constexpr (VEC) {
+                // (rows of frequent tokens stay in L2, what is written does not)
+                raw[j][0] = load16(reinterpret_cast<const uint4*>(src), keep);
+                if constexpr (DT == SOT_F32) raw[j][1] = load16(reinterpret_cast<const uint4*>(src) + 1, keep);
+            } else
+                one[j] = *src;
         }
 #pragma unroll
         for (int j = 0; j < EMB_U; ++j)
@@ -96,10 +129,10 @@ __global__ void __launch_bounds__(EMB_NT) embed_kernel(const EmbedArgs a, unsign
                     float2 f[4];
                     floats_of<DT>(raw[j], f);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) f[w] = named[j] ? make_float2(f[w].x * a.scale, f[w].y * a.scale) : make_float2(0.f, 0.f);
+                    for (int w = 0; w < 4; ++w) f[w] = id[j] >= 0 ? make_float2(f[w].x * a.scale, f[w].y * a.scale) : make_float2(0.f, 0.f);
                     store8<DO>(out, f, drop);
                 } else
-                    *out = Elem<DO>::put(named[j] ? Elem<DT>::get(one[j]) * a.scale : 0.f);
+                    *out = Elem<DO>::put(id[j] >= 0 ? Elem<DT>::get(one[j]) * a.scale : 0.f);
             }
     }
 }
@@ -112,87 +145,92 @@ struct SortSmem {
     unsigned total[SORT_MAX_BINS];        // of this CTA
     unsigned base[SORT_MAX_BINS];         // place of the first token of a bin in this CTA
     unsigned sums[SORT_NW];
+    // a warp's batch of tokens: row, place, and rank among those of its digit in the warp
+    unsigned key[SORT_NW][32 * SORT_U], pos[SORT_NW][32 * SORT_U];
+    unsigned order[SORT_NW][32 * SORT_U];
 };
 
 // The lanes of a warp with the same digit, from a vote for each of its bits.  `in`: lanes that have one.
-__device__ __forceinline__ unsigned same_digit(unsigned digit, int bits, bool in) {
+__device__ __forceinline__ unsigned same_digit(unsigned digit, bool in) {
     unsigned peers = __ballot_sync(0xffffffffu, in);
 #pragma unroll
-    for (int b = 0; b < SORT_MAX_BITS; ++b)
-        if (b < bits) {
-            const unsigned set = __ballot_sync(0xffffffffu, digit >> b & 1u);
-            peers &= digit >> b & 1u ? set : ~set;
-        }
+    for (int b = 0; b < SORT_MAX_BITS; ++b) {
+        const unsigned set = __ballot_sync(0xffffffffu, digit >> b & 1u);
+        peers &= digit >> b & 1u ? set : ~set;
+    }
     return peers;
 }
 
-// Row of token t; tokens without one come last.
-__device__ __forceinline__ unsigned token_key(const EmbedGradArgs& a, long long t) {
-    const int id = load_index(a.ids, a.ids_type, t, a.V);
-    return id < 0 ? (unsigned)a.V : (unsigned)id;
-}
-
+// The code runs once from end to end, so most of what it costs is fetching its instructions: loops stay loops, with a
+// warp's batch of tokens in shared memory.
 __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSmem& sm) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int bins = 1 << bits;
     // a warp's share: contiguous, whole steps of 32
-    const long long workers = SORT_CL * SORT_NW, steps = (a.T + 31) / 32, per = (steps + workers - 1) / workers * 32;
-    const long long begin = (rank * SORT_NW + warp) * per;
-    const long long end = min(begin + per, a.T);
+    const unsigned workers = SORT_CL * SORT_NW, T = (unsigned)a.T, steps = (T + 31) / 32, per = (steps + workers - 1) / workers * 32;
+    const unsigned begin = min(T, (rank * SORT_NW + warp) * per), end = min(T, begin + per);
+    unsigned *const key = sm.key[warp], *const pos = sm.pos[warp], *const at = sm.at[warp];
+    unsigned* const order = sm.order[warp];
+    if (a.named)
+#pragma unroll 1
+        for (int i = (int)rank * SORT_NT + tid; i < (a.V + 31) / 32; i += SORT_CL * SORT_NT) a.named[i] = 0u;
+#pragma unroll 1
     for (int p = 0; p < passes; ++p) {
         // (the last pass writes to buffer 0)
         const bool odd = (passes - 1 - p) & 1;
-        const unsigned *key_in = odd ? a.key[0] : a.key[1], *pos_in = odd ? a.pos[0] : a.pos[1];
-        unsigned *key_out = odd ? a.key[1] : a.key[0], *pos_out = odd ? a.pos[1] : a.pos[0];
+        const unsigned *const key_in = odd ? a.key[0] : a.key[1], *const pos_in = odd ? a.pos[0] : a.pos[1];
+        unsigned *const key_out = odd ? a.key[1] : a.key[0], *const pos_out = odd ? a.pos[1] : a.pos[0];
         const int shift = p * bits;
-        // (keys come SORT_U steps at a time: a load a step would leave the warp waiting for each)
-        const auto load_keys = [&](long long t, unsigned (&key)[SORT_U]) {
+        // A batch of tokens: counts, and each token's rank among those of its digit in the warp so far.
+        const auto count = [&](unsigned t0) {
+            if (p == 0) {
+                int id[SORT_U];
+                load_indices<SORT_U>(a.ids, a.ids_type, t0 + lane, 32, T, a.V, id);
 #pragma unroll
-            for (int u = 0; u < SORT_U; ++u) {
-                const long long i = t + u * 32;
-                key[u] = i < end ? (p == 0 ? token_key(a, i) : __ldcg(key_in + i)) : 0u;
-            }
-        };
-        if (p == 0 && a.named)
-            for (int i = (int)rank * SORT_NT + tid; i < (a.V + 31) / 32; i += SORT_CL * SORT_NT) a.named[i] = 0u;
-        for (int b = lane; b < bins; b += 32) sm.at[warp][b] = 0;
-        __syncwarp();
-        // Counts, and each token's rank among those of its digit in the warp.
-        unsigned key[SORT_U], pos[SORT_U], rank_of[SORT_U];
-        const auto count = [&](long long t0) {
-            load_keys(t0 + lane, key);
-#pragma unroll
-            for (int u = 0; u < SORT_U; ++u) {
-                const long long i = t0 + u * 32 + lane;
-                pos[u] = p == 0 || i >= end ? (unsigned)i : __ldcg(pos_in + i);
-            }
-#pragma unroll
-            for (int u = 0; u < SORT_U; ++u)
-                if (t0 + u * 32 < end) {
-                    const bool in = t0 + u * 32 + lane < end;
-                    const unsigned d = key[u] >> shift & (bins - 1), peers = same_digit(d, bits, in);
-                    const unsigned before = in ? sm.at[warp][d] : 0u;
-                    rank_of[u] = before + __popc(peers & ((1u << lane) - 1u));
-                    __syncwarp();
-                    if (in && lane == __ffs(peers) - 1) sm.at[warp][d] = before + __popc(peers);
-                    __syncwarp();
+                for (int u = 0; u < SORT_U; ++u) {  // tokens without a row come last
+                    key[u * 32 + lane] = id[u] < 0 ? (unsigned)a.V : (unsigned)id[u];
+                    pos[u * 32 + lane] = t0 + u * 32 + lane;
                 }
+            } else {
+                unsigned k[SORT_U], q[SORT_U];
+#pragma unroll
+                for (int u = 0; u < SORT_U; ++u) {
+                    const unsigned i = min(t0 + u * 32 + lane, T - 1);
+                    k[u] = __ldcg(key_in + i);
+                    q[u] = __ldcg(pos_in + i);
+                }
+#pragma unroll
+                for (int u = 0; u < SORT_U; ++u) {
+                    key[u * 32 + lane] = k[u];
+                    pos[u * 32 + lane] = q[u];
+                }
+            }
+#pragma unroll 1
+            for (unsigned i = lane; t0 + i - lane < end && i < 32 * SORT_U; i += 32) {
+                const bool in = t0 + i < end;
+                const unsigned d = key[i] >> shift & (bins - 1), peers = same_digit(d, in);
+                const unsigned before = in ? at[d] : 0u;
+                order[i] = before + __popc(peers & ((1u << lane) - 1u));
+                __syncwarp();
+                if (in && lane == __ffs(peers) - 1) at[d] = before + __popc(peers);
+                __syncwarp();
+            }
         };
-        for (long long t0 = begin; t0 < end; t0 += 32 * SORT_U) count(t0);
+        for (int b = lane; b < bins; b += 32) at[b] = 0;
+        __syncwarp();
+        // A share of one batch (65536 tokens in all) keeps its ranks; a longer one is counted here and again below.
+        const bool once = per <= 32 * SORT_U;
+#pragma unroll 1
+        for (unsigned t0 = begin; t0 < end; t0 += 32 * SORT_U) count(t0);
         __syncthreads();
         unsigned mine = 0;  // this CTA's count of bin tid
         if (tid < bins) {
-#pragma unroll
-            for (int w0 = 0; w0 < SORT_NW; w0 += 8) {
-                unsigned c[8];
-#pragma unroll
-                for (int w = 0; w < 8; ++w) c[w] = sm.at[w0 + w][tid];
-#pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    sm.at[w0 + w][tid] = mine;
-                    mine += c[w];
-                }
+#pragma unroll 8
+            for (int w = 0; w < SORT_NW; ++w) {
+                const unsigned c = sm.at[w][tid];
+                sm.at[w][tid] = mine;
+                mine += c;
             }
             sm.total[tid] = mine;
         }
@@ -217,24 +255,21 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
         }
         if (lane == 31) sm.sums[warp] = scan;
         __syncthreads();
-        unsigned base = scan - all + before;
-        for (int w = 0; w < warp; ++w) base += sm.sums[w];
+        const unsigned sums = lane < warp ? sm.sums[lane] : 0u;
+        const unsigned base = __reduce_add_sync(0xffffffffu, sums) + scan - all + before;
         if (tid < bins) sm.base[tid] = base;
         __syncthreads();
-        // Places.  A share of one batch (65536 tokens in all) has its ranks still in registers; a longer one is counted
-        // again from the start, on top of the other warps' counts.
-        const bool once = end - begin <= 32 * SORT_U;
-        for (long long t0 = begin; t0 < end; t0 += 32 * SORT_U) {
+#pragma unroll 1
+        for (unsigned t0 = begin; t0 < end; t0 += 32 * SORT_U) {
             if (!once) count(t0);
-#pragma unroll
-            for (int u = 0; u < SORT_U; ++u)
-                if (t0 + u * 32 + lane < end) {
-                    const unsigned d = key[u] >> shift & (bins - 1);
-                    const unsigned to = sm.base[d] + rank_of[u] + (once ? sm.at[warp][d] : 0u);
-                    key_out[to] = key[u];
-                    pos_out[to] = pos[u];
-                    if (p == passes - 1 && a.named && key[u] < (unsigned)a.V) atomicOr(a.named + key[u] / 32, 1u << key[u] % 32);
-                }
+#pragma unroll 2
+            for (unsigned i = lane; t0 + i < end && i < 32 * SORT_U; i += 32) {
+                const unsigned k = key[i], d = k >> shift & (bins - 1);
+                const unsigned to = sm.base[d] + order[i] + (once ? at[d] : 0u);
+                key_out[to] = k;
+                pos_out[to] = pos[i];
+                if (p == passes - 1 && a.named && k < (unsigned)a.V) atomicOr(a.named + k / 32, 1u << k % 32);
+            }
         }
         cluster_sync();  // the other CTAs' part of the order is written, and nobody reads this CTA's totals any more
     }
@@ -311,7 +346,8 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, unsigned v, in
         }
     }
 }
-// Partial sums: slot 0 of a chunk is what it has of the row that began before it, slot 1 of the row that goes on after it.
+// Partial sums of rows that end beyond the chunk after the one they begin in: slot 0 of a chunk is what it has of the
+// row that began before it, slot 1 of the row that goes on after it.
 __device__ __forceinline__ float* part_row(const EmbedGradArgs& a, long long chunk, int slot) {
     return a.part + (chunk * 2 + slot) * a.D;
 }
@@ -322,7 +358,7 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
     using T = typename Elem<DT>::T;
     constexpr int RAW = DT == SOT_F32 ? 2 : 1;
     constexpr int SUM_U = VEC && RAW == 1 ? 8 : 4;  // rows whose loads are under way together: as many as registers hold
-    __shared__ unsigned key[SUM_R + 2], pos[SUM_R];
+    __shared__ unsigned key[2 * SUM_R + 1], pos[2 * SUM_R];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // `zeros` CTAs, spread evenly over the grid, write zeros
     const long long zero = blockIdx.x * zeros / gridDim.x, block = blockIdx.x - zero;
@@ -334,41 +370,51 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
     const long long chunk = block / tiles;
     const int c0 = (int)(block % tiles) * SUM_COLS, tid = threadIdx.x;
     const long long at = chunk * SUM_R;
+    // The keys from the token before the chunk to the end of the next chunk; V: none.
     unsigned mine = (unsigned)a.V;
-    if (tid < SUM_R + 2) {  // with the token before and the one after; V: none
-        const long long i = at + tid - 1;
-        if (i >= 0 && i < a.T) mine = a.key[0][i];
-        key[tid] = mine;
-        if (tid < SUM_R) pos[tid] = at + tid < a.T ? a.pos[0][at + tid] : 0u;
+    const auto key_at = [&](long long i) { return i >= 0 && i < a.T ? __ldg(a.key[0] + i) : (unsigned)a.V; };
+    if (tid < 2 * SUM_R + 1) {
+        key[tid] = mine = key_at(at + tid - 1);
+        if (tid < 2 * SUM_R) pos[tid] = at + tid < a.T ? __ldg(a.pos[0] + at + tid) : 0u;
     }
+    const unsigned long_before = key_at(at - SUM_R - 1), long_after = key_at(at + 2 * SUM_R);
     // tokens of the chunk that have a row: they come first
     const int n = __syncthreads_count(tid >= 1 && tid <= SUM_R && mine < (unsigned)a.V);
+    const auto row = [&](int i) { return i < 2 * SUM_R ? key[i + 1] : long_after; };
+    if (n == 0) return;
+    // The chunk before finishes a row that begins in it and ends here; this one does the same for the next.
+    const bool open = key[0] == key[1];
+    int from = 0, end = n;
+    if (open && long_before != key[1] && row(SUM_R) != key[1])
+        while (from < n && row(from) == key[1]) ++from;
+    const unsigned tail = row(n - 1);
+    if (n == SUM_R && row(SUM_R) == tail && !(open && key[1] == tail) && long_after != tail)
+        while (end < 2 * SUM_R && row(end) == tail) ++end;
     float acc[8] = {};
-    bool first = true;
-    for (int i0 = 0; i0 < n; i0 += SUM_U) {
+    for (int i0 = from; i0 < end; i0 += SUM_U) {
         uint4 raw[SUM_U][RAW];
         T one[VEC ? 1 : SUM_U][8];
 #pragma unroll
         for (int u = 0; u < SUM_U; ++u)
-            if (i0 + u < n) {
-                const T* const from = static_cast<const T*>(a.g) + (long long)pos[i0 + u] * a.ld;
+            if (i0 + u < end) {
+                const T* const src = static_cast<const T*>(a.g) + (long long)pos[i0 + u] * a.ld;
                 if constexpr (VEC) {
                     const int c = sum_col<VEC, SUM_NT>(c0, tid, 0);
                     if (c < a.D) {
 #pragma unroll
-                        for (int w = 0; w < RAW; ++w) raw[u][w] = __ldcs(reinterpret_cast<const uint4*>(from + c) + w);
+                        for (int w = 0; w < RAW; ++w) raw[u][w] = __ldcs(reinterpret_cast<const uint4*>(src + c) + w);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int c = sum_col<VEC, SUM_NT>(c0, tid, j);
-                        one[u][j] = c < a.D ? from[c] : Elem<DT>::put(0.f);
+                        one[u][j] = c < a.D ? src[c] : Elem<DT>::put(0.f);
                     }
                 }
             }
 #pragma unroll
         for (int u = 0; u < SUM_U; ++u)
-            if (i0 + u < n) {
+            if (i0 + u < end) {
                 const int i = i0 + u;
                 if constexpr (VEC) {
                     float2 f[4];
@@ -382,9 +428,9 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
 #pragma unroll
                     for (int j = 0; j < 8; ++j) acc[j] += Elem<DT>::get(one[u][j]);
                 }
-                const unsigned v = key[i + 1];
-                if (i == n - 1 || key[i + 2] != v) {  // the last token of the row in this chunk
-                    const bool before = first && key[0] == v, after = key[i + 2] == v;
+                const unsigned v = row(i);
+                if (i == end - 1 || row(i + 1) != v) {  // the last token of the row here
+                    const bool before = open && from == 0 && key[1] == v, after = row(i + 1) == v;
                     if (before || after) {
                         float* const to = part_row(a, chunk, before ? 0 : 1);
 #pragma unroll
@@ -397,7 +443,6 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
                         write_row<DG, VEC, SUM_NT>(a, v, c0, tid, acc);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-                    first = false;
                 }
             }
     }
@@ -415,22 +460,17 @@ __device__ __forceinline__ bool add_chunks(const EmbedGradArgs& a, float (&acc)[
     bool on = true;
     for (int i = 0; on && i < n; i += JOIN_U, c += JOIN_U * step) {
         float f[JOIN_U][4];
-        bool mine[JOIN_U];
+        unsigned key[JOIN_U];
 #pragma unroll
-        for (int u = 0; u < JOIN_U; ++u) {
-            const long long at = c + u * step;
-            mine[u] = at < chunks && __ldcg(a.key[0] + at * SUM_R) == v;
-            if (at < chunks) {
+        for (int u = 0; u < JOIN_U; ++u) {  // (no branch on what is loaded before all loads are out)
+            const long long at = min(c + u * step, chunks - 1);
+            key[u] = __ldcg(a.key[0] + at * SUM_R);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = c0 + j * 32 + lane;
-                    f[u][j] = col < a.D ? __ldcg(part_row(a, at, 0) + col) : 0.f;
-                }
-            }
+            for (int j = 0; j < 4; ++j) f[u][j] = __ldcg(part_row(a, at, 0) + min(c0 + j * 32 + lane, a.D - 1));
         }
 #pragma unroll
         for (int u = 0; u < JOIN_U; ++u) {
-            on = on && mine[u];
+            on = on && c + u * step < chunks && key[u] == v;
             if (on) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[j] += f[u][j];
