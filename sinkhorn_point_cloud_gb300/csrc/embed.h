@@ -23,9 +23,10 @@ struct EmbedGradArgs {
     float scale;
     int accumulate;
     void* grad;  // [V, D]
-    // scratch: tokens sorted by row (two buffers), the chunks where a row begins that goes on in the next and that row,
+    // scratch: (row, token) sorted by row (two buffers), the chunks where a row begins that goes on in the next and that row,
     // a bit for each row that a token names, partial sums
-    unsigned *key[2], *pos[2], *spans, *named;
+    uint2* sorted[2];
+    unsigned *spans, *named;
     uint2* span;
     float* part;
 };
@@ -33,7 +34,7 @@ struct EmbedGradArgs {
 struct EmbedGradPlan {
     int passes, bits;  // of the sort
     long long chunks;
-    size_t key_at[2], pos_at[2], spans_at, span_at, named_at, part_at, scratch;
+    size_t sorted_at[2], spans_at, span_at, named_at, part_at, scratch;
 };
 EmbedGradPlan embed_grad_plan(long long T, int V, int D);
 cudaError_t launch_embed(const EmbedArgs& a, int sms, cudaStream_t st);

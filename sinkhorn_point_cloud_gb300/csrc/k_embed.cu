@@ -143,10 +143,12 @@ constexpr int SORT_NT = 1024, SORT_NW = SORT_NT / 32, SORT_CL = 8, SORT_MAX_BITS
 struct SortSmem {
     unsigned at[SORT_NW][SORT_MAX_BINS];  // per warp: counts, then places within the CTA's
     unsigned total[SORT_MAX_BINS];        // of this CTA
-    unsigned base[SORT_MAX_BINS];         // place of the first token of a bin in this CTA
-    unsigned sums[SORT_NW];
+    unsigned start[SORT_MAX_BINS];        // place of a bin's first token among this CTA's
+    unsigned base[SORT_MAX_BINS];         // from there to its place among all
+    uint2 sums[SORT_NW];
     // a warp's batch of tokens: row, place, and rank among those of its digit in the warp
-    unsigned key[SORT_NW][32 * SORT_U], pos[SORT_NW][32 * SORT_U];
+    alignas(8) unsigned key[SORT_NW][32 * SORT_U];
+    unsigned pos[SORT_NW][32 * SORT_U];
     unsigned order[SORT_NW][32 * SORT_U];
 };
 
@@ -179,8 +181,8 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
     for (int p = 0; p < passes; ++p) {
         // (the last pass writes to buffer 0)
         const bool odd = (passes - 1 - p) & 1;
-        const unsigned *const key_in = odd ? a.key[0] : a.key[1], *const pos_in = odd ? a.pos[0] : a.pos[1];
-        unsigned *const key_out = odd ? a.key[1] : a.key[0], *const pos_out = odd ? a.pos[1] : a.pos[0];
+        const uint2* const in = odd ? a.sorted[0] : a.sorted[1];
+        uint2* const out = odd ? a.sorted[1] : a.sorted[0];
         const int shift = p * bits;
         // A batch of tokens: counts, and each token's rank among those of its digit in the warp so far.
         const auto count = [&](unsigned t0) {
@@ -193,17 +195,13 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
                     pos[u * 32 + lane] = t0 + u * 32 + lane;
                 }
             } else {
-                unsigned k[SORT_U], q[SORT_U];
+                uint2 v[SORT_U];
+#pragma unroll
+                for (int u = 0; u < SORT_U; ++u) v[u] = __ldcg(in + min(t0 + u * 32 + lane, T - 1));
 #pragma unroll
                 for (int u = 0; u < SORT_U; ++u) {
-                    const unsigned i = min(t0 + u * 32 + lane, T - 1);
-                    k[u] = __ldcg(key_in + i);
-                    q[u] = __ldcg(pos_in + i);
-                }
-#pragma unroll
-                for (int u = 0; u < SORT_U; ++u) {
-                    key[u * 32 + lane] = k[u];
-                    pos[u * 32 + lane] = q[u];
+                    key[u * 32 + lane] = v[u].x;
+                    pos[u * 32 + lane] = v[u].y;
                 }
             }
 #pragma unroll 1
@@ -247,28 +245,63 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
                 if (r < rank) before += c;
                 all += c;
             }
-        unsigned scan = all;  // inclusive over the bins
+        unsigned scan = all, own = mine;  // inclusive over the bins: of the cluster, of this CTA
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const unsigned v = __shfl_up_sync(0xffffffffu, scan, o);
-            if (lane >= o) scan += v;
+            const unsigned v = __shfl_up_sync(0xffffffffu, scan, o), w = __shfl_up_sync(0xffffffffu, own, o);
+            if (lane >= o) {
+                scan += v;
+                own += w;
+            }
         }
-        if (lane == 31) sm.sums[warp] = scan;
+        if (lane == 31) sm.sums[warp] = make_uint2(scan, own);
         __syncthreads();
-        const unsigned sums = lane < warp ? sm.sums[lane] : 0u;
-        const unsigned base = __reduce_add_sync(0xffffffffu, sums) + scan - all + before;
-        if (tid < bins) sm.base[tid] = base;
+        const uint2 sums = lane < warp ? sm.sums[lane] : make_uint2(0u, 0u);
+        const unsigned base = __reduce_add_sync(0xffffffffu, sums.x) + scan - all + before;
+        const unsigned start = __reduce_add_sync(0xffffffffu, sums.y) + own - mine;
+        if (tid < bins) {
+            sm.base[tid] = base - start;
+            sm.start[tid] = start;
+        }
         __syncthreads();
-#pragma unroll 1
-        for (unsigned t0 = begin; t0 < end; t0 += 32 * SORT_U) {
-            if (!once) count(t0);
+        const auto write = [&](unsigned to, uint2 v) {
+            out[to] = v;
+            if (p == passes - 1 && a.named && v.x < (unsigned)a.V) atomicOr(a.named + v.x / 32, 1u << v.x % 32);
+        };
+        if (once) {
+            // The CTA's tokens change places in shared memory first, so that tokens of a digit leave side by side
+            // (scattered from where they were, 65001 tokens took 10 us a pass, a sector each).
+            uint2 v[SORT_U];
+            unsigned to[SORT_U];
+            const int n = (int)(end - begin);
+#pragma unroll
+            for (int u = 0; u < SORT_U; ++u) {
+                const int i = u * 32 + lane;
+                v[u] = make_uint2(key[i], pos[i]);
+                const unsigned d = v[u].x >> shift & (bins - 1);
+                to[u] = sm.start[d] + order[i] + at[d];
+            }
+            __syncthreads();
+            uint2* const local = reinterpret_cast<uint2*>(&sm.key[0][0]);  // (over keys and positions, now in registers)
+#pragma unroll
+            for (int u = 0; u < SORT_U; ++u)
+                if (u * 32 + lane < n) local[to[u]] = v[u];
+            __syncthreads();
+            const int count = (int)(min(T, (rank + 1) * SORT_NW * per) - min(T, rank * SORT_NW * per));
 #pragma unroll 2
-            for (unsigned i = lane; t0 + i < end && i < 32 * SORT_U; i += 32) {
-                const unsigned k = key[i], d = k >> shift & (bins - 1);
-                const unsigned to = sm.base[d] + order[i] + (once ? at[d] : 0u);
-                key_out[to] = k;
-                pos_out[to] = pos[i];
-                if (p == passes - 1 && a.named && k < (unsigned)a.V) atomicOr(a.named + k / 32, 1u << k % 32);
+            for (int i = tid; i < count; i += SORT_NT) {
+                const uint2 w = local[i];
+                write(sm.base[w.x >> shift & (bins - 1)] + i, w);
+            }
+        } else {
+#pragma unroll 1
+            for (unsigned t0 = begin; t0 < end; t0 += 32 * SORT_U) {
+                count(t0);
+#pragma unroll 2
+                for (unsigned i = lane; t0 + i < end && i < 32 * SORT_U; i += 32) {
+                    const unsigned d = key[i] >> shift & (bins - 1);
+                    write(sm.base[d] + sm.start[d] + order[i], make_uint2(key[i], pos[i]));
+                }
             }
         }
         cluster_sync();  // the other CTAs' part of the order is written, and nobody reads this CTA's totals any more
@@ -372,10 +405,13 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
     const long long at = chunk * SUM_R;
     // The keys from the token before the chunk to the end of the next chunk; V: none.
     unsigned mine = (unsigned)a.V;
-    const auto key_at = [&](long long i) { return i >= 0 && i < a.T ? __ldg(a.key[0] + i) : (unsigned)a.V; };
+    const uint2* const sorted = a.sorted[0];
+    const auto key_at = [&](long long i) { return i >= 0 && i < a.T ? __ldg(&sorted[i].x) : (unsigned)a.V; };
     if (tid < 2 * SUM_R + 1) {
-        key[tid] = mine = key_at(at + tid - 1);
-        if (tid < 2 * SUM_R) pos[tid] = at + tid < a.T ? __ldg(a.pos[0] + at + tid) : 0u;
+        const long long i = at + tid - 1;
+        const uint2 t = i >= 0 && i < a.T ? __ldg(sorted + i) : make_uint2((unsigned)a.V, 0u);
+        key[tid] = mine = t.x;
+        if (tid > 0) pos[tid - 1] = t.y;
     }
     const unsigned long_before = key_at(at - SUM_R - 1), long_after = key_at(at + 2 * SUM_R);
     // tokens of the chunk that have a row: they come first
@@ -448,89 +484,57 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
     }
 }
 
-// Rows that span chunks, from the list of the chunks where one begins (in no order: each is summed by itself).  A warp takes
-// JOIN_COLS columns of a row and adds up what its first JOIN_OWN other chunks have; most rows span no more.  For those that
-// do, the CTA's warps take every eighth of the remaining chunks each, and their sums are added in order.  Eight chunks' sums are
-// fetched before it is known that they belong to the row, so that one wait finds both out.
-constexpr int JOIN_NT = 256, JOIN_NW = JOIN_NT / 32, JOIN_COLS = 128, JOIN_U = 8, JOIN_OWN = 8;
-
-// Adds what chunks c, c + step, ... (n of them at most) have of row v to acc; returns whether the row goes on.
-__device__ __forceinline__ bool add_chunks(const EmbedGradArgs& a, float (&acc)[4], long long c, int step, int n, long long chunks,
-                                           unsigned v, int c0, int lane) {
-    bool on = true;
-    for (int i = 0; on && i < n; i += JOIN_U, c += JOIN_U * step) {
-        float f[JOIN_U][4];
-        unsigned key[JOIN_U];
-#pragma unroll
-        for (int u = 0; u < JOIN_U; ++u) {  // (no branch on what is loaded before all loads are out)
-            const long long at = min(c + u * step, chunks - 1);
-            key[u] = __ldcg(a.key[0] + at * SUM_R);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) f[u][j] = __ldcg(part_row(a, at, 0) + min(c0 + j * 32 + lane, a.D - 1));
-        }
-#pragma unroll
-        for (int u = 0; u < JOIN_U; ++u) {
-            on = on && c + u * step < chunks && key[u] == v;
-            if (on) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] += f[u][j];
-            }
-        }
-    }
-    return on;
-}
+// Rows that span chunks, from the list of the chunks where one begins (in no order: each is summed by itself).  A CTA takes
+// JOIN_COLS columns of a row.  Warp w adds up the row's chunks w, w + 8, ..., the warps' sums are added in order.  Eight
+// chunks' sums are fetched before it is known that they belong to the row, so that one wait finds both out.
+constexpr int JOIN_NT = 256, JOIN_NW = JOIN_NT / 32, JOIN_COLS = 128, JOIN_U = 8;
 
 template <int DG, bool VEC>
-__global__ void __launch_bounds__(JOIN_NT) embed_join_kernel(const EmbedGradArgs a, int tiles) {
-    __shared__ float sums[JOIN_NW][JOIN_COLS], rest[JOIN_NW][JOIN_COLS];
-    __shared__ bool more[JOIN_NW];
+__global__ void __launch_bounds__(JOIN_NT, 4) embed_join_kernel(const EmbedGradArgs a, int tiles) {
+    __shared__ float sums[JOIN_NW][JOIN_COLS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long spans = __ldcg(a.spans), work = spans * tiles, chunks = (a.T + SUM_R - 1) / SUM_R;
-    // (columns go through shared memory from the order they are summed in to the order they are written in)
-    const auto write = [&](const float* from, unsigned v, int c0) {
-        float f[8];
-        if (lane >= 16) return;
+    for (long long w = blockIdx.x; w < work; w += gridDim.x) {
+        const uint2 span = __ldcg(a.span + w % spans);
+        const int c0 = (int)(w / spans) * JOIN_COLS;
+        int col[4];
+        float acc[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = from[sum_col<VEC, 16>(0, lane, j)];
-        write_row<DG, VEC, 16>(a, v, c0, lane, f);
-    };
-    for (long long w0 = (long long)blockIdx.x * JOIN_NW; w0 < work; w0 += (long long)gridDim.x * JOIN_NW) {
-        const long long w = w0 + warp;
-        if (lane == 0) more[warp] = false;
-        if (w < work) {
-            const uint2 span = __ldcg(a.span + w % spans);
-            const int c0 = (int)(w / spans) * JOIN_COLS;
-            float acc[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int col = c0 + j * 32 + lane;
-                acc[j] = col < a.D ? __ldcg(part_row(a, span.x, 1) + col) : 0.f;
-            }
-            const bool on = add_chunks(a, acc, span.x + 1, 1, JOIN_OWN, chunks, span.y, c0, lane);
-            if (lane == 0) more[warp] = on;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sums[warp][j * 32 + lane] = acc[j];
-            __syncwarp();
-            if (!on) write(sums[warp], span.y, c0);
+        for (int j = 0; j < 4; ++j) {  // (columns past the end are summed as the last one, and not written)
+            col[j] = min(c0 + j * 32 + lane, a.D - 1);
+            acc[j] = warp == 0 ? __ldcg(part_row(a, span.x, 1) + col[j]) : 0.f;
         }
-        __syncthreads();
-        for (int k = 0; k < JOIN_NW; ++k) {
-            if (!more[k]) continue;
-            const uint2 span = __ldcg(a.span + (w0 + k) % spans);
-            const int c0 = (int)((w0 + k) / spans) * JOIN_COLS;
-            float acc[4] = {}, own = tid < JOIN_COLS ? sums[k][tid] : 0.f;
-            add_chunks(a, acc, span.x + 1 + JOIN_OWN + warp, JOIN_NW, 0x7fffffff, chunks, span.y, c0, lane);
-            __syncthreads();
+        bool on = true;
+        for (long long c = span.x + 1 + warp; on; c += JOIN_U * JOIN_NW) {
+            float f[JOIN_U][4];
+            unsigned key[JOIN_U];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) rest[warp][j * 32 + lane] = acc[j];
-            __syncthreads();
-            if (tid < JOIN_COLS) {
-                for (int i = 0; i < JOIN_NW; ++i) own += rest[i][tid];
-                sums[k][tid] = own;
+            for (int u = 0; u < JOIN_U; ++u) {  // (no branch on what is loaded before all loads are out)
+                const long long at = min(c + u * JOIN_NW, chunks - 1);
+                key[u] = __ldcg(&a.sorted[0][at * SUM_R].x);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[u][j] = __ldcg(part_row(a, at, 0) + col[j]);
             }
-            __syncthreads();
-            if (warp == 0) write(sums[k], span.y, c0);
+#pragma unroll
+            for (int u = 0; u < JOIN_U; ++u) {
+                on = on && c + u * JOIN_NW < chunks && key[u] == span.y;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[j] += on ? f[u][j] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[warp][j * 32 + lane] = acc[j];
+        __syncthreads();
+        if (tid < JOIN_COLS / 8) {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = sum_col<VEC, JOIN_COLS / 8>(0, tid, j);
+                f[j] = sums[0][at];
+                for (int k = 1; k < JOIN_NW; ++k) f[j] += sums[k][at];
+            }
+            write_row<DG, VEC, JOIN_COLS / 8>(a, span.y, c0, tid, f);
         }
         __syncthreads();
     }
@@ -618,10 +622,10 @@ cudaError_t launch_sum(const EmbedGradArgs& a, const EmbedGradPlan& p, bool vec,
                                        (unsigned)blocks, SUM_NT, args, st);
     if (e != cudaSuccess || p.chunks < 2) return e;
     void* join_args[] = {&b, &join_tiles};
-    const long long most = (p.chunks * join_tiles + JOIN_NW - 1) / JOIN_NW;  // rows that span chunks are fewer than chunks
+    const long long most = p.chunks * join_tiles;  // rows that span chunks are fewer than chunks
     count_launches(1);
     return launch_after(vec ? (const void*)embed_join_kernel<DG, true> : (const void*)embed_join_kernel<DG, false>,
-                        (unsigned)(most < 5ll * sms ? most : 5ll * sms), JOIN_NT, join_args, st);
+                        (unsigned)(most < 4ll * sms ? most : 4ll * sms), JOIN_NT, join_args, st);
 }
 
 }  // namespace
@@ -655,10 +659,7 @@ EmbedGradPlan embed_grad_plan(long long T, int V, int D) {
         p.scratch = (at + bytes + 255) & ~(size_t)255;
         return at;
     };
-    for (int i = 0; i < 2; ++i) {
-        p.key_at[i] = place(sizeof(unsigned) * T);
-        p.pos_at[i] = place(sizeof(unsigned) * T);
-    }
+    for (int i = 0; i < 2; ++i) p.sorted_at[i] = place(sizeof(uint2) * T);
     p.spans_at = place(sizeof(unsigned));
     p.span_at = place(sizeof(uint2) * p.chunks);
     p.named_at = place(4 * (((size_t)V + 31) / 32));
@@ -668,10 +669,7 @@ EmbedGradPlan embed_grad_plan(long long T, int V, int D) {
 
 cudaError_t launch_embed_grad(EmbedGradArgs a, const EmbedGradPlan& p, unsigned char* scratch, int sms, cudaStream_t st) {
     if (a.T == 0 && a.accumulate) return cudaSuccess;
-    for (int i = 0; i < 2; ++i) {
-        a.key[i] = reinterpret_cast<unsigned*>(scratch + p.key_at[i]);
-        a.pos[i] = reinterpret_cast<unsigned*>(scratch + p.pos_at[i]);
-    }
+    for (int i = 0; i < 2; ++i) a.sorted[i] = reinterpret_cast<uint2*>(scratch + p.sorted_at[i]);
     a.spans = reinterpret_cast<unsigned*>(scratch + p.spans_at);
     a.span = reinterpret_cast<uint2*>(scratch + p.span_at);
     a.named = a.accumulate ? nullptr : reinterpret_cast<unsigned*>(scratch + p.named_at);
