@@ -308,9 +308,9 @@ __device__ void sort_tokens(const EmbedGradArgs& a, int passes, int bits, SortSm
     }
 }
 
-// Zeros of the rows in [v0, v1), those in `named` (a bit each; NULL: none) excepted, by NT threads.
+// Zeros of the rows in [v0, v1), those in `named` (a bit for each row from `base` on; NULL: none) excepted, by NT threads.
 template <int DG, int NT>
-__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, long long v0, long long v1, const unsigned* named) {
+__device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, long long v0, long long v1, const unsigned* named, long long base) {
     using G = typename Elem<DG>::T;
     constexpr int N = Elem<DG>::N;
     const uint64_t policy = policy_drop();
@@ -319,7 +319,7 @@ __device__ __forceinline__ void zero_rows(const EmbedGradArgs& a, long long v0, 
     while (width > 1 && width / 2 * N >= a.D) width /= 2;
     const int c = threadIdx.x % width;
     for (long long v = v0 + threadIdx.x / width; v < v1; v += NT / width) {
-        if (named && named[v / 32] >> (v % 32) & 1u) continue;
+        if (named && named[(v - base) / 32] >> ((v - base) % 32) & 1u) continue;
         G* const to = static_cast<G*>(a.grad) + v * a.ldg;
         // whole granules, and the elements before and after them one by one
         const int head = min(a.D, (int)((16 - ((unsigned long long)to & 15)) & 15) / (int)sizeof(G)), whole = (a.D - head) / N;
@@ -340,42 +340,78 @@ __global__ void __launch_bounds__(SORT_NT) embed_sort_kernel(const EmbedGradArgs
         return;
     }
     const long long parts = gridDim.x - SORT_CL, part = blockIdx.x - SORT_CL;
-    zero_rows<DG, SORT_NT>(a, rows * part / parts, rows * (part + 1) / parts, nullptr);
+    zero_rows<DG, SORT_NT>(a, rows * part / parts, rows * (part + 1) / parts, nullptr, 0);
 }
 
 // ---- gradient: sums ----
-constexpr int SUM_NT = 128, SUM_R = 32, SUM_COLS = SUM_NT * 8;
+constexpr int SUM_NT = 128, SUM_R = 32;
+// Columns of a thread: a granule of the incoming gradient, or four where its rows are not whole granules.
+template <int DT, bool VEC>
+constexpr int SUM_W = VEC ? Elem<DT>::N : 4;
+
+constexpr int ZERO_BYTES = 64 << 10;  // of zeros a CTA of the sums writes
 
 // The columns of a thread, of NT that share a tile: eight in a row where rows are whole granules (VEC), else NT apart.
-template <bool VEC, int NT>
+template <bool VEC, int NT, int W>
 __device__ __forceinline__ int sum_col(int c0, int i, int j) {
-    return VEC ? c0 + i * 8 + j : c0 + j * NT + i;
+    return VEC ? c0 + i * W + j : c0 + j * NT + i;
 }
-template <int DG, bool VEC, int NT>
-__device__ __forceinline__ void write_row(const EmbedGradArgs& a, unsigned v, int c0, int i, const float (&acc)[8]) {
+// W elements as floats, W * their size being 8, 16 or 32 bytes at an address aligned to that or to 16.
+template <int DG, int W>
+__device__ __forceinline__ void read_some(const typename Elem<DG>::T* p, float (&f)[W]) {
+    if constexpr (W * sizeof(*p) == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        float2 h[Elem<DG>::N / 2];
+        unpack<DG>(make_uint4(v.x, v.y, 0u, 0u), h);
+        f[0] = h[0].x, f[1] = h[0].y, f[2] = h[1].x, f[3] = h[1].y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += Elem<DG>::N) {
+            float2 h[Elem<DG>::N / 2];
+            unpack<DG>(*reinterpret_cast<const uint4*>(p + i), h);
+#pragma unroll
+            for (int j = 0; j < Elem<DG>::N / 2; ++j) f[i + 2 * j] = h[j].x, f[i + 2 * j + 1] = h[j].y;
+        }
+    }
+}
+template <int DG, int W>
+__device__ __forceinline__ void write_some(typename Elem<DG>::T* p, const float (&f)[W]) {
+    if constexpr (W * sizeof(*p) == 8) {
+        const float2 h[Elem<DG>::N / 2] = {{f[0], f[1]}, {f[2], f[3]}};
+        const uint4 v = pack<DG>(h);
+        __stcs(reinterpret_cast<uint2*>(p), make_uint2(v.x, v.y));
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += Elem<DG>::N) {
+            float2 h[Elem<DG>::N / 2];
+#pragma unroll
+            for (int j = 0; j < Elem<DG>::N / 2; ++j) h[j] = make_float2(f[i + 2 * j], f[i + 2 * j + 1]);
+            store16(reinterpret_cast<uint4*>(p + i), pack<DG>(h), policy_drop());
+        }
+    }
+}
+template <int DG, bool VEC, int NT, int W>
+__device__ __forceinline__ void write_row(const EmbedGradArgs& a, unsigned v, int c0, int i, const float (&acc)[W]) {
     using G = typename Elem<DG>::T;
     G* const to = static_cast<G*>(a.grad) + (long long)v * a.ldg;
     if constexpr (VEC) {
-        const int c = sum_col<VEC, NT>(c0, i, 0);
+        const int c = sum_col<VEC, NT, W>(c0, i, 0);
         if (c >= a.D) return;
-        uint4 was[DG == SOT_F32 ? 2 : 1] = {};
-        float2 old[4] = {}, f[4];
+        float f[W];
+        if (a.accumulate) read_some<DG, W>(to + c, f);
+#pragma unroll
+        for (int j = 0; j < W; ++j) f[j] = a.accumulate ? fmaf(a.scale, acc[j], f[j]) : a.scale * acc[j];
+        write_some<DG, W>(to + c, f);
+    } else {
+        G old[W];
         if (a.accumulate) {
-            was[0] = *reinterpret_cast<const uint4*>(to + c);
-            if constexpr (DG == SOT_F32) was[1] = *(reinterpret_cast<const uint4*>(to + c) + 1);
-            floats_of<DG>(was, old);
+#pragma unroll
+            for (int j = 0; j < W; ++j) old[j] = to[min(sum_col<VEC, NT, W>(c0, i, j), a.D - 1)];
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            f[j] = a.accumulate ? make_float2(fmaf(a.scale, acc[2 * j], old[j].x), fmaf(a.scale, acc[2 * j + 1], old[j].y))
-                                : make_float2(a.scale * acc[2 * j], a.scale * acc[2 * j + 1]);
-        store8<DG>(to + c, f, policy_drop());
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = sum_col<VEC, NT>(c0, i, j);
-            if (c < a.D)
-                to[c] = Elem<DG>::put(a.accumulate ? fmaf(a.scale, acc[j], Elem<DG>::get(to[c])) : a.scale * acc[j]);
+        for (int j = 0; j < W; ++j) {
+            const int c = sum_col<VEC, NT, W>(c0, i, j);
+            if (c < a.D) to[c] = Elem<DG>::put(a.accumulate ? fmaf(a.scale, acc[j], Elem<DG>::get(old[j])) : a.scale * acc[j]);
         }
     }
 }
@@ -385,23 +421,117 @@ __device__ __forceinline__ float* part_row(const EmbedGradArgs& a, long long chu
     return a.part + (chunk * 2 + slot) * a.D;
 }
 
+// A thread's columns of several rows of the incoming gradient, fetched together: as many as registers hold.
+template <int DT, bool VEC>
+struct SumRows {
+    using T = typename Elem<DT>::T;
+    static constexpr int W = SUM_W<DT, VEC>, U = 8;
+    uint4 raw[VEC ? U : 1];
+    T one[VEC ? 1 : U][W];
+    // Rows pos[i0 ..]; past `end` the last one again, past the last column that one: no branch lies between two loads.
+    __device__ __forceinline__ void load(const EmbedGradArgs& a, const unsigned* pos, int i0, int end, int c0) {
+        const T* const g = static_cast<const T*>(a.g);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const T* const src = g + (long long)pos[min(i0 + u, end - 1)] * a.ld;
+            if constexpr (VEC)
+                raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + min(sum_col<VEC, SUM_NT, W>(c0, threadIdx.x, 0), a.D - W)));
+            else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) one[u][j] = src[min(sum_col<VEC, SUM_NT, W>(c0, threadIdx.x, j), a.D - 1)];
+            }
+        }
+    }
+    __device__ __forceinline__ void add(int u, float (&acc)[W]) const {
+        if constexpr (VEC) {
+            float2 f[W / 2];
+            unpack<DT>(raw[u], f);
+#pragma unroll
+            for (int j = 0; j < W / 2; ++j) {
+                acc[2 * j] += f[j].x;
+                acc[2 * j + 1] += f[j].y;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) acc[j] += Elem<DT>::get(one[u][j]);
+        }
+    }
+};
+
+// Few tokens: no sort.  Every CTA reads all ids; the one of a row's first token (and a tile of columns) gathers the others of
+// the row, in order.  One launch instead of three.
+constexpr int FEW_TOKENS = 512;
+
+template <int DT, int DG, bool VEC>
+__global__ void __launch_bounds__(SUM_NT, 8) embed_few_kernel(const EmbedGradArgs a, int tiles, long long zeros, int zero_share) {
+    constexpr int U = SumRows<DT, VEC>::U, W = SUM_W<DT, VEC>, PER = FEW_TOKENS / SUM_NT;
+    __shared__ int ids[FEW_TOKENS];
+    __shared__ unsigned mark[FEW_TOKENS > ZERO_BYTES / 32 ? FEW_TOKENS : ZERO_BYTES / 32];  // rows of this CTA; or the row's tokens
+    __shared__ int length;
+    const int tid = threadIdx.x, lane = tid & 31, T = (int)a.T;
+    int id[PER];
+    if (T > 0) load_indices<PER>(a.ids, a.ids_type, tid, SUM_NT, T, a.V, id);
+#pragma unroll
+    for (int u = 0; u < PER; ++u) ids[u * SUM_NT + tid] = u * SUM_NT + tid < T ? id[u] : -1;
+    const long long zero = blockIdx.x * zeros / gridDim.x, block = blockIdx.x - zero;
+    if ((blockIdx.x + 1) * zeros / gridDim.x > zero) {
+        const long long v0 = zero * zero_share, v1 = min((long long)a.V, v0 + zero_share);
+        for (int i = tid; i < (zero_share + 31) / 32; i += SUM_NT) mark[i] = 0u;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const long long r = ids[u * SUM_NT + tid] - v0;
+            if (r >= 0 && r < v1 - v0) atomicOr(&mark[r / 32], 1u << r % 32);
+        }
+        __syncthreads();
+        zero_rows<DG, SUM_NT>(a, v0, v1, mark, v0);
+        return;
+    }
+    const int t = (int)(block / tiles), c0 = (int)(block % tiles) * SUM_NT * W;
+    __syncthreads();
+    const int v = ids[t];
+    bool later = v < 0;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) later = later || (u * SUM_NT + tid < t && ids[u * SUM_NT + tid] == v);
+    if (__syncthreads_or(later)) return;
+    unsigned* const pos = mark;
+    if (tid < 32) {
+        int n = 0;
+        for (int i = t / 32 * 32; i < T; i += 32) {
+            const unsigned hit = __ballot_sync(0xffffffffu, ids[i + lane] == v);
+            if (hit >> lane & 1u) pos[n + __popc(hit & ((1u << lane) - 1u))] = i + lane;
+            n += __popc(hit);
+        }
+        if (lane == 0) length = n;
+    }
+    __syncthreads();
+    const int n = length;
+    float acc[W] = {};
+    for (int i0 = 0; i0 < n; i0 += U) {
+        SumRows<DT, VEC> rows;
+        rows.load(a, pos, i0, n, c0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u < n) rows.add(u, acc);
+    }
+    write_row<DG, VEC, SUM_NT, W>(a, (unsigned)v, c0, tid, acc);
+}
+
 template <int DT, int DG, bool VEC>
 __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArgs a, int tiles, long long zeros, long long zero_from,
                                                               int zero_share) {
-    using T = typename Elem<DT>::T;
-    constexpr int RAW = DT == SOT_F32 ? 2 : 1;
-    constexpr int SUM_U = VEC && RAW == 1 ? 8 : 4;  // rows whose loads are under way together: as many as registers hold
+    constexpr int SUM_U = SumRows<DT, VEC>::U, W = SUM_W<DT, VEC>;
     __shared__ unsigned key[2 * SUM_R + 1], pos[2 * SUM_R];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // `zeros` CTAs, spread evenly over the grid, write zeros
     const long long zero = blockIdx.x * zeros / gridDim.x, block = blockIdx.x - zero;
     if ((blockIdx.x + 1) * zeros / gridDim.x > zero) {
         const long long v = zero_from + zero * zero_share;
-        zero_rows<DG, SUM_NT>(a, v, min((long long)a.V, v + zero_share), a.named);
+        zero_rows<DG, SUM_NT>(a, v, min((long long)a.V, v + zero_share), a.named, 0);
         return;
     }
     const long long chunk = block / tiles;
-    const int c0 = (int)(block % tiles) * SUM_COLS, tid = threadIdx.x;
+    const int c0 = (int)(block % tiles) * SUM_NT * W, tid = threadIdx.x;
     const long long at = chunk * SUM_R;
     // The keys from the token before the chunk to the end of the next chunk; V: none.
     unsigned mine = (unsigned)a.V;
@@ -426,59 +556,30 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
     const unsigned tail = row(n - 1);
     if (n == SUM_R && row(SUM_R) == tail && !(open && key[1] == tail) && long_after != tail)
         while (end < 2 * SUM_R && row(end) == tail) ++end;
-    float acc[8] = {};
+    float acc[W] = {};
     for (int i0 = from; i0 < end; i0 += SUM_U) {
-        uint4 raw[SUM_U][RAW];
-        T one[VEC ? 1 : SUM_U][8];
-#pragma unroll
-        for (int u = 0; u < SUM_U; ++u)
-            if (i0 + u < end) {
-                const T* const src = static_cast<const T*>(a.g) + (long long)pos[i0 + u] * a.ld;
-                if constexpr (VEC) {
-                    const int c = sum_col<VEC, SUM_NT>(c0, tid, 0);
-                    if (c < a.D) {
-#pragma unroll
-                        for (int w = 0; w < RAW; ++w) raw[u][w] = __ldcs(reinterpret_cast<const uint4*>(src + c) + w);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int c = sum_col<VEC, SUM_NT>(c0, tid, j);
-                        one[u][j] = c < a.D ? src[c] : Elem<DT>::put(0.f);
-                    }
-                }
-            }
+        SumRows<DT, VEC> rows;
+        rows.load(a, pos, i0, end, c0);
 #pragma unroll
         for (int u = 0; u < SUM_U; ++u)
             if (i0 + u < end) {
                 const int i = i0 + u;
-                if constexpr (VEC) {
-                    float2 f[4];
-                    floats_of<DT>(raw[u], f);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc[2 * j] += f[j].x;
-                        acc[2 * j + 1] += f[j].y;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[j] += Elem<DT>::get(one[u][j]);
-                }
+                rows.add(u, acc);
                 const unsigned v = row(i);
                 if (i == end - 1 || row(i + 1) != v) {  // the last token of the row here
                     const bool before = open && from == 0 && key[1] == v, after = row(i + 1) == v;
                     if (before || after) {
                         float* const to = part_row(a, chunk, before ? 0 : 1);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int c = sum_col<VEC, SUM_NT>(c0, tid, j);
+                        for (int j = 0; j < W; ++j) {
+                            const int c = sum_col<VEC, SUM_NT, W>(c0, tid, j);
                             if (c < a.D) __stcg(to + c, acc[j]);
                         }
                         if (!before && tid == 0 && c0 == 0) a.span[atomicAdd(a.spans, 1u)] = make_uint2((unsigned)chunk, v);
                     } else
-                        write_row<DG, VEC, SUM_NT>(a, v, c0, tid, acc);
+                        write_row<DG, VEC, SUM_NT, W>(a, v, c0, tid, acc);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+                    for (int j = 0; j < W; ++j) acc[j] = 0.f;
                 }
             }
     }
@@ -530,11 +631,11 @@ __global__ void __launch_bounds__(JOIN_NT, 4) embed_join_kernel(const EmbedGradA
             float f[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int at = sum_col<VEC, JOIN_COLS / 8>(0, tid, j);
+                const int at = sum_col<VEC, JOIN_COLS / 8, 8>(0, tid, j);
                 f[j] = sums[0][at];
                 for (int k = 1; k < JOIN_NW; ++k) f[j] += sums[k][at];
             }
-            write_row<DG, VEC, JOIN_COLS / 8>(a, span.y, c0, tid, f);
+            write_row<DG, VEC, JOIN_COLS / 8, 8>(a, span.y, c0, tid, f);
         }
         __syncthreads();
     }
@@ -605,17 +706,25 @@ cudaError_t launch_sort(const EmbedGradArgs& a, const EmbedGradPlan& p, int sms,
 template <int DT, int DG>
 cudaError_t launch_sum(const EmbedGradArgs& a, const EmbedGradPlan& p, bool vec, int sms, cudaStream_t st) {
     EmbedGradArgs b = a;
-    int tiles = (a.D + SUM_COLS - 1) / SUM_COLS, join_tiles = (a.D + JOIN_COLS - 1) / JOIN_COLS;
-    long long from = early_rows(a), zeros = 0;
+    const int cols = SUM_NT * (vec ? SUM_W<DT, true> : SUM_W<DT, false>);
+    int tiles = (a.D + cols - 1) / cols, join_tiles = (a.D + JOIN_COLS - 1) / JOIN_COLS;
+    const bool few = p.passes == 0;
+    long long from = few ? 0 : early_rows(a), zeros = 0;
     int share = 1;
-    if (!a.accumulate) {  // 64 KB of zeros a CTA
-        const long long row = (long long)a.D * (a.grad_type == SOT_F32 ? 4 : 2), fit = (64 << 10) / row;
+    if (!a.accumulate) {
+        const long long row = (long long)a.D * (a.grad_type == SOT_F32 ? 4 : 2), fit = ZERO_BYTES / row;
         share = (int)(fit > 1 ? fit : 1);
         zeros = (a.V - from + share - 1) / share;
     }
-    const long long blocks = p.chunks * tiles + zeros;
+    const long long blocks = (few ? a.T : p.chunks) * tiles + zeros;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     if (blocks == 0) return cudaSuccess;
+    if (few) {
+        count_launches(1);
+        if (vec) embed_few_kernel<DT, DG, true><<<(unsigned)blocks, SUM_NT, 0, st>>>(b, tiles, zeros, share);
+        else embed_few_kernel<DT, DG, false><<<(unsigned)blocks, SUM_NT, 0, st>>>(b, tiles, zeros, share);
+        return cudaGetLastError();
+    }
     void* args[] = {&b, &tiles, &zeros, &from, &share};
     count_launches(1);
     const cudaError_t e = launch_after(vec ? (const void*)embed_sum_kernel<DT, DG, true> : (const void*)embed_sum_kernel<DT, DG, false>,
@@ -649,6 +758,7 @@ cudaError_t launch_embed(const EmbedArgs& a, int sms, cudaStream_t st) {
 
 EmbedGradPlan embed_grad_plan(long long T, int V, int D) {
     EmbedGradPlan p = {};
+    if (T <= FEW_TOKENS) return p;  // (no sort, no scratch)
     int need = 1;
     while (need < 32 && (unsigned)V >> need) ++need;  // keys 0 .. V
     p.passes = (need + SORT_MAX_BITS - 1) / SORT_MAX_BITS;
@@ -675,7 +785,8 @@ cudaError_t launch_embed_grad(EmbedGradArgs a, const EmbedGradPlan& p, unsigned 
     a.named = a.accumulate ? nullptr : reinterpret_cast<unsigned*>(scratch + p.named_at);
     a.part = reinterpret_cast<float*>(scratch + p.part_at);
     const bool vec_out = whole_rows(a.grad, a.ldg, a.D, a.grad_type);
-    const cudaError_t e = a.grad_type == SOT_F32   ? launch_sort<SOT_F32>(a, p, sms, st)
+    const cudaError_t e = p.passes == 0 ? cudaSuccess
+                          : a.grad_type == SOT_F32   ? launch_sort<SOT_F32>(a, p, sms, st)
                           : a.grad_type == SOT_F16 ? launch_sort<SOT_F16>(a, p, sms, st)
                                                    : launch_sort<SOT_BF16>(a, p, sms, st);
     if (e != cudaSuccess) return e;

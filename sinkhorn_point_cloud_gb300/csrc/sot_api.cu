@@ -1957,8 +1957,8 @@ int sot_embed_grad(const void* grad_out, long long T, int D, long long ld, int t
     a.grad = grad;
     Scratch S((cudaStream_t)stream);
     const EmbedGradPlan p = embed_grad_plan(T, V, D);
-    unsigned char* scratch = S.alloc<unsigned char>(p.scratch);
-    if (!scratch) return fail(SOT_ERR_NOMEM, "scratch allocation failed");
+    unsigned char* scratch = nullptr;
+    if (p.scratch && !(scratch = S.alloc<unsigned char>(p.scratch))) return fail(SOT_ERR_NOMEM, "scratch allocation failed");
     SOT_CUDA(launch_embed_grad(a, p, scratch, device_sms(), (cudaStream_t)stream));
     return SOT_OK;
 }
