@@ -581,12 +581,11 @@ __global__ void __launch_bounds__(NT * TEAMS<NT>, NT == 32 ? 3 : 1024 / NT) topk
 //   tau dx_v = G_v - p_v (G + gH (ln 2 t_v + H)) = G_v + p_v (c0 + c1 t_v).
 // One read and one write per logit, each granule on its own.  The entries' columns are
 // formed again after the rest, from logits read before anything is written.
-constexpr int TOPK_GRAD_NT = 256;
-
-template <int DT>
-__global__ void __launch_bounds__(TOPK_GRAD_NT) topk_grad_kernel(const TopkGradArgs a, int G, int chunks) {
+// A CTA of NT threads takes G granules of a row.
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1536 / NT) topk_grad_kernel(const TopkGradArgs a, int G, int chunks) {
     using T = typename Elem<DT>::T;
-    constexpr int N = Elem<DT>::N, U = 4, NT = TOPK_GRAD_NT;
+    constexpr int N = Elem<DT>::N, U = 4;
     extern __shared__ __align__(16) float ent[];  // entries of the slice: logit
     __shared__ float red[NT / 32];
     const int tid = threadIdx.x;
@@ -595,11 +594,13 @@ __global__ void __launch_bounds__(TOPK_GRAD_NT) topk_grad_kernel(const TopkGradA
     T* const grow = static_cast<T*>(a.grad) + row * a.ldg;
     const Slice s = slice_at<DT>(x, a.V, G, blockIdx.x % chunks);
     const bool aligned = same_granules<T>(x, grow);
+    // (the row's values are fetched together, whether they turn out to count or not: one wait instead of three)
+    const float lse = a.lse[row], row_gl = a.g_logp ? a.g_logp[row] : 0.f, row_gh = a.g_entropy ? a.g_entropy[row] : 0.f;
+    const float row_h = a.g_entropy ? a.entropy[row] : 0.f;
     const int tgt = a.target ? load_index(a.target, a.target_type, row, a.V) : -1;
     const bool keep = !a.target || tgt >= 0;
     const float inv_tau = 1.f / a.tau;
-    const float gl = keep && tgt >= 0 && a.g_logp ? a.g_logp[row] : 0.f;
-    const float gh = keep && a.g_entropy ? a.g_entropy[row] : 0.f;
+    const float gl = tgt >= 0 ? row_gl : 0.f, gh = keep ? row_gh : 0.f;
     float gt = 0.f;
     bool any = gl != 0.f || gh != 0.f;
     const int e0 = s.e0, e1 = s.e0 + s.ng * N;  // the slice's columns
@@ -620,8 +621,8 @@ __global__ void __launch_bounds__(TOPK_GRAD_NT) topk_grad_kernel(const TopkGradA
         slice_zero<DT>(s, grow, a.V, aligned, tid, NT);
         return;
     }
-    const float lse = a.lse[row], u = lse * SOT_LOG2E, sc = SOT_LOG2E / a.tau;
-    const float H = gh != 0.f ? a.entropy[row] : 0.f;
+    const float u = lse * SOT_LOG2E, sc = SOT_LOG2E / a.tau;
+    const float H = gh != 0.f ? row_h : 0.f;
     // (a row without a lse has no gradient: NaN)
     const float c0 = -(gl + gt + gh * H) * inv_tau + (lse - lse), c1 = -gh * SOT_LN2 * inv_tau;
     const bool far = !(fabsf(u) < 0x1p10f);
@@ -737,8 +738,11 @@ cudaError_t launch_topk_t(const TopkArgs& a, const TopkPlan& p, cudaStream_t st)
 }
 
 template <int DT>
-cudaError_t launch_topk_grad_t(const TopkGradArgs& a, int G, int chunks, cudaStream_t st) {
-    topk_grad_kernel<DT><<<(unsigned)(a.T * chunks), TOPK_GRAD_NT, a.g_top ? a.K * sizeof(float) : 0, st>>>(a, G, chunks);
+cudaError_t launch_topk_grad_t(const TopkGradArgs& a, int NT, int G, int chunks, cudaStream_t st) {
+    const unsigned blocks = (unsigned)(a.T * chunks);
+    const size_t smem = a.g_top ? a.K * sizeof(float) : 0;
+    if (NT == 64) topk_grad_kernel<DT, 64><<<blocks, 64, smem, st>>>(a, G, chunks);
+    else topk_grad_kernel<DT, 256><<<blocks, 256, smem, st>>>(a, G, chunks);
     return cudaGetLastError();
 }
 
@@ -746,8 +750,8 @@ cudaError_t launch_topk_grad_t(const TopkGradArgs& a, int G, int chunks, cudaStr
 cudaError_t launch_topk_f32(const TopkArgs& a, const TopkPlan& p, cudaStream_t st);
 cudaError_t launch_topk_f16(const TopkArgs& a, const TopkPlan& p, cudaStream_t st);
 cudaError_t launch_topk_bf16(const TopkArgs& a, const TopkPlan& p, cudaStream_t st);
-cudaError_t launch_topk_grad_f32(const TopkGradArgs& a, int G, int chunks, cudaStream_t st);
-cudaError_t launch_topk_grad_f16(const TopkGradArgs& a, int G, int chunks, cudaStream_t st);
-cudaError_t launch_topk_grad_bf16(const TopkGradArgs& a, int G, int chunks, cudaStream_t st);
+cudaError_t launch_topk_grad_f32(const TopkGradArgs& a, int NT, int G, int chunks, cudaStream_t st);
+cudaError_t launch_topk_grad_f16(const TopkGradArgs& a, int NT, int G, int chunks, cudaStream_t st);
+cudaError_t launch_topk_grad_bf16(const TopkGradArgs& a, int NT, int G, int chunks, cudaStream_t st);
 
 }  // namespace sot
