@@ -28,8 +28,9 @@ void topk_plan(bool whole, const TopkArgs& a, int sms, TopkPlan* p) {
     // (a slice's chunk maxima have to fit shared memory)
     while (CL < ROW_MAX_CL && total > CL * 262144ll) CL *= 2;
     const long long G = (total + CL - 1) / CL;
-    // Chunks of eight granules where that leaves twice as many chunks as alternatives, otherwise single ones.
-    p->U = G >= 16ll * a.K || G > 16384 ? 8 : 1;
+    // Chunks of a batch of granules where that leaves twice as many chunks as alternatives, otherwise single ones.
+    const int batch = p->NT == 32 ? BATCH_OF<32> : BATCH_OF<256>;
+    p->U = G >= 2ll * batch * a.K || G > 16384 ? batch : 1;
     p->L.CL = CL;
     p->L.G = (int)G;
     p->L.chunks = a.K ? (int)((G + p->U * p->NT - 1) / (p->U * p->NT)) * p->NT : 0;

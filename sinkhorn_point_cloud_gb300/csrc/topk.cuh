@@ -149,6 +149,10 @@ struct SelectSmem {
 // (a CTA for each warp would leave an SM with seven of them at a time).
 template <int NT>
 constexpr int TEAMS = NT == 32 ? 8 : 1;
+// Granules of a thread that are under way together; a chunk is as many, or one.  (A warp with a row of its own: four, for more
+// warps on an SM: 16384 x 2048 bf16 and K = 8 take 37 us, with eight 43.)
+template <int NT>
+constexpr int BATCH_OF = NT == 32 ? 4 : 8;
 template <int NT>
 __device__ __forceinline__ int team_tid() {
     return NT == 32 ? threadIdx.x & 31 : threadIdx.x;
@@ -435,9 +439,9 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
 
 // A row a team, or a cluster's CTAs a slice of it each.
 template <int DT, int NT, int U>
-__global__ void __launch_bounds__(NT * TEAMS<NT>, NT == 32 ? 3 : 1024 / NT) topk_kernel(const TopkArgs a, const TopkLaunch L) {
+__global__ void __launch_bounds__(NT * TEAMS<NT>, NT == 32 ? 4 : 1024 / NT) topk_kernel(const TopkArgs a, const TopkLaunch L) {
     using T = typename Elem<DT>::T;
-    constexpr int N = Elem<DT>::N, P = 8, NW = NT / 32;
+    constexpr int N = Elem<DT>::N, P = BATCH_OF<NT>, NW = NT / 32;
     extern __shared__ __align__(16) unsigned char dyn[];
     __shared__ SelectSmem<NT> select[TEAMS<NT>];
     __shared__ MSA rec[NW];
@@ -730,7 +734,7 @@ struct TopkPlan {
 
 template <int DT, int NT>
 cudaError_t launch_topk_u(const TopkArgs& a, const TopkPlan& p, cudaStream_t st) {
-    return p.U == 1 ? launch_topk_n<DT, NT, 1>(a, p.L, st) : launch_topk_n<DT, NT, 8>(a, p.L, st);
+    return p.U == 1 ? launch_topk_n<DT, NT, 1>(a, p.L, st) : launch_topk_n<DT, NT, BATCH_OF<NT>>(a, p.L, st);
 }
 template <int DT>
 cudaError_t launch_topk_t(const TopkArgs& a, const TopkPlan& p, cudaStream_t st) {
