@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(NT) routed_scores_kernel(const RoutedArgs a, i
     constexpr int N = Elem<DT>::N;
     __shared__ float2 part[NW];
     __shared__ float plain[NW];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (barrier && blockIdx.x == 0 && threadIdx.x < 4) barrier[threadIdx.x] = 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, splits = NW / tokens;
     const int e = blockIdx.x % a.E, t = blockIdx.x / a.E * tokens + warp / splits, split = warp % splits;

@@ -414,9 +414,14 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         tmem_alloc(smem_u32(slot), cols);
         tmem_relinquish();
     }
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&up) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&down) : "memory");
+    }
     // choose
     for (int i = tid; i < E; i += NT) mask[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores, and the barriers' zeros
     for (int tok = warp; tok < t.r.T; tok += NWARP) {
         int id;
         float w;
@@ -647,7 +652,21 @@ cudaError_t launch_routed_tc(const RoutedArgs& a, const RoutedTcPlan& p, unsigne
     if (e != cudaSuccess) return e;
     void* args[] = {&t, &up, &down};
     count_launches(1);
-    return cudaLaunchCooperativeKernel(kern, dim3(sms), dim3(NT), args, t.L.total, st);
+    // All CTAs wait for one another, so all have to be there; and they may come while the scores are still being
+    // formed, which they wait for before they read them.
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(sms, 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.dynamicSmemBytes = t.L.total;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
 }  // namespace sot
