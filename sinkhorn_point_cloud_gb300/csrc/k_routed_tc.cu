@@ -3,12 +3,12 @@
 // After the scores (k_routed.cu) one cooperative kernel, a CTA an SM, does the rest:
 //   choose  every CTA forms the choice of all tokens and each expert's list of tokens for itself;
 //   up      products gate_up x^T: an expert's rows are the M of a tcgen05.mma (64 gate rows and the 64 up rows that
-//           belong to them), its tokens the N.  The units of all experts (16 KB of weights, K = 64) are dealt out evenly, so a
+//           belong to them), its tokens the N.  The units of all experts (16 KB of weights, K = 64, or twice that) are dealt out evenly, so a
 //           CTA starts and ends inside a tile; it leaves a partial sum for each piece;
 //   act     h = silu(gate) up of the joined pieces, rounded to the type;
 //   down    products down h^T, the same way;
 //   join    the weighted sum over a token's experts.
-// The weights are read once and bound it.  They come by TMA through a ring of stages, 16 KB each, from a warp that waits
+// The weights are read once and bound it.  They come by TMA through a ring of stages, 16 or 32 KB each, from a warp that waits
 // for nothing but free stages: across the phases' grid barriers the next phase's weights are already on their way.
 // Every wait is bounded; one that runs out ends the call with NaN outputs and the timeout status.
 #include <cuda.h>
@@ -22,17 +22,19 @@ namespace sot {
 
 namespace {
 
-constexpr int LOADERS = 8;  // warps that fetch the tokens' side, a unit each in turn
+constexpr int LOADERS = 8;  // warps that fetch the tokens' side, a unit each in turn (as many of them as the ring has stages)
 constexpr int NWARP = 6 + LOADERS, NT = NWARP * 32;
 constexpr int W_PRODUCER = 0, W_MMA = 1, W_EPI = 2, W_LOAD = 6;  // first warps of each role (4 in the epilogue)
 constexpr int WORKERS = (4 + LOADERS) * 32;                      // threads of the last two
-constexpr int KSTEP = 64, A_BYTES = 128 * KSTEP * 2;
-constexpr int MIN_STAGES = 3, MAX_STAGES = 12;
+constexpr int KSTEP = 64, A_BYTES = 128 * KSTEP * 2;  // columns of a swizzled row (128 bytes), 128 rows of them
+constexpr int MIN_STAGES = 3, MAX_STAGES = 12, HEAD = 2;
 constexpr unsigned long long WAIT_NS = 2000000000ull;
 constexpr int PHASES = 2;  // 0: up, 1: down
 
 struct Layout {  // byte offsets in dynamic shared memory (from a 1024-byte boundary)
     int stage, stages, npad;
+    int wide;  // slices of KSTEP columns in a unit: two where the tokens' side leaves room (a unit costs the multiplying
+               // thread 250 ns whatever its width), else one
     int bars, weight, toks, list, act, id, info, mask, total;
 };
 
@@ -135,24 +137,27 @@ __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
 
 __device__ void produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, const CUtensorMap* down) {
     const uint64_t policy = policy_drop();
-    const int stages = c.S, stage = t.L.stage;
+    const int stages = c.S, stage = t.L.stage, wide = t.L.wide, step = wide * KSTEP;
     Turn at;
     int issued = 0;
-    // The loading warps' first requests go out first: behind a ring of weights they take 5 us instead of 1.
-    bool ok = mbar_wait_bounded(c.go(), 0, c.abort, WAIT_NS);
+    bool ok = true;
     for (int ph = 0; ok && ph < PHASES; ++ph) {
         const CUtensorMap* const map = ph ? down : up;
         for (int u = c.first[ph]; ok && u < c.end[ph];) {
             const Piece p = piece_at(c, ph, u);
             const int a = p.job / c.tiles[ph], tile = p.job - a * c.tiles[ph], e = c.info[a].expert;
             const int r0 = ph ? e * t.r.H + tile * 128 : e * 2 * t.r.F + tile * 64, r1 = ph ? r0 + 64 : r0 + t.r.F;
-            for (int k = p.ks * KSTEP, end = k + p.n * KSTEP; k < end; k += KSTEP) {
-                ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
+            for (int k = p.ks * step, end = k + p.n * step; k < end; k += step) {
+                // The loading warps' first requests go out before most of the ring's: behind all of it they take 5 us.
+                if (issued == HEAD) ok = mbar_wait_bounded(c.go(), 0, c.abort, WAIT_NS);
+                ok = ok && mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
                 if (!ok) break;
                 const uint32_t full = c.full(at.s), dst = c.base + at.s * stage;
-                mbar_arrive_expect_tx(full, A_BYTES);
-                tma_rows(dst, map, k, r0, full, policy);
-                tma_rows(dst + A_BYTES / 2, map, k, r1, full, policy);
+                mbar_arrive_expect_tx(full, wide * A_BYTES);
+                for (int i = 0; i < wide; ++i) {  // (columns past the matrix's last one come as zeros)
+                    tma_rows(dst + i * A_BYTES, map, k + i * KSTEP, r0, full, policy);
+                    tma_rows(dst + i * A_BYTES + A_BYTES / 2, map, k + i * KSTEP, r1, full, policy);
+                }
                 at.next(stages);
                 ++issued;
             }
@@ -176,6 +181,8 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
     constexpr uint32_t format = DT == SOT_BF16 ? (1u << 7) | (1u << 10) : 0u;
     const int stages = c.S;
     const uint64_t a0 = sw128_desc(c.base), step = t.L.stage >> 4;
+    const int wide = t.L.wide;
+    const uint64_t tokens = wide * A_BYTES >> 4, slice = t.L.npad * KSTEP * 2 >> 4;
     Turn at;
     int seg = 0;
     bool ok = true, issued = false;
@@ -191,11 +198,15 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t a = a0 + at.s * step, b = a + (A_BYTES >> 4);
+                const uint64_t a = a0 + at.s * step, b = a + tokens;
                 if (elect_one()) {
-                    tc_mma_f16(d, a, b, idesc, i > 0);
 #pragma unroll
-                    for (int k = 1; k < KSTEP / 16; ++k) tc_mma_f16(d, a + 2 * k, b + 2 * k, idesc, 1u);
+                    for (int k = 0; k < KSTEP / 16; ++k) tc_mma_f16(d, a + 2 * k, b + 2 * k, idesc, i > 0 || k > 0);
+                    if (wide == 2) {
+#pragma unroll
+                        for (int k = 0; k < KSTEP / 16; ++k)
+                            tc_mma_f16(d, a + (A_BYTES >> 4) + 2 * k, b + slice + 2 * k, idesc, 1u);
+                    }
                     tc_commit(c.empty(at.s));
                     if (i == p.n - 1) tc_commit(c.accfull(seg & 1));
                 }
@@ -215,25 +226,36 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
 // The tokens' side of a phase: rows of x or h, swizzled as the tensor cores read them.  A row past the expert's
 // last token is not written: what it holds only reaches columns that nobody reads.
 __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int& turn) {
-    const int lane = threadIdx.x & 31, ch = lane & 7, stages = c.S, stage = t.L.stage;
+    const int lane = threadIdx.x & 31, ch = lane & 7, stages = c.S, stage = t.L.stage, wide = t.L.wide;
     const int K = ph ? t.r.F : t.r.H;
     const long long ld = ph ? t.r.F : t.r.ldx;
     const unsigned short* const from = static_cast<const unsigned short*>(ph ? t.h : t.r.x) + ch * 8;
     const unsigned short* const rows = ph ? c.list : c.toks;
+    // A warp's next unit must not lie more than a ring ahead of its last one: further on, the parity it waits for
+    // could be that of the use before the last, and the place still taken.
+    const int loaders = min(LOADERS, stages);
     bool first = ph == 0;
+    if ((threadIdx.x >> 5) - W_LOAD >= loaders) {
+        if (first && lane == 0) mbar_arrive(c.go());
+        return true;
+    }
     for (int u = c.first[ph]; u < c.end[ph];) {
         const Piece p = piece_at(c, ph, u);
         const Info e = c.info[p.job / c.tiles[ph]];
         // turn: units until this warp's next one, whose place in the ring is `at`
-        for (; turn < p.n; turn += LOADERS) {
-            const int k0 = (p.ks + turn) * KSTEP;
+        for (; turn < p.n; turn += loaders) {
+            const int k0 = (p.ks + turn) * wide * KSTEP;
             const bool ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
             if (!__all_sync(0xffffffffu, ok)) return false;
-            const uint32_t dst = c.base + at.s * stage + A_BYTES;
-            const bool real = k0 + ch * 8 < K;
+            const uint32_t dst = c.base + at.s * stage + wide * A_BYTES, slice = t.L.npad * KSTEP * 2;
             for (int row = lane >> 3; row < e.n; row += 4) {
                 const unsigned short* const src = from + rows[e.start + row] * ld;
-                copy16(dst + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4), real ? src + k0 : src, real ? 16 : 0);
+                const uint32_t to = dst + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4);
+                for (int i = 0; i < wide; ++i) {
+                    const int k = k0 + i * KSTEP;
+                    const bool real = k + ch * 8 < K;
+                    copy16(to + i * slice, real ? src + k : src, real ? 16 : 0);
+                }
             }
             if (first && lane == 0) mbar_arrive(c.go());
             first = false;
@@ -241,7 +263,7 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(c.full(at.s));
-            at.skip(LOADERS, stages);
+            at.skip(loaders, stages);
         }
         turn -= p.n;
         u += p.n;
@@ -493,7 +515,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     c.tiles[0] = (t.r.F + 63) / 64;
     c.tiles[1] = (t.r.H + 127) / 128;
     for (int ph = 0; ph < PHASES; ++ph) {
-        c.KS[ph] = (dims[ph] + KSTEP - 1) / KSTEP;
+        c.KS[ph] = (dims[ph] + t.L.wide * KSTEP - 1) / (t.L.wide * KSTEP);
         const int U = c.active * c.tiles[ph] * c.KS[ph];
         // An even share each, but not so small that a tile has more pieces than there is room for.
         c.chunk[ph] = max(1, max((U + (int)gridDim.x - 1) / (int)gridDim.x,
@@ -581,7 +603,8 @@ Layout layout(const RoutedArgs& a) {
         return here;
     };
     L.npad = (a.T + 15) / 16 * 16;
-    L.stage = A_BYTES + (L.npad * KSTEP * 2 + 1023) / 1024 * 1024;
+    L.wide = L.npad <= 64 ? 2 : 1;
+    L.stage = L.wide * (A_BYTES + L.npad * KSTEP * 2);
     const int other = (BAR_BYTES + 15) / 16 * 16 + (4 * P + 15) / 16 * 16 + 4 * ((2 * P + 15) / 16 * 16) +
                       ((int)sizeof(Info) * a.E + 15) / 16 * 16 + 16 * a.E;
     L.stages = (MAX_SMEM - 1024 - other) / L.stage;
@@ -601,7 +624,7 @@ Layout layout(const RoutedArgs& a) {
 
 // Pieces of a tile that there is room for: those an even share leaves where the tokens choose no more than K experts.
 int pieces(const RoutedArgs& a, int ph, int sms) {
-    const int KS = ((ph ? a.F : a.H) + KSTEP - 1) / KSTEP, tiles = ph ? (a.H + 127) / 128 : (a.F + 63) / 64;
+    const int step = layout(a).wide * KSTEP, KS = ((ph ? a.F : a.H) + step - 1) / step, tiles = ph ? (a.H + 127) / 128 : (a.F + 63) / 64;
     const int p = (sms + tiles * a.K - 1) / (tiles * a.K) + 1;
     return p < KS ? p : KS;
 }
