@@ -27,9 +27,10 @@ constexpr int NWARP = 6 + LOADERS, NT = NWARP * 32;
 constexpr int W_PRODUCER = 0, W_MMA = 1, W_EPI = 2, W_LOAD = 6;  // first warps of each role (4 in the epilogue)
 constexpr int WORKERS = (4 + LOADERS) * 32;                      // threads of the last two
 constexpr int KSTEP = 64, A_BYTES = 128 * KSTEP * 2;  // columns of a swizzled row (128 bytes), 128 rows of them
-constexpr int MIN_STAGES = 3, MAX_STAGES = 12, HEAD = 2;
+constexpr int MIN_STAGES = 3, MAX_STAGES = 12, HEAD = 3;
 constexpr unsigned long long WAIT_NS = 2000000000ull;
 constexpr int PHASES = 2;  // 0: up, 1: down
+constexpr int FUSED_PAIRS = 16;
 
 struct Layout {  // byte offsets in dynamic shared memory (from a 1024-byte boundary)
     int stage, stages, npad;
@@ -46,6 +47,7 @@ struct TcArgs {
     float* part[PHASES];  // [pieces][T K][2 F or H]
     void* h;              // [T K][F]
     int pieces[PHASES];   // of a tile, at most
+    bool fused;           // the loading warps form h
 };
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int k, int row, uint32_t bar, uint64_t policy) {
@@ -223,8 +225,74 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
     }
 }
 
+__device__ __forceinline__ float silu_times(float gate, float up) { return gate / (1.f + expf(-gate)) * up; }
+
+// Pieces of a tile: the CTAs that have units of it.
+__device__ __forceinline__ int pieces_of(const Ctx& c, int ph, int job) {
+    const int u = job * c.KS[ph];
+    return (u + c.KS[ph] - 1) / c.chunk[ph] - u / c.chunk[ph] + 1;
+}
+
+template <int DT>
+__device__ void activate(const Ctx& c, const TcArgs& t) {
+    using T = typename Elem<DT>::T;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - W_EPI, tiles = c.tiles[0], F = t.r.F;
+    for (int i = blockIdx.x + w * gridDim.x; i < c.P * tiles; i += gridDim.x * (WORKERS / 32)) {
+        const int p = i / tiles, tile = i - p * tiles, f = tile * 64 + lane * 2;
+        if (c.id[p] < 0 || f >= F) continue;
+        const int n = pieces_of(c, 0, c.act[p] * tiles + tile);
+        float2 g = make_float2(0.f, 0.f), u = g;
+        const float* from = t.part[0] + (long long)p * 2 * F + f;
+        for (int k = 0; k < n; ++k, from += (long long)c.P * 2 * F) {
+            g = fadd2(g, __ldcg(reinterpret_cast<const float2*>(from)));
+            u = fadd2(u, __ldcg(reinterpret_cast<const float2*>(from + F)));
+        }
+        T* const to = static_cast<T*>(t.h) + (long long)p * F + f;
+        to[0] = Elem<DT>::put(silu_times(g.x, u.x));
+        to[1] = Elem<DT>::put(silu_times(g.y, u.y));
+    }
+}
+
+// For few tokens the loading warps do that for themselves, each unit's columns as it is loaded: every tile of an expert
+// does it again, but there is no phase of its own and no barrier behind it
+// (H = 2048, F = 1024, 8 of 64 experts: one token 31.4 us, else 33.7; two 44.6, else 45.7; four 71.9, else 71.0).
+// 64 columns from k on of pair p's h, for the swizzled row at `row` of a slice at `dst`: four columns a lane, 16 lanes a slice.
+template <int DT>
+__device__ __forceinline__ void activate_into(const Ctx& c, const TcArgs& t, uint32_t dst, int row, int p, int expert, int k0) {
+    constexpr int MOST = 3;  // pieces fetched together
+    const int lane = threadIdx.x & 31, F = t.r.F;
+    const int slice = lane >> 4, k = k0 + lane * 4, tile = k >> 6;
+    if (slice >= t.L.wide) return;
+    float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
+    const bool real = k < F;
+    const int n = real ? pieces_of(c, 0, expert * c.tiles[0] + tile) : 0;
+    const float* const from = t.part[0] + (long long)p * 2 * F + (real ? k : 0);
+    const long long step = (long long)c.P * 2 * F;
+    for (int j0 = 0; j0 < n; j0 += MOST) {
+        float4 a[MOST], b[MOST];
+#pragma unroll
+        for (int j = 0; j < MOST; ++j) {  // (a piece that is not there: the last one again, not added)
+            const float* const at = from + min(j0 + j, n - 1) * step;
+            a[j] = __ldcg(reinterpret_cast<const float4*>(at));
+            b[j] = __ldcg(reinterpret_cast<const float4*>(at + F));
+        }
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            if (j0 + j < n) {
+                g = make_float4(g.x + a[j].x, g.y + a[j].y, g.z + a[j].z, g.w + a[j].w);
+                u = make_float4(u.x + b[j].x, u.y + b[j].y, u.z + b[j].z, u.w + b[j].w);
+            }
+    }
+    const float2 f[Elem<DT>::N / 2] = {{silu_times(g.x, u.x), silu_times(g.y, u.y)}, {silu_times(g.z, u.z), silu_times(g.w, u.w)}};
+    const uint4 v = pack<DT>(f);
+    const int ch = lane >> 1 & 7;
+    const uint32_t to = dst + slice * t.L.npad * KSTEP * 2 + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4) + (lane & 1) * 8;
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(v.x), "r"(v.y) : "memory");
+}
+
 // The tokens' side of a phase: rows of x or h, swizzled as the tensor cores read them.  A row past the expert's
 // last token is not written: what it holds only reaches columns that nobody reads.
+template <int DT>
 __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int& turn) {
     const int lane = threadIdx.x & 31, ch = lane & 7, stages = c.S, stage = t.L.stage, wide = t.L.wide;
     const int K = ph ? t.r.F : t.r.H;
@@ -241,14 +309,18 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
     }
     for (int u = c.first[ph]; u < c.end[ph];) {
         const Piece p = piece_at(c, ph, u);
-        const Info e = c.info[p.job / c.tiles[ph]];
+        const int place = p.job / c.tiles[ph];
+        const Info e = c.info[place];
         // turn: units until this warp's next one, whose place in the ring is `at`
         for (; turn < p.n; turn += loaders) {
             const int k0 = (p.ks + turn) * wide * KSTEP;
             const bool ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
             if (!__all_sync(0xffffffffu, ok)) return false;
             const uint32_t dst = c.base + at.s * stage + wide * A_BYTES, slice = t.L.npad * KSTEP * 2;
-            for (int row = lane >> 3; row < e.n; row += 4) {
+            if (ph && t.fused)
+                for (int row = 0; row < e.n; ++row) activate_into<DT>(c, t, dst, row, rows[e.start + row], place, k0);
+            else
+              for (int row = lane >> 3; row < e.n; row += 4) {
                 const unsigned short* const src = from + rows[e.start + row] * ld;
                 const uint32_t to = dst + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4);
                 for (int i = 0; i < wide; ++i) {
@@ -321,32 +393,6 @@ __device__ bool grid_barrier(const Ctx& c, const TcArgs& t, int which) {
     }
     worker_sync();
     return !*c.abort;
-}
-
-// Pieces of a tile: the CTAs that have units of it.
-__device__ __forceinline__ int pieces_of(const Ctx& c, int ph, int job) {
-    const int u = job * c.KS[ph];
-    return (u + c.KS[ph] - 1) / c.chunk[ph] - u / c.chunk[ph] + 1;
-}
-
-template <int DT>
-__device__ void activate(const Ctx& c, const TcArgs& t) {
-    using T = typename Elem<DT>::T;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - W_EPI, tiles = c.tiles[0], F = t.r.F;
-    for (int i = blockIdx.x + w * gridDim.x; i < c.P * tiles; i += gridDim.x * (WORKERS / 32)) {
-        const int p = i / tiles, tile = i - p * tiles, f = tile * 64 + lane * 2;
-        if (c.id[p] < 0 || f >= F) continue;
-        const int n = pieces_of(c, 0, c.act[p] * tiles + tile);
-        float2 g = make_float2(0.f, 0.f), u = g;
-        const float* from = t.part[0] + (long long)p * 2 * F + f;
-        for (int k = 0; k < n; ++k, from += (long long)c.P * 2 * F) {
-            g = fadd2(g, __ldcg(reinterpret_cast<const float2*>(from)));
-            u = fadd2(u, __ldcg(reinterpret_cast<const float2*>(from + F)));
-        }
-        T* const to = static_cast<T*>(t.h) + (long long)p * F + f;
-        to[0] = Elem<DT>::put(g.x / (1.f + expf(-g.x)) * u.x);
-        to[1] = Elem<DT>::put(g.y / (1.f + expf(-g.y)) * u.y);
-    }
 }
 
 // A warp takes 32 columns of a token: four lanes share four columns and take a quarter of the experts each.
@@ -538,14 +584,16 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         if (warp < W_LOAD) store_pieces(c, t, 0, seg, tmem);
         else {
             at.skip(turn, c.S);
-            load_tokens(c, t, 0, at, turn);
+            load_tokens<DT>(c, t, 0, at, turn);
         }
         bool ok = grid_barrier(c, t, 0);
-        if (ok) activate<DT>(c, t);
-        if (ok) ok = grid_barrier(c, t, 1);
+        if (ok && !t.fused) {
+            activate<DT>(c, t);
+            ok = grid_barrier(c, t, 1);
+        }
         if (ok) {
             if (warp < W_LOAD) store_pieces(c, t, 1, seg, tmem);
-            else load_tokens(c, t, 1, at, turn);
+            else load_tokens<DT>(c, t, 1, at, turn);
             ok = grid_barrier(c, t, 2);
         }
         if (ok) join<DT>(c, t);
@@ -664,6 +712,7 @@ cudaError_t launch_routed_tc(const RoutedArgs& a, const RoutedTcPlan& p, unsigne
     t.part[1] = reinterpret_cast<float*>(scratch + p.down_at);
     t.h = scratch + p.h_at;
     for (int ph = 0; ph < PHASES; ++ph) t.pieces[ph] = pieces(a, ph, sms);
+    t.fused = a.T * a.K <= FUSED_PAIRS;
     cudaError_t e = async_status_address(&t.status);
     if (e != cudaSuccess) return e;
     CUtensorMap up, down;
