@@ -32,11 +32,21 @@ constexpr unsigned long long WAIT_NS = 2000000000ull;
 constexpr int PHASES = 2;  // 0: up, 1: down
 constexpr int FUSED_PAIRS = 16;
 
-struct Layout {  // byte offsets in dynamic shared memory (from a 1024-byte boundary)
-    int stage, stages, npad;
-    int wide;  // slices of KSTEP columns in a unit: two where the tokens' side leaves room (a unit costs the multiplying
-               // thread 250 ns whatever its width), else one
+struct Layout {  // byte offsets in dynamic shared memory (from a 1024-byte boundary, where the ring is)
+    int ring, most;  // bytes of the ring; tokens that an expert may have, in sixteens
     int bars, weight, toks, list, act, id, info, mask, total;
+};
+// How the ring is cut for experts of at most npad tokens.
+struct Cut {
+    int npad, wide;  // wide: slices of KSTEP columns in a unit: two where that leaves four stages (a unit costs the
+                     // multiplying thread 250 ns whatever its width), else one
+    int stage, stages;
+    __host__ __device__ Cut(int npad_, int ring) : npad(npad_) {
+        wide = 4 * 2 * (A_BYTES + npad * KSTEP * 2) <= ring ? 2 : 1;
+        stage = wide * (A_BYTES + npad * KSTEP * 2);
+        stages = ring / stage;
+        if (stages > MAX_STAGES) stages = MAX_STAGES;
+    }
 };
 
 struct TcArgs {
@@ -98,7 +108,7 @@ struct Ctx {
     int KS[PHASES], tiles[PHASES];
     int chunk[PHASES];  // units of a CTA
     int first[PHASES], end[PHASES];
-    int S;
+    int npad, wide, stage, S;  // the ring's cut
     __device__ __forceinline__ uint32_t full(int s) const { return bars + 8 * s; }
     __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8 * (MAX_STAGES + s); }
     __device__ __forceinline__ uint32_t accfull(int b) const { return bars + 8 * (2 * MAX_STAGES + b); }
@@ -139,7 +149,7 @@ __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
 
 __device__ void produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, const CUtensorMap* down) {
     const uint64_t policy = policy_drop();
-    const int stages = c.S, stage = t.L.stage, wide = t.L.wide, step = wide * KSTEP;
+    const int stages = c.S, stage = c.stage, wide = c.wide, step = wide * KSTEP;
     Turn at;
     int issued = 0;
     bool ok = true;
@@ -182,9 +192,9 @@ template <int DT>
 __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
     constexpr uint32_t format = DT == SOT_BF16 ? (1u << 7) | (1u << 10) : 0u;
     const int stages = c.S;
-    const uint64_t a0 = sw128_desc(c.base), step = t.L.stage >> 4;
-    const int wide = t.L.wide;
-    const uint64_t tokens = wide * A_BYTES >> 4, slice = t.L.npad * KSTEP * 2 >> 4;
+    const uint64_t a0 = sw128_desc(c.base), step = c.stage >> 4;
+    const int wide = c.wide;
+    const uint64_t tokens = wide * A_BYTES >> 4, slice = c.npad * KSTEP * 2 >> 4;
     Turn at;
     int seg = 0;
     bool ok = true, issued = false;
@@ -192,7 +202,7 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
         for (int u = c.first[ph]; ok && u < c.end[ph]; ++seg) {
             const Piece p = piece_at(c, ph, u);
             const uint32_t idesc = f16_idesc(128, pad16(c.info[p.job / c.tiles[ph]].n)) | format;
-            const uint32_t d = tmem + (seg & 1) * t.L.npad;
+            const uint32_t d = tmem + (seg & 1) * c.npad;
             ok = mbar_wait_bounded(c.accempty(seg & 1), ((seg >> 1) & 1) ^ 1, c.abort, WAIT_NS);
             ok = __all_sync(0xffffffffu, ok);
             for (int i = 0; ok && i < p.n; ++i) {
@@ -262,7 +272,7 @@ __device__ __forceinline__ void activate_into(const Ctx& c, const TcArgs& t, uin
     constexpr int MOST = 3;  // pieces fetched together
     const int lane = threadIdx.x & 31, F = t.r.F;
     const int slice = lane >> 4, k = k0 + lane * 4, tile = k >> 6;
-    if (slice >= t.L.wide) return;
+    if (slice >= c.wide) return;
     float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
     const bool real = k < F;
     const int n = real ? pieces_of(c, 0, expert * c.tiles[0] + tile) : 0;
@@ -286,7 +296,7 @@ __device__ __forceinline__ void activate_into(const Ctx& c, const TcArgs& t, uin
     const float2 f[Elem<DT>::N / 2] = {{silu_times(g.x, u.x), silu_times(g.y, u.y)}, {silu_times(g.z, u.z), silu_times(g.w, u.w)}};
     const uint4 v = pack<DT>(f);
     const int ch = lane >> 1 & 7;
-    const uint32_t to = dst + slice * t.L.npad * KSTEP * 2 + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4) + (lane & 1) * 8;
+    const uint32_t to = dst + slice * c.npad * KSTEP * 2 + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4) + (lane & 1) * 8;
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(v.x), "r"(v.y) : "memory");
 }
 
@@ -294,7 +304,7 @@ __device__ __forceinline__ void activate_into(const Ctx& c, const TcArgs& t, uin
 // last token is not written: what it holds only reaches columns that nobody reads.
 template <int DT>
 __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int& turn) {
-    const int lane = threadIdx.x & 31, ch = lane & 7, stages = c.S, stage = t.L.stage, wide = t.L.wide;
+    const int lane = threadIdx.x & 31, ch = lane & 7, stages = c.S, stage = c.stage, wide = c.wide;
     const int K = ph ? t.r.F : t.r.H;
     const long long ld = ph ? t.r.F : t.r.ldx;
     const unsigned short* const from = static_cast<const unsigned short*>(ph ? t.h : t.r.x) + ch * 8;
@@ -316,7 +326,7 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
             const int k0 = (p.ks + turn) * wide * KSTEP;
             const bool ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
             if (!__all_sync(0xffffffffu, ok)) return false;
-            const uint32_t dst = c.base + at.s * stage + wide * A_BYTES, slice = t.L.npad * KSTEP * 2;
+            const uint32_t dst = c.base + at.s * stage + wide * A_BYTES, slice = c.npad * KSTEP * 2;
             if (ph && t.fused)
                 for (int row = 0; row < e.n; ++row) activate_into<DT>(c, t, dst, row, rows[e.start + row], place, k0);
             else
@@ -359,7 +369,7 @@ __device__ bool store_pieces(const Ctx& c, const TcArgs& t, int ph, int& seg, ui
         bool ok = mbar_wait_bounded(c.accfull(seg & 1), (seg >> 1) & 1, c.abort, WAIT_NS);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
-        const uint32_t from = tmem + (seg & 1) * t.L.npad + ((uint32_t)(q * 32) << 16);
+        const uint32_t from = tmem + (seg & 1) * c.npad + ((uint32_t)(q * 32) << 16);
         for (int n0 = 0; n0 < e.n; n0 += 16) {
             float v[16];
             tmem_ld16(from + n0, v);
@@ -459,11 +469,10 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     c.id = reinterpret_cast<short*>(c.sm + t.L.id);
     c.info = reinterpret_cast<Info*>(c.sm + t.L.info);
     uint4* const mask = reinterpret_cast<uint4*>(c.sm + t.L.mask);  // the tokens of each expert
-    c.S = t.L.stages;
     c.P = t.r.T * t.r.K;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = t.r.E, K = t.r.K;
     if (tid == 0) {
-        for (int s = 0; s < c.S; ++s) {
+        for (int s = 0; s < MAX_STAGES; ++s) {
             mbar_init(c.full(s), 2);  // the producer's arrival and a loading warp's
             mbar_init(c.empty(s), 1);
         }
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         *c.abort = 0;
     }
     int cols = 32;
-    while (cols < 2 * t.L.npad) cols *= 2;
+    while (cols < 2 * t.L.most) cols *= 2;
     if (warp == W_MMA) {
         tmem_alloc(smem_u32(slot), cols);
         tmem_relinquish();
@@ -508,7 +517,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     __syncthreads();
     // The experts in use, in order, and where their lists start: a thread four experts.
     constexpr int PER = (ROUTED_MAX_E + NT - 1) / NT;
-    int used = 0, tokens = 0, n[PER];
+    int used = 0, tokens = 0, most = 0, n[PER];
     uint4 m[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
@@ -516,6 +525,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         n[j] = __popc(m[j].x) + __popc(m[j].y) + __popc(m[j].z) + __popc(m[j].w);
         used += n[j] > 0;
         tokens += n[j];
+        most = max(most, n[j]);
     }
     int before = used | tokens << 16;  // (at most 1024 and 4096)
 #pragma unroll
@@ -523,14 +533,24 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         const int v = __shfl_up_sync(0xffffffffu, before, o);
         if (lane >= o) before += v;
     }
-    if (lane == 31) counts[0][warp] = before;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 31) {
+        counts[0][warp] = before;
+        counts[1][warp] = most;
+    }
     __syncthreads();
     int at = before - (used | tokens << 16), all = 0;
 #pragma unroll
     for (int w = 0; w < NWARP; ++w) {
         if (w < warp) at += counts[0][w];
         all += counts[0][w];
+        most = max(most, counts[1][w]);
     }
+    const Cut cut(max(16, pad16(most)), t.L.ring);
+    c.npad = cut.npad;
+    c.wide = cut.wide;
+    c.stage = cut.stage;
+    c.S = cut.stages;
     c.active = all & 0xffff;
     int a = at & 0xffff, start = at >> 16;
 #pragma unroll
@@ -561,7 +581,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     c.tiles[0] = (t.r.F + 63) / 64;
     c.tiles[1] = (t.r.H + 127) / 128;
     for (int ph = 0; ph < PHASES; ++ph) {
-        c.KS[ph] = (dims[ph] + t.L.wide * KSTEP - 1) / (t.L.wide * KSTEP);
+        c.KS[ph] = (dims[ph] + c.wide * KSTEP - 1) / (c.wide * KSTEP);
         const int U = c.active * c.tiles[ph] * c.KS[ph];
         // An even share each, but not so small that a tile has more pieces than there is room for.
         c.chunk[ph] = max(1, max((U + (int)gridDim.x - 1) / (int)gridDim.x,
@@ -650,14 +670,11 @@ Layout layout(const RoutedArgs& a) {
         at = (at + bytes + 15) / 16 * 16;
         return here;
     };
-    L.npad = (a.T + 15) / 16 * 16;
-    L.wide = L.npad <= 64 ? 2 : 1;
-    L.stage = L.wide * (A_BYTES + L.npad * KSTEP * 2);
+    L.most = (a.T + 15) / 16 * 16;
     const int other = (BAR_BYTES + 15) / 16 * 16 + (4 * P + 15) / 16 * 16 + 4 * ((2 * P + 15) / 16 * 16) +
                       ((int)sizeof(Info) * a.E + 15) / 16 * 16 + 16 * a.E;
-    L.stages = (MAX_SMEM - 1024 - other) / L.stage;
-    if (L.stages > MAX_STAGES) L.stages = MAX_STAGES;
-    place(L.stages * L.stage);
+    L.ring = (MAX_SMEM - 1024 - other) / 1024 * 1024;
+    place(L.ring);
     L.bars = place(BAR_BYTES);
     L.weight = place(4 * P);
     L.toks = place(2 * P);
@@ -672,7 +689,7 @@ Layout layout(const RoutedArgs& a) {
 
 // Pieces of a tile that there is room for: those an even share leaves where the tokens choose no more than K experts.
 int pieces(const RoutedArgs& a, int ph, int sms) {
-    const int step = layout(a).wide * KSTEP, KS = ((ph ? a.F : a.H) + step - 1) / step, tiles = ph ? (a.H + 127) / 128 : (a.F + 63) / 64;
+    const int KS = ((ph ? a.F : a.H) + KSTEP - 1) / KSTEP, tiles = ph ? (a.H + 127) / 128 : (a.F + 63) / 64;
     const int p = (sms + tiles * a.K - 1) / (tiles * a.K) + 1;
     return p < KS ? p : KS;
 }
@@ -685,7 +702,7 @@ bool routed_tc_fits(const RoutedArgs& a) {
            (long long)a.E * 2 * a.F < 1ll << 31 && (long long)a.E * a.H < 1ll << 31 &&
            // (units are counted in 32 bits)
            (long long)a.E * ((a.F + 63) / 64) * ((a.H + 63) / 64) < 1ll << 30 &&
-           (long long)a.E * ((a.H + 127) / 128) * ((a.F + 63) / 64) < 1ll << 30 && layout(a).stages >= MIN_STAGES;
+           (long long)a.E * ((a.H + 127) / 128) * ((a.F + 63) / 64) < 1ll << 30 && Cut(layout(a).most, layout(a).ring).stages >= MIN_STAGES;
 }
 
 RoutedTcPlan routed_tc_plan(const RoutedArgs& a, int sms) {
