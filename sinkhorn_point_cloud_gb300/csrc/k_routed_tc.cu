@@ -34,7 +34,7 @@ constexpr int FUSED_PAIRS = 16;
 
 struct Layout {  // byte offsets in dynamic shared memory (from a 1024-byte boundary, where the ring is)
     int ring, most;  // bytes of the ring; tokens that an expert may have, in sixteens
-    int bars, weight, toks, list, act, id, info, mask, total;
+    int bars, weight, toks, list, act, id, info, mask, place, total;
 };
 // How the ring is cut for experts of at most npad tokens.
 struct Cut {
@@ -243,23 +243,65 @@ __device__ __forceinline__ int pieces_of(const Ctx& c, int ph, int job) {
     return (u + c.KS[ph] - 1) / c.chunk[ph] - u / c.chunk[ph] + 1;
 }
 
+// Four columns of the pieces of a tile: three are fetched before the first is added, and before other tiles' are.
+struct Pieces {
+    static constexpr int MOST = 3;
+    const float* from;
+    long long step;
+    int n;
+    float4 v[MOST];
+    __device__ __forceinline__ void fetch(const float* from_, long long step_, int n_) {
+        from = from_;
+        step = step_;
+        n = n_;
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)  // (a piece that is not there: another one again, not added)
+            v[j] = __ldcg(reinterpret_cast<const float4*>(from + max(0, min(j, n - 1)) * step));
+    }
+    __device__ __forceinline__ float4 sum() const {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        const auto add = [&](const float4& a) { s = make_float4(s.x + a.x, s.y + a.y, s.z + a.z, s.w + a.w); };
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            if (j < n) add(v[j]);
+#pragma unroll 1
+        for (int j = MOST; j < n; ++j) add(__ldcg(reinterpret_cast<const float4*>(from + j * step)));
+        return s;
+    }
+};
+template <int DT>
+__device__ __forceinline__ uint2 activated(const Pieces& gate, const Pieces& up) {
+    const float4 g = gate.sum(), u = up.sum();
+    const float2 f[Elem<DT>::N / 2] = {{silu_times(g.x, u.x), silu_times(g.y, u.y)}, {silu_times(g.z, u.z), silu_times(g.w, u.w)}};
+    const uint4 v = pack<DT>(f);
+    return make_uint2(v.x, v.y);
+}
+
+// A half-warp takes 64 columns of a pair, two at a time.
 template <int DT>
 __device__ void activate(const Ctx& c, const TcArgs& t) {
-    using T = typename Elem<DT>::T;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - W_EPI, tiles = c.tiles[0], F = t.r.F;
-    for (int i = blockIdx.x + w * gridDim.x; i < c.P * tiles; i += gridDim.x * (WORKERS / 32)) {
-        const int p = i / tiles, tile = i - p * tiles, f = tile * 64 + lane * 2;
-        if (c.id[p] < 0 || f >= F) continue;
-        const int n = pieces_of(c, 0, c.act[p] * tiles + tile);
-        float2 g = make_float2(0.f, 0.f), u = g;
-        const float* from = t.part[0] + (long long)p * 2 * F + f;
-        for (int k = 0; k < n; ++k, from += (long long)c.P * 2 * F) {
-            g = fadd2(g, __ldcg(reinterpret_cast<const float2*>(from)));
-            u = fadd2(u, __ldcg(reinterpret_cast<const float2*>(from + F)));
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - W_EPI, tiles = c.tiles[0], F = t.r.F, all = c.P * tiles;
+    const int teams = gridDim.x * (WORKERS / 32) * 2;
+    const long long step = (long long)c.P * 2 * F;
+#pragma unroll 1
+    for (int i = (blockIdx.x + w * gridDim.x) * 2 + (lane >> 4); i < all; i += 2 * teams) {
+        Pieces gate[2], up[2];
+        unsigned short* to[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int at = min(i + j * teams, all - 1), p = at / tiles, tile = at - p * tiles, f = tile * 64 + (lane & 15) * 4;
+            const bool real = i + j * teams < all && c.id[p] >= 0 && f < F;
+            const int n = real ? pieces_of(c, 0, c.act[p] * tiles + tile) : 0;
+            const float* const from = t.part[0] + (long long)p * 2 * F + (real ? f : 0);
+            gate[j].fetch(from, step, n);
+            up[j].fetch(from + F, step, n);
+            to[j] = real ? static_cast<unsigned short*>(t.h) + (long long)p * F + f : nullptr;
         }
-        T* const to = static_cast<T*>(t.h) + (long long)p * F + f;
-        to[0] = Elem<DT>::put(silu_times(g.x, u.x));
-        to[1] = Elem<DT>::put(silu_times(g.y, u.y));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint2 h = activated<DT>(gate[j], up[j]);
+            if (to[j]) *reinterpret_cast<uint2*>(to[j]) = h;
+        }
     }
 }
 
@@ -269,32 +311,16 @@ __device__ void activate(const Ctx& c, const TcArgs& t) {
 // 64 columns from k on of pair p's h, for the swizzled row at `row` of a slice at `dst`: four columns a lane, 16 lanes a slice.
 template <int DT>
 __device__ __forceinline__ void activate_into(const Ctx& c, const TcArgs& t, uint32_t dst, int row, int p, int expert, int k0) {
-    constexpr int MOST = 3;  // pieces fetched together
     const int lane = threadIdx.x & 31, F = t.r.F;
     const int slice = lane >> 4, k = k0 + lane * 4, tile = k >> 6;
     if (slice >= c.wide) return;
-    float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
     const bool real = k < F;
     const int n = real ? pieces_of(c, 0, expert * c.tiles[0] + tile) : 0;
     const float* const from = t.part[0] + (long long)p * 2 * F + (real ? k : 0);
-    const long long step = (long long)c.P * 2 * F;
-    for (int j0 = 0; j0 < n; j0 += MOST) {
-        float4 a[MOST], b[MOST];
-#pragma unroll
-        for (int j = 0; j < MOST; ++j) {  // (a piece that is not there: the last one again, not added)
-            const float* const at = from + min(j0 + j, n - 1) * step;
-            a[j] = __ldcg(reinterpret_cast<const float4*>(at));
-            b[j] = __ldcg(reinterpret_cast<const float4*>(at + F));
-        }
-#pragma unroll
-        for (int j = 0; j < MOST; ++j)
-            if (j0 + j < n) {
-                g = make_float4(g.x + a[j].x, g.y + a[j].y, g.z + a[j].z, g.w + a[j].w);
-                u = make_float4(u.x + b[j].x, u.y + b[j].y, u.z + b[j].z, u.w + b[j].w);
-            }
-    }
-    const float2 f[Elem<DT>::N / 2] = {{silu_times(g.x, u.x), silu_times(g.y, u.y)}, {silu_times(g.z, u.z), silu_times(g.w, u.w)}};
-    const uint4 v = pack<DT>(f);
+    Pieces gate, up;
+    gate.fetch(from, (long long)c.P * 2 * F, n);
+    up.fetch(from + F, (long long)c.P * 2 * F, n);
+    const uint2 v = activated<DT>(gate, up);
     const int ch = lane >> 1 & 7;
     const uint32_t to = dst + slice * c.npad * KSTEP * 2 + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4) + (lane & 1) * 8;
     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(v.x), "r"(v.y) : "memory");
@@ -385,22 +411,23 @@ __device__ bool store_pieces(const Ctx& c, const TcArgs& t, int ph, int& seg, ui
     return true;
 }
 
-// All CTAs' workers have come this far, and what they wrote is seen.
+// One thread of each CTA, for all that the CTA has done before: all CTAs have come this far, and what they wrote is seen.
+__device__ __forceinline__ void meet(const Ctx& c, const TcArgs& t, int which) {
+    unsigned* const at = t.barrier + which;
+    __threadfence();
+    if (!*c.abort) atomicAdd(at, 1u);  // (a CTA that gave up holds the others, whose waits then run out too)
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+        if (v >= gridDim.x || *c.abort) break;
+        if (globaltimer_ns() - t0 > WAIT_NS) *c.abort = 1;
+    }
+    __threadfence();
+}
 __device__ bool grid_barrier(const Ctx& c, const TcArgs& t, int which) {
     worker_sync();
-    if (threadIdx.x == W_EPI * 32) {
-        unsigned* const at = t.barrier + which;
-        __threadfence();
-        if (!*c.abort) atomicAdd(at, 1u);  // (a CTA that gave up holds the others, whose waits then run out too)
-        const uint64_t t0 = globaltimer_ns();
-        for (;;) {
-            unsigned v;
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
-            if (v >= gridDim.x || *c.abort) break;
-            if (globaltimer_ns() - t0 > WAIT_NS) *c.abort = 1;
-        }
-        __threadfence();
-    }
+    if (threadIdx.x == W_EPI * 32) meet(c, t, which);
     worker_sync();
     return !*c.abort;
 }
@@ -414,27 +441,26 @@ __device__ void join(const Ctx& c, const TcArgs& t) {
         const int tok = i / per, col = (i - tok * per) * 32 + (lane & 7) * 4;
         const bool real = col < H;
         float s[4] = {};
-        for (int k = lane >> 3; k < t.r.K; k += 4) {
-            const int p = tok * t.r.K + k;
-            const float wt = c.weight[p];
-            if (c.id[p] < 0 || !real) {  // 0, or NaN
+#pragma unroll 1
+        for (int k0 = lane >> 3; k0 < t.r.K; k0 += 8) {
+            Pieces y[2];
+            float wt[2];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] += wt;
-                continue;
+            for (int j = 0; j < 2; ++j) {
+                const int k = k0 + 4 * j, p = tok * t.r.K + min(k, t.r.K - 1);
+                const bool chosen = k < t.r.K && c.id[p] >= 0 && real;
+                wt[j] = k < t.r.K ? c.weight[p] : 0.f;  // (not chosen: 0, or NaN)
+                const int n = chosen ? pieces_of(c, 1, c.act[p] * c.tiles[1] + (col >> 7)) : 0;
+                y[j].fetch(t.part[1] + (long long)p * H + (real ? col : 0), (long long)c.P * H, n);
             }
-            const int n = pieces_of(c, 1, c.act[p] * c.tiles[1] + (col >> 7));
-            const float* from = t.part[1] + (long long)p * H + col;
-            float4 y = __ldcg(reinterpret_cast<const float4*>(from));
-#pragma unroll 2
-            for (int j = 1; j < n; ++j) {
-                from += (long long)c.P * H;
-                const float4 z = __ldcg(reinterpret_cast<const float4*>(from));
-                y = make_float4(y.x + z.x, y.y + z.y, y.z + z.z, y.w + z.w);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float4 v = y[j].n > 0 ? y[j].sum() : make_float4(1.f, 1.f, 1.f, 1.f);
+                s[0] = fmaf(wt[j], v.x, s[0]);
+                s[1] = fmaf(wt[j], v.y, s[1]);
+                s[2] = fmaf(wt[j], v.z, s[2]);
+                s[3] = fmaf(wt[j], v.w, s[3]);
             }
-            s[0] = fmaf(wt, y.x, s[0]);
-            s[1] = fmaf(wt, y.y, s[1]);
-            s[2] = fmaf(wt, y.z, s[2]);
-            s[3] = fmaf(wt, y.w, s[3]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -453,7 +479,7 @@ template <int DT>
 __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const __grid_constant__ CUtensorMap up,
                                                           const __grid_constant__ CUtensorMap down) {
     extern __shared__ unsigned char raw[];
-    __shared__ int counts[2][NWARP];
+    __shared__ int counts[2];
     const uint32_t lead = smem_u32(raw);
     const uint32_t skip = (1024 - (lead & 1023)) & 1023;
     Ctx c;
@@ -469,6 +495,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     c.id = reinterpret_cast<short*>(c.sm + t.L.id);
     c.info = reinterpret_cast<Info*>(c.sm + t.L.info);
     uint4* const mask = reinterpret_cast<uint4*>(c.sm + t.L.mask);  // the tokens of each expert
+    unsigned short* const place = reinterpret_cast<unsigned short*>(c.sm + t.L.place);  // of each expert in info
     c.P = t.r.T * t.r.K;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, E = t.r.E, K = t.r.K;
     if (tid == 0) {
@@ -495,87 +522,88 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         asm volatile("prefetch.tensormap [%0];" ::"l"(&up) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&down) : "memory");
     }
-    // choose
+    // Choose: a warp a token.  Every CTA does it for all tokens where that takes a round; otherwise the tokens are shared out
+    // and read back behind a barrier (64 tokens of 128 experts: ?? us instead of 12).
     for (int i = tid; i < E; i += NT) mask[i] = make_uint4(0u, 0u, 0u, 0u);
+    const auto take = [&](int p, int id, float w) {
+        c.id[p] = (short)id;
+        c.weight[p] = w;
+        if (id >= 0) atomicOr(reinterpret_cast<unsigned*>(mask + id) + (p / K >> 5), 1u << (p / K & 31));
+    };
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores, and the barriers' zeros
-    for (int tok = warp; tok < t.r.T; tok += NWARP) {
+    const bool shared = t.r.T > NWARP;
+#pragma unroll 1
+    for (int tok = shared ? blockIdx.x + warp * gridDim.x : warp; tok < t.r.T; tok += NWARP * (shared ? gridDim.x : 1)) {
         int id;
         float w;
         routed_choose(t.r.logits + (long long)tok * E, E, K, t.r.renorm, t.r.scale, id, w);
         if (lane < K) {
             const int p = tok * K + lane;
-            c.id[p] = (short)id;
-            c.weight[p] = w;
-            if (id >= 0) atomicOr(reinterpret_cast<unsigned*>(mask + id) + (tok >> 5), 1u << (tok & 31));
-            if (tok % gridDim.x == blockIdx.x) {
+            if (!shared) take(p, id, w);
+            if (shared || tok % gridDim.x == blockIdx.x) {
                 t.r.ids[p] = id;
                 t.r.weights[p] = w;
             }
         }
     }
     __syncthreads();
-    // The experts in use, in order, and where their lists start: a thread four experts.
-    constexpr int PER = (ROUTED_MAX_E + NT - 1) / NT;
-    int used = 0, tokens = 0, most = 0, n[PER];
-    uint4 m[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        m[j] = tid * PER + j < E ? mask[tid * PER + j] : make_uint4(0u, 0u, 0u, 0u);
-        n[j] = __popc(m[j].x) + __popc(m[j].y) + __popc(m[j].z) + __popc(m[j].w);
-        used += n[j] > 0;
-        tokens += n[j];
-        most = max(most, n[j]);
+    if (shared) {
+        if (tid == 0) meet(c, t, 3);
+        __syncthreads();
+#pragma unroll 1
+        for (int p = tid; p < c.P; p += NT) take(p, __ldcg(t.r.ids + p), __ldcg(t.r.weights + p));
+        __syncthreads();
     }
-    int before = used | tokens << 16;  // (at most 1024 and 4096)
+    // The experts in use, in order, and where their lists start.  (Loops stay loops here: this runs once, and fetching
+    // instructions is most of what it costs.)
+    if (warp == 0) {
+        int used = 0, start = 0, most = 0;
+#pragma unroll 1
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const uint4 m = e0 + lane < E ? mask[e0 + lane] : make_uint4(0u, 0u, 0u, 0u);
+            const int n = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+            const unsigned on = __ballot_sync(0xffffffffu, n > 0);
+            int upto = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += v;
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if (lane == 31) {
-        counts[0][warp] = before;
-        counts[1][warp] = most;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (n > 0) {
+                const int a = used + __popc(on & ((1u << lane) - 1u));
+                c.info[a] = Info{e0 + lane, start + upto - n, n};
+                place[e0 + lane] = (unsigned short)a;
+            }
+            used += __popc(on);
+            start += __shfl_sync(0xffffffffu, upto, 31);
+            most = max(most, n);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+            counts[0] = *c.abort ? 0 : used;
+            counts[1] = most;
+        }
     }
     __syncthreads();
-    int at = before - (used | tokens << 16), all = 0;
-#pragma unroll
-    for (int w = 0; w < NWARP; ++w) {
-        if (w < warp) at += counts[0][w];
-        all += counts[0][w];
-        most = max(most, counts[1][w]);
-    }
-    const Cut cut(max(16, pad16(most)), t.L.ring);
+    c.active = counts[0];
+    const Cut cut(max(16, pad16(counts[1])), t.L.ring);
     c.npad = cut.npad;
     c.wide = cut.wide;
     c.stage = cut.stage;
     c.S = cut.stages;
-    c.active = all & 0xffff;
-    int a = at & 0xffff, start = at >> 16;
-#pragma unroll
-    for (int j = 0; j < PER; ++j)
-        if (n[j] > 0) {
-            c.info[a] = Info{tid * PER + j, start, n[j]};
-            const unsigned word[4] = {m[j].x, m[j].y, m[j].z, m[j].w};
-            int k = start;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                for (unsigned left = word[q]; left; left &= left - 1) c.toks[k++] = (unsigned short)(q * 32 + __ffs(left) - 1);
-            ++a;
-            start += n[j];
-        }
-    __syncthreads();
-    // From tokens to pairs: which of the token's choices it is, and the pair's expert.
-    for (int i = warp; i < c.active; i += NWARP) {
-        const Info e = c.info[i];
-        for (int j = lane; j < e.n; j += 32) {
-            const int tok = c.toks[e.start + j];
-            int k = 0;
-            while (c.id[tok * K + k] != e.expert) ++k;
-            c.list[e.start + j] = (unsigned short)(tok * K + k);
-            c.act[tok * K + k] = (unsigned short)i;
-        }
+    // A pair's place in its expert's list: the tokens before its own.
+#pragma unroll 1
+    for (int p = tid; p < c.P; p += NT) {
+        const int id = c.id[p], tok = p / K;
+        if (id < 0 || c.active == 0) continue;
+        const unsigned* const m = reinterpret_cast<const unsigned*>(mask + id);
+        int at = __popc(m[tok >> 5] & ((1u << (tok & 31)) - 1u));
+        for (int q = 0; q < tok >> 5; ++q) at += __popc(m[q]);
+        at += c.info[place[id]].start;
+        c.toks[at] = (unsigned short)tok;
+        c.list[at] = (unsigned short)p;
+        c.act[p] = place[id];
     }
     const int dims[PHASES] = {t.r.H, t.r.F};
     c.tiles[0] = (t.r.F + 63) / 64;
@@ -672,7 +700,7 @@ Layout layout(const RoutedArgs& a) {
     };
     L.most = (a.T + 15) / 16 * 16;
     const int other = (BAR_BYTES + 15) / 16 * 16 + (4 * P + 15) / 16 * 16 + 4 * ((2 * P + 15) / 16 * 16) +
-                      ((int)sizeof(Info) * a.E + 15) / 16 * 16 + 16 * a.E;
+                      ((int)sizeof(Info) * a.E + 15) / 16 * 16 + 16 * a.E + (2 * a.E + 15) / 16 * 16;
     L.ring = (MAX_SMEM - 1024 - other) / 1024 * 1024;
     place(L.ring);
     L.bars = place(BAR_BYTES);
@@ -683,6 +711,7 @@ Layout layout(const RoutedArgs& a) {
     L.id = place(2 * P);
     L.info = place((int)sizeof(Info) * a.E);
     L.mask = place(16 * a.E);
+    L.place = place(2 * a.E);
     L.total = at + 1024;
     return L;
 }
