@@ -762,6 +762,16 @@ def _matrix(t, name, rows, D, dev):
     return at, ld, dt
 
 
+def _float_type(dtype, default):
+    """sot_dtype of a torch float type; the default for None."""
+    if dtype is None:
+        return default
+    try:
+        return _FLOATS[dtype]
+    except (KeyError, TypeError):
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}") from None
+
+
 def sot_embed(table, ids, scale=1.0, dtype=None, out=None, stream=None):
     """Embedding lookup with scaling: out [T, D] = scale table[ids], rounded once; rows of zeros for ids outside
     [0, V).  table [V, D] may have a row stride, ids is [T]; ``dtype`` (default the table's) is the type of a new out."""
@@ -770,13 +780,17 @@ def sot_embed(table, ids, scale=1.0, dtype=None, out=None, stream=None):
         raise ValueError("ids must be a torch.Tensor of shape [T]")
     T = ids.shape[0]
     i, ty = _indices(ids, "ids", (T,), dev)
-    if out is None and dtype is not None and dtype not in _FLOATS:
-        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    ot = _float_type(dtype, dt)
+    if out is not None:
+        at, ldo, ot = _matrix(out, "out", T, D, dev)
 
     def call(s):
-        o = torch.empty((T, D), dtype=dtype or table.dtype, device=table.device) if out is None else out
-        at, ldo, ot = _matrix(o, "out", T, D, dev)
-        rc = load().sot_embed(x, V, D, ld, dt, i, ty, T, scale, at, ldo, ot, s)
+        if out is not None:
+            o, to, ld_out = out, at, ldo
+        else:
+            o = torch.empty((T, D), dtype=dtype or table.dtype, device=table.device)
+            to, ld_out = o.data_ptr(), D
+        rc = load().sot_embed(x, V, D, ld, dt, i, ty, T, scale, to, ld_out, ot, s)
         if rc:
             _check(rc, "sot_embed")
         return o
@@ -795,13 +809,17 @@ def sot_embed_grad(grad_out, ids, V, scale=1.0, dtype=None, grad=None, accumulat
         raise ValueError("V must be >= 1")
     if accumulate and grad is None:
         raise TypeError("accumulate needs a gradient to add to")
-    if grad is None and dtype is not None and dtype not in _FLOATS:
-        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    gt = _float_type(dtype, dt)
+    if grad is not None:
+        at, ldg, gt = _matrix(grad, "grad", V, D, dev)
 
     def call(s):
-        g = torch.empty((V, D), dtype=dtype or grad_out.dtype, device=grad_out.device) if grad is None else grad
-        at, ldg, gt = _matrix(g, "grad", V, D, dev)
-        rc = load().sot_embed_grad(x, T, D, ld, dt, i, ty, V, scale, 1 if accumulate else 0, at, ldg, gt, s)
+        if grad is not None:
+            g, to, ld_grad = grad, at, ldg
+        else:
+            g = torch.empty((V, D), dtype=dtype or grad_out.dtype, device=grad_out.device)
+            to, ld_grad = g.data_ptr(), D
+        rc = load().sot_embed_grad(x, T, D, ld, dt, i, ty, V, scale, 1 if accumulate else 0, to, ld_grad, gt, s)
         if rc:
             _check(rc, "sot_embed_grad")
         return g
@@ -830,11 +848,17 @@ def sot_routed_layer(x, router, gate_up, down, K, bias=None, renorm=True, scale=
     if K < 1 or K > E:
         raise ValueError(f"K must satisfy 1 <= K <= {E}")
 
-    def call(s):
-        o = torch.empty((T, H), dtype=x.dtype, device=x.device) if out is None else out
-        oat, ldo, ot = _matrix(o, "out", T, H, dev)
+    if out is not None:
+        to, ld_out, ot = _matrix(out, "out", T, H, dev)
         if ot != dt:
-            raise TypeError(f"out must be {x.dtype}, got {o.dtype}")
+            raise TypeError(f"out must be {x.dtype}, got {out.dtype}")
+
+    def call(s):
+        if out is not None:
+            o, oat, ldo = out, to, ld_out
+        else:
+            o = torch.empty((T, H), dtype=x.dtype, device=x.device)
+            oat, ldo = o.data_ptr(), H
         logits = torch.empty((T, E), dtype=_F32, device=x.device)
         ids = torch.empty((T, K), dtype=torch.int32, device=x.device)
         weights = torch.empty((T, K), dtype=_F32, device=x.device)

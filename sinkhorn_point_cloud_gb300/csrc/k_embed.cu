@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(SORT_NT) embed_sort_kernel(const EmbedGradArgs
 }
 
 // ---- gradient: sums ----
-constexpr int SUM_NT = 128, SUM_R = 32;
+constexpr int SUM_NT = 128, SUM_R = 16;
 // Columns of a thread: a granule of the incoming gradient, or four where its rows are not whole granules.
 template <int DT, bool VEC>
 constexpr int SUM_W = VEC ? Elem<DT>::N : 4;

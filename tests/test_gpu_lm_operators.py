@@ -5,7 +5,7 @@ Tolerances.  Log-sum-exp and log-probabilities: 2^-16 and 2^-23 of the logits' s
 losses (a thread's chain is at most 256 additions, 2^-24 each, and exp2 is good to 2^-22).  Entropy: log S - A / S with
 the same relative error, 2^-16, of each sum, where log S and A / S are at most log V.  A gradient: 2^-14 of
 the size of its terms (the lse's and the entropy's errors enter as factors of p) and half an ulp of its type.
-Embedding: one product, 2^-24, and half an ulp; its gradient: 2^-24 for each addition of a chain (64 in a chunk, then one a
+Embedding: one product, 2^-24, and half an ulp; its gradient: 2^-24 for each addition of a chain (32 in a chunk, then one a
 chunk) of the size of the terms.  Routed layer: 2^-24 for each addition of a chain of products (under 256, and the tree) in
 each of the two products, 2^-16 in all, h rounded to the type (half an ulp) on the tensor cores, and half an ulp
 of the output; softmax weights 2^-20."""
@@ -309,7 +309,7 @@ def test_embed_grad(sot, T, V, D, src, dst):
             ids[2] = V
         i = torch.from_numpy(ids).to(it).cuda()
         ref, size = R.embed_grad(host(g), ids, V, 0.5)
-        chain = 2.0 ** -24 * (66 + T / 32)
+        chain = 2.0 ** -24 * (34 + T / 16)
         got = sot.sot_embed_grad(g, i, V, scale=0.5, dtype=TYPES[dst])
         near(got, ref, HALF_ULP[dst] * np.abs(ref) + chain * size + TINY[dst])
         assert torch.equal(sot.sot_embed_grad(g, i, V, scale=0.5, dtype=TYPES[dst]), got)  # the same bits again
