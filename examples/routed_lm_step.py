@@ -9,9 +9,10 @@ respect to the logits straight from the library:
   balance        the router's choices on all of these, with per-expert counts
 
 The library writes gradients with respect to logits, torch carries them on to the
-weights:  torch.autograd.backward([logits, ...], [grad, ...]).
+weights:  torch.autograd.backward([logits, ...], [grad, ...]).  The embedding lookup and its gradient, the
+teacher's best entries and the rollouts' entropies are the library's too; --bonus adds the entropies' gradient.
 
-  python examples/routed_lm_step.py [--steps 40]
+  python examples/routed_lm_step.py [--steps 40] [--bonus 0.01]
 """
 from __future__ import annotations
 
@@ -27,6 +28,20 @@ import sinkhorn_point_cloud_gb300 as sot  # noqa: E402
 VOCAB, WIDTH, EXPERTS, CHOICES = 4000, 128, 8, 2
 
 
+class Lookup(torch.autograd.Function):
+    """Rows of a table, and the table's gradient by sorted tokens."""
+
+    @staticmethod
+    def forward(ctx, table, tokens):
+        ctx.save_for_backward(tokens)
+        ctx.rows = table.shape[0]
+        return sot.sot_embed(table, tokens)
+
+    @staticmethod
+    def backward(ctx, grad):
+        return sot.sot_embed_grad(grad.contiguous(), ctx.saved_tensors[0], ctx.rows), None
+
+
 class RoutedLM(torch.nn.Module):
     """Embedding, one routed layer, output head: next-token logits from the current token."""
 
@@ -40,7 +55,7 @@ class RoutedLM(torch.nn.Module):
 
     def forward(self, tokens):
         """(logits [T, VOCAB] bf16, router logits [T, EXPERTS] fp32, experts chosen [T, CHOICES])"""
-        x = self.embed[tokens]
+        x = Lookup.apply(self.embed, tokens)
         r = x @ self.router.T + self.lean
         gate, ids = torch.softmax(r, 1).topk(CHOICES, 1)
         y = torch.einsum("td,tkde->tke", x, self.experts[ids])
@@ -52,7 +67,7 @@ def batch(T, g, dev):
     return torch.randint(0, VOCAB, (T,), generator=g, device=dev)
 
 
-def train(steps=40, lr=1e-3, seed=0, report=True):
+def train(steps=40, lr=1e-3, seed=0, report=True, bonus=0.0):
     """Runs the steps; returns one dict of losses per step."""
     dev = torch.device("cuda")
     g = torch.Generator(device=dev).manual_seed(seed)
@@ -66,8 +81,7 @@ def train(steps=40, lr=1e-3, seed=0, report=True):
     said, answers = batch(int(lens.sum()), g, dev), batch(int(lens.sum()), g, dev)
     answers[::7] = -100  # tokens of the prompt take no part
     with torch.no_grad():
-        top, ids = torch.log_softmax(16.0 * teacher(text)[0].float(), 1).topk(8, 1)
-        ids = ids.to(torch.int32)
+        ids, top = sot.sot_token_topk(teacher(text)[0], 8, temperature=1.0 / 16.0)[3:]
         before = sot.sot_token_logprob(model(prompts)[0], actions)[0]  # the starting model's
         answered = sot.sot_token_logprob(model(said)[0], answers)[0]
     history = []
@@ -78,6 +92,10 @@ def train(steps=40, lr=1e-3, seed=0, report=True):
         router, choices = torch.cat(routers), torch.cat(chosen)
         distil, d_text = sot.sot_distill_topk(logits[0].detach(), ids, top, tail=True)
         policy, _, kl, d_roll = sot.sot_policy_loss(logits[1].detach(), actions, old, advantage, ref_logp=before, kl_coef=0.05)
+        _, roll_lse, entropy, _, _ = sot.sot_token_topk(logits[1].detach(), 0)
+        if bonus:
+            d_roll += sot.sot_token_topk_grad(logits[1].detach(), roll_lse, entropy=entropy,
+                                              grad_entropy=torch.full_like(entropy, -bonus / len(entropy)))
         logp, lse = sot.sot_token_logprob(logits[2].detach(), answers)
         prefer, margin, d_logp = sot.sot_preference_loss(logp, offsets, ref_logp=answered, target=answers, beta=0.1)
         d_pairs = sot.sot_token_logprob_grad(logits[2].detach(), answers, lse, d_logp)
@@ -86,6 +104,7 @@ def train(steps=40, lr=1e-3, seed=0, report=True):
         torch.autograd.backward([*logits, router], [d_text, d_roll, d_pairs, d_router])
         opt.step()
         history.append(dict(distil=distil.sum().item(), policy=policy.sum().item(), kl=kl.mean().item(),
+                            entropy=entropy.mean().item(),
                             prefer=prefer.mean().item(), margin=margin.mean().item(), balance=balance[0].item(),
                             busiest=counts.max().item() / max(1, counts.sum().item())))
         if report and (step % 10 == 0 or step == steps - 1):
@@ -96,4 +115,6 @@ def train(steps=40, lr=1e-3, seed=0, report=True):
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=40)
-    train(ap.parse_args().steps)
+    ap.add_argument("--bonus", type=float, default=0.0, help="weight of the rollouts' entropy")
+    args = ap.parse_args()
+    train(args.steps, bonus=args.bonus)

@@ -23,6 +23,7 @@ struct EmbedGradArgs {
     float scale;
     int accumulate;
     void* grad;  // [V, D]
+    int chunk;   // sorted tokens of a chunk
     // scratch: (row, token) sorted by row (two buffers), the chunks where a row begins that goes on in the next and that row,
     // a bit for each row that a token names, partial sums
     uint2* sorted[2];
@@ -34,6 +35,7 @@ struct EmbedGradArgs {
 struct EmbedGradPlan {
     int passes, bits;  // of the sort
     long long chunks;
+    int chunk;  // tokens of one
     size_t sorted_at[2], spans_at, span_at, named_at, part_at, scratch;
 };
 EmbedGradPlan embed_grad_plan(long long T, int V, int D);

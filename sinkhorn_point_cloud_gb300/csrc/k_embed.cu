@@ -344,7 +344,10 @@ __global__ void __launch_bounds__(SORT_NT) embed_sort_kernel(const EmbedGradArgs
 }
 
 // ---- gradient: sums ----
-constexpr int SUM_NT = 128, SUM_R = 16;
+// Sorted tokens of a chunk: few, for short chains and many CTAs (8192 tokens, 32000 x 1024 bf16: 39 us, with 32 44); twice that
+// for long batches, whose partial sums take T D / 2 bytes with 16.
+constexpr int SUM_NT = 128, SUM_MAX_R = 32;
+int chunk_tokens(long long T) { return T <= 65536 ? 16 : SUM_MAX_R; }
 // Columns of a thread: a granule of the incoming gradient, or four where its rows are not whole granules.
 template <int DT, bool VEC>
 constexpr int SUM_W = VEC ? Elem<DT>::N : 4;
@@ -521,7 +524,8 @@ template <int DT, int DG, bool VEC>
 __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArgs a, int tiles, long long zeros, long long zero_from,
                                                               int zero_share) {
     constexpr int SUM_U = SumRows<DT, VEC>::U, W = SUM_W<DT, VEC>;
-    __shared__ unsigned key[2 * SUM_R + 1], pos[2 * SUM_R];
+    __shared__ unsigned key[2 * SUM_MAX_R + 1], pos[2 * SUM_MAX_R];
+    const int R = a.chunk;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // `zeros` CTAs, spread evenly over the grid, write zeros
     const long long zero = blockIdx.x * zeros / gridDim.x, block = blockIdx.x - zero;
@@ -532,30 +536,30 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
     }
     const long long chunk = block / tiles;
     const int c0 = (int)(block % tiles) * SUM_NT * W, tid = threadIdx.x;
-    const long long at = chunk * SUM_R;
+    const long long at = chunk * R;
     // The keys from the token before the chunk to the end of the next chunk; V: none.
     unsigned mine = (unsigned)a.V;
     const uint2* const sorted = a.sorted[0];
     const auto key_at = [&](long long i) { return i >= 0 && i < a.T ? __ldg(&sorted[i].x) : (unsigned)a.V; };
-    if (tid < 2 * SUM_R + 1) {
+    if (tid < 2 * R + 1) {
         const long long i = at + tid - 1;
         const uint2 t = i >= 0 && i < a.T ? __ldg(sorted + i) : make_uint2((unsigned)a.V, 0u);
         key[tid] = mine = t.x;
         if (tid > 0) pos[tid - 1] = t.y;
     }
-    const unsigned long_before = key_at(at - SUM_R - 1), long_after = key_at(at + 2 * SUM_R);
+    const unsigned long_before = key_at(at - R - 1), long_after = key_at(at + 2 * R);
     // tokens of the chunk that have a row: they come first
-    const int n = __syncthreads_count(tid >= 1 && tid <= SUM_R && mine < (unsigned)a.V);
-    const auto row = [&](int i) { return i < 2 * SUM_R ? key[i + 1] : long_after; };
+    const int n = __syncthreads_count(tid >= 1 && tid <= R && mine < (unsigned)a.V);
+    const auto row = [&](int i) { return i < 2 * R ? key[i + 1] : long_after; };
     if (n == 0) return;
     // The chunk before finishes a row that begins in it and ends here; this one does the same for the next.
     const bool open = key[0] == key[1];
     int from = 0, end = n;
-    if (open && long_before != key[1] && row(SUM_R) != key[1])
+    if (open && long_before != key[1] && row(R) != key[1])
         while (from < n && row(from) == key[1]) ++from;
     const unsigned tail = row(n - 1);
-    if (n == SUM_R && row(SUM_R) == tail && !(open && key[1] == tail) && long_after != tail)
-        while (end < 2 * SUM_R && row(end) == tail) ++end;
+    if (n == R && row(R) == tail && !(open && key[1] == tail) && long_after != tail)
+        while (end < 2 * R && row(end) == tail) ++end;
     float acc[W] = {};
     for (int i0 = from; i0 < end; i0 += SUM_U) {
         SumRows<DT, VEC> rows;
@@ -595,7 +599,8 @@ __global__ void __launch_bounds__(JOIN_NT, 4) embed_join_kernel(const EmbedGradA
     __shared__ float sums[JOIN_NW][JOIN_COLS];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long spans = __ldcg(a.spans), work = spans * tiles, chunks = (a.T + SUM_R - 1) / SUM_R;
+    const int R = a.chunk;
+    const long long spans = __ldcg(a.spans), work = spans * tiles, chunks = (a.T + R - 1) / R;
     for (long long w = blockIdx.x; w < work; w += gridDim.x) {
         const uint2 span = __ldcg(a.span + w % spans);
         const int c0 = (int)(w / spans) * JOIN_COLS;
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(JOIN_NT, 4) embed_join_kernel(const EmbedGradA
 #pragma unroll
             for (int u = 0; u < JOIN_U; ++u) {  // (no branch on what is loaded before all loads are out)
                 const long long at = min(c + u * JOIN_NW, chunks - 1);
-                key[u] = __ldcg(&a.sorted[0][at * SUM_R].x);
+                key[u] = __ldcg(&a.sorted[0][at * R].x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[u][j] = __ldcg(part_row(a, at, 0) + col[j]);
             }
@@ -763,7 +768,8 @@ EmbedGradPlan embed_grad_plan(long long T, int V, int D) {
     while (need < 32 && (unsigned)V >> need) ++need;  // keys 0 .. V
     p.passes = (need + SORT_MAX_BITS - 1) / SORT_MAX_BITS;
     p.bits = (need + p.passes - 1) / p.passes;
-    p.chunks = (T + SUM_R - 1) / SUM_R;
+    p.chunk = chunk_tokens(T);
+    p.chunks = (T + p.chunk - 1) / p.chunk;
     const auto place = [&](size_t bytes) {
         const size_t at = p.scratch;
         p.scratch = (at + bytes + 255) & ~(size_t)255;
@@ -780,6 +786,7 @@ EmbedGradPlan embed_grad_plan(long long T, int V, int D) {
 cudaError_t launch_embed_grad(EmbedGradArgs a, const EmbedGradPlan& p, unsigned char* scratch, int sms, cudaStream_t st) {
     if (a.T == 0 && a.accumulate) return cudaSuccess;
     for (int i = 0; i < 2; ++i) a.sorted[i] = reinterpret_cast<uint2*>(scratch + p.sorted_at[i]);
+    a.chunk = p.chunk;
     a.spans = reinterpret_cast<unsigned*>(scratch + p.spans_at);
     a.span = reinterpret_cast<uint2*>(scratch + p.span_at);
     a.named = a.accumulate ? nullptr : reinterpret_cast<unsigned*>(scratch + p.named_at);
