@@ -832,22 +832,20 @@ def sot_routed_layer(x, router, gate_up, down, K, bias=None, renorm=True, scale=
     out = sum over a token's K best experts of weight * down (silu(gate x) * up x).  logits and ids go on to
     sot_balance_loss."""
     at, T, H, ld, dt, dev = _logits(x, "x")
-    if not isinstance(router, torch.Tensor) or router.dim() != 2:
-        raise ValueError("router must be a torch.Tensor of shape [E, H]")
-    E = router.shape[0]
-    if not isinstance(down, torch.Tensor) or down.dim() != 3:
-        raise ValueError("down must be a torch.Tensor of shape [E, H, F]")
-    F, K = down.shape[2], int(K)
-    if not isinstance(gate_up, torch.Tensor) or tuple(gate_up.shape) != (E, 2 * F, H) or tuple(down.shape) != (E, H, F) or \
-            router.shape[1] != H:
-        raise ValueError(f"x [T, H], router [E, H], gate_up [E, 2 F, H] and down [E, H, F] disagree: {tuple(x.shape)}, "
-                         f"{tuple(router.shape)}, {tuple(getattr(gate_up, 'shape', ()))}, {tuple(down.shape)}")
+    K = int(K)
+    try:
+        E, F = router.shape[0], down.shape[2]
+        agree = router.shape == (E, H) and gate_up.shape == (E, 2 * F, H) and down.shape == (E, H, F)
+    except (AttributeError, IndexError):
+        agree = False
+    if not agree:
+        raise ValueError("x [T, H], router [E, H], gate_up [E, 2 F, H] and down [E, H, F] must be torch.Tensors that agree, got "
+                         + ", ".join(str(tuple(getattr(t, "shape", ()))) for t in (x, router, gate_up, down)))
     r = _floats(router, "router", E * H, dev, x.dtype)
     gu, dn = _floats(gate_up, "gate_up", E * 2 * F * H, dev, x.dtype), _floats(down, "down", E * H * F, dev, x.dtype)
     b = _floats(bias, "bias", E, dev)
     if K < 1 or K > E:
         raise ValueError(f"K must satisfy 1 <= K <= {E}")
-
     if out is not None:
         to, ld_out, ot = _matrix(out, "out", T, H, dev)
         if ot != dt:
