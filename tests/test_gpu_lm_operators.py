@@ -106,6 +106,42 @@ def test_many_alternatives(sot, T, V, K, dtype):
     check_scores(sot, put(normal(T, V, seed=K, scale=3.0), dtype, 1), K)
 
 
+@pytest.mark.parametrize("dtype,V", [("f32", 17000), ("bf16", 34001), ("f16", 33000)])
+def test_many_long_rows(sot, V, dtype):
+    """More rows than a GPU holds at a time, ordinary ones between ties, masks, bad rows and rows left out."""
+    rng = np.random.default_rng(V)
+    kinds = normal(12, V, seed=V, scale=2.0)
+    few = rng.random(V) < 0.001
+    few[V // 2] = True
+    kinds[1] = 1.5
+    kinds[2, ~few] = -np.inf
+    kinds[3, ~few] = LOWEST[dtype]
+    kinds[4] = -np.inf
+    kinds[5, 7] = np.nan
+    kinds[6, V - 1] = np.inf
+    kinds[7] = rng.integers(0, 3, V)
+    kinds[8] = np.linspace(-4, 4, V)
+    kinds[9, ::2] = -np.inf
+    which = rng.integers(0, 12, 1000)
+    which[:12] = np.arange(12)
+    x = put(kinds, dtype, 3, 1)[torch.from_numpy(which).cuda()]  # (rows are whole here)
+    wide = torch.full((1000, V + 3), float("nan"), dtype=TYPES[dtype], device="cuda")
+    wide[:, :V] = x
+    tg = torch.full((12,), V // 2, dtype=torch.int64)
+    tg[11] = -1
+    for view, K in ((x, 1), (wide[:, :V], 33), (x, 128), (x, 129)):
+        with np.errstate(all="ignore"):
+            rp, rl, re, ri, rt = R.token_topk(host(view[:12]), tg.numpy(), K, 0.9)
+            # (the type's lowest value over 0.9 lies beyond the range of a float: -inf there)
+            rp, rl, rt = (np.where(np.abs(v) > 3.4028235e38, -np.inf, v) for v in (rp, rl, rt))
+        logp, lse, ent, ids, top = sot.sot_token_topk(view, K, target=tg[torch.from_numpy(which)].cuda(), temperature=0.9)
+        assert np.array_equal(ids.cpu().numpy(), ri[which])
+        near(lse, rl[which], ATOL + RTOL * np.where(np.isfinite(rl), np.abs(rl), 0)[which])
+        near(ent, re[which], ATOL * (1 + np.log(V)))
+        near(top, rt[which], ATOL + RTOL * np.where(np.isfinite(rt), np.abs(rt), 0)[which])
+        near(logp, rp[which], ATOL + RTOL * np.where(np.isfinite(rp), np.abs(rp), 0)[which])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("V", [300, 5000, 70001])
 def test_equal_logits_go_by_column(sot, V, dtype):
