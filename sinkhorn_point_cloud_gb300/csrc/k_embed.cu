@@ -12,6 +12,10 @@
 //            time: writes alone reach 0.8 of the copy bandwidth);
 //   join     adds up the partial sums, in a fixed order.
 // No atomics on floats: repeated calls give the same bits.
+//
+// bf16, 4096 columns: 32768 lookups in fp32 77 us (0.80 of the measured copy bandwidth), 16384 tokens into 131072 rows 201 to
+// 204 us (0.87; most of it is zeros).  65001 tokens of 1001 fp32 columns into 32003 rows 131 us (0.41: rows that are not whole
+// granules are fetched 4 bytes a lane, 100 us with 1000 columns).
 #include <cuda_runtime.h>
 
 #include "embed.h"

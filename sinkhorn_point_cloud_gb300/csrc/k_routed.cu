@@ -4,6 +4,8 @@
 //   w    = their softmax weights (over all experts, or over the chosen ones),
 //   out_t = sum_k w_k down_e (silu(gate_e x_t) * up_e x_t),   e = the k-th expert of t.
 // A few tokens read far more weights than they compute with: the chosen experts' 3 F H weights bound it.
+// Here are the scores (64 tokens of 64 experts, H = 2048: 9 us, beside which the next kernel comes up) and, for fp32 and for
+// sizes that the tensor cores' copies do not take, a kernel of warps for each step (k_routed_tc.cu has the others).
 #include <cuda_runtime.h>
 
 #include "kernels.h"

@@ -1,7 +1,7 @@
 // k_routed_tc.cu -- the routed layer for a few tokens on the tensor cores, 16-bit types.
 //
 // After the scores (k_routed.cu) one cooperative kernel, a CTA an SM, does the rest:
-//   choose  every CTA forms the choice of all tokens and each expert's list of tokens for itself;
+//   choose  the tokens' experts (few tokens: every CTA for itself), then every CTA each expert's list of tokens;
 //   up      products gate_up x^T: an expert's rows are the M of a tcgen05.mma (64 gate rows and the 64 up rows that
 //           belong to them), its tokens the N.  The units of all experts (16 KB of weights, K = 64, or twice that) are dealt out evenly, so a
 //           CTA starts and ends inside a tile; it leaves a partial sum for each piece;
@@ -11,6 +11,11 @@
 // The weights are read once and bound it.  They come by TMA through a ring of stages, 16 or 32 KB each, from a warp that waits
 // for nothing but free stages: across the phases' grid barriers the next phase's weights are already on their way.
 // Every wait is bounded; one that runs out ends the call with NaN outputs and the timeout status.
+//
+// bf16, H = 4096, F = 1408, 8 of 128 experts, 64 tokens: 646 us for 4.36 GB, 0.99 of the measured copy bandwidth.  H = 2048,
+// F = 1024, 8 of 64 experts: one token 30.6 us for 101 MB (about 4.5 us until the first weights, 16 of weights, the rest waits of
+// phases on one another), 8 tokens 99 us, 128 tokens 157 us (0.76: the tokens' side of the units takes a third of the
+// ring).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         asm volatile("prefetch.tensormap [%0];" ::"l"(&down) : "memory");
     }
     // Choose: a warp a token.  Every CTA does it for all tokens where that takes a round; otherwise the tokens are shared out
-    // and read back behind a barrier (64 tokens of 128 experts: ?? us instead of 12).
+    // and read back behind a barrier (64 tokens of 128 experts: products begin after 8 us, with all in every CTA after 20).
     for (int i = tid; i < E; i += NT) mask[i] = make_uint4(0u, 0u, 0u, 0u);
     const auto take = [&](int p, int id, float w) {
         c.id[p] = (short)id;
