@@ -74,22 +74,47 @@ __device__ __forceinline__ void load_indices(const void* ids, int type, long lon
 }
 
 // ---- lookup ----
-constexpr int EMB_NT = 256, EMB_U = 4;
+constexpr int EMB_NT = 256, EMB_W = 8;
+template <bool VEC>
+constexpr int EMB_PIECES = VEC ? 4 : 2;
 
-// A thread takes U pieces of a tile of NT U pieces: eight columns where rows are whole granules (VEC), else one.
+// The eight elements from byte `from` on of G granules in a row.
+template <int DT, int G>
+__device__ __forceinline__ void eight_from(const uint4 (&v)[G], unsigned from, uint4 (&out)[G - 1]) {
+    unsigned w[4 * G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) w[4 * i] = v[i].x, w[4 * i + 1] = v[i].y, w[4 * i + 2] = v[i].z, w[4 * i + 3] = v[i].w;
+#pragma unroll
+    for (int k = 2; k > 0; k /= 2) {
+        const bool on = from & 4u * k;
+#pragma unroll
+        for (int i = 0; i + k < 4 * G; ++i) w[i] = on ? w[i + k] : w[i];
+    }
+    if constexpr (DT != SOT_F32) {
+#pragma unroll
+        for (int i = 0; i < 4 * (G - 1); ++i) w[i] = __funnelshift_r(w[i], w[i + 1], from % 4 * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < G - 1; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// A thread takes U pieces of a tile of NT U pieces, eight columns each.  Where rows of table or output are not
+// whole granules (VEC = false), a piece begins at a granule of the output, its columns are cut out of the table's granules
+// that hold them, and a row's first and last piece are written by elements (20000 rows of 1003 bf16: 19 us, an element a
+// thread 47).
 template <int DT, int DO, bool VEC>
 __global__ void __launch_bounds__(EMB_NT) embed_kernel(const EmbedArgs a, unsigned per_row) {
     using T = typename Elem<DT>::T;
     using O = typename Elem<DO>::T;
-    constexpr int W = VEC ? 8 : 1;
+    constexpr int R = DT == SOT_F32 ? 2 : 1, EMB_U = EMB_PIECES<VEC>;  // granules of a piece of the table
+    constexpr long long NONE = -1ll << 62;
     const long long total = a.T * per_row, tile = (long long)EMB_NT * EMB_U;
     const uint64_t keep = policy_keep(), drop = policy_drop();
     for (long long base = blockIdx.x * tile; base < total; base += gridDim.x * tile) {
         // (one division in 64 bits for a tile, the others in 32)
         const long long row0 = base / per_row;
         const unsigned first = (unsigned)(base - row0 * per_row), left = (unsigned)min(tile, total - base);
-        uint4 raw[EMB_U][VEC && DT == SOT_F32 ? 2 : 1];
-        T one[EMB_U];
+        uint4 raw[EMB_U][VEC ? R : R + 1];
         long long to[EMB_U];
         int id[EMB_U], col[EMB_U];
         {
@@ -99,9 +124,11 @@ __global__ void __launch_bounds__(EMB_NT) embed_kernel(const EmbedArgs a, unsign
 #pragma unroll
             for (int j = 0; j < EMB_U; ++j) {  // (a piece past the end is the tile's first one again, and is not written)
                 const unsigned i = j * EMB_NT + threadIdx.x, at = first + (i < left ? i : 0u), r = at / per_row;
-                col[j] = (int)(at - r * per_row) * W;
+                col[j] = (int)(at - r * per_row) * EMB_W;
                 t[j] = row0 + r;
-                to[j] = i < left ? t[j] * a.ldo + col[j] : -1;
+                const long long row = t[j] * a.ldo;
+                if (!VEC) col[j] -= (int)((unsigned long long)(static_cast<O*>(a.out) + row) & 15) / (int)sizeof(O);
+                to[j] = i < left && (VEC || col[j] < a.D) ? row + col[j] : NONE;
             }
             if (a.ids_type == SOT_I64) {
 #pragma unroll
@@ -115,28 +142,41 @@ __global__ void __launch_bounds__(EMB_NT) embed_kernel(const EmbedArgs a, unsign
                 for (int j = 0; j < EMB_U; ++j) id[j] = narrow[j] >= 0 && narrow[j] < a.V ? narrow[j] : -1;
             }
         }
+        // (rows of frequent tokens stay in L2, what is written does not)
+        const auto row_of = [&](int j) { return static_cast<const T*>(a.table) + (long long)max(id[j], 0) * a.ld; };
 #pragma unroll
         for (int j = 0; j < EMB_U; ++j) {  // (a row for a token without one too: a branch would wait)
-            const T* const src = static_cast<const T*>(a.table) + (long long)max(id[j], 0) * a.ld + col[j];
             if constexpr (VEC) {
-                // (rows of frequent tokens stay in L2, what is written does not)
-                raw[j][0] = load16(reinterpret_cast<const uint4*>(src), keep);
-                if constexpr (DT == SOT_F32) raw[j][1] = load16(reinterpret_cast<const uint4*>(src) + 1, keep);
-            } else
-                one[j] = *src;
+#pragma unroll
+                for (int i = 0; i < R; ++i) raw[j][i] = load16(reinterpret_cast<const uint4*>(row_of(j) + col[j]) + i, keep);
+            } else {
+                // the granules from the one with the piece's first column on, none that holds nothing of the row
+                const T* const row = row_of(j);
+                const unsigned long long lo = (unsigned long long)row & ~15ull, hi = (unsigned long long)(row + a.D - 1) & ~15ull;
+                const unsigned long long at = (unsigned long long)(row + col[j]) & ~15ull;
+#pragma unroll
+                for (int i = 0; i <= R; ++i) raw[j][i] = load16(reinterpret_cast<const uint4*>(min(max(at + 16 * i, lo), hi)), keep);
+            }
         }
 #pragma unroll
         for (int j = 0; j < EMB_U; ++j)
-            if (to[j] >= 0) {
+            if (to[j] != NONE) {
                 O* const out = static_cast<O*>(a.out) + to[j];
-                if constexpr (VEC) {
-                    float2 f[4];
-                    floats_of<DT>(raw[j], f);
+                float2 f[4];
+                if constexpr (VEC) floats_of<DT>(raw[j], f);
+                else {
+                    uint4 v[R];
+                    eight_from<DT>(raw[j], (unsigned)(unsigned long long)(row_of(j) + col[j]) & 15u, v);
+                    floats_of<DT>(v, f);
+                }
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) f[w] = id[j] >= 0 ? make_float2(f[w].x * a.scale, f[w].y * a.scale) : make_float2(0.f, 0.f);
-                    store8<DO>(out, f, drop);
-                } else
-                    *out = Elem<DO>::put(id[j] >= 0 ? Elem<DT>::get(one[j]) * a.scale : 0.f);
+                for (int w = 0; w < 4; ++w) f[w] = id[j] >= 0 ? make_float2(f[w].x * a.scale, f[w].y * a.scale) : make_float2(0.f, 0.f);
+                if (VEC || (col[j] >= 0 && col[j] + EMB_W <= a.D)) store8<DO>(out, f, drop);
+                else {
+#pragma unroll
+                    for (int w = 0; w < EMB_W; ++w)
+                        if (col[j] + w >= 0 && col[j] + w < a.D) out[w] = Elem<DO>::put(w & 1 ? f[w / 2].y : f[w / 2].x);
+                }
             }
     }
 }
@@ -658,8 +698,10 @@ bool whole_rows(const void* p, long long ld, int D, int type) {
 template <int DT, int DO>
 cudaError_t launch_embed_t(const EmbedArgs& a, int sms, cudaStream_t st) {
     const bool vec = whole_rows(a.table, a.ld, a.D, a.type) && whole_rows(a.out, a.ldo, a.D, a.out_type);
-    const unsigned per = vec ? a.D / 8 : a.D;
-    const long long tiles = (a.T * per + EMB_NT * EMB_U - 1) / (EMB_NT * EMB_U);
+    // (columns before a row's first granule of the output count as the row's)
+    const unsigned per = vec ? a.D / EMB_W : (a.D + 16 / (int)sizeof(typename Elem<DO>::T) - 1 + EMB_W - 1) / EMB_W;
+    const int tile = EMB_NT * (vec ? EMB_PIECES<true> : EMB_PIECES<false>);
+    const long long tiles = (a.T * per + tile - 1) / tile;
     const unsigned blocks = (unsigned)(tiles < 1ll << 30 ? tiles : 1ll << 30);
     if (vec) embed_kernel<DT, DO, true><<<blocks, EMB_NT, 0, st>>>(a, per);
     else embed_kernel<DT, DO, false><<<blocks, EMB_NT, 0, st>>>(a, per);
