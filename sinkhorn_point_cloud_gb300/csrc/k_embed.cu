@@ -14,8 +14,8 @@
 // No atomics on floats: repeated calls give the same bits.
 //
 // bf16, 4096 columns: 32768 lookups in fp32 77 us (0.80 of the measured copy bandwidth), 16384 tokens into 131072 rows 201 to
-// 204 us (0.87; most of it is zeros).  65001 tokens of 1001 fp32 columns into 32003 rows 131 us (0.41: rows that are not whole
-// granules are fetched 4 bytes a lane, 100 us with 1000 columns).
+// 204 us (0.87; most of it is zeros).  65001 tokens of 1001 fp32 columns into 32003 rows 124 us (0.43; 100 us with 1000 columns,
+// which need no cutting).
 #include <cuda_runtime.h>
 
 #include "embed.h"
@@ -78,9 +78,9 @@ constexpr int EMB_NT = 256, EMB_W = 8;
 template <bool VEC>
 constexpr int EMB_PIECES = VEC ? 4 : 2;
 
-// The eight elements from byte `from` on of G granules in a row.
+// The elements from byte `from` on of G granules in a row, G - 1 granules of them.
 template <int DT, int G>
-__device__ __forceinline__ void eight_from(const uint4 (&v)[G], unsigned from, uint4 (&out)[G - 1]) {
+__device__ __forceinline__ void cut_out(const uint4 (&v)[G], unsigned from, uint4 (&out)[G - 1]) {
     unsigned w[4 * G];
 #pragma unroll
     for (int i = 0; i < G; ++i) w[4 * i] = v[i].x, w[4 * i + 1] = v[i].y, w[4 * i + 2] = v[i].z, w[4 * i + 3] = v[i].w;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(EMB_NT) embed_kernel(const EmbedArgs a, unsign
                 if constexpr (VEC) floats_of<DT>(raw[j], f);
                 else {
                     uint4 v[R];
-                    eight_from<DT>(raw[j], (unsigned)(unsigned long long)(row_of(j) + col[j]) & 15u, v);
+                    cut_out<DT>(raw[j], (unsigned)(unsigned long long)(row_of(j) + col[j]) & 15u, v);
                     floats_of<DT>(v, f);
                 }
 #pragma unroll
@@ -392,17 +392,12 @@ __global__ void __launch_bounds__(SORT_NT) embed_sort_kernel(const EmbedGradArgs
 // for long batches, whose partial sums take T D / 2 bytes with 16.
 constexpr int SUM_NT = 128, SUM_MAX_R = 32;
 int chunk_tokens(long long T) { return T <= 65536 ? 16 : SUM_MAX_R; }
-// Columns of a thread: a granule of the incoming gradient, or four where its rows are not whole granules.
-template <int DT, bool VEC>
-constexpr int SUM_W = VEC ? Elem<DT>::N : 4;
+// Columns of a thread: as many as a granule of the incoming gradient has.
+template <int DT>
+constexpr int SUM_W = Elem<DT>::N;
 
 constexpr int ZERO_BYTES = 64 << 10;  // of zeros a CTA of the sums writes
 
-// The columns of a thread, of NT that share a tile: eight in a row where rows are whole granules (VEC), else NT apart.
-template <bool VEC, int NT, int W>
-__device__ __forceinline__ int sum_col(int c0, int i, int j) {
-    return VEC ? c0 + i * W + j : c0 + j * NT + i;
-}
 // W elements as floats, W * their size being 8, 16 or 32 bytes at an address aligned to that or to 16.
 template <int DG, int W>
 __device__ __forceinline__ void read_some(const typename Elem<DG>::T* p, float (&f)[W]) {
@@ -437,30 +432,33 @@ __device__ __forceinline__ void write_some(typename Elem<DG>::T* p, const float 
         }
     }
 }
-template <int DG, bool VEC, int NT, int W>
-__device__ __forceinline__ void write_row(const EmbedGradArgs& a, unsigned v, int c0, int i, const float (&acc)[W]) {
+// Where rows are not whole granules, a thread's W columns of row v begin this many before a multiple of W, so that they
+// are aligned in the row.
+template <int DG, int W>
+constexpr int SUM_ALIGN = W * sizeof(typename Elem<DG>::T) < 16 ? W * sizeof(typename Elem<DG>::T) : 16;
+template <int DG, int W, bool VEC>
+__device__ __forceinline__ int shift_of(const EmbedGradArgs& a, unsigned v) {
     using G = typename Elem<DG>::T;
-    G* const to = static_cast<G*>(a.grad) + (long long)v * a.ldg;
-    if constexpr (VEC) {
-        const int c = sum_col<VEC, NT, W>(c0, i, 0);
-        if (c >= a.D) return;
-        float f[W];
-        if (a.accumulate) read_some<DG, W>(to + c, f);
+    return VEC ? 0 : (int)((unsigned long long)(static_cast<G*>(a.grad) + (long long)v * a.ldg) & (SUM_ALIGN<DG, W> - 1)) / (int)sizeof(G);
+}
+// Columns c .. c + W - 1 of row v (c aligned as above), those outside [0, D) excepted.
+template <int DG, bool VEC, int W>
+__device__ __forceinline__ void write_row(const EmbedGradArgs& a, unsigned v, int c, const float (&acc)[W]) {
+    using G = typename Elem<DG>::T;
+    G* const to = static_cast<G*>(a.grad) + (long long)v * a.ldg + c;
+    if (c >= a.D) return;
+    if constexpr (W > 1)
+        if (VEC || (c >= 0 && c + W <= a.D)) {
+            float f[W];
+            if (a.accumulate) read_some<DG, W>(to, f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) f[j] = a.accumulate ? fmaf(a.scale, acc[j], f[j]) : a.scale * acc[j];
-        write_some<DG, W>(to + c, f);
-    } else {
-        G old[W];
-        if (a.accumulate) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) old[j] = to[min(sum_col<VEC, NT, W>(c0, i, j), a.D - 1)];
+            for (int j = 0; j < W; ++j) f[j] = a.accumulate ? fmaf(a.scale, acc[j], f[j]) : a.scale * acc[j];
+            write_some<DG, W>(to, f);
+            return;
         }
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            const int c = sum_col<VEC, NT, W>(c0, i, j);
-            if (c < a.D) to[c] = Elem<DG>::put(a.accumulate ? fmaf(a.scale, acc[j], Elem<DG>::get(old[j])) : a.scale * acc[j]);
-        }
-    }
+    for (int j = 0; j < W; ++j)
+        if (c + j >= 0 && c + j < a.D) to[j] = Elem<DG>::put(a.accumulate ? fmaf(a.scale, acc[j], Elem<DG>::get(to[j])) : a.scale * acc[j]);
 }
 // Partial sums of rows that end beyond the chunk after the one they begin in: slot 0 of a chunk is what it has of the
 // row that began before it, slot 1 of the row that goes on after it.
@@ -468,39 +466,46 @@ __device__ __forceinline__ float* part_row(const EmbedGradArgs& a, long long chu
     return a.part + (chunk * 2 + slot) * a.D;
 }
 
-// A thread's columns of several rows of the incoming gradient, fetched together: as many as registers hold.
+// A thread's columns of several rows of the incoming gradient, fetched together: as many as registers hold.  Columns that do not
+// begin at a granule are cut out of two (16-bit rows of 1003: three rows at a time 58 us, four 65; fp32 of 1001: four 124,
+// three 128).
 template <int DT, bool VEC>
 struct SumRows {
     using T = typename Elem<DT>::T;
-    static constexpr int W = SUM_W<DT, VEC>, U = 8;
-    uint4 raw[VEC ? U : 1];
-    T one[VEC ? 1 : U][W];
-    // Rows pos[i0 ..]; past `end` the last one again, past the last column that one: no branch lies between two loads.
-    __device__ __forceinline__ void load(const EmbedGradArgs& a, const unsigned* pos, int i0, int end, int c0) {
-        const T* const g = static_cast<const T*>(a.g);
+    static constexpr int W = SUM_W<DT>, U = VEC ? 8 : DT == SOT_F32 ? 4 : 3, G = VEC ? 1 : 2;
+    uint4 raw[U][G];
+    unsigned from[VEC ? 1 : U];  // the first column's byte in raw[u]
+    // Rows pos[i0 ..], columns col(i0) ..; past `end` the last one again, past the row's granules its last: no branch lies
+    // between two loads.
+    template <class Col>
+    __device__ __forceinline__ void load(const EmbedGradArgs& a, const unsigned* pos, int i0, int end, Col col) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const T* const src = g + (long long)pos[min(i0 + u, end - 1)] * a.ld;
+            const int i = min(i0 + u, end - 1), c = col(i);
+            const T* const src = static_cast<const T*>(a.g) + (long long)pos[i] * a.ld;
             if constexpr (VEC)
-                raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + min(sum_col<VEC, SUM_NT, W>(c0, threadIdx.x, 0), a.D - W)));
+                raw[u][0] = __ldcs(reinterpret_cast<const uint4*>(src + min(c, a.D - W)));
             else {
+                const unsigned long long lo = (unsigned long long)src & ~15ull, hi = (unsigned long long)(src + a.D - 1) & ~15ull;
+                const unsigned long long at = (unsigned long long)(src + c);
+                from[u] = (unsigned)at & 15u;
 #pragma unroll
-                for (int j = 0; j < W; ++j) one[u][j] = src[min(sum_col<VEC, SUM_NT, W>(c0, threadIdx.x, j), a.D - 1)];
+                for (int j = 0; j < G; ++j)
+                    raw[u][j] = __ldg(reinterpret_cast<const uint4*>(min(max((at & ~15ull) + 16 * j, lo), hi)));
             }
         }
     }
+    // (columns outside the row get anything)
     __device__ __forceinline__ void add(int u, float (&acc)[W]) const {
-        if constexpr (VEC) {
-            float2 f[W / 2];
-            unpack<DT>(raw[u], f);
+        uint4 v[1];
+        if constexpr (VEC) v[0] = raw[u][0];
+        else cut_out<DT>(raw[u], from[u], v);
+        float2 f[W / 2];
+        unpack<DT>(v[0], f);
 #pragma unroll
-            for (int j = 0; j < W / 2; ++j) {
-                acc[2 * j] += f[j].x;
-                acc[2 * j + 1] += f[j].y;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < W; ++j) acc[j] += Elem<DT>::get(one[u][j]);
+        for (int j = 0; j < W / 2; ++j) {
+            acc[2 * j] += f[j].x;
+            acc[2 * j + 1] += f[j].y;
         }
     }
 };
@@ -511,7 +516,7 @@ constexpr int FEW_TOKENS = 512;
 
 template <int DT, int DG, bool VEC>
 __global__ void __launch_bounds__(SUM_NT, 8) embed_few_kernel(const EmbedGradArgs a, int tiles, long long zeros, int zero_share) {
-    constexpr int U = SumRows<DT, VEC>::U, W = SUM_W<DT, VEC>, PER = FEW_TOKENS / SUM_NT;
+    constexpr int U = SumRows<DT, VEC>::U, W = SUM_W<DT>, PER = FEW_TOKENS / SUM_NT;
     __shared__ int ids[FEW_TOKENS];
     __shared__ unsigned mark[FEW_TOKENS > ZERO_BYTES / 32 ? FEW_TOKENS : ZERO_BYTES / 32];  // rows of this CTA; or the row's tokens
     __shared__ int length;
@@ -552,22 +557,22 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_few_kernel(const EmbedGradArg
         if (lane == 0) length = n;
     }
     __syncthreads();
-    const int n = length;
+    const int n = length, col = c0 + tid * W - shift_of<DG, W, VEC>(a, (unsigned)v);
     float acc[W] = {};
     for (int i0 = 0; i0 < n; i0 += U) {
         SumRows<DT, VEC> rows;
-        rows.load(a, pos, i0, n, c0);
+        rows.load(a, pos, i0, n, [&](int) { return col; });
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i0 + u < n) rows.add(u, acc);
     }
-    write_row<DG, VEC, SUM_NT, W>(a, (unsigned)v, c0, tid, acc);
+    write_row<DG, VEC, W>(a, (unsigned)v, col, acc);
 }
 
 template <int DT, int DG, bool VEC>
 __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArgs a, int tiles, long long zeros, long long zero_from,
                                                               int zero_share) {
-    constexpr int SUM_U = SumRows<DT, VEC>::U, W = SUM_W<DT, VEC>;
+    constexpr int SUM_U = SumRows<DT, VEC>::U, W = SUM_W<DT>;
     __shared__ unsigned key[2 * SUM_MAX_R + 1], pos[2 * SUM_MAX_R];
     const int R = a.chunk;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -604,10 +609,11 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
     const unsigned tail = row(n - 1);
     if (n == R && row(R) == tail && !(open && key[1] == tail) && long_after != tail)
         while (end < 2 * R && row(end) == tail) ++end;
+    const auto col = [&](unsigned v) { return c0 + tid * W - shift_of<DG, W, VEC>(a, v); };
     float acc[W] = {};
     for (int i0 = from; i0 < end; i0 += SUM_U) {
         SumRows<DT, VEC> rows;
-        rows.load(a, pos, i0, end, c0);
+        rows.load(a, pos, i0, end, [&](int i) { return col(row(i)); });
 #pragma unroll
         for (int u = 0; u < SUM_U; ++u)
             if (i0 + u < end) {
@@ -618,14 +624,13 @@ __global__ void __launch_bounds__(SUM_NT, 8) embed_sum_kernel(const EmbedGradArg
                     const bool before = open && from == 0 && key[1] == v, after = row(i + 1) == v;
                     if (before || after) {
                         float* const to = part_row(a, chunk, before ? 0 : 1);
+                        const int c = col(v);
 #pragma unroll
-                        for (int j = 0; j < W; ++j) {
-                            const int c = sum_col<VEC, SUM_NT, W>(c0, tid, j);
-                            if (c < a.D) __stcg(to + c, acc[j]);
-                        }
+                        for (int j = 0; j < W; ++j)
+                            if (c + j >= 0 && c + j < a.D) __stcg(to + c + j, acc[j]);
                         if (!before && tid == 0 && c0 == 0) a.span[atomicAdd(a.spans, 1u)] = make_uint2((unsigned)chunk, v);
                     } else
-                        write_row<DG, VEC, SUM_NT, W>(a, v, c0, tid, acc);
+                        write_row<DG, VEC, W>(a, v, col(v), acc);
 #pragma unroll
                     for (int j = 0; j < W; ++j) acc[j] = 0.f;
                 }
@@ -676,15 +681,15 @@ __global__ void __launch_bounds__(JOIN_NT, 4) embed_join_kernel(const EmbedGradA
 #pragma unroll
         for (int j = 0; j < 4; ++j) sums[warp][j * 32 + lane] = acc[j];
         __syncthreads();
-        if (tid < JOIN_COLS / 8) {
-            float f[8];
+        constexpr int W = VEC ? 8 : 1;
+        if (tid < JOIN_COLS / W) {
+            float f[W];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int at = sum_col<VEC, JOIN_COLS / 8, 8>(0, tid, j);
-                f[j] = sums[0][at];
-                for (int k = 1; k < JOIN_NW; ++k) f[j] += sums[k][at];
+            for (int j = 0; j < W; ++j) {
+                f[j] = sums[0][tid * W + j];
+                for (int k = 1; k < JOIN_NW; ++k) f[j] += sums[k][tid * W + j];
             }
-            write_row<DG, VEC, JOIN_COLS / 8, 8>(a, span.y, c0, tid, f);
+            write_row<DG, VEC, W>(a, span.y, c0 + tid * W, f);
         }
         __syncthreads();
     }
@@ -757,8 +762,8 @@ cudaError_t launch_sort(const EmbedGradArgs& a, const EmbedGradPlan& p, int sms,
 template <int DT, int DG>
 cudaError_t launch_sum(const EmbedGradArgs& a, const EmbedGradPlan& p, bool vec, int sms, cudaStream_t st) {
     EmbedGradArgs b = a;
-    const int cols = SUM_NT * (vec ? SUM_W<DT, true> : SUM_W<DT, false>);
-    int tiles = (a.D + cols - 1) / cols, join_tiles = (a.D + JOIN_COLS - 1) / JOIN_COLS;
+    constexpr int W = SUM_W<DT>, cols = SUM_NT * W, shift = SUM_ALIGN<DG, W> / sizeof(typename Elem<DG>::T) - 1;
+    int tiles = (a.D + (vec ? 0 : shift) + cols - 1) / cols, join_tiles = (a.D + JOIN_COLS - 1) / JOIN_COLS;
     const bool few = p.passes == 0;
     long long from = few ? 0 : early_rows(a), zeros = 0;
     int share = 1;
