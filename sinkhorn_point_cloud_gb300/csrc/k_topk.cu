@@ -1,6 +1,8 @@
 // k_topk.cu -- how the rows of the scores kernel (topk.cuh) and of its gradient are cut.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "kernels.h"
 #include "topk.cuh"
 
@@ -36,7 +38,9 @@ void topk_plan(bool whole, const TopkArgs& a, int sms, TopkPlan* p) {
     p->L.chunks = a.K ? (int)((G + p->U * p->NT - 1) / (p->U * p->NT)) * p->NT : 0;
     const int most = (CL > 2 ? CL : 2) * a.K;  // candidates to sort, or slices' alternatives to join
     p->L.cap = a.K ? pow2_from(most > 256 ? most : 256) : 0;
-    const long long bytes = (long long)(sizeof(unsigned long long) + sizeof(int)) * p->L.cap + sizeof(unsigned) * p->L.chunks;
+    // candidates, chunks to look at again, and the chunks' maxima, where the candidates are put in order later
+    const long long last = std::max<long long>(sizeof(unsigned) * p->L.chunks, sizeof(unsigned long long) * p->L.cap);
+    const long long bytes = (long long)(sizeof(unsigned long long) + sizeof(int)) * p->L.cap + last;
     p->L.bytes = (int)(bytes < TOPK_MAX_SMEM + 1 ? bytes : TOPK_MAX_SMEM + 1);
 }
 
