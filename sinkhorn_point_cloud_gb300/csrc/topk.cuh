@@ -212,17 +212,26 @@ __device__ __forceinline__ uint4 inside(const uint4& v, int e, int V) {
     return pack<DT>(f);
 }
 
-// Calls use(logit, column) for the elements of granule g of a slice (-inf outside the row).
+// Calls use(logits, first column) for granule g of a slice (-inf outside the row), or use(logit, column) for its elements.
 template <int DT, class Use>
-__device__ __forceinline__ void each_logit(const Slice& s, int g, int V, Use use) {
+__device__ __forceinline__ void each_granule(const Slice& s, int g, int V, Use use) {
     constexpr int N = Elem<DT>::N;
     uint4 v = s.src[g];
     const int e = s.e0 + g * N;
     if (g < s.lo || g >= s.hi) v = inside<DT>(v, e, V);
     float2 f[N / 2];
     unpack<DT>(v, f);
+    float x[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) use(i & 1 ? f[i / 2].y : f[i / 2].x, e + i);
+    for (int i = 0; i < N; ++i) x[i] = i & 1 ? f[i / 2].y : f[i / 2].x;
+    use(x, e);
+}
+template <int DT, class Use>
+__device__ __forceinline__ void each_logit(const Slice& s, int g, int V, Use use) {
+    each_granule<DT>(s, g, V, [&](const float (&x)[Elem<DT>::N], int col) {
+#pragma unroll
+        for (int i = 0; i < Elem<DT>::N; ++i) use(x[i], col + i);
+    });
 }
 
 // The K largest of the n numbers of v in order, zeros behind them where there are fewer (a 0 among them is a place that a
@@ -361,6 +370,7 @@ __device__ __forceinline__ unsigned warp_threshold(const unsigned (&key)[R], uns
 template <int DT, int NT, int U>
 __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* ckey, unsigned best, int C, const Slice& s, int V, int K,
                                             int cap, unsigned long long* cand, int* hit, unsigned long long* spare) {
+    constexpr int N = Elem<DT>::N;
     const int tid = team_tid<NT>(), lane = tid & 31;
     const unsigned floor = Key<DT>::NOTHING + 1;
     unsigned at, top;  // a threshold that K logits reach (or all there are); the largest key
@@ -457,17 +467,25 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
         for (unsigned i = tid; i < hits * U; i += NT) {
             const int c = hit[i / U], g = c / NT * U * NT + c % NT + (int)(i % U) * NT;
             if (g < s.ng)
-                each_logit<DT>(s, g, V, [&](float x, int col) {
-                    if (x >= least) {
-                        const unsigned k = atomicAdd(&sh.found, 1u);
-                        if (k < (unsigned)cap) cand[k] = pair_of(Key<DT>::of(x), col);
-                    }
+                each_granule<DT>(s, g, V, [&](const float (&x)[N], int col) {
+                    unsigned on = 0;
+#pragma unroll
+                    for (int j = 0; j < N; ++j) on |= x[j] >= least ? 1u << j : 0u;
+                    if (on == 0) return;
+                    unsigned k = atomicAdd(&sh.found, (unsigned)__popc(on));
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        if (on >> j & 1u) {
+                            if (k < (unsigned)cap) cand[k] = pair_of(Key<DT>::of(x[j]), col + j);
+                            ++k;
+                        }
                 });
         }
         team_sync<NT>();
         return sh.found;
     };
-    unsigned n = gather(at);
+    // (Where nearly every chunk has a candidate there are more of them than places, which need not be found out.)
+    unsigned n = 5ll * K > 4ll * ((s.ng + U - 1) / U) && s.ng > cap / N ? cap + 1u : gather(at);
     if (n > (unsigned)cap) {
         // Many large logits in few chunks, or many equal ones: a threshold that enough of them reach and not too many, by counting
         // over the whole slice.  Where there is none this ends at the K-th largest logit itself: those above it, and as many of
