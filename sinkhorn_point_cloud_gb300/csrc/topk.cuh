@@ -7,7 +7,7 @@
 // chunks have a maximum that is not below the K-th largest chunk maximum, so neither is the row's
 // K-th largest logit: only chunks that reach this threshold, about K of them, are read again (from L2) for the
 // K best.  The logits are read once: 4096 rows of 131072 bf16 take 156 us with K = 0 (1.02 of the measured copy
-// bandwidth).  K = 64 takes 206: a row's selection is a chain of shared-memory steps (threshold, second look, order) that ends with
+// bandwidth).  K = 64 takes 206 (2048 rows and K = 200: 144): a row's selection is a chain of shared-memory steps (threshold, second look, order) that ends with
 // its CTA's registers idle, and the rows beside it do not cover all of it.
 // The gradient is one pass with the stored lse: 8192 rows of 65536 bf16, a third left out, 270 us (0.97).
 #pragma once
