@@ -143,6 +143,36 @@ def test_many_long_rows(sot, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,V,Ks", [(40, 300, (17, 65, 250)), (40, 1000, (32, 100, 250)), (40, 1600, (120, 200)),
+                                    (40, 4090, (65, 129, 256)), (200, 5000, (64, 65, 200)), (200, 9001, (97, 257)),
+                                    (160, 70001, (96, 97, 128, 200)), (2, 70001, (65, 128, 400))])
+def test_alternatives_of_all_kinds_of_rows(sot, T, V, Ks, dtype):
+    """Ordinary rows, few distinct values, large ones side by side, masks that leave fewer than K, values far apart."""
+    rng = np.random.default_rng(V)
+    kinds = normal(9, V, seed=V, scale=2.0)
+    kinds[1] = np.round(kinds[1])
+    kinds[2] = np.round(kinds[2] * 4) / 4
+    kinds[3, :V // 3] += 20.0
+    kinds[4, rng.permutation(V)[:V - Ks[0] // 2]] = -np.inf
+    kinds[5, rng.permutation(V)[:V - Ks[-1] - 1]] = LOWEST[dtype]
+    kinds[6] = np.where(kinds[6] > 0, np.exp(4 * kinds[6]).clip(0, 6e4), -np.exp(-4 * kinds[6]).clip(0, 6e4))
+    kinds[7] = np.where(np.arange(V) % 8 == 3, 3.0, kinds[7])
+    kinds[8, :] = 0.0
+    kinds[8, V - 20:] = np.arange(20)
+    which = np.arange(T) % 9
+    x = put(kinds, dtype, 5, 1)
+    many = torch.full((T, V + 5), float("nan"), dtype=x.dtype, device="cuda")
+    many[:, 2:V + 2] = x[torch.from_numpy(which).cuda()] if T > 9 else x[:T]
+    for K in Ks:
+        with np.errstate(all="ignore"):
+            _, rl, _, ri, rt = R.token_topk(host(x), None, K, 1.0)
+        _, lse, _, ids, top = sot.sot_token_topk(many[:, 2:V + 2], K)
+        assert np.array_equal(ids.cpu().numpy(), ri[which])
+        near(lse, rl[which], ATOL + RTOL * np.abs(rl)[which])
+        near(top, rt[which], ATOL + RTOL * np.where(np.isfinite(rt), np.abs(rt), 0)[which])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("V", [300, 5000, 70001])
 def test_equal_logits_go_by_column(sot, V, dtype):
     rng = np.random.default_rng(V)
