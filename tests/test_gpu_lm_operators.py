@@ -388,6 +388,28 @@ def test_embed_grad(sot, T, V, D, src, dst):
         assert (host(old)[~named] == 0.25).all() and (old[:, D:] == 0.25).all()  # nothing else is touched
 
 
+@pytest.mark.parametrize("src,dst", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32"), ("f32", "f16")])
+@pytest.mark.parametrize("T", [63, 64, 65, 512, 513, 1000, 1024, 1025])
+def test_embed_grad_of_rows_with_many_tokens(sot, T, src, dst):
+    """One row with every token, two with half each, one with two thirds among ordinary ones, at widths that end inside
+    a thread's columns and a tile."""
+    rng = np.random.default_rng(T)
+    V = 50
+    for D, pad, shift in ((8, 0, 0), (1003, 2, 1), (1500, 4, 0), (2057, 0, 1)):
+        g = put(rng.standard_normal((T, D)), src, pad, shift)
+        for ids in (np.full(T, V - 1), np.arange(T) % 2 * 7, np.where(rng.random(T) < 0.67, 3, rng.integers(-2, V + 2, T))):
+            i = torch.from_numpy(ids).cuda()
+            ref, size = R.embed_grad(host(g), ids, V, 1.0)
+            chain = 2.0 ** -24 * (64 + 16 + T / 16)  # up to 63 tokens in a chain, or a sixteenth of a row's and sixteen sums
+            got = sot.sot_embed_grad(g, i, V, dtype=TYPES[dst])
+            near(got, ref, HALF_ULP[dst] * np.abs(ref) + chain * size + TINY[dst])
+            assert torch.equal(sot.sot_embed_grad(g, i, V, dtype=TYPES[dst]), got)
+            old = torch.full((V, D + 3), 0.5, dtype=TYPES[dst], device="cuda")
+            sot.sot_embed_grad(g, i, V, grad=old[:, :D], accumulate=True)
+            near(old[:, :D], ref + 0.5, HALF_ULP[dst] * np.abs(ref + 0.5) + chain * size + 2.0 ** -24 * (0.5 + size) + TINY[dst])
+            assert (old[:, D:] == 0.5).all()
+
+
 def test_embed_without_tokens(sot):
     g, ids = torch.zeros(0, 24, device="cuda"), torch.zeros(0, dtype=torch.int64, device="cuda")
     grad = torch.full((9, 24), 3.0, device="cuda")
