@@ -8,8 +8,8 @@
 //            the launch fill the time with zeros for the table's first rows;
 //   sum      a CTA takes a chunk of sorted tokens and a tile of columns, and writes
 //            the rows that begin in its chunk and end there or in the next one.  A row that spans more leaves a partial sum in
-//            each chunk.  Other CTAs, in between, write the zeros of the remaining rows that no token names (reads and writes at the same
-//            time: writes alone reach 0.8 of the copy bandwidth);
+//            each chunk.  Other CTAs, in between, write the zeros of the remaining rows that no token names (reads and
+//            writes at the same time: writes alone reach 0.8 of the copy bandwidth);
 //   join     adds up the partial sums, in a fixed order.
 // No atomics on floats: repeated calls give the same bits.
 //

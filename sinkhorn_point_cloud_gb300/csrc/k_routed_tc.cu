@@ -3,8 +3,8 @@
 // After the scores (k_routed.cu) one cooperative kernel, a CTA an SM, does the rest:
 //   choose  the tokens' experts (few tokens: every CTA for itself), then every CTA each expert's list of tokens;
 //   up      products gate_up x^T: an expert's rows are the M of a tcgen05.mma (64 gate rows and the 64 up rows that
-//           belong to them), its tokens the N.  The units of all experts (16 KB of weights, K = 64, or twice that) are dealt out evenly, so a
-//           CTA starts and ends inside a tile; it leaves a partial sum for each piece;
+//           belong to them), its tokens the N.  The units of all experts (16 KB of weights, K = 64, or twice that) are
+//           dealt out evenly, so a CTA starts and ends inside a tile; it leaves a partial sum for each piece;
 //   act     h = silu(gate) up of the joined pieces, rounded to the type;
 //   down    products down h^T, the same way;
 //   join    the weighted sum over a token's experts.

@@ -7,8 +7,8 @@
 // chunks have a maximum that is not below the K-th largest chunk maximum, so neither is the row's
 // K-th largest logit: only chunks that reach this threshold, about K of them, are read again (from L2) for the
 // K best.  The logits are read once: 4096 rows of 131072 bf16 take 156 us with K = 0 (1.02 of the measured copy
-// bandwidth).  K = 64 takes 206 (2048 rows and K = 200: 144): a row's selection is a chain of shared-memory steps (threshold, second look, order) that ends with
-// its CTA's registers idle, and the rows beside it do not cover all of it.
+// bandwidth).  K = 64 takes 206 (2048 rows and K = 200: 144): a row's selection is a chain of shared-memory steps (threshold,
+// second look, order) that ends with its CTA's registers idle, and the rows beside it do not cover all of it.
 // The gradient is one pass with the stored lse: 8192 rows of 65536 bf16, a third left out, 270 us (0.97).
 #pragma once
 #include <cuda_runtime.h>
@@ -348,6 +348,14 @@ __device__ __forceinline__ void order(SelectSmem<NT>& sh, unsigned long long* v,
     team_sync<NT>();
 }
 
+// A key in (lo, hi], of finite values: half of the way in value, or in keys.  (Logits lie evenly in value, where a few steps
+// find a threshold; taking turns, no rows need more than twice a key's bits.)
+template <int DT>
+__device__ __forceinline__ unsigned between(unsigned lo, unsigned hi, bool linear) {
+    const float mid = 0.5f * Key<DT>::value(lo) + 0.5f * Key<DT>::value(hi);
+    return linear ? min(max(Key<DT>::of(mid), lo + 1), hi) : lo + (hi - lo + 1) / 2;
+}
+
 // The largest threshold in [lo, hi] that K of the numbers of a warp reach (lo does), R of them a lane; one that not
 // more than `enough` reach will do.
 template <int R>
@@ -417,8 +425,9 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
         // The same with the chunks' maxima, which are more.
         unsigned lo = 0xffffffffu, hi = 0;
         for (int c = tid; c < C; c += NT) {
-            lo = min(lo, ckey[c]);
-            hi = max(hi, ckey[c]);
+            const unsigned k = ckey[c];
+            if (k >= floor) lo = min(lo, k);
+            hi = max(hi, k);
         }
         lo = __reduce_min_sync(0xffffffffu, lo);
         hi = __reduce_max_sync(0xffffffffu, hi);
@@ -440,8 +449,8 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
         hi = max(hi, lo);
         top = hi;
         if (C < K || reach(lo) < (unsigned)K) lo = hi = floor;
-        while (lo < hi) {
-            const unsigned mid = lo + (hi - lo + 1) / 2, n = reach(mid);
+        for (bool linear = true; lo < hi; linear = !linear) {
+            const unsigned mid = between<DT>(lo, hi, linear), n = reach(mid);
             if (n >= (unsigned)K) lo = mid;
             else hi = mid - 1;
             if (n >= (unsigned)K && n <= (unsigned)(K + K / 4)) break;
@@ -496,8 +505,8 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
             for (int g = tid; g < s.ng; g += NT) each_logit<DT>(s, g, V, [&](float x, int) { n += x >= least; });
             return team_count<NT>(sh, n, step);
         };
-        while (at < top && n > (unsigned)cap) {
-            const unsigned mid = at + (top - at + 1) / 2, reached = above(mid);
+        for (bool linear = true; at < top && n > (unsigned)cap; linear = !linear) {
+            const unsigned mid = between<DT>(at, top, linear), reached = above(mid);
             if (reached >= (unsigned)K) at = mid, n = reached;
             else top = mid - 1;
         }
