@@ -20,7 +20,9 @@ void topk_plan(bool whole, const TopkArgs& a, int sms, TopkPlan* p) {
     const int N = a.dtype == SOT_F32 ? 4 : 8;
     const long long total = ((long long)a.V + (whole ? N - 1 : 2 * N - 2)) / N;  // granules of a row
     int CL = 1;
-    if (total <= 512 && a.K <= 256) p->NT = 32;
+    // A warp takes a short row where there are more of them than CTAs of 128 threads find room, or little to select
+    // (V = 4000 bf16, K = 64: 300 rows 15.3 us, with a CTA a row 8.6; 2400 rows 19.8 and 21.6.  V = 1000, K = 8: 1200 rows 6.9 and 9.2).
+    if (total <= 512 && a.K <= 256 && (a.T > 8ll * sms || (total <= 128 && a.K <= 16))) p->NT = 32;
     else if (a.T < sms || total > 8192) p->NT = 256;
     else p->NT = 128;
     // Few rows: cut a row further, up to eight granules a thread and a CTA for each SM, as far as the

@@ -236,8 +236,9 @@ __device__ __forceinline__ void each_logit(const Slice& s, int g, int V, Use use
 
 // The K largest of the n numbers of v in order, zeros behind them where there are fewer (a 0 among them is a place that a
 // slice could not fill).  A few are placed by counting the larger ones of each.  More are first shared out over BINS bins by
-// their key's distance from the largest, so that only those of a bin are counted.  (n steps of a sorting network or of
-// counting were half of the time: 4096 x 5000 bf16, K = 200: 66 us, was 100.)  Where one bin has many, the network does it.
+// their key's distance from the largest, so that only those of a bin are counted.  (Steps of a
+// sorting network were a third of the time: 4096 x 5000 bf16, K = 200 took 100 us with it, 66 like this, and 58 with the
+// search in between().)  Where one bin has many, the network does it.
 // bins: BINS places; to: n of them.
 template <int NT>
 __device__ __forceinline__ void order(SelectSmem<NT>& sh, unsigned long long* v, int n, int K, int* bins, unsigned long long* to) {

@@ -145,7 +145,8 @@ def test_many_long_rows(sot, V, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T,V,Ks", [(40, 300, (17, 65, 250)), (40, 1000, (32, 100, 250)), (40, 1600, (120, 200)),
                                     (40, 4090, (65, 129, 256)), (200, 5000, (64, 65, 200)), (200, 9001, (97, 257)),
-                                    (160, 70001, (96, 97, 128, 200)), (2, 70001, (65, 128, 400))])
+                                    (1300, 300, (9, 17, 65, 250)), (1300, 1000, (32, 100, 250)), (1300, 1600, (120, 200)),
+                                    (1300, 4090, (16, 65, 129, 256)), (160, 70001, (96, 97, 128, 200)), (2, 70001, (65, 128, 400))])
 def test_alternatives_of_all_kinds_of_rows(sot, T, V, Ks, dtype):
     """Ordinary rows, few distinct values, large ones side by side, masks that leave fewer than K, values far apart."""
     rng = np.random.default_rng(V)
