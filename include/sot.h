@@ -483,8 +483,9 @@ int sot_embed_grad(const void* grad_out, long long T, int D, long long ld, int t
  * 1 <= K <= min(E, 32), E <= 1024.  A logit of -inf (a bias of -inf) removes an expert; where a token has fewer than K
  * left, the rest of its ids are -1 with weight 0.  A token with a logit of NaN or +inf has ids -1, weights NaN and an
  * output of NaN.  Sums are held in 32 bits.  Where the type has 16 bits, H and F are multiples of 8, x, gate_up and down
- * are 16-byte aligned and ld is a multiple of 8, the products run on the tensor cores and silu(.) * (.) is rounded to the
- * type before the second one.  There a wait that runs out of time gives an output of NaN and SOT_ERR_TIMEOUT
+ * are 16-byte aligned and ld is a multiple of 8, the products run on the tensor cores, where silu(.) * (.) is the sum of two
+ * numbers of the type (fp16: times a power of two a token and expert, so that its range is that of 32 bits): good to 2^-17
+ * (bf16) or 2^-22 (fp16) of itself.  There a wait that runs out of time gives an output of NaN and SOT_ERR_TIMEOUT
  * from sot_async_status.
  * logits, ids and weights are what sot_balance_loss takes and what a backward pass needs; out [T][H] has
  * row stride ld_out and must not overlap the inputs.

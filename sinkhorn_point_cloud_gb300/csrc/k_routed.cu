@@ -30,13 +30,13 @@ __device__ __forceinline__ void add_product(float2& s, float2& low, float2 x, fl
     s = t;
 }
 template <int DT>
-__global__ void __launch_bounds__(NT) routed_scores_kernel(const RoutedArgs a, int tokens, bool whole, unsigned* barrier) {
+__global__ void __launch_bounds__(NT) routed_scores_kernel(const RoutedArgs a, int tokens, bool whole, unsigned* zero, int zeros) {
     using T = typename Elem<DT>::T;
     constexpr int N = Elem<DT>::N;
     __shared__ float2 part[NW];
     __shared__ float plain[NW];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (barrier && blockIdx.x == 0 && threadIdx.x < 4) barrier[threadIdx.x] = 0;
+    for (int i = blockIdx.x * NT + threadIdx.x; i < zeros; i += gridDim.x * NT) zero[i] = 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, splits = NW / tokens;
     const int e = blockIdx.x % a.E, t = blockIdx.x / a.E * tokens + warp / splits, split = warp % splits;
     float2 s = make_float2(0.f, 0.f), low = s;
@@ -75,13 +75,13 @@ __global__ void __launch_bounds__(NT) routed_scores_kernel(const RoutedArgs a, i
     a.logits[(long long)t * a.E + e] = fabsf(all) < INFINITY ? sum.x + sum.y : all;
 }
 template <int DT>
-cudaError_t launch_scores(const RoutedArgs& a, unsigned* barrier, cudaStream_t st) {
+cudaError_t launch_scores(const RoutedArgs& a, unsigned* zero, int zeros, cudaStream_t st) {
     int tokens = 1;
     while (tokens < NW && tokens < a.T) tokens *= 2;
     const bool whole = a.H % Elem<DT>::N == 0 && a.ldx % Elem<DT>::N == 0 && (unsigned long long)a.x % 16 == 0 &&
                        (unsigned long long)a.router % 16 == 0;
     count_launches(1);
-    routed_scores_kernel<DT><<<a.E * ((a.T + tokens - 1) / tokens), NT, 0, st>>>(a, tokens, whole, barrier);
+    routed_scores_kernel<DT><<<a.E * ((a.T + tokens - 1) / tokens), NT, 0, st>>>(a, tokens, whole, zero, zeros);
     return cudaGetLastError();
 }
 
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(NT) routed_join_kernel(const RoutedArgs a) {
 template <int DT>
 cudaError_t launch_plain(const RoutedArgs& a, cudaStream_t st) {
     const int up = (a.F + NW - 1) / NW, down = (a.H + NW - 1) / NW;
-    const cudaError_t e = launch_scores<DT>(a, nullptr, st);
+    const cudaError_t e = launch_scores<DT>(a, nullptr, 0, st);
     if (e != cudaSuccess) return e;
     count_launches(4);
     routed_choose_kernel<<<(a.T + NW - 1) / NW, NT, 0, st>>>(a);
@@ -189,8 +189,9 @@ RoutedPlan routed_plan(const RoutedArgs& a, int sms) {
 cudaError_t launch_routed(RoutedArgs a, const RoutedPlan& p, unsigned char* scratch, int sms, cudaStream_t st) {
     if (a.T == 0) return cudaSuccess;
     if (p.tc) {
-        unsigned* const barrier = reinterpret_cast<unsigned*>(scratch + p.on_tc.barrier_at);
-        const cudaError_t e = a.dtype == SOT_BF16 ? launch_scores<SOT_BF16>(a, barrier, st) : launch_scores<SOT_F16>(a, barrier, st);
+        unsigned* const zero = reinterpret_cast<unsigned*>(scratch + p.on_tc.barrier_at);
+        const int zeros = p.on_tc.zeros;
+        const cudaError_t e = a.dtype == SOT_BF16 ? launch_scores<SOT_BF16>(a, zero, zeros, st) : launch_scores<SOT_F16>(a, zero, zeros, st);
         return e != cudaSuccess ? e : launch_routed_tc(a, p.on_tc, scratch, sms, st);
     }
     a.h = reinterpret_cast<float*>(scratch + p.h_at);

@@ -5,17 +5,17 @@
 //   up      products gate_up x^T: an expert's rows are the M of a tcgen05.mma (64 gate rows and the 64 up rows that
 //           belong to them), its tokens the N.  The units of all experts (16 KB of weights, K = 64, or twice that) are
 //           dealt out evenly, so a CTA starts and ends inside a tile; it leaves a partial sum for each piece;
-//   act     h = silu(gate) up of the joined pieces, rounded to the type;
-//   down    products down h^T, the same way;
+//   act     h = silu(gate) up of the joined pieces, as a sum of two numbers of the type;
+//   down    products down h^T, the same way, both parts of h into one accumulator;
 //   join    the weighted sum over a token's experts.
 // The weights are read once and bound it.  They come by TMA through a ring of stages, 16 or 32 KB each, from a warp that waits
 // for nothing but free stages: across the phases' grid barriers the next phase's weights are already on their way.
 // Every wait is bounded; one that runs out ends the call with NaN outputs and the timeout status.
 //
-// bf16, H = 4096, F = 1408, 8 of 128 experts, 64 tokens: 646 us for 4.36 GB, 0.99 of the measured copy bandwidth.  H = 2048,
-// F = 1024, 8 of 64 experts: one token 30.6 us for 101 MB (about 4.5 us until the first weights, 16 of weights, the rest waits of
-// phases on one another), 8 tokens 99 us, 128 tokens 157 us (0.76: the tokens' side of the units takes a third of the
-// ring).
+// bf16, H = 4096, F = 1408, 8 of 128 experts, 64 tokens: 650 us for 4.36 GB, 0.99 of the measured copy bandwidth.  H = 2048,
+// F = 1024, 8 of 64 experts: one token 31.3 us for 101 MB (about 4.5 us until the first weights, 16 of weights, the rest waits of
+// phases on one another), 8 tokens 98 us, 128 tokens 158 us (fp16 160; 0.75: the tokens' side of the units takes a third of
+// the ring and more).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -41,14 +41,18 @@ struct Layout {  // byte offsets in dynamic shared memory (from a 1024-byte boun
     int ring, most;  // bytes of the ring; tokens that an expert may have, in sixteens
     int bars, weight, toks, list, act, id, info, mask, place, total;
 };
-// How the ring is cut for experts of at most npad tokens.
+// Numbers of the type that h is the sum of.  One alone would be most of the output's error (bf16: 2.4e-3 of it, where its
+// own rounding makes 1.6e-3); two cost 0 to 5 % (one token 31.3 us, was 30.7; 37 fp16 tokens of 10 experts 44.6, was 42.5).
+constexpr int PARTS = 2;
+
+// How the ring is cut for experts of at most npad tokens: weights, then the parts of the tokens' side of each slice.
 struct Cut {
     int npad, wide;  // wide: slices of KSTEP columns in a unit: two where that leaves four stages (a unit costs the
                      // multiplying thread 250 ns whatever its width), else one
-    int stage, stages;
-    __host__ __device__ Cut(int npad_, int ring) : npad(npad_) {
-        wide = 4 * 2 * (A_BYTES + npad * KSTEP * 2) <= ring ? 2 : 1;
-        stage = wide * (A_BYTES + npad * KSTEP * 2);
+    int part, stage, stages;
+    __host__ __device__ Cut(int npad_, int ring) : npad(npad_), part(npad_ * KSTEP * 2) {
+        wide = 4 * 2 * (A_BYTES + PARTS * part) <= ring ? 2 : 1;
+        stage = wide * (A_BYTES + PARTS * part);
         stages = ring / stage;
         if (stages > MAX_STAGES) stages = MAX_STAGES;
     }
@@ -60,7 +64,8 @@ struct TcArgs {
     unsigned* barrier;   // [4] grid barriers, zeroed by the scores' kernel
     unsigned* status;    // the device's status word
     float* part[PHASES];  // [pieces][T K][2 F or H]
-    void* h;              // [T K][F]
+    unsigned* peak;       // fp16: [2][T K] largest |gate| and |up| of a pair's pieces, as bits; zeroed like the barriers
+    void* h;              // [PARTS][T K][F]
     int pieces[PHASES];   // of a tile, at most
     bool fused;           // the loading warps form h
 };
@@ -113,7 +118,8 @@ struct Ctx {
     int KS[PHASES], tiles[PHASES];
     int chunk[PHASES];  // units of a CTA
     int first[PHASES], end[PHASES];
-    int npad, wide, stage, S;  // the ring's cut
+    int npad, wide, part, stage, S;  // the ring's cut
+    int doublings;                   // of a bound: a tile has at most two to this many pieces
     __device__ __forceinline__ uint32_t full(int s) const { return bars + 8 * s; }
     __device__ __forceinline__ uint32_t empty(int s) const { return bars + 8 * (MAX_STAGES + s); }
     __device__ __forceinline__ uint32_t accfull(int b) const { return bars + 8 * (2 * MAX_STAGES + b); }
@@ -199,7 +205,7 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
     const int stages = c.S;
     const uint64_t a0 = sw128_desc(c.base), step = c.stage >> 4;
     const int wide = c.wide;
-    const uint64_t tokens = wide * A_BYTES >> 4, slice = c.npad * KSTEP * 2 >> 4;
+    const uint64_t tokens = wide * A_BYTES >> 4, part = c.part >> 4;
     Turn at;
     int seg = 0;
     bool ok = true, issued = false;
@@ -217,12 +223,15 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
                 tc_fence_after();
                 const uint64_t a = a0 + at.s * step, b = a + tokens;
                 if (elect_one()) {
+                    const auto product = [&](uint64_t a, uint64_t b, bool first) {
 #pragma unroll
-                    for (int k = 0; k < KSTEP / 16; ++k) tc_mma_f16(d, a + 2 * k, b + 2 * k, idesc, i > 0 || k > 0);
+                        for (int k = 0; k < KSTEP / 16; ++k) tc_mma_f16(d, a + 2 * k, b + 2 * k, idesc, !first || k > 0);
+                    };
+                    product(a, b, i == 0);
+                    if (ph) product(a, b + part, false);
                     if (wide == 2) {
-#pragma unroll
-                        for (int k = 0; k < KSTEP / 16; ++k)
-                            tc_mma_f16(d, a + (A_BYTES >> 4) + 2 * k, b + slice + 2 * k, idesc, 1u);
+                        product(a + (A_BYTES >> 4), b + PARTS * part, false);
+                        if (ph) product(a + (A_BYTES >> 4), b + (PARTS + 1) * part, false);
                     }
                     tc_commit(c.empty(at.s));
                     if (i == p.n - 1) tc_commit(c.accfull(seg & 1));
@@ -274,12 +283,44 @@ struct Pieces {
         return s;
     }
 };
+// fp16 has too few exponents for h, so a pair's h is multiplied by a power of two, which its products are divided by as they
+// leave the accumulators.  |h| <= |gate| |up|, each at most as many times its largest piece as a tile has pieces: with
+// that bound below 2^15 nothing overflows, and what two parts cannot hold is 2^-40 of the bound.  (A bound, because
+// the exact maximum of a pair would be known a phase too late; the exponent alone, so that no bit of h changes.)
 template <int DT>
-__device__ __forceinline__ uint2 activated(const Pieces& gate, const Pieces& up) {
+__device__ __forceinline__ int exponent_of(const Ctx& c, unsigned gate, unsigned up) {
+    if constexpr (DT != SOT_F16) return 0;
+    // |v| < 2^(e - 126) with e the exponent's bits; an h that is finite at all is below 2^128
+    const int bound = min(128, (int)(gate >> 23) - 126 + (int)(up >> 23) - 126 + 2 * c.doublings);
+    return min(126, 15 - bound);
+}
+template <int DT>
+__device__ __forceinline__ int exponent_at(const Ctx& c, const TcArgs& t, int p) {
+    if constexpr (DT != SOT_F16) return 0;
+    return exponent_of<DT>(c, __ldcg(t.peak + p), __ldcg(t.peak + c.P + p));
+}
+__device__ __forceinline__ float two_to(int k) { return __uint_as_float((unsigned)(k + 127) << 23); }  // -127 < k < 128
+
+template <int DT>
+struct Most {  // the type's largest number
+    static constexpr float value = DT == SOT_F16 ? 65504.f : 3.3895313892515355e38f;
+};
+// Four numbers h 2^k as two parts each; infinities and NaN are in the second one.
+template <int DT>
+__device__ __forceinline__ void activated(const Pieces& gate, const Pieces& up, int k, uint2 (&part)[PARTS]) {
     const float4 g = gate.sum(), u = up.sum();
-    const float2 f[Elem<DT>::N / 2] = {{silu_times(g.x, u.x), silu_times(g.y, u.y)}, {silu_times(g.z, u.z), silu_times(g.w, u.w)}};
-    const uint4 v = pack<DT>(f);
-    return make_uint2(v.x, v.y);
+    float h[4] = {silu_times(g.x, u.x), silu_times(g.y, u.y), silu_times(g.z, u.z), silu_times(g.w, u.w)};
+    float2 a[Elem<DT>::N / 2] = {}, b[Elem<DT>::N / 2] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == SOT_F16) h[i] *= two_to(k);
+        const float first = Elem<DT>::get(Elem<DT>::put(fminf(fmaxf(h[i], -Most<DT>::value), Most<DT>::value)));
+        (i & 1 ? a[i / 2].y : a[i / 2].x) = first;
+        (i & 1 ? b[i / 2].y : b[i / 2].x) = h[i] - first;
+    }
+    const uint4 v = pack<DT>(a), w = pack<DT>(b);
+    part[0] = make_uint2(v.x, v.y);
+    part[1] = make_uint2(w.x, w.y);
 }
 
 // A half-warp takes 64 columns of a pair, two at a time.
@@ -292,6 +333,7 @@ __device__ void activate(const Ctx& c, const TcArgs& t) {
     for (int i = (blockIdx.x + w * gridDim.x) * 2 + (lane >> 4); i < all; i += 2 * teams) {
         Pieces gate[2], up[2];
         unsigned short* to[2];
+        int k[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int at = min(i + j * teams, all - 1), p = at / tiles, tile = at - p * tiles, f = tile * 64 + (lane & 15) * 4;
@@ -300,12 +342,17 @@ __device__ void activate(const Ctx& c, const TcArgs& t) {
             const float* const from = t.part[0] + (long long)p * 2 * F + (real ? f : 0);
             gate[j].fetch(from, step, n);
             up[j].fetch(from + F, step, n);
+            k[j] = exponent_at<DT>(c, t, p);
             to[j] = real ? static_cast<unsigned short*>(t.h) + (long long)p * F + f : nullptr;
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint2 h = activated<DT>(gate[j], up[j]);
-            if (to[j]) *reinterpret_cast<uint2*>(to[j]) = h;
+            uint2 h[PARTS];
+            activated<DT>(gate[j], up[j], k[j], h);
+            if (to[j]) {
+                *reinterpret_cast<uint2*>(to[j]) = h[0];
+                *reinterpret_cast<uint2*>(to[j] + (long long)c.P * F) = h[1];
+            }
         }
     }
 }
@@ -325,19 +372,22 @@ __device__ __forceinline__ void activate_into(const Ctx& c, const TcArgs& t, uin
     Pieces gate, up;
     gate.fetch(from, (long long)c.P * 2 * F, n);
     up.fetch(from + F, (long long)c.P * 2 * F, n);
-    const uint2 v = activated<DT>(gate, up);
+    uint2 h[PARTS];
+    activated<DT>(gate, up, exponent_at<DT>(c, t, p), h);
     const int ch = lane >> 1 & 7;
-    const uint32_t to = dst + slice * c.npad * KSTEP * 2 + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4) + (lane & 1) * 8;
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(v.x), "r"(v.y) : "memory");
+    const uint32_t to = dst + slice * PARTS * c.part + (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4) + (lane & 1) * 8;
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i)
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + i * c.part), "r"(h[i].x), "r"(h[i].y) : "memory");
 }
 
-// The tokens' side of a phase: rows of x or h, swizzled as the tensor cores read them.  A row past the expert's
+// The tokens' side of a phase: rows of x or of h's parts, swizzled as the tensor cores read them.  A row past the expert's
 // last token is not written: what it holds only reaches columns that nobody reads.
 template <int DT>
 __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int& turn) {
     const int lane = threadIdx.x & 31, ch = lane & 7, stages = c.S, stage = c.stage, wide = c.wide;
     const int K = ph ? t.r.F : t.r.H;
-    const long long ld = ph ? t.r.F : t.r.ldx;
+    const long long ld = ph ? t.r.F : t.r.ldx, second = (long long)c.P * t.r.F;
     const unsigned short* const from = static_cast<const unsigned short*>(ph ? t.h : t.r.x) + ch * 8;
     const unsigned short* const rows = ph ? c.list : c.toks;
     // A warp's next unit must not lie more than a ring ahead of its last one: further on, the parity it waits for
@@ -357,7 +407,7 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
             const int k0 = (p.ks + turn) * wide * KSTEP;
             const bool ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
             if (!__all_sync(0xffffffffu, ok)) return false;
-            const uint32_t dst = c.base + at.s * stage + wide * A_BYTES, slice = c.npad * KSTEP * 2;
+            const uint32_t dst = c.base + at.s * stage + wide * A_BYTES;
             if (ph && t.fused)
                 for (int row = 0; row < e.n; ++row) activate_into<DT>(c, t, dst, row, rows[e.start + row], place, k0);
             else
@@ -367,7 +417,8 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
                 for (int i = 0; i < wide; ++i) {
                     const int k = k0 + i * KSTEP;
                     const bool real = k + ch * 8 < K;
-                    copy16(to + i * slice, real ? src + k : src, real ? 16 : 0);
+                    copy16(to + i * PARTS * c.part, real ? src + k : src, real ? 16 : 0);
+                    if (ph) copy16(to + (i * PARTS + 1) * c.part, real ? src + second + k : src, real ? 16 : 0);
                 }
             }
             if (first && lane == 0) mbar_arrive(c.go());
@@ -386,6 +437,7 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
 }
 
 // The accumulators of a phase's pieces, as partial sums [piece of the tile][pair][row].
+template <int DT>
 __device__ bool store_pieces(const Ctx& c, const TcArgs& t, int ph, int& seg, uint32_t tmem) {
     const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, m = q * 32 + lane;
     const int ld = ph ? t.r.H : 2 * t.r.F;
@@ -397,6 +449,9 @@ __device__ bool store_pieces(const Ctx& c, const TcArgs& t, int ph, int& seg, ui
         const bool real = ph ? col < t.r.H : tile * 64 + (m & 63) < t.r.F;
         const int ord = blockIdx.x - p.job * c.KS[ph] / c.chunk[ph];
         float* const to = t.part[ph] + (long long)ord * c.P * ld + col;
+        // fp16: what lane n's token of the next sixteen multiplies h by
+        const auto exponent = [&](int n0) { return lane < 16 && n0 + lane < e.n ? exponent_at<DT>(c, t, c.list[e.start + n0 + lane]) : 0; };
+        int k = DT == SOT_F16 && ph ? exponent(0) : 0;
         bool ok = mbar_wait_bounded(c.accfull(seg & 1), (seg >> 1) & 1, c.abort, WAIT_NS);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
@@ -404,9 +459,23 @@ __device__ bool store_pieces(const Ctx& c, const TcArgs& t, int ph, int& seg, ui
         for (int n0 = 0; n0 < e.n; n0 += 16) {
             float v[16];
             tmem_ld16(from + n0, v);
+            if (DT == SOT_F16 && ph) {
+                if (n0 > 0) k = exponent(n0);
+#pragma unroll
+                for (int n = 0; n < 16; ++n) v[n] *= two_to(-__shfl_sync(0xffffffffu, k, n));
+            }
 #pragma unroll
             for (int n = 0; n < 16; ++n)
                 if (n0 + n < e.n && real) __stcg(to + (long long)c.list[e.start + n0 + n] * ld, v[n]);
+            if (DT == SOT_F16 && !ph) {
+                unsigned most = 0;
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    const unsigned w = __reduce_max_sync(0xffffffffu, real ? __float_as_uint(fabsf(v[n])) : 0u);
+                    if (lane == n) most = w;
+                }
+                if (lane < 16 && n0 + lane < e.n) atomicMax(t.peak + (q < 2 ? 0 : c.P) + c.list[e.start + n0 + lane], most);
+            }
         }
         tc_fence_before();
         __syncwarp();
@@ -595,6 +664,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     const Cut cut(max(16, pad16(counts[1])), t.L.ring);
     c.npad = cut.npad;
     c.wide = cut.wide;
+    c.part = cut.part;
     c.stage = cut.stage;
     c.S = cut.stages;
     // A pair's place in its expert's list: the tokens before its own.
@@ -622,6 +692,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         c.first[ph] = (int)min((long long)U, (long long)blockIdx.x * c.chunk[ph]);
         c.end[ph] = min(U, c.first[ph] + c.chunk[ph]);
     }
+    c.doublings = 32 - __clz(min(c.KS[0], (c.KS[0] + c.chunk[0] - 2) / c.chunk[0] + 1) - 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -634,7 +705,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     } else {
         int seg = 0, turn = warp - W_LOAD;
         Turn at;
-        if (warp < W_LOAD) store_pieces(c, t, 0, seg, tmem);
+        if (warp < W_LOAD) store_pieces<DT>(c, t, 0, seg, tmem);
         else {
             at.skip(turn, c.S);
             load_tokens<DT>(c, t, 0, at, turn);
@@ -645,7 +716,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
             ok = grid_barrier(c, t, 1);
         }
         if (ok) {
-            if (warp < W_LOAD) store_pieces(c, t, 1, seg, tmem);
+            if (warp < W_LOAD) store_pieces<DT>(c, t, 1, seg, tmem);
             else load_tokens<DT>(c, t, 1, at, turn);
             ok = grid_barrier(c, t, 2);
         }
@@ -747,10 +818,11 @@ RoutedTcPlan routed_tc_plan(const RoutedArgs& a, int sms) {
         return at;
     };
     const size_t P = (size_t)a.T * a.K;
-    p.barrier_at = place(4 * sizeof(unsigned));
+    p.zeros = 4 + (a.dtype == SOT_F16 ? 2 * (int)P : 0);
+    p.barrier_at = place(p.zeros * sizeof(unsigned));
     p.up_at = place(sizeof(float) * pieces(a, 0, sms) * P * 2 * a.F);
     p.down_at = place(sizeof(float) * pieces(a, 1, sms) * P * a.H);
-    p.h_at = place(2 * P * a.F);
+    p.h_at = place(2 * PARTS * P * a.F);
     return p;
 }
 
@@ -759,6 +831,7 @@ cudaError_t launch_routed_tc(const RoutedArgs& a, const RoutedTcPlan& p, unsigne
     t.r = a;
     t.L = layout(a);
     t.barrier = reinterpret_cast<unsigned*>(scratch + p.barrier_at);
+    t.peak = t.barrier + 4;
     t.part[0] = reinterpret_cast<float*>(scratch + p.up_at);
     t.part[1] = reinterpret_cast<float*>(scratch + p.down_at);
     t.h = scratch + p.h_at;

@@ -28,6 +28,7 @@ struct RoutedArgs {
 
 struct RoutedTcPlan {
     size_t barrier_at, up_at, down_at, h_at, scratch;
+    int zeros;  // words at barrier_at that the scores' kernel writes zeros to
 };
 struct RoutedPlan {
     bool tc;  // the experts' products on the tensor cores
