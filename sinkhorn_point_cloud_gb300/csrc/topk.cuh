@@ -176,10 +176,11 @@ __device__ __forceinline__ unsigned team_count(SelectSmem<NT>& sh, unsigned mine
     const int now = step % 3, next = (step + 1) % 3;
     ++step;
     if ((threadIdx.x & 31) == 0 && w) atomicAdd(&sh.count[now], w);
+    // (the next step's: its last readers, two steps ago, have passed the barrier of the last step, and its next writers come
+    // behind this one)
+    if (threadIdx.x == 0) sh.count[next] = 0;
     __syncthreads();
-    const unsigned r = sh.count[now];
-    if (threadIdx.x == 0) sh.count[next] = 0;  // (its last readers passed the barrier above)
-    return r;
+    return sh.count[now];
 }
 
 // Sorts n2 (a power of two) numbers, largest first.
@@ -515,7 +516,7 @@ __device__ __forceinline__ void select_best(SelectSmem<NT>& sh, const unsigned* 
         team_sync<NT>();
         if (tid == 0) sh.found = sh.hits = 0;
         team_sync<NT>();
-        n = gather(ties ? at + 1 : at);  // (of ties: fewer than K)
+        n = min(gather(ties ? at + 1 : at), (unsigned)cap);  // (of ties: fewer than K)
         const float tie = Key<DT>::value(at);
         for (int g0 = 0; ties && g0 < s.ng && n < (unsigned)K; g0 += NT) {
             const int g = g0 + tid;
