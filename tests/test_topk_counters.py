@@ -27,7 +27,7 @@ static unsigned __reduce_add_sync(unsigned, unsigned v) { return v; }
 static void atomicAdd(volatile unsigned* p, unsigned v) { __atomic_fetch_add(p, v, __ATOMIC_SEQ_CST); }
 static void pause_some() {
     state = state * 1664525u + 1013904223u;
-    if (threadIdx.x / 32 == late && (state >> 24) % 2) usleep(300);
+    if (threadIdx.x / 32 == late && (state >> 24 & 1)) usleep(300);
 }
 static void __syncthreads() {
     pause_some();
@@ -35,7 +35,7 @@ static void __syncthreads() {
     pause_some();
 }
 template <int NT> struct SelectSmem { volatile unsigned count[3]; };
-%s
+FUNCTION
 constexpr int NT = 256, STEPS = 40;
 int main(int, char** argv) {
     late = atoi(argv[1]);
@@ -57,7 +57,7 @@ int main(int, char** argv) {
     for (auto& t : warps) t.join();
     int n = 0;
     for (int v : wrong) n += v;
-    printf("%%d\n", n);
+    printf("%d\n", n);
 }
 """
 
@@ -67,7 +67,7 @@ def program(tmp_path_factory):
     text = open(SOURCE).read()
     body = re.search(r"template <int NT>\n__device__ __forceinline__ unsigned team_count\(.*?\n}\n", text, re.S).group(0)
     at = tmp_path_factory.mktemp("counters")
-    (at / "count.cpp").write_text(FRAME % body)
+    (at / "count.cpp").write_text(FRAME.replace("FUNCTION", body))
     subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", str(at / "count.cpp"), "-o", str(at / "count")], check=True)
     return str(at / "count")
 
