@@ -109,7 +109,7 @@ struct Info {  // an expert that some token chose
 struct Ctx {
     unsigned char* sm;
     uint32_t base, bars;
-    volatile int* abort;
+    volatile int *abort, *met;  // a wait has run out; the last meeting took place
     float* weight;
     unsigned short *toks, *list, *act;  // by expert: tokens, pairs (token, choice); by pair: its expert's place in info
     short* id;
@@ -127,7 +127,7 @@ struct Ctx {
     __device__ __forceinline__ uint32_t drain() const { return bars + 8 * (2 * MAX_STAGES + 4); }
     __device__ __forceinline__ uint32_t go() const { return bars + 8 * (2 * MAX_STAGES + 5); }
 };
-constexpr int BAR_BYTES = 8 * (2 * MAX_STAGES + 6) + 8;  // and the TMEM address, and the abort flag
+constexpr int BAR_BYTES = 8 * (2 * MAX_STAGES + 6) + 16;  // and the TMEM address, and the two flags
 
 // A piece: units [u, u + n) of one tile.
 struct Piece {
@@ -485,25 +485,32 @@ __device__ bool store_pieces(const Ctx& c, const TcArgs& t, int ph, int& seg, ui
     return true;
 }
 
-// One thread of each CTA, for all that the CTA has done before: all CTAs have come this far, and what they wrote is seen.
-__device__ __forceinline__ void meet(const Ctx& c, const TcArgs& t, int which) {
+__device__ __forceinline__ unsigned load_acquire(const unsigned* at) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+    return v;
+}
+// One thread of each CTA, for all that the CTA has done before: whether all CTAs have come this far (what they wrote is
+// then seen) and this one has not given up.
+__device__ __forceinline__ bool meet(const Ctx& c, const TcArgs& t, int which) {
     unsigned* const at = t.barrier + which;
     __threadfence();
     if (!*c.abort) atomicAdd(at, 1u);  // (a CTA that gave up holds the others, whose waits then run out too)
     const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        unsigned v;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
-        if (v >= gridDim.x || *c.abort) break;
+    bool ok = false;
+    while (!*c.abort && !(ok = load_acquire(at) >= gridDim.x))
         if (globaltimer_ns() - t0 > WAIT_NS) *c.abort = 1;
-    }
     __threadfence();
+    return ok;
 }
+// All workers of a CTA get one answer.  (The flag itself may be raised by another role between two of them looking at it, and
+// they would wait for each other at different barriers.  Nobody else writes the answer, and the next one is
+// written behind a barrier that comes after all have read this one.)
 __device__ bool grid_barrier(const Ctx& c, const TcArgs& t, int which) {
     worker_sync();
-    if (threadIdx.x == W_EPI * 32) meet(c, t, which);
+    if (threadIdx.x == W_EPI * 32) *c.met = meet(c, t, which);
     worker_sync();
-    return !*c.abort;
+    return *c.met != 0;
 }
 
 // A warp takes 32 columns of a token: four lanes share four columns and take a quarter of the experts each.
@@ -560,8 +567,9 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     c.sm = raw + skip;
     c.base = lead + skip;
     c.bars = c.base + t.L.bars;
-    uint32_t* const slot = reinterpret_cast<uint32_t*>(c.sm + t.L.bars + BAR_BYTES - 8);
+    uint32_t* const slot = reinterpret_cast<uint32_t*>(c.sm + t.L.bars + BAR_BYTES - 16);
     c.abort = reinterpret_cast<volatile int*>(slot + 1);
+    c.met = c.abort + 1;
     c.weight = reinterpret_cast<float*>(c.sm + t.L.weight);
     c.toks = reinterpret_cast<unsigned short*>(c.sm + t.L.toks);
     c.list = reinterpret_cast<unsigned short*>(c.sm + t.L.list);
