@@ -158,7 +158,8 @@ struct Turn {
 };
 __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
 
-__device__ void produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, const CUtensorMap* down) {
+// Returns the units that were requested.
+__device__ int produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, const CUtensorMap* down) {
     const uint64_t policy = policy_drop();
     const int stages = c.S, stage = c.stage, wide = c.wide, step = wide * KSTEP;
     Turn at;
@@ -187,15 +188,17 @@ __device__ void produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, co
             u += p.n;
         }
     }
-    if (*c.abort) {
-        // Copies in flight land before the CTA goes: the loading warps may have given up, so their arrivals are made
-        // here (one too many does no harm any more).
-        int dummy = 0;
-        for (int i = max(0, issued - stages); i < issued; ++i) {
-            const int s = i % stages;
-            if (!mbar_try_wait(c.full(s), (i / stages) & 1)) mbar_arrive(c.full(s));
-            mbar_wait_bounded(c.full(s), (i / stages) & 1, &dummy, WAIT_NS);
-        }
+    return issued;
+}
+// After a wait that ran out, once no role is at work any more: copies in flight land before the CTA goes.  A unit's barrier
+// wants the arrival of its loading warp too, which may have given up before it; loaded: units that each has arrived for.
+__device__ void settle(const Ctx& c, int issued, const int* loaded) {
+    const int stages = c.S, loaders = min(LOADERS, stages);
+    int dummy = 0;
+    for (int i = max(0, issued - stages); i < issued; ++i) {
+        const int s = i % stages;
+        if (i / loaders >= loaded[i % loaders]) mbar_arrive(c.full(s));
+        mbar_wait_bounded(c.full(s), (i / stages) & 1, &dummy, WAIT_NS);
     }
 }
 
@@ -384,7 +387,7 @@ __device__ __forceinline__ void activate_into(const Ctx& c, const TcArgs& t, uin
 // The tokens' side of a phase: rows of x or of h's parts, swizzled as the tensor cores read them.  A row past the expert's
 // last token is not written: what it holds only reaches columns that nobody reads.
 template <int DT>
-__device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int& turn) {
+__device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int& turn, int& loaded) {
     const int lane = threadIdx.x & 31, ch = lane & 7, stages = c.S, stage = c.stage, wide = c.wide;
     const int K = ph ? t.r.F : t.r.H;
     const long long ld = ph ? t.r.F : t.r.ldx, second = (long long)c.P * t.r.F;
@@ -427,6 +430,7 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(c.full(at.s));
+            ++loaded;
             at.skip(loaders, stages);
         }
         turn -= p.n;
@@ -560,7 +564,7 @@ template <int DT>
 __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const __grid_constant__ CUtensorMap up,
                                                           const __grid_constant__ CUtensorMap down) {
     extern __shared__ unsigned char raw[];
-    __shared__ int counts[2];
+    __shared__ int counts[2], issued, loaded[LOADERS];
     const uint32_t lead = smem_u32(raw);
     const uint32_t skip = (1024 - (lead & 1023)) & 1023;
     Ctx c;
@@ -707,16 +711,16 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     const uint32_t tmem = *slot;
 
     if (warp == W_PRODUCER) {
-        if (lane == 0) produce(c, t, &up, &down);
+        if (lane == 0) issued = produce(c, t, &up, &down);
     } else if (warp == W_MMA) {
         multiply<DT>(c, t, tmem);
     } else {
-        int seg = 0, turn = warp - W_LOAD;
+        int seg = 0, turn = warp - W_LOAD, units = 0;
         Turn at;
         if (warp < W_LOAD) store_pieces<DT>(c, t, 0, seg, tmem);
         else {
             at.skip(turn, c.S);
-            load_tokens<DT>(c, t, 0, at, turn);
+            load_tokens<DT>(c, t, 0, at, turn, units);
         }
         bool ok = grid_barrier(c, t, 0);
         if (ok && !t.fused) {
@@ -725,7 +729,7 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
         }
         if (ok) {
             if (warp < W_LOAD) store_pieces<DT>(c, t, 1, seg, tmem);
-            else load_tokens<DT>(c, t, 1, at, turn);
+            else load_tokens<DT>(c, t, 1, at, turn, units);
             ok = grid_barrier(c, t, 2);
         }
         if (ok) join<DT>(c, t);
@@ -736,10 +740,12 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
                 static_cast<T*>(t.r.out)[i / t.r.H * t.r.ldo + i % t.r.H] = Elem<DT>::put(NAN);
             if (tid == W_EPI * 32) atomicOr(t.status, SOT_DEV_TIMEOUT);
         }
+        if (warp >= W_LOAD && lane == 0) loaded[warp - W_LOAD] = units;
     }
     tc_fence_before();
     __syncthreads();
     if (warp == W_MMA) tmem_dealloc(tmem, cols);
+    if (tid == 0 && *c.abort) settle(c, issued, loaded);
 }
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
