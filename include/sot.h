@@ -486,7 +486,7 @@ int sot_embed_grad(const void* grad_out, long long T, int D, long long ld, int t
  * are 16-byte aligned and ld is a multiple of 8, the products run on the tensor cores, where silu(.) * (.) is the sum of two
  * numbers of the type (fp16: times a power of two a token and expert, so that its range is that of 32 bits): good to 2^-17
  * (bf16) or 2^-22 (fp16) of itself.  There a wait that runs out of time gives an output of NaN and SOT_ERR_TIMEOUT
- * from sot_async_status.
+ * from sot_async_status; logits, ids and weights are whole all the same.
  * logits, ids and weights are what sot_balance_loss takes and what a backward pass needs; out [T][H] has
  * row stride ld_out and must not overlap the inputs.
  */
@@ -569,6 +569,14 @@ int sot_async_status(void* stream);
  * it between calls.  Not for production use.
  */
 int sot_test_hold_tile(int tile, int after_launches, long long wait_ns);
+
+/*
+ * The same for sot_routed_layer on the tensor cores: one of its CTAs withholds its arrival at the meeting of all CTAs
+ * behind the first product (what = 0), silu(.) * (.) (1, where T K > 16), the second product (2) or the choice
+ * (3, where T > 14), or the weights of its unit of work n (from 0) and those after it (what = 4 + n).  Waits run out
+ * after wait_ns (<= 0: the default 2 s); what < 0 turns the hook off and restores the default limit.
+ */
+int sot_test_hold_routed(int what, long long wait_ns);
 
 /*
  * Which kernel family a solve of dimension d with these flags would use:

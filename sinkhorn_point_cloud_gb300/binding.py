@@ -107,6 +107,7 @@ def load(path: str | None = None):
         "sot_async_status": [P],
         "sot_hvp": [P, P, P, P, i, i, i, i, P, P, f, P, i, f, P, i, P],
         "sot_test_hold_tile": [i, i, ll],
+        "sot_test_hold_routed": [i, ll],
         "sot_plan_coo_operands": [P, P, P, P, i, i, i, i, P, P, f, f, P, P, P, P, P, P, P, P,
                                   C.POINTER(C.c_float), P],
         "sot_token_logprob": [P, ll, i, ll, i, f, P, i, P, P, P],
@@ -879,6 +880,12 @@ def sot_test_hold_tile(tile: int, after_launches: int = 0, wait_ns: int = 0):
     kernels withhold column tile `tile` of their chunk onward (tile < 0: off),
     so their waits run out after wait_ns nanoseconds."""
     _check(load().sot_test_hold_tile(int(tile), int(after_launches), int(wait_ns)), "sot_test_hold_tile")
+
+
+def sot_test_hold_routed(what: int, wait_ns: int = 0):
+    """Testing hook: a CTA of the routed layer's tensor-core kernel withholds its arrival at a meeting (what = 0 to 3) or its
+    weights from unit what - 4 on (what < 0: off), so that waits run out after wait_ns nanoseconds."""
+    _check(load().sot_test_hold_routed(int(what), int(wait_ns)), "sot_test_hold_routed")
 
 
 def sot_check_inputs(X, Y, a=None, b=None, stream=None) -> int:

@@ -19,6 +19,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "kernels.h"
 #include "routed.cuh"
 #include "tc_ptx.cuh"
@@ -68,6 +70,8 @@ struct TcArgs {
     void* h;              // [PARTS][T K][F]
     int pieces[PHASES];   // of a tile, at most
     bool fused;           // the loading warps form h
+    unsigned long long wait_ns;  // limit of a wait
+    int hold;  // testing hook: what CTA 0 withholds, its arrival at meeting 0 to 3 or its units from hold - 4 on (-1: nothing)
 };
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int k, int row, uint32_t bar, uint64_t policy) {
@@ -172,9 +176,10 @@ __device__ int produce(const Ctx& c, const TcArgs& t, const CUtensorMap* up, con
             const int a = p.job / c.tiles[ph], tile = p.job - a * c.tiles[ph], e = c.info[a].expert;
             const int r0 = ph ? e * t.r.H + tile * 128 : e * 2 * t.r.F + tile * 64, r1 = ph ? r0 + 64 : r0 + t.r.F;
             for (int k = p.ks * step, end = k + p.n * step; k < end; k += step) {
+                if (t.hold >= 4 && issued >= t.hold - 4 && blockIdx.x == 0) return issued;
                 // The loading warps' first requests go out before most of the ring's: behind all of it they take 5 us.
-                if (issued == HEAD) ok = mbar_wait_bounded(c.go(), 0, c.abort, WAIT_NS);
-                ok = ok && mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
+                if (issued == HEAD) ok = mbar_wait_bounded(c.go(), 0, c.abort, t.wait_ns);
+                ok = ok && mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, t.wait_ns);
                 if (!ok) break;
                 const uint32_t full = c.full(at.s), dst = c.base + at.s * stage;
                 mbar_arrive_expect_tx(full, wide * A_BYTES);
@@ -217,10 +222,10 @@ __device__ void multiply(const Ctx& c, const TcArgs& t, uint32_t tmem) {
             const Piece p = piece_at(c, ph, u);
             const uint32_t idesc = f16_idesc(128, pad16(c.info[p.job / c.tiles[ph]].n)) | format;
             const uint32_t d = tmem + (seg & 1) * c.npad;
-            ok = mbar_wait_bounded(c.accempty(seg & 1), ((seg >> 1) & 1) ^ 1, c.abort, WAIT_NS);
+            ok = mbar_wait_bounded(c.accempty(seg & 1), ((seg >> 1) & 1) ^ 1, c.abort, t.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             for (int i = 0; ok && i < p.n; ++i) {
-                ok = mbar_wait_bounded(c.full(at.s), at.phase, c.abort, WAIT_NS);
+                ok = mbar_wait_bounded(c.full(at.s), at.phase, c.abort, t.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -408,7 +413,7 @@ __device__ bool load_tokens(const Ctx& c, const TcArgs& t, int ph, Turn& at, int
         // turn: units until this warp's next one, whose place in the ring is `at`
         for (; turn < p.n; turn += loaders) {
             const int k0 = (p.ks + turn) * wide * KSTEP;
-            const bool ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, WAIT_NS);
+            const bool ok = mbar_wait_bounded(c.empty(at.s), at.phase ^ 1, c.abort, t.wait_ns);
             if (!__all_sync(0xffffffffu, ok)) return false;
             const uint32_t dst = c.base + at.s * stage + wide * A_BYTES;
             if (ph && t.fused)
@@ -456,7 +461,7 @@ __device__ bool store_pieces(const Ctx& c, const TcArgs& t, int ph, int& seg, ui
         // fp16: what lane n's token of the next sixteen multiplies h by
         const auto exponent = [&](int n0) { return lane < 16 && n0 + lane < e.n ? exponent_at<DT>(c, t, c.list[e.start + n0 + lane]) : 0; };
         int k = DT == SOT_F16 && ph ? exponent(0) : 0;
-        bool ok = mbar_wait_bounded(c.accfull(seg & 1), (seg >> 1) & 1, c.abort, WAIT_NS);
+        bool ok = mbar_wait_bounded(c.accfull(seg & 1), (seg >> 1) & 1, c.abort, t.wait_ns);
         if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
         const uint32_t from = tmem + (seg & 1) * c.npad + ((uint32_t)(q * 32) << 16);
@@ -499,11 +504,12 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned* at) {
 __device__ __forceinline__ bool meet(const Ctx& c, const TcArgs& t, int which) {
     unsigned* const at = t.barrier + which;
     __threadfence();
-    if (!*c.abort) atomicAdd(at, 1u);  // (a CTA that gave up holds the others, whose waits then run out too)
+    // (a CTA that gave up holds the others, whose waits then run out too)
+    if (!*c.abort && !(t.hold == which && blockIdx.x == 0)) atomicAdd(at, 1u);
     const uint64_t t0 = globaltimer_ns();
     bool ok = false;
     while (!*c.abort && !(ok = load_acquire(at) >= gridDim.x))
-        if (globaltimer_ns() - t0 > WAIT_NS) *c.abort = 1;
+        if (globaltimer_ns() - t0 > t.wait_ns) *c.abort = 1;
     __threadfence();
     return ok;
 }
@@ -637,8 +643,10 @@ __global__ void __launch_bounds__(NT, 1) routed_tc_kernel(const TcArgs t, const 
     if (shared) {
         if (tid == 0) meet(c, t, 3);
         __syncthreads();
+        if (!*c.abort) {  // (otherwise some tokens' choices may not be there, only what the memory held before)
 #pragma unroll 1
-        for (int p = tid; p < c.P; p += NT) take(p, __ldcg(t.r.ids + p), __ldcg(t.r.weights + p));
+            for (int p = tid; p < c.P; p += NT) take(p, __ldcg(t.r.ids + p), __ldcg(t.r.weights + p));
+        }
         __syncthreads();
     }
     // The experts in use, in order, and where their lists start.  (Loops stay loops here: this runs once, and fetching
@@ -777,6 +785,10 @@ bool weight_map(CUtensorMap* map, const void* p, int dtype, long long rows, int 
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Host-side settings that every launch takes.
+std::atomic<int> g_hold{-1};
+std::atomic<unsigned long long> g_wait_ns{WAIT_NS};
+
 constexpr int MAX_SMEM = 227 * 1024 - 1024;  // the kernel's static part is below 1 KB
 
 Layout layout(const RoutedArgs& a) {
@@ -815,6 +827,11 @@ int pieces(const RoutedArgs& a, int ph, int sms) {
 
 }  // namespace
 
+void routed_set_test_hold(int what, unsigned long long wait_ns) {
+    g_hold.store(what < 0 ? -1 : what);
+    g_wait_ns.store(wait_ns > 0 ? wait_ns : WAIT_NS);
+}
+
 bool routed_tc_fits(const RoutedArgs& a) {
     return a.dtype != SOT_F32 && a.H % 8 == 0 && a.F % 8 == 0 && a.ldx % 8 == 0 && (unsigned long long)a.x % 16 == 0 &&
            (unsigned long long)a.gate_up % 16 == 0 && (unsigned long long)a.down % 16 == 0 &&
@@ -851,6 +868,8 @@ cudaError_t launch_routed_tc(const RoutedArgs& a, const RoutedTcPlan& p, unsigne
     t.h = scratch + p.h_at;
     for (int ph = 0; ph < PHASES; ++ph) t.pieces[ph] = pieces(a, ph, sms);
     t.fused = a.T * a.K <= FUSED_PAIRS;
+    t.wait_ns = g_wait_ns.load();
+    t.hold = g_hold.load();
     cudaError_t e = async_status_address(&t.status);
     if (e != cudaSuccess) return e;
     CUtensorMap up, down;

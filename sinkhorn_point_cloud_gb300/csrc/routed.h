@@ -39,6 +39,7 @@ RoutedPlan routed_plan(const RoutedArgs& a, int sms);
 cudaError_t launch_routed(RoutedArgs a, const RoutedPlan& p, unsigned char* scratch, int sms, cudaStream_t st);
 
 // The tensor cores' part (k_routed_tc.cu): everything after the scores.
+void routed_set_test_hold(int what, unsigned long long wait_ns);  // wait_ns 0: the default
 bool routed_tc_fits(const RoutedArgs& a);
 RoutedTcPlan routed_tc_plan(const RoutedArgs& a, int sms);
 cudaError_t launch_routed_tc(const RoutedArgs& a, const RoutedTcPlan& p, unsigned char* scratch, int sms, cudaStream_t st);

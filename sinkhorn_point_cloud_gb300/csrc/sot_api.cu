@@ -867,6 +867,12 @@ int sot_test_hold_tile(int tile, int after_launches, long long wait_ns) {
     return SOT_OK;
 }
 
+int sot_test_hold_routed(int what, long long wait_ns) {
+    g_err[0] = 0;
+    routed_set_test_hold(what, wait_ns > 0 ? (unsigned long long)wait_ns : 0ull);
+    return SOT_OK;
+}
+
 int sot_potentials(const float* X, const float* Y, const float* a, const float* b, int B, int n, int m, int d,
                    float eps, int iters, float* f, float* g, void* stream) {
     if (iters < 0) return fail(SOT_ERR_INVALID_ARG, "iters must be >= 0");
