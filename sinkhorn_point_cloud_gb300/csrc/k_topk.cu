@@ -38,12 +38,19 @@ void topk_plan(bool whole, const TopkArgs& a, int sms, TopkPlan* p) {
     p->L.CL = CL;
     p->L.G = (int)G;
     p->L.chunks = a.K ? (int)((G + p->U * p->NT - 1) / (p->U * p->NT)) * p->NT : 0;
-    const int most = (CL > 2 ? CL : 2) * a.K;  // candidates to sort, or slices' alternatives to join
-    p->L.cap = a.K ? pow2_from(most > 256 ? most : 256) : 0;
-    // candidates, chunks to look at again, and the chunks' maxima, where the candidates are put in order later
-    const long long last = std::max<long long>(sizeof(unsigned) * p->L.chunks, sizeof(unsigned long long) * p->L.cap);
-    const long long bytes = (long long)(sizeof(unsigned long long) + sizeof(int)) * p->L.cap + last;
-    p->L.bytes = (int)(bytes < TOPK_MAX_SMEM + 1 ? bytes : TOPK_MAX_SMEM + 1);
+    p->L.join = a.K ? pow2_from(CL * a.K) : 0;
+    const auto place = [&](int candidates) {
+        p->L.cap = a.K ? pow2_from(std::max(candidates, 256)) : 0;
+        // candidates, chunks to look at again, and the chunks' maxima, where the candidates are put in order later
+        const long long last = std::max<long long>(sizeof(unsigned) * p->L.chunks, sizeof(unsigned long long) * p->L.cap);
+        long long bytes = (long long)(sizeof(unsigned long long) + sizeof(int)) * p->L.cap + last;
+        if (CL > 1 && a.K) bytes = std::max(bytes, (long long)sizeof(unsigned long long) * 2 * p->L.join + (long long)sizeof(int) * BINS);
+        p->L.bytes = (int)(bytes < TOPK_MAX_SMEM + 1 ? bytes : TOPK_MAX_SMEM + 1);
+    };
+    // As many candidates of a slice as all slices' alternatives together; where the chunks' maxima leave no room for them, twice
+    // its own (more of them are looked for with a higher threshold).
+    place(std::max(CL, 2) * a.K);
+    if (p->L.bytes > TOPK_MAX_SMEM) place(2 * a.K);
 }
 
 }  // namespace

@@ -23,6 +23,7 @@ struct TopkLaunch {
     int CL, G;     // CTAs a row, granules a slice
     int chunks;    // places for chunk maxima in shared memory
     int cap;       // places for candidates: a power of two, at least 2 K
+    int join;      // places for those of all slices, which take the whole of shared memory once they are found
     int bytes;     // of shared memory for a team
 };
 
@@ -663,7 +664,8 @@ __global__ void __launch_bounds__(NT * TEAMS<NT>, NT == 32 ? 4 : 1024 / NT) topk
                     cand[i] = cluster_load64(cluster_addr(smem_u32(cand + (i - r * a.K)), r));
                 }
                 __syncthreads();
-                order<NT>(sh, cand, L.CL * a.K, a.K, hit, spare);
+                int* const bins = reinterpret_cast<int*>(cand + L.join);
+                order<NT>(sh, cand, L.CL * a.K, a.K, bins, reinterpret_cast<unsigned long long*>(bins + BINS));
             }
         }
         cluster_sync();  // nobody leaves while rank 0 reads
