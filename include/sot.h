@@ -445,7 +445,8 @@ int sot_token_topk(const void* logits, long long T, int V, long long ld, int dty
  *   g_v = grad_logp[t] [v = target[t]] + sum_k grad_top[t][k] [v = ids[t][k]].
  * ids[t][k] outside [0, V) is an unused entry; the used ones of a row are distinct (a row that repeats one has an
  * unspecified result).  Rows left out, and rows whose incoming gradients are all 0, are written as zeros without being
- * read.  entropy may be NULL where grad_entropy is.  Probabilities are as good as the lse: 2^-24 of its size.
+ * read.  entropy may be NULL where grad_entropy is.  Probabilities come from the lse: a log-probability is good to 2^-22 of
+ * the lse's size, which 32 bits cannot tell apart where that nears 1.
  * grad may be the logits' own array with the same stride.
  */
 int sot_token_topk_grad(const void* logits, long long T, int V, long long ld, int dtype, float temperature,
