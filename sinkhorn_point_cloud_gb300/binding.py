@@ -691,6 +691,14 @@ def _run(dev, stream, call):
         return call(_raw_stream(dev))
 
 
+def _count(n, name, least):
+    """A whole number that the library takes in 32 bits (ctypes would cut a larger one off without a word)."""
+    n = int(n)
+    if not least <= n < 1 << 31:
+        raise ValueError(f"{name} must satisfy {least} <= {name} < 2^31, got {n}")
+    return n
+
+
 def sot_token_topk(logits, K, target=None, temperature=1.0, stream=None):
     """Scores of given tokens with entropies and the best alternatives: (logp [T] or None, lse [T], entropy [T],
     ids [T, K] int32, top_logp [T, K]) of logits [T, V].  ids are the columns of the K largest logits, largest first,
@@ -699,9 +707,7 @@ def sot_token_topk(logits, K, target=None, temperature=1.0, stream=None):
     without target every row takes part and logp is None."""
     x, T, V, ld, dt, dev = _logits(logits)
     tg, ty = (None, SOT_I32) if target is None else _indices(target, "target", (T,), dev)
-    K = int(K)
-    if K < 0:
-        raise ValueError("K must be >= 0")
+    K = _count(K, "K", 0)
 
     def call(s):
         lse = torch.empty(T, dtype=_F32, device=logits.device)
@@ -777,6 +783,7 @@ def sot_embed(table, ids, scale=1.0, dtype=None, out=None, stream=None):
     """Embedding lookup with scaling: out [T, D] = scale table[ids], rounded once; rows of zeros for ids outside
     [0, V).  table [V, D] may have a row stride, ids is [T]; ``dtype`` (default the table's) is the type of a new out."""
     x, V, D, ld, dt, dev = _logits(table, "table")
+    V = _count(V, "V", 1)
     if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
         raise ValueError("ids must be a torch.Tensor of shape [T]")
     T = ids.shape[0]
@@ -805,9 +812,7 @@ def sot_embed_grad(grad_out, ids, V, scale=1.0, dtype=None, grad=None, accumulat
     gradient).  ``dtype`` (default grad_out's) is the type of a new gradient."""
     x, T, D, ld, dt, dev = _logits(grad_out, "grad_out")
     i, ty = _indices(ids, "ids", (T,), dev)
-    V = int(V)
-    if V < 1:
-        raise ValueError("V must be >= 1")
+    V = _count(V, "V", 1)
     if accumulate and grad is None:
         raise TypeError("accumulate needs a gradient to add to")
     gt = _float_type(dtype, dt)

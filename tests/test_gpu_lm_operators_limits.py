@@ -133,3 +133,19 @@ def test_routed_layer_with_all_tokens_at_the_same_experts(sot, K, dtype):
     bias[which] = 14.0 + torch.arange(K, device="cuda") % 2
     _, _, ids, _ = check_routed(sot, (x, router, gu, dn, bias), K, dtype)
     assert torch.equal(ids.sort(1).values.long(), which.expand(128, K))
+
+
+# ---- whole numbers beyond 32 bits -----------------------------------------------------------------------------------------
+def test_numbers_beyond_32_bits_are_refused(sot):
+    """Not taken for what is left of them: 2^32 + 5 rows are not five."""
+    x, ids = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda"), torch.tensor([7], device="cuda")
+    for V in ((1 << 32) + 5, 1 << 31):
+        with pytest.raises(ValueError, match="V must satisfy"):
+            sot.sot_embed_grad(x, ids, V)
+    with pytest.raises(ValueError, match="K must satisfy"):
+        sot.sot_token_topk(x, (1 << 32) + 3)
+    table = torch.empty((1 << 32) + 5, 1, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="V must satisfy"):
+        sot.sot_embed(table, ids)
+    with pytest.raises(ValueError, match="V must satisfy"):
+        sot.sot_embed_grad(x, ids, (1 << 32) + 5, grad=table)
