@@ -80,12 +80,14 @@ cudaMemPool_t scratch_pool() {
         pr.location.type = cudaMemLocationTypeDevice;
         pr.location.id = dev;
         cudaMemPool_t mp = nullptr;
-        if (cudaMemPoolCreate(&mp, &pr) != cudaSuccess) {
-            cudaGetLastError();
-            return nullptr;
-        }
+        // (Making a pool is no stream's work: a capture under way, for which it would be an error, has nothing to record of it.)
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+        const bool made = cudaMemPoolCreate(&mp, &pr) == cudaSuccess;
         unsigned long long keep = SCRATCH_KEEP_BYTES;
-        if (cudaMemPoolSetAttribute(mp, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) cudaGetLastError();
+        if (!made || cudaMemPoolSetAttribute(mp, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) cudaGetLastError();
+        if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
+        if (!made) return nullptr;
         pools[dev] = mp;
     }
     return pools[dev];
