@@ -780,7 +780,7 @@ def _float_type(dtype, default):
 
 
 def sot_embed(table, ids, scale=1.0, dtype=None, out=None, stream=None):
-    """Embedding lookup with scaling: out [T, D] = scale table[ids], rounded once; rows of zeros for ids outside
+    """Embedding lookup with scaling: out [T, D] = scale table[ids] in 32 bits, rounded; rows of zeros for ids outside
     [0, V).  table [V, D] may have a row stride, ids is [T]; ``dtype`` (default the table's) is the type of a new out."""
     x, V, D, ld, dt, dev = _logits(table, "table")
     V = _count(V, "V", 1)
@@ -836,7 +836,8 @@ def sot_routed_layer(x, router, gate_up, down, K, bias=None, renorm=True, scale=
     """A routed layer for a few tokens (at most 128): (out [T, H], logits [T, E] float32, ids [T, K] int32, weights [T, K]
     float32) of x [T, H], router [E, H], gate_up [E, 2 F, H], down [E, H, F] (one type) and bias [E] float32.
     out = sum over a token's K best experts of weight * down (silu(gate x) * up x).  logits and ids go on to
-    sot_balance_loss."""
+    sot_balance_loss.  The tensor cores take float16 and bfloat16 with H, F and x's row stride multiples of 8 and x, gate_up
+    and down at 16-byte addresses; anything else is right too, but many times slower (x.contiguous() before the call)."""
     at, T, H, ld, dt, dev = _logits(x, "x")
     K = int(K)
     try:

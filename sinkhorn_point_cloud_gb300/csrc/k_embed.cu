@@ -13,8 +13,8 @@
 //   join     adds up the partial sums, in a fixed order.
 // No atomics on floats: repeated calls give the same bits.
 //
-// bf16, 4096 columns: 32768 lookups in fp32 77 us (0.80 of the measured copy bandwidth), 16384 tokens into 131072 rows 201 to
-// 204 us (0.87; most of it is zeros).  65001 tokens of 1001 fp32 columns into 32003 rows 124 us (0.43; 100 us with 1000 columns,
+// bf16, 4096 columns: 32768 lookups in fp32 77 us (0.80 of the measured copy bandwidth), 16384 tokens into 131072 rows 205 us
+// (0.87; most of it is zeros).  65001 tokens of 1001 fp32 columns into 32003 rows 124 us (0.43; 100 us with 1000 columns,
 // which need no cutting).
 #include <cuda_runtime.h>
 
@@ -717,6 +717,8 @@ __global__ void __launch_bounds__(JOIN_NT, 4) embed_join_kernel(const EmbedGradA
     }
 }
 
+// Rows of whole pieces of eight columns.  (In fp32 four would do for whole granules; 20000 rows of 1004: lookup 24.5 us, of
+// 1008 24.8, gradient 67 and 61.)
 bool whole_rows(const void* p, long long ld, int D, int type) {
     const long long b = type == SOT_F32 ? 4 : 2;
     return (unsigned long long)p % 16 == 0 && ld * b % 16 == 0 && D % 8 == 0;
@@ -748,7 +750,9 @@ cudaError_t launch_after(const void* kern, unsigned blocks, int threads, void** 
     return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
-// Rows that get their zeros beside the sort: as many as that leaves time for.
+// Rows that get their zeros beside the sort: as many as that leaves time for (8192 tokens, 32000 x 1024 bf16 to fp32: 37 us,
+// without any and with four times as many 43; 2000, 20000 x 2048 bf16: 28, 35 and 33; 4000, 100000 x 1024: 47, 54 and 55;
+// 1500, 200000 x 512: 45, 51 and 52; 65001, 32003 x 1000 fp32: 101, 107 and 100).
 constexpr long long EARLY_BYTES = 40 << 20, EARLY_BYTES_A_TOKEN = 1200;
 long long early_rows(const EmbedGradArgs& a) {
     if (a.accumulate) return 0;

@@ -5,7 +5,9 @@
 //   out_t = sum_k w_k down_e (silu(gate_e x_t) * up_e x_t),   e = the k-th expert of t.
 // A few tokens read far more weights than they compute with: the chosen experts' 3 F H weights bound it.
 // Here are the scores (64 tokens of 64 experts, H = 2048: 9 us, beside which the next kernel comes up) and, for fp32 and for
-// sizes that the tensor cores' copies do not take, a kernel of warps for each step (k_routed_tc.cu has the others).
+// sizes that the tensor cores' copies do not take, a kernel of warps for each step (k_routed_tc.cu has the others): a warp an
+// output, an expert's row read again for each of its tokens (H = 2048, F = 1024, 8 of 64 experts, 1 / 8 / 64 tokens: bf16 with
+// rows of x off their 16 bytes 73 / 311 / 1850 us, where the tensor cores take 31 / 97 / 150; fp32 78 / 364 / 2410).
 #include <cuda_runtime.h>
 
 #include "kernels.h"
